@@ -51,7 +51,8 @@ extern "C" {
 #define S1_ERR_DEVICE_TIMEOUT 6   /* a bounded device-side wait gave up                  */
 #define S1_ERR_UNSUPPORTED 7      /* shape the kernels do not handle (message says why)  */
 
-enum { S1_F32 = 0, S1_BF16 = 1 };            /* dtype of the host weight arrays        */
+enum { S1_F32 = 0, S1_BF16 = 1,             /* dtype of the host weight arrays        */
+       S1_F16 = 2 };                        /* (device arrays of the operators only)  */
 enum { S1_CHOICE = 0, S1_SCORE = 1, S1_NOUL = 2 };
 
 typedef struct s1_model s1_model;

@@ -4,7 +4,8 @@
  * These expose single steps of the decision path on DEVICE pointers so each kernel can be
  * checked on its own against an independent reference, and timed. They are blocking
  * (they synchronise the given stream before returning) and may allocate small device
- * temporaries; they are not needed by the decision API in s1.h.
+ * temporaries, except the stream-ordered operators (names ending in _async), which do neither;
+ * they are not needed by the decision API in s1.h.
  * Return codes and s1_last_error() as in s1.h.
  */
 #ifndef S1_OPS_H_
@@ -96,6 +97,97 @@ int s1_op_attention(const void* q, const void* k_new, const void* v_new, const v
 /* out f16 [R, d] = x / sqrt(mean(x^2) + eps) * w;  x fp32 [R, d], w fp32 [d]. */
 int s1_op_rmsnorm(const float* x, const float* w, int32_t R, int32_t d, float eps, void* out,
                   void* stream);
+
+/* ---- stream-ordered operators over a long shared prefix ------------------------------------
+ * These serve a batch of sequences that continue one prefix: an 8-bit form of the K/V snapshot,
+ * attention that reads the prefix once for the whole batch, and linear attention with a decay
+ * per head (prompts and single tokens). Pointers are DEVICE pointers of the current device
+ * unless marked host; host arrays are read during the call only. They launch on `stream`
+ * (a cudaStream_t, NULL = legacy default), allocate nothing, do not synchronise and can be
+ * captured into a CUDA graph, which bakes every argument's value (the device arrays' contents
+ * are read at replay). Bad arguments are refused before any launch with S1_ERR_INVALID_ARG, or
+ * S1_ERR_UNSUPPORTED for a shape the kernels do not take. Outputs must not overlap inputs
+ * except where stated. A workspace holds nothing between calls: calls ordered on one stream may
+ * share one, calls (or graph replays) that can overlap need one each. */
+enum { S1_KV_F16 = 0, S1_KV_E4M3 = 1 };   /* formats of a K/V snapshot */
+
+/* Waits for `stream` and reports a bounded device wait that gave up in any of the operators
+ * below on the current device since the last report (S1_ERR_DEVICE_TIMEOUT; the outputs of the
+ * calls in question are then unspecified). */
+int s1_op_sync(void* stream);
+
+/* Writes n_rows rows of keys and values into an 8-bit snapshot, quantising them on the way.
+ * k, v: dtype S1_F16, S1_BF16 or S1_F32, row i at k + i * k_stride (strides in elements, at
+ * least Hkv * hd: slices of a fused projection's rows are fine; 16-byte aligned rows take wide
+ * loads, others element loads), [Hkv][hd] within a row; hd 64 or 128.
+ * codes: e4m3 bytes [2, cap, Hkv, hd] (K plane, V plane; 16-byte aligned), scales: fp32
+ * [2, Hkv, cap]. Source row i becomes snapshot row pos0 + i (pos0 + n_rows <= cap); no other row
+ * is touched. Per plane, row and head: a = max |x| over the finite x; scale = 2^E with E the
+ * smallest integer >= -126 for which 448 * 2^E >= a (E = 0 for a = 0); code = x / scale (exact)
+ * rounded to the nearest e4m3 value, ties to even. Infinities become +-448, NaN stays NaN. */
+int s1_op_kv_quant_async(const void* k, const void* v, int32_t dtype, int64_t k_stride, int64_t v_stride,
+                         int32_t n_rows, int32_t Hkv, int32_t hd, void* codes, float* scales, int32_t cap,
+                         int32_t pos0, void* stream);
+
+/* Reads rows pos0 .. pos0 + n_rows - 1 of an 8-bit snapshot back: code * scale, rounded once to
+ * dtype (to nearest even), held at the type's largest finite value where it lies beyond it.
+ * k, v: as in s1_op_kv_quant_async, written. */
+int s1_op_kv_dequant_async(const void* codes, const float* scales, int32_t cap, int32_t pos0, int32_t n_rows,
+                           int32_t Hkv, int32_t hd, void* k, void* v, int32_t dtype, int64_t k_stride,
+                           int64_t v_stride, void* stream);
+
+/* Attention of a batch over one shared prefix: sequence s covers rows row0[s] .. +len[s]-1
+ * (host arrays; len >= 0, sequences in ascending order without overlap, unused rows between
+ * them allowed: they are neither read nor written). Each of its queries attends to the P rows
+ * of the snapshot and causally to its own sequence's rows:
+ *   out = softmax(sm_scale q.k) v, q head h reading kv head floor(h * Hkv / Hq).
+ * The prefix is read once for up to floor(128 / (Hq / Hkv)) query rows, whichever sequences
+ * they belong to (s1_op_attention reads it once per sequence and q head); single tokens
+ * (len 1) are the serving form. q f16 [., Hq, hd] with row stride q_stride; k_new, v_new f16
+ * [., Hkv, hd] with row stride kv_stride (elements, multiples of 8; 16-byte aligned pointers),
+ * already rotated; both NULL: queries see the prefix only. kv: f16 [2, cap, Hkv, hd]
+ * (S1_KV_F16, scales NULL), or codes and scales as written by s1_op_kv_quant_async
+ * (S1_KV_E4M3; used as the f16 values s1_op_kv_dequant_async gives); rows P .. cap-1 are not
+ * read; may be NULL when P == 0. hd 64 or 128, Hq % Hkv == 0, Hq / Hkv <= 128. Softmax
+ * statistics and sums are fp32; the weights are rounded to f16 for the products. A query that
+ * sees nothing, or whose scores are all -inf, gives zeros. Values that a query does not see
+ * never reach it, whatever they hold (NaN and infinities included). out f16 [., Hq, hd],
+ * contiguous rows, 16-byte aligned. workspace: 16-byte aligned, at least the bytes that
+ * s1_op_attention_shared_workspace gives for these sizes on this device. */
+int s1_op_attention_shared_async(const void* q, int64_t q_stride, const void* k_new, const void* v_new,
+                                 int64_t kv_stride, int32_t n_seq, const int32_t* row0, const int32_t* len,
+                                 const void* kv, const float* scales, int32_t kv_format, int32_t P, int32_t cap,
+                                 int32_t Hq, int32_t Hkv, int32_t hd, float sm_scale, void* out, void* workspace,
+                                 int64_t workspace_bytes, void* stream);
+int s1_op_attention_shared_workspace(int32_t n_seq, const int32_t* len, int32_t P, int32_t Hq, int32_t Hkv,
+                                     int32_t hd, int64_t* bytes);
+
+/* Linear attention with a decay per head over packed sequences:
+ *   S_t = exp(log_decay[h]) S_{t-1} + v_t k_t^T,   o_t = scale * S_t q_t.
+ * q, k [., H, dk], v [., H, dv] of dtype S1_F16 or S1_BF16, row strides in elements (multiples
+ * of 8, 16-byte aligned pointers); dk, dv 64 or 128. log_decay: fp32 [H], <= 0 (-inf: no
+ * memory); larger values count as 0. row0, len: as in s1_op_attention_shared_async.
+ * S_in: fp32 [n_seq, H, dv, dk] initial states, sequence s reading S_in + s * s_in_stride:
+ * s_in_stride = H * dv * dk for a state of its own, 0 for one state that all sequences
+ * continue; NULL: zero. S_out: fp32 [n_seq, H, dv, dk] final states, or NULL; S_out == S_in is
+ * allowed with s_in_stride = H * dv * dk (states advanced in place), no other overlap. An empty
+ * sequence's final state is its initial one. out: dtype [., H, dv], contiguous rows, 16-byte
+ * aligned. States, and sums over rows, are fp32. workspace: as above,
+ * s1_op_linattn_workspace. A row never reaches an earlier row or another sequence, whatever it
+ * holds. */
+int s1_op_linattn_async(const void* q, const void* k, const void* v, int32_t dtype, int64_t q_stride,
+                        int64_t k_stride, int64_t v_stride, const float* log_decay, int32_t n_seq,
+                        const int32_t* row0, const int32_t* len, int32_t H, int32_t dk, int32_t dv, float scale,
+                        const float* S_in, int64_t s_in_stride, float* S_out, void* out, void* workspace,
+                        int64_t workspace_bytes, void* stream);
+int s1_op_linattn_workspace(int32_t n_seq, const int32_t* len, int32_t H, int32_t dk, int32_t dv, int64_t* bytes);
+
+/* One token for each of n sequences (row s of q, k, v, out): the recurrence above for a single
+ * step, arguments as in s1_op_linattn_async. S_out NULL leaves the states as they are. */
+int s1_op_linattn_step_async(const void* q, const void* k, const void* v, int32_t dtype, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const float* log_decay, int32_t n, int32_t H,
+                             int32_t dk, int32_t dv, float scale, const float* S_in, int64_t s_in_stride,
+                             float* S_out, void* out, void* stream);
 
 /* ---- instrumentation of a model (handles from s1.h) -------------------------------------
  * s1_profile(m, 1) starts recording CUDA events around every launch of the model on its

@@ -16,7 +16,8 @@ LIB_PATH = os.path.join(PKG, "libs1.so")
 
 S1_OK, S1_ERR_INVALID_ARG, S1_ERR_INVALID_HANDLE, S1_ERR_OOM, S1_ERR_BUDGET, S1_ERR_CUDA, \
     S1_ERR_DEVICE_TIMEOUT, S1_ERR_UNSUPPORTED = range(8)
-S1_F32, S1_BF16 = 0, 1
+S1_F32, S1_BF16, S1_F16 = 0, 1, 2
+S1_KV_F16, S1_KV_E4M3 = 0, 1             # K/V snapshot formats of op_attention_shared_async
 S1_NOALLOC_WS_FLOATS = 4 * 1024 * 1024   # fixed split-K scratch of s1_op_gemm_noalloc (include/s1_ops.h)
 S1_STAT_COUNT = 8
 PROF_NCLASS = 8
@@ -66,7 +67,7 @@ def lib():
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m prefill_only_decision_gb300.build`")
     L = C.CDLL(LIB_PATH)
-    vp, i32, f32 = C.c_void_p, C.c_int32, C.c_float
+    vp, i32, i64, f32 = C.c_void_p, C.c_int32, C.c_int64, C.c_float
     P = C.POINTER
     sig = {
         "s1_model_create": (C.c_int, [P(Shape), P(Weights), P(vp)]),
@@ -102,6 +103,17 @@ def lib():
         "s1_set_graphs": (C.c_int, [vp, C.c_int]),
         "s1_counters": (C.c_int, [vp, P(C.c_longlong), P(C.c_longlong), P(C.c_longlong)]),
         "s1_split_prefix": (C.c_int, [P(P(i32)), P(i32), i32, i32, i32, P(i32)]),
+        "s1_op_sync": (C.c_int, [vp]),
+        "s1_op_kv_quant_async": (C.c_int, [vp, vp, i32, i64, i64, i32, i32, i32, vp, vp, i32, i32, vp]),
+        "s1_op_kv_dequant_async": (C.c_int, [vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, i64, i64, vp]),
+        "s1_op_attention_shared_async": (C.c_int, [vp, i64, vp, vp, i64, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32,
+                                                   i32, f32, vp, vp, i64, vp]),
+        "s1_op_attention_shared_workspace": (C.c_int, [i32, vp, i32, i32, i32, i32, P(i64)]),
+        "s1_op_linattn_async": (C.c_int, [vp, vp, vp, i32, i64, i64, i64, vp, i32, vp, vp, i32, i32, i32, f32, vp, i64,
+                                          vp, vp, vp, i64, vp]),
+        "s1_op_linattn_workspace": (C.c_int, [i32, vp, i32, i32, i32, P(i64)]),
+        "s1_op_linattn_step_async": (C.c_int, [vp, vp, vp, i32, i64, i64, i64, vp, i32, i32, i32, i32, f32, vp, i64,
+                                               vp, vp, vp]),
         "s1_gemm_plan": (C.c_int, [i32, i32, i32, i32, i32, i32, P(i32)]),
     }
     for name, (res, args) in sig.items():
@@ -456,3 +468,74 @@ def gemm_plan(M: int, N: int, K: int, epi: int, num_sms: int, pair: bool = False
 def op_rmsnorm(x: int, w: int, R: int, d: int, eps: float, out: int, stream: int = 0):
     check(lib().s1_op_rmsnorm(C.c_void_p(x), C.c_void_p(w), R, d, eps, C.c_void_p(out),
                               C.c_void_p(stream) if stream else None))
+
+
+# -- stream-ordered operators over a long shared prefix ----------------------------------------
+# Device pointers are integers (0: NULL), strides in elements, row0 and lens host integers; the
+# calls return once the work is on `stream`.
+def op_sync(stream: int = 0):
+    """Wait for `stream` and report a device-side timeout of the operators below (s1_op_sync)."""
+    check(lib().s1_op_sync(stream))
+
+
+def op_kv_quant_async(k: int, v: int, dtype: int, k_stride: int, v_stride: int, n_rows: int, Hkv: int, hd: int,
+                      codes: int, scales: int, cap: int, pos0: int, stream: int = 0):
+    """Write K/V rows into an 8-bit snapshot (s1_op_kv_quant_async)."""
+    check(lib().s1_op_kv_quant_async(k, v, dtype, k_stride, v_stride, n_rows, Hkv, hd, codes, scales, cap, pos0,
+                                     stream))
+
+
+def op_kv_dequant_async(codes: int, scales: int, cap: int, pos0: int, n_rows: int, Hkv: int, hd: int, k: int, v: int,
+                        dtype: int, k_stride: int, v_stride: int, stream: int = 0):
+    """Read rows of an 8-bit snapshot back (s1_op_kv_dequant_async)."""
+    check(lib().s1_op_kv_dequant_async(codes, scales, cap, pos0, n_rows, Hkv, hd, k, v, dtype, k_stride, v_stride,
+                                       stream))
+
+
+def _seq_arrays(row0, lens):
+    r0, ln = _i32(row0), _i32(lens)
+    if r0.shape != ln.shape or r0.ndim != 1:
+        raise ValueError("row0 and lens must be 1-D and of the same length")
+    return r0, ln
+
+
+def op_attention_shared_async(q: int, q_stride: int, k_new: int, v_new: int, kv_stride: int, row0, lens, kv: int,
+                              scales: int, kv_format: int, P: int, cap: int, Hq: int, Hkv: int, hd: int,
+                              sm_scale: float, out: int, workspace: int, workspace_bytes: int, stream: int = 0):
+    """Attention of a batch over one shared prefix (s1_op_attention_shared_async)."""
+    r0, ln = _seq_arrays(row0, lens)
+    check(lib().s1_op_attention_shared_async(q, q_stride, k_new, v_new, kv_stride, len(r0), r0.ctypes.data,
+                                             ln.ctypes.data, kv, scales, kv_format, P, cap, Hq, Hkv, hd, sm_scale,
+                                             out, workspace, workspace_bytes, stream))
+
+
+def op_attention_shared_workspace(lens, P: int, Hq: int, Hkv: int, hd: int) -> int:
+    """Workspace bytes of op_attention_shared_async for these sizes on the current device."""
+    ln, out = _i32(lens), C.c_int64()
+    check(lib().s1_op_attention_shared_workspace(len(ln), ln.ctypes.data, P, Hq, Hkv, hd, C.byref(out)))
+    return out.value
+
+
+def op_linattn_async(q: int, k: int, v: int, dtype: int, q_stride: int, k_stride: int, v_stride: int, log_decay: int,
+                     row0, lens, H: int, dk: int, dv: int, scale: float, S_in: int, s_in_stride: int, S_out: int,
+                     out: int, workspace: int, workspace_bytes: int, stream: int = 0):
+    """Linear attention with a decay per head over packed sequences (s1_op_linattn_async)."""
+    r0, ln = _seq_arrays(row0, lens)
+    check(lib().s1_op_linattn_async(q, k, v, dtype, q_stride, k_stride, v_stride, log_decay, len(r0), r0.ctypes.data,
+                                    ln.ctypes.data, H, dk, dv, scale, S_in, s_in_stride, S_out, out, workspace,
+                                    workspace_bytes, stream))
+
+
+def op_linattn_workspace(lens, H: int, dk: int, dv: int) -> int:
+    """Workspace bytes of op_linattn_async for these sizes on the current device."""
+    ln, out = _i32(lens), C.c_int64()
+    check(lib().s1_op_linattn_workspace(len(ln), ln.ctypes.data, H, dk, dv, C.byref(out)))
+    return out.value
+
+
+def op_linattn_step_async(q: int, k: int, v: int, dtype: int, q_stride: int, k_stride: int, v_stride: int,
+                          log_decay: int, n: int, H: int, dk: int, dv: int, scale: float, S_in: int, s_in_stride: int,
+                          S_out: int, out: int, stream: int = 0):
+    """One token of the recurrence for each of n sequences (s1_op_linattn_step_async)."""
+    check(lib().s1_op_linattn_step_async(q, k, v, dtype, q_stride, k_stride, v_stride, log_decay, n, H, dk, dv, scale,
+                                         S_in, s_in_stride, S_out, out, stream))

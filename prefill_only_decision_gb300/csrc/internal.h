@@ -179,4 +179,60 @@ cudaError_t launch_short_conv(const float* x, float* out, int ld, int channels, 
                               int layer_g, cudaStream_t st);
 cudaError_t launch_rope_table(float2* tab, int max_pos, int hd, double theta, cudaStream_t st);
 
+// ---- operators over a long shared prefix (stream-ordered; s1_ops.h) ----
+// Element types of operator rows (the values of S1_F32 / S1_BF16 / S1_F16).
+enum ElemType { ELEM_F32 = 0, ELEM_BF16 = 1, ELEM_F16 = 2 };
+
+// Packed sequences of one launch, passed by value (a captured graph keeps its own copy): rows of
+// sequence s are row0[s] .. row0[s] + cum[s + 1] - cum[s] - 1, cum[s] the rows of the sequences
+// before it.
+template <int N>
+struct SeqTab {
+  int n;
+  int cum[N + 1];
+  int row0[N];
+};
+constexpr int SEQ_TAB_SMALL = 64, SEQ_TAB_LARGE = 2048;   // sequences per launch (0.5 KB, 16 KB)
+
+// Device word of the current device that bounded waits of the operators record in.
+cudaError_t op_error_word(int** out);
+
+cudaError_t launch_kv_quant(const void* k, const void* v, int dtype, int64_t k_stride, int64_t v_stride, int rows,
+                            int Hkv, int hd, uint8_t* codes, float* scales, int cap, int pos0, cudaStream_t st);
+cudaError_t launch_kv_dequant(const uint8_t* codes, const float* scales, int cap, int pos0, int rows, int Hkv, int hd,
+                              void* k, void* v, int dtype, int64_t k_stride, int64_t v_stride, cudaStream_t st);
+
+struct SharedAttnArgs {
+  const f16 *q, *kn, *vn;      // kn, vn NULL: prefix only
+  int64_t q_stride, kv_stride;
+  const void* kv;              // f16 or e4m3 [2, cap, Hkv, hd]
+  const float* scales;         // [2, Hkv, cap] (e4m3)
+  int e4m3, P, cap, Hq, Hkv, hd;
+  float scale;
+  f16* out;
+  void* ws;
+};
+// Sequences as host arrays (empty ones allowed).
+cudaError_t launch_attention_shared(const SharedAttnArgs& a, int n_seq, const int* row0, const int* len, int num_sms,
+                                    cudaStream_t st);
+int64_t attention_shared_ws_bytes(int n_seq, const int* len, int P, int Hq, int Hkv, int hd, int num_sms);
+
+struct LinAttnArgs {
+  const void *q, *k, *v;
+  int dtype;                   // ELEM_F16 or ELEM_BF16
+  int64_t q_stride, k_stride, v_stride;
+  const float* log_decay;
+  int H, dk, dv;
+  float scale;
+  const float* S_in;
+  int64_t s_in_stride;
+  float* S_out;
+  void* out;
+  void* ws;
+};
+cudaError_t launch_linattn(const LinAttnArgs& a, int n_seq, const int* row0, const int* len, int num_sms,
+                           cudaStream_t st);
+int64_t linattn_ws_bytes(int n_seq, const int* len, int H, int dk, int dv, int num_sms);
+cudaError_t launch_linattn_step(const LinAttnArgs& a, int n, cudaStream_t st);
+
 }  // namespace s1
