@@ -883,6 +883,19 @@ bool make_map(CUtensorMap* out, const void* ptr, int rows, int cols, int box_row
 
 }  // namespace tc
 
+bool encode_tensor_map(CUtensorMap* out, CUtensorMapDataType dtype, int rank, const void* ptr, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
+  if (rank < 1 || rank > 5) return false;
+  tc::EncodeTiledFn enc = tc::get_encode();
+  if (!enc) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], e[5];
+  for (int i = 0; i < rank; ++i) { d[i] = dims[i]; b[i] = box[i]; e[i] = 1; }
+  for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
+  return enc(out, dtype, (cuuint32_t)rank, const_cast<void*>(ptr), d, st, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tensor_map(CUtensorMap* out, CUtensorMapDataType dtype, int rank, const void* ptr, const uint64_t* dims,
                 const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
   static std::mutex mu;
@@ -895,15 +908,7 @@ bool tensor_map(CUtensorMap* out, CUtensorMapDataType dtype, int rank, const voi
   std::lock_guard<std::mutex> lk(mu);
   auto it = cache.find(key);
   if (it != cache.end()) { *out = it->second; return true; }
-  tc::EncodeTiledFn enc = tc::get_encode();
-  if (!enc) return false;
-  cuuint64_t d[5], st[4];
-  cuuint32_t b[5], e[5];
-  for (int i = 0; i < rank; ++i) { d[i] = dims[i]; b[i] = box[i]; e[i] = 1; }
-  for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
-  CUresult r = enc(out, dtype, (cuuint32_t)rank, const_cast<void*>(ptr), d, st, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return false;
+  if (!encode_tensor_map(out, dtype, rank, ptr, dims, strides, box, swizzle)) return false;
   if (cache.size() > 4096) cache.clear();
   cache[key] = *out;
   return true;

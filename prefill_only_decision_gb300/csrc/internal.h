@@ -196,6 +196,9 @@ constexpr int SEQ_TAB_SMALL = 64, SEQ_TAB_LARGE = 2048;   // sequences per launc
 
 // Device word of the current device that bounded waits of the operators record in.
 cudaError_t op_error_word(int** out);
+// A tensor map encoded afresh (arguments as tensor_map's).
+bool encode_tensor_map(CUtensorMap* out, CUtensorMapDataType dtype, int rank, const void* ptr, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
 
 cudaError_t launch_kv_quant(const void* k, const void* v, int dtype, int64_t k_stride, int64_t v_stride, int rows,
                             int Hkv, int hd, uint8_t* codes, float* scales, int cap, int pos0, cudaStream_t st);

@@ -14,10 +14,6 @@ int set_error(int code, const char* msg);   // s1_api.cu: the thread-local messa
 static_assert((int)ELEM_F32 == (int)S1_F32 && (int)ELEM_BF16 == (int)S1_BF16 && (int)ELEM_F16 == (int)S1_F16,
               "element types are the ABI's");
 
-// Bounded waits of the operators record here; one word per device, cleared when it is reported.
-__device__ int g_op_err;
-
-cudaError_t op_error_word(int** out) { return cudaGetSymbolAddress(reinterpret_cast<void**>(out), g_op_err); }
 }  // namespace s1
 
 namespace {
