@@ -2,32 +2,38 @@
 //
 // Query row i of sequence s attends to the P rows of the snapshot and to rows 0 .. i of its own
 // sequence: o = softmax(scale q.k) v. All sequences see the same prefix, so their query rows (and
-// the G = Hq / Hkv q heads that share a kv head) are packed into tiles of 128 products' rows:
+// the G = Hq / Hkv q heads that share a kv head) are packed into tiles of 128 matrix rows:
 // RT = floor(128 / G) query rows x G heads per tile, whichever sequences the rows belong to. A
 // tile reads each 128-key tile of the prefix once; s1_op_attention's kernel, one tile per
-// (sequence, q head), would read it once per sequence and head.
+// (sequence, q head), reads it once per sequence and head.
 //
-// One pass over the keys with a running maximum and sum in fp32. Work items are (kv head, tile of
-// query rows); when there are fewer items than SMs the key tiles of an item are split over `ns`
-// CTAs whose (o, m, l) are joined in part order by combine_kernel (no atomics: the same bits every
-// time). One CTA per SM, 14 warps:
-//   warp 0      TMA producer: prefix tiles (f16 K/V tiles, or e4m3 tiles into a ring of raw stages)
-//   warp 1      TMEM allocation, MMA issue: S = Q K^T into one of two TMEM buffers, O += P V with P
-//               read from TMEM (f16, written by the softmax warps; no shared-memory round trip)
-//   warps 2-9   softmax, two threads per row (64 keys each): mask, running max with a lazy rescale
-//               (O and l move only when the row's maximum grows by more than 2^8), P back to TMEM;
-//               warps whose 32 rows are all past the tile's last row only keep the barriers going
+// One pass over the keys with a running maximum and sum in fp32, in two streams of S = Q K^T,
+// softmax, O += P V that take turns on the tensor cores, so that one stream's softmax runs under
+// the other's products. The streams are two query tiles over the same key tiles or, for the last
+// query tile of an odd count, one query tile over the even and the odd key tiles (joined at the
+// end). Work items are (kv head, pair of query tiles); an item's key tiles are split over `ns`
+// CTAs when that shortens the call, and combine_kernel joins their (o, m, l) in part order (no
+// atomics: the same bits every time). One CTA per SM, 15 warps:
+//   warp 0      TMA producer: prefix tiles (f16 tiles, or e4m3 tiles into a ring of raw stages)
+//   warps 1, 14 MMA issue of stream 0 and 1 (a stream's products wait for its own softmax only)
+//   warps 2-5, 6-9  softmax of stream 0, 1: one thread per row (TMEM lane). Running max with a lazy
+//               rescale (O and l move only when the row's maximum grows by more than 2^8). P (f16)
+//               goes back into the second half of the TMEM columns of S and is the A operand of
+//               O += P V from there: no shared-memory round trip. Warps whose 32 rows are all past
+//               the tile's last row only keep the barriers going.
 //   warps 10-13 loaders: the batch's own keys (gathered row by row through the sequence table), and
 //               e4m3 prefix tiles: codes from the raw stage to f16 in the MMA's swizzled layout
+// K and V tiles share one ring of stages in the order the products take them.
 // Own keys are packed the same way as queries: row r's visible own keys are the packed rows
 // start(r) .. r, so one masked tile serves many short sequences. A masked weight is an exact zero,
-// but 0 x NaN is not: the loaders replace non-finite own V elements by 0 and flag the tile, and
-// the epilogue of a flagged tile adds them to exactly the rows that see them.
+// but 0 x NaN is not: the loaders replace non-finite own V elements by 0 and flag the CTA, and
+// the epilogue then adds them to exactly the rows that see them.
 // An e4m3 code times its scale is exact in f16 for scales 2^-6 .. 2^7 (and rounded as the read-back
 // rounds it otherwise), so the products run on f16 operands as with an f16 snapshot.
 // Every mbarrier wait is bounded; on expiry an error word is set and every role leaves.
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include <cuda_fp8.h>
 
@@ -39,11 +45,9 @@ namespace sha {
 using namespace t5;
 
 constexpr int BQ = 128, BKV = 128;
-constexpr int NTHREADS = 14 * 32;
-constexpr int ST = 2;                        // f16 K and V stages
-constexpr int RS = 3;                        // raw e4m3 stages (K and V tiles in turn)
-constexpr int TMEM_COLS = 512;               // S 2 x 128 | O hd at 256 | P 2 x 64 at 384
-constexpr int T_O = 256, T_P = 384;
+constexpr int NTHREADS = 15 * 32;
+constexpr int TMEM_COLS = 512;               // S of stream x at 128 x, O at 256 + 128 x
+constexpr int T_O = 256;
 constexpr int ERR_TIMEOUT = 0x401;
 
 __device__ int g_err;                        // bounded waits record here (one word per device)
@@ -51,24 +55,76 @@ __device__ int g_err;                        // bounded waits record here (one w
 struct Plan {
   int V;          // packed query rows
   int G, RT, MT;  // q heads per kv head, query rows per tile, tiles
+  int MP;         // pairs of tiles: work items per kv head
+  int nt;         // tiles per item (1 or 2)
   int ns;         // key parts per item
   int ncache;     // prefix tiles
 };
 
+// Shared memory: Q tiles, stages of f16 K or V tiles, raw e4m3 stages. Two query tiles: F stages that
+// both streams read; one query tile: its Q and a ring of FR stages for each stream (227 KB at hd 128:
+// 2 x 32 + 5 x 32, or 1 x 32 + 6 x 32; with raw stages 64 + 3 x 32 + 64, or 32 + 4 x 32 + 64).
 template <int HD, bool E4M3>
 struct Lay {
   static constexpr int TILE = BKV * HD * 2;
   static constexpr int RAW = BKV * HD;
-  static constexpr int Q = 0;                             // HD/64 boxes of [128 rows][128 B]
-  static constexpr int K = Q + BQ * HD * 2;
-  static constexpr int V = K + ST * TILE;
-  static constexpr int R = V + ST * TILE;
-  static constexpr int XCH = R + (E4M3 ? RS * RAW : 0);   // row maxima / sums of the halves [3][2][BQ]
-  static constexpr int BAR = XCH + 3 * 2 * BQ * 4;
+  static constexpr int F = HD == 128 ? (E4M3 ? 3 : 5) : (E4M3 ? 5 : 7);
+  static constexpr int FR = (F + 1) / 2;
+  static constexpr int RS = E4M3 ? (HD == 128 ? 4 : 6) : 1;
+  static constexpr int Q = 0;                             // per tile HD/64 boxes of [128 rows][128 B]
+  static constexpr int KV2 = Q + 2 * BQ * HD * 2;         // stages with two query tiles
+  static constexpr int KV1 = Q + BQ * HD * 2;             // with one
+  static constexpr int R = KV2 + F * TILE;
+  static constexpr int BAR = R + (E4M3 ? RS * RAW : 0);
   static constexpr int USED = BAR + 512 + 1024;           // barriers, alignment slack
   // above half an SM: each CTA allocates all of TMEM, so two never share one
   static constexpr int BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
+  static constexpr int OSTR = HD + 4;                     // floats per row of a stream's published sums
+  static_assert(KV1 + 2 * FR * TILE <= R, "both rings fit");
+  static_assert(BQ * OSTR * 4 <= 2 * FR * TILE, "published sums fit the K/V stages");
 };
+
+// The tiles of K and V in the order the products take them: K_0 .. K_{lead-1}, then V_t, K_{t+lead}
+// for t = 0, 1, ... (lead = 1 when both streams take the same key tiles, 2 when they take turns).
+// f(slot, phase, is_v, tile) returns false to stop. With one query tile a stream only ever waits for
+// its own slots: a parity wait must never run more than one phase ahead of a slot, which waiting
+// past the other stream's fills (they complete in any order) could.
+template <int F, int FR, typename Fn>
+__device__ __forceinline__ void for_ring(int n, bool two, Fn f) {
+  int c[2] = {0, 0};
+  auto step = [&](bool is_v, int t) {
+    if (two) {
+      const int i = c[0]++;
+      return f(i % F, (i / F) & 1, is_v, t);
+    }
+    const int i = (t & 1) ? c[1]++ : c[0]++;
+    return f(((t & 1) ? FR : 0) + i % FR, (i / FR) & 1, is_v, t);
+  };
+  const int lead = two ? 1 : 2;
+  for (int t = 0; t < lead && t < n; ++t)
+    if (!step(false, t)) return;
+  for (int t = 0; t < n; ++t) {
+    if (!step(true, t)) return;
+    if (t + lead < n && !step(false, t + lead)) return;
+  }
+}
+
+// Two fp32 lanes at once.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float hi2(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
 
 // The sequence that packed row vr (< cum[n]) belongs to.
 template <int N>
@@ -91,16 +147,17 @@ __device__ __forceinline__ uint32_t drop_nonfinite2(uint32_t h2) {
   return h2;
 }
 
-// Sixteen e4m3 codes times scale to f16 (round to nearest even, held at +-65504). fast: the scale
+// Sixteen e4m3 codes times scale to f16 (round to nearest even, held at +-65504). FAST: the scale
 // is an f16 value of at most 2^7, so the f16 product is the rounded value and cannot overflow.
-__device__ __forceinline__ void codes_to_half(const uint4 c, float scale, bool fast, uint32_t* h) {
+template <bool FAST>
+__device__ __forceinline__ void codes_to_half(const uint4 c, float scale, uint32_t* h) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   const __half2 s2 = __float2half2_rn(scale);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const __half2 x = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3));
     __half2 y;
-    if (fast) {
+    if constexpr (FAST) {
       y = __hmul2(x, s2);
     } else {
       const float2 f = __half22float2(x);
@@ -117,50 +174,45 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     shared_kernel(const __grid_constant__ SeqTab<N> tab, const __grid_constant__ CUtensorMap mapKV,
                   const __grid_constant__ SharedAttnArgs a, const Plan pl) {
   using L = Lay<HD, E4M3>;
-  constexpr int NB = HD / 64;
+  constexpr int NB = HD / 64, F = L::F, FR = L::FR, NS = 2 * FR > F ? 2 * FR : F, RS = L::RS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint64_t* bars = (uint64_t*)(sm + L::BAR);
   uint64_t* q_full = bars;
-  uint64_t* k_full = bars + 1;                 // [ST]
-  uint64_t* v_full = k_full + ST;              // [ST]
-  uint64_t* k_empty = v_full + ST;             // [ST]
-  uint64_t* v_empty = k_empty + ST;            // [ST]
-  uint64_t* s_full = v_empty + ST;             // [2]
-  uint64_t* s_empty = s_full + 2;              // [2]
-  uint64_t* p_full = s_empty + 2;              // [2]
-  uint64_t* o_done = p_full + 2;               // [2]
-  uint64_t* mma_idle = o_done + 2;
-  uint64_t* xbar = mma_idle + 1;               // [4 quadrants][3]: the two warps of a row quadrant meet
-  uint64_t* raw_full = xbar + 12;              // [RS]
+  uint64_t* full = bars + 1;                   // [NS]
+  uint64_t* empty = full + NS;                 // [NS]
+  uint64_t* s_full = empty + NS;               // [2] by stream
+  uint64_t* p_full = s_full + 2;               // [2]
+  uint64_t* o_done = p_full + 2;               // [2] the stream's last product has completed
+  uint64_t* mma_idle = o_done + 2;             // [2]
+  uint64_t* joined = mma_idle + 2;             // [4 quadrants] stream 1's sums are published
+  uint64_t* raw_full = joined + 4;             // [RS]
   uint64_t* raw_empty = raw_full + RS;         // [RS]
   uint32_t* tmem_slot = (uint32_t*)(raw_empty + RS);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // some own V element of this CTA is not finite
-  static_assert((1 + 4 * ST + 9 + 12 + 2 * RS) * 8 + 16 <= 512, "barriers fit");
+  static_assert((1 + 2 * NS + 6 + 2 + 4 + 2 * RS) * 8 + 16 <= 512, "barriers fit");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int part = (int)(blockIdx.x % pl.ns), item = (int)(blockIdx.x / pl.ns);
-  const int mt = item % pl.MT, g = item / pl.MT;
-  const int v0 = mt * pl.RT;                   // first packed row of the tile, and one past its last
-  const int v1 = min(pl.V, v0 + pl.RT);
+  const int mp = item % pl.MP, g = item / pl.MP;
+  const bool two = 2 * mp + 1 < pl.MT;         // two query tiles; else one over alternate key tiles
+  const int v0 = 2 * mp * pl.RT;               // first packed row of the item, and one past its last
+  const int v1 = min(pl.V, v0 + (two ? 2 : 1) * pl.RT);
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 8);
-    for (int s = 0; s < ST; ++s) {
-      mbar_init(&k_full[s], E4M3 ? 4 : 5);
-      mbar_init(&v_full[s], E4M3 ? 4 : 5);
-      mbar_init(&k_empty[s], 1);
-      mbar_init(&v_empty[s], 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], E4M3 ? 4 : 5);
+      mbar_init(&empty[s], two ? 2 : 1);       // the streams that read the slot
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&s_full[b], 1);
-      mbar_init(&s_empty[b], 8);
-      mbar_init(&p_full[b], 8);
-      mbar_init(&o_done[b], 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&mma_idle[x], 1);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);
+      mbar_init(&o_done[x], 1);
     }
-    mbar_init(mma_idle, 1);
-    for (int x = 0; x < 12; ++x) mbar_init(&xbar[x], 2);
+    for (int x = 0; x < 4; ++x) mbar_init(&joined[x], 1);
     for (int r = 0; r < RS; ++r) { mbar_init(&raw_full[r], 1); mbar_init(&raw_empty[r], 4); }
     *abort_flag = 0;
     *v_flag = 0;
@@ -175,7 +227,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int total = pl.ncache + nown;
   const int per = (total + pl.ns - 1) / pl.ns;
   const int jb = min(total, part * per), je = min(total, jb + per);
-  const int n = je - jb;
+  const int n = je - jb, lead = two ? 1 : 2;
+  uint8_t* kvst = sm + (two ? L::KV2 : L::KV1);
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -183,105 +236,93 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (warp == 0) {
     // ---- TMA producer
     if (lane == 0) {
-      int i = 0;
-      if constexpr (E4M3) {
-        int it = 0;                            // raw items issued: K and V tiles in turn
-        bool ok = true;
-        for (; i < n && jb + i < pl.ncache && ok; ++i)
-          for (int pln = 0; pln < 2 && ok; ++pln, ++it) {
-            const int r = it % RS;
-            ok = mbar_wait(&raw_empty[r], ((it / RS) & 1) ^ 1, abort_flag, &g_err, ERR_TIMEOUT);
-            if (!ok) break;
-            mbar_expect_tx(&raw_full[r], L::RAW);
-            tma4(sm + L::R + r * L::RAW, &mapKV, &raw_full[r], 0, g, (jb + i) * BKV, pln);
-          }
+      if constexpr (E4M3) {                    // raw items: the ring's prefix tiles in its order
+        int issued = 0;
+        for_ring<F, FR>(n, two, [&](int, int, bool is_v, int t) {
+          if (jb + t >= pl.ncache) return true;
+          const int r = issued % RS;
+          if (!mbar_wait(&raw_empty[r], ((issued / RS) & 1) ^ 1, abort_flag, &g_err, ERR_TIMEOUT)) return false;
+          mbar_expect_tx(&raw_full[r], L::RAW);
+          tma4(sm + L::R + r * L::RAW, &mapKV, &raw_full[r], 0, g, (jb + t) * BKV, is_v ? 1 : 0);
+          ++issued;
+          return true;
+        });
         if (*abort_flag)                       // copies in flight land before the CTA leaves
-          for (int x = it > RS ? it - RS : 0; x < it; ++x) mbar_drain(&raw_full[x % RS], (x / RS) & 1);
+          for (int x = issued > RS ? issued - RS : 0; x < issued; ++x) mbar_drain(&raw_full[x % RS], (x / RS) & 1);
       } else {
-        bool ok = true;
-        int ki = 0, vi = 0;                    // fills begun
-        for (; i < n && ok; ++i) {
-          const int s = i % ST, j = jb + i;
-          const uint32_t ph = ((i / ST) & 1) ^ 1;
-          ok = mbar_wait(&k_empty[s], ph, abort_flag, &g_err, ERR_TIMEOUT);
-          if (!ok) break;
+        uint32_t fills = 0;                    // per slot: begun (bit s), parity of the last fill (bit 16 + s)
+        for_ring<F, FR>(n, two, [&](int s, int ph, bool is_v, int t) {
+          const int j = jb + t;
+          if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, &g_err, ERR_TIMEOUT)) return false;
           if (j < pl.ncache) {
-            mbar_expect_tx(&k_full[s], L::TILE);
+            mbar_expect_tx(&full[s], L::TILE);
             for (int b = 0; b < NB; ++b)
-              tma4(sm + L::K + s * L::TILE + b * BKV * 128, &mapKV, &k_full[s], 64 * b, g, j * BKV, 0);
+              tma4(kvst + s * L::TILE + b * BKV * 128, &mapKV, &full[s], 64 * b, g, j * BKV, is_v ? 1 : 0);
           } else {
-            mbar_arrive(&k_full[s]);
+            mbar_arrive(&full[s]);
           }
-          ki = i + 1;
-          ok = mbar_wait(&v_empty[s], ph, abort_flag, &g_err, ERR_TIMEOUT);
-          if (!ok) break;
-          if (j < pl.ncache) {
-            mbar_expect_tx(&v_full[s], L::TILE);
-            for (int b = 0; b < NB; ++b)
-              tma4(sm + L::V + s * L::TILE + b * BKV * 128, &mapKV, &v_full[s], 64 * b, g, j * BKV, 1);
-          } else {
-            mbar_arrive(&v_full[s]);
-          }
-          vi = i + 1;
-        }
-        if (*abort_flag) {
-          for (int x = ki > ST ? ki - ST : 0; x < ki; ++x) mbar_drain(&k_full[x % ST], (x / ST) & 1);
-          for (int x = vi > ST ? vi - ST : 0; x < vi; ++x) mbar_drain(&v_full[x % ST], (x / ST) & 1);
-        }
+          fills = (fills & ~(1u << (16 + s))) | 1u << s | (uint32_t)ph << (16 + s);
+          return true;
+        });
+        if (*abort_flag)
+          for (int s = 0; s < NS; ++s)
+            if ((fills >> s) & 1) mbar_drain(&full[s], (fills >> (16 + s)) & 1);
       }
     }
-  } else if (warp == 1) {
-    // ---- MMA issuer
-    if (lane == 0 && n > 0) {
-      constexpr uint32_t ID_S = idesc_f16(BKV, 0, 0, 0), ID_O = idesc_f16(HD, 0, 0, 1);
-      bool ok = mbar_wait(q_full, 0, abort_flag, &g_err, ERR_TIMEOUT);
-      auto issue_s = [&](int i) -> bool {      // S_i = Q K_i^T into buffer i & 1
-        const int s = i % ST, b = i & 1;
-        if (!mbar_wait(&k_full[s], (i / ST) & 1, abort_flag, &g_err, ERR_TIMEOUT)) return false;
-        if (!mbar_wait(&s_empty[b], ((i >> 1) & 1) ^ 1, abort_flag, &g_err, ERR_TIMEOUT)) return false;
-        fence_after();
-        const uint32_t qa = smem_u32(sm + L::Q), ka = smem_u32(sm + L::K + s * L::TILE);
+  } else if (warp == 1 || warp == 14) {
+    // ---- MMA issue of stream x: the whole warp waits, one lane issues. A stream's products run in
+    // the order they are issued, so S of its next tile may take the columns that P V reads before it
+    const int x = warp == 1 ? 0 : 1;
+    const bool leader = elect_one();
+    constexpr uint32_t ID_S = idesc_f16(BKV, 0, 0, 0), ID_O = idesc_f16(HD, 0, 0, 1);
+    const uint32_t tS = tmem + x * 128, tP = tS + 64, tO = tmem + T_O + x * 128;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_err, ERR_TIMEOUT) ? 1 : 0) != 0;
+    };
+    const uint64_t qd = desc_sw128(smem_u32(sm + L::Q) + (two && x ? BQ * HD * 2 : 0), 16);
+    int done = 0;                              // products P V issued
+    if (n > 0 && wait(q_full, 0))
+      for_ring<F, FR>(n, two, [&](int s, int ph, bool is_v, int t) {
+        if (!two && (t & 1) != x) return true;           // the other stream's tile
+        if (!wait(&full[s], ph)) return false;
+        const uint32_t addr = smem_u32(kvst + s * L::TILE);
+        if (is_v) {
+          if (!wait(&p_full[x], done & 1)) return false;
+          fence_after();
+          if (leader) {                        // O += P V
+            const uint64_t vd = desc_sw128(addr, BKV * 128);
 #pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint32_t off = (uint32_t)((kk >> 2) * (128 * 128) + (kk & 3) * 32);
-          mma_ss(tmem + b * 128, desc_sw128(qa + off, 16), desc_sw128(ka + off, 16), ID_S, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < BKV / 16; ++kk)
+              mma_ts(tO, tP + kk * 8, vd + (uint64_t)(kk * 16 * 128 >> 4), ID_O, (done > 0 || kk > 0) ? 1u : 0u);
+            if (t + (two ? 1 : 2) >= n) commit(&o_done[x]);
+            commit(&empty[s]);
+          }
+          ++done;
+        } else {
+          fence_after();
+          if (leader) {                        // S = Q K^T
+            const uint64_t kd = desc_sw128(addr, 16);
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; ++kk) {
+              const uint64_t off = (uint64_t)(((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4);
+              mma_ss(tS, qd + off, kd + off, ID_S, kk > 0 ? 1u : 0u);
+            }
+            commit(&s_full[x]);
+            commit(&empty[s]);
+          }
         }
-        commit(&s_full[b]);
-        commit(&k_empty[s]);
+        __syncwarp();
         return true;
-      };
-      auto issue_pv = [&](int i) -> bool {     // O += P_i V_i
-        const int s = i % ST, b = i & 1;
-        if (!mbar_wait(&p_full[b], (i >> 1) & 1, abort_flag, &g_err, ERR_TIMEOUT)) return false;
-        if (!mbar_wait(&v_full[s], (i / ST) & 1, abort_flag, &g_err, ERR_TIMEOUT)) return false;
-        fence_after();
-        const uint32_t va = smem_u32(sm + L::V + s * L::TILE);
-#pragma unroll
-        for (int kk = 0; kk < BKV / 16; ++kk)
-          mma_ts(tmem + T_O, tmem + T_P + b * 64 + kk * 8, desc_sw128(va + kk * 16 * 128, BKV * 128), ID_O,
-                 (i > 0 || kk > 0) ? 1u : 0u);
-        commit(&o_done[b]);
-        commit(&v_empty[s]);
-        return true;
-      };
-      if (ok) ok = issue_s(0);
-      for (int i = 0; i < n && ok; ++i) {
-        if (i + 1 < n) ok = issue_s(i + 1);
-        if (ok) ok = issue_pv(i);
-      }
-      commit(mma_idle);
-      mbar_drain(mma_idle, 0);                 // every MMA issued above has completed
+      });
+    if (leader) {
+      commit(&mma_idle[x]);
+      mbar_drain(&mma_idle[x], 0);             // every MMA issued above has completed
     }
   } else if (warp >= 10) {
     // ---- loaders: rows 32 lw .. +31 of every tile
     const int lw = warp - 10;
     auto wwait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_err, ERR_TIMEOUT) ? 1 : 0) != 0;
-    };
-    auto publish = [&](uint64_t* bar) {        // this warp's writes to shared memory are the MMA's to read
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
     };
     // own rows of tile jo: CH chunks of 16 bytes per row, RPI rows per pass of the warp
     constexpr int CH = HD / 8, RPI = 32 / CH, PASSES = 32 / RPI;
@@ -315,237 +356,336 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       if (bad) *v_flag = 1;
     };
-    bool ok = true;
-    for (int i = 0; i < n && ok; ++i) {
-      const int s = i % ST, j = jb + i;
-      const uint32_t ph = ((i / ST) & 1) ^ 1;
-      const bool cache = j < pl.ncache;
-#pragma unroll
-      for (int pln = 0; pln < 2; ++pln) {
-        uint64_t* empty = pln ? &v_empty[s] : &k_empty[s];
-        uint64_t* full = pln ? &v_full[s] : &k_full[s];
-        uint8_t* dst = sm + (pln ? L::V : L::K) + s * L::TILE;
-        if (!cache) {
-          ok = wwait(empty, ph);
-          if (!ok) break;
-          load_own(j - pl.ncache, pln ? a.vn : a.kn, dst, pln == 1);
-        } else if constexpr (E4M3) {
-          const int it = 2 * i + pln, r = it % RS;
-          const int key = j * BKV + lw * 32 + lane;
-          const float sc = key < a.P ? a.scales[((int64_t)pln * a.Hkv + g) * a.cap + key] : 1.f;
-          const bool fast = __all_sync(0xffffffffu, sc <= 128.f && __half2float(__float2half_rn(sc)) == sc);
-          ok = wwait(&raw_full[r], (it / RS) & 1) && wwait(empty, ph);
-          if (!ok) break;
-          // LPR lanes of 16 codes per row; the lanes of a row's second 64 columns (or of odd rows)
-          // write their two 16-byte chunks in the other order, so that no store conflicts
-          constexpr int LPR = HD / 16, RP = 32 / LPR;
-          const int ci = lane % LPR;
-          const uint8_t* raw = sm + L::R + r * L::RAW + (lw * 32) * HD + lane * 16;
-#pragma unroll 4
-          for (int p = 0; p < 32 / RP; ++p) {
-            const int lr = p * RP + lane / LPR, row = lw * 32 + lr;
-            const uint4 c = *reinterpret_cast<const uint4*>(raw + p * RP * HD);
-            uint32_t h[8];
-            codes_to_half(c, __shfl_sync(0xffffffffu, sc, lr), fast, h);
-            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-            const bool swap = HD == 128 && ci >= 4;
-            uint8_t* d = dst + (ci >> 2) * (BKV * 128) + row * 128;
-            const int c0 = (2 * ci) & 7;
-            *reinterpret_cast<uint4*>(d + (((c0 + (swap ? 1 : 0)) ^ (row & 7)) << 4)) = swap ? hi : lo;
-            *reinterpret_cast<uint4*>(d + (((c0 + (swap ? 0 : 1)) ^ (row & 7)) << 4)) = swap ? lo : hi;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&raw_empty[r]);
-        } else {
-          ok = wwait(empty, ph);               // the producer's tile: only the arrival
-          if (!ok) break;
-        }
-        publish(full);
-      }
+    // the scale of this lane's row of a prefix tile (1 past the prefix)
+    auto scale_of = [&](bool is_v, int j) {
+      const int64_t key = (int64_t)j * BKV + lw * 32 + lane;
+      return key < a.P ? a.scales[((int64_t)(is_v ? a.Hkv : 0) + g) * a.cap + key] : 1.f;
+    };
+    // e4m3: the scales of the next two tiles of the ring are loaded ahead. With lead K tiles first,
+    // ring position p holds: p < lead: K_p; else, q = p - lead: V_{q/2} (q even) or K_{q/2+lead}
+    // (q odd), until the K tiles run out; past that the positions hold V tiles only.
+    const int first = min(lead, n), mixed = first + 2 * (n - first);   // positions before the V-only end
+    auto scale_at = [&](int p) {
+      bool is_v;
+      int t;
+      if (p < first) { is_v = false; t = p; }
+      else if (p < mixed) { is_v = ((p - first) & 1) == 0; t = is_v ? (p - first) / 2 : (p - first) / 2 + lead; }
+      else { is_v = true; t = (n - first) + (p - mixed); }
+      return t < n && jb + t < pl.ncache ? scale_of(is_v, jb + t) : 1.f;
+    };
+    float sc0 = 1.f, sc1 = 1.f;
+    int raw = 0, pos = 0;                      // raw items taken, position in the ring order
+    if constexpr (E4M3) {
+      sc0 = scale_at(0);
+      sc1 = scale_at(1);
     }
+    for_ring<F, FR>(n, two, [&](int s, int fill_ph, bool is_v, int t) {
+      const int j = jb + t;
+      const uint32_t ph = fill_ph ^ 1;
+      uint8_t* dst = kvst + s * L::TILE;
+      float sc = sc0;
+      if constexpr (E4M3) {
+        sc0 = sc1;
+        sc1 = scale_at(pos + 2);
+        ++pos;
+      }
+      if (j >= pl.ncache) {
+        if (!wwait(&empty[s], ph)) return false;
+        load_own(j - pl.ncache, is_v ? a.vn : a.kn, dst, is_v);
+      } else if constexpr (E4M3) {
+        const int r = raw % RS;
+        const bool fast = __all_sync(0xffffffffu, sc <= 128.f && __half2float(__float2half_rn(sc)) == sc);
+        if (!wwait(&raw_full[r], (raw / RS) & 1) || !wwait(&empty[s], ph)) return false;
+        // LPR lanes of 16 codes per row; the lanes of a row's second 64 columns write their two
+        // 16-byte chunks in the other order, so that no store conflicts
+        constexpr int LPR = HD / 16, RP = 32 / LPR;
+        const int ci = lane % LPR;
+        const uint8_t* rp = sm + L::R + r * L::RAW + (lw * 32) * HD + lane * 16;
+        auto convert = [&](auto is_fast, int p) {
+          const int lr = p * RP + lane / LPR, row = lw * 32 + lr;
+          const uint4 c = *reinterpret_cast<const uint4*>(rp + p * RP * HD);
+          uint32_t h[8];
+          codes_to_half<decltype(is_fast)::value>(c, __shfl_sync(0xffffffffu, sc, lr), h);
+          const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+          const bool swap = HD == 128 && ci >= 4;
+          uint8_t* d = dst + (ci >> 2) * (BKV * 128) + row * 128;
+          const int c0 = (2 * ci) & 7;
+          *reinterpret_cast<uint4*>(d + (((c0 + (swap ? 1 : 0)) ^ (row & 7)) << 4)) = swap ? hi : lo;
+          *reinterpret_cast<uint4*>(d + (((c0 + (swap ? 0 : 1)) ^ (row & 7)) << 4)) = swap ? lo : hi;
+        };
+        if (fast) {
+#pragma unroll 4
+          for (int p = 0; p < 32 / RP; ++p) convert(std::true_type{}, p);
+        } else {
+#pragma unroll 1
+          for (int p = 0; p < 32 / RP; ++p) convert(std::false_type{}, p);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&raw_empty[r]);
+        ++raw;
+      } else {
+        if (!wwait(&empty[s], ph)) return false;   // the producer's tile: only the arrival
+      }
+      fence_async_smem();                          // this warp's writes are the MMA's to read
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[s]);
+      return true;
+    });
   } else {
-    // ---- softmax: row r = TMEM lane r; warps 2-5 keys 0..63 of a tile, warps 6-9 keys 64..127
+    // ---- softmax of stream x: row r = TMEM lane r
     auto wwait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_err, ERR_TIMEOUT) ? 1 : 0) != 0;
     };
-    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const int x = (warp - 2) >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;
-    const int vq = v0 + r / pl.G;              // packed query row of this row
-    const bool live = r < pl.RT * pl.G && vq < v1;
+    const int q0 = v0 + (two && x ? pl.RT : 0);          // the tile's first packed row
+    const int vq = q0 + r / pl.G;                        // this row's
+    const bool live = r < pl.RT * pl.G && vq < v1 && vq < q0 + pl.RT;
     const int h = g * pl.G + r % pl.G;
     int vs = 0;
-    int64_t row = -1;                          // row of q and out
+    int64_t row = -1;                                    // row of q and out
     if (live) {
       const int s = seq_of(tab, vq);
       vs = tab.cum[s];
       row = (int64_t)tab.row0[s] + (vq - vs);
     }
-    const bool idle = !__any_sync(0xffffffffu, live);   // (the same for both halves of a quadrant)
-    {   // Q rows of the quadrant: half 0 the row's first chunks, half 1 the rest; absent rows are zeros
-      constexpr int CHH = HD / 16, RPI = 32 / CHH;      // 16-byte chunks of a half row
+    const bool idle = !__any_sync(0xffffffffu, live);
+    {   // Q rows of the quadrant; absent rows are zeros. One tile: each stream loads half of a row
+      constexpr int CH = HD / 8;
       const int64_t off = live ? row * a.q_stride + (int64_t)h * HD : -1;
-      const int c = half * CHH + lane % CHH;
-      uint4 x[32 / RPI];
+      uint8_t* dst = sm + L::Q + (two && x ? BQ * HD * 2 : 0);
 #pragma unroll
-      for (int p = 0; p < 32 / RPI; ++p) {
-        const int64_t o = __shfl_sync(0xffffffffu, off, p * RPI + lane / CHH);
-        x[p] = o >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.q + o) + c) : make_uint4(0, 0, 0, 0);
-      }
+      for (int p0 = 0; p0 < CH; p0 += 8) {               // 32 rows x CH chunks: CH passes of the warp
+        if (!two && (CH == 16 ? p0 / 8 != x : x != 0)) continue;
+        uint4 v[8];
 #pragma unroll
-      for (int p = 0; p < 32 / RPI; ++p) {
-        const int rr = quad * 32 + p * RPI + lane / CHH;
-        *reinterpret_cast<uint4*>(sm + L::Q + (c >> 3) * (BQ * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x[p];
+        for (int p = 0; p < 8; ++p) {
+          const int e = (p0 + p) * 32 + lane;
+          const int64_t o = __shfl_sync(0xffffffffu, off, e / CH);
+          v[p] = o >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.q + o) + e % CH) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const int e = (p0 + p) * 32 + lane, rr = quad * 32 + e / CH, c = e % CH;
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * (BQ * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v[p];
+        }
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     }
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t tO = tmem + lane_off + T_O + (uint32_t)(half * (HD / 2));
-    float* xch = reinterpret_cast<float*>(sm + L::XCH);
-    auto pair_meet = [&](int slot, uint32_t parity) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&xbar[quad * 3 + slot]);
-      return wwait(&xbar[quad * 3 + slot], parity);
-    };
-    constexpr int HB = BKV / 2, HO = HD / 2;
+    const uint32_t tS = tmem + lane_off + x * 128, tO = tmem + lane_off + T_O + x * 128;
     const float sl2 = a.scale * 1.4426950408889634f;
-    float m = -INFINITY, l = 0.f;              // maximum (log2 domain), this half's share of the sum
+    const uint64_t sl2_2 = pack2(sl2, sl2);
+    float m = -INFINITY;                       // running maximum (log2 domain)
+    uint64_t l2 = 0;                           // the row's sum, two partial sums
     bool ok = true;
-    for (int i = 0; i < n && ok; ++i) {
-      const int j = jb + i, b = i & 1;
-      const uint32_t ph = (i >> 1) & 1;
-      if (!wwait(&s_full[b], ph)) { ok = false; break; }
+    int li = 0;                                // tiles this stream has taken
+    for (int t = two ? 0 : x; t < n && ok; t += two ? 1 : 2, ++li) {
+      if (!wwait(&s_full[x], li & 1)) { ok = false; break; }
       if (idle) {
-        if (lane == 0) mbar_arrive(&s_empty[b]);
-        if (i >= 2 && !wwait(&o_done[b], ph ^ 1)) { ok = false; break; }
-        if (lane == 0) mbar_arrive(&p_full[b]);
+        if (lane == 0) mbar_arrive(&p_full[x]);
         continue;
       }
       fence_after();
-      uint32_t u[HB];
-      tld32(tmem + lane_off + b * 128 + half * HB, u);
-      tld32(tmem + lane_off + b * 128 + half * HB + 32, u + 32);
-      ld_wait();
-      pin32(u);
-      pin32(u + 32);
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s_empty[b]);
-      // visible keys of this half tile: lo .. hi
+      // visible keys of this tile: columns lo .. hi
+      const int j = jb + t;
       int lo = 0, hi;
       if (j < pl.ncache) {
-        hi = a.P - 1 - j * BKV - half * HB;
+        hi = a.P - 1 - j * BKV;
       } else {
-        const int base = kb + (j - pl.ncache) * BKV + half * HB;
+        const int base = kb + (j - pl.ncache) * BKV;
         lo = vs - base;
         hi = live ? vq - base : -1;
       }
-      float mx = -INFINITY;
-      if (__all_sync(0xffffffffu, lo <= 0 && hi >= HB - 1)) {
+      // the first half of the scores is read for the maximum now and again for the weights later,
+      // the second half stays in registers: P takes over its columns
+      auto tile = [&](auto masked) {
+        constexpr bool MASK = decltype(masked)::value;
+        auto mask = [&](uint32_t* w, int c0) {
+          if constexpr (MASK) {
 #pragma unroll
-        for (int c = 0; c < HB; ++c) mx = fmaxf(mx, __uint_as_float(u[c]));
-      } else {
+            for (int c = 0; c < 32; ++c)
+              if (c0 + c < lo || c0 + c > hi) w[c] = 0xff800000u;
+          }
+        };
+        uint32_t u[64];
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto maximum = [&](const uint32_t* w) {
 #pragma unroll
-        for (int c = 0; c < HB; ++c) {
-          if (c < lo || c > hi) u[c] = 0xff800000u;
-          mx = fmaxf(mx, __uint_as_float(u[c]));
+          for (int c = 0; c < 32; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx4[e] = fmaxf(mx4[e], fmaxf(__uint_as_float(w[c + e]), __uint_as_float(w[c + 4 + e])));
+        };
+        tld32(tS, u);
+        tld32(tS + 32, u + 32);
+        ld_wait();
+        pin32(u);
+        pin32(u + 32);
+        mask(u, 0);
+        maximum(u);
+        mask(u + 32, 32);
+        maximum(u + 32);
+        tld32(tS + 64, u);
+        tld32(tS + 96, u + 32);
+        ld_wait();
+        pin32(u);
+        pin32(u + 32);
+        mask(u, 64);
+        maximum(u);
+        mask(u + 32, 96);
+        maximum(u + 32);
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
+        float alpha = 1.f;
+        if (mx > m + 8.f) {
+          alpha = m == -INFINITY ? 1.f : ex2(m - mx);
+          m = mx;
         }
-      }
-      xch[(b * 2 + half) * BQ + r] = mx;
-      if (!pair_meet(b, ph)) { ok = false; break; }
-      mx = fmaxf(mx, xch[(b * 2 + (half ^ 1)) * BQ + r]) * sl2;
-      float alpha = 1.f;
-      if (mx > m + 8.f) {
-        alpha = m == -INFINITY ? 1.f : ex2(m - mx);
-        m = mx;
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-      if (i >= 2 && !wwait(&o_done[b], ph ^ 1)) { ok = false; break; }         // P_{i-2} has been read
-      if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        if (!wwait(&o_done[b ^ 1], ((i - 1) >> 1) & 1)) { ok = false; break; }   // O holds P_{i-1} V_{i-1}
-        fence_after();
-        uint32_t w[32];
+        const float base = m == -INFINITY ? 0.f : m;
+        if (li > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {   // (S of this tile came after the last P V)
+          uint32_t w[32];
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 32) {
+            tld32(tO + c, w);
+            ld_wait();
+            pin32(w);
 #pragma unroll
-        for (int c = 0; c < HO; c += 32) {
-          tld32(tO + c, w);
-          ld_wait();
-          pin32(w);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
-          tst32(tO + c, w);
+            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
+            tst32(tO + c, w);
+          }
+          l2 = pack2(lo2(l2) * alpha, hi2(l2) * alpha);
         }
-        l *= alpha;
-      }
-      fence_after();
-      float rs = 0.f;
-      uint32_t pk[32];
+        const uint64_t nb = pack2(-base, -base);
+        auto weights = [&](const uint32_t* w, uint32_t* pk) {    // 32 scores -> 16 f16 pairs
 #pragma unroll
-      for (int c = 0; c < HB; c += 2) {
-        const float p0 = ex2(fmaf(__uint_as_float(u[c]), sl2, -base));
-        const float p1 = ex2(fmaf(__uint_as_float(u[c + 1]), sl2, -base));
-        rs += p0 + p1;
-        pk[c / 2] = h2u(p0, p1);
-      }
-      l += rs;
-      tst32(tmem + lane_off + T_P + b * 64 + half * 32, pk);
+          for (int c = 0; c < 32; c += 2) {
+            const uint64_t z = fma2((uint64_t)w[c + 1] << 32 | w[c], sl2_2, nb);
+            const float p0 = ex2(lo2(z)), p1 = ex2(hi2(z));
+            l2 = add2(l2, pack2(p0, p1));
+            pk[c / 2] = h2u(p0, p1);
+          }
+        };
+        // (chunk k's weights take columns 64 + 16 k: over scores already in registers)
+        uint32_t pk[16];
+        weights(u, pk);
+        tst16(tS + 96, pk);
+        tld32(tS, u);
+        weights(u + 32, pk);
+        tst16(tS + 112, pk);
+        ld_wait();
+        pin32(u);
+        tld32(tS + 32, u + 32);
+        mask(u, 0);
+        weights(u, pk);
+        tst16(tS + 64, pk);
+        ld_wait();
+        pin32(u + 32);
+        mask(u + 32, 32);
+        weights(u + 32, pk);
+        tst16(tS + 80, pk);
+      };
+      if (__all_sync(0xffffffffu, lo <= 0 && hi >= BKV - 1)) tile(std::false_type{});
+      else tile(std::true_type{});
       st_wait();
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[b]);
+      if (lane == 0) mbar_arrive(&p_full[x]);
     }
-    // ---- epilogue: each thread its half of the row's output columns
-    if (ok && n > 0) ok = wwait(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
-    if (!idle) {
-      xch[(2 * 2 + half) * BQ + r] = l;
-      if (pair_meet(2, 0)) l += xch[(2 * 2 + (half ^ 1)) * BQ + r];
-      else ok = false;
-      float o[HO];
-      if (ok && n > 0) {
-        fence_after();
-        uint32_t w[32];
-#pragma unroll
-        for (int c = 0; c < HO; c += 32) {
-          tld32(tO + c, w);
-          ld_wait();
-          pin32(w);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[c + e] = __uint_as_float(w[e]);
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < HO; ++c) o[c] = 0.f;
+    // ---- epilogue
+    float l = lo2(l2) + hi2(l2);
+    if (ok && li > 0) ok = wwait(&o_done[x], 0);
+    fence_after();
+    auto sums = [&](int c, float* o) {         // 32 columns of this row's sums (zeros without a tile)
+      uint32_t w[32];
+      __syncwarp();
+      if (li > 0) {
+        tld32(tO + c, w);
+        ld_wait();
+        pin32(w);
       }
-      if (ok && live && *v_flag) {             // non-finite own V elements: into the rows that see them
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = li > 0 ? __uint_as_float(w[e]) : 0.f;
+    };
+    float* pub = reinterpret_cast<float*>(kvst) + r * L::OSTR;
+    float w0 = 1.f, w1 = 0.f;                  // weights of the two streams' sums
+    if (!two && x == 1 && !idle) {
+      // publish (o, m, l) in the K/V stages once stream 0 has read its last tile from them
+      if (ok && n > 0) ok = wwait(&o_done[0], 0);
+      if (ok) {
+        float o[32];
+#pragma unroll
+        for (int c = 0; c < HD; c += 32) {
+          sums(c, o);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(pub + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+        *reinterpret_cast<float2*>(pub + HD) = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&joined[quad]);
+      }
+    } else if (!idle) {
+      if (!two && ok) {
+        ok = wwait(&joined[quad], 0);
+        if (ok) {
+          const float2 ml = *reinterpret_cast<const float2*>(pub + HD);
+          const bool has0 = !(m == -INFINITY && l == 0.f), has1 = !(ml.x == -INFINITY && ml.y == 0.f);
+          const float M = fmaxf(m, ml.x);
+          w0 = has0 ? ex2(m - M) : 0.f;
+          w1 = has1 ? ex2(ml.x - M) : 0.f;
+          if (m == ml.x) w0 = has0 ? 1.f : 0.f, w1 = has1 ? 1.f : 0.f;   // (also both infinite)
+          l = (has0 ? w0 * l : 0.f) + (has1 ? w1 * ml.y : 0.f);
+          m = M;
+        }
+      }
+      if (ok) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const bool fix = live && *v_flag;      // non-finite own V elements: into the rows that see them
         const int k0 = max(vs, kb + (max(jb, pl.ncache) - pl.ncache) * BKV);
         const int k1 = min(vq, kb + (je - pl.ncache) * BKV - 1);
-        for (int kv = k0; kv <= k1; ++kv) {
-          const f16* vp = a.vn + (row - (vq - kv)) * a.kv_stride + (int64_t)g * HD + half * HO;
+        const int64_t pi = ((int64_t)blockIdx.x * pl.nt + (two ? x : 0)) * BQ + r;
 #pragma unroll
-          for (int c = 0; c < HO; ++c) {
-            const float x = h2f(vp[c]);
-            if (!isfinite(x)) o[c] += x;
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          sums(c, o);
+          if (!live) continue;                 // (sums is warp-collective, what follows is not)
+          if (!two) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(pub + c + e);
+              o[e] = (w0 != 0.f ? w0 * o[e] : 0.f) + (w1 != 0.f ? w1 * y.x : 0.f);
+              o[e + 1] = (w0 != 0.f ? w0 * o[e + 1] : 0.f) + (w1 != 0.f ? w1 * y.y : 0.f);
+              o[e + 2] = (w0 != 0.f ? w0 * o[e + 2] : 0.f) + (w1 != 0.f ? w1 * y.z : 0.f);
+              o[e + 3] = (w0 != 0.f ? w0 * o[e + 3] : 0.f) + (w1 != 0.f ? w1 * y.w : 0.f);
+            }
+          }
+          if (fix)
+            for (int kv = k0; kv <= k1; ++kv) {
+              const f16* vp = a.vn + (row - (vq - kv)) * a.kv_stride + (int64_t)g * HD + c;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float y = h2f(vp[e]);
+                if (!isfinite(y)) o[e] += y;
+              }
+            }
+          if (pl.ns == 1) {
+            f16* op = a.out + (row * a.Hq + h) * HD + c;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(op + e) =
+                  make_uint4(h2u(o[e] * inv, o[e + 1] * inv), h2u(o[e + 2] * inv, o[e + 3] * inv),
+                             h2u(o[e + 4] * inv, o[e + 5] * inv), h2u(o[e + 6] * inv, o[e + 7] * inv));
+          } else {                             // [parts][BQ][HD] sums, then [parts][BQ] (m, l)
+            float* wo = (float*)a.ws + pi * HD + c;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(wo + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         }
-      }
-      if (ok && live) {
-        if (pl.ns == 1) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          f16* op = a.out + (row * a.Hq + h) * HD + half * HO;
-#pragma unroll
-          for (int c = 0; c < HO; c += 8)
-            *reinterpret_cast<uint4*>(op + c) =
-                make_uint4(h2u(o[c] * inv, o[c + 1] * inv), h2u(o[c + 2] * inv, o[c + 3] * inv),
-                           h2u(o[c + 4] * inv, o[c + 5] * inv), h2u(o[c + 6] * inv, o[c + 7] * inv));
-        } else {                               // [items * ns][BQ][HD] sums, then [..][BQ] (m, l)
-          const int64_t pi = (int64_t)blockIdx.x * BQ + r;
-          float* wo = (float*)a.ws + pi * HD + half * HO;
-#pragma unroll
-          for (int c = 0; c < HO; c += 4)
-            *reinterpret_cast<float4*>(wo + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
-          if (half == 0)
-            reinterpret_cast<float2*>((float*)a.ws + (int64_t)gridDim.x * BQ * HD)[pi] = make_float2(m, l);
-        }
+        if (live && pl.ns > 1)
+          reinterpret_cast<float2*>((float*)a.ws + (int64_t)gridDim.x * pl.nt * BQ * HD)[pi] = make_float2(m, l);
       }
     }
   }
@@ -570,15 +710,17 @@ __global__ void __launch_bounds__(256)
   if (vr >= pl.V) return;
   const int g = h / pl.G, mt = vr / pl.RT;
   const int r = (vr - mt * pl.RT) * pl.G + h % pl.G;
-  const int64_t p0 = ((int64_t)g * pl.MT + mt) * pl.ns;        // the item's first part
-  const float2* ml = reinterpret_cast<const float2*>((const float*)a.ws + (int64_t)pl.MT * a.Hkv * pl.ns * BQ * HD);
+  // this tile's parts lie nt slots apart, from p0 on
+  const int64_t p0 = ((int64_t)g * pl.MP + mt / 2) * pl.ns * pl.nt + mt % 2;
+  const float2* ml =
+      reinterpret_cast<const float2*>((const float*)a.ws + (int64_t)pl.MP * a.Hkv * pl.ns * pl.nt * BQ * HD);
   const float* po = (const float*)a.ws + (p0 * BQ + r) * HD + lane * E;
   float2 x[2];                                                 // ns <= 64: parts lane and lane + 32
   float M = -INFINITY;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int p = lane + 32 * k;
-    x[k] = p < pl.ns ? ml[(p0 + p) * BQ + r] : make_float2(-INFINITY, 0.f);
+    x[k] = p < pl.ns ? ml[(p0 + (int64_t)p * pl.nt) * BQ + r] : make_float2(-INFINITY, 0.f);
     M = fmaxf(M, x[k].x);
   }
   M = warp_max(M);
@@ -598,7 +740,7 @@ __global__ void __launch_bounds__(256)
   for (int p = 0; p < pl.ns; ++p) {
     const float f = __shfl_sync(0xffffffffu, p < 32 ? wt[0] : wt[1], p & 31);
     if (!(((p < 32 ? used0 : used1) >> (p & 31)) & 1)) continue;
-    const float* op = po + (int64_t)p * BQ * HD;
+    const float* op = po + (int64_t)p * pl.nt * BQ * HD;
     float v[E];
     if constexpr (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(op);
     else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(op);
@@ -612,24 +754,28 @@ __global__ void __launch_bounds__(256)
   for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(out + e) = t5::h2u(o[e] * inv, o[e + 1] * inv);
 }
 
-// How many parts an item's key tiles are split into: the count with the least time in units of one
-// key tile, (waves of CTAs) x (tiles per part + a CTA's fixed cost of about 4 tiles), plus, when
-// split, the join's launch and its reads of the parts. At most 64 parts, at most 8 CTAs an SM.
+// How many parts an item's key tiles are split into: the count with the least estimated time, waves
+// of CTAs x (key tiles per part + a CTA's fixed cost), plus, when split, the join's launch and its
+// reads of the parts. Units: a key tile of two query tiles; one query tile alone takes about 0.55
+// of it. At most 64 parts, at most 8 CTAs an SM.
 Plan make_plan(int V, int max_len, int P, int Hq, int Hkv, int num_sms) {
   Plan p;
   p.V = V;
   p.G = Hq / Hkv;
   p.RT = BQ / p.G;
   p.MT = (V + p.RT - 1) / p.RT;
+  p.MP = (p.MT + 1) / 2;
+  p.nt = p.MT > 1 ? 2 : 1;
   p.ncache = (int)(((int64_t)P + BKV - 1) / BKV);
-  const int64_t items = (int64_t)p.MT * Hkv;
-  const int64_t total = p.ncache + (std::min<int64_t>(V, (int64_t)max_len - 1 + p.RT) + BKV - 1) / BKV;
+  const int64_t items = (int64_t)p.MP * Hkv;
+  const int64_t total = p.ncache + (std::min<int64_t>(V, (int64_t)max_len - 1 + p.nt * p.RT) + BKV - 1) / BKV;
+  const double unit = p.nt == 2 ? 1.0 : 0.55;
   p.ns = 1;
   double best = 0;
   for (int ns = 1; ns <= 64 && ns <= total && (ns == 1 || items * ns <= 8ll * num_sms); ++ns) {
     const double waves = (double)((items * ns + num_sms - 1) / num_sms);
-    double t = waves * ((double)((total + ns - 1) / ns) + 4.0);
-    if (ns > 1) t += 5.0 + 0.02 * (double)(items * ns);
+    double t = waves * (unit * (double)((total + ns - 1) / ns) + 2.5);
+    if (ns > 1) t += 2.5 + 0.01 * (double)(items * ns * p.nt);
     if (ns == 1 || t < best) {
       best = t;
       p.ns = ns;
@@ -661,7 +807,7 @@ cudaError_t launch_group(const SharedAttnArgs& a, const SeqTab<N>& tab, const Pl
                          cudaStream_t st) {
   using L = Lay<HD, E4M3>;
   CK_RET(cudaFuncSetAttribute(shared_kernel<HD, E4M3, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES));
-  CK_RET(launch_pdl(shared_kernel<HD, E4M3, N>, dim3((unsigned)((int64_t)pl.MT * a.Hkv * pl.ns)), dim3(NTHREADS),
+  CK_RET(launch_pdl(shared_kernel<HD, E4M3, N>, dim3((unsigned)((int64_t)pl.MP * a.Hkv * pl.ns)), dim3(NTHREADS),
                     L::BYTES, st, tab, map, a, pl));
   if (pl.ns > 1) {
     const int64_t warps = (int64_t)pl.V * a.Hq;
@@ -690,7 +836,7 @@ int64_t attention_shared_ws_bytes(int n_seq, const int* len, int P, int Hq, int 
     s = sha::pack_group(t, s, n_seq, nullptr, len, &max_len);
     if (t.n == 0) continue;
     const sha::Plan p = sha::make_plan(t.cum[t.n], max_len, P, Hq, Hkv, num_sms);
-    if (p.ns > 1) need = std::max<int64_t>(need, (int64_t)p.MT * Hkv * p.ns * sha::BQ * (hd + 2) * 4);
+    if (p.ns > 1) need = std::max<int64_t>(need, (int64_t)p.MP * Hkv * p.ns * p.nt * sha::BQ * (hd + 2) * 4);
   }
   return need;
 }
@@ -714,7 +860,7 @@ cudaError_t launch_attention_shared(const SharedAttnArgs& a, int n_seq, const in
     s = sha::pack_group(t, s, n_seq, row0, len, &max_len);
     if (t.n == 0) continue;
     const sha::Plan pl = sha::make_plan(t.cum[t.n], max_len, a.P, a.Hq, a.Hkv, num_sms);
-    if ((int64_t)pl.MT * a.Hkv * pl.ns > INT_MAX) return cudaErrorInvalidValue;
+    if ((int64_t)pl.MP * a.Hkv * pl.ns > INT_MAX) return cudaErrorInvalidValue;
     if (t.n <= SEQ_TAB_SMALL) {
       SeqTab<SEQ_TAB_SMALL> u;
       u.n = t.n;
