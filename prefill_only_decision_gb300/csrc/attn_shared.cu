@@ -75,8 +75,13 @@ struct Lay {
   static constexpr int KV2 = Q + 2 * BQ * HD * 2;         // stages with two query tiles
   static constexpr int KV1 = Q + BQ * HD * 2;             // with one
   static constexpr int R = KV2 + F * TILE;
-  static constexpr int BAR = R + (E4M3 ? RS * RAW : 0);
-  static constexpr int USED = BAR + 512 + 1024;           // barriers, alignment slack
+  static constexpr int SC = R + (E4M3 ? RS * RAW : 0);    // raw tiles' scales [RS][BKV]
+  static constexpr int TAB = SC + (E4M3 ? RS * BKV * 4 : 0);       // a copy of a small sequence table
+  static constexpr int BAR = TAB + (2 * SEQ_TAB_SMALL + 2) * 4;
+  static constexpr int NS = 2 * FR > F ? 2 * FR : F;
+  static constexpr int NBAR = 1 + 2 * NS + 6 + 2 + 4 + (E4M3 ? 2 * RS : 0);
+  static constexpr int USED = BAR + NBAR * 8 + 16;
+  static_assert(USED <= 227 * 1024, "shared memory of one CTA");
   // above half an SM: each CTA allocates all of TMEM, so two never share one
   static constexpr int BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
   static constexpr int OSTR = HD + 4;                     // floats per row of a stream's published sums
@@ -126,9 +131,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float((uint32_t)a); }
 __device__ __forceinline__ float hi2(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
 
+// Sequence tables as a kernel searches them: a small one from its copy in shared memory, a large
+// one where it is.
+struct TabView {
+  int n;
+  const int *cum, *row0;
+};
 // The sequence that packed row vr (< cum[n]) belongs to.
-template <int N>
-__device__ __forceinline__ int seq_of(const SeqTab<N>& t, int vr) {
+__device__ __forceinline__ int seq_of(const TabView& t, int vr) {
   int lo = 0, hi = t.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -171,12 +181,11 @@ __device__ __forceinline__ void codes_to_half(const uint4 c, float scale, uint32
 
 template <int HD, bool E4M3, int N>
 __global__ void __launch_bounds__(NTHREADS, 1)
-    shared_kernel(const __grid_constant__ SeqTab<N> tab, const __grid_constant__ CUtensorMap mapKV,
+    shared_kernel(const __grid_constant__ SeqTab<N> table, const __grid_constant__ CUtensorMap mapKV,
                   const __grid_constant__ SharedAttnArgs a, const Plan pl) {
   using L = Lay<HD, E4M3>;
-  constexpr int NB = HD / 64, F = L::F, FR = L::FR, NS = 2 * FR > F ? 2 * FR : F, RS = L::RS;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  constexpr int NB = HD / 64, F = L::F, FR = L::FR, NS = L::NS, RS = L::RS;
+  extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* bars = (uint64_t*)(sm + L::BAR);
   uint64_t* q_full = bars;
   uint64_t* full = bars + 1;                   // [NS]
@@ -186,12 +195,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* o_done = p_full + 2;               // [2] the stream's last product has completed
   uint64_t* mma_idle = o_done + 2;             // [2]
   uint64_t* joined = mma_idle + 2;             // [4 quadrants] stream 1's sums are published
-  uint64_t* raw_full = joined + 4;             // [RS]
+  uint64_t* raw_full = joined + 4;             // [RS] (e4m3)
   uint64_t* raw_empty = raw_full + RS;         // [RS]
-  uint32_t* tmem_slot = (uint32_t*)(raw_empty + RS);
+  uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // some own V element of this CTA is not finite
-  static_assert((1 + 2 * NS + 6 + 2 + 4 + 2 * RS) * 8 + 16 <= 512, "barriers fit");
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const int part = (int)(blockIdx.x % pl.ns), item = (int)(blockIdx.x / pl.ns);
@@ -213,37 +221,67 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_init(&o_done[x], 1);
     }
     for (int x = 0; x < 4; ++x) mbar_init(&joined[x], 1);
-    for (int r = 0; r < RS; ++r) { mbar_init(&raw_full[r], 1); mbar_init(&raw_empty[r], 4); }
+    if constexpr (E4M3)
+      for (int r = 0; r < RS; ++r) {
+        mbar_init(&raw_full[r], 1 + 32);       // the tile's copy, and each producer lane's scales
+        mbar_init(&raw_empty[r], 4);
+      }
     *abort_flag = 0;
     *v_flag = 0;
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc<TMEM_COLS>(tmem_slot);
+  TabView tab{table.n, table.cum, table.row0};
+  if constexpr (N == SEQ_TAB_SMALL) {
+    int* copy = reinterpret_cast<int*>(sm + L::TAB);
+    if (threadIdx.x >= 64 && threadIdx.x < 64 + N) {
+      const int i = threadIdx.x - 64;
+      if (i < table.n) {
+        copy[i] = table.cum[i];
+        copy[N + 1 + i] = table.row0[i];
+      }
+    }
+    tab.cum = copy;
+    tab.row0 = copy + N + 1;
+  }
   allow_dependents();
-  wait_prerequisites();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
   // key tiles of this part: prefix tiles 0 .. ncache-1, then own tiles from packed row kb on
   const int kb = a.kn ? tab.cum[seq_of(tab, v0)] : 0;
   const int nown = a.kn ? (v1 - kb + BKV - 1) / BKV : 0;
   const int total = pl.ncache + nown;
   const int per = (total + pl.ns - 1) / pl.ns;
   const int jb = min(total, part * per), je = min(total, jb + per);
-  const int n = je - jb, lead = two ? 1 : 2;
+  const int n = je - jb;
   uint8_t* kvst = sm + (two ? L::KV2 : L::KV1);
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
-    // ---- TMA producer
-    if (lane == 0) {
+    // ---- TMA producer (e4m3: lane 0 the tiles, every lane four of a tile's scales)
+    wait_prerequisites();
+    if (E4M3 || lane == 0) {
       if constexpr (E4M3) {                    // raw items: the ring's prefix tiles in its order
         int issued = 0;
         for_ring<F, FR>(n, two, [&](int, int, bool is_v, int t) {
           if (jb + t >= pl.ncache) return true;
           const int r = issued % RS;
-          if (!mbar_wait(&raw_empty[r], ((issued / RS) & 1) ^ 1, abort_flag, &g_err, ERR_TIMEOUT)) return false;
-          mbar_expect_tx(&raw_full[r], L::RAW);
-          tma4(sm + L::R + r * L::RAW, &mapKV, &raw_full[r], 0, g, (jb + t) * BKV, is_v ? 1 : 0);
+          if (!__all_sync(0xffffffffu, mbar_wait(&raw_empty[r], ((issued / RS) & 1) ^ 1, abort_flag, &g_err,
+                                                 ERR_TIMEOUT) ? 1 : 0))
+            return false;
+          const int key0 = (jb + t) * BKV;
+          if (lane == 0) {
+            mbar_expect_tx(&raw_full[r], L::RAW);
+            tma4(sm + L::R + r * L::RAW, &mapKV, &raw_full[r], 0, g, key0, is_v ? 1 : 0);
+          }
+          float* sc = reinterpret_cast<float*>(sm + L::SC) + r * BKV;
+          const float* src = a.scales + ((int64_t)(is_v ? a.Hkv : 0) + g) * a.cap;
+#pragma unroll
+          for (int k = lane; k < BKV; k += 32) {
+            const bool in = key0 + k < a.P;    // (rows past the prefix: codes and scales are zeros)
+            cp_async4(sc + k, src + (in ? key0 + k : 0), in);
+          }
+          cp_async_arrive(&raw_full[r]);
           ++issued;
           return true;
         });
@@ -335,67 +373,38 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       const int c = lane % CH;
       bool bad = false;
+      uint4 x[PASSES];
 #pragma unroll
-      for (int p0 = 0; p0 < PASSES; p0 += 8) {
-        uint4 x[8];
+      for (int p = 0; p < PASSES; ++p) {
+        const int64_t o = __shfl_sync(0xffffffffu, off, p * RPI + lane / CH);
+        x[p] = o >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + o) + c) : make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-        for (int p = 0; p < 8 && p0 + p < PASSES; ++p) {
-          const int64_t o = __shfl_sync(0xffffffffu, off, (p0 + p) * RPI + lane / CH);
-          x[p] = o >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + o) + c) : make_uint4(0, 0, 0, 0);
+      for (int p = 0; p < PASSES; ++p) {
+        if (is_v && (nonfinite2(x[p].x) || nonfinite2(x[p].y) || nonfinite2(x[p].z) || nonfinite2(x[p].w))) {
+          bad = true;
+          x[p] = make_uint4(drop_nonfinite2(x[p].x), drop_nonfinite2(x[p].y), drop_nonfinite2(x[p].z),
+                            drop_nonfinite2(x[p].w));
         }
-#pragma unroll
-        for (int p = 0; p < 8 && p0 + p < PASSES; ++p) {
-          if (is_v && (nonfinite2(x[p].x) || nonfinite2(x[p].y) || nonfinite2(x[p].z) || nonfinite2(x[p].w))) {
-            bad = true;
-            x[p] = make_uint4(drop_nonfinite2(x[p].x), drop_nonfinite2(x[p].y), drop_nonfinite2(x[p].z),
-                              drop_nonfinite2(x[p].w));
-          }
-          const int r = lw * 32 + (p0 + p) * RPI + lane / CH;
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * (BKV * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x[p];
-        }
+        const int r = lw * 32 + p * RPI + lane / CH;
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * (BKV * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x[p];
       }
       if (bad) *v_flag = 1;
     };
-    // the scale of this lane's row of a prefix tile (1 past the prefix)
-    auto scale_of = [&](bool is_v, int j) {
-      const int64_t key = (int64_t)j * BKV + lw * 32 + lane;
-      return key < a.P ? a.scales[((int64_t)(is_v ? a.Hkv : 0) + g) * a.cap + key] : 1.f;
-    };
-    // e4m3: the scales of the next two tiles of the ring are loaded ahead. With lead K tiles first,
-    // ring position p holds: p < lead: K_p; else, q = p - lead: V_{q/2} (q even) or K_{q/2+lead}
-    // (q odd), until the K tiles run out; past that the positions hold V tiles only.
-    const int first = min(lead, n), mixed = first + 2 * (n - first);   // positions before the V-only end
-    auto scale_at = [&](int p) {
-      bool is_v;
-      int t;
-      if (p < first) { is_v = false; t = p; }
-      else if (p < mixed) { is_v = ((p - first) & 1) == 0; t = is_v ? (p - first) / 2 : (p - first) / 2 + lead; }
-      else { is_v = true; t = (n - first) + (p - mixed); }
-      return t < n && jb + t < pl.ncache ? scale_of(is_v, jb + t) : 1.f;
-    };
-    float sc0 = 1.f, sc1 = 1.f;
-    int raw = 0, pos = 0;                      // raw items taken, position in the ring order
-    if constexpr (E4M3) {
-      sc0 = scale_at(0);
-      sc1 = scale_at(1);
-    }
+    int raw = 0;                               // raw items taken
+    wait_prerequisites();
     for_ring<F, FR>(n, two, [&](int s, int fill_ph, bool is_v, int t) {
       const int j = jb + t;
       const uint32_t ph = fill_ph ^ 1;
       uint8_t* dst = kvst + s * L::TILE;
-      float sc = sc0;
-      if constexpr (E4M3) {
-        sc0 = sc1;
-        sc1 = scale_at(pos + 2);
-        ++pos;
-      }
       if (j >= pl.ncache) {
         if (!wwait(&empty[s], ph)) return false;
         load_own(j - pl.ncache, is_v ? a.vn : a.kn, dst, is_v);
       } else if constexpr (E4M3) {
         const int r = raw % RS;
-        const bool fast = __all_sync(0xffffffffu, sc <= 128.f && __half2float(__float2half_rn(sc)) == sc);
         if (!wwait(&raw_full[r], (raw / RS) & 1) || !wwait(&empty[s], ph)) return false;
+        const float sc = reinterpret_cast<const float*>(sm + L::SC)[r * BKV + lw * 32 + lane];   // this lane's row
+        const bool fast = __all_sync(0xffffffffu, sc <= 128.f && __half2float(__float2half_rn(sc)) == sc);
         // LPR lanes of 16 codes per row; the lanes of a row's second 64 columns write their two
         // 16-byte chunks in the other order, so that no store conflicts
         constexpr int LPR = HD / 16, RP = 32 / LPR;
@@ -450,26 +459,28 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       row = (int64_t)tab.row0[s] + (vq - vs);
     }
     const bool idle = !__any_sync(0xffffffffu, live);
-    {   // Q rows of the quadrant; absent rows are zeros. One tile: each stream loads half of a row
+    wait_prerequisites();
+    {   // Q rows of the quadrant; absent rows are zeros. One tile: each stream loads half of the chunks
       constexpr int CH = HD / 8;
       const int64_t off = live ? row * a.q_stride + (int64_t)h * HD : -1;
       uint8_t* dst = sm + L::Q + (two && x ? BQ * HD * 2 : 0);
+      auto load = [&](auto count, int first) {           // `count` of the CH passes over 32 rows x CH chunks
+        constexpr int PN = decltype(count)::value;
+        uint4 v[PN];
 #pragma unroll
-      for (int p0 = 0; p0 < CH; p0 += 8) {               // 32 rows x CH chunks: CH passes of the warp
-        if (!two && (CH == 16 ? p0 / 8 != x : x != 0)) continue;
-        uint4 v[8];
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          const int e = (p0 + p) * 32 + lane;
+        for (int p = 0; p < PN; ++p) {
+          const int e = (first + p) * 32 + lane;
           const int64_t o = __shfl_sync(0xffffffffu, off, e / CH);
           v[p] = o >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.q + o) + e % CH) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          const int e = (p0 + p) * 32 + lane, rr = quad * 32 + e / CH, c = e % CH;
+        for (int p = 0; p < PN; ++p) {
+          const int e = (first + p) * 32 + lane, rr = quad * 32 + e / CH, c = e % CH;
           *reinterpret_cast<uint4*>(dst + (c >> 3) * (BQ * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v[p];
         }
-      }
+      };
+      if (two) load(std::integral_constant<int, CH>{}, 0);
+      else load(std::integral_constant<int, CH / 2>{}, x * (CH / 2));
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
@@ -499,17 +510,26 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         lo = vs - base;
         hi = live ? vq - base : -1;
       }
+      if (!__all_sync(0xffffffffu, lo <= 0 && hi >= BKV - 1)) {
+        // some row does not see all keys: -inf into its hidden scores, in place
+#pragma unroll 1
+        for (int c = 0; c < BKV; c += 32) {
+          const int a0 = min(max(lo - c, 0), 32), a1 = min(max(hi - c + 1, 0), 32);   // columns a0 .. a1-1
+          const uint32_t seen = a1 > a0 ? (0xffffffffu >> (32 - (a1 - a0))) << a0 : 0u;
+          uint32_t w[32];
+          tld32(tS + c, w);
+          ld_wait();
+          pin32(w);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(seen & (1u << e))) w[e] = 0xff800000u;
+          tst32(tS + c, w);
+        }
+        st_wait();
+      }
       // the first half of the scores is read for the maximum now and again for the weights later,
       // the second half stays in registers: P takes over its columns
-      auto tile = [&](auto masked) {
-        constexpr bool MASK = decltype(masked)::value;
-        auto mask = [&](uint32_t* w, int c0) {
-          if constexpr (MASK) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (c0 + c < lo || c0 + c > hi) w[c] = 0xff800000u;
-          }
-        };
+      {
         uint32_t u[64];
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         auto maximum = [&](const uint32_t* w) {
@@ -524,18 +544,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         ld_wait();
         pin32(u);
         pin32(u + 32);
-        mask(u, 0);
         maximum(u);
-        mask(u + 32, 32);
         maximum(u + 32);
         tld32(tS + 64, u);
         tld32(tS + 96, u + 32);
         ld_wait();
         pin32(u);
         pin32(u + 32);
-        mask(u, 64);
         maximum(u);
-        mask(u + 32, 96);
         maximum(u + 32);
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
         float alpha = 1.f;
@@ -577,17 +593,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         ld_wait();
         pin32(u);
         tld32(tS + 32, u + 32);
-        mask(u, 0);
         weights(u, pk);
         tst16(tS + 64, pk);
         ld_wait();
         pin32(u + 32);
-        mask(u + 32, 32);
         weights(u + 32, pk);
         tst16(tS + 80, pk);
-      };
-      if (__all_sync(0xffffffffu, lo <= 0 && hi >= BKV - 1)) tile(std::false_type{});
-      else tile(std::true_type{});
+      }
       st_wait();
       fence_before();
       __syncwarp();
@@ -645,7 +657,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const bool fix = live && *v_flag;      // non-finite own V elements: into the rows that see them
         const int k0 = max(vs, kb + (max(jb, pl.ncache) - pl.ncache) * BKV);
         const int k1 = min(vq, kb + (je - pl.ncache) * BKV - 1);
-        const int64_t pi = ((int64_t)blockIdx.x * pl.nt + (two ? x : 0)) * BQ + r;
+        const int64_t pi = (int64_t)blockIdx.x * pl.nt + (two ? x : 0);
+        uint8_t* ostage = sm + L::Q + (two && x ? BQ * HD * 2 : 0);
 #pragma unroll
         for (int c = 0; c < HD; c += 32) {
           float o[32];
@@ -670,22 +683,34 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 if (!isfinite(y)) o[e] += y;
               }
             }
-          if (pl.ns == 1) {
-            f16* op = a.out + (row * a.Hq + h) * HD + c;
+          if (pl.ns == 1) {                    // f16 row into the (consumed) Q tile, chunks swizzled
+            uint8_t* dst = ostage + r * (HD * 2);
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(op + e) =
+              *reinterpret_cast<uint4*>(dst + ((((c + e) / 8) ^ (r & 7)) << 4)) =
                   make_uint4(h2u(o[e] * inv, o[e + 1] * inv), h2u(o[e + 2] * inv, o[e + 3] * inv),
                              h2u(o[e + 4] * inv, o[e + 5] * inv), h2u(o[e + 6] * inv, o[e + 7] * inv));
-          } else {                             // [parts][BQ][HD] sums, then [parts][BQ] (m, l)
-            float* wo = (float*)a.ws + pi * HD + c;
+          } else {                             // [parts][HD / 4][BQ] groups of 4 sums: coalesced over the rows
+            float4* wo = reinterpret_cast<float4*>(a.ws) + (pi * (HD / 4) + c / 4) * BQ + r;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(wo + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 32; e += 4) wo[e / 4 * BQ] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+        if (pl.ns == 1) {                      // whole rows out of the warp's stage
+          __syncwarp();
+          constexpr int CH = HD / 8;
+          const int64_t off = live ? (row * a.Hq + h) * HD : -1;
+#pragma unroll
+          for (int p = 0; p < CH; ++p) {
+            const int e = p * 32 + lane, rr = quad * 32 + e / CH, c = e % CH;
+            const int64_t o = __shfl_sync(0xffffffffu, off, e / CH);
+            if (o >= 0)
+              *reinterpret_cast<uint4*>(a.out + o + c * 8) =
+                  *reinterpret_cast<const uint4*>(ostage + rr * (HD * 2) + ((c ^ (rr & 7)) << 4));
           }
         }
         if (live && pl.ns > 1)
-          reinterpret_cast<float2*>((float*)a.ws + (int64_t)gridDim.x * pl.nt * BQ * HD)[pi] = make_float2(m, l);
+          reinterpret_cast<float2*>((float*)a.ws + (int64_t)gridDim.x * pl.nt * BQ * HD)[pi * BQ + r] = make_float2(m, l);
       }
     }
   }
@@ -697,61 +722,53 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 }
 
 // Joins the parts of a row in part order: M = max m, o = sum 2^(m - M) o / sum 2^(m - M) l. One
-// warp per (packed row, q head). A part without a visible key (m = -inf, l = 0) holds no sums.
+// thread per (row of a query tile, 4 columns), consecutive threads on consecutive rows: the parts
+// are read in whole lines. A part without a visible key (m = -inf, l = 0) holds no sums.
+constexpr int CTHREADS = 128;
 template <int HD, int N>
-__global__ void __launch_bounds__(256)
-    combine_kernel(const __grid_constant__ SeqTab<N> tab, const __grid_constant__ SharedAttnArgs a, const Plan pl) {
-  constexpr int E = HD / 32;
+__global__ void __launch_bounds__(CTHREADS)
+    combine_kernel(const __grid_constant__ SeqTab<N> table, const __grid_constant__ SharedAttnArgs a, const Plan pl) {
   allow_dependents();
+  const int r = threadIdx.x, c4 = blockIdx.x % (HD / 4), tile = blockIdx.x / (HD / 4);
+  const int mt = tile % pl.MT, g = tile / pl.MT;
+  const int vr = mt * pl.RT + r / pl.G;
+  const bool live = r < pl.RT * pl.G && vr < pl.V;
+  int64_t row = 0;
+  if (live) {
+    const TabView tab{table.n, table.cum, table.row0};
+    const int s = seq_of(tab, vr);
+    row = (int64_t)tab.row0[s] + vr - tab.cum[s];
+  }
   wait_prerequisites();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int vr = (int)(w / a.Hq), h = (int)(w % a.Hq);
-  if (vr >= pl.V) return;
-  const int g = h / pl.G, mt = vr / pl.RT;
-  const int r = (vr - mt * pl.RT) * pl.G + h % pl.G;
-  // this tile's parts lie nt slots apart, from p0 on
+  if (!live) return;
+  // this tile's parts lie nt apart, from p0 on
   const int64_t p0 = ((int64_t)g * pl.MP + mt / 2) * pl.ns * pl.nt + mt % 2;
   const float2* ml =
-      reinterpret_cast<const float2*>((const float*)a.ws + (int64_t)pl.MP * a.Hkv * pl.ns * pl.nt * BQ * HD);
-  const float* po = (const float*)a.ws + (p0 * BQ + r) * HD + lane * E;
-  float2 x[2];                                                 // ns <= 64: parts lane and lane + 32
+      reinterpret_cast<const float2*>((const float*)a.ws + (int64_t)pl.MP * a.Hkv * pl.ns * pl.nt * BQ * HD) +
+      p0 * BQ + r;
+  const float4* po = reinterpret_cast<const float4*>(a.ws) + (p0 * (HD / 4) + c4) * BQ + r;
   float M = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int p = lane + 32 * k;
-    x[k] = p < pl.ns ? ml[(p0 + (int64_t)p * pl.nt) * BQ + r] : make_float2(-INFINITY, 0.f);
-    M = fmaxf(M, x[k].x);
-  }
-  M = warp_max(M);
-  float sum = 0.f, wt[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    wt[k] = x[k].x == -INFINITY && x[k].y == 0.f ? 0.f : t5::ex2(x[k].x - M);
-    sum += wt[k] == 0.f && x[k].y == 0.f ? 0.f : wt[k] * x[k].y;
-  }
-  sum = warp_sum(sum);
-  float o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  const unsigned used0 = __ballot_sync(0xffffffffu, !(x[0].x == -INFINITY && x[0].y == 0.f));
-  const unsigned used1 = __ballot_sync(0xffffffffu, !(x[1].x == -INFINITY && x[1].y == 0.f));
-#pragma unroll 4
+#pragma unroll 8
+  for (int p = 0; p < pl.ns; ++p) M = fmaxf(M, ml[(int64_t)p * pl.nt * BQ].x);
+  float sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
   for (int p = 0; p < pl.ns; ++p) {
-    const float f = __shfl_sync(0xffffffffu, p < 32 ? wt[0] : wt[1], p & 31);
-    if (!(((p < 32 ? used0 : used1) >> (p & 31)) & 1)) continue;
-    const float* op = po + (int64_t)p * pl.nt * BQ * HD;
-    float v[E];
-    if constexpr (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(op);
-    else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(op);
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += f * v[e];
+    const float2 x = ml[(int64_t)p * pl.nt * BQ];
+    const float4 v = po[(int64_t)p * pl.nt * (HD / 4) * BQ];
+    const bool none = x.x == -INFINITY && x.y == 0.f;
+    const float w = x.x == M ? 1.f : t5::ex2(x.x - M);         // (M infinite: the parts that reach it)
+    if (!none) {
+      sum += w * x.y;
+      o.x += w * v.x;
+      o.y += w * v.y;
+      o.z += w * v.z;
+      o.w += w * v.w;
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int s = seq_of(tab, vr);
-  f16* out = a.out + (((int64_t)tab.row0[s] + vr - tab.cum[s]) * a.Hq + h) * HD + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(out + e) = t5::h2u(o[e] * inv, o[e + 1] * inv);
+  *reinterpret_cast<uint2*>(a.out + (row * a.Hq + g * pl.G + r % pl.G) * HD + c4 * 4) =
+      make_uint2(t5::h2u(o.x * inv, o.y * inv), t5::h2u(o.z * inv, o.w * inv));
 }
 
 // How many parts an item's key tiles are split into: the count with the least estimated time, waves
@@ -810,8 +827,8 @@ cudaError_t launch_group(const SharedAttnArgs& a, const SeqTab<N>& tab, const Pl
   CK_RET(launch_pdl(shared_kernel<HD, E4M3, N>, dim3((unsigned)((int64_t)pl.MP * a.Hkv * pl.ns)), dim3(NTHREADS),
                     L::BYTES, st, tab, map, a, pl));
   if (pl.ns > 1) {
-    const int64_t warps = (int64_t)pl.V * a.Hq;
-    CK_RET(launch_pdl(combine_kernel<HD, N>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, tab, a, pl));
+    CK_RET(launch_pdl(combine_kernel<HD, N>, dim3((unsigned)((int64_t)pl.MT * a.Hkv * (HD / 4))), dim3(CTHREADS), 0, st,
+                      tab, a, pl));
   }
   return cudaSuccess;
 }
@@ -860,7 +877,7 @@ cudaError_t launch_attention_shared(const SharedAttnArgs& a, int n_seq, const in
     s = sha::pack_group(t, s, n_seq, row0, len, &max_len);
     if (t.n == 0) continue;
     const sha::Plan pl = sha::make_plan(t.cum[t.n], max_len, a.P, a.Hq, a.Hkv, num_sms);
-    if ((int64_t)pl.MP * a.Hkv * pl.ns > INT_MAX) return cudaErrorInvalidValue;
+    if ((int64_t)pl.MP * a.Hkv * std::max(pl.ns, pl.nt * a.hd / 4) > INT_MAX) return cudaErrorInvalidValue;
     if (t.n <= SEQ_TAB_SMALL) {
       SeqTab<SEQ_TAB_SMALL> u;
       u.n = t.n;
