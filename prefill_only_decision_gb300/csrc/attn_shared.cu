@@ -843,7 +843,7 @@ cudaError_t launch_tab(const SharedAttnArgs& a, const SeqTab<N>& tab, const Plan
 
 }  // namespace sha
 
-cudaError_t op_error_word(int** out) { return cudaGetSymbolAddress(reinterpret_cast<void**>(out), sha::g_err); }
+cudaError_t attention_shared_error_word(int** out) { return cudaGetSymbolAddress(reinterpret_cast<void**>(out), sha::g_err); }
 
 int64_t attention_shared_ws_bytes(int n_seq, const int* len, int P, int Hq, int Hkv, int hd, int num_sms) {
   int64_t need = 0;

@@ -1,53 +1,652 @@
 // Linear attention with a decay per head: S_t = lam_h S_{t-1} + v_t k_t^T, o_t = scale S_t q_t,
 // lam_h = exp(log_decay[h]). Prompts (launch_linattn) and single tokens (launch_linattn_step).
+//
+// Prompts run in chunks of 128 rows on the 5th-generation tensor cores. Within a chunk of n rows,
+// with S the state before it:
+//   O  = diag(scale lam^(i+1)) Q S^T + (scale lam^(i-j) q_i.k_j for j <= i, else 0) V
+//   S' = lam^n S + sum_j (lam^(n-1-j) v_j) k_j^T
+// One CTA takes a segment of consecutive chunks of one (sequence, head) in order, the state in TMEM
+// (fp32, lane = value row). A call with too few (sequence, head) pairs for the GPU cuts sequences
+// into segments: a first launch forms every segment's own contribution to the state (the second
+// line alone, from zero), a second joins them into the segments' start states, a third is the
+// pass over the chunks. What bounds it: q, k, v read and o written once, 4 x 32 KB per chunk and
+// head at 128 x 128, about 2.9 us of an SM's share of the HBM rate; the products of a chunk take
+// about 1.3 us of tensor time.
+// Operand precision: products take 16-bit operands and sum in fp32. Q, K and V enter as given. The
+// weights of V in a chunk, the decayed Q rows and the state's operand copy are rounded once to the
+// rows' type (the state itself never is). The decayed values v_j lam^(n-1-j) of the state update are
+// split into two such numbers (hi + lo), because the state is kept and returned in fp32: one
+// rounding of 2^-9 (bf16) would show in it. f16 rows: weights, decayed Q and the state's copy are
+// scaled by powers of two so that they use f16's range whatever the magnitudes: the state's copy by
+// 2^a (a per chunk), row i's weights by 2^c_i, its decayed Q by 2^(c_i - a), the output row by 2^-c_i,
+// and the decayed values, with the state they are added to, by 2^b (b per chunk, so that the low
+// parts stay above f16's smallest number).
+// One CTA per SM, 10 warps: 0 TMA producer (two stages of Q, K, V), 1 MMA issue, 2-5 rows of the
+// chunk (TMEM lane = row: weights, decayed Q, outputs), 6-9 value rows (TMEM lane = value row: the
+// state's copy and decay, the split decayed values).
+// 0 x NaN: rows past the sequence are zeroed in shared memory; non-finite V elements are replaced
+// by 0 and their terms are added, in the plain order of the formula, to exactly the rows and state
+// rows that they belong to.
 #include <algorithm>
+#include <climits>
+#include <type_traits>
 
 #include "common.cuh"
+#include "tcgen05.cuh"
 
 namespace s1 {
 namespace lin {
+using namespace t5;
 
 __device__ __forceinline__ float ld_f(const f16* p) { return __half2float(*p); }
 __device__ __forceinline__ float ld_f(const bf16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void st_f(f16* p, float x) { *p = __float2half_rn(x); }
 __device__ __forceinline__ void st_f(bf16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ uint32_t pack(f16, float lo, float hi) { return h2u(lo, hi); }
+__device__ __forceinline__ uint32_t pack(bf16, float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack(f16, uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+__device__ __forceinline__ float2 unpack(bf16, uint32_t u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+// an element's exponent field is all ones
+__device__ __forceinline__ bool nonfinite(f16, uint32_t u16) { return (u16 & 0x7c00u) == 0x7c00u; }
+__device__ __forceinline__ bool nonfinite(bf16, uint32_t u16) { return (u16 & 0x7f80u) == 0x7f80u; }
 
+// log2 of a head's decay: at most 0, and never -inf (2^-1e4 is 0 as well, and 0 * -1e4 is 0)
+__device__ __forceinline__ float log2_decay(float log_decay) {
+  return fmaxf(fminf(log_decay, 0.f) * 1.4426950408889634f, -1e4f);
+}
 // exp of a head's log decay: at most 1, exactly 0 for -inf
 __device__ __forceinline__ float decay(float log_decay) { return expf(fminf(log_decay, 0.f)); }
 
-// Token by token, one warp per (sequence, head, value row): the state row in registers.
-template <typename T, int DK, int N>
-__global__ void __launch_bounds__(128)
-    token_kernel(const __grid_constant__ SeqTab<N> tab, const LinAttnArgs a, int seq0) {
-  constexpr int E = DK / 32;
+constexpr int C = 128;                       // rows of a chunk
+constexpr int NTHREADS = 10 * 32;
+constexpr int ERR_TIMEOUT = 0x501;
+
+__device__ int g_err;                        // bounded waits record here (one word per device)
+
+constexpr int MAX_SEQ = 256;                 // sequences per launch
+
+// The sequences of a launch: rows row0[s] .. + len[s] - 1, segments segcum[s] .. segcum[s+1] - 1 of
+// seg_rows rows each (the last one shorter; an empty sequence has one). ws_seg[s]: the sequence's
+// first start state in the workspace, or -1 when it has a single segment.
+struct Tab {
+  int n, seq0, seg_rows;
+  int segcum[MAX_SEQ + 1];
+  int row0[MAX_SEQ], len[MAX_SEQ], ws_seg[MAX_SEQ];
+};
+
+// TMEM columns: weights of V (fp32, then 16-bit in the upper half; the lower half takes the low part
+// of the decayed values) | outputs | state | decayed Q | high part of the decayed values
+constexpr int TMEM_COLS = 512;
+constexpr int T_P = 0, T_O = 128, T_S = 256, T_Q = 384, T_VH = 448;
+
+template <int DK, int DV>
+struct Lay {
+  static constexpr int QB = C * DK * 2, VB = C * DV * 2;   // bytes of a Q or K tile, of a V tile
+  static constexpr int STAGE = 2 * QB + VB;                // Q, K, V
+  static constexpr int S16 = 2 * STAGE;                    // the state's operand copy [DV][DK]
+  static constexpr int PW = S16 + DV * DK * 2;             // lam^d, d = 0 .. 128
+  static constexpr int BAR = PW + (C + 4) * 4;
+  static constexpr int NBAR = 16;
+  static constexpr int USED = BAR + NBAR * 8 + 96;
+  static_assert(USED <= 227 * 1024, "shared memory of one CTA");
+  // above half an SM: each CTA allocates all of TMEM, so two never share one
+  static constexpr int BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
+};
+
+// Smallest e with |x| < 2^e (finite x != 0).
+__device__ __forceinline__ int exp_above(float x) { return (int)((__float_as_uint(x) >> 23) & 255) - 126; }
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 .. 127
+
+// OUT: outputs and final states from the segments' start states. !OUT: the segments' own
+// contributions to the state into the workspace (all segments but each sequence's last).
+template <typename T, int DK, int DV, bool OUT>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    chunk_kernel(const __grid_constant__ Tab tab, const __grid_constant__ CUtensorMap mapQ,
+                 const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                 const __grid_constant__ LinAttnArgs a) {
+  using L = Lay<DK, DV>;
+  constexpr bool F16 = std::is_same<T, f16>::value;
+  constexpr uint32_t BF = F16 ? 0 : 1;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  uint64_t* bars = (uint64_t*)(sm + L::BAR);
+  uint64_t* full = bars;                       // [2] the stage's tiles have landed
+  uint64_t* empty = bars + 2;                  // [2] the stage may be filled again
+  uint64_t* clean = bars + 4;                  // [2] its rows past the end and non-finite V are zeros
+  uint64_t* p_full = bars + 6;                 // Q K^T is in TMEM
+  uint64_t* p_ready = bars + 7;                // weights and decayed Q are in TMEM
+  uint64_t* s_ready = bars + 8;                // the state's copy is in shared memory, its decay applied
+  uint64_t* v_ready = bars + 9;                // the decayed values are in TMEM
+  uint64_t* o_full = bars + 10;                // outputs are in TMEM
+  uint64_t* ds_done = bars + 11;               // the state holds this chunk
+  uint64_t* smax = bars + 12;                  // the state's maximum over the four warps is known
+  uint64_t* mma_idle = bars + 13;
+  uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // V has held a non-finite element
+  volatile int* s_exp = (volatile int*)(tmem_slot + 3);    // a of the chunk
+  volatile float* wmax = (volatile float*)(tmem_slot + 4); // [2][4] |S| per warp, by chunk parity
+  volatile int* vmax = (volatile int*)(tmem_slot + 12);    // [2][4] |V| as f16 bits, by stage
+  float* pw = reinterpret_cast<float*>(sm + L::PW);
+
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  // this CTA's segment
+  const int h = blockIdx.x % a.H, seg = blockIdx.x / a.H;
+  int s = 0;
+  for (int lo = 0, hi = tab.n - 1; lo < hi;) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tab.segcum[mid] <= seg) lo = mid;
+    else hi = mid - 1;
+    s = lo;
+  }
+  const int k_seg = seg - tab.segcum[s];       // segment of the sequence
+  const bool last = seg + 1 == tab.segcum[s + 1];
+  if (!OUT && last) {                          // (nothing needs its contribution)
+    allow_dependents();
+    wait_prerequisites();
+    return;
+  }
+  const int len = tab.len[s], beg = k_seg * tab.seg_rows, end = min(len, beg + tab.seg_rows);
+  const int nch = (end - beg + C - 1) / C;     // chunks (0 for an empty sequence)
+  const int64_t row0 = (int64_t)tab.row0[s] + beg;
+  const int64_t per = (int64_t)a.H * DV * DK, head = (int64_t)h * DV * DK;
+  float* ws_state = (float*)a.ws + (tab.ws_seg[s] < 0 ? 0 : tab.ws_seg[s] + k_seg) * per + head;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], OUT ? 1 + 4 : 1);
+      mbar_init(&clean[i], 4);
+    }
+    mbar_init(p_full, 1);
+    mbar_init(p_ready, 4);
+    mbar_init(s_ready, 4);
+    mbar_init(v_ready, 4);
+    mbar_init(o_full, 1);
+    mbar_init(ds_done, 1);
+    mbar_init(smax, 4);
+    mbar_init(mma_idle, 1);
+    *abort_flag = 0;
+    *v_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc<TMEM_COLS>(tmem_slot);
   allow_dependents();
   wait_prerequisites();
-  const int lane = threadIdx.x & 31;
-  const int w = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int h = w / a.dv, r = w % a.dv, s = blockIdx.y;
-  const int64_t at = ((int64_t)h * a.dv + r) * DK + lane * E, per = (int64_t)a.H * a.dv * DK;
-  float S[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) S[e] = a.S_in ? a.S_in[(int64_t)(seq0 + s) * a.s_in_stride + at + e] : 0.f;
-  const float lam = decay(a.log_decay[h]);
-  const int64_t row0 = tab.row0[s], n = tab.cum[s + 1] - tab.cum[s];
-  for (int64_t t = row0; t < row0 + n; ++t) {
-    const T* q = (const T*)a.q + t * a.q_stride + h * DK + lane * E;
-    const T* k = (const T*)a.k + t * a.k_stride + h * DK + lane * E;
-    const float v = ld_f((const T*)a.v + t * a.v_stride + h * a.dv + r);
-    float o = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      S[e] = lam * S[e] + v * ld_f(k + e);
-      o += S[e] * ld_f(q + e);
+  const float l2 = log2_decay(a.log_decay[h]);
+  if (threadIdx.x <= C) pw[threadIdx.x] = exp2f(l2 * (float)threadIdx.x);
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto wwait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_err, ERR_TIMEOUT) ? 1 : 0) != 0;
+  };
+  auto arrive = [&](uint64_t* bar) {           // once per warp, after what it wrote
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+
+  if (warp == 0) {
+    // ---- TMA producer
+    if (lane == 0) {
+      int c = 0;
+      for (; c < nch; ++c) {
+        const int st = c & 1, r = (int)(row0 + c * C);
+        if (!mbar_wait(&empty[st], ((c >> 1) & 1) ^ 1, abort_flag, &g_err, ERR_TIMEOUT)) break;
+        uint8_t* base = sm + st * L::STAGE;
+        mbar_expect_tx(&full[st], (OUT ? L::QB : 0) + L::QB + L::VB);
+        for (int b = 0; b < DK / 64; ++b) {
+          if (OUT) tma3(base + b * C * 128, &mapQ, &full[st], 64 * b, h, r);
+          tma3(base + L::QB + b * C * 128, &mapK, &full[st], 64 * b, h, r);
+        }
+        for (int b = 0; b < DV / 64; ++b) tma3(base + 2 * L::QB + b * C * 128, &mapV, &full[st], 64 * b, h, r);
+      }
+      if (*abort_flag)                         // copies in flight land before the CTA leaves
+        for (int x = c > 2 ? c - 2 : 0; x < c; ++x) mbar_drain(&full[x & 1], (x >> 1) & 1);
     }
-    o = warp_sum(o);
-    if (lane == 0) st_f((T*)a.out + (t * a.H + h) * a.dv + r, o * a.scale);
-  }
-  if (a.S_out) {
+  } else if (warp == 1) {
+    // ---- MMA issue
+    const bool leader = elect_one();
+    constexpr uint32_t ID_P = idesc_f16(C, BF, 0, 0), ID_QS = idesc_f16(DV, BF, 0, 0), ID_PV = idesc_f16(DV, BF, 0, 1),
+                       ID_S = idesc_f16(DK, BF, 0, 1);
+    for (int c = 0; c < nch; ++c) {
+      const int st = c & 1;
+      const uint32_t ph = c & 1, sph = (c >> 1) & 1;
+      const uint32_t base = smem_u32(sm + st * L::STAGE);
+      const uint32_t ka = base + L::QB, va = base + 2 * L::QB;
+      if (!wwait(&full[st], sph)) break;
+      if constexpr (OUT) {
+        fence_after();
+        if (leader) {                          // Q K^T
+          const uint64_t qd = desc_sw128(base, 16), kd = desc_sw128(ka, 16);
 #pragma unroll
-    for (int e = 0; e < E; ++e) a.S_out[(seq0 + s) * per + at + e] = S[e];
+          for (int kk = 0; kk < DK / 16; ++kk) {
+            const uint64_t off = (uint64_t)(((kk >> 2) * (C * 128) + (kk & 3) * 32) >> 4);
+            mma_ss(tmem + T_P, qd + off, kd + off, ID_P, kk > 0 ? 1u : 0u);
+          }
+          commit(p_full);
+        }
+        __syncwarp();
+        if (!wwait(s_ready, ph) || !wwait(p_ready, ph) || !wwait(&clean[st], sph)) break;
+        fence_after();
+        if (leader) {                          // O = (decayed Q) S^T + weights V
+          const uint64_t sd = desc_sw128(smem_u32(sm + L::S16), 16), vd = desc_sw128(va, C * 128);
+#pragma unroll
+          for (int kk = 0; kk < DK / 16; ++kk)
+            mma_ts(tmem + T_O, tmem + T_Q + kk * 8, sd + (uint64_t)(((kk >> 2) * (DV * 128) + (kk & 3) * 32) >> 4),
+                   ID_QS, kk > 0 ? 1u : 0u);
+#pragma unroll
+          for (int kk = 0; kk < C / 16; ++kk)
+            mma_ts(tmem + T_O, tmem + T_P + 64 + kk * 8, vd + (uint64_t)(kk * 16 * 128 >> 4), ID_PV, 1u);
+          commit(o_full);
+        }
+        __syncwarp();
+      }
+      if (!wwait(v_ready, ph)) break;
+      fence_after();
+      if (leader) {                            // S += (decayed V)^T K, high and low parts
+        const uint64_t kd = desc_sw128(ka, C * 128);
+#pragma unroll
+        for (int kk = 0; kk < C / 16; ++kk)
+          mma_ts(tmem + T_S, tmem + T_VH + kk * 8, kd + (uint64_t)(kk * 16 * 128 >> 4), ID_S,
+                 OUT || c > 0 || kk > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < C / 16; ++kk)
+          mma_ts(tmem + T_S, tmem + T_P + kk * 8, kd + (uint64_t)(kk * 16 * 128 >> 4), ID_S, 1u);
+        commit(ds_done);
+        commit(&empty[st]);
+      }
+      __syncwarp();
+    }
+    if (leader) {
+      commit(mma_idle);
+      mbar_drain(mma_idle, 0);                 // every MMA issued above has completed
+    }
+  } else if (warp < 6) {
+    // ---- rows of the chunk: thread = row i
+    if constexpr (OUT) {
+      const int quad = warp & 3, i = quad * 32 + lane;
+      const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+      const uint32_t tP = tmem + lane_off + T_P, tO = tmem + lane_off + T_O, tQ = tmem + lane_off + T_Q;
+      for (int c = 0; c < nch; ++c) {
+        const int st = c & 1, n = min(C, end - beg - c * C);
+        const uint32_t ph = c & 1, sph = (c >> 1) & 1;
+        const uint8_t* qrow = sm + st * L::STAGE + i * 128;
+        if (!wwait(&full[st], sph) || !wwait(p_full, ph)) break;
+        fence_after();
+        // weights of V: scale lam^(i-j) q_i.k_j, 0 for j > i
+        float p[C];
+#pragma unroll
+        for (int b = 0; b < C; b += 32) {
+          uint32_t u[32];
+          tld32(tP + b, u);
+          ld_wait();
+          pin32(u);
+          const float* w = pw + i - b;         // lam^(i-j) at w[-(j - b)]; rows above the diagonal: unused
+#pragma unroll
+          for (int e = 0; e < 32; ++e) p[b + e] = b + e <= i ? __uint_as_float(u[e]) * (a.scale * w[-e]) : 0.f;
+        }
+        const float qs = a.scale * pw[i + 1];
+        auto q8 = [&](int k, float* x) {       // 8 decayed elements of the Q row
+          const uint4 v = *reinterpret_cast<const uint4*>(qrow + (k >> 3) * (C * 128) + (((k & 7) ^ (i & 7)) << 4));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack(T(), w[e]);
+            x[2 * e] = f.x * qs;
+            x[2 * e + 1] = f.y * qs;
+          }
+        };
+        int cexp = 0;                          // c_i
+        float fp = 1.f, fq = 1.f;
+        if constexpr (F16) {
+          float mp = 0.f, mq = 0.f;
+#pragma unroll
+          for (int e = 0; e < C; ++e) mp = fmaxf(mp, fabsf(p[e]));
+#pragma unroll
+          for (int k = 0; k < DK / 8; ++k) {
+            float x[8];
+            q8(k, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mq = fmaxf(mq, fabsf(x[e]));
+          }
+          if (!wwait(s_ready, ph)) break;
+          const int sa = *s_exp;
+          cexp = 100;
+          if (mp > 0.f) cexp = min(cexp, 14 - exp_above(mp));
+          if (mq > 0.f && sa < 100) cexp = min(cexp, sa + 14 - exp_above(mq));
+          cexp = max(cexp, -100);
+          fp = pow2f(cexp);
+          const int qe = cexp - sa;            // (at most 14 - the exponent of mq, or the state is zero)
+          fq = qe < -126 ? 0.f : pow2f(min(qe, 126));
+        }
+#pragma unroll
+        for (int b = 0; b < C; b += 32) {
+          uint32_t u[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) u[e] = pack(T(), p[b + 2 * e] * fp, p[b + 2 * e + 1] * fp);
+          tst16(tP + 64 + b / 2, u);
+        }
+#pragma unroll
+        for (int k = 0; k < DK / 8; k += 4) {
+          uint32_t u[16];
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4) {
+            float x[8];
+            q8(k + k4, x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[4 * k4 + e] = pack(T(), x[2 * e] * fq, x[2 * e + 1] * fq);
+          }
+          tst16(tQ + k * 4, u);
+        }
+        st_wait();
+        fence_before();
+        arrive(p_ready);
+        // outputs; staged in the V tile once the decayed values have been taken from it
+        if (!wwait(o_full, ph) || !wwait(v_ready, ph)) break;
+        fence_after();
+        const float fo = F16 ? pow2f(-cexp) : 1.f;
+        const bool fix = *v_flag && i < n;
+        uint8_t* stage = sm + st * L::STAGE + 2 * L::QB;
+#pragma unroll
+        for (int b = 0; b < DV; b += 32) {
+          uint32_t u[32];
+          __syncwarp();
+          tld32(tO + b, u);
+          ld_wait();
+          pin32(u);
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]) * fo;
+          if (fix) {                           // terms of non-finite V elements
+            const int64_t r0 = row0 + c * C;
+            const T* q = (const T*)a.q + (r0 + i) * a.q_stride + h * DK;
+#pragma unroll 1
+            for (int j = 0; j <= i; ++j) {
+              const T* v = (const T*)a.v + (r0 + j) * a.v_stride + h * DV + b;
+              bool any = false;
+              for (int e = 0; e < 32; ++e) any |= !isfinite(ld_f(v + e));
+              if (!any) continue;
+              const T* k = (const T*)a.k + (r0 + j) * a.k_stride + h * DK;
+              float z = 0.f;
+              for (int e = 0; e < DK; ++e) z += ld_f(q + e) * ld_f(k + e);
+              z *= a.scale * pw[i - j];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float x = ld_f(v + e);
+                if (!isfinite(x)) o[e] += z * x;
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4*>(stage + i * (DV * 2) + ((((b + e) / 8) ^ (i & 7)) << 4)) =
+                make_uint4(pack(T(), o[e], o[e + 1]), pack(T(), o[e + 2], o[e + 3]), pack(T(), o[e + 4], o[e + 5]),
+                           pack(T(), o[e + 6], o[e + 7]));
+        }
+        __syncwarp();
+        constexpr int CH = DV / 8;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+          const int e = k * 32 + lane, r = quad * 32 + e / CH, q = e % CH;
+          if (r < n)
+            *reinterpret_cast<uint4*>((T*)a.out + ((row0 + c * C + r) * a.H + h) * DV + q * 8) =
+                *reinterpret_cast<const uint4*>(stage + r * (DV * 2) + ((q ^ (r & 7)) << 4));
+        }
+        fence_async_smem();                    // the stage's next fill is a TMA write
+        fence_before();
+        arrive(&empty[st]);
+      }
+    }
+  } else {
+    // ---- value rows: thread = row dv of the state (64 value rows: twice over the 128 lanes)
+    const int quad = warp & 3, r = quad * 32 + lane, dv = r % DV;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t tS = tmem + lane_off + T_S, tVH = tmem + lane_off + T_VH, tVL = tmem + lane_off + T_P;
+    bool ok = true;
+    int bexp = 0;                              // b: the state in TMEM is 2^b times the state (f16)
+    // adds chunk c's terms of non-finite V elements to this value row's state columns b .. b+31
+    auto fix_state = [&](int c, int b, float* x) {
+      const int n = min(C, end - beg - c * C);
+      const int64_t r0 = row0 + c * C;
+#pragma unroll 1
+      for (int t = 0; t < n; ++t) {
+        const float v = ld_f((const T*)a.v + (r0 + t) * a.v_stride + h * DV + dv);
+        if (isfinite(v)) continue;
+        const T* k = (const T*)a.k + (r0 + t) * a.k_stride + h * DK + b;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] += pw[n - 1 - t] * v * ld_f(k + e);
+      }
+    };
+    if constexpr (OUT) {
+      // the start state into TMEM
+      const float* src = tab.ws_seg[s] >= 0 ? ws_state
+                                            : (a.S_in ? a.S_in + (int64_t)(tab.seq0 + s) * a.s_in_stride + head : nullptr);
+#pragma unroll
+      for (int b = 0; b < DK; b += 32) {
+        uint32_t u[32];
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 v = src ? *reinterpret_cast<const float4*>(src + (int64_t)dv * DK + b + e)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+          u[e] = __float_as_uint(v.x);
+          u[e + 1] = __float_as_uint(v.y);
+          u[e + 2] = __float_as_uint(v.z);
+          u[e + 3] = __float_as_uint(v.w);
+        }
+        tst32(tS + b, u);
+      }
+      st_wait();
+    }
+    for (int c = 0; c < nch; ++c) {
+      const int st = c & 1, n = min(C, end - beg - c * C);
+      const uint32_t ph = c & 1, sph = (c >> 1) & 1;
+      uint8_t* kt = sm + st * L::STAGE + L::QB;
+      uint8_t* vt = kt + L::QB;
+      if (!wwait(&full[st], sph)) { ok = false; break; }
+      // rows past the end to zeros (K and V), non-finite V elements to zero
+      {
+        constexpr int KC = DK / 8, VC = DV / 8;
+        const int tid = (warp - 6) * 32 + lane;
+        if (n < C) {
+          for (int e = tid; e < (C - n) * KC; e += 128) {
+            const int t = n + e / KC, q = e % KC;
+            *reinterpret_cast<uint4*>(kt + (q >> 3) * (C * 128) + t * 128 + ((q & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+          for (int e = tid; e < (C - n) * VC; e += 128) {
+            const int t = n + e / VC, q = e % VC;
+            *reinterpret_cast<uint4*>(vt + (q >> 3) * (C * 128) + t * 128 + ((q & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        bool bad = false;
+        uint32_t vm = 0;
+#pragma unroll 4
+        for (int e = tid; e < n * VC; e += 128) {
+          uint4* at = reinterpret_cast<uint4*>(vt + (e % VC >> 3) * (C * 128) + (e / VC) * 128 + ((e % VC & 7) << 4));
+          uint4 v = *at;
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          bool hit = false;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const bool b0 = nonfinite(T(), w[q] & 0xffffu), b1 = nonfinite(T(), w[q] >> 16);
+            if (b0) w[q] &= 0xffff0000u;
+            if (b1) w[q] &= 0xffffu;
+            hit |= b0 || b1;
+            if constexpr (F16) vm = max(vm, max(w[q] & 0x7fffu, (w[q] >> 16) & 0x7fffu));
+          }
+          if (hit) *at = make_uint4(w[0], w[1], w[2], w[3]);
+          bad |= hit;
+        }
+        if (bad) *v_flag = 1;
+        if constexpr (F16) {
+          vm = __reduce_max_sync(0xffffffffu, vm);
+          if (lane == 0) vmax[st * 4 + warp - 6] = (int)vm;
+        }
+        fence_async_smem();
+        arrive(&clean[st]);
+        // (this role's own reads of V below: all four warps have cleaned their share)
+        if (!wwait(&clean[st], sph)) { ok = false; break; }
+      }
+      if (c > 0 && !wwait(ds_done, (c - 1) & 1)) { ok = false; break; }
+      fence_after();
+      const float dec = pw[n];
+      int bnew = 0;
+      if constexpr (F16) {                     // decayed values below 2^14
+        const int vm = max(max(vmax[st * 4], vmax[st * 4 + 1]), max(vmax[st * 4 + 2], vmax[st * 4 + 3]));
+        if (vm > 0) bnew = 14 - exp_above(__half2float(__ushort_as_half((unsigned short)vm)));
+      }
+      if (OUT || c > 0) {
+        // state: operand copy (scaled for f16), then decayed in place
+        float x[DK];
+#pragma unroll
+        for (int b = 0; b < DK; b += 32) {
+          uint32_t u[32];
+          tld32(tS + b, u);
+          ld_wait();
+          pin32(u);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[b + e] = F16 ? __uint_as_float(u[e]) * pow2f(-bexp) : __uint_as_float(u[e]);
+          if (c > 0 && *v_flag) fix_state(c - 1, b, x + b);
+        }
+        if constexpr (OUT) {
+          float f = 1.f;
+          if constexpr (F16) {
+            float m = 0.f;
+#pragma unroll
+            for (int e = 0; e < DK; ++e) m = fmaxf(m, isfinite(x[e]) ? fabsf(x[e]) : 0.f);
+            m = warp_max(m);
+            if (lane == 0) wmax[ph * 4 + warp - 6] = m;
+            arrive(smax);
+            if (!wwait(smax, ph)) { ok = false; break; }
+            m = fmaxf(fmaxf(wmax[ph * 4], wmax[ph * 4 + 1]), fmaxf(wmax[ph * 4 + 2], wmax[ph * 4 + 3]));
+            const int sa = m > 0.f ? max(-100, min(100, 14 - exp_above(m))) : 100;
+            if (warp == 6 && lane == 0) *s_exp = sa;
+            f = pow2f(sa);
+            if (m > 0.f) bnew = min(bnew, 120 - exp_above(m));   // (the scaled state stays finite)
+          }
+          if (r < DV) {
+#pragma unroll
+            for (int k = 0; k < DK / 8; ++k) {
+              const float* y = x + 8 * k;
+              *reinterpret_cast<uint4*>(sm + L::S16 + (k >> 3) * (DV * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4)) =
+                  make_uint4(pack(T(), y[0] * f, y[1] * f), pack(T(), y[2] * f, y[3] * f),
+                             pack(T(), y[4] * f, y[5] * f), pack(T(), y[6] * f, y[7] * f));
+            }
+          }
+        }
+        const float ds = F16 ? dec * pow2f(bnew) : dec;
+#pragma unroll
+        for (int b = 0; b < DK; b += 32) {
+          uint32_t u[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(x[b + e] * ds);
+          tst32(tS + b, u);
+        }
+        st_wait();
+        if constexpr (OUT) {
+          fence_async_smem();
+          fence_before();
+          arrive(s_ready);
+        }
+      }
+      bexp = bnew;
+      const float sb = F16 ? pow2f(bnew) : 1.f;
+      // decayed values, split: high part (nearest), low part (what it leaves)
+      {
+        const uint8_t* col = vt + (dv >> 6) * (C * 128) + (dv & 7) * 2;
+        const int ch = (dv & 63) >> 3;
+        uint32_t hi[64], lo[64];
+#pragma unroll
+        for (int t = 0; t < C; t += 2) {
+          float y[2], yh[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const T v = *reinterpret_cast<const T*>(col + (t + e) * 128 + ((ch ^ ((t + e) & 7)) << 4));
+            const int d = n - 1 - (t + e);
+            y[e] = ld_f(&v) * (d >= 0 ? pw[d] * sb : 0.f);
+          }
+          hi[t / 2] = pack(T(), y[0], y[1]);
+          const float2 f = unpack(T(), hi[t / 2]);
+          yh[0] = f.x;
+          yh[1] = f.y;
+          lo[t / 2] = pack(T(), y[0] - yh[0], y[1] - yh[1]);
+        }
+        tst32(tVH, hi);
+        tst32(tVH + 32, hi + 32);
+        if constexpr (OUT) {                   // the low part's columns: the weights have left them
+          if (!wwait(p_ready, ph)) { ok = false; break; }
+          fence_after();
+        }
+        tst32(tVL, lo);
+        tst32(tVL + 32, lo + 32);
+        st_wait();
+        fence_before();
+        arrive(v_ready);
+      }
+    }
+    // ---- the state after the segment
+    float* dst = OUT ? (last && a.S_out ? a.S_out + (int64_t)(tab.seq0 + s) * per + head : nullptr) : ws_state;
+    if (ok && nch > 0) ok = wwait(ds_done, (nch - 1) & 1);
+    fence_after();
+    if (ok && dst) {
+#pragma unroll
+      for (int b = 0; b < DK; b += 32) {
+        uint32_t u[32];
+        __syncwarp();
+        tld32(tS + b, u);
+        ld_wait();
+        pin32(u);
+        float x[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = F16 ? __uint_as_float(u[e]) * pow2f(-bexp) : __uint_as_float(u[e]);
+        if (nch > 0 && *v_flag) fix_state(nch - 1, b, x);
+        if (r < DV) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(dst + (int64_t)dv * DK + b + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        }
+      }
+    }
   }
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    tmem_free<TMEM_COLS>(tmem);
+  }
+}
+
+// Start states: in each sequence of several segments, slot k of the workspace (segment k's own
+// contribution) becomes the state before segment k (segment 0's is the initial state: the last
+// segment may overwrite that one in place). One thread per four state elements.
+__global__ void __launch_bounds__(256)
+    scan_kernel(const __grid_constant__ Tab tab, const __grid_constant__ LinAttnArgs a) {
+  allow_dependents();
+  wait_prerequisites();
+  const int s = blockIdx.y;
+  if (tab.ws_seg[s] < 0) return;
+  const int64_t per4 = (int64_t)a.H * a.dv * a.dk / 4, hd4 = (int64_t)a.dv * a.dk / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= per4) return;
+  const float f = exp2f(log2_decay(a.log_decay[i / hd4]) * (float)tab.seg_rows);
+  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.S_in)
+    S = *reinterpret_cast<const float4*>(a.S_in + (int64_t)(tab.seq0 + s) * a.s_in_stride + 4 * i);
+  const int n = tab.segcum[s + 1] - tab.segcum[s];
+  float4* w = reinterpret_cast<float4*>(a.ws) + (int64_t)tab.ws_seg[s] * per4 + i;
+#pragma unroll 4
+  for (int k = 0; k + 1 < n; ++k) {
+    const float4 b = w[(int64_t)k * per4];
+    w[(int64_t)k * per4] = S;
+    S.x = f * S.x + b.x;
+    S.y = f * S.y + b.y;
+    S.z = f * S.z + b.z;
+    S.w = f * S.w + b.w;
+  }
+  w[(int64_t)(n - 1) * per4] = S;
 }
 
 // One token per sequence. A block takes 32 value rows of one (sequence, head), a warp 8 of them:
@@ -99,40 +698,110 @@ __global__ void __launch_bounds__(128)
 
 }  // namespace lin
 
-int64_t linattn_ws_bytes(int, const int*, int, int, int, int) { return 0; }
+cudaError_t linattn_error_word(int** out) { return cudaGetSymbolAddress(reinterpret_cast<void**>(out), lin::g_err); }
 
-template <int N>
-static cudaError_t lin_group(const LinAttnArgs& a, const SeqTab<N>& tab, int seq0, cudaStream_t st) {
-  const dim3 grid(a.H * a.dv / 4, tab.n), block(128);
-  if (a.dtype == ELEM_F16)
-    return a.dk == 128 ? launch_pdl(lin::token_kernel<f16, 128, N>, grid, block, 0, st, tab, a, seq0)
-                       : launch_pdl(lin::token_kernel<f16, 64, N>, grid, block, 0, st, tab, a, seq0);
-  return a.dk == 128 ? launch_pdl(lin::token_kernel<bf16, 128, N>, grid, block, 0, st, tab, a, seq0)
-                     : launch_pdl(lin::token_kernel<bf16, 64, N>, grid, block, 0, st, tab, a, seq0);
+// Rows per segment (a multiple of the chunk) for a group of sequences: the count with the least
+// estimated time in us, waves of CTAs x (chunks of a segment + a CTA's fixed cost), with the
+// contributions' launch and the join added once sequences are cut.
+static int seg_rows_for(const int* len, int n, int H, int num_sms) {
+  int longest = 1;
+  for (int s = 0; s < n; ++s) longest = std::max(longest, len[s]);
+  const int max_ch = (int)(((int64_t)longest + lin::C - 1) / lin::C);
+  int best_m = max_ch;
+  double best = 1e30;
+  for (int m = max_ch; m >= 1; m = m > 8 ? m - (m + 7) / 8 : m - 1) {
+    int64_t ctas = 0, first = 0;
+    for (int s = 0; s < n; ++s) {
+      const int64_t segs = std::max<int64_t>(1, ((int64_t)len[s] + (int64_t)m * lin::C - 1) / ((int64_t)m * lin::C));
+      ctas += segs * H;
+      first += (segs - 1) * H;
+    }
+    double t = (double)((ctas + num_sms - 1) / num_sms) * (3.0 * m + 4.0);
+    if (first > 0) t += (double)((first + num_sms - 1) / num_sms) * (2.0 * m + 3.0) + 4.0;
+    if (t < best) {
+      best = t;
+      best_m = m;
+    }
+  }
+  return (int)std::min<int64_t>((int64_t)best_m * lin::C, INT_MAX - INT_MAX % lin::C);
 }
 
-cudaError_t launch_linattn(const LinAttnArgs& a, int n_seq, const int* row0, const int* len, int, cudaStream_t st) {
-  int s = 0;
-  while (s < n_seq) {
-    const int seq0 = s;
-    SeqTab<SEQ_TAB_LARGE> t;
-    t.n = 0;
-    t.cum[0] = 0;
-    for (; s < n_seq && t.n < SEQ_TAB_LARGE; ++s) {
-      if ((int64_t)t.cum[t.n] + len[s] > INT32_MAX) break;
-      t.row0[t.n] = row0[s];
-      t.cum[t.n + 1] = t.cum[t.n] + len[s];
-      ++t.n;
-    }
-    if (t.n <= SEQ_TAB_SMALL) {
-      SeqTab<SEQ_TAB_SMALL> u;
-      u.n = t.n;
-      std::copy(t.cum, t.cum + t.n + 1, u.cum);
-      std::copy(t.row0, t.row0 + t.n, u.row0);
-      CK_RET(lin_group(a, u, seq0, st));
-    } else {
-      CK_RET(lin_group(a, t, seq0, st));
-    }
+// Fills `t` with sequences from `s` on; returns the first one not taken. *slots: start states that
+// the group keeps in the workspace.
+static int lin_group(lin::Tab& t, int s, int n_seq, const int* row0, const int* len, int H, int num_sms,
+                     int64_t* slots) {
+  t.seq0 = s;
+  t.n = std::min(n_seq - s, lin::MAX_SEQ);
+  t.seg_rows = seg_rows_for(len + s, t.n, H, num_sms);
+  t.segcum[0] = 0;
+  *slots = 0;
+  for (int i = 0; i < t.n; ++i) {
+    const int segs = std::max(1, (int)(((int64_t)len[s + i] + t.seg_rows - 1) / t.seg_rows));
+    t.row0[i] = row0 ? row0[s + i] : 0;
+    t.len[i] = len[s + i];
+    t.segcum[i + 1] = t.segcum[i] + segs;
+    t.ws_seg[i] = segs > 1 ? (int)*slots : -1;
+    if (segs > 1) *slots += segs;
+  }
+  return s + t.n;
+}
+
+int64_t linattn_ws_bytes(int n_seq, const int* len, int H, int dk, int dv, int num_sms) {
+  int64_t need = 0, slots;
+  lin::Tab t;
+  for (int s = 0; s < n_seq;) {
+    s = lin_group(t, s, n_seq, nullptr, len, H, num_sms, &slots);
+    need = std::max(need, slots * H * dk * dv * 4);
+  }
+  return need;
+}
+
+template <typename T, int DK, int DV>
+static cudaError_t lin_launch(const LinAttnArgs& a, const lin::Tab& t, int64_t slots, const CUtensorMap* m,
+                              cudaStream_t st) {
+  using L = lin::Lay<DK, DV>;
+  const dim3 grid((unsigned)((int64_t)t.segcum[t.n] * a.H)), block(lin::NTHREADS);
+  if (slots > 0) {
+    CK_RET(cudaFuncSetAttribute(lin::chunk_kernel<T, DK, DV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                L::BYTES));
+    CK_RET(launch_pdl(lin::chunk_kernel<T, DK, DV, false>, grid, block, L::BYTES, st, t, m[0], m[1], m[2], a));
+    const int64_t per4 = (int64_t)a.H * DK * DV / 4;
+    CK_RET(launch_pdl(lin::scan_kernel, dim3((unsigned)((per4 + 255) / 256), t.n), dim3(256), 0, st, t, a));
+  }
+  CK_RET(cudaFuncSetAttribute(lin::chunk_kernel<T, DK, DV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES));
+  return launch_pdl(lin::chunk_kernel<T, DK, DV, true>, grid, block, L::BYTES, st, t, m[0], m[1], m[2], a);
+}
+
+cudaError_t launch_linattn(const LinAttnArgs& a, int n_seq, const int* row0, const int* len, int num_sms,
+                           cudaStream_t st) {
+  int64_t rows = 1;
+  for (int s = 0; s < n_seq; ++s)
+    if (len[s]) rows = std::max(rows, (int64_t)row0[s] + len[s]);
+  CUtensorMap m[3];
+  const void* ptr[3] = {a.q, a.k, a.v};
+  const int d[3] = {a.dk, a.dk, a.dv};
+  const int64_t ld[3] = {a.q_stride, a.k_stride, a.v_stride};
+  for (int i = 0; i < 3; ++i) {
+    const uint64_t dims[3] = {(uint64_t)d[i], (uint64_t)a.H, (uint64_t)rows};
+    const uint64_t str[2] = {(uint64_t)d[i] * 2, (uint64_t)ld[i] * 2};
+    const uint32_t box[3] = {64, 1, lin::C};
+    if (!encode_tensor_map(&m[i], a.dtype == ELEM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                           3, ptr[i], dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  lin::Tab t;
+  for (int s = 0; s < n_seq;) {
+    int64_t slots;
+    s = lin_group(t, s, n_seq, row0, len, a.H, num_sms, &slots);
+    if ((int64_t)t.segcum[t.n] * a.H > INT_MAX) return cudaErrorInvalidValue;
+#define LIN_GO(T)                                                                                        \
+  CK_RET(a.dk == 128 ? (a.dv == 128 ? lin_launch<T, 128, 128>(a, t, slots, m, st)                   \
+                                    : lin_launch<T, 128, 64>(a, t, slots, m, st))                   \
+                     : (a.dv == 128 ? lin_launch<T, 64, 128>(a, t, slots, m, st)                    \
+                                    : lin_launch<T, 64, 64>(a, t, slots, m, st)))
+    if (a.dtype == ELEM_F16) LIN_GO(f16);
+    else LIN_GO(bf16);
+#undef LIN_GO
   }
   return cudaSuccess;
 }

@@ -101,17 +101,21 @@ extern "C" {
 
 int s1_op_sync(void* stream) {
   cudaStream_t st = (cudaStream_t)stream;
-  int* word = nullptr;
-  int h = 0, zero = 0;
-  cudaError_t e = op_error_word(&word);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(&h, word, sizeof(int), cudaMemcpyDeviceToHost, st);
+  int* word[2] = {nullptr, nullptr};
+  int h[2] = {0, 0};
+  const int zero = 0;
+  cudaError_t e = attention_shared_error_word(&word[0]);
+  if (e == cudaSuccess) e = linattn_error_word(&word[1]);
+  for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+    e = cudaMemcpyAsync(&h[i], word[i], sizeof(int), cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  if (e == cudaSuccess && h) {
-    e = cudaMemcpyAsync(word, &zero, sizeof(int), cudaMemcpyHostToDevice, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  }
+  for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+    if (h[i]) {
+      e = cudaMemcpyAsync(word[i], &zero, sizeof(int), cudaMemcpyHostToDevice, st);
+      if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    }
   if (e != cudaSuccess) return cuda_rc(e, "op_sync");
-  if (h) return s1::set_error(S1_ERR_DEVICE_TIMEOUT, "op_sync: a bounded device wait gave up");
+  if (h[0] || h[1]) return s1::set_error(S1_ERR_DEVICE_TIMEOUT, "op_sync: a bounded device wait gave up");
   return S1_OK;
 }
 
