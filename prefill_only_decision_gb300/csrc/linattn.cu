@@ -21,9 +21,9 @@
 // 2^a (a per chunk), row i's weights by 2^c_i, its decayed Q by 2^(c_i - a), the output row by 2^-c_i,
 // and the decayed values, with the state they are added to, by 2^b (b per chunk, so that the low
 // parts stay above f16's smallest number).
-// One CTA per SM, 10 warps: 0 TMA producer (two stages of Q, K, V), 1 MMA issue, 2-5 rows of the
-// chunk (TMEM lane = row: weights, decayed Q, outputs), 6-9 value rows (TMEM lane = value row: the
-// state's copy and decay, the split decayed values).
+// One CTA per SM, 18 warps: 0 TMA producer (two stages of Q, K, V), 1 MMA issue, 2-9 rows of the
+// chunk (TMEM lane = row, two threads a row: weights, decayed Q, outputs), 10-17 value rows (TMEM
+// lane = value row, two threads a row: the state's copy and decay, the split decayed values).
 // 0 x NaN: rows past the sequence are zeroed in shared memory; non-finite V elements are replaced
 // by 0 and their terms are added, in the plain order of the formula, to exactly the rows and state
 // rows that they belong to.
@@ -63,7 +63,7 @@ __device__ __forceinline__ float log2_decay(float log_decay) {
 __device__ __forceinline__ float decay(float log_decay) { return expf(fminf(log_decay, 0.f)); }
 
 constexpr int C = 128;                       // rows of a chunk
-constexpr int NTHREADS = 10 * 32;
+constexpr int NTHREADS = 18 * 32;
 constexpr int ERR_TIMEOUT = 0x501;
 
 __device__ int g_err;                        // bounded waits record here (one word per device)
@@ -90,9 +90,10 @@ struct Lay {
   static constexpr int STAGE = 2 * QB + VB;                // Q, K, V
   static constexpr int S16 = 2 * STAGE;                    // the state's operand copy [DV][DK]
   static constexpr int PW = S16 + DV * DK * 2;             // lam^d, d = 0 .. 128
-  static constexpr int BAR = PW + (C + 4) * 4;
-  static constexpr int NBAR = 16;
-  static constexpr int USED = BAR + NBAR * 8 + 96;
+  static constexpr int RMAX = PW + (C + 4) * 4;            // |weights|, |decayed Q| of the row halves [2][C]
+  static constexpr int BAR = RMAX + 2 * C * 8;
+  static constexpr int NBAR = 18;
+  static constexpr int USED = BAR + NBAR * 8 + 16 + 128;
   static_assert(USED <= 227 * 1024, "shared memory of one CTA");
   // above half an SM: each CTA allocates all of TMEM, so two never share one
   static constexpr int BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
@@ -125,12 +126,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* ds_done = bars + 11;               // the state holds this chunk
   uint64_t* smax = bars + 12;                  // the state's maximum over the four warps is known
   uint64_t* mma_idle = bars + 13;
+  uint64_t* pair = bars + 14;                  // [4] the two warps of a quadrant have read their weights
   uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // V has held a non-finite element
   volatile int* s_exp = (volatile int*)(tmem_slot + 3);    // a of the chunk
-  volatile float* wmax = (volatile float*)(tmem_slot + 4); // [2][4] |S| per warp, by chunk parity
-  volatile int* vmax = (volatile int*)(tmem_slot + 12);    // [2][4] |V| as f16 bits, by stage
+  volatile float* wmax = (volatile float*)(tmem_slot + 4); // [2][8] |S| per warp, by chunk parity
+  volatile int* vmax = (volatile int*)(tmem_slot + 20);    // [2][8] |V| as f16 bits, by stage
   float* pw = reinterpret_cast<float*>(sm + L::PW);
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -159,17 +161,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], OUT ? 1 + 4 : 1);
-      mbar_init(&clean[i], 4);
+      mbar_init(&empty[i], OUT ? 1 + 8 : 1);
+      mbar_init(&clean[i], 8);
     }
     mbar_init(p_full, 1);
-    mbar_init(p_ready, 4);
-    mbar_init(s_ready, 4);
-    mbar_init(v_ready, 4);
+    mbar_init(p_ready, 8);
+    mbar_init(s_ready, 8);
+    mbar_init(v_ready, 8);
     mbar_init(o_full, 1);
     mbar_init(ds_done, 1);
-    mbar_init(smax, 4);
+    mbar_init(smax, 8);
     mbar_init(mma_idle, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&pair[i], 2);
     *abort_flag = 0;
     *v_flag = 0;
     mbar_init_fence();
@@ -266,33 +269,48 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       commit(mma_idle);
       mbar_drain(mma_idle, 0);                 // every MMA issued above has completed
     }
-  } else if (warp < 6) {
-    // ---- rows of the chunk: thread = row i
+  } else if (warp < 10) {
+    // ---- rows of the chunk: two threads per row i, each half of its weights, Q and outputs
     if constexpr (OUT) {
-      const int quad = warp & 3, i = quad * 32 + lane;
+      const int quad = warp & 3, half = (warp - 2) >> 2, i = quad * 32 + lane;
       const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
       const uint32_t tP = tmem + lane_off + T_P, tO = tmem + lane_off + T_O, tQ = tmem + lane_off + T_Q;
+      float2* rmax = reinterpret_cast<float2*>(sm + L::RMAX);
       for (int c = 0; c < nch; ++c) {
         const int st = c & 1, n = min(C, end - beg - c * C);
         const uint32_t ph = c & 1, sph = (c >> 1) & 1;
         const uint8_t* qrow = sm + st * L::STAGE + i * 128;
         if (!wwait(&full[st], sph) || !wwait(p_full, ph)) break;
         fence_after();
-        // weights of V: scale lam^(i-j) q_i.k_j, 0 for j > i
-        float p[C];
+        // weights of V: scale lam^(i-j) q_i.k_j, 0 for j > i; this thread's columns 32 half + 64 k
+        float p[64];
 #pragma unroll
-        for (int b = 0; b < C; b += 32) {
+        for (int k = 0; k < 2; ++k) {
+          const int b = 64 * k + 32 * half;
           uint32_t u[32];
-          tld32(tP + b, u);
-          ld_wait();
-          pin32(u);
-          const float* w = pw + i - b;         // lam^(i-j) at w[-(j - b)]; rows above the diagonal: unused
+          if (b <= quad * 32) {                // (uniform over the warp)
+            tld32(tP + b, u);
+            ld_wait();
+            pin32(u);
+          }
+          if (b < quad * 32) {                 // before every row: lam^(i-j) = lam^(i-(b+31)) lam^(b+31-j)
+            const float f = a.scale * pw[i - b - 31];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) p[b + e] = b + e <= i ? __uint_as_float(u[e]) * (a.scale * w[-e]) : 0.f;
+            for (int e = 0; e < 32; ++e) p[32 * k + e] = __uint_as_float(u[e]) * (f * pw[31 - e]);
+          } else if (b == quad * 32) {         // across the diagonal: rows above it are not used
+            const float* w = pw + lane;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) p[32 * k + e] = e <= lane ? __uint_as_float(u[e]) * (a.scale * w[-e]) : 0.f;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) p[32 * k + e] = 0.f;
+          }
         }
         const float qs = a.scale * pw[i + 1];
-        auto q8 = [&](int k, float* x) {       // 8 decayed elements of the Q row
-          const uint4 v = *reinterpret_cast<const uint4*>(qrow + (k >> 3) * (C * 128) + (((k & 7) ^ (i & 7)) << 4));
+        constexpr int QC = DK / 16;            // 16-byte chunks of this half of the Q row
+        auto q8 = [&](int k, float* x) {       // 8 decayed elements
+          const int q = half * QC + k;
+          const uint4 v = *reinterpret_cast<const uint4*>(qrow + (q >> 3) * (C * 128) + (((q & 7) ^ (i & 7)) << 4));
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -306,14 +324,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if constexpr (F16) {
           float mp = 0.f, mq = 0.f;
 #pragma unroll
-          for (int e = 0; e < C; ++e) mp = fmaxf(mp, fabsf(p[e]));
+          for (int e = 0; e < 64; ++e) mp = fmaxf(mp, fabsf(p[e]));
 #pragma unroll
-          for (int k = 0; k < DK / 8; ++k) {
+          for (int k = 0; k < QC; ++k) {
             float x[8];
             q8(k, x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) mq = fmaxf(mq, fabsf(x[e]));
           }
+          rmax[half * C + i] = make_float2(mp, mq);
+        }
+        // both warps of the quadrant have their weights in registers: the columns may be written
+        fence_before();
+        arrive(&pair[quad]);
+        if (!wwait(&pair[quad], ph)) break;
+        fence_after();
+        if constexpr (F16) {
+          const float2 m0 = rmax[i], m1 = rmax[C + i];
+          const float mp = fmaxf(m0.x, m1.x), mq = fmaxf(m0.y, m1.y);
           if (!wwait(s_ready, ph)) break;
           const int sa = *s_exp;
           cexp = 100;
@@ -325,14 +353,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           fq = qe < -126 ? 0.f : pow2f(min(qe, 126));
         }
 #pragma unroll
-        for (int b = 0; b < C; b += 32) {
+        for (int k = 0; k < 2; ++k) {
           uint32_t u[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) u[e] = pack(T(), p[b + 2 * e] * fp, p[b + 2 * e + 1] * fp);
-          tst16(tP + 64 + b / 2, u);
+          for (int e = 0; e < 16; ++e) u[e] = pack(T(), p[32 * k + 2 * e] * fp, p[32 * k + 2 * e + 1] * fp);
+          tst16(tP + 64 + 32 * k + 16 * half, u);
         }
 #pragma unroll
-        for (int k = 0; k < DK / 8; k += 4) {
+        for (int k = 0; k < QC; k += 4) {
           uint32_t u[16];
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4) {
@@ -341,7 +369,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) u[4 * k4 + e] = pack(T(), x[2 * e] * fq, x[2 * e + 1] * fq);
           }
-          tst16(tQ + k * 4, u);
+          tst16(tQ + half * (DK / 4) + k * 4, u);
         }
         st_wait();
         fence_before();
@@ -353,7 +381,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const bool fix = *v_flag && i < n;
         uint8_t* stage = sm + st * L::STAGE + 2 * L::QB;
 #pragma unroll
-        for (int b = 0; b < DV; b += 32) {
+        for (int b = half * (DV / 2); b < (half + 1) * (DV / 2); b += 32) {
           uint32_t u[32];
           __syncwarp();
           tld32(tO + b, u);
@@ -369,10 +397,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int j = 0; j <= i; ++j) {
               const T* v = (const T*)a.v + (r0 + j) * a.v_stride + h * DV + b;
               bool any = false;
+#pragma unroll 1
               for (int e = 0; e < 32; ++e) any |= !isfinite(ld_f(v + e));
               if (!any) continue;
               const T* k = (const T*)a.k + (r0 + j) * a.k_stride + h * DK;
               float z = 0.f;
+#pragma unroll 1
               for (int e = 0; e < DK; ++e) z += ld_f(q + e) * ld_f(k + e);
               z *= a.scale * pw[i - j];
 #pragma unroll
@@ -389,10 +419,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                            pack(T(), o[e + 6], o[e + 7]));
         }
         __syncwarp();
-        constexpr int CH = DV / 8;
+        constexpr int CH = DV / 16;            // chunks of this half of a row
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-          const int e = k * 32 + lane, r = quad * 32 + e / CH, q = e % CH;
+          const int e = k * 32 + lane, r = quad * 32 + e / CH, q = half * CH + e % CH;
           if (r < n)
             *reinterpret_cast<uint4*>((T*)a.out + ((row0 + c * C + r) * a.H + h) * DV + q * 8) =
                 *reinterpret_cast<const uint4*>(stage + r * (DV * 2) + ((q ^ (r & 7)) << 4));
@@ -403,13 +433,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     }
   } else {
-    // ---- value rows: thread = row dv of the state (64 value rows: twice over the 128 lanes)
-    const int quad = warp & 3, r = quad * 32 + lane, dv = r % DV;
+    // ---- value rows: two threads per row dv of the state (64 value rows: twice over the 128 lanes),
+    // each half of its columns, and half of the chunk's rows of the decayed values
+    const int wi = warp - 10, quad = warp & 3, half = wi >> 2, r = quad * 32 + lane, dv = r % DV;
+    constexpr int HK = DK / 2;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t tS = tmem + lane_off + T_S, tVH = tmem + lane_off + T_VH, tVL = tmem + lane_off + T_P;
+    const uint32_t tS = tmem + lane_off + T_S + half * HK;
+    const uint32_t tVH = tmem + lane_off + T_VH + half * 32, tVL = tmem + lane_off + T_P + half * 32;
     bool ok = true;
     int bexp = 0;                              // b: the state in TMEM is 2^b times the state (f16)
-    // adds chunk c's terms of non-finite V elements to this value row's state columns b .. b+31
+    // adds chunk c's terms of non-finite V elements to this thread's state columns b .. b+31
     auto fix_state = [&](int c, int b, float* x) {
       const int n = min(C, end - beg - c * C);
       const int64_t r0 = row0 + c * C;
@@ -417,7 +450,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int t = 0; t < n; ++t) {
         const float v = ld_f((const T*)a.v + (r0 + t) * a.v_stride + h * DV + dv);
         if (isfinite(v)) continue;
-        const T* k = (const T*)a.k + (r0 + t) * a.k_stride + h * DK + b;
+        const T* k = (const T*)a.k + (r0 + t) * a.k_stride + h * DK + half * HK + b;
 #pragma unroll
         for (int e = 0; e < 32; ++e) x[e] += pw[n - 1 - t] * v * ld_f(k + e);
       }
@@ -427,11 +460,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const float* src = tab.ws_seg[s] >= 0 ? ws_state
                                             : (a.S_in ? a.S_in + (int64_t)(tab.seq0 + s) * a.s_in_stride + head : nullptr);
 #pragma unroll
-      for (int b = 0; b < DK; b += 32) {
+      for (int b = 0; b < HK; b += 32) {
         uint32_t u[32];
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-          const float4 v = src ? *reinterpret_cast<const float4*>(src + (int64_t)dv * DK + b + e)
+          const float4 v = src ? *reinterpret_cast<const float4*>(src + (int64_t)dv * DK + half * HK + b + e)
                                : make_float4(0.f, 0.f, 0.f, 0.f);
           u[e] = __float_as_uint(v.x);
           u[e + 1] = __float_as_uint(v.y);
@@ -450,45 +483,45 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (!wwait(&full[st], sph)) { ok = false; break; }
       // rows past the end to zeros (K and V), non-finite V elements to zero
       {
-        constexpr int KC = DK / 8, VC = DV / 8;
-        const int tid = (warp - 6) * 32 + lane;
+        constexpr int KC = DK / 8, VC = DV / 8, PER = C * VC / 256;
+        const int tid = wi * 32 + lane;
         if (n < C) {
-          for (int e = tid; e < (C - n) * KC; e += 128) {
+          for (int e = tid; e < (C - n) * KC; e += 256) {
             const int t = n + e / KC, q = e % KC;
             *reinterpret_cast<uint4*>(kt + (q >> 3) * (C * 128) + t * 128 + ((q & 7) << 4)) = make_uint4(0, 0, 0, 0);
           }
-          for (int e = tid; e < (C - n) * VC; e += 128) {
-            const int t = n + e / VC, q = e % VC;
-            *reinterpret_cast<uint4*>(vt + (q >> 3) * (C * 128) + t * 128 + ((q & 7) << 4)) = make_uint4(0, 0, 0, 0);
-          }
         }
+        uint4 v[PER];
         bool bad = false;
         uint32_t vm = 0;
-#pragma unroll 4
-        for (int e = tid; e < n * VC; e += 128) {
-          uint4* at = reinterpret_cast<uint4*>(vt + (e % VC >> 3) * (C * 128) + (e / VC) * 128 + ((e % VC & 7) << 4));
-          uint4 v = *at;
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < PER; ++k) v[k] = *reinterpret_cast<const uint4*>(vt + (k * 256 + tid) * 16);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {        // 16-byte chunks in memory order: box, row, chunk
+          const int t = ((k * 256 + tid) >> 3) % C;
+          uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
           bool hit = false;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const bool b0 = nonfinite(T(), w[q] & 0xffffu), b1 = nonfinite(T(), w[q] >> 16);
+            hit |= b0 || b1;
             if (b0) w[q] &= 0xffff0000u;
             if (b1) w[q] &= 0xffffu;
-            hit |= b0 || b1;
-            if constexpr (F16) vm = max(vm, max(w[q] & 0x7fffu, (w[q] >> 16) & 0x7fffu));
+            if constexpr (F16)
+              if (t < n) vm = max(vm, max(w[q] & 0x7fffu, (w[q] >> 16) & 0x7fffu));
           }
-          if (hit) *at = make_uint4(w[0], w[1], w[2], w[3]);
-          bad |= hit;
+          if (t >= n) *reinterpret_cast<uint4*>(vt + (k * 256 + tid) * 16) = make_uint4(0, 0, 0, 0);
+          else if (hit) *reinterpret_cast<uint4*>(vt + (k * 256 + tid) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          bad |= hit && t < n;
         }
         if (bad) *v_flag = 1;
         if constexpr (F16) {
           vm = __reduce_max_sync(0xffffffffu, vm);
-          if (lane == 0) vmax[st * 4 + warp - 6] = (int)vm;
+          if (lane == 0) vmax[st * 8 + wi] = (int)vm;
         }
         fence_async_smem();
         arrive(&clean[st]);
-        // (this role's own reads of V below: all four warps have cleaned their share)
+        // (this role's own reads of V below: all its warps have cleaned their share)
         if (!wwait(&clean[st], sph)) { ok = false; break; }
       }
       if (c > 0 && !wwait(ds_done, (c - 1) & 1)) { ok = false; break; }
@@ -496,43 +529,52 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const float dec = pw[n];
       int bnew = 0;
       if constexpr (F16) {                     // decayed values below 2^14
-        const int vm = max(max(vmax[st * 4], vmax[st * 4 + 1]), max(vmax[st * 4 + 2], vmax[st * 4 + 3]));
+        int vm = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) vm = max(vm, vmax[st * 8 + k]);
         if (vm > 0) bnew = 14 - exp_above(__half2float(__ushort_as_half((unsigned short)vm)));
       }
       if (OUT || c > 0) {
         // state: operand copy (scaled for f16), then decayed in place
-        float x[DK];
+        float x[HK];
+        {
+          uint32_t u[HK];
 #pragma unroll
-        for (int b = 0; b < DK; b += 32) {
-          uint32_t u[32];
-          tld32(tS + b, u);
+          for (int b = 0; b < HK; b += 32) tld32(tS + b, u + b);
           ld_wait();
-          pin32(u);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[b + e] = F16 ? __uint_as_float(u[e]) * pow2f(-bexp) : __uint_as_float(u[e]);
-          if (c > 0 && *v_flag) fix_state(c - 1, b, x + b);
+          for (int b = 0; b < HK; b += 32) pin32(u + b);
+#pragma unroll
+          for (int e = 0; e < HK; ++e) x[e] = F16 ? __uint_as_float(u[e]) * pow2f(-bexp) : __uint_as_float(u[e]);
+        }
+        if (c > 0 && *v_flag) {
+#pragma unroll
+          for (int b = 0; b < HK; b += 32) fix_state(c - 1, b, x + b);
         }
         if constexpr (OUT) {
           float f = 1.f;
           if constexpr (F16) {
             float m = 0.f;
 #pragma unroll
-            for (int e = 0; e < DK; ++e) m = fmaxf(m, isfinite(x[e]) ? fabsf(x[e]) : 0.f);
+            for (int e = 0; e < HK; ++e) m = fmaxf(m, isfinite(x[e]) ? fabsf(x[e]) : 0.f);
             m = warp_max(m);
-            if (lane == 0) wmax[ph * 4 + warp - 6] = m;
+            if (lane == 0) wmax[ph * 8 + wi] = m;
             arrive(smax);
             if (!wwait(smax, ph)) { ok = false; break; }
-            m = fmaxf(fmaxf(wmax[ph * 4], wmax[ph * 4 + 1]), fmaxf(wmax[ph * 4 + 2], wmax[ph * 4 + 3]));
+            m = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m = fmaxf(m, wmax[ph * 8 + k]);
             const int sa = m > 0.f ? max(-100, min(100, 14 - exp_above(m))) : 100;
-            if (warp == 6 && lane == 0) *s_exp = sa;
+            if (wi == 0 && lane == 0) *s_exp = sa;
             f = pow2f(sa);
             if (m > 0.f) bnew = min(bnew, 120 - exp_above(m));   // (the scaled state stays finite)
           }
           if (r < DV) {
 #pragma unroll
-            for (int k = 0; k < DK / 8; ++k) {
+            for (int k = 0; k < HK / 8; ++k) {
               const float* y = x + 8 * k;
-              *reinterpret_cast<uint4*>(sm + L::S16 + (k >> 3) * (DV * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4)) =
+              const int q = half * (HK / 8) + k;
+              *reinterpret_cast<uint4*>(sm + L::S16 + (q >> 3) * (DV * 128) + r * 128 + (((q & 7) ^ (r & 7)) << 4)) =
                   make_uint4(pack(T(), y[0] * f, y[1] * f), pack(T(), y[2] * f, y[3] * f),
                              pack(T(), y[4] * f, y[5] * f), pack(T(), y[6] * f, y[7] * f));
             }
@@ -540,7 +582,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         const float ds = F16 ? dec * pow2f(bnew) : dec;
 #pragma unroll
-        for (int b = 0; b < DK; b += 32) {
+        for (int b = 0; b < HK; b += 32) {
           uint32_t u[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(x[b + e] * ds);
@@ -555,34 +597,30 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       bexp = bnew;
       const float sb = F16 ? pow2f(bnew) : 1.f;
-      // decayed values, split: high part (nearest), low part (what it leaves)
+      // decayed values of rows 64 half .. +63, split: high part (nearest), low part (what it leaves)
       {
-        const uint8_t* col = vt + (dv >> 6) * (C * 128) + (dv & 7) * 2;
+        const uint8_t* col = vt + (dv >> 6) * (C * 128) + (dv & 7) * 2 + half * (64 * 128);
         const int ch = (dv & 63) >> 3;
-        uint32_t hi[64], lo[64];
+        const int d0 = n - 1 - 64 * half;      // decay exponent of this half's first row
+        uint32_t hi[32], lo[32];
 #pragma unroll
-        for (int t = 0; t < C; t += 2) {
-          float y[2], yh[2];
+        for (int t = 0; t < 64; t += 2) {
+          float y[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const T v = *reinterpret_cast<const T*>(col + (t + e) * 128 + ((ch ^ ((t + e) & 7)) << 4));
-            const int d = n - 1 - (t + e);
-            y[e] = ld_f(&v) * (d >= 0 ? pw[d] * sb : 0.f);
+            y[e] = ld_f(&v) * (d0 - t - e >= 0 ? pw[d0 - t - e] * sb : 0.f);
           }
           hi[t / 2] = pack(T(), y[0], y[1]);
           const float2 f = unpack(T(), hi[t / 2]);
-          yh[0] = f.x;
-          yh[1] = f.y;
-          lo[t / 2] = pack(T(), y[0] - yh[0], y[1] - yh[1]);
+          lo[t / 2] = pack(T(), y[0] - f.x, y[1] - f.y);
         }
         tst32(tVH, hi);
-        tst32(tVH + 32, hi + 32);
         if constexpr (OUT) {                   // the low part's columns: the weights have left them
           if (!wwait(p_ready, ph)) { ok = false; break; }
           fence_after();
         }
         tst32(tVL, lo);
-        tst32(tVL + 32, lo + 32);
         st_wait();
         fence_before();
         arrive(v_ready);
@@ -594,7 +632,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     fence_after();
     if (ok && dst) {
 #pragma unroll
-      for (int b = 0; b < DK; b += 32) {
+      for (int b = 0; b < HK; b += 32) {
         uint32_t u[32];
         __syncwarp();
         tld32(tS + b, u);
@@ -607,7 +645,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (r < DV) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(dst + (int64_t)dv * DK + b + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            *reinterpret_cast<float4*>(dst + (int64_t)dv * DK + half * HK + b + e) =
+                make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         }
       }
     }
@@ -637,14 +676,21 @@ __global__ void __launch_bounds__(256)
     S = *reinterpret_cast<const float4*>(a.S_in + (int64_t)(tab.seq0 + s) * a.s_in_stride + 4 * i);
   const int n = tab.segcum[s + 1] - tab.segcum[s];
   float4* w = reinterpret_cast<float4*>(a.ws) + (int64_t)tab.ws_seg[s] * per4 + i;
-#pragma unroll 4
-  for (int k = 0; k + 1 < n; ++k) {
-    const float4 b = w[(int64_t)k * per4];
-    w[(int64_t)k * per4] = S;
-    S.x = f * S.x + b.x;
-    S.y = f * S.y + b.y;
-    S.z = f * S.z + b.z;
-    S.w = f * S.w + b.w;
+  constexpr int AHEAD = 8;                     // contributions loaded before they are joined
+  for (int k0 = 0; k0 + 1 < n; k0 += AHEAD) {
+    float4 b[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (k0 + k + 1 < n) b[k] = w[(int64_t)(k0 + k) * per4];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (k0 + k + 1 < n) {
+        w[(int64_t)(k0 + k) * per4] = S;
+        S.x = f * S.x + b[k].x;
+        S.y = f * S.y + b[k].y;
+        S.z = f * S.z + b[k].z;
+        S.w = f * S.w + b[k].w;
+      }
   }
   w[(int64_t)(n - 1) * per4] = S;
 }
