@@ -21,9 +21,12 @@
 // 2^a (a per chunk), row i's weights by 2^c_i, its decayed Q by 2^(c_i - a), the output row by 2^-c_i,
 // and the decayed values, with the state they are added to, by 2^b (b per chunk, so that the low
 // parts stay above f16's smallest number).
-// One CTA per SM, 18 warps: 0 TMA producer (two stages of Q, K, V), 1 MMA issue, 2-9 rows of the
-// chunk (TMEM lane = row, two threads a row: weights, decayed Q, outputs), 10-17 value rows (TMEM
-// lane = value row, two threads a row: the state's copy and decay, the split decayed values).
+// One CTA per SM, 19 warps: 0 TMA producer (two stages of Q, K, V); 1 and 18 MMA issue (1: Q K^T and
+// the outputs, 18: the state); 2-9 rows of the chunk (TMEM lane = row, two threads a row: weights,
+// decayed Q); 10-17 value rows (TMEM lane = value row, two threads a row: the split decayed values,
+// the state's copy and decay; then the outputs of the chunk before). Their passes are loops over 32
+// columns, not unrolled code: a chunk's worth of straight-line code per role does not stay in the
+// instruction cache, and took twice as long.
 // 0 x NaN: rows past the sequence are zeroed in shared memory; non-finite V elements are replaced
 // by 0 and their terms are added, in the plain order of the formula, to exactly the rows and state
 // rows that they belong to.
@@ -63,7 +66,7 @@ __device__ __forceinline__ float log2_decay(float log_decay) {
 __device__ __forceinline__ float decay(float log_decay) { return expf(fminf(log_decay, 0.f)); }
 
 constexpr int C = 128;                       // rows of a chunk
-constexpr int NTHREADS = 18 * 32;
+constexpr int NTHREADS = 19 * 32;
 constexpr int ERR_TIMEOUT = 0x501;
 
 __device__ int g_err;                        // bounded waits record here (one word per device)
@@ -79,20 +82,22 @@ struct Tab {
   int row0[MAX_SEQ], len[MAX_SEQ], ws_seg[MAX_SEQ];
 };
 
-// TMEM columns: weights of V (fp32, then 16-bit in the upper half; the lower half takes the low part
-// of the decayed values) | outputs | state | decayed Q | high part of the decayed values
+// TMEM columns: weights of V, per half of 64 columns: fp32, then 16-bit in its first 32 columns and
+// the half's decayed Q in its last 32 | outputs | state | low and high parts of the decayed values
 constexpr int TMEM_COLS = 512;
-constexpr int T_P = 0, T_O = 128, T_S = 256, T_Q = 384, T_VH = 448;
+constexpr int T_P = 0, T_O = 128, T_S = 256, T_VL = 384, T_VH = 448;
 
 template <int DK, int DV>
 struct Lay {
   static constexpr int QB = C * DK * 2, VB = C * DV * 2;   // bytes of a Q or K tile, of a V tile
   static constexpr int STAGE = 2 * QB + VB;                // Q, K, V
   static constexpr int S16 = 2 * STAGE;                    // the state's operand copy [DV][DK]
-  static constexpr int PW = S16 + DV * DK * 2;             // lam^d, d = 0 .. 128
-  static constexpr int RMAX = PW + (C + 4) * 4;            // |weights|, |decayed Q| of the row halves [2][C]
-  static constexpr int BAR = RMAX + 2 * C * 8;
-  static constexpr int NBAR = 18;
+  static constexpr int WV = S16 + DV * DK * 2 + 16;        // lam^(127-t), t = -1 .. 127; the same for the last
+                                                           // chunk's length, t = 0 .. 127
+  static constexpr int RMAX = WV + 2 * C * 4;              // f16: exponents of the row halves' maxima [2][C]
+  static constexpr int ROWS = RMAX + 2 * C * 4;            // f16: c_i, by chunk parity [2][C]
+  static constexpr int BAR = ROWS + 2 * C * 2;
+  static constexpr int NBAR = 20;
   static constexpr int USED = BAR + NBAR * 8 + 16 + 128;
   static_assert(USED <= 227 * 1024, "shared memory of one CTA");
   // above half an SM: each CTA allocates all of TMEM, so two never share one
@@ -120,20 +125,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* clean = bars + 4;                  // [2] its rows past the end and non-finite V are zeros
   uint64_t* p_full = bars + 6;                 // Q K^T is in TMEM
   uint64_t* p_ready = bars + 7;                // weights and decayed Q are in TMEM
-  uint64_t* s_ready = bars + 8;                // the state's copy is in shared memory, its decay applied
-  uint64_t* v_ready = bars + 9;                // the decayed values are in TMEM
+  uint64_t* s_ready = bars + 8;                // the state's copy is in shared memory, its decay applied,
+                                               // the decayed values are in TMEM
+  uint64_t* o_free = bars + 9;                 // the outputs have left TMEM
   uint64_t* o_full = bars + 10;                // outputs are in TMEM
   uint64_t* ds_done = bars + 11;               // the state holds this chunk
   uint64_t* smax = bars + 12;                  // the state's maximum over the four warps is known
-  uint64_t* mma_idle = bars + 13;
-  uint64_t* pair = bars + 14;                  // [4] the two warps of a quadrant have read their weights
+  uint64_t* mma_idle = bars + 13;              // [2]
+  uint64_t* pair = bars + 15;                  // [4] the two warps of a quadrant know their maxima (f16)
   uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // V has held a non-finite element
   volatile int* s_exp = (volatile int*)(tmem_slot + 3);    // a of the chunk
   volatile float* wmax = (volatile float*)(tmem_slot + 4); // [2][8] |S| per warp, by chunk parity
   volatile int* vmax = (volatile int*)(tmem_slot + 20);    // [2][8] |V| as f16 bits, by stage
-  float* pw = reinterpret_cast<float*>(sm + L::PW);
+  float* wv = reinterpret_cast<float*>(sm + L::WV);
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
   // this CTA's segment
@@ -161,17 +167,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], OUT ? 1 + 8 : 1);
+      mbar_init(&empty[i], OUT ? 1 + 8 : 1);     // the state's products, and the outputs' stores
+      mbar_init(&mma_idle[i], 1);
       mbar_init(&clean[i], 8);
     }
     mbar_init(p_full, 1);
     mbar_init(p_ready, 8);
     mbar_init(s_ready, 8);
-    mbar_init(v_ready, 8);
+    mbar_init(o_free, 8);
     mbar_init(o_full, 1);
     mbar_init(ds_done, 1);
     mbar_init(smax, 8);
-    mbar_init(mma_idle, 1);
     for (int i = 0; i < 4; ++i) mbar_init(&pair[i], 2);
     *abort_flag = 0;
     *v_flag = 0;
@@ -181,13 +187,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   allow_dependents();
   wait_prerequisites();
   const float l2 = log2_decay(a.log_decay[h]);
-  if (threadIdx.x <= C) pw[threadIdx.x] = exp2f(l2 * (float)threadIdx.x);
+  if (threadIdx.x <= C) {
+    const int d = threadIdx.x, tail = (end - beg) % C;
+    wv[C - 1 - d] = exp2f(l2 * (float)d);
+    if (d < C) wv[C + d] = d < tail ? exp2f(l2 * (float)(tail - 1 - d)) : 0.f;
+  }
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
   auto wwait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_err, ERR_TIMEOUT) ? 1 : 0) != 0;
   };
+  // f16: c_i of row i, by chunk parity
+  auto s_row = [&](int i, uint32_t parity) { return reinterpret_cast<int16_t*>(sm + L::ROWS) + parity * C + i; };
+  auto pw = [&](int d) { return wv[C - 1 - d]; };   // lam^d, d = 0 .. 128
   auto arrive = [&](uint64_t* bar) {           // once per warp, after what it wrote
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
@@ -212,20 +225,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int x = c > 2 ? c - 2 : 0; x < c; ++x) mbar_drain(&full[x & 1], (x >> 1) & 1);
     }
   } else if (warp == 1) {
-    // ---- MMA issue
-    const bool leader = elect_one();
-    constexpr uint32_t ID_P = idesc_f16(C, BF, 0, 0), ID_QS = idesc_f16(DV, BF, 0, 0), ID_PV = idesc_f16(DV, BF, 0, 1),
-                       ID_S = idesc_f16(DK, BF, 0, 1);
-    for (int c = 0; c < nch; ++c) {
-      const int st = c & 1;
-      const uint32_t ph = c & 1, sph = (c >> 1) & 1;
-      const uint32_t base = smem_u32(sm + st * L::STAGE);
-      const uint32_t ka = base + L::QB, va = base + 2 * L::QB;
-      if (!wwait(&full[st], sph)) break;
-      if constexpr (OUT) {
+    // ---- MMA issue: weights and outputs
+    if constexpr (OUT) {
+      const bool leader = elect_one();
+      constexpr uint32_t ID_P = idesc_f16(C, BF, 0, 0), ID_QS = idesc_f16(DV, BF, 0, 0),
+                         ID_PV = idesc_f16(DV, BF, 0, 1);
+      for (int c = 0; c < nch; ++c) {
+        const int st = c & 1;
+        const uint32_t ph = c & 1, sph = (c >> 1) & 1;
+        const uint32_t base = smem_u32(sm + st * L::STAGE);
+        if (!wwait(&full[st], sph)) break;
         fence_after();
-        if (leader) {                          // Q K^T
-          const uint64_t qd = desc_sw128(base, 16), kd = desc_sw128(ka, 16);
+        if (leader) {                          // Q K^T (in order behind the products that read these columns)
+          const uint64_t qd = desc_sw128(base, 16), kd = desc_sw128(base + L::QB, 16);
 #pragma unroll
           for (int kk = 0; kk < DK / 16; ++kk) {
             const uint64_t off = (uint64_t)(((kk >> 2) * (C * 128) + (kk & 3) * 32) >> 4);
@@ -234,212 +246,169 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           commit(p_full);
         }
         __syncwarp();
-        if (!wwait(s_ready, ph) || !wwait(p_ready, ph) || !wwait(&clean[st], sph)) break;
+        if (!wwait(&clean[st], sph) || !wwait(s_ready, ph) || !wwait(p_ready, ph)) break;
+        if (c > 0 && !wwait(o_free, (c - 1) & 1)) break;
         fence_after();
         if (leader) {                          // O = (decayed Q) S^T + weights V
-          const uint64_t sd = desc_sw128(smem_u32(sm + L::S16), 16), vd = desc_sw128(va, C * 128);
+          const uint64_t sd = desc_sw128(smem_u32(sm + L::S16), 16), vd = desc_sw128(base + 2 * L::QB, C * 128);
 #pragma unroll
-          for (int kk = 0; kk < DK / 16; ++kk)
-            mma_ts(tmem + T_O, tmem + T_Q + kk * 8, sd + (uint64_t)(((kk >> 2) * (DV * 128) + (kk & 3) * 32) >> 4),
-                   ID_QS, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < DK / 16; ++kk) {
+            const int q = kk < DK / 32 ? 32 + kk * 8 : 96 + (kk - DK / 32) * 8;
+            mma_ts(tmem + T_O, tmem + T_P + q, sd + (uint64_t)(((kk >> 2) * (DV * 128) + (kk & 3) * 32) >> 4), ID_QS,
+                   kk > 0 ? 1u : 0u);
+          }
 #pragma unroll
           for (int kk = 0; kk < C / 16; ++kk)
-            mma_ts(tmem + T_O, tmem + T_P + 64 + kk * 8, vd + (uint64_t)(kk * 16 * 128 >> 4), ID_PV, 1u);
+            mma_ts(tmem + T_O, tmem + T_P + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8),
+                   vd + (uint64_t)(kk * 16 * 128 >> 4), ID_PV, 1u);
           commit(o_full);
         }
         __syncwarp();
       }
-      if (!wwait(v_ready, ph)) break;
+      if (leader) {
+        commit(&mma_idle[0]);
+        mbar_drain(&mma_idle[0], 0);           // every MMA issued above has completed
+      }
+    }
+  } else if (warp == 18) {
+    // ---- MMA issue: S += (decayed V)^T K, high and low parts
+    const bool leader = elect_one();
+    constexpr uint32_t ID_S = idesc_f16(DK, BF, 0, 1);
+    for (int c = 0; c < nch; ++c) {
+      const int st = c & 1;
+      if (!wwait(&full[st], (c >> 1) & 1) || !wwait(s_ready, c & 1)) break;
       fence_after();
-      if (leader) {                            // S += (decayed V)^T K, high and low parts
-        const uint64_t kd = desc_sw128(ka, C * 128);
+      if (leader) {
+        const uint64_t kd = desc_sw128(smem_u32(sm + st * L::STAGE + L::QB), C * 128);
 #pragma unroll
         for (int kk = 0; kk < C / 16; ++kk)
           mma_ts(tmem + T_S, tmem + T_VH + kk * 8, kd + (uint64_t)(kk * 16 * 128 >> 4), ID_S,
                  OUT || c > 0 || kk > 0 ? 1u : 0u);
 #pragma unroll
         for (int kk = 0; kk < C / 16; ++kk)
-          mma_ts(tmem + T_S, tmem + T_P + kk * 8, kd + (uint64_t)(kk * 16 * 128 >> 4), ID_S, 1u);
+          mma_ts(tmem + T_S, tmem + T_VL + kk * 8, kd + (uint64_t)(kk * 16 * 128 >> 4), ID_S, 1u);
         commit(ds_done);
         commit(&empty[st]);
       }
       __syncwarp();
     }
     if (leader) {
-      commit(mma_idle);
-      mbar_drain(mma_idle, 0);                 // every MMA issued above has completed
+      commit(&mma_idle[1]);
+      mbar_drain(&mma_idle[1], 0);
     }
   } else if (warp < 10) {
-    // ---- rows of the chunk: two threads per row i, each half of its weights, Q and outputs
+    // ---- rows of the chunk: two threads per row i, each half of its weights (columns 64 half ..)
+    // and of its decayed Q
     if constexpr (OUT) {
       const int quad = warp & 3, half = (warp - 2) >> 2, i = quad * 32 + lane;
-      const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-      const uint32_t tP = tmem + lane_off + T_P, tO = tmem + lane_off + T_O, tQ = tmem + lane_off + T_Q;
-      float2* rmax = reinterpret_cast<float2*>(sm + L::RMAX);
+      const uint32_t tP = tmem + ((uint32_t)(quad * 32) << 16) + T_P + half * 64;
+      volatile int* rmax = reinterpret_cast<volatile int*>(sm + L::RMAX);
+      constexpr int HQ = DK / 2;               // this half's Q elements
+      const float qs = a.scale * pw(i + 1);
       for (int c = 0; c < nch; ++c) {
-        const int st = c & 1, n = min(C, end - beg - c * C);
+        const int st = c & 1;
         const uint32_t ph = c & 1, sph = (c >> 1) & 1;
         const uint8_t* qrow = sm + st * L::STAGE + i * 128;
         if (!wwait(&full[st], sph) || !wwait(p_full, ph)) break;
         fence_after();
-        // weights of V: scale lam^(i-j) q_i.k_j, 0 for j > i; this thread's columns 32 half + 64 k
-        float p[64];
+        // 32 weights of V: scale lam^(i-j) q_i.k_j, 0 for j > i (columns b .. b+31 of the chunk)
+        auto weights = [&](int k, float* p) {
+          const int b = 64 * half + 32 * k;
+          if (b > quad * 32) {                 // behind every row of this warp
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int b = 64 * k + 32 * half;
+            for (int e = 0; e < 32; ++e) p[e] = 0.f;
+            return;
+          }
           uint32_t u[32];
-          if (b <= quad * 32) {                // (uniform over the warp)
-            tld32(tP + b, u);
-            ld_wait();
-            pin32(u);
-          }
-          if (b < quad * 32) {                 // before every row: lam^(i-j) = lam^(i-(b+31)) lam^(b+31-j)
-            const float f = a.scale * pw[i - b - 31];
+          tld32(tP + 32 * k, u);
+          ld_wait();
+          pin32(u);
+          const float* w = wv + C - 1 - i + b; // lam^(i-b-e) at w[e] (past the diagonal: not used)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) p[32 * k + e] = __uint_as_float(u[e]) * (f * pw[31 - e]);
-          } else if (b == quad * 32) {         // across the diagonal: rows above it are not used
-            const float* w = pw + lane;
+          for (int e = 0; e < 32; ++e) p[e] = b + e <= i ? __uint_as_float(u[e]) * (a.scale * w[e]) : 0.f;
+        };
+        // 32 elements of the decayed Q row
+        auto decayed = [&](int k, float* x) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) p[32 * k + e] = e <= lane ? __uint_as_float(u[e]) * (a.scale * w[-e]) : 0.f;
-          } else {
+          for (int k4 = 0; k4 < 4; ++k4) {
+            const int q = half * (HQ / 8) + 4 * k + k4;
+            const uint4 v = *reinterpret_cast<const uint4*>(qrow + (q >> 3) * (C * 128) + (((q & 7) ^ (i & 7)) << 4));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int e = 0; e < 32; ++e) p[32 * k + e] = 0.f;
-          }
-        }
-        const float qs = a.scale * pw[i + 1];
-        constexpr int QC = DK / 16;            // 16-byte chunks of this half of the Q row
-        auto q8 = [&](int k, float* x) {       // 8 decayed elements
-          const int q = half * QC + k;
-          const uint4 v = *reinterpret_cast<const uint4*>(qrow + (q >> 3) * (C * 128) + (((q & 7) ^ (i & 7)) << 4));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack(T(), w[e]);
-            x[2 * e] = f.x * qs;
-            x[2 * e + 1] = f.y * qs;
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = unpack(T(), w[e]);
+              x[8 * k4 + 2 * e] = f.x * qs;
+              x[8 * k4 + 2 * e + 1] = f.y * qs;
+            }
           }
         };
-        int cexp = 0;                          // c_i
         float fp = 1.f, fq = 1.f;
-        if constexpr (F16) {
+        if constexpr (F16) {                   // c_i from the row's maxima and the state's scale
           float mp = 0.f, mq = 0.f;
+#pragma unroll 1
+          for (int k = 0; k < 2; ++k) {
+            float p[32];
+            weights(k, p);
 #pragma unroll
-          for (int e = 0; e < 64; ++e) mp = fmaxf(mp, fabsf(p[e]));
-#pragma unroll
-          for (int k = 0; k < QC; ++k) {
-            float x[8];
-            q8(k, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) mq = fmaxf(mq, fabsf(x[e]));
+            for (int e = 0; e < 32; ++e) mp = fmaxf(mp, fabsf(p[e]));
           }
-          rmax[half * C + i] = make_float2(mp, mq);
-        }
-        // both warps of the quadrant have their weights in registers: the columns may be written
-        fence_before();
-        arrive(&pair[quad]);
-        if (!wwait(&pair[quad], ph)) break;
-        fence_after();
-        if constexpr (F16) {
-          const float2 m0 = rmax[i], m1 = rmax[C + i];
-          const float mp = fmaxf(m0.x, m1.x), mq = fmaxf(m0.y, m1.y);
+#pragma unroll 1
+          for (int k = 0; k < HQ / 32; ++k) {
+            float x[32];
+            decayed(k, x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mq = fmaxf(mq, fabsf(x[e]));
+          }
+          // (exponents; -1000: all zero)
+          const int ep = mp > 0.f ? exp_above(mp) : -1000, eq = mq > 0.f ? exp_above(mq) : -1000;
+          rmax[half * C + i] = (ep << 16) | (eq & 0xffff);
+          arrive(&pair[quad]);
+          if (!wwait(&pair[quad], ph)) break;
+          const int m1 = rmax[(half ^ 1) * C + i];
+          const int mep = max(ep, m1 >> 16), meq = max(eq, (int)(int16_t)(m1 & 0xffff));
           if (!wwait(s_ready, ph)) break;
           const int sa = *s_exp;
-          cexp = 100;
-          if (mp > 0.f) cexp = min(cexp, 14 - exp_above(mp));
-          if (mq > 0.f && sa < 100) cexp = min(cexp, sa + 14 - exp_above(mq));
+          int cexp = 100;
+          if (mep > -1000) cexp = min(cexp, 14 - mep);
+          if (meq > -1000 && sa < 100) cexp = min(cexp, sa + 14 - meq);
           cexp = max(cexp, -100);
           fp = pow2f(cexp);
           const int qe = cexp - sa;            // (at most 14 - the exponent of mq, or the state is zero)
           fq = qe < -126 ? 0.f : pow2f(min(qe, 126));
+          if (half == 0) *s_row(i, ph) = (int16_t)cexp;
         }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {          // in place: behind the columns still to be read
+          float p[32];
+          weights(k, p);
           uint32_t u[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) u[e] = pack(T(), p[32 * k + 2 * e] * fp, p[32 * k + 2 * e + 1] * fp);
-          tst16(tP + 64 + 32 * k + 16 * half, u);
+          for (int e = 0; e < 16; ++e) u[e] = pack(T(), p[2 * e] * fp, p[2 * e + 1] * fp);
+          tst16(tP + 16 * k, u);
         }
-#pragma unroll
-        for (int k = 0; k < QC; k += 4) {
+#pragma unroll 1
+        for (int k = 0; k < HQ / 32; ++k) {
+          float x[32];
+          decayed(k, x);
           uint32_t u[16];
 #pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4) {
-            float x[8];
-            q8(k + k4, x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) u[4 * k4 + e] = pack(T(), x[2 * e] * fq, x[2 * e + 1] * fq);
-          }
-          tst16(tQ + half * (DK / 4) + k * 4, u);
+          for (int e = 0; e < 16; ++e) u[e] = pack(T(), x[2 * e] * fq, x[2 * e + 1] * fq);
+          tst16(tP + 32 + 16 * k, u);
         }
         st_wait();
         fence_before();
         arrive(p_ready);
-        // outputs; staged in the V tile once the decayed values have been taken from it
-        if (!wwait(o_full, ph) || !wwait(v_ready, ph)) break;
-        fence_after();
-        const float fo = F16 ? pow2f(-cexp) : 1.f;
-        const bool fix = *v_flag && i < n;
-        uint8_t* stage = sm + st * L::STAGE + 2 * L::QB;
-#pragma unroll
-        for (int b = half * (DV / 2); b < (half + 1) * (DV / 2); b += 32) {
-          uint32_t u[32];
-          __syncwarp();
-          tld32(tO + b, u);
-          ld_wait();
-          pin32(u);
-          float o[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]) * fo;
-          if (fix) {                           // terms of non-finite V elements
-            const int64_t r0 = row0 + c * C;
-            const T* q = (const T*)a.q + (r0 + i) * a.q_stride + h * DK;
-#pragma unroll 1
-            for (int j = 0; j <= i; ++j) {
-              const T* v = (const T*)a.v + (r0 + j) * a.v_stride + h * DV + b;
-              bool any = false;
-#pragma unroll 1
-              for (int e = 0; e < 32; ++e) any |= !isfinite(ld_f(v + e));
-              if (!any) continue;
-              const T* k = (const T*)a.k + (r0 + j) * a.k_stride + h * DK;
-              float z = 0.f;
-#pragma unroll 1
-              for (int e = 0; e < DK; ++e) z += ld_f(q + e) * ld_f(k + e);
-              z *= a.scale * pw[i - j];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float x = ld_f(v + e);
-                if (!isfinite(x)) o[e] += z * x;
-              }
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(stage + i * (DV * 2) + ((((b + e) / 8) ^ (i & 7)) << 4)) =
-                make_uint4(pack(T(), o[e], o[e + 1]), pack(T(), o[e + 2], o[e + 3]), pack(T(), o[e + 4], o[e + 5]),
-                           pack(T(), o[e + 6], o[e + 7]));
-        }
-        __syncwarp();
-        constexpr int CH = DV / 16;            // chunks of this half of a row
-#pragma unroll
-        for (int k = 0; k < CH; ++k) {
-          const int e = k * 32 + lane, r = quad * 32 + e / CH, q = half * CH + e % CH;
-          if (r < n)
-            *reinterpret_cast<uint4*>((T*)a.out + ((row0 + c * C + r) * a.H + h) * DV + q * 8) =
-                *reinterpret_cast<const uint4*>(stage + r * (DV * 2) + ((q ^ (r & 7)) << 4));
-        }
-        fence_async_smem();                    // the stage's next fill is a TMA write
-        fence_before();
-        arrive(&empty[st]);
       }
     }
   } else {
     // ---- value rows: two threads per row dv of the state (64 value rows: twice over the 128 lanes),
-    // each half of its columns, and half of the chunk's rows of the decayed values
+    // each half of its columns, and half of the chunk's rows of the decayed values; and the outputs,
+    // two threads per row of the chunk
     const int wi = warp - 10, quad = warp & 3, half = wi >> 2, r = quad * 32 + lane, dv = r % DV;
-    constexpr int HK = DK / 2;
+    constexpr int HK = DK / 2, HV = DV / 2;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t tS = tmem + lane_off + T_S + half * HK;
-    const uint32_t tVH = tmem + lane_off + T_VH + half * 32, tVL = tmem + lane_off + T_P + half * 32;
+    const uint32_t tS = tmem + lane_off + T_S + half * HK, tO = tmem + lane_off + T_O + half * HV;
+    const uint32_t tVH = tmem + lane_off + T_VH + half * 32, tVL = tmem + lane_off + T_VL + half * 32;
     bool ok = true;
     int bexp = 0;                              // b: the state in TMEM is 2^b times the state (f16)
     // adds chunk c's terms of non-finite V elements to this thread's state columns b .. b+31
@@ -452,14 +421,86 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (isfinite(v)) continue;
         const T* k = (const T*)a.k + (r0 + t) * a.k_stride + h * DK + half * HK + b;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] += pw[n - 1 - t] * v * ld_f(k + e);
+        for (int e = 0; e < 32; ++e) x[e] += pw(n - 1 - t) * v * ld_f(k + e);
       }
+    };
+    // 32 columns of this thread's state row (chunk c in it), unscaled
+    auto state32 = [&](int c, int b, float* x) {
+      uint32_t u[32];
+      __syncwarp();
+      tld32(tS + b, u);
+      ld_wait();
+      pin32(u);
+      const float f = F16 ? pow2f(-bexp) : 1.f;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[e] = F16 ? __uint_as_float(u[e]) * f : __uint_as_float(u[e]);
+      if (c >= 0 && *v_flag) fix_state(c, b, x);
+    };
+    // chunk c's outputs: rows scaled back, staged in its V tile (already taken), stored in whole lines
+    auto outputs = [&](int c) {
+      const int st = c & 1, n = min(C, end - beg - c * C);
+      if (!wwait(o_full, c & 1)) return false;
+      fence_after();
+      const float fo = F16 ? pow2f(-(int)*s_row(r, c & 1)) : 1.f;
+      const bool fix = *v_flag && r < n;
+      uint8_t* stage = sm + st * L::STAGE + 2 * L::QB;
+#pragma unroll 1
+      for (int b = 0; b < HV; b += 32) {
+        uint32_t u[32];
+        __syncwarp();
+        tld32(tO + b, u);
+        ld_wait();
+        pin32(u);
+        float o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]) * fo;
+        if (fix) {                             // terms of non-finite V elements
+          const int64_t r0 = row0 + c * C;
+          const T* q = (const T*)a.q + (r0 + r) * a.q_stride + h * DK;
+#pragma unroll 1
+          for (int j = 0; j <= r; ++j) {
+            const T* v = (const T*)a.v + (r0 + j) * a.v_stride + h * DV + half * HV + b;
+            bool any = false;
+#pragma unroll 1
+            for (int e = 0; e < 32; ++e) any |= !isfinite(ld_f(v + e));
+            if (!any) continue;
+            const T* k = (const T*)a.k + (r0 + j) * a.k_stride + h * DK;
+            float z = 0.f;
+#pragma unroll 1
+            for (int e = 0; e < DK; ++e) z += ld_f(q + e) * ld_f(k + e);
+            z *= a.scale * pw(r - j);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float x = ld_f(v + e);
+              if (!isfinite(x)) o[e] += z * x;
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+          *reinterpret_cast<uint4*>(stage + r * (DV * 2) + ((((half * HV + b + e) / 8) ^ (r & 7)) << 4)) =
+              make_uint4(pack(T(), o[e], o[e + 1]), pack(T(), o[e + 2], o[e + 3]), pack(T(), o[e + 4], o[e + 5]),
+                         pack(T(), o[e + 6], o[e + 7]));
+      }
+      fence_before();
+      arrive(o_free);                          // (also orders the stage's writes within the warp)
+      constexpr int CH = DV / 16;              // chunks of this half of a row
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int e = k * 32 + lane, rr = quad * 32 + e / CH, q = half * CH + e % CH;
+        if (rr < n)
+          *reinterpret_cast<uint4*>((T*)a.out + ((row0 + c * C + rr) * a.H + h) * DV + q * 8) =
+              *reinterpret_cast<const uint4*>(stage + rr * (DV * 2) + ((q ^ (rr & 7)) << 4));
+      }
+      fence_async_smem();                      // the stage's next fill is a TMA write
+      arrive(&empty[st]);
+      return true;
     };
     if constexpr (OUT) {
       // the start state into TMEM
       const float* src = tab.ws_seg[s] >= 0 ? ws_state
                                             : (a.S_in ? a.S_in + (int64_t)(tab.seq0 + s) * a.s_in_stride + head : nullptr);
-#pragma unroll
+#pragma unroll 1
       for (int b = 0; b < HK; b += 32) {
         uint32_t u[32];
 #pragma unroll
@@ -491,28 +532,39 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             *reinterpret_cast<uint4*>(kt + (q >> 3) * (C * 128) + t * 128 + ((q & 7) << 4)) = make_uint4(0, 0, 0, 0);
           }
         }
-        uint4 v[PER];
         bool bad = false;
         uint32_t vm = 0;
+#pragma unroll 1
+        for (int k0 = 0; k0 < PER; k0 += 4) {
+          uint4 v[4];
 #pragma unroll
-        for (int k = 0; k < PER; ++k) v[k] = *reinterpret_cast<const uint4*>(vt + (k * 256 + tid) * 16);
+          for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(vt + ((k0 + k) * 256 + tid) * 16);
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {        // 16-byte chunks in memory order: box, row, chunk
-          const int t = ((k * 256 + tid) >> 3) % C;
-          uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-          bool hit = false;
+          for (int k = 0; k < 4; ++k) {        // 16-byte chunks in memory order: box, row, chunk
+            uint8_t* at = vt + ((k0 + k) * 256 + tid) * 16;
+            const int t = (((k0 + k) * 256 + tid) >> 3) % C;
+            uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            bool hit = false;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const bool b0 = nonfinite(T(), w[q] & 0xffffu), b1 = nonfinite(T(), w[q] >> 16);
-            hit |= b0 || b1;
-            if (b0) w[q] &= 0xffff0000u;
-            if (b1) w[q] &= 0xffffu;
-            if constexpr (F16)
-              if (t < n) vm = max(vm, max(w[q] & 0x7fffu, (w[q] >> 16) & 0x7fffu));
+            for (int q = 0; q < 4; ++q) hit |= nonfinite(T(), w[q] & 0xffffu) || nonfinite(T(), w[q] >> 16);
+            if (t >= n) {
+              *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            if (hit) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (nonfinite(T(), w[q] & 0xffffu)) w[q] &= 0xffff0000u;
+                if (nonfinite(T(), w[q] >> 16)) w[q] &= 0xffffu;
+              }
+              *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+              bad = true;
+            }
+            if constexpr (F16) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) vm = max(vm, max(w[q] & 0x7fffu, (w[q] >> 16) & 0x7fffu));
+            }
           }
-          if (t >= n) *reinterpret_cast<uint4*>(vt + (k * 256 + tid) * 16) = make_uint4(0, 0, 0, 0);
-          else if (hit) *reinterpret_cast<uint4*>(vt + (k * 256 + tid) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-          bad |= hit && t < n;
         }
         if (bad) *v_flag = 1;
         if constexpr (F16) {
@@ -524,9 +576,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // (this role's own reads of V below: all its warps have cleaned their share)
         if (!wwait(&clean[st], sph)) { ok = false; break; }
       }
-      if (c > 0 && !wwait(ds_done, (c - 1) & 1)) { ok = false; break; }
-      fence_after();
-      const float dec = pw[n];
       int bnew = 0;
       if constexpr (F16) {                     // decayed values below 2^14
         int vm = 0;
@@ -534,114 +583,103 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int k = 0; k < 8; ++k) vm = max(vm, vmax[st * 8 + k]);
         if (vm > 0) bnew = 14 - exp_above(__half2float(__ushort_as_half((unsigned short)vm)));
       }
+      if (c > 0 && !wwait(ds_done, (c - 1) & 1)) { ok = false; break; }
+      if (OUT && c > 0 && !wwait(o_full, (c - 1) & 1)) { ok = false; break; }   // (its state copy has been read)
+      fence_after();
+      // state: operand copy (scaled for f16), then decayed in place
       if (OUT || c > 0) {
-        // state: operand copy (scaled for f16), then decayed in place
-        float x[HK];
-        {
-          uint32_t u[HK];
+        float f = 1.f;
+        if constexpr (OUT && F16) {
+          float m = 0.f;
+#pragma unroll 1
+          for (int b = 0; b < HK; b += 32) {
+            float x[32];
+            state32(c - 1, b, x);
 #pragma unroll
-          for (int b = 0; b < HK; b += 32) tld32(tS + b, u + b);
-          ld_wait();
-#pragma unroll
-          for (int b = 0; b < HK; b += 32) pin32(u + b);
-#pragma unroll
-          for (int e = 0; e < HK; ++e) x[e] = F16 ? __uint_as_float(u[e]) * pow2f(-bexp) : __uint_as_float(u[e]);
-        }
-        if (c > 0 && *v_flag) {
-#pragma unroll
-          for (int b = 0; b < HK; b += 32) fix_state(c - 1, b, x + b);
-        }
-        if constexpr (OUT) {
-          float f = 1.f;
-          if constexpr (F16) {
-            float m = 0.f;
-#pragma unroll
-            for (int e = 0; e < HK; ++e) m = fmaxf(m, isfinite(x[e]) ? fabsf(x[e]) : 0.f);
-            m = warp_max(m);
-            if (lane == 0) wmax[ph * 8 + wi] = m;
-            arrive(smax);
-            if (!wwait(smax, ph)) { ok = false; break; }
-            m = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) m = fmaxf(m, wmax[ph * 8 + k]);
-            const int sa = m > 0.f ? max(-100, min(100, 14 - exp_above(m))) : 100;
-            if (wi == 0 && lane == 0) *s_exp = sa;
-            f = pow2f(sa);
-            if (m > 0.f) bnew = min(bnew, 120 - exp_above(m));   // (the scaled state stays finite)
+            for (int e = 0; e < 32; ++e) m = fmaxf(m, isfinite(x[e]) ? fabsf(x[e]) : 0.f);
           }
-          if (r < DV) {
+          m = warp_max(m);
+          if (lane == 0) wmax[ph * 8 + wi] = m;
+          arrive(smax);
+          if (!wwait(smax, ph)) { ok = false; break; }
+          m = 0.f;
 #pragma unroll
-            for (int k = 0; k < HK / 8; ++k) {
+          for (int k = 0; k < 8; ++k) m = fmaxf(m, wmax[ph * 8 + k]);
+          const int sa = m > 0.f ? max(-100, min(100, 14 - exp_above(m))) : 100;
+          if (wi == 0 && lane == 0) *s_exp = sa;
+          f = pow2f(sa);
+          if (m > 0.f) bnew = min(bnew, 120 - exp_above(m));   // (the scaled state stays finite)
+        }
+        const float ds = F16 ? pw(n) * pow2f(bnew) : pw(n);
+#pragma unroll 1
+        for (int b = 0; b < HK; b += 32) {
+          float x[32];
+          state32(c - 1, b, x);
+          if (OUT && r < DV) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
               const float* y = x + 8 * k;
-              const int q = half * (HK / 8) + k;
+              const int q = (half * HK + b) / 8 + k;
               *reinterpret_cast<uint4*>(sm + L::S16 + (q >> 3) * (DV * 128) + r * 128 + (((q & 7) ^ (r & 7)) << 4)) =
                   make_uint4(pack(T(), y[0] * f, y[1] * f), pack(T(), y[2] * f, y[3] * f),
                              pack(T(), y[4] * f, y[5] * f), pack(T(), y[6] * f, y[7] * f));
             }
           }
-        }
-        const float ds = F16 ? dec * pow2f(bnew) : dec;
-#pragma unroll
-        for (int b = 0; b < HK; b += 32) {
           uint32_t u[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(x[b + e] * ds);
+          for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(x[e] * ds);
+          __syncwarp();
           tst32(tS + b, u);
-        }
-        st_wait();
-        if constexpr (OUT) {
-          fence_async_smem();
-          fence_before();
-          arrive(s_ready);
         }
       }
       bexp = bnew;
-      const float sb = F16 ? pow2f(bnew) : 1.f;
       // decayed values of rows 64 half .. +63, split: high part (nearest), low part (what it leaves)
       {
+        const float sb = F16 ? pow2f(bnew) : 1.f;
         const uint8_t* col = vt + (dv >> 6) * (C * 128) + (dv & 7) * 2 + half * (64 * 128);
         const int ch = (dv & 63) >> 3;
-        const int d0 = n - 1 - 64 * half;      // decay exponent of this half's first row
-        uint32_t hi[32], lo[32];
+        const float* w = wv + (n == C ? 0 : C) + half * 64;
+#pragma unroll 1
+        for (int t0 = 0; t0 < 64; t0 += 32) {
+          uint32_t hi[16], lo[16];
 #pragma unroll
-        for (int t = 0; t < 64; t += 2) {
-          float y[2];
+          for (int t = 0; t < 32; t += 4) {
+            const float4 w4 = *reinterpret_cast<const float4*>(w + t0 + t);
+            const float ww[4] = {w4.x, w4.y, w4.z, w4.w};
+            float y[4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const T v = *reinterpret_cast<const T*>(col + (t + e) * 128 + ((ch ^ ((t + e) & 7)) << 4));
-            y[e] = ld_f(&v) * (d0 - t - e >= 0 ? pw[d0 - t - e] * sb : 0.f);
+            for (int e = 0; e < 4; ++e) {
+              const T v = *reinterpret_cast<const T*>(col + (t0 + t + e) * 128 + ((ch ^ ((t + e) & 7)) << 4));
+              y[e] = ld_f(&v) * (F16 ? ww[e] * sb : ww[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const uint32_t hp = pack(T(), y[e], y[e + 1]);
+              const float2 f = unpack(T(), hp);
+              hi[(t + e) / 2] = hp;
+              lo[(t + e) / 2] = pack(T(), y[e] - f.x, y[e + 1] - f.y);
+            }
           }
-          hi[t / 2] = pack(T(), y[0], y[1]);
-          const float2 f = unpack(T(), hi[t / 2]);
-          lo[t / 2] = pack(T(), y[0] - f.x, y[1] - f.y);
+          tst16(tVH + t0 / 2, hi);
+          tst16(tVL + t0 / 2, lo);
         }
-        tst32(tVH, hi);
-        if constexpr (OUT) {                   // the low part's columns: the weights have left them
-          if (!wwait(p_ready, ph)) { ok = false; break; }
-          fence_after();
-        }
-        tst32(tVL, lo);
-        st_wait();
-        fence_before();
-        arrive(v_ready);
       }
+      st_wait();
+      fence_async_smem();
+      fence_before();
+      arrive(s_ready);
+      if (OUT && c > 0 && !outputs(c - 1)) { ok = false; break; }
     }
+    if (OUT && ok && nch > 0) ok = outputs(nch - 1);
     // ---- the state after the segment
     float* dst = OUT ? (last && a.S_out ? a.S_out + (int64_t)(tab.seq0 + s) * per + head : nullptr) : ws_state;
     if (ok && nch > 0) ok = wwait(ds_done, (nch - 1) & 1);
     fence_after();
     if (ok && dst) {
-#pragma unroll
+#pragma unroll 1
       for (int b = 0; b < HK; b += 32) {
-        uint32_t u[32];
-        __syncwarp();
-        tld32(tS + b, u);
-        ld_wait();
-        pin32(u);
         float x[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = F16 ? __uint_as_float(u[e]) * pow2f(-bexp) : __uint_as_float(u[e]);
-        if (nch > 0 && *v_flag) fix_state(nch - 1, b, x);
+        state32(nch - 1, b, x);
         if (r < DV) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
