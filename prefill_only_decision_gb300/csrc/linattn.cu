@@ -18,7 +18,7 @@
 // split into two such numbers (hi + lo), because the state is kept and returned in fp32: one
 // rounding of 2^-9 (bf16) would show in it. f16 rows: weights, decayed Q and the state's copy are
 // scaled by powers of two so that they use f16's range whatever the magnitudes: the state's copy by
-// 2^a (a per chunk), row i's weights by 2^c_i, its decayed Q by 2^(c_i - a), the output row by 2^-c_i,
+// 2^a (a per chunk, from a running bound lam^n bound + n max|v| max|k| on the state), row i's weights by 2^c_i, its decayed Q by 2^(c_i - a), the output row by 2^-c_i,
 // and the decayed values, with the state they are added to, by 2^b (b per chunk, so that the low
 // parts stay above f16's smallest number).
 // One CTA per SM, 19 warps: 0 TMA producer (two stages of Q, K, V); 1 and 18 MMA issue (1: Q K^T and
@@ -97,8 +97,8 @@ struct Lay {
   static constexpr int RMAX = WV + 2 * C * 4;              // f16: exponents of the row halves' maxima [2][C]
   static constexpr int ROWS = RMAX + 2 * C * 4;            // f16: c_i, by chunk parity [2][C]
   static constexpr int BAR = ROWS + 2 * C * 2;
-  static constexpr int NBAR = 20;
-  static constexpr int USED = BAR + NBAR * 8 + 16 + 128;
+  static constexpr int NBAR = 28;
+  static constexpr int USED = BAR + NBAR * 8 + 24 * 4;
   static_assert(USED <= 227 * 1024, "shared memory of one CTA");
   // above half an SM: each CTA allocates all of TMEM, so two never share one
   static constexpr int BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
@@ -120,25 +120,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   constexpr uint32_t BF = F16 ? 0 : 1;
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* bars = (uint64_t*)(sm + L::BAR);
-  uint64_t* full = bars;                       // [2] the stage's tiles have landed
-  uint64_t* empty = bars + 2;                  // [2] the stage may be filled again
-  uint64_t* clean = bars + 4;                  // [2] its rows past the end and non-finite V are zeros
-  uint64_t* p_full = bars + 6;                 // Q K^T is in TMEM
-  uint64_t* p_ready = bars + 7;                // weights and decayed Q are in TMEM
-  uint64_t* s_ready = bars + 8;                // the state's copy is in shared memory, its decay applied,
+  uint64_t* full = bars;                       // [3 of Q, K, V][2 stages] the tile has landed
+  uint64_t* empty = bars + 6;                  // [3][2] its slot may be filled again
+  uint64_t* clean = bars + 12;                 // [2] K and V: rows past the end and non-finite V are zeros
+  uint64_t* p_full = bars + 14;                // Q K^T is in TMEM
+  uint64_t* p_ready = bars + 15;               // weights and decayed Q are in TMEM
+  uint64_t* s_ready = bars + 16;               // the state's copy is in shared memory, its decay applied,
                                                // the decayed values are in TMEM
-  uint64_t* o_free = bars + 9;                 // the outputs have left TMEM
-  uint64_t* o_full = bars + 10;                // outputs are in TMEM
-  uint64_t* ds_done = bars + 11;               // the state holds this chunk
-  uint64_t* smax = bars + 12;                  // the state's maximum over the four warps is known
-  uint64_t* mma_idle = bars + 13;              // [2]
-  uint64_t* pair = bars + 15;                  // [4] the two warps of a quadrant know their maxima (f16)
+  uint64_t* o_free = bars + 17;                // the outputs have left TMEM
+  uint64_t* o_full = bars + 18;                // outputs are in TMEM
+  uint64_t* ds_done = bars + 19;               // the state holds this chunk
+  uint64_t* smax = bars + 20;                  // the start state's maximum over the warps is known (f16)
+  uint64_t* mma_idle = bars + 21;              // [2]
+  uint64_t* pair = bars + 23;                  // [4] the two warps of a quadrant know their maxima (f16)
   uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // V has held a non-finite element
-  volatile int* s_exp = (volatile int*)(tmem_slot + 3);    // a of the chunk
-  volatile float* wmax = (volatile float*)(tmem_slot + 4); // [2][8] |S| per warp, by chunk parity
-  volatile int* vmax = (volatile int*)(tmem_slot + 20);    // [2][8] |V| as f16 bits, by stage
+  volatile int* s_exp = (volatile int*)(tmem_slot + 3);    // [2] a, by chunk parity
+  volatile int* tmax = (volatile int*)(tmem_slot + 5);     // [2 stages][8 warps]: max |V| and |K| as f16 bits
+  volatile float* wmax = (volatile float*)(tmax + 8);      // [8] max |start state| per warp, before the chunks
   float* wv = reinterpret_cast<float*>(sm + L::WV);
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -165,11 +165,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   float* ws_state = (float*)a.ws + (tab.ws_seg[s] < 0 ? 0 : tab.ws_seg[s] + k_seg) * per + head;
 
   if (threadIdx.x == 0) {
+    for (int i = 0; i < 6; ++i) mbar_init(&full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], OUT ? 1 + 8 : 1);     // the state's products, and the outputs' stores
-      mbar_init(&mma_idle[i], 1);
+      mbar_init(&empty[i], 8);                 // Q: the row warps have read it (behind its products)
+      mbar_init(&empty[2 + i], OUT ? 2 : 1);   // K: the products of the weights, and of the state
+      mbar_init(&empty[4 + i], 1);             // V: the products of the outputs (!OUT: of the state)
       mbar_init(&clean[i], 8);
+      mbar_init(&mma_idle[i], 1);
     }
     mbar_init(p_full, 1);
     mbar_init(p_ready, 8);
@@ -209,20 +211,26 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (warp == 0) {
     // ---- TMA producer
     if (lane == 0) {
-      int c = 0;
-      for (; c < nch; ++c) {
+      uint32_t fills = 0;                      // per slot: begun (bit i), parity of the last fill (bit 8 + i)
+      bool ok = true;
+      for (int c = 0; c < nch && ok; ++c) {
         const int st = c & 1, r = (int)(row0 + c * C);
-        if (!mbar_wait(&empty[st], ((c >> 1) & 1) ^ 1, abort_flag, &g_err, ERR_TIMEOUT)) break;
         uint8_t* base = sm + st * L::STAGE;
-        mbar_expect_tx(&full[st], (OUT ? L::QB : 0) + L::QB + L::VB);
-        for (int b = 0; b < DK / 64; ++b) {
-          if (OUT) tma3(base + b * C * 128, &mapQ, &full[st], 64 * b, h, r);
-          tma3(base + L::QB + b * C * 128, &mapK, &full[st], 64 * b, h, r);
-        }
-        for (int b = 0; b < DV / 64; ++b) tma3(base + 2 * L::QB + b * C * 128, &mapV, &full[st], 64 * b, h, r);
+        auto load = [&](int which, const CUtensorMap* map, uint8_t* dst, int boxes, int bytes) {
+          const int slot = 2 * which + st;
+          ok = ok && mbar_wait(&empty[slot], ((c >> 1) & 1) ^ 1, abort_flag, &g_err, ERR_TIMEOUT);
+          if (!ok) return;
+          mbar_expect_tx(&full[slot], bytes);
+          for (int b = 0; b < boxes; ++b) tma3(dst + b * C * 128, map, &full[slot], 64 * b, h, r);
+          fills = (fills & ~(1u << (8 + slot))) | 1u << slot | (uint32_t)((c >> 1) & 1) << (8 + slot);
+        };
+        if (OUT) load(0, &mapQ, base, DK / 64, L::QB);
+        load(1, &mapK, base + L::QB, DK / 64, L::QB);
+        load(2, &mapV, base + 2 * L::QB, DV / 64, L::VB);
       }
       if (*abort_flag)                         // copies in flight land before the CTA leaves
-        for (int x = c > 2 ? c - 2 : 0; x < c; ++x) mbar_drain(&full[x & 1], (x >> 1) & 1);
+        for (int i = 0; i < 6; ++i)
+          if ((fills >> i) & 1) mbar_drain(&full[i], (fills >> (8 + i)) & 1);
     }
   } else if (warp == 1) {
     // ---- MMA issue: weights and outputs
@@ -234,7 +242,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int st = c & 1;
         const uint32_t ph = c & 1, sph = (c >> 1) & 1;
         const uint32_t base = smem_u32(sm + st * L::STAGE);
-        if (!wwait(&full[st], sph)) break;
+        if (!wwait(&full[st], sph) || !wwait(&full[2 + st], sph)) break;
         fence_after();
         if (leader) {                          // Q K^T (in order behind the products that read these columns)
           const uint64_t qd = desc_sw128(base, 16), kd = desc_sw128(base + L::QB, 16);
@@ -244,6 +252,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mma_ss(tmem + T_P, qd + off, kd + off, ID_P, kk > 0 ? 1u : 0u);
           }
           commit(p_full);
+          commit(&empty[2 + st]);
         }
         __syncwarp();
         if (!wwait(&clean[st], sph) || !wwait(s_ready, ph) || !wwait(p_ready, ph)) break;
@@ -262,6 +271,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mma_ts(tmem + T_O, tmem + T_P + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8),
                    vd + (uint64_t)(kk * 16 * 128 >> 4), ID_PV, 1u);
           commit(o_full);
+          commit(&empty[4 + st]);
         }
         __syncwarp();
       }
@@ -276,7 +286,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     constexpr uint32_t ID_S = idesc_f16(DK, BF, 0, 1);
     for (int c = 0; c < nch; ++c) {
       const int st = c & 1;
-      if (!wwait(&full[st], (c >> 1) & 1) || !wwait(s_ready, c & 1)) break;
+      if (!wwait(&full[2 + st], (c >> 1) & 1) || !wwait(s_ready, c & 1)) break;
       fence_after();
       if (leader) {
         const uint64_t kd = desc_sw128(smem_u32(sm + st * L::STAGE + L::QB), C * 128);
@@ -288,7 +298,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int kk = 0; kk < C / 16; ++kk)
           mma_ts(tmem + T_S, tmem + T_VL + kk * 8, kd + (uint64_t)(kk * 16 * 128 >> 4), ID_S, 1u);
         commit(ds_done);
-        commit(&empty[st]);
+        commit(&empty[2 + st]);
+        if (!OUT) commit(&empty[4 + st]);
       }
       __syncwarp();
     }
@@ -366,8 +377,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (!wwait(&pair[quad], ph)) break;
           const int m1 = rmax[(half ^ 1) * C + i];
           const int mep = max(ep, m1 >> 16), meq = max(eq, (int)(int16_t)(m1 & 0xffff));
-          if (!wwait(s_ready, ph)) break;
-          const int sa = *s_exp;
+          if (!wwait(&clean[st], sph)) break;
+          const int sa = s_exp[ph];
           int cexp = 100;
           if (mep > -1000) cexp = min(cexp, 14 - mep);
           if (meq > -1000 && sa < 100) cexp = min(cexp, sa + 14 - meq);
@@ -398,6 +409,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         st_wait();
         fence_before();
         arrive(p_ready);
+        if (lane == 0) mbar_arrive(&empty[st]);
       }
     }
   } else {
@@ -436,14 +448,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int e = 0; e < 32; ++e) x[e] = F16 ? __uint_as_float(u[e]) * f : __uint_as_float(u[e]);
       if (c >= 0 && *v_flag) fix_state(c, b, x);
     };
-    // chunk c's outputs: rows scaled back, staged in its V tile (already taken), stored in whole lines
+    // chunk c's outputs, rows scaled back
     auto outputs = [&](int c) {
-      const int st = c & 1, n = min(C, end - beg - c * C);
+      const int n = min(C, end - beg - c * C);
       if (!wwait(o_full, c & 1)) return false;
       fence_after();
       const float fo = F16 ? pow2f(-(int)*s_row(r, c & 1)) : 1.f;
       const bool fix = *v_flag && r < n;
-      uint8_t* stage = sm + st * L::STAGE + 2 * L::QB;
+      T* out = (T*)a.out + ((row0 + c * C + r) * a.H + h) * DV + half * HV;
 #pragma unroll 1
       for (int b = 0; b < HV; b += 32) {
         uint32_t u[32];
@@ -476,26 +488,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
           }
         }
+        if (r < n)
 #pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          *reinterpret_cast<uint4*>(stage + r * (DV * 2) + ((((half * HV + b + e) / 8) ^ (r & 7)) << 4)) =
-              make_uint4(pack(T(), o[e], o[e + 1]), pack(T(), o[e + 2], o[e + 3]), pack(T(), o[e + 4], o[e + 5]),
-                         pack(T(), o[e + 6], o[e + 7]));
+          for (int e = 0; e < 32; e += 8)      // (whole sectors: 64 bytes of the row)
+            *reinterpret_cast<uint4*>(out + b + e) = make_uint4(pack(T(), o[e], o[e + 1]), pack(T(), o[e + 2], o[e + 3]),
+                                                                pack(T(), o[e + 4], o[e + 5]), pack(T(), o[e + 6], o[e + 7]));
       }
       fence_before();
-      arrive(o_free);                          // (also orders the stage's writes within the warp)
-      constexpr int CH = DV / 16;              // chunks of this half of a row
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        const int e = k * 32 + lane, rr = quad * 32 + e / CH, q = half * CH + e % CH;
-        if (rr < n)
-          *reinterpret_cast<uint4*>((T*)a.out + ((row0 + c * C + rr) * a.H + h) * DV + q * 8) =
-              *reinterpret_cast<const uint4*>(stage + rr * (DV * 2) + ((q ^ (rr & 7)) << 4));
-      }
-      fence_async_smem();                      // the stage's next fill is a TMA write
-      arrive(&empty[st]);
+      arrive(o_free);
       return true;
     };
+    float bound = 0.f;                         // at least every finite |state element| (f16)
     if constexpr (OUT) {
       // the start state into TMEM
       const float* src = tab.ws_seg[s] >= 0 ? ws_state
@@ -512,104 +515,122 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           u[e + 2] = __float_as_uint(v.z);
           u[e + 3] = __float_as_uint(v.w);
         }
+        if constexpr (F16) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float x = fabsf(__uint_as_float(u[e]));
+            if (x < INFINITY) bound = fmaxf(bound, x);
+          }
+        }
         tst32(tS + b, u);
       }
       st_wait();
+      if constexpr (F16) {
+        bound = warp_max(bound);
+        if (lane == 0) wmax[wi] = bound;
+        arrive(smax);
+        ok = wwait(smax, 0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) bound = fmaxf(bound, wmax[k]);
+      }
     }
-    for (int c = 0; c < nch; ++c) {
+    // rows past the end to zeros (K and V), non-finite V elements to zero; f16: the tiles' maxima, and a
+    auto cleaning = [&](int c) {
       const int st = c & 1, n = min(C, end - beg - c * C);
-      const uint32_t ph = c & 1, sph = (c >> 1) & 1;
+      const uint32_t sph = (c >> 1) & 1;
       uint8_t* kt = sm + st * L::STAGE + L::QB;
       uint8_t* vt = kt + L::QB;
-      if (!wwait(&full[st], sph)) { ok = false; break; }
-      // rows past the end to zeros (K and V), non-finite V elements to zero
-      {
-        constexpr int KC = DK / 8, VC = DV / 8, PER = C * VC / 256;
-        const int tid = wi * 32 + lane;
-        if (n < C) {
-          for (int e = tid; e < (C - n) * KC; e += 256) {
-            const int t = n + e / KC, q = e % KC;
-            *reinterpret_cast<uint4*>(kt + (q >> 3) * (C * 128) + t * 128 + ((q & 7) << 4)) = make_uint4(0, 0, 0, 0);
-          }
-        }
-        bool bad = false;
-        uint32_t vm = 0;
+      constexpr int KC = DK / 8;
+      const int tid = wi * 32 + lane;
+      if (!wwait(&full[2 + st], sph) || !wwait(&full[4 + st], sph)) return false;
+      bool bad = false;
+      uint32_t vm = 0, km = 0;
+      // 16-byte chunks of a tile in memory order (box, row, chunk), 256 x 4 at a time
+      auto chunks = [&](uint8_t* tile, int bytes, bool is_v) {
 #pragma unroll 1
-        for (int k0 = 0; k0 < PER; k0 += 4) {
+        for (int at0 = tid * 16; at0 < bytes; at0 += 256 * 64) {
           uint4 v[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(vt + ((k0 + k) * 256 + tid) * 16);
+          for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(tile + at0 + k * 4096);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {        // 16-byte chunks in memory order: box, row, chunk
-            uint8_t* at = vt + ((k0 + k) * 256 + tid) * 16;
-            const int t = (((k0 + k) * 256 + tid) >> 3) % C;
+          for (int k = 0; k < 4; ++k) {
+            uint4* at = reinterpret_cast<uint4*>(tile + at0 + k * 4096);
             uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            if (((at0 + k * 4096) >> 7) % C >= n) {
+              *at = make_uint4(0, 0, 0, 0);
+              continue;
+            }
             bool hit = false;
 #pragma unroll
             for (int q = 0; q < 4; ++q) hit |= nonfinite(T(), w[q] & 0xffffu) || nonfinite(T(), w[q] >> 16);
-            if (t >= n) {
-              *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
-              continue;
-            }
             if (hit) {
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 if (nonfinite(T(), w[q] & 0xffffu)) w[q] &= 0xffff0000u;
                 if (nonfinite(T(), w[q] >> 16)) w[q] &= 0xffffu;
               }
-              *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-              bad = true;
+              if (is_v) {
+                *at = make_uint4(w[0], w[1], w[2], w[3]);
+                bad = true;
+              }
             }
             if constexpr (F16) {
+              uint32_t m = 0;
 #pragma unroll
-              for (int q = 0; q < 4; ++q) vm = max(vm, max(w[q] & 0x7fffu, (w[q] >> 16) & 0x7fffu));
+              for (int q = 0; q < 4; ++q) m = max(m, max(w[q] & 0x7fffu, (w[q] >> 16) & 0x7fffu));
+              if (is_v) vm = max(vm, m);
+              else km = max(km, m);
             }
           }
         }
-        if (bad) *v_flag = 1;
-        if constexpr (F16) {
-          vm = __reduce_max_sync(0xffffffffu, vm);
-          if (lane == 0) vmax[st * 8 + wi] = (int)vm;
+      };
+      chunks(vt, L::VB, true);
+      if constexpr (OUT && F16) {
+        chunks(kt, L::QB, false);
+      } else if (n < C) {
+        for (int e = tid; e < (C - n) * KC; e += 256) {
+          const int t = n + e / KC, q = e % KC;
+          *reinterpret_cast<uint4*>(kt + (q >> 3) * (C * 128) + t * 128 + ((q & 7) << 4)) = make_uint4(0, 0, 0, 0);
         }
-        fence_async_smem();
-        arrive(&clean[st]);
-        // (this role's own reads of V below: all its warps have cleaned their share)
-        if (!wwait(&clean[st], sph)) { ok = false; break; }
       }
-      int bnew = 0;
-      if constexpr (F16) {                     // decayed values below 2^14
-        int vm = 0;
+      if (bad) *v_flag = 1;
+      if constexpr (F16) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, vm) << 16 | __reduce_max_sync(0xffffffffu, km);
+        if (lane == 0) tmax[st * 8 + wi] = (int)m;
+        if (wi == 0 && lane == 0) s_exp[c & 1] = bound > 0.f ? max(-100, min(100, 14 - exp_above(bound))) : 100;
+      }
+      fence_async_smem();
+      arrive(&clean[st]);
+      return true;
+    };
+    if (ok && nch > 0) ok = cleaning(0);
+    for (int c = 0; c < nch && ok; ++c) {
+      const int st = c & 1, n = min(C, end - beg - c * C);
+      const uint32_t ph = c & 1, sph = (c >> 1) & 1;
+      const uint8_t* vt = sm + st * L::STAGE + 2 * L::QB;
+      if (!wwait(&clean[st], sph)) { ok = false; break; }   // (all warps' shares)
+      int bnew = 0, sa = 0;
+      float grow = 0.f;                        // bound on what the chunk adds to a state element
+      if constexpr (F16) {                     // decayed values below 2^14, and the scaled state finite
+        uint32_t vm = 0, km = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) vm = max(vm, vmax[st * 8 + k]);
-        if (vm > 0) bnew = 14 - exp_above(__half2float(__ushort_as_half((unsigned short)vm)));
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t m = (uint32_t)tmax[st * 8 + k];
+          vm = max(vm, m >> 16);
+          km = max(km, m & 0xffffu);
+        }
+        const float fv = __half2float(__ushort_as_half((unsigned short)vm));
+        grow = 1.00001f * (float)n * fv * __half2float(__ushort_as_half((unsigned short)km));
+        if (fv > 0.f) bnew = 14 - exp_above(fv);
+        if (bound > 0.f) bnew = min(bnew, 120 - exp_above(bound));
+        sa = bound > 0.f ? max(-100, min(100, 14 - exp_above(bound))) : 100;
       }
       if (c > 0 && !wwait(ds_done, (c - 1) & 1)) { ok = false; break; }
       if (OUT && c > 0 && !wwait(o_full, (c - 1) & 1)) { ok = false; break; }   // (its state copy has been read)
       fence_after();
       // state: operand copy (scaled for f16), then decayed in place
       if (OUT || c > 0) {
-        float f = 1.f;
-        if constexpr (OUT && F16) {
-          float m = 0.f;
-#pragma unroll 1
-          for (int b = 0; b < HK; b += 32) {
-            float x[32];
-            state32(c - 1, b, x);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) m = fmaxf(m, isfinite(x[e]) ? fabsf(x[e]) : 0.f);
-          }
-          m = warp_max(m);
-          if (lane == 0) wmax[ph * 8 + wi] = m;
-          arrive(smax);
-          if (!wwait(smax, ph)) { ok = false; break; }
-          m = 0.f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) m = fmaxf(m, wmax[ph * 8 + k]);
-          const int sa = m > 0.f ? max(-100, min(100, 14 - exp_above(m))) : 100;
-          if (wi == 0 && lane == 0) *s_exp = sa;
-          f = pow2f(sa);
-          if (m > 0.f) bnew = min(bnew, 120 - exp_above(m));   // (the scaled state stays finite)
-        }
+        const float f = F16 ? pow2f(sa) : 1.f;
         const float ds = F16 ? pw(n) * pow2f(bnew) : pw(n);
 #pragma unroll 1
         for (int b = 0; b < HK; b += 32) {
@@ -633,6 +654,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       }
       bexp = bnew;
+      bound = bound * pw(n) * 1.00001f + grow;
       // decayed values of rows 64 half .. +63, split: high part (nearest), low part (what it leaves)
       {
         const float sb = F16 ? pow2f(bnew) : 1.f;
@@ -669,6 +691,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       fence_before();
       arrive(s_ready);
       if (OUT && c > 0 && !outputs(c - 1)) { ok = false; break; }
+      if (c + 1 < nch && !cleaning(c + 1)) { ok = false; break; }
     }
     if (OUT && ok && nch > 0) ok = outputs(nch - 1);
     // ---- the state after the segment
