@@ -18,15 +18,17 @@
 // split into two such numbers (hi + lo), because the state is kept and returned in fp32: one
 // rounding of 2^-9 (bf16) would show in it. f16 rows: weights, decayed Q and the state's copy are
 // scaled by powers of two so that they use f16's range whatever the magnitudes: the state's copy by
-// 2^a (a per chunk, from a running bound lam^n bound + n max|v| max|k| on the state), row i's weights by 2^c_i, its decayed Q by 2^(c_i - a), the output row by 2^-c_i,
-// and the decayed values, with the state they are added to, by 2^b (b per chunk, so that the low
-// parts stay above f16's smallest number).
+// 2^a (from a running bound lam^n bound + n max|v| max|k| on the state), the weights by 2^c (from
+// dk max|q| max|k|, c for each 32 rows), the decayed Q by 2^(c - a), the outputs by 2^-c; f16's 30
+// binades leave room for how far above the values such bounds lie. The decayed values, with the
+// state they are added to, are scaled by 2^b (b per chunk), so that the low parts stay above f16's
+// smallest number.
 // One CTA per SM, 19 warps: 0 TMA producer (two stages of Q, K, V); 1 and 18 MMA issue (1: Q K^T and
 // the outputs, 18: the state); 2-9 rows of the chunk (TMEM lane = row, two threads a row: weights,
-// decayed Q); 10-17 value rows (TMEM lane = value row, two threads a row: the split decayed values,
-// the state's copy and decay; then the outputs of the chunk before). Their passes are loops over 32
-// columns, not unrolled code: a chunk's worth of straight-line code per role does not stay in the
-// instruction cache, and took twice as long.
+// decayed Q, and the outputs of the chunk before); 10-17 value rows (TMEM lane = value row, two
+// threads a row: the split decayed values, the state's copy and decay). Their passes are loops over
+// 32 columns, not unrolled code: a chunk's worth of straight-line code per role does not stay in the
+// instruction cache, and took longer.
 // 0 x NaN: rows past the sequence are zeroed in shared memory; non-finite V elements are replaced
 // by 0 and their terms are added, in the plain order of the formula, to exactly the rows and state
 // rows that they belong to.
@@ -94,9 +96,7 @@ struct Lay {
   static constexpr int S16 = 2 * STAGE;                    // the state's operand copy [DV][DK]
   static constexpr int WV = S16 + DV * DK * 2 + 16;        // lam^(127-t), t = -1 .. 127; the same for the last
                                                            // chunk's length, t = 0 .. 127
-  static constexpr int RMAX = WV + 2 * C * 4;              // f16: exponents of the row halves' maxima [2][C]
-  static constexpr int ROWS = RMAX + 2 * C * 4;            // f16: c_i, by chunk parity [2][C]
-  static constexpr int BAR = ROWS + 2 * C * 2;
+  static constexpr int BAR = WV + 2 * C * 4;
   static constexpr int NBAR = 28;
   static constexpr int USED = BAR + NBAR * 8 + 24 * 4;
   static_assert(USED <= 227 * 1024, "shared memory of one CTA");
@@ -106,6 +106,7 @@ struct Lay {
 
 // Smallest e with |x| < 2^e (finite x != 0).
 __device__ __forceinline__ int exp_above(float x) { return (int)((__float_as_uint(x) >> 23) & 255) - 126; }
+__device__ __forceinline__ float h_bits(uint32_t u) { return __half2float(__ushort_as_half((unsigned short)u)); }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 .. 127
 
 // OUT: outputs and final states from the segments' start states. !OUT: the segments' own
@@ -132,7 +133,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* ds_done = bars + 19;               // the state holds this chunk
   uint64_t* smax = bars + 20;                  // the start state's maximum over the warps is known (f16)
   uint64_t* mma_idle = bars + 21;              // [2]
-  uint64_t* pair = bars + 23;                  // [4] the two warps of a quadrant know their maxima (f16)
   uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // V has held a non-finite element
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&empty[i], 8);                 // Q: the row warps have read it (behind its products)
       mbar_init(&empty[2 + i], OUT ? 2 : 1);   // K: the products of the weights, and of the state
-      mbar_init(&empty[4 + i], 1);             // V: the products of the outputs (!OUT: of the state)
+      mbar_init(&empty[4 + i], OUT ? 8 : 1);   // V: the outputs, staged there (!OUT: the state's products)
       mbar_init(&clean[i], 8);
       mbar_init(&mma_idle[i], 1);
     }
@@ -180,7 +180,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(o_full, 1);
     mbar_init(ds_done, 1);
     mbar_init(smax, 8);
-    for (int i = 0; i < 4; ++i) mbar_init(&pair[i], 2);
     *abort_flag = 0;
     *v_flag = 0;
     mbar_init_fence();
@@ -200,8 +199,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   auto wwait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_err, ERR_TIMEOUT) ? 1 : 0) != 0;
   };
-  // f16: c_i of row i, by chunk parity
-  auto s_row = [&](int i, uint32_t parity) { return reinterpret_cast<int16_t*>(sm + L::ROWS) + parity * C + i; };
   auto pw = [&](int d) { return wv[C - 1 - d]; };   // lam^d, d = 0 .. 128
   auto arrive = [&](uint64_t* bar) {           // once per warp, after what it wrote
     __syncwarp();
@@ -271,7 +268,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mma_ts(tmem + T_O, tmem + T_P + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8),
                    vd + (uint64_t)(kk * 16 * 128 >> 4), ID_PV, 1u);
           commit(o_full);
-          commit(&empty[4 + st]);
         }
         __syncwarp();
       }
@@ -308,118 +304,168 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_drain(&mma_idle[1], 0);
     }
   } else if (warp < 10) {
-    // ---- rows of the chunk: two threads per row i, each half of its weights (columns 64 half ..)
-    // and of its decayed Q
+    // ---- rows of the chunk: two threads per row i, each half of its weights (columns 64 half ..), of
+    // its decayed Q and of its outputs. `scale` enters with the outputs
     if constexpr (OUT) {
       const int quad = warp & 3, half = (warp - 2) >> 2, i = quad * 32 + lane;
-      const uint32_t tP = tmem + ((uint32_t)(quad * 32) << 16) + T_P + half * 64;
-      volatile int* rmax = reinterpret_cast<volatile int*>(sm + L::RMAX);
-      constexpr int HQ = DK / 2;               // this half's Q elements
-      const float qs = a.scale * pw(i + 1);
+      const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+      constexpr int HQ = DK / 2, HV = DV / 2;  // this half's Q and output elements
+      const uint32_t tP = tmem + lane_off + T_P + half * 64, tO = tmem + lane_off + T_O + half * HV;
+      const float qs = pw(i + 1);
+      // chunk c's outputs, scaled by f, staged in its V tile (which nothing else reads any more)
+      auto outputs = [&](int c, float f) {
+        const int st = c & 1, n = min(C, end - beg - c * C);
+        if (!wwait(o_full, c & 1)) return false;
+        fence_after();
+        const bool fix = *v_flag && i < n;
+        uint8_t* stage = sm + st * L::STAGE + 2 * L::QB;
+#pragma unroll 1
+        for (int b = 0; b < HV; b += 32) {
+          uint32_t u[32];
+          __syncwarp();
+          tld32(tO + b, u);
+          ld_wait();
+          pin32(u);
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]) * f;
+          if (fix) {                           // terms of non-finite V elements
+            const int64_t r0 = row0 + c * C;
+            const T* q = (const T*)a.q + (r0 + i) * a.q_stride + h * DK;
+#pragma unroll 1
+            for (int j = 0; j <= i; ++j) {
+              const T* v = (const T*)a.v + (r0 + j) * a.v_stride + h * DV + half * HV + b;
+              bool any = false;
+#pragma unroll 1
+              for (int e = 0; e < 32; ++e) any |= !isfinite(ld_f(v + e));
+              if (!any) continue;
+              const T* k = (const T*)a.k + (r0 + j) * a.k_stride + h * DK;
+              float z = 0.f;
+#pragma unroll 1
+              for (int e = 0; e < DK; ++e) z += ld_f(q + e) * ld_f(k + e);
+              z *= a.scale * pw(i - j);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float x = ld_f(v + e);
+                if (!isfinite(x)) o[e] += z * x;
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4*>(stage + i * (DV * 2) + ((((half * HV + b + e) / 8) ^ (i & 7)) << 4)) =
+                make_uint4(pack(T(), o[e], o[e + 1]), pack(T(), o[e + 2], o[e + 3]), pack(T(), o[e + 4], o[e + 5]),
+                           pack(T(), o[e + 6], o[e + 7]));
+        }
+        fence_before();
+        arrive(o_free);                        // (also orders the stage's writes within the warp)
+        constexpr int CH = DV / 16;            // 16-byte chunks of this half of a row
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+          const int e = k * 32 + lane, r = quad * 32 + e / CH, q = half * CH + e % CH;
+          if (r < n)
+            *reinterpret_cast<uint4*>((T*)a.out + ((row0 + c * C + r) * a.H + h) * DV + q * 8) =
+                *reinterpret_cast<const uint4*>(stage + r * (DV * 2) + ((q ^ (r & 7)) << 4));
+        }
+        fence_async_smem();                    // the slot's next fill is a TMA write
+        arrive(&empty[4 + st]);
+        return true;
+      };
+      bool ok = true;
+      float f_prev = 0.f, f_out = a.scale;     // output scales of the chunk before, and of this one
       for (int c = 0; c < nch; ++c) {
         const int st = c & 1;
         const uint32_t ph = c & 1, sph = (c >> 1) & 1;
         const uint8_t* qrow = sm + st * L::STAGE + i * 128;
-        if (!wwait(&full[st], sph) || !wwait(p_full, ph)) break;
+        auto q16 = [&](int q) {                // 16-byte chunk q of the Q row
+          return *reinterpret_cast<const uint4*>(qrow + (q >> 3) * (C * 128) + (((q & 7) ^ (i & 7)) << 4));
+        };
+        if (!wwait(&full[st], sph)) { ok = false; break; }
+        float fp = 1.f, fq = qs;
+        f_prev = f_out;
+        if constexpr (F16) {                   // c of these 32 rows
+          uint32_t m = 0;
+#pragma unroll 4
+          for (int q = 0; q < DK / 8; ++q) {
+            const uint4 v = q16(q);
+            m = __vmaxu2(__vmaxu2(m, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
+            m = __vmaxu2(__vmaxu2(m, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
+          }
+          // (rows with a non-finite element, and rows of another sequence, take no part)
+          uint32_t qm = max(m & 0xffffu, m >> 16);
+          if (qm >= 0x7c00u || i >= end - beg - c * C) qm = 0;
+          qm = __reduce_max_sync(0xffffffffu, qm);
+          if (!wwait(&clean[st], sph)) { ok = false; break; }
+          uint32_t km = 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) km = max(km, (uint32_t)tmax[st * 8 + k] & 0xffffu);
+          const int sa = s_exp[ph];
+          const int eq = exp_above(h_bits(qm)), ek = exp_above(h_bits(km));
+          int cexp = 100;
+          if (qm > 0 && km > 0) cexp = min(cexp, 14 - (eq + ek + (DK == 128 ? 7 : 6)));
+          if (qm > 0 && sa < 100) cexp = min(cexp, sa + 14 - eq);
+          cexp = max(cexp, -100);
+          fp = pow2f(cexp);
+          const int qe = cexp - sa;            // (at most 14 - eq, or the state is zero)
+          fq = qe < -126 ? 0.f : qs * pow2f(min(qe, 126));
+          f_out = a.scale * pow2f(-cexp);
+        }
+        if (!wwait(p_full, ph)) { ok = false; break; }
         fence_after();
-        // 32 weights of V: scale lam^(i-j) q_i.k_j, 0 for j > i (columns b .. b+31 of the chunk)
-        auto weights = [&](int k, float* p) {
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          // 32 weights of V: lam^(i-j) q_i.k_j, 0 for j > i; 16-bit in place, behind what is still to be read
           const int b = 64 * half + 32 * k;
+          uint32_t p[16];
           if (b > quad * 32) {                 // behind every row of this warp
 #pragma unroll
-            for (int e = 0; e < 32; ++e) p[e] = 0.f;
-            return;
-          }
-          uint32_t u[32];
-          tld32(tP + 32 * k, u);
-          ld_wait();
-          pin32(u);
-          const float* w = wv + C - 1 - i + b; // lam^(i-b-e) at w[e] (past the diagonal: not used)
+            for (int e = 0; e < 16; ++e) p[e] = 0;
+          } else {
+            uint32_t u[32];
+            tld32(tP + 32 * k, u);
+            ld_wait();
+            pin32(u);
+            const float* w = wv + C - 1 - i + b;   // lam^(i-b-e) at w[e] (past the diagonal: not used)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) p[e] = b + e <= i ? __uint_as_float(u[e]) * (a.scale * w[e]) : 0.f;
-        };
-        // 32 elements of the decayed Q row
-        auto decayed = [&](int k, float* x) {
+            for (int e = 0; e < 32; e += 2) {
+              const float x0 = __uint_as_float(u[e]) * (F16 ? w[e] * fp : w[e]);
+              const float x1 = __uint_as_float(u[e + 1]) * (F16 ? w[e + 1] * fp : w[e + 1]);
+              p[e / 2] = pack(T(), b + e <= i ? x0 : 0.f, b + e + 1 <= i ? x1 : 0.f);
+            }
+          }
+          __syncwarp();
+          tst16(tP + 16 * k, p);
+        }
+#pragma unroll 1
+        for (int k = 0; k < HQ / 32; ++k) {    // decayed Q
+          uint32_t u[16];
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4) {
-            const int q = half * (HQ / 8) + 4 * k + k4;
-            const uint4 v = *reinterpret_cast<const uint4*>(qrow + (q >> 3) * (C * 128) + (((q & 7) ^ (i & 7)) << 4));
+            const uint4 v = q16(half * (HQ / 8) + 4 * k + k4);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float2 f = unpack(T(), w[e]);
-              x[8 * k4 + 2 * e] = f.x * qs;
-              x[8 * k4 + 2 * e + 1] = f.y * qs;
+              u[4 * k4 + e] = pack(T(), f.x * fq, f.y * fq);
             }
           }
-        };
-        float fp = 1.f, fq = 1.f;
-        if constexpr (F16) {                   // c_i from the row's maxima and the state's scale
-          float mp = 0.f, mq = 0.f;
-#pragma unroll 1
-          for (int k = 0; k < 2; ++k) {
-            float p[32];
-            weights(k, p);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mp = fmaxf(mp, fabsf(p[e]));
-          }
-#pragma unroll 1
-          for (int k = 0; k < HQ / 32; ++k) {
-            float x[32];
-            decayed(k, x);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mq = fmaxf(mq, fabsf(x[e]));
-          }
-          // (exponents; -1000: all zero)
-          const int ep = mp > 0.f ? exp_above(mp) : -1000, eq = mq > 0.f ? exp_above(mq) : -1000;
-          rmax[half * C + i] = (ep << 16) | (eq & 0xffff);
-          arrive(&pair[quad]);
-          if (!wwait(&pair[quad], ph)) break;
-          const int m1 = rmax[(half ^ 1) * C + i];
-          const int mep = max(ep, m1 >> 16), meq = max(eq, (int)(int16_t)(m1 & 0xffff));
-          if (!wwait(&clean[st], sph)) break;
-          const int sa = s_exp[ph];
-          int cexp = 100;
-          if (mep > -1000) cexp = min(cexp, 14 - mep);
-          if (meq > -1000 && sa < 100) cexp = min(cexp, sa + 14 - meq);
-          cexp = max(cexp, -100);
-          fp = pow2f(cexp);
-          const int qe = cexp - sa;            // (at most 14 - the exponent of mq, or the state is zero)
-          fq = qe < -126 ? 0.f : pow2f(min(qe, 126));
-          if (half == 0) *s_row(i, ph) = (int16_t)cexp;
-        }
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {          // in place: behind the columns still to be read
-          float p[32];
-          weights(k, p);
-          uint32_t u[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) u[e] = pack(T(), p[2 * e] * fp, p[2 * e + 1] * fp);
-          tst16(tP + 16 * k, u);
-        }
-#pragma unroll 1
-        for (int k = 0; k < HQ / 32; ++k) {
-          float x[32];
-          decayed(k, x);
-          uint32_t u[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) u[e] = pack(T(), x[2 * e] * fq, x[2 * e + 1] * fq);
           tst16(tP + 32 + 16 * k, u);
         }
         st_wait();
         fence_before();
         arrive(p_ready);
         if (lane == 0) mbar_arrive(&empty[st]);
+        if (c > 0 && !outputs(c - 1, f_prev)) { ok = false; break; }
       }
+      if (ok && nch > 0) outputs(nch - 1, f_out);
     }
   } else {
     // ---- value rows: two threads per row dv of the state (64 value rows: twice over the 128 lanes),
-    // each half of its columns, and half of the chunk's rows of the decayed values; and the outputs,
-    // two threads per row of the chunk
+    // each half of its columns, and half of the chunk's rows of the decayed values
     const int wi = warp - 10, quad = warp & 3, half = wi >> 2, r = quad * 32 + lane, dv = r % DV;
-    constexpr int HK = DK / 2, HV = DV / 2;
+    constexpr int HK = DK / 2;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t tS = tmem + lane_off + T_S + half * HK, tO = tmem + lane_off + T_O + half * HV;
+    const uint32_t tS = tmem + lane_off + T_S + half * HK;
     const uint32_t tVH = tmem + lane_off + T_VH + half * 32, tVL = tmem + lane_off + T_VL + half * 32;
     bool ok = true;
     int bexp = 0;                              // b: the state in TMEM is 2^b times the state (f16)
@@ -447,56 +493,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
       for (int e = 0; e < 32; ++e) x[e] = F16 ? __uint_as_float(u[e]) * f : __uint_as_float(u[e]);
       if (c >= 0 && *v_flag) fix_state(c, b, x);
-    };
-    // chunk c's outputs, rows scaled back
-    auto outputs = [&](int c) {
-      const int n = min(C, end - beg - c * C);
-      if (!wwait(o_full, c & 1)) return false;
-      fence_after();
-      const float fo = F16 ? pow2f(-(int)*s_row(r, c & 1)) : 1.f;
-      const bool fix = *v_flag && r < n;
-      T* out = (T*)a.out + ((row0 + c * C + r) * a.H + h) * DV + half * HV;
-#pragma unroll 1
-      for (int b = 0; b < HV; b += 32) {
-        uint32_t u[32];
-        __syncwarp();
-        tld32(tO + b, u);
-        ld_wait();
-        pin32(u);
-        float o[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]) * fo;
-        if (fix) {                             // terms of non-finite V elements
-          const int64_t r0 = row0 + c * C;
-          const T* q = (const T*)a.q + (r0 + r) * a.q_stride + h * DK;
-#pragma unroll 1
-          for (int j = 0; j <= r; ++j) {
-            const T* v = (const T*)a.v + (r0 + j) * a.v_stride + h * DV + half * HV + b;
-            bool any = false;
-#pragma unroll 1
-            for (int e = 0; e < 32; ++e) any |= !isfinite(ld_f(v + e));
-            if (!any) continue;
-            const T* k = (const T*)a.k + (r0 + j) * a.k_stride + h * DK;
-            float z = 0.f;
-#pragma unroll 1
-            for (int e = 0; e < DK; ++e) z += ld_f(q + e) * ld_f(k + e);
-            z *= a.scale * pw(r - j);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float x = ld_f(v + e);
-              if (!isfinite(x)) o[e] += z * x;
-            }
-          }
-        }
-        if (r < n)
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)      // (whole sectors: 64 bytes of the row)
-            *reinterpret_cast<uint4*>(out + b + e) = make_uint4(pack(T(), o[e], o[e + 1]), pack(T(), o[e + 2], o[e + 3]),
-                                                                pack(T(), o[e + 4], o[e + 5]), pack(T(), o[e + 6], o[e + 7]));
-      }
-      fence_before();
-      arrive(o_free);
-      return true;
     };
     float bound = 0.f;                         // at least every finite |state element| (f16)
     if constexpr (OUT) {
@@ -560,27 +556,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               *at = make_uint4(0, 0, 0, 0);
               continue;
             }
-            bool hit = false;
+            uint32_t m = 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) hit |= nonfinite(T(), w[q] & 0xffffu) || nonfinite(T(), w[q] >> 16);
-            if (hit) {
+            for (int q = 0; q < 4; ++q) m = __vmaxu2(m, w[q] & 0x7fff7fffu);
+            if (max(m & 0xffffu, m >> 16) >= (F16 ? 0x7c00u : 0x7f80u)) {   // a non-finite element
+              m = 0;
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 if (nonfinite(T(), w[q] & 0xffffu)) w[q] &= 0xffff0000u;
                 if (nonfinite(T(), w[q] >> 16)) w[q] &= 0xffffu;
+                m = __vmaxu2(m, w[q] & 0x7fff7fffu);
               }
               if (is_v) {
                 *at = make_uint4(w[0], w[1], w[2], w[3]);
                 bad = true;
               }
             }
-            if constexpr (F16) {
-              uint32_t m = 0;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) m = max(m, max(w[q] & 0x7fffu, (w[q] >> 16) & 0x7fffu));
-              if (is_v) vm = max(vm, m);
-              else km = max(km, m);
-            }
+            if (is_v) vm = __vmaxu2(vm, m);
+            else km = __vmaxu2(km, m);
           }
         }
       };
@@ -595,7 +588,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       if (bad) *v_flag = 1;
       if constexpr (F16) {
-        const uint32_t m = __reduce_max_sync(0xffffffffu, vm) << 16 | __reduce_max_sync(0xffffffffu, km);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, max(vm & 0xffffu, vm >> 16)) << 16 |
+                           __reduce_max_sync(0xffffffffu, max(km & 0xffffu, km >> 16));
         if (lane == 0) tmax[st * 8 + wi] = (int)m;
         if (wi == 0 && lane == 0) s_exp[c & 1] = bound > 0.f ? max(-100, min(100, 14 - exp_above(bound))) : 100;
       }
@@ -606,7 +600,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (ok && nch > 0) ok = cleaning(0);
     for (int c = 0; c < nch && ok; ++c) {
       const int st = c & 1, n = min(C, end - beg - c * C);
-      const uint32_t ph = c & 1, sph = (c >> 1) & 1;
+      const uint32_t sph = (c >> 1) & 1;
       const uint8_t* vt = sm + st * L::STAGE + 2 * L::QB;
       if (!wwait(&clean[st], sph)) { ok = false; break; }   // (all warps' shares)
       int bnew = 0, sa = 0;
@@ -619,8 +613,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           vm = max(vm, m >> 16);
           km = max(km, m & 0xffffu);
         }
-        const float fv = __half2float(__ushort_as_half((unsigned short)vm));
-        grow = 1.00001f * (float)n * fv * __half2float(__ushort_as_half((unsigned short)km));
+        const float fv = h_bits(vm);
+        grow = 1.00001f * (float)n * fv * h_bits(km);
         if (fv > 0.f) bnew = 14 - exp_above(fv);
         if (bound > 0.f) bnew = min(bnew, 120 - exp_above(bound));
         sa = bound > 0.f ? max(-100, min(100, 14 - exp_above(bound))) : 100;
@@ -690,10 +684,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       fence_async_smem();
       fence_before();
       arrive(s_ready);
-      if (OUT && c > 0 && !outputs(c - 1)) { ok = false; break; }
       if (c + 1 < nch && !cleaning(c + 1)) { ok = false; break; }
     }
-    if (OUT && ok && nch > 0) ok = outputs(nch - 1);
     // ---- the state after the segment
     float* dst = OUT ? (last && a.S_out ? a.S_out + (int64_t)(tab.seq0 + s) * per + head : nullptr) : ws_state;
     if (ok && nch > 0) ok = wwait(ds_done, (nch - 1) & 1);
