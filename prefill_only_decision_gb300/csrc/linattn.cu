@@ -25,7 +25,7 @@
 // smallest number.
 // One CTA per SM, 19 warps: 0 TMA producer (two stages of Q, K, V); 1 and 18 MMA issue (1: Q K^T and
 // the outputs, 18: the state); 2-9 rows of the chunk (TMEM lane = row, two threads a row: weights,
-// decayed Q, and the outputs of the chunk before); 10-17 value rows (TMEM lane = value row, two
+// decayed Q, outputs); 10-17 value rows (TMEM lane = value row, two
 // threads a row: the split decayed values, the state's copy and decay). Their passes are loops over
 // 32 columns, not unrolled code: a chunk's worth of straight-line code per role does not stay in the
 // instruction cache, and took longer.
@@ -75,14 +75,26 @@ __device__ int g_err;                        // bounded waits record here (one w
 
 constexpr int MAX_SEQ = 256;                 // sequences per launch
 
-// The sequences of a launch: rows row0[s] .. + len[s] - 1, segments segcum[s] .. segcum[s+1] - 1 of
-// seg_rows rows each (the last one shorter; an empty sequence has one). ws_seg[s]: the sequence's
-// first start state in the workspace, or -1 when it has a single segment.
+// The sequences of a launch: rows row0[s] .. + len[s] - 1, cut into segments of seg_rows rows.
+// Sequence s has fullcum[s+1] - fullcum[s] segments of that length, then possibly a shorter last one
+// (an empty sequence has one of no rows): blocks take all full segments first, then the short ones,
+// tailcum[s] of them before sequence s's. ws_seg[s]: the sequence's first start state in the
+// workspace, or -1 when it has a single segment.
 struct Tab {
   int n, seq0, seg_rows;
-  int segcum[MAX_SEQ + 1];
+  int fullcum[MAX_SEQ + 1], tailcum[MAX_SEQ + 1];
   int row0[MAX_SEQ], len[MAX_SEQ], ws_seg[MAX_SEQ];
 };
+// The entry that index i falls into: cum[s] <= i < cum[s + 1].
+__device__ __forceinline__ int find(const int* cum, int n, int i) {
+  int lo = 0, hi = n;                          // cum[lo] <= i < cum[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cum[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
 
 // TMEM columns: weights of V, per half of 64 columns: fp32, then 16-bit in its first 32 columns and
 // the half's decayed Q in its last 32 | outputs | state | low and high parts of the decayed values
@@ -126,8 +138,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* clean = bars + 12;                 // [2] K and V: rows past the end and non-finite V are zeros
   uint64_t* p_full = bars + 14;                // Q K^T is in TMEM
   uint64_t* p_ready = bars + 15;               // weights and decayed Q are in TMEM
-  uint64_t* s_ready = bars + 16;               // the state's copy is in shared memory, its decay applied,
-                                               // the decayed values are in TMEM
+  uint64_t* s_ready = bars + 16;               // the state's copy is in shared memory, its decay applied
+  uint64_t* v_ready = bars + 23;               // [2] the decayed values are in TMEM, V has been read for them
+                                               // (two: the row warps may see one a chunk late)
   uint64_t* o_free = bars + 17;                // the outputs have left TMEM
   uint64_t* o_full = bars + 18;                // outputs are in TMEM
   uint64_t* ds_done = bars + 19;               // the state holds this chunk
@@ -144,15 +157,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int warp = warp_index(), lane = threadIdx.x & 31;
   // this CTA's segment
   const int h = blockIdx.x % a.H, seg = blockIdx.x / a.H;
-  int s = 0;
-  for (int lo = 0, hi = tab.n - 1; lo < hi;) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (tab.segcum[mid] <= seg) lo = mid;
-    else hi = mid - 1;
-    s = lo;
-  }
-  const int k_seg = seg - tab.segcum[s];       // segment of the sequence
-  const bool last = seg + 1 == tab.segcum[s + 1];
+  const bool is_full = seg < tab.fullcum[tab.n];
+  const int s = is_full ? find(tab.fullcum, tab.n, seg) : find(tab.tailcum, tab.n, seg - tab.fullcum[tab.n]);
+  const int n_full = tab.fullcum[s + 1] - tab.fullcum[s];
+  const int k_seg = is_full ? seg - tab.fullcum[s] : n_full;   // segment of the sequence
+  const bool last = k_seg + 1 == n_full + (tab.tailcum[s + 1] - tab.tailcum[s]);
   if (!OUT && last) {                          // (nothing needs its contribution)
     allow_dependents();
     wait_prerequisites();
@@ -171,6 +180,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_init(&empty[2 + i], OUT ? 2 : 1);   // K: the products of the weights, and of the state
       mbar_init(&empty[4 + i], OUT ? 8 : 1);   // V: the outputs, staged there (!OUT: the state's products)
       mbar_init(&clean[i], 8);
+      mbar_init(&v_ready[i], 8);
       mbar_init(&mma_idle[i], 1);
     }
     mbar_init(p_full, 1);
@@ -221,6 +231,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           for (int b = 0; b < boxes; ++b) tma3(dst + b * C * 128, map, &full[slot], 64 * b, h, r);
           fills = (fills & ~(1u << (8 + slot))) | 1u << slot | (uint32_t)((c >> 1) & 1) << (8 + slot);
         };
+        // the chunk after the next into L2: its loads wait for slots, and then find it there
+        const int cp = c == 0 ? 1 : c + 2;
+        for (int d = cp; d <= c + 2 && d < nch; ++d) {
+          const int rp = (int)(row0 + d * C);
+          for (int b = 0; b < DK / 64; ++b) {
+            if (OUT) tma3_prefetch(&mapQ, 64 * b, h, rp);
+            tma3_prefetch(&mapK, 64 * b, h, rp);
+          }
+          for (int b = 0; b < DV / 64; ++b) tma3_prefetch(&mapV, 64 * b, h, rp);
+        }
         if (OUT) load(0, &mapQ, base, DK / 64, L::QB);
         load(1, &mapK, base + L::QB, DK / 64, L::QB);
         load(2, &mapV, base + 2 * L::QB, DV / 64, L::VB);
@@ -282,7 +302,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     constexpr uint32_t ID_S = idesc_f16(DK, BF, 0, 1);
     for (int c = 0; c < nch; ++c) {
       const int st = c & 1;
-      if (!wwait(&full[2 + st], (c >> 1) & 1) || !wwait(s_ready, c & 1)) break;
+      if (!wwait(&full[2 + st], (c >> 1) & 1) || !wwait(&v_ready[st], (c >> 1) & 1)) break;
       fence_after();
       if (leader) {
         const uint64_t kd = desc_sw128(smem_u32(sm + st * L::STAGE + L::QB), C * 128);
@@ -315,7 +335,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // chunk c's outputs, scaled by f, staged in its V tile (which nothing else reads any more)
       auto outputs = [&](int c, float f) {
         const int st = c & 1, n = min(C, end - beg - c * C);
-        if (!wwait(o_full, c & 1)) return false;
+        if (!wwait(o_full, c & 1) || !wwait(&v_ready[st], (c >> 1) & 1)) return false;
         fence_after();
         const bool fix = *v_flag && i < n;
         uint8_t* stage = sm + st * L::STAGE + 2 * L::QB;
@@ -371,8 +391,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         arrive(&empty[4 + st]);
         return true;
       };
-      bool ok = true;
-      float f_prev = 0.f, f_out = a.scale;     // output scales of the chunk before, and of this one
       for (int c = 0; c < nch; ++c) {
         const int st = c & 1;
         const uint32_t ph = c & 1, sph = (c >> 1) & 1;
@@ -380,9 +398,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         auto q16 = [&](int q) {                // 16-byte chunk q of the Q row
           return *reinterpret_cast<const uint4*>(qrow + (q >> 3) * (C * 128) + (((q & 7) ^ (i & 7)) << 4));
         };
-        if (!wwait(&full[st], sph)) { ok = false; break; }
-        float fp = 1.f, fq = qs;
-        f_prev = f_out;
+        if (!wwait(&full[st], sph)) break;
+        float fp = 1.f, fq = qs, f_out = a.scale;
         if constexpr (F16) {                   // c of these 32 rows
           uint32_t m = 0;
 #pragma unroll 4
@@ -395,7 +412,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           uint32_t qm = max(m & 0xffffu, m >> 16);
           if (qm >= 0x7c00u || i >= end - beg - c * C) qm = 0;
           qm = __reduce_max_sync(0xffffffffu, qm);
-          if (!wwait(&clean[st], sph)) { ok = false; break; }
+          if (!wwait(&clean[st], sph)) break;
           uint32_t km = 0;
 #pragma unroll
           for (int k = 0; k < 8; ++k) km = max(km, (uint32_t)tmax[st * 8 + k] & 0xffffu);
@@ -410,7 +427,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           fq = qe < -126 ? 0.f : qs * pow2f(min(qe, 126));
           f_out = a.scale * pow2f(-cexp);
         }
-        if (!wwait(p_full, ph)) { ok = false; break; }
+        if (!wwait(p_full, ph)) break;
         fence_after();
 #pragma unroll 1
         for (int k = 0; k < 2; ++k) {
@@ -455,9 +472,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         fence_before();
         arrive(p_ready);
         if (lane == 0) mbar_arrive(&empty[st]);
-        if (c > 0 && !outputs(c - 1, f_prev)) { ok = false; break; }
+        if (!outputs(c, f_out)) break;
       }
-      if (ok && nch > 0) outputs(nch - 1, f_out);
     }
   } else {
     // ---- value rows: two threads per row dv of the state (64 value rows: twice over the 128 lanes),
@@ -539,51 +555,48 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       constexpr int KC = DK / 8;
       const int tid = wi * 32 + lane;
       if (!wwait(&full[2 + st], sph) || !wwait(&full[4 + st], sph)) return false;
-      bool bad = false;
+      bool bad = false, wrote = false;
       uint32_t vm = 0, km = 0;
-      // 16-byte chunks of a tile in memory order (box, row, chunk), 256 x 4 at a time
-      auto chunks = [&](uint8_t* tile, int bytes, bool is_v) {
-#pragma unroll 1
-        for (int at0 = tid * 16; at0 < bytes; at0 += 256 * 64) {
-          uint4 v[4];
+      // a tile's 16-byte chunks in memory order (box, row, chunk), 256 threads x PER
+      auto chunks = [&](uint8_t* tile, auto count, bool is_v) {
+        constexpr int PER = decltype(count)::value;
+        uint4 v[PER];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(tile + at0 + k * 4096);
+        for (int k = 0; k < PER; ++k) v[k] = *reinterpret_cast<const uint4*>(tile + (k * 256 + tid) * 16);
+        uint32_t m = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint4* at = reinterpret_cast<uint4*>(tile + at0 + k * 4096);
+        for (int k = 0; k < PER; ++k) {
+          uint32_t mk = __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
+                                 __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu));
+          const bool past = (((k * 256 + tid) >> 3) % C) >= n;
+          if (past || max(mk & 0xffffu, mk >> 16) >= (F16 ? 0x7c00u : 0x7f80u)) {   // to be replaced
             uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-            if (((at0 + k * 4096) >> 7) % C >= n) {
-              *at = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint32_t m = 0;
+            mk = 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) m = __vmaxu2(m, w[q] & 0x7fff7fffu);
-            if (max(m & 0xffffu, m >> 16) >= (F16 ? 0x7c00u : 0x7f80u)) {   // a non-finite element
-              m = 0;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if (nonfinite(T(), w[q] & 0xffffu)) w[q] &= 0xffff0000u;
-                if (nonfinite(T(), w[q] >> 16)) w[q] &= 0xffffu;
-                m = __vmaxu2(m, w[q] & 0x7fff7fffu);
-              }
-              if (is_v) {
-                *at = make_uint4(w[0], w[1], w[2], w[3]);
-                bad = true;
-              }
+            for (int q = 0; q < 4; ++q) {
+              if (past || nonfinite(T(), w[q] & 0xffffu)) w[q] &= 0xffff0000u;
+              if (past || nonfinite(T(), w[q] >> 16)) w[q] &= 0xffffu;
+              mk = __vmaxu2(mk, w[q] & 0x7fff7fffu);
             }
-            if (is_v) vm = __vmaxu2(vm, m);
-            else km = __vmaxu2(km, m);
+            if (past || is_v) {
+              *reinterpret_cast<uint4*>(tile + (k * 256 + tid) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+              wrote = true;
+            }
+            bad |= is_v && !past;
           }
+          m = __vmaxu2(m, mk);
         }
+        if (is_v) vm = m;
+        else km = m;
       };
-      chunks(vt, L::VB, true);
+      chunks(vt, std::integral_constant<int, C * DV / 8 / 256>{}, true);
       if constexpr (OUT && F16) {
-        chunks(kt, L::QB, false);
+        chunks(kt, std::integral_constant<int, C * DK / 8 / 256>{}, false);
       } else if (n < C) {
         for (int e = tid; e < (C - n) * KC; e += 256) {
           const int t = n + e / KC, q = e % KC;
           *reinterpret_cast<uint4*>(kt + (q >> 3) * (C * 128) + t * 128 + ((q & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          wrote = true;
         }
       }
       if (bad) *v_flag = 1;
@@ -593,7 +606,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (lane == 0) tmax[st * 8 + wi] = (int)m;
         if (wi == 0 && lane == 0) s_exp[c & 1] = bound > 0.f ? max(-100, min(100, 14 - exp_above(bound))) : 100;
       }
-      fence_async_smem();
+      if (wrote) fence_async_smem();
       arrive(&clean[st]);
       return true;
     };
@@ -646,6 +659,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           __syncwarp();
           tst32(tS + b, u);
         }
+        if constexpr (OUT) {
+          st_wait();
+          fence_async_smem();
+          fence_before();
+          arrive(s_ready);
+        }
       }
       bexp = bnew;
       bound = bound * pw(n) * 1.00001f + grow;
@@ -681,9 +700,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       }
       st_wait();
-      fence_async_smem();
       fence_before();
-      arrive(s_ready);
+      arrive(&v_ready[st]);
       if (c + 1 < nch && !cleaning(c + 1)) { ok = false; break; }
     }
     // ---- the state after the segment
@@ -727,7 +745,7 @@ __global__ void __launch_bounds__(256)
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.S_in)
     S = *reinterpret_cast<const float4*>(a.S_in + (int64_t)(tab.seq0 + s) * a.s_in_stride + 4 * i);
-  const int n = tab.segcum[s + 1] - tab.segcum[s];
+  const int n = tab.fullcum[s + 1] - tab.fullcum[s] + tab.tailcum[s + 1] - tab.tailcum[s];
   float4* w = reinterpret_cast<float4*>(a.ws) + (int64_t)tab.ws_seg[s] * per4 + i;
   constexpr int AHEAD = 8;                     // contributions loaded before they are joined
   for (int k0 = 0; k0 + 1 < n; k0 += AHEAD) {
@@ -800,23 +818,45 @@ __global__ void __launch_bounds__(128)
 cudaError_t linattn_error_word(int** out) { return cudaGetSymbolAddress(reinterpret_cast<void**>(out), lin::g_err); }
 
 // Rows per segment (a multiple of the chunk) for a group of sequences: the count with the least
-// estimated time in us, waves of CTAs x (chunks of a segment + a CTA's fixed cost), with the
-// contributions' launch and the join added once sequences are cut.
-static int seg_rows_for(const int* len, int n, int H, int num_sms) {
+// estimated time in us. A CTA's cost is a fixed part and a part per chunk, as measured at 128 x 128;
+// the full segments fill the SMs in rounds, the shorter last ones go where SMs are free.
+static int seg_rows_for(const int* len, int n, int H, int dk, int dv, int num_sms) {
   int longest = 1;
   for (int s = 0; s < n; ++s) longest = std::max(longest, len[s]);
+  const double area = (double)dk * dv / (128.0 * 128.0);
   const int max_ch = (int)(((int64_t)longest + lin::C - 1) / lin::C);
   int best_m = max_ch;
-  double best = 1e30;
-  for (int m = max_ch; m >= 1; m = m > 8 ? m - (m + 7) / 8 : m - 1) {
-    int64_t ctas = 0, first = 0;
+  double best = 1e300;
+  for (int m = max_ch; m >= 1; m = m > 8 ? m - (m + 15) / 16 : m - 1) {
+    const int64_t L = (int64_t)m * lin::C;
+    int64_t full = 0, inner = 0, cut = 0;      // full segments, those before a sequence's last; sequences cut
+    double tail_out = 0, longest_tail = 0;
+    const double out_full = 4.0 * m + 6.0, con_full = 1.8 * m + 4.0;
+    int64_t slots = 0;
     for (int s = 0; s < n; ++s) {
-      const int64_t segs = std::max<int64_t>(1, ((int64_t)len[s] + (int64_t)m * lin::C - 1) / ((int64_t)m * lin::C));
-      ctas += segs * H;
-      first += (segs - 1) * H;
+      const int64_t f = len[s] / L, rest = len[s] - f * L, segs = f + (rest > 0 || len[s] == 0 ? 1 : 0);
+      full += f * H;
+      if (segs > f) {
+        const double t = 4.0 * (double)((rest + lin::C - 1) / lin::C) + 6.0;
+        tail_out += t * H;
+        longest_tail = std::max(longest_tail, t);
+      }
+      if (segs > 1) {
+        ++cut;
+        slots += segs * H;
+        inner += (segs - 1) * H;
+      }
     }
-    double t = (double)((ctas + num_sms - 1) / num_sms) * (3.0 * m + 4.0);
-    if (first > 0) t += (double)((first + num_sms - 1) / num_sms) * (2.0 * m + 3.0) + 4.0;
+    auto span = [&](int64_t count, double each, double rest, double rest_longest) {
+      const int64_t rounds = count / num_sms, over = count % num_sms;
+      double t = (double)rounds * each;
+      const double room = over ? (double)(num_sms - over) * each : 0.0;
+      if (over) t += each;
+      if (rest > room) t += std::max((rest - room) / num_sms, rest_longest);
+      return std::max(t, rest_longest);
+    };
+    double t = span(full, out_full, tail_out, longest_tail);
+    if (cut) t += span(inner, con_full, 0.0, 0.0) + 4.0 + (double)slots * area * 0.02;
     if (t < best) {
       best = t;
       best_m = m;
@@ -827,20 +867,21 @@ static int seg_rows_for(const int* len, int n, int H, int num_sms) {
 
 // Fills `t` with sequences from `s` on; returns the first one not taken. *slots: start states that
 // the group keeps in the workspace.
-static int lin_group(lin::Tab& t, int s, int n_seq, const int* row0, const int* len, int H, int num_sms,
-                     int64_t* slots) {
+static int lin_group(lin::Tab& t, int s, int n_seq, const int* row0, const int* len, int H, int dk, int dv,
+                     int num_sms, int64_t* slots) {
   t.seq0 = s;
   t.n = std::min(n_seq - s, lin::MAX_SEQ);
-  t.seg_rows = seg_rows_for(len + s, t.n, H, num_sms);
-  t.segcum[0] = 0;
+  t.seg_rows = seg_rows_for(len + s, t.n, H, dk, dv, num_sms);
+  t.fullcum[0] = t.tailcum[0] = 0;
   *slots = 0;
   for (int i = 0; i < t.n; ++i) {
-    const int segs = std::max(1, (int)(((int64_t)len[s + i] + t.seg_rows - 1) / t.seg_rows));
+    const int full = len[s + i] / t.seg_rows, tail = len[s + i] % t.seg_rows > 0 || len[s + i] == 0 ? 1 : 0;
     t.row0[i] = row0 ? row0[s + i] : 0;
     t.len[i] = len[s + i];
-    t.segcum[i + 1] = t.segcum[i] + segs;
-    t.ws_seg[i] = segs > 1 ? (int)*slots : -1;
-    if (segs > 1) *slots += segs;
+    t.fullcum[i + 1] = t.fullcum[i] + full;
+    t.tailcum[i + 1] = t.tailcum[i] + tail;
+    t.ws_seg[i] = full + tail > 1 ? (int)*slots : -1;
+    if (full + tail > 1) *slots += full + tail;
   }
   return s + t.n;
 }
@@ -849,7 +890,7 @@ int64_t linattn_ws_bytes(int n_seq, const int* len, int H, int dk, int dv, int n
   int64_t need = 0, slots;
   lin::Tab t;
   for (int s = 0; s < n_seq;) {
-    s = lin_group(t, s, n_seq, nullptr, len, H, num_sms, &slots);
+    s = lin_group(t, s, n_seq, nullptr, len, H, dk, dv, num_sms, &slots);
     need = std::max(need, slots * H * dk * dv * 4);
   }
   return need;
@@ -859,7 +900,7 @@ template <typename T, int DK, int DV>
 static cudaError_t lin_launch(const LinAttnArgs& a, const lin::Tab& t, int64_t slots, const CUtensorMap* m,
                               cudaStream_t st) {
   using L = lin::Lay<DK, DV>;
-  const dim3 grid((unsigned)((int64_t)t.segcum[t.n] * a.H)), block(lin::NTHREADS);
+  const dim3 grid((unsigned)((int64_t)(t.fullcum[t.n] + t.tailcum[t.n]) * a.H)), block(lin::NTHREADS);
   if (slots > 0) {
     CK_RET(cudaFuncSetAttribute(lin::chunk_kernel<T, DK, DV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 L::BYTES));
@@ -891,8 +932,8 @@ cudaError_t launch_linattn(const LinAttnArgs& a, int n_seq, const int* row0, con
   lin::Tab t;
   for (int s = 0; s < n_seq;) {
     int64_t slots;
-    s = lin_group(t, s, n_seq, row0, len, a.H, num_sms, &slots);
-    if ((int64_t)t.segcum[t.n] * a.H > INT_MAX) return cudaErrorInvalidValue;
+    s = lin_group(t, s, n_seq, row0, len, a.H, a.dk, a.dv, num_sms, &slots);
+    if (((int64_t)t.fullcum[t.n] + t.tailcum[t.n]) * a.H > INT_MAX) return cudaErrorInvalidValue;
 #define LIN_GO(T)                                                                                        \
   CK_RET(a.dk == 128 ? (a.dv == 128 ? lin_launch<T, 128, 128>(a, t, slots, m, st)                   \
                                     : lin_launch<T, 128, 64>(a, t, slots, m, st))                   \
