@@ -23,11 +23,11 @@
 // binades leave room for how far above the values such bounds lie. The decayed values, with the
 // state they are added to, are scaled by 2^b (b per chunk), so that the low parts stay above f16's
 // smallest number.
-// One CTA per SM, 19 warps: 0 TMA producer (two stages of Q, K, V); 1 and 18 MMA issue (1: Q K^T and
+// One CTA per SM, 23 warps: 0 TMA producer (two stages of Q, K, V); 1 and 18 MMA issue (1: Q K^T and
 // the outputs, 18: the state); 2-9 rows of the chunk (TMEM lane = row, two threads a row: weights,
-// decayed Q, outputs); 10-17 value rows (TMEM lane = value row, two
-// threads a row: the split decayed values, the state's copy and decay). Their passes are loops over
-// 32 columns, not unrolled code: a chunk's worth of straight-line code per role does not stay in the
+// decayed Q); 10-17 value rows (TMEM lane = value row, two threads a row: the split decayed values,
+// the state's copy and decay); 19-22 outputs (a thread a row). Their passes are loops over 32
+// columns, not unrolled code: a chunk's worth of straight-line code per role does not stay in the
 // instruction cache, and took longer.
 // 0 x NaN: rows past the sequence are zeroed in shared memory; non-finite V elements are replaced
 // by 0 and their terms are added, in the plain order of the formula, to exactly the rows and state
@@ -68,7 +68,7 @@ __device__ __forceinline__ float log2_decay(float log_decay) {
 __device__ __forceinline__ float decay(float log_decay) { return expf(fminf(log_decay, 0.f)); }
 
 constexpr int C = 128;                       // rows of a chunk
-constexpr int NTHREADS = 19 * 32;
+constexpr int NTHREADS = 23 * 32;
 constexpr int ERR_TIMEOUT = 0x501;
 
 __device__ int g_err;                        // bounded waits record here (one word per device)
@@ -110,7 +110,7 @@ struct Lay {
                                                            // chunk's length, t = 0 .. 127
   static constexpr int BAR = WV + 2 * C * 4;
   static constexpr int NBAR = 28;
-  static constexpr int USED = BAR + NBAR * 8 + 24 * 4;
+  static constexpr int USED = BAR + NBAR * 8 + 32 * 4;
   static_assert(USED <= 227 * 1024, "shared memory of one CTA");
   // above half an SM: each CTA allocates all of TMEM, so two never share one
   static constexpr int BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   volatile int* s_exp = (volatile int*)(tmem_slot + 3);    // [2] a, by chunk parity
   volatile int* tmax = (volatile int*)(tmem_slot + 5);     // [2 stages][8 warps]: max |V| and |K| as f16 bits
   volatile float* wmax = (volatile float*)(tmax + 8);      // [8] max |start state| per warp, before the chunks
+  volatile int* c_exp = (volatile int*)(tmem_slot + 21);   // [2][4] c of 32 rows, by chunk parity (f16)
   float* wv = reinterpret_cast<float*>(sm + L::WV);
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&empty[i], 8);                 // Q: the row warps have read it (behind its products)
       mbar_init(&empty[2 + i], OUT ? 2 : 1);   // K: the products of the weights, and of the state
-      mbar_init(&empty[4 + i], OUT ? 8 : 1);   // V: the outputs, staged there (!OUT: the state's products)
+      mbar_init(&empty[4 + i], OUT ? 4 : 1);   // V: the outputs, staged there (!OUT: the state's products)
       mbar_init(&clean[i], 8);
       mbar_init(&v_ready[i], 8);
       mbar_init(&mma_idle[i], 1);
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(p_full, 1);
     mbar_init(p_ready, 8);
     mbar_init(s_ready, 8);
-    mbar_init(o_free, 8);
+    mbar_init(o_free, 4);
     mbar_init(o_full, 1);
     mbar_init(ds_done, 1);
     mbar_init(smax, 8);
@@ -325,72 +326,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
   } else if (warp < 10) {
     // ---- rows of the chunk: two threads per row i, each half of its weights (columns 64 half ..), of
-    // its decayed Q and of its outputs. `scale` enters with the outputs
+    // its decayed Q. `scale` enters with the outputs
     if constexpr (OUT) {
       const int quad = warp & 3, half = (warp - 2) >> 2, i = quad * 32 + lane;
       const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-      constexpr int HQ = DK / 2, HV = DV / 2;  // this half's Q and output elements
-      const uint32_t tP = tmem + lane_off + T_P + half * 64, tO = tmem + lane_off + T_O + half * HV;
+      constexpr int HQ = DK / 2;               // this half's Q elements
+      const uint32_t tP = tmem + lane_off + T_P + half * 64;
       const float qs = pw(i + 1);
-      // chunk c's outputs, scaled by f, staged in its V tile (which nothing else reads any more)
-      auto outputs = [&](int c, float f) {
-        const int st = c & 1, n = min(C, end - beg - c * C);
-        if (!wwait(o_full, c & 1) || !wwait(&v_ready[st], (c >> 1) & 1)) return false;
-        fence_after();
-        const bool fix = *v_flag && i < n;
-        uint8_t* stage = sm + st * L::STAGE + 2 * L::QB;
-#pragma unroll 1
-        for (int b = 0; b < HV; b += 32) {
-          uint32_t u[32];
-          __syncwarp();
-          tld32(tO + b, u);
-          ld_wait();
-          pin32(u);
-          float o[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]) * f;
-          if (fix) {                           // terms of non-finite V elements
-            const int64_t r0 = row0 + c * C;
-            const T* q = (const T*)a.q + (r0 + i) * a.q_stride + h * DK;
-#pragma unroll 1
-            for (int j = 0; j <= i; ++j) {
-              const T* v = (const T*)a.v + (r0 + j) * a.v_stride + h * DV + half * HV + b;
-              bool any = false;
-#pragma unroll 1
-              for (int e = 0; e < 32; ++e) any |= !isfinite(ld_f(v + e));
-              if (!any) continue;
-              const T* k = (const T*)a.k + (r0 + j) * a.k_stride + h * DK;
-              float z = 0.f;
-#pragma unroll 1
-              for (int e = 0; e < DK; ++e) z += ld_f(q + e) * ld_f(k + e);
-              z *= a.scale * pw(i - j);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float x = ld_f(v + e);
-                if (!isfinite(x)) o[e] += z * x;
-              }
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(stage + i * (DV * 2) + ((((half * HV + b + e) / 8) ^ (i & 7)) << 4)) =
-                make_uint4(pack(T(), o[e], o[e + 1]), pack(T(), o[e + 2], o[e + 3]), pack(T(), o[e + 4], o[e + 5]),
-                           pack(T(), o[e + 6], o[e + 7]));
-        }
-        fence_before();
-        arrive(o_free);                        // (also orders the stage's writes within the warp)
-        constexpr int CH = DV / 16;            // 16-byte chunks of this half of a row
-#pragma unroll
-        for (int k = 0; k < CH; ++k) {
-          const int e = k * 32 + lane, r = quad * 32 + e / CH, q = half * CH + e % CH;
-          if (r < n)
-            *reinterpret_cast<uint4*>((T*)a.out + ((row0 + c * C + r) * a.H + h) * DV + q * 8) =
-                *reinterpret_cast<const uint4*>(stage + r * (DV * 2) + ((q ^ (r & 7)) << 4));
-        }
-        fence_async_smem();                    // the slot's next fill is a TMA write
-        arrive(&empty[4 + st]);
-        return true;
-      };
       for (int c = 0; c < nch; ++c) {
         const int st = c & 1;
         const uint32_t ph = c & 1, sph = (c >> 1) & 1;
@@ -399,7 +341,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           return *reinterpret_cast<const uint4*>(qrow + (q >> 3) * (C * 128) + (((q & 7) ^ (i & 7)) << 4));
         };
         if (!wwait(&full[st], sph)) break;
-        float fp = 1.f, fq = qs, f_out = a.scale;
+        float fp = 1.f, fq = qs;
         if constexpr (F16) {                   // c of these 32 rows
           uint32_t m = 0;
 #pragma unroll 4
@@ -425,7 +367,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           fp = pow2f(cexp);
           const int qe = cexp - sa;            // (at most 14 - eq, or the state is zero)
           fq = qe < -126 ? 0.f : qs * pow2f(min(qe, 126));
-          f_out = a.scale * pow2f(-cexp);
+          if (half == 0 && lane == 0) c_exp[ph * 4 + quad] = cexp;
         }
         if (!wwait(p_full, ph)) break;
         fence_after();
@@ -442,12 +384,26 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tld32(tP + 32 * k, u);
             ld_wait();
             pin32(u);
-            const float* w = wv + C - 1 - i + b;   // lam^(i-b-e) at w[e] (past the diagonal: not used)
+            if (b < quad * 32) {               // before every row: lam^(i-j) = lam^(i-b-31) lam^(b+31-j)
+              const float f = pw(i - b - 31) * fp;
+              const uint64_t f2 = pack2(f, f);
+              const float4* cw = reinterpret_cast<const float4*>(wv + C - 32);   // lam^(31-e)
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float x0 = __uint_as_float(u[e]) * (F16 ? w[e] * fp : w[e]);
-              const float x1 = __uint_as_float(u[e + 1]) * (F16 ? w[e + 1] * fp : w[e + 1]);
-              p[e / 2] = pack(T(), b + e <= i ? x0 : 0.f, b + e + 1 <= i ? x1 : 0.f);
+              for (int e = 0; e < 32; e += 4) {
+                const float4 w = cw[e / 4];
+                const uint64_t x = mul2(pack2u(u[e], u[e + 1]), mul2(pack2(w.x, w.y), f2));
+                const uint64_t y = mul2(pack2u(u[e + 2], u[e + 3]), mul2(pack2(w.z, w.w), f2));
+                p[e / 2] = pack(T(), lo2(x), hi2(x));
+                p[e / 2 + 1] = pack(T(), lo2(y), hi2(y));
+              }
+            } else {                           // across the diagonal
+              const float* w = wv + C - 1 - lane;    // lam^(lane-e) at w[e] (past the diagonal: not used)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float x0 = __uint_as_float(u[e]) * (F16 ? w[e] * fp : w[e]);
+                const float x1 = __uint_as_float(u[e + 1]) * (F16 ? w[e + 1] * fp : w[e + 1]);
+                p[e / 2] = pack(T(), e <= lane ? x0 : 0.f, e + 1 <= lane ? x1 : 0.f);
+              }
             }
           }
           __syncwarp();
@@ -472,7 +428,75 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         fence_before();
         arrive(p_ready);
         if (lane == 0) mbar_arrive(&empty[st]);
-        if (!outputs(c, f_out)) break;
+      }
+    }
+  } else if (warp >= 19) {
+    // ---- outputs: thread = row i; scaled, staged in the V tile (which nothing else reads any more),
+    // stored in whole rows
+    if constexpr (OUT) {
+      const int quad = warp & 3, i = quad * 32 + lane;
+      const uint32_t tO = tmem + ((uint32_t)(quad * 32) << 16) + T_O;
+      for (int c = 0; c < nch; ++c) {
+        const int st = c & 1, n = min(C, end - beg - c * C);
+        if (!wwait(o_full, c & 1) || !wwait(&v_ready[st], (c >> 1) & 1)) break;
+        fence_after();
+        const float f = F16 ? a.scale * pow2f(-c_exp[(c & 1) * 4 + quad]) : a.scale;
+        const uint64_t f2 = pack2(f, f);
+        const bool fix = *v_flag && i < n;
+        uint8_t* stage = sm + st * L::STAGE + 2 * L::QB;
+#pragma unroll 1
+        for (int b = 0; b < DV; b += 32) {
+          uint32_t u[32];
+          __syncwarp();
+          tld32(tO + b, u);
+          ld_wait();
+          pin32(u);
+          if (fix) {                           // terms of non-finite V elements, before the scale
+            const int64_t r0 = row0 + c * C;
+            const T* q = (const T*)a.q + (r0 + i) * a.q_stride + h * DK;
+#pragma unroll 1
+            for (int j = 0; j <= i; ++j) {
+              const T* v = (const T*)a.v + (r0 + j) * a.v_stride + h * DV + b;
+              bool any = false;
+#pragma unroll 1
+              for (int e = 0; e < 32; ++e) any |= !isfinite(ld_f(v + e));
+              if (!any) continue;
+              const T* k = (const T*)a.k + (r0 + j) * a.k_stride + h * DK;
+              float z = 0.f;
+#pragma unroll 1
+              for (int e = 0; e < DK; ++e) z += ld_f(q + e) * ld_f(k + e);
+              z *= pw(i - j);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float x = ld_f(v + e);
+                if (!isfinite(x)) u[e] = __float_as_uint(__uint_as_float(u[e]) + z * x);
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint64_t x = mul2(pack2u(u[e + 2 * k], u[e + 2 * k + 1]), f2);
+              o[k] = pack(T(), lo2(x), hi2(x));
+            }
+            *reinterpret_cast<uint4*>(stage + i * (DV * 2) + ((((b + e) / 8) ^ (i & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        fence_before();
+        arrive(o_free);                        // (also orders the stage's writes within the warp)
+        constexpr int CH = DV / 8;             // 16-byte chunks of a row
+#pragma unroll 4
+        for (int k = 0; k < CH; ++k) {
+          const int e = k * 32 + lane, r = quad * 32 + e / CH, q = e % CH;
+          if (r < n)
+            *reinterpret_cast<uint4*>((T*)a.out + ((row0 + c * C + r) * a.H + h) * DV + q * 8) =
+                *reinterpret_cast<const uint4*>(stage + r * (DV * 2) + ((q ^ (r & 7)) << 4));
+        }
+        fence_async_smem();                    // the slot's next fill is a TMA write
+        arrive(&empty[4 + st]);
       }
     }
   } else {
