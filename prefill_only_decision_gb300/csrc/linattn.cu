@@ -110,7 +110,7 @@ struct Lay {
                                                            // chunk's length, t = 0 .. 127
   static constexpr int BAR = WV + 2 * C * 4;
   static constexpr int NBAR = 28;
-  static constexpr int USED = BAR + NBAR * 8 + 32 * 4;
+  static constexpr int USED = BAR + NBAR * 8 + 52 * 4;
   static_assert(USED <= 227 * 1024, "shared memory of one CTA");
   // above half an SM: each CTA allocates all of TMEM, so two never share one
   static constexpr int BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
@@ -127,6 +127,7 @@ template <typename T, int DK, int DV, bool OUT>
 __global__ void __launch_bounds__(NTHREADS, 1)
     chunk_kernel(const __grid_constant__ Tab tab, const __grid_constant__ CUtensorMap mapQ,
                  const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                 const __grid_constant__ CUtensorMap mapO,
                  const __grid_constant__ LinAttnArgs a) {
   using L = Lay<DK, DV>;
   constexpr bool F16 = std::is_same<T, f16>::value;
@@ -146,13 +147,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* ds_done = bars + 19;               // the state holds this chunk
   uint64_t* smax = bars + 20;                  // the start state's maximum over the warps is known (f16)
   uint64_t* mma_idle = bars + 21;              // [2]
+  uint64_t* k_known = bars + 25;               // max |K| of the chunk is known (f16)
   uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // V has held a non-finite element
-  volatile int* s_exp = (volatile int*)(tmem_slot + 3);    // [2] a, by chunk parity
-  volatile int* tmax = (volatile int*)(tmem_slot + 5);     // [2 stages][8 warps]: max |V| and |K| as f16 bits
-  volatile float* wmax = (volatile float*)(tmax + 8);      // [8] max |start state| per warp, before the chunks
-  volatile int* c_exp = (volatile int*)(tmem_slot + 21);   // [2][4] c of 32 rows, by chunk parity (f16)
+  volatile int* vmax = (volatile int*)(tmem_slot + 3);     // [2 stages][8 warps] max |V| as f16 bits
+  volatile int* kmax = (volatile int*)(tmem_slot + 19);    // [2][8] max |K|, by chunk parity
+  volatile float* wmax = (volatile float*)(tmem_slot + 35);  // [8] max |start state| per warp
+  volatile int* c_exp = (volatile int*)(tmem_slot + 43);   // [2][4] c of 32 rows, by chunk parity (f16)
   float* wv = reinterpret_cast<float*>(sm + L::WV);
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -191,6 +193,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(o_full, 1);
     mbar_init(ds_done, 1);
     mbar_init(smax, 8);
+    mbar_init(k_known, 8);
     *abort_flag = 0;
     *v_flag = 0;
     mbar_init_fence();
@@ -209,6 +212,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const uint32_t tmem = *tmem_slot;
   auto wwait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_err, ERR_TIMEOUT) ? 1 : 0) != 0;
+  };
+  // f16: the state's scale exponent a, and the bound on the state after a chunk of n rows
+  auto max8 = [](volatile int* m) {
+    int x = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x = max(x, m[k]);
+    return (uint32_t)x;
+  };
+  auto start_bound = [&]() {
+    float x = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x = fmaxf(x, wmax[k]);
+    return x;
+  };
+  auto scale_exp = [](float bound) { return bound > 0.f ? max(-100, min(100, 14 - exp_above(bound))) : 100; };
+  auto grown = [&](float bound, int n, uint32_t vm, uint32_t km) {
+    // (each product rounded by itself: two roles form the same number)
+    const float add = __fmul_rn(__fmul_rn(1.00001f * (float)n, h_bits(vm)), h_bits(km));
+    return __fadd_rn(__fmul_rn(__fmul_rn(bound, wv[C - 1 - n]), 1.00001f), add);
   };
   auto pw = [&](int d) { return wv[C - 1 - d]; };   // lam^d, d = 0 .. 128
   auto arrive = [&](uint64_t* bar) {           // once per warp, after what it wrote
@@ -333,6 +355,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       constexpr int HQ = DK / 2;               // this half's Q elements
       const uint32_t tP = tmem + lane_off + T_P + half * 64;
       const float qs = pw(i + 1);
+      float bound = 0.f;                       // at least every finite |state element| (f16)
+      if (F16 && nch > 0 && wwait(smax, 0)) bound = start_bound();
       for (int c = 0; c < nch; ++c) {
         const int st = c & 1;
         const uint32_t ph = c & 1, sph = (c >> 1) & 1;
@@ -343,22 +367,42 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (!wwait(&full[st], sph)) break;
         float fp = 1.f, fq = qs;
         if constexpr (F16) {                   // c of these 32 rows
-          uint32_t m = 0;
+          uint32_t m = 0, mk = 0;
 #pragma unroll 4
           for (int q = 0; q < DK / 8; ++q) {
             const uint4 v = q16(q);
-            m = __vmaxu2(__vmaxu2(m, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
-            m = __vmaxu2(__vmaxu2(m, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
+            m = absmax2(T(), m, absmax2(T(), absmax2(T(), v.x, v.y), absmax2(T(), v.z, v.w)));
           }
           // (rows with a non-finite element, and rows of another sequence, take no part)
           uint32_t qm = max(m & 0xffffu, m >> 16);
           if (qm >= 0x7c00u || i >= end - beg - c * C) qm = 0;
           qm = __reduce_max_sync(0xffffffffu, qm);
+          // this warp's share of K, once its rows past the end are zeros; non-finite elements aside
           if (!wwait(&clean[st], sph)) break;
-          uint32_t km = 0;
+          const uint8_t* kt = sm + st * L::STAGE + L::QB + (warp - 2) * (L::QB / 8) + lane * 16;
+#pragma unroll 4
+          for (int k = 0; k < L::QB / 8 / 512; ++k) {
+            const uint4 v = *reinterpret_cast<const uint4*>(kt + k * 512);
+            uint32_t x = absmax2(T(), absmax2(T(), v.x, v.y), absmax2(T(), v.z, v.w));
+            if (max(x & 0xffffu, x >> 16) >= 0x7c00u) {
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              x = 0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) km = max(km, (uint32_t)tmax[st * 8 + k] & 0xffffu);
-          const int sa = s_exp[ph];
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t lo = nonfinite(T(), w[q] & 0xffffu) ? 0u : w[q] & 0x7fffu;
+                const uint32_t hi = nonfinite(T(), w[q] >> 16) ? 0u : w[q] >> 16 & 0x7fffu;
+                x = absmax2(T(), x, lo | hi << 16);
+              }
+            }
+            mk = absmax2(T(), mk, x);
+          }
+          mk = __reduce_max_sync(0xffffffffu, max(mk & 0xffffu, mk >> 16));
+          if (lane == 0) kmax[ph * 8 + warp - 2] = (int)mk;
+          arrive(k_known);
+          if (!wwait(k_known, ph)) break;
+          const uint32_t km = max8(kmax + ph * 8), vm = max8(vmax + st * 8);
+          const int sa = scale_exp(bound);
+          bound = grown(bound, min(C, end - beg - c * C), vm, km);
           const int eq = exp_above(h_bits(qm)), ek = exp_above(h_bits(km));
           int cexp = 100;
           if (qm > 0 && km > 0) cexp = min(cexp, 14 - (eq + ek + (DK == 128 ? 7 : 6)));
@@ -481,23 +525,35 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               const uint64_t x = mul2(pack2u(u[e + 2 * k], u[e + 2 * k + 1]), f2);
               o[k] = pack(T(), lo2(x), hi2(x));
             }
-            *reinterpret_cast<uint4*>(stage + i * (DV * 2) + ((((b + e) / 8) ^ (i & 7)) << 4)) =
+            const int q = (b + e) / 8;         // (the layout of a TMA tile: boxes of 64 columns, swizzled)
+            *reinterpret_cast<uint4*>(stage + (q >> 3) * (C * 128) + i * 128 + (((q & 7) ^ (i & 7)) << 4)) =
                 make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
         fence_before();
+        fence_async_smem();                    // (read by the TMA store, and the slot's next fill is a TMA write)
         arrive(o_free);                        // (also orders the stage's writes within the warp)
-        constexpr int CH = DV / 8;             // 16-byte chunks of a row
-#pragma unroll 4
-        for (int k = 0; k < CH; ++k) {
-          const int e = k * 32 + lane, r = quad * 32 + e / CH, q = e % CH;
-          if (r < n)
-            *reinterpret_cast<uint4*>((T*)a.out + ((row0 + c * C + r) * a.H + h) * DV + q * 8) =
-                *reinterpret_cast<const uint4*>(stage + r * (DV * 2) + ((q ^ (r & 7)) << 4));
+        if (quad * 32 + 32 <= n) {             // 32 whole rows
+          if (lane == 0) {
+            for (int b = 0; b < DV / 64; ++b)
+              tma3_store(&mapO, stage + b * (C * 128) + quad * 32 * 128, 64 * b, h, (int)(row0 + c * C + quad * 32));
+            tma_store_commit();
+            tma_store_read_wait();
+          }
+        } else {
+          constexpr int CH = DV / 8;           // 16-byte chunks of a row
+#pragma unroll 1
+          for (int k = 0; k < CH; ++k) {
+            const int e = k * 32 + lane, r = quad * 32 + e / CH, q = e % CH;
+            if (r < n)
+              *reinterpret_cast<uint4*>((T*)a.out + ((row0 + c * C + r) * a.H + h) * DV + q * 8) =
+                  *reinterpret_cast<const uint4*>(stage + (q >> 3) * (C * 128) + r * 128 + (((q & 7) ^ (r & 7)) << 4));
+          }
+          fence_async_smem();
         }
-        fence_async_smem();                    // the slot's next fill is a TMA write
         arrive(&empty[4 + st]);
       }
+      if (lane == 0) tma_store_wait();         // the stores are complete before the CTA leaves
     }
   } else {
     // ---- value rows: two threads per row dv of the state (64 value rows: twice over the 128 lanes),
@@ -566,98 +622,74 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (lane == 0) wmax[wi] = bound;
         arrive(smax);
         ok = wwait(smax, 0);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) bound = fmaxf(bound, wmax[k]);
+        bound = start_bound();
       }
     }
-    // rows past the end to zeros (K and V), non-finite V elements to zero; f16: the tiles' maxima, and a
+    // rows past the end to zeros (K and V), non-finite V elements to zero; f16: max |V|
     auto cleaning = [&](int c) {
       const int st = c & 1, n = min(C, end - beg - c * C);
       const uint32_t sph = (c >> 1) & 1;
       uint8_t* kt = sm + st * L::STAGE + L::QB;
       uint8_t* vt = kt + L::QB;
-      constexpr int KC = DK / 8;
+      constexpr int KC = DK / 8, PER = C * DV / 8 / 256;
       const int tid = wi * 32 + lane;
       if (!wwait(&full[2 + st], sph) || !wwait(&full[4 + st], sph)) return false;
       bool bad = false, wrote = false;
-      uint32_t vm = 0, km = 0;
-      // a tile's 16-byte chunks in memory order (box, row, chunk), 256 threads x PER
-      auto chunks = [&](uint8_t* tile, auto count, bool is_v) {
-        constexpr int PER = decltype(count)::value;
-        uint4 v[PER];
+      uint32_t vm = 0;
+      uint4 v[PER];
 #pragma unroll
-        for (int k = 0; k < PER; ++k) v[k] = *reinterpret_cast<const uint4*>(tile + (k * 256 + tid) * 16);
-        uint32_t m = 0;
+      for (int k = 0; k < PER; ++k) v[k] = *reinterpret_cast<const uint4*>(vt + (k * 256 + tid) * 16);
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
-          uint32_t mk = __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
-                                 __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu));
-          const bool past = (((k * 256 + tid) >> 3) % C) >= n;
-          if (past || max(mk & 0xffffu, mk >> 16) >= (F16 ? 0x7c00u : 0x7f80u)) {   // to be replaced
-            uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-            mk = 0;
+      for (int k = 0; k < PER; ++k) {          // 16-byte chunks in memory order: box, row, chunk
+        uint32_t mk = absmax2(T(), absmax2(T(), v[k].x, v[k].y), absmax2(T(), v[k].z, v[k].w));
+        const bool past = (((k * 256 + tid) >> 3) % C) >= n;
+        if (past || max(mk & 0xffffu, mk >> 16) >= (F16 ? 0x7c00u : 0x7f80u)) {   // to be replaced
+          uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+          mk = 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (past || nonfinite(T(), w[q] & 0xffffu)) w[q] &= 0xffff0000u;
-              if (past || nonfinite(T(), w[q] >> 16)) w[q] &= 0xffffu;
-              mk = __vmaxu2(mk, w[q] & 0x7fff7fffu);
-            }
-            if (past || is_v) {
-              *reinterpret_cast<uint4*>(tile + (k * 256 + tid) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-              wrote = true;
-            }
-            bad |= is_v && !past;
+          for (int q = 0; q < 4; ++q) {
+            if (past || nonfinite(T(), w[q] & 0xffffu)) w[q] &= 0xffff0000u;
+            if (past || nonfinite(T(), w[q] >> 16)) w[q] &= 0xffffu;
+            mk = absmax2(T(), mk, w[q]);
           }
-          m = __vmaxu2(m, mk);
+          *reinterpret_cast<uint4*>(vt + (k * 256 + tid) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          wrote = true;
+          bad |= !past;
         }
-        if (is_v) vm = m;
-        else km = m;
-      };
-      chunks(vt, std::integral_constant<int, C * DV / 8 / 256>{}, true);
-      if constexpr (OUT && F16) {
-        chunks(kt, std::integral_constant<int, C * DK / 8 / 256>{}, false);
-      } else if (n < C) {
+        vm = absmax2(T(), vm, mk);
+      }
+      if (n < C)
         for (int e = tid; e < (C - n) * KC; e += 256) {
           const int t = n + e / KC, q = e % KC;
           *reinterpret_cast<uint4*>(kt + (q >> 3) * (C * 128) + t * 128 + ((q & 7) << 4)) = make_uint4(0, 0, 0, 0);
           wrote = true;
         }
-      }
       if (bad) *v_flag = 1;
       if constexpr (F16) {
-        const uint32_t m = __reduce_max_sync(0xffffffffu, max(vm & 0xffffu, vm >> 16)) << 16 |
-                           __reduce_max_sync(0xffffffffu, max(km & 0xffffu, km >> 16));
-        if (lane == 0) tmax[st * 8 + wi] = (int)m;
-        if (wi == 0 && lane == 0) s_exp[c & 1] = bound > 0.f ? max(-100, min(100, 14 - exp_above(bound))) : 100;
+        vm = __reduce_max_sync(0xffffffffu, max(vm & 0xffffu, vm >> 16));
+        if (lane == 0) vmax[st * 8 + wi] = (int)vm;
       }
       if (wrote) fence_async_smem();
       arrive(&clean[st]);
       return true;
     };
     if (ok && nch > 0) ok = cleaning(0);
+    uint32_t vm = 0;                           // max |V| of the last chunk begun (f16)
     for (int c = 0; c < nch && ok; ++c) {
       const int st = c & 1, n = min(C, end - beg - c * C);
       const uint32_t sph = (c >> 1) & 1;
       const uint8_t* vt = sm + st * L::STAGE + 2 * L::QB;
       if (!wwait(&clean[st], sph)) { ok = false; break; }   // (all warps' shares)
-      int bnew = 0, sa = 0;
-      float grow = 0.f;                        // bound on what the chunk adds to a state element
-      if constexpr (F16) {                     // decayed values below 2^14, and the scaled state finite
-        uint32_t vm = 0, km = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t m = (uint32_t)tmax[st * 8 + k];
-          vm = max(vm, m >> 16);
-          km = max(km, m & 0xffffu);
-        }
-        const float fv = h_bits(vm);
-        grow = 1.00001f * (float)n * fv * h_bits(km);
-        if (fv > 0.f) bnew = 14 - exp_above(fv);
-        if (bound > 0.f) bnew = min(bnew, 120 - exp_above(bound));
-        sa = bound > 0.f ? max(-100, min(100, 14 - exp_above(bound))) : 100;
-      }
       if (c > 0 && !wwait(ds_done, (c - 1) & 1)) { ok = false; break; }
       if (OUT && c > 0 && !wwait(o_full, (c - 1) & 1)) { ok = false; break; }   // (its state copy has been read)
+      int bnew = 0, sa = 0;
+      if constexpr (F16) {                     // decayed values below 2^14, and the scaled state finite
+        if (OUT && c > 0) bound = grown(bound, C, vm, max8(kmax + (st ^ 1) * 8));
+        vm = max8(vmax + st * 8);
+        if (vm > 0) bnew = 14 - exp_above(h_bits(vm));
+        if (bound > 0.f) bnew = min(bnew, 120 - exp_above(bound));
+        sa = scale_exp(bound);
+      }
       fence_after();
       // state: operand copy (scaled for f16), then decayed in place
       if (OUT || c > 0) {
@@ -691,7 +723,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       }
       bexp = bnew;
-      bound = bound * pw(n) * 1.00001f + grow;
       // decayed values of rows 64 half .. +63, split: high part (nearest), low part (what it leaves)
       {
         const float sb = F16 ? pow2f(bnew) : 1.f;
@@ -928,12 +959,12 @@ static cudaError_t lin_launch(const LinAttnArgs& a, const lin::Tab& t, int64_t s
   if (slots > 0) {
     CK_RET(cudaFuncSetAttribute(lin::chunk_kernel<T, DK, DV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 L::BYTES));
-    CK_RET(launch_pdl(lin::chunk_kernel<T, DK, DV, false>, grid, block, L::BYTES, st, t, m[0], m[1], m[2], a));
+    CK_RET(launch_pdl(lin::chunk_kernel<T, DK, DV, false>, grid, block, L::BYTES, st, t, m[0], m[1], m[2], m[3], a));
     const int64_t per4 = (int64_t)a.H * DK * DV / 4;
     CK_RET(launch_pdl(lin::scan_kernel, dim3((unsigned)((per4 + 255) / 256), t.n), dim3(256), 0, st, t, a));
   }
   CK_RET(cudaFuncSetAttribute(lin::chunk_kernel<T, DK, DV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES));
-  return launch_pdl(lin::chunk_kernel<T, DK, DV, true>, grid, block, L::BYTES, st, t, m[0], m[1], m[2], a);
+  return launch_pdl(lin::chunk_kernel<T, DK, DV, true>, grid, block, L::BYTES, st, t, m[0], m[1], m[2], m[3], a);
 }
 
 cudaError_t launch_linattn(const LinAttnArgs& a, int n_seq, const int* row0, const int* len, int num_sms,
@@ -941,14 +972,14 @@ cudaError_t launch_linattn(const LinAttnArgs& a, int n_seq, const int* row0, con
   int64_t rows = 1;
   for (int s = 0; s < n_seq; ++s)
     if (len[s]) rows = std::max(rows, (int64_t)row0[s] + len[s]);
-  CUtensorMap m[3];
-  const void* ptr[3] = {a.q, a.k, a.v};
-  const int d[3] = {a.dk, a.dk, a.dv};
-  const int64_t ld[3] = {a.q_stride, a.k_stride, a.v_stride};
-  for (int i = 0; i < 3; ++i) {
+  CUtensorMap m[4];                            // q, k, v, out
+  const void* ptr[4] = {a.q, a.k, a.v, a.out};
+  const int d[4] = {a.dk, a.dk, a.dv, a.dv};
+  const int64_t ld[4] = {a.q_stride, a.k_stride, a.v_stride, (int64_t)a.H * a.dv};
+  for (int i = 0; i < 4; ++i) {
     const uint64_t dims[3] = {(uint64_t)d[i], (uint64_t)a.H, (uint64_t)rows};
     const uint64_t str[2] = {(uint64_t)d[i] * 2, (uint64_t)ld[i] * 2};
-    const uint32_t box[3] = {64, 1, lin::C};
+    const uint32_t box[3] = {64, 1, i < 3 ? (uint32_t)lin::C : 32u};
     if (!encode_tensor_map(&m[i], a.dtype == ELEM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                            3, ptr[i], dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;

@@ -82,6 +82,17 @@ __device__ __forceinline__ void tma3(void* dst, const CUtensorMap* map, uint64_t
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
+// Stores a tile from shared memory; committed with tma_store_commit, its shared memory free again
+// after tma_store_read_wait, the store complete after tma_store_wait.
+__device__ __forceinline__ void tma3_store(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_read_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // Asks for a tile in L2 ahead of its load.
 __device__ __forceinline__ void tma3_prefetch(const CUtensorMap* map, int x, int y, int z) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
@@ -201,6 +212,17 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The larger of two pairs of magnitudes, element by element; NaN where either is NaN.
+__device__ __forceinline__ uint32_t absmax2(f16, uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+  return d;
+}
+__device__ __forceinline__ uint32_t absmax2(bf16, uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+  return d;
+}
 // Two fp32 lanes at once.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
