@@ -121,13 +121,63 @@ __device__ __forceinline__ int exp_above(float x) { return (int)((__float_as_uin
 __device__ __forceinline__ float h_bits(uint32_t u) { return __half2float(__ushort_as_half((unsigned short)u)); }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 .. 127
 
+// Terms of non-finite V elements, which the products leave out (out of line: hardly ever taken).
+// Outputs: rows r0 .. r0 + n - 1 of head h, this warp's row `i` and every column.
+template <typename T>
+__device__ __noinline__ void fix_outputs(const LinAttnArgs& a, const float* wv, int64_t r0, int i, int h) {
+  const T* q = (const T*)a.q + (r0 + i) * a.q_stride + h * a.dk;
+  T* out = (T*)a.out + ((r0 + i) * a.H + h) * a.dv;
+  for (int j = 0; j <= i; ++j) {
+    const T* v = (const T*)a.v + (r0 + j) * a.v_stride + h * a.dv;
+    const T* k = (const T*)a.k + (r0 + j) * a.k_stride + h * a.dk;
+    float z = 0.f;
+    bool have = false;
+    for (int e = 0; e < a.dv; ++e) {
+      const float x = ld_f(v + e);
+      if (isfinite(x)) continue;
+      if (!have) {
+        for (int d = 0; d < a.dk; ++d) z += ld_f(q + d) * ld_f(k + d);
+        z *= a.scale * wv[C - 1 - (i - j)];
+        have = true;
+      }
+      st_f(out + e, ld_f(out + e) + z * x);
+    }
+  }
+}
+// State: value row dv, columns col .. col + ncol - 1 of head h at TMEM address tS, which hold 2^b
+// times the state after rows r0 .. r0 + n - 1.
+template <typename T>
+__device__ __noinline__ void fix_state(const LinAttnArgs& a, const float* wv, int64_t r0, int n, int h, int dv, int col,
+                                       int ncol, uint32_t tS, float scale) {
+  for (int b = 0; b < ncol; b += 32) {
+    uint32_t u[32];
+    __syncwarp();
+    tld32(tS + b, u);
+    ld_wait();
+    pin32(u);
+#pragma unroll 1
+    for (int t = 0; t < n; ++t) {
+      const float v = ld_f((const T*)a.v + (r0 + t) * a.v_stride + h * a.dv + dv);
+      if (isfinite(v)) continue;
+      const T* k = (const T*)a.k + (r0 + t) * a.k_stride + h * a.dk + col + b;
+      const float w = wv[C - n + t] * scale;   // lam^(n-1-t)
+#pragma unroll
+      for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) + w * v * ld_f(k + e));
+    }
+    __syncwarp();
+    tst32(tS + b, u);
+    st_wait();
+  }
+}
+
 // OUT: outputs and final states from the segments' start states. !OUT: the segments' own
 // contributions to the state into the workspace (all segments but each sequence's last).
 template <typename T, int DK, int DV, bool OUT>
 __global__ void __launch_bounds__(NTHREADS, 1)
     chunk_kernel(const __grid_constant__ Tab tab, const __grid_constant__ CUtensorMap mapQ,
                  const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
-                 const __grid_constant__ CUtensorMap mapO,
+                 const __grid_constant__ CUtensorMap mapO, const __grid_constant__ CUtensorMap mapIn,
+                 const __grid_constant__ CUtensorMap mapWs, const __grid_constant__ CUtensorMap mapFin,
                  const __grid_constant__ LinAttnArgs a) {
   using L = Lay<DK, DV>;
   constexpr bool F16 = std::is_same<T, f16>::value;
@@ -147,6 +197,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* ds_done = bars + 19;               // the state holds this chunk
   uint64_t* smax = bars + 20;                  // the start state's maximum over the warps is known (f16)
   uint64_t* mma_idle = bars + 21;              // [2]
+  uint64_t* in_full = bars + 26;               // the start state is in shared memory
+  uint64_t* in_free = bars + 27;               // it has been taken from there
   uint64_t* k_known = bars + 25;               // max |K| of the chunk is known (f16)
   uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
@@ -173,8 +225,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int len = tab.len[s], beg = k_seg * tab.seg_rows, end = min(len, beg + tab.seg_rows);
   const int nch = (end - beg + C - 1) / C;     // chunks (0 for an empty sequence)
   const int64_t row0 = (int64_t)tab.row0[s] + beg;
-  const int64_t per = (int64_t)a.H * DV * DK, head = (int64_t)h * DV * DK;
-  float* ws_state = (float*)a.ws + (tab.ws_seg[s] < 0 ? 0 : tab.ws_seg[s] + k_seg) * per + head;
+  const int ws_slot = tab.ws_seg[s] + k_seg;   // (of a sequence with several segments)
+  // where the start state is, if there is one: as tiles of 32 floats x 32 value rows, copied into the
+  // second stage's slots before that stage is used
+  const bool from_ws = tab.ws_seg[s] >= 0;
+  const bool has_start = OUT && (from_ws || a.S_in != nullptr);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 6; ++i) mbar_init(&full[i], 1);
@@ -194,6 +249,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(ds_done, 1);
     mbar_init(smax, 8);
     mbar_init(k_known, 8);
+    mbar_init(in_full, 1);
+    mbar_init(in_free, 8);
     *abort_flag = 0;
     *v_flag = 0;
     mbar_init_fence();
@@ -243,7 +300,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (lane == 0) {
       uint32_t fills = 0;                      // per slot: begun (bit i), parity of the last fill (bit 8 + i)
       bool ok = true;
+      if (has_start) {
+        mbar_expect_tx(in_full, DV * DK * 4);
+        for (int b = 0; b < DK / 32; ++b)
+          for (int y = 0; y < DV; y += 32)
+            tma4(sm + L::STAGE + b * (DV * 128) + y * 128, from_ws ? &mapWs : &mapIn, in_full, 32 * b, y, h,
+                 from_ws ? ws_slot : (a.s_in_stride ? tab.seq0 + s : 0));
+      }
       for (int c = 0; c < nch && ok; ++c) {
+        if (c == 1 && has_start) ok = mbar_wait(in_free, 0, abort_flag, &g_err, ERR_TIMEOUT);
+        if (!ok) break;
         const int st = c & 1, r = (int)(row0 + c * C);
         uint8_t* base = sm + st * L::STAGE;
         auto load = [&](int which, const CUtensorMap* map, uint8_t* dst, int boxes, int bytes) {
@@ -268,6 +334,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         load(1, &mapK, base + L::QB, DK / 64, L::QB);
         load(2, &mapV, base + 2 * L::QB, DV / 64, L::VB);
       }
+      if (*abort_flag && has_start) mbar_drain(in_full, 0);
       if (*abort_flag)                         // copies in flight land before the CTA leaves
         for (int i = 0; i < 6; ++i)
           if ((fills >> i) & 1) mbar_drain(&full[i], (fills >> (8 + i)) & 1);
@@ -377,32 +444,33 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           uint32_t qm = max(m & 0xffffu, m >> 16);
           if (qm >= 0x7c00u || i >= end - beg - c * C) qm = 0;
           qm = __reduce_max_sync(0xffffffffu, qm);
-          // this warp's share of K, once its rows past the end are zeros; non-finite elements aside
-          if (!wwait(&clean[st], sph)) break;
-          const uint8_t* kt = sm + st * L::STAGE + L::QB + (warp - 2) * (L::QB / 8) + lane * 16;
-#pragma unroll 4
+          // this warp's share of K; rows past the end and non-finite elements aside
+          const int n = min(C, end - beg - c * C), k0 = (warp - 2) * (L::QB / 8) + lane * 16;
+          if (!wwait(&full[2 + st], sph)) break;
+          const uint8_t* kt = sm + st * L::STAGE + L::QB + k0;
+#pragma unroll
           for (int k = 0; k < L::QB / 8 / 512; ++k) {
             const uint4 v = *reinterpret_cast<const uint4*>(kt + k * 512);
-            uint32_t x = absmax2(T(), absmax2(T(), v.x, v.y), absmax2(T(), v.z, v.w));
-            if (max(x & 0xffffu, x >> 16) >= 0x7c00u) {
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-              x = 0;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const uint32_t lo = nonfinite(T(), w[q] & 0xffffu) ? 0u : w[q] & 0x7fffu;
-                const uint32_t hi = nonfinite(T(), w[q] >> 16) ? 0u : w[q] >> 16 & 0x7fffu;
-                x = absmax2(T(), x, lo | hi << 16);
-              }
+            const uint32_t x = absmax2(T(), absmax2(T(), v.x, v.y), absmax2(T(), v.z, v.w));
+            if ((k0 + k * 512 >> 7) % C < n) mk = absmax2(T(), mk, x);
+          }
+          if (max(mk & 0xffffu, mk >> 16) >= 0x7c00u) {
+            mk = 0;
+#pragma unroll 1
+            for (int k = 0; k < L::QB / 8 / 512 * 4; ++k) {
+              const bool in = (k0 + (k >> 2) * 512 >> 7) % C < n;
+              const uint32_t w = in ? *reinterpret_cast<const uint32_t*>(kt + (k >> 2) * 512 + (k & 3) * 4) : 0u;
+              const uint32_t lo = nonfinite(T(), w & 0xffffu) ? 0u : w & 0x7fffu;
+              const uint32_t hi = nonfinite(T(), w >> 16) ? 0u : w >> 16 & 0x7fffu;
+              mk = absmax2(T(), mk, lo | hi << 16);
             }
-            mk = absmax2(T(), mk, x);
           }
           mk = __reduce_max_sync(0xffffffffu, max(mk & 0xffffu, mk >> 16));
           if (lane == 0) kmax[ph * 8 + warp - 2] = (int)mk;
           arrive(k_known);
           if (!wwait(k_known, ph)) break;
-          const uint32_t km = max8(kmax + ph * 8), vm = max8(vmax + st * 8);
+          const uint32_t km = max8(kmax + ph * 8);
           const int sa = scale_exp(bound);
-          bound = grown(bound, min(C, end - beg - c * C), vm, km);
           const int eq = exp_above(h_bits(qm)), ek = exp_above(h_bits(km));
           int cexp = 100;
           if (qm > 0 && km > 0) cexp = min(cexp, 14 - (eq + ek + (DK == 128 ? 7 : 6)));
@@ -428,26 +496,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tld32(tP + 32 * k, u);
             ld_wait();
             pin32(u);
-            if (b < quad * 32) {               // before every row: lam^(i-j) = lam^(i-b-31) lam^(b+31-j)
-              const float f = pw(i - b - 31) * fp;
-              const uint64_t f2 = pack2(f, f);
-              const float4* cw = reinterpret_cast<const float4*>(wv + C - 32);   // lam^(31-e)
+            const float* w = wv + C - 1 - i + b;   // lam^(i-b-e) at w[e] (past the diagonal: not used)
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 w = cw[e / 4];
-                const uint64_t x = mul2(pack2u(u[e], u[e + 1]), mul2(pack2(w.x, w.y), f2));
-                const uint64_t y = mul2(pack2u(u[e + 2], u[e + 3]), mul2(pack2(w.z, w.w), f2));
-                p[e / 2] = pack(T(), lo2(x), hi2(x));
-                p[e / 2 + 1] = pack(T(), lo2(y), hi2(y));
-              }
-            } else {                           // across the diagonal
-              const float* w = wv + C - 1 - lane;    // lam^(lane-e) at w[e] (past the diagonal: not used)
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float x0 = __uint_as_float(u[e]) * (F16 ? w[e] * fp : w[e]);
-                const float x1 = __uint_as_float(u[e + 1]) * (F16 ? w[e + 1] * fp : w[e + 1]);
-                p[e / 2] = pack(T(), e <= lane ? x0 : 0.f, e + 1 <= lane ? x1 : 0.f);
-              }
+            for (int e = 0; e < 32; e += 2) {
+              const float x0 = __uint_as_float(u[e]) * (F16 ? w[e] * fp : w[e]);
+              const float x1 = __uint_as_float(u[e + 1]) * (F16 ? w[e + 1] * fp : w[e + 1]);
+              p[e / 2] = pack(T(), b + e <= i ? x0 : 0.f, b + e + 1 <= i ? x1 : 0.f);
             }
           }
           __syncwarp();
@@ -470,6 +524,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         st_wait();
         fence_before();
+        if constexpr (F16) {                   // (before p_ready: V's maximum is there until then)
+          if (!wwait(&clean[st], sph)) break;
+          bound = grown(bound, min(C, end - beg - c * C), max8(vmax + st * 8), max8(kmax + ph * 8));
+        }
         arrive(p_ready);
         if (lane == 0) mbar_arrive(&empty[st]);
       }
@@ -486,7 +544,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         fence_after();
         const float f = F16 ? a.scale * pow2f(-c_exp[(c & 1) * 4 + quad]) : a.scale;
         const uint64_t f2 = pack2(f, f);
-        const bool fix = *v_flag && i < n;
+        const bool fix = *v_flag;
         uint8_t* stage = sm + st * L::STAGE + 2 * L::QB;
 #pragma unroll 1
         for (int b = 0; b < DV; b += 32) {
@@ -495,28 +553,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           tld32(tO + b, u);
           ld_wait();
           pin32(u);
-          if (fix) {                           // terms of non-finite V elements, before the scale
-            const int64_t r0 = row0 + c * C;
-            const T* q = (const T*)a.q + (r0 + i) * a.q_stride + h * DK;
-#pragma unroll 1
-            for (int j = 0; j <= i; ++j) {
-              const T* v = (const T*)a.v + (r0 + j) * a.v_stride + h * DV + b;
-              bool any = false;
-#pragma unroll 1
-              for (int e = 0; e < 32; ++e) any |= !isfinite(ld_f(v + e));
-              if (!any) continue;
-              const T* k = (const T*)a.k + (r0 + j) * a.k_stride + h * DK;
-              float z = 0.f;
-#pragma unroll 1
-              for (int e = 0; e < DK; ++e) z += ld_f(q + e) * ld_f(k + e);
-              z *= pw(i - j);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float x = ld_f(v + e);
-                if (!isfinite(x)) u[e] = __float_as_uint(__uint_as_float(u[e]) + z * x);
-              }
-            }
-          }
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             uint32_t o[4];
@@ -551,6 +587,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           fence_async_smem();
         }
+        if (fix) {
+          if (lane == 0) tma_store_wait();
+          __syncwarp();
+          if (i < n) fix_outputs<T>(a, wv, row0 + c * C, i, h);
+        }
         arrive(&empty[4 + st]);
       }
       if (lane == 0) tma_store_wait();         // the stores are complete before the CTA leaves
@@ -565,21 +606,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t tVH = tmem + lane_off + T_VH + half * 32, tVL = tmem + lane_off + T_VL + half * 32;
     bool ok = true;
     int bexp = 0;                              // b: the state in TMEM is 2^b times the state (f16)
-    // adds chunk c's terms of non-finite V elements to this thread's state columns b .. b+31
-    auto fix_state = [&](int c, int b, float* x) {
-      const int n = min(C, end - beg - c * C);
-      const int64_t r0 = row0 + c * C;
-#pragma unroll 1
-      for (int t = 0; t < n; ++t) {
-        const float v = ld_f((const T*)a.v + (r0 + t) * a.v_stride + h * DV + dv);
-        if (isfinite(v)) continue;
-        const T* k = (const T*)a.k + (r0 + t) * a.k_stride + h * DK + half * HK + b;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] += pw(n - 1 - t) * v * ld_f(k + e);
-      }
+    // adds chunk c's terms of non-finite V elements to this thread's state columns
+    auto fix = [&](int c) {
+      if (*v_flag)
+        fix_state<T>(a, wv, row0 + c * C, min(C, end - beg - c * C), h, dv, half * HK, HK, tS,
+                     F16 ? pow2f(bexp) : 1.f);
     };
-    // 32 columns of this thread's state row (chunk c in it), unscaled
-    auto state32 = [&](int c, int b, float* x) {
+    // 32 columns of this thread's state row, unscaled
+    auto state32 = [&](int b, float* x) {
       uint32_t u[32];
       __syncwarp();
       tld32(tS + b, u);
@@ -588,43 +622,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const float f = F16 ? pow2f(-bexp) : 1.f;
 #pragma unroll
       for (int e = 0; e < 32; ++e) x[e] = F16 ? __uint_as_float(u[e]) * f : __uint_as_float(u[e]);
-      if (c >= 0 && *v_flag) fix_state(c, b, x);
     };
     float bound = 0.f;                         // at least every finite |state element| (f16)
-    if constexpr (OUT) {
-      // the start state into TMEM
-      const float* src = tab.ws_seg[s] >= 0 ? ws_state
-                                            : (a.S_in ? a.S_in + (int64_t)(tab.seq0 + s) * a.s_in_stride + head : nullptr);
-#pragma unroll 1
-      for (int b = 0; b < HK; b += 32) {
-        uint32_t u[32];
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 v = src ? *reinterpret_cast<const float4*>(src + (int64_t)dv * DK + half * HK + b + e)
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
-          u[e] = __float_as_uint(v.x);
-          u[e + 1] = __float_as_uint(v.y);
-          u[e + 2] = __float_as_uint(v.z);
-          u[e + 3] = __float_as_uint(v.w);
-        }
-        if constexpr (F16) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float x = fabsf(__uint_as_float(u[e]));
-            if (x < INFINITY) bound = fmaxf(bound, x);
-          }
-        }
-        tst32(tS + b, u);
-      }
-      st_wait();
-      if constexpr (F16) {
-        bound = warp_max(bound);
-        if (lane == 0) wmax[wi] = bound;
-        arrive(smax);
-        ok = wwait(smax, 0);
-        bound = start_bound();
-      }
-    }
     // rows past the end to zeros (K and V), non-finite V elements to zero; f16: max |V|
     auto cleaning = [&](int c) {
       const int st = c & 1, n = min(C, end - beg - c * C);
@@ -636,33 +635,42 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (!wwait(&full[2 + st], sph) || !wwait(&full[4 + st], sph)) return false;
       bool bad = false, wrote = false;
       uint32_t vm = 0;
-      uint4 v[PER];
+      {
+        uint4 v[PER];                          // 16-byte chunks in memory order: box, row, chunk
 #pragma unroll
-      for (int k = 0; k < PER; ++k) v[k] = *reinterpret_cast<const uint4*>(vt + (k * 256 + tid) * 16);
+        for (int k = 0; k < PER; ++k) v[k] = *reinterpret_cast<const uint4*>(vt + (k * 256 + tid) * 16);
 #pragma unroll
-      for (int k = 0; k < PER; ++k) {          // 16-byte chunks in memory order: box, row, chunk
-        uint32_t mk = absmax2(T(), absmax2(T(), v[k].x, v[k].y), absmax2(T(), v[k].z, v[k].w));
-        const bool past = (((k * 256 + tid) >> 3) % C) >= n;
-        if (past || max(mk & 0xffffu, mk >> 16) >= (F16 ? 0x7c00u : 0x7f80u)) {   // to be replaced
-          uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-          mk = 0;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (past || nonfinite(T(), w[q] & 0xffffu)) w[q] &= 0xffff0000u;
-            if (past || nonfinite(T(), w[q] >> 16)) w[q] &= 0xffffu;
-            mk = absmax2(T(), mk, w[q]);
-          }
-          *reinterpret_cast<uint4*>(vt + (k * 256 + tid) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-          wrote = true;
-          bad |= !past;
+        for (int k = 0; k < PER; ++k) {
+          const uint32_t x = absmax2(T(), absmax2(T(), v[k].x, v[k].y), absmax2(T(), v[k].z, v[k].w));
+          if ((((k * 256 + tid) >> 3) % C) < n) vm = absmax2(T(), vm, x);
+          else *reinterpret_cast<uint4*>(vt + (k * 256 + tid) * 16) = make_uint4(0, 0, 0, 0);
         }
-        vm = absmax2(T(), vm, mk);
+      }
+      wrote = n < C;
+      if (max(vm & 0xffffu, vm >> 16) >= (F16 ? 0x7c00u : 0x7f80u)) {   // some element is to be replaced
+        vm = 0;
+#pragma unroll 1
+        for (int k = 0; k < PER; ++k) {
+          uint32_t* at = reinterpret_cast<uint32_t*>(vt + (k * 256 + tid) * 16);
+          const bool past = (((k * 256 + tid) >> 3) % C) >= n;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t w = at[q];
+            if (past) continue;
+            const bool lo = nonfinite(T(), w & 0xffffu), hi = nonfinite(T(), w >> 16);
+            bad |= lo || hi;
+            if (lo) w &= 0xffff0000u;
+            if (hi) w &= 0xffffu;
+            at[q] = w;
+            vm = absmax2(T(), vm, w);
+          }
+        }
+        wrote = true;
       }
       if (n < C)
         for (int e = tid; e < (C - n) * KC; e += 256) {
           const int t = n + e / KC, q = e % KC;
           *reinterpret_cast<uint4*>(kt + (q >> 3) * (C * 128) + t * 128 + ((q & 7) << 4)) = make_uint4(0, 0, 0, 0);
-          wrote = true;
         }
       if (bad) *v_flag = 1;
       if constexpr (F16) {
@@ -673,7 +681,49 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       arrive(&clean[st]);
       return true;
     };
-    if (ok && nch > 0) ok = cleaning(0);
+    // this thread's place for columns b + 4 e .. + 3 of a state row in shared memory (swizzled tiles)
+    auto state_at = [&](uint8_t* base, int b, int e) {
+      const int col = half * HK + b;
+      return reinterpret_cast<float4*>(base + (col >> 5) * (DV * 128) + dv * 128 + ((e ^ (dv & 7)) << 4));
+    };
+    if (nch > 0) ok = cleaning(0);
+    if constexpr (OUT) {
+      // the start state into TMEM
+      if (ok && has_start) ok = wwait(in_full, 0);
+#pragma unroll 1
+      for (int b = 0; b < HK && ok; b += 32) {
+        uint32_t u[32];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float4 v = has_start ? *state_at(sm + L::STAGE, b, e) : make_float4(0.f, 0.f, 0.f, 0.f);
+          u[4 * e] = __float_as_uint(v.x);
+          u[4 * e + 1] = __float_as_uint(v.y);
+          u[4 * e + 2] = __float_as_uint(v.z);
+          u[4 * e + 3] = __float_as_uint(v.w);
+        }
+        if constexpr (F16) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float x = fabsf(__uint_as_float(u[e]));
+            if (x < INFINITY) bound = fmaxf(bound, x);
+          }
+        }
+        __syncwarp();
+        tst32(tS + b, u);
+      }
+      st_wait();
+      if (has_start) {
+        fence_async_smem();                    // (the slots' next fill is a TMA write)
+        arrive(in_free);
+      }
+      if constexpr (F16) {
+        bound = warp_max(bound);
+        if (lane == 0) wmax[wi] = bound;
+        arrive(smax);
+        if (ok) ok = wwait(smax, 0);
+        bound = start_bound();
+      }
+    }
     uint32_t vm = 0;                           // max |V| of the last chunk begun (f16)
     for (int c = 0; c < nch && ok; ++c) {
       const int st = c & 1, n = min(C, end - beg - c * C);
@@ -693,12 +743,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       fence_after();
       // state: operand copy (scaled for f16), then decayed in place
       if (OUT || c > 0) {
+        if (c > 0) fix(c - 1);
         const float f = F16 ? pow2f(sa) : 1.f;
         const float ds = F16 ? pw(n) * pow2f(bnew) : pw(n);
 #pragma unroll 1
         for (int b = 0; b < HK; b += 32) {
           float x[32];
-          state32(c - 1, b, x);
+          state32(b, x);
           if (OUT && r < DV) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -760,20 +811,30 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (c + 1 < nch && !cleaning(c + 1)) { ok = false; break; }
     }
     // ---- the state after the segment
-    float* dst = OUT ? (last && a.S_out ? a.S_out + (int64_t)(tab.seq0 + s) * per + head : nullptr) : ws_state;
+    // stored through the other stage's Q and K slots (nothing is loaded any more), 32 rows a warp
+    const bool keep = OUT ? last && a.S_out != nullptr : true;
     if (ok && nch > 0) ok = wwait(ds_done, (nch - 1) & 1);
     fence_after();
-    if (ok && dst) {
+    if (ok && nch > 0) fix(nch - 1);
+    if (ok && keep) {
+      uint8_t* stage = sm + (nch & 1) * L::STAGE;
 #pragma unroll 1
       for (int b = 0; b < HK; b += 32) {
         float x[32];
-        state32(nch - 1, b, x);
-        if (r < DV) {
+        state32(b, x);
+        if (r < DV)
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(dst + (int64_t)dv * DK + half * HK + b + e) =
-                make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-        }
+          for (int e = 0; e < 8; ++e)
+            *state_at(stage, b, e) = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0 && quad * 32 < DV) {
+        for (int b = 0; b < HK; b += 32)
+          tma4_store(OUT ? &mapFin : &mapWs, stage + ((half * HK + b) >> 5) * (DV * 128) + quad * 32 * 128,
+                     half * HK + b, quad * 32, h, OUT ? tab.seq0 + s : ws_slot);
+        tma_store_commit();
+        tma_store_wait();
       }
     }
   }
@@ -959,12 +1020,12 @@ static cudaError_t lin_launch(const LinAttnArgs& a, const lin::Tab& t, int64_t s
   if (slots > 0) {
     CK_RET(cudaFuncSetAttribute(lin::chunk_kernel<T, DK, DV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 L::BYTES));
-    CK_RET(launch_pdl(lin::chunk_kernel<T, DK, DV, false>, grid, block, L::BYTES, st, t, m[0], m[1], m[2], m[3], a));
+    CK_RET(launch_pdl(lin::chunk_kernel<T, DK, DV, false>, grid, block, L::BYTES, st, t, m[0], m[1], m[2], m[3], m[4], m[5], m[6], a));
     const int64_t per4 = (int64_t)a.H * DK * DV / 4;
     CK_RET(launch_pdl(lin::scan_kernel, dim3((unsigned)((per4 + 255) / 256), t.n), dim3(256), 0, st, t, a));
   }
   CK_RET(cudaFuncSetAttribute(lin::chunk_kernel<T, DK, DV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES));
-  return launch_pdl(lin::chunk_kernel<T, DK, DV, true>, grid, block, L::BYTES, st, t, m[0], m[1], m[2], m[3], a);
+  return launch_pdl(lin::chunk_kernel<T, DK, DV, true>, grid, block, L::BYTES, st, t, m[0], m[1], m[2], m[3], m[4], m[5], m[6], a);
 }
 
 cudaError_t launch_linattn(const LinAttnArgs& a, int n_seq, const int* row0, const int* len, int num_sms,
@@ -972,7 +1033,9 @@ cudaError_t launch_linattn(const LinAttnArgs& a, int n_seq, const int* row0, con
   int64_t rows = 1;
   for (int s = 0; s < n_seq; ++s)
     if (len[s]) rows = std::max(rows, (int64_t)row0[s] + len[s]);
-  CUtensorMap m[4];                            // q, k, v, out
+  CUtensorMap m[7] = {};                       // q, k, v, out; initial states, start states, final states
+  const CUtensorMapDataType ty =
+      a.dtype == ELEM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const void* ptr[4] = {a.q, a.k, a.v, a.out};
   const int d[4] = {a.dk, a.dk, a.dv, a.dv};
   const int64_t ld[4] = {a.q_stride, a.k_stride, a.v_stride, (int64_t)a.H * a.dv};
@@ -980,15 +1043,23 @@ cudaError_t launch_linattn(const LinAttnArgs& a, int n_seq, const int* row0, con
     const uint64_t dims[3] = {(uint64_t)d[i], (uint64_t)a.H, (uint64_t)rows};
     const uint64_t str[2] = {(uint64_t)d[i] * 2, (uint64_t)ld[i] * 2};
     const uint32_t box[3] = {64, 1, i < 3 ? (uint32_t)lin::C : 32u};
-    if (!encode_tensor_map(&m[i], a.dtype == ELEM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                           3, ptr[i], dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!encode_tensor_map(&m[i], ty, 3, ptr[i], dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
+  auto state_map = [&](CUtensorMap* map, const void* base, int64_t n) {   // [n][H][dv][dk] fp32
+    const uint64_t dims[4] = {(uint64_t)a.dk, (uint64_t)a.dv, (uint64_t)a.H, (uint64_t)n};
+    const uint64_t str[3] = {(uint64_t)a.dk * 4, (uint64_t)a.dv * a.dk * 4, (uint64_t)a.H * a.dv * a.dk * 4};
+    const uint32_t box[4] = {32, 32, 1, 1};
+    return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if (a.S_in && !state_map(&m[4], a.S_in, a.s_in_stride ? n_seq : 1)) return cudaErrorInvalidValue;
+  if (a.S_out && !state_map(&m[6], a.S_out, n_seq)) return cudaErrorInvalidValue;
   lin::Tab t;
   for (int s = 0; s < n_seq;) {
     int64_t slots;
     s = lin_group(t, s, n_seq, row0, len, a.H, a.dk, a.dv, num_sms, &slots);
     if (((int64_t)t.fullcum[t.n] + t.tailcum[t.n]) * a.H > INT_MAX) return cudaErrorInvalidValue;
+    if (slots > 0 && !state_map(&m[5], a.ws, slots)) return cudaErrorInvalidValue;
 #define LIN_GO(T)                                                                                        \
   CK_RET(a.dk == 128 ? (a.dv == 128 ? lin_launch<T, 128, 128>(a, t, slots, m, st)                   \
                                     : lin_launch<T, 128, 64>(a, t, slots, m, st))                   \

@@ -38,6 +38,7 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// One poll; the hardware may suspend the thread for a while.
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -48,32 +49,28 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 // Bounded wait; false (with `code` recorded in *d_err) on expiry, or when another role gave up. The
-// timer is only read once many polls have failed: it is slow, and a wait on the critical path that
-// read it first would cost more than what it waits for.
+// timer and the flag are looked at once in 64 polls: a wait on the critical path that read them first
+// would cost more than what it waits for (a flag read in every poll: 2 to 4 % of these kernels' time).
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* d_err,
                                           int code) {
   uint64_t t0 = 0;
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try(bar, parity)) return true;
-    if ((it & 127) == 0) {
-      if (*abort_flag) return false;
+  for (uint32_t it = 1; !mbar_try(bar, parity); ++it)
+    if ((it & 63) == 0) {
       const uint64_t t = now_ns();
       if (t0 == 0) t0 = t;
-      if (t - t0 > WAIT_NS) {
+      if (*abort_flag || t - t0 > WAIT_NS) {
         *abort_flag = 1;
-        atomicExch(d_err, code);
+        if (t - t0 > WAIT_NS) *reinterpret_cast<volatile int*>(d_err) = code;
         return false;
       }
     }
-  }
+  return true;
 }
 // Bounded wait that ignores the abort flag (copies and products in flight before leaving).
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = now_ns();
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try(bar, parity)) return;
-    if ((it & 255) == 0 && now_ns() - t0 > WAIT_NS) return;
-  }
+  for (uint32_t it = 1; !mbar_try(bar, parity); ++it)
+    if ((it & 63) == 0 && now_ns() - t0 > WAIT_NS) return;
 }
 __device__ __forceinline__ void tma3(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
   asm volatile(
@@ -88,6 +85,12 @@ __device__ __forceinline__ void tma3_store(const CUtensorMap* map, const void* s
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
                "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void tma4_store(const CUtensorMap* map, const void* src, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(src))
                : "memory");
 }
 __device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
