@@ -9,26 +9,28 @@
 //
 // Both directions move every byte once and compute next to nothing: HBM bound. Eight elements a
 // thread: a 16-byte load of f16 or bf16 (two of fp32) and an 8-byte store of codes, so that both
-// sides of a warp cover whole 128-byte lines, hd / 8 threads per vector.
+// sides of a warp cover whole 128-byte lines, hd / 8 threads per vector. Large calls give a thread
+// U = 4 vectors, all loaded before the first is used: with one (8 bytes of codes in flight a thread
+// when reading back) 150001 x 8 x 64 to bf16 ran at 4.8 TB/s and 100000 x 8 x 128 from f16 at
+// 4.3 TB/s. Small calls keep one, and four times the blocks.
 #include <algorithm>
 
 #include <cuda_fp8.h>
 
+#include <string.h>
+#include <type_traits>
+
 #include "common.cuh"
+#include "tcgen05.cuh"
 
 namespace s1 {
 namespace kvc {
 
 constexpr int THREADS = 256;
 
-template <typename T>
-__device__ __forceinline__ float to_f(T x);
-template <>
-__device__ __forceinline__ float to_f<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f<f16>(f16 x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_f<bf16>(bf16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(f16 x) { return __half2float(x); }
+__device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
 
 // x rounded to T, held at its largest finite value (NaN passes through)
 template <typename T>
@@ -46,21 +48,68 @@ __device__ __forceinline__ bf16 from_f<bf16>(float x) {
   return __float2bfloat16_rn(fabsf(x) > 3.3895313892515355e38f ? copysignf(3.3895313892515355e38f, x) : x);
 }
 
-// Eight consecutive elements; VEC: the address is 16-byte aligned.
+// Eight consecutive elements of a vector, as they are in memory; VEC: the address is 16-byte aligned.
+template <typename T>
+struct Raw {
+  uint32_t w[2 * sizeof(T)];
+};
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, float* x) {
-  T t[8];
+__device__ __forceinline__ Raw<T> load8(const T* p) {
+  Raw<T> r;
   if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-      reinterpret_cast<uint4*>(t)[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+      r.w[4 * i] = v.x;
+      r.w[4 * i + 1] = v.y;
+      r.w[4 * i + 2] = v.z;
+      r.w[4 * i + 3] = v.w;
+    }
   } else {
+    T t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = p[i];
+    memcpy(&r, t, sizeof(t));
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = to_f<T>(t[i]);
+  return r;
 }
+// max |x| over the finite elements. The common case (all finite) is a maximum of bit patterns, two
+// 16-bit ones at a time; instructions, not bytes, bound the 16-bit types otherwise.
+template <typename T>
+__device__ __forceinline__ float max_finite(const Raw<T>& r) {
+  if constexpr (sizeof(T) == 4) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, r.w[i] & 0x7fffffffu);
+    if (m >= 0x7f800000u) {
+      m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t a = r.w[i] & 0x7fffffffu;
+        m = max(m, a < 0x7f800000u ? a : 0u);
+      }
+    }
+    return __uint_as_float(m);
+  } else {
+    constexpr uint32_t TOP = std::is_same<T, f16>::value ? 0x7c00u : 0x7f80u;
+    uint32_t m = t5::absmax2(T(), t5::absmax2(T(), r.w[0], r.w[1]), t5::absmax2(T(), r.w[2], r.w[3]));
+    m = max(m & 0xffffu, m >> 16);
+    if (m >= TOP) {
+      m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = r.w[i] & 0x7fffu, hi = r.w[i] >> 16 & 0x7fffu;
+        m = max(m, max(lo < TOP ? lo : 0u, hi < TOP ? hi : 0u));
+      }
+    }
+    if constexpr (std::is_same<T, f16>::value) return __half2float(__ushort_as_half((unsigned short)m));
+    else return __uint_as_float(m << 16);
+  }
+}
+// The eight codes of x * 2^-E.
+template <typename T>
+__device__ __forceinline__ uint2 codes8(const Raw<T>& r, int E);
+
 template <typename T, bool VEC>
 __device__ __forceinline__ void store8(T* p, const float* x) {
   T t[8];
@@ -86,66 +135,119 @@ __device__ __forceinline__ int scale_exp(float a) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 .. 127
 
-// grid (vectors * LPV / THREADS, 2 planes): vector i = row * Hkv + head.
-template <typename T, int HD, bool VEC>
+__device__ __forceinline__ uint2 pack_codes(const uint16_t* c) {
+  return make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
+}
+template <typename T>
+__device__ __forceinline__ uint2 codes8(const Raw<T>& r, int E) {
+  uint16_t c[4];
+  // f16: the product is exact wherever a code is not zero (a code's half step 2^-10 is a normal f16),
+  // so the codes come from f16 pairs; 2^-E is an f16 number for E from -15 to 14
+  if constexpr (std::is_same<T, f16>::value) {
+    if (E >= -15 && E <= 14) {
+      const __half2 s = __float2half2_rn(pow2(-E));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&r.w[e]), s);
+        c[e] = __nv_cvt_halfraw2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+      }
+      return pack_codes(c);
+    }
+  }
+  T t[8];
+  memcpy(t, &r, sizeof(t));
+  const float inv = pow2(-E);                // 2^-120 .. 2^126
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    c[e] = __nv_cvt_float2_to_fp8x2(make_float2(to_f(t[2 * e]) * inv, to_f(t[2 * e + 1]) * inv), __NV_SATFINITE,
+                                    __NV_E4M3);
+  return pack_codes(c);
+}
+
+// Rows and heads of vectors i0, i0 + PER, ...: one division.
+template <int PER, int U>
+__device__ __forceinline__ void vectors(uint32_t i0, uint32_t Hkv, uint32_t* row, uint32_t* h) {
+  row[0] = i0 / Hkv;
+  h[0] = i0 - row[0] * Hkv;
+  if constexpr (U > 1) {
+    const uint32_t dr = PER / Hkv, dh = PER - dr * Hkv;
+#pragma unroll
+    for (int u = 1; u < U; ++u) {
+      const uint32_t x = h[u - 1] + dh;
+      const bool wrap = x >= Hkv;
+      h[u] = wrap ? x - Hkv : x;
+      row[u] = row[u - 1] + dr + (wrap ? 1u : 0u);
+    }
+  }
+}
+
+// grid (vectors * LPV / THREADS / U, 2 planes): vector i = row * Hkv + head.
+template <typename T, int HD, bool VEC, int U>
 __global__ void __launch_bounds__(THREADS)
     quant_kernel(const T* k, const T* v, int64_t k_stride, int64_t v_stride, uint32_t n_vec, int Hkv, uint8_t* codes,
                  float* scales, int cap, int pos0) {
-  constexpr int LPV = HD / 8;
+  constexpr int LPV = HD / 8, PER = THREADS / LPV;
   allow_dependents();
   wait_prerequisites();
-  const uint32_t i = blockIdx.x * (THREADS / LPV) + threadIdx.x / LPV;
-  const int l = threadIdx.x % LPV;
-  const bool live = i < n_vec;               // (shuffles below take whole warps)
-  const uint32_t row = live ? i / (uint32_t)Hkv : 0, h = live ? i % (uint32_t)Hkv : 0;
-  const int plane = blockIdx.y;
-  const T* src = plane ? v + (int64_t)row * v_stride : k + (int64_t)row * k_stride;
-  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (live) load8<T, VEC>(src + (int64_t)h * HD + l * 8, x);
-  float a = 0.f;
+  const int l = threadIdx.x % LPV, plane = blockIdx.y;
+  const uint32_t i0 = blockIdx.x * (PER * U) + threadIdx.x / LPV;
+  uint32_t row[U], h[U];
+  vectors<PER, U>(i0, (uint32_t)Hkv, row, h);
+  Raw<T> x[U];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) a = fmaxf(a, isfinite(x[e]) ? fabsf(x[e]) : 0.f);
+  for (int u = 0; u < U; ++u) {              // (threads past the end take part in the shuffles with zeros)
+    x[u] = Raw<T>{};
+    const T* src = plane ? v + (int64_t)row[u] * v_stride : k + (int64_t)row[u] * k_stride;
+    if (i0 + u * PER < n_vec) x[u] = load8<T, VEC>(src + h[u] * HD + l * 8);
+  }
 #pragma unroll
-  for (int o = LPV / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-  if (!live) return;
-  const int E = scale_exp(a);
-  const float inv = pow2(-E);                // -120 .. 126
-  uint16_t c[4];
+  for (int u = 0; u < U; ++u) {
+    float a = max_finite(x[u]);
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    c[e] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * e] * inv, x[2 * e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-  const int64_t crow = (int64_t)plane * cap + pos0 + row;
-  *reinterpret_cast<uint2*>(codes + (crow * Hkv + h) * HD + l * 8) =
-      make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
-  if (l == 0) scales[((int64_t)plane * Hkv + h) * cap + pos0 + row] = pow2(E);
+    for (int o = LPV / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    if (i0 + u * PER >= n_vec) continue;
+    const int E = scale_exp(a);
+    const int64_t crow = (int64_t)plane * cap + pos0 + row[u];
+    *reinterpret_cast<uint2*>(codes + (crow * Hkv + h[u]) * HD + l * 8) = codes8(x[u], E);
+    if (l == 0) scales[((int64_t)plane * Hkv + h[u]) * cap + pos0 + row[u]] = pow2(E);
+  }
 }
 
-template <typename T, int HD, bool VEC>
+template <typename T, int HD, bool VEC, int U>
 __global__ void __launch_bounds__(THREADS)
     dequant_kernel(const uint8_t* codes, const float* scales, int cap, int pos0, uint32_t n_vec, int Hkv, T* k, T* v,
                    int64_t k_stride, int64_t v_stride) {
-  constexpr int LPV = HD / 8;
+  constexpr int LPV = HD / 8, PER = THREADS / LPV;
   allow_dependents();
   wait_prerequisites();
-  const uint32_t i = blockIdx.x * (THREADS / LPV) + threadIdx.x / LPV;
-  const int l = threadIdx.x % LPV;
-  if (i >= n_vec) return;
-  const uint32_t row = i / (uint32_t)Hkv, h = i % (uint32_t)Hkv;
-  const int plane = blockIdx.y;
-  const int64_t crow = (int64_t)plane * cap + pos0 + row;
-  const uint2 c = __ldcs(reinterpret_cast<const uint2*>(codes + (crow * Hkv + h) * HD + l * 8));
-  const float s = scales[((int64_t)plane * Hkv + h) * cap + pos0 + row];
-  float x[8];
+  const int l = threadIdx.x % LPV, plane = blockIdx.y;
+  const uint32_t i0 = blockIdx.x * (PER * U) + threadIdx.x / LPV;
+  uint32_t row[U], h[U];
+  vectors<PER, U>(i0, (uint32_t)Hkv, row, h);
+  uint2 c[U];
+  float s[U];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t w = e < 2 ? c.x : c.y;
-    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * (e & 1))), __NV_E4M3);
-    const float2 f = __half22float2(__half2(r));
-    x[2 * e] = f.x * s;
-    x[2 * e + 1] = f.y * s;
+  for (int u = 0; u < U; ++u) {
+    if (i0 + u * PER >= n_vec) continue;
+    const int64_t crow = (int64_t)plane * cap + pos0 + row[u];
+    c[u] = __ldcs(reinterpret_cast<const uint2*>(codes + (crow * Hkv + h[u]) * HD + l * 8));
+    s[u] = scales[((int64_t)plane * Hkv + h[u]) * cap + pos0 + row[u]];
   }
-  T* dst = plane ? v + (int64_t)row * v_stride : k + (int64_t)row * k_stride;
-  store8<T, VEC>(dst + (int64_t)h * HD + l * 8, x);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (i0 + u * PER >= n_vec) continue;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t w = e < 2 ? c[u].x : c[u].y;
+      const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * (e & 1))), __NV_E4M3);
+      const float2 f = __half22float2(__half2(r));
+      x[2 * e] = f.x * s[u];
+      x[2 * e + 1] = f.y * s[u];
+    }
+    T* dst = plane ? v + (int64_t)row[u] * v_stride : k + (int64_t)row[u] * k_stride;
+    store8<T, VEC>(dst + h[u] * HD + l * 8, x);
+  }
 }
 
 // Rows whose every vector starts on a 16-byte boundary.
@@ -155,6 +257,8 @@ inline bool rows_aligned(const void* k, const void* v, int64_t ks, int64_t vs, i
 
 // Vectors of one launch: 32-bit indices, grid.x well below its limit.
 constexpr int64_t MAX_VEC = 1 << 28;
+// Threads from which a call is large: about twice what the GPU holds at once.
+constexpr int64_t LARGE = 2ll * 152 * 2048;
 
 }  // namespace kvc
 
@@ -165,8 +269,10 @@ static cudaError_t quant_t(const T* k, const T* v, int64_t ks, int64_t vs, int r
   const int step = (int)std::max<int64_t>(1, kvc::MAX_VEC / Hkv);
   for (int r = 0; r < rows; r += std::min(step, rows - r)) {
     const uint32_t n_vec = (uint32_t)((int64_t)std::min(step, rows - r) * Hkv);
-    CK_RET(launch_pdl(kvc::quant_kernel<T, HD, VEC>, dim3((n_vec + per - 1) / per, 2), dim3(kvc::THREADS), 0, st,
-                      k + (int64_t)r * ks, v + (int64_t)r * vs, ks, vs, n_vec, Hkv, codes, scales, cap, pos0 + r));
+    const bool large = 2ll * n_vec * (HD / 8) >= kvc::LARGE;
+    const uint32_t bl = large ? 4 * per : per;
+    CK_RET(launch_pdl(large ? kvc::quant_kernel<T, HD, VEC, 4> : kvc::quant_kernel<T, HD, VEC, 1>,
+                      dim3((n_vec + bl - 1) / bl, 2), dim3(kvc::THREADS), 0, st, k + (int64_t)r * ks, v + (int64_t)r * vs, ks, vs, n_vec, Hkv, codes, scales, cap, pos0 + r));
   }
   return cudaSuccess;
 }
@@ -177,8 +283,10 @@ static cudaError_t dequant_t(const uint8_t* codes, const float* scales, int cap,
   const int step = (int)std::max<int64_t>(1, kvc::MAX_VEC / Hkv);
   for (int r = 0; r < rows; r += std::min(step, rows - r)) {
     const uint32_t n_vec = (uint32_t)((int64_t)std::min(step, rows - r) * Hkv);
-    CK_RET(launch_pdl(kvc::dequant_kernel<T, HD, VEC>, dim3((n_vec + per - 1) / per, 2), dim3(kvc::THREADS), 0, st,
-                      codes, scales, cap, pos0 + r, n_vec, Hkv, k + (int64_t)r * ks, v + (int64_t)r * vs, ks, vs));
+    const bool large = 2ll * n_vec * (HD / 8) >= kvc::LARGE;
+    const uint32_t bl = large ? 4 * per : per;
+    CK_RET(launch_pdl(large ? kvc::dequant_kernel<T, HD, VEC, 4> : kvc::dequant_kernel<T, HD, VEC, 1>,
+                      dim3((n_vec + bl - 1) / bl, 2), dim3(kvc::THREADS), 0, st, codes, scales, cap, pos0 + r, n_vec, Hkv, k + (int64_t)r * ks, v + (int64_t)r * vs, ks, vs));
   }
   return cudaSuccess;
 }
