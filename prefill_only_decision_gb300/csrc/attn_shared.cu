@@ -13,16 +13,21 @@
 // query tile of an odd count, one query tile over the even and the odd key tiles (joined at the
 // end). Work items are (kv head, pair of query tiles); an item's key tiles are split over `ns`
 // CTAs when that shortens the call, and combine_kernel joins their (o, m, l) in part order (no
-// atomics: the same bits every time). One CTA per SM, 15 warps:
+// atomics: the same bits every time). One CTA per SM, 15 warps (19 with an e4m3 prefix):
 //   warp 0      TMA producer: prefix tiles (f16 tiles, or e4m3 tiles into a ring of raw stages)
-//   warps 1, 14 MMA issue of stream 0 and 1 (a stream's products wait for its own softmax only)
+//   warps 1, 14 MMA issue of stream 0 and 1. With two query tiles they take turns, a stream's P V and
+//               next S = Q K^T at a time: issued side by side the products share the tensor cores, both
+//               streams get them late, and their softmaxes then run at the same time with the tensor
+//               cores idle (16 q heads, 1340 rows over 65536: 606 us, by turns 575 us)
 //   warps 2-5, 6-9  softmax of stream 0, 1: one thread per row (TMEM lane). Running max with a lazy
 //               rescale (O and l move only when the row's maximum grows by more than 2^8). P (f16)
-//               goes back into the second half of the TMEM columns of S and is the A operand of
+//               goes back into the TMEM columns of S and is the A operand of
 //               O += P V from there: no shared-memory round trip. Warps whose 32 rows are all past
 //               the tile's last row only keep the barriers going.
 //   warps 10-13 loaders: the batch's own keys (gathered row by row through the sequence table), and
-//               e4m3 prefix tiles: codes from the raw stage to f16 in the MMA's swizzled layout
+//               e4m3 prefix tiles: codes from the raw stage to f16 in the MMA's swizzled layout. With
+//               an e4m3 prefix they take the K tiles and warps 15-18 the V tiles: four warps alone
+//               (2050 cycles a tile) held a CTA to 15 GB/s of codes, half its share of the HBM rate
 // K and V tiles share one ring of stages in the order the products take them.
 // Own keys are packed the same way as queries: row r's visible own keys are the packed rows
 // start(r) .. r, so one masked tile serves many short sequences. A masked weight is an exact zero,
@@ -45,7 +50,7 @@ namespace sha {
 using namespace t5;
 
 constexpr int BQ = 128, BKV = 128;
-constexpr int NTHREADS = 15 * 32;
+constexpr int threads_of(bool e4m3) { return (e4m3 ? 19 : 15) * 32; }
 constexpr int TMEM_COLS = 512;               // S of stream x at 128 x, O at 256 + 128 x
 constexpr int T_O = 256;
 constexpr int ERR_TIMEOUT = 0x401;
@@ -79,7 +84,7 @@ struct Lay {
   static constexpr int TAB = SC + (E4M3 ? RS * BKV * 4 : 0);       // a copy of a small sequence table
   static constexpr int BAR = TAB + (2 * SEQ_TAB_SMALL + 2) * 4;
   static constexpr int NS = 2 * FR > F ? 2 * FR : F;
-  static constexpr int NBAR = 1 + 2 * NS + 6 + 2 + 4 + (E4M3 ? 2 * RS : 0);
+  static constexpr int NBAR = 1 + 2 * NS + 6 + 2 + 2 + 4 + (E4M3 ? 2 * RS : 0);
   static constexpr int USED = BAR + NBAR * 8 + 16;
   static_assert(USED <= 227 * 1024, "shared memory of one CTA");
   // above half an SM: each CTA allocates all of TMEM, so two never share one
@@ -140,18 +145,18 @@ __device__ __forceinline__ uint32_t drop_nonfinite2(uint32_t h2) {
   return h2;
 }
 
-// Sixteen e4m3 codes times scale to f16 (round to nearest even, held at +-65504). FAST: the scale
+// Eight e4m3 codes times scale to f16 (round to nearest even, held at +-65504). FAST: the scale
 // is an f16 value of at most 2^7, so the f16 product is the rounded value and cannot overflow.
 template <bool FAST>
-__device__ __forceinline__ void codes_to_half(const uint4 c, float scale, uint32_t* h) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  const __half2 s2 = __float2half2_rn(scale);
+__device__ __forceinline__ uint4 codes_to_half(const uint2 c, float scale) {
+  const uint32_t w[2] = {c.x, c.y};
+  uint32_t h[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const __half2 x = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3));
     __half2 y;
     if constexpr (FAST) {
-      y = __hmul2(x, s2);
+      y = __hmul2(x, __float2half2_rn(scale));
     } else {
       const float2 f = __half22float2(x);
       const float a = f.x * scale, b = f.y * scale;
@@ -160,10 +165,11 @@ __device__ __forceinline__ void codes_to_half(const uint4 c, float scale, uint32
     }
     h[i] = *reinterpret_cast<const uint32_t*>(&y);
   }
+  return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
 template <int HD, bool E4M3, int N>
-__global__ void __launch_bounds__(NTHREADS, 1)
+__global__ void __launch_bounds__(threads_of(E4M3), 1)
     shared_kernel(const __grid_constant__ SeqTab<N> table, const __grid_constant__ CUtensorMap mapKV,
                   const __grid_constant__ SharedAttnArgs a, const Plan pl) {
   using L = Lay<HD, E4M3>;
@@ -177,7 +183,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* p_full = s_full + 2;               // [2]
   uint64_t* o_done = p_full + 2;               // [2] the stream's last product has completed
   uint64_t* mma_idle = o_done + 2;             // [2]
-  uint64_t* joined = mma_idle + 2;             // [4 quadrants] stream 1's sums are published
+  uint64_t* turn = mma_idle + 2;               // [2] the stream may issue its products (two query tiles)
+  uint64_t* joined = turn + 2;                 // [4 quadrants] stream 1's sums are published
   uint64_t* raw_full = joined + 4;             // [RS] (e4m3)
   uint64_t* raw_empty = raw_full + RS;         // [RS]
   uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
@@ -199,6 +206,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&mma_idle[x], 1);
+      mbar_init(&turn[x], 1);
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 4);
       mbar_init(&o_done[x], 1);
@@ -207,7 +215,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if constexpr (E4M3)
       for (int r = 0; r < RS; ++r) {
         mbar_init(&raw_full[r], 1 + 32);       // the tile's copy, and each producer lane's scales
-        mbar_init(&raw_empty[r], 4);
+        mbar_init(&raw_empty[r], 8);           // every loader warp has seen it, and its own have taken it
       }
     *abort_flag = 0;
     *v_flag = 0;
@@ -296,30 +304,38 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int x = warp == 1 ? 0 : 1;
     const bool leader = elect_one();
     constexpr uint32_t ID_S = idesc_f16(BKV, 0, 0, 0), ID_O = idesc_f16(HD, 0, 0, 1);
-    const uint32_t tS = tmem + x * 128, tP = tS + 64, tO = tmem + T_O + x * 128;
+    const uint32_t tS = tmem + x * 128, tO = tmem + T_O + x * 128;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_err, ERR_TIMEOUT) ? 1 : 0) != 0;
     };
     const uint64_t qd = desc_sw128(smem_u32(sm + L::Q) + (two && x ? BQ * HD * 2 : 0), 16);
     int done = 0;                              // products P V issued
+    int group = 0;                             // turns taken
+    auto take_turn = [&]() { return !two || wait(&turn[x], (x ? group : group - 1) & 1); };
+    auto pass_turn = [&]() {
+      if (two && leader) mbar_arrive(&turn[x ^ 1]);
+      ++group;
+    };
     if (n > 0 && wait(q_full, 0))
       for_ring<F, FR>(n, two, [&](int s, int ph, bool is_v, int t) {
         if (!two && (t & 1) != x) return true;           // the other stream's tile
         if (!wait(&full[s], ph)) return false;
         const uint32_t addr = smem_u32(kvst + s * L::TILE);
         if (is_v) {
-          if (!wait(&p_full[x], done & 1)) return false;
+          if (!wait(&p_full[x], done & 1) || !take_turn()) return false;
           fence_after();
           if (leader) {                        // O += P V
             const uint64_t vd = desc_sw128(addr, BKV * 128);
 #pragma unroll
             for (int kk = 0; kk < BKV / 16; ++kk)
-              mma_ts(tO, tP + kk * 8, vd + (uint64_t)(kk * 16 * 128 >> 4), ID_O, (done > 0 || kk > 0) ? 1u : 0u);
+              mma_ts(tO, tS + kk * 8, vd + (uint64_t)(kk * 16 * 128 >> 4), ID_O, (done > 0 || kk > 0) ? 1u : 0u);
             if (t + (two ? 1 : 2) >= n) commit(&o_done[x]);
             commit(&empty[s]);
           }
           ++done;
+          if (two && t + 1 >= n) pass_turn();
         } else {
+          if (t == 0 && !take_turn()) return false;
           fence_after();
           if (leader) {                        // S = Q K^T
             const uint64_t kd = desc_sw128(addr, 16);
@@ -331,6 +347,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             commit(&s_full[x]);
             commit(&empty[s]);
           }
+          if (two) pass_turn();
         }
         __syncwarp();
         return true;
@@ -339,9 +356,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       commit(&mma_idle[x]);
       mbar_drain(&mma_idle[x], 0);             // every MMA issued above has completed
     }
-  } else if (warp >= 10) {
+  } else if (warp >= 10 && warp != 14) {
     // ---- loaders: rows 32 lw .. +31 of every tile
-    const int lw = warp - 10;
+    const int lw = warp < 14 ? warp - 10 : warp - 15, plane = warp < 14 ? 0 : 1;   // (f16 prefix: both planes)
     auto wwait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_err, ERR_TIMEOUT) ? 1 : 0) != 0;
     };
@@ -381,32 +398,40 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const uint32_t ph = fill_ph ^ 1;
       uint8_t* dst = kvst + s * L::TILE;
       if (j >= pl.ncache) {
+        if (E4M3 && is_v != (plane == 1)) return true;
         if (!wwait(&empty[s], ph)) return false;
         load_own(j - pl.ncache, is_v ? a.vn : a.kn, dst, is_v);
       } else if constexpr (E4M3) {
+        // every loader warp looks at every raw tile (a parity wait must see each phase), its plane's
+        // warps convert it
         const int r = raw % RS;
-        if (!wwait(&raw_full[r], (raw / RS) & 1) || !wwait(&empty[s], ph)) return false;
+        if (!wwait(&raw_full[r], (raw / RS) & 1)) return false;
+        ++raw;
+        if (is_v != (plane == 1)) {
+          if (lane == 0) mbar_arrive(&raw_empty[r]);
+          return true;
+        }
+        if (!wwait(&empty[s], ph)) return false;
         const float sc = reinterpret_cast<const float*>(sm + L::SC)[r * BKV + lw * 32 + lane];   // this lane's row
         const bool fast = __all_sync(0xffffffffu, sc <= 128.f && __half2float(__float2half_rn(sc)) == sc);
-        // LPR lanes of 16 codes per row; the lanes of a row's second 64 columns write their two
-        // 16-byte chunks in the other order, so that no store conflicts
+        // LPR lanes of 16 codes per row, RP rows a pass; the lanes of a row's second 64 columns take
+        // their two 8-code halves in the other order, so that no store conflicts
         constexpr int LPR = HD / 16, RP = 32 / LPR;
-        const int ci = lane % LPR;
-        const uint8_t* rp = sm + L::R + r * L::RAW + (lw * 32) * HD + lane * 16;
+        const int ci = lane % LPR, sw = HD == 128 && ci >= 4 ? 1 : 0;
+        const uint8_t* src = sm + L::R + r * L::RAW + (lw * 32) * HD + lane * 16;
+        uint8_t* d = dst + (ci >> 2) * (BKV * 128) + (lw * 32 + lane / LPR) * 128;
+        const int c0 = ((2 * ci) & 7) + sw, c1 = ((2 * ci) & 7) + 1 - sw;
         auto convert = [&](auto is_fast, int p) {
-          const int lr = p * RP + lane / LPR, row = lw * 32 + lr;
-          const uint4 c = *reinterpret_cast<const uint4*>(rp + p * RP * HD);
-          uint32_t h[8];
-          codes_to_half<decltype(is_fast)::value>(c, __shfl_sync(0xffffffffu, sc, lr), h);
-          const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-          const bool swap = HD == 128 && ci >= 4;
-          uint8_t* d = dst + (ci >> 2) * (BKV * 128) + row * 128;
-          const int c0 = (2 * ci) & 7;
-          *reinterpret_cast<uint4*>(d + (((c0 + (swap ? 1 : 0)) ^ (row & 7)) << 4)) = swap ? hi : lo;
-          *reinterpret_cast<uint4*>(d + (((c0 + (swap ? 0 : 1)) ^ (row & 7)) << 4)) = swap ? lo : hi;
+          constexpr bool FAST = decltype(is_fast)::value;
+          const float rs = __shfl_sync(0xffffffffu, sc, p * RP + lane / LPR);
+          const int x = (p * RP + lane / LPR) & 7;
+          const uint2 a0 = *reinterpret_cast<const uint2*>(src + p * RP * HD + sw * 8);
+          const uint2 a1 = *reinterpret_cast<const uint2*>(src + p * RP * HD + 8 - sw * 8);
+          *reinterpret_cast<uint4*>(d + p * RP * 128 + ((c0 ^ x) << 4)) = codes_to_half<FAST>(a0, rs);
+          *reinterpret_cast<uint4*>(d + p * RP * 128 + ((c1 ^ x) << 4)) = codes_to_half<FAST>(a1, rs);
         };
         if (fast) {
-#pragma unroll 4
+#pragma unroll
           for (int p = 0; p < 32 / RP; ++p) convert(std::true_type{}, p);
         } else {
 #pragma unroll 1
@@ -414,7 +439,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&raw_empty[r]);
-        ++raw;
       } else {
         if (!wwait(&empty[s], ph)) return false;   // the producer's tile: only the arrival
       }
@@ -510,78 +534,60 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         st_wait();
       }
-      // the first half of the scores is read for the maximum now and again for the weights later,
-      // the second half stays in registers: P takes over its columns
-      {
-        uint32_t u[64];
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto maximum = [&](const uint32_t* w) {
-#pragma unroll
-          for (int c = 0; c < 32; c += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx4[e] = fmaxf(mx4[e], fmaxf(__uint_as_float(w[c + e]), __uint_as_float(w[c + 4 + e])));
-        };
-        tld32(tS, u);
-        tld32(tS + 32, u + 32);
-        ld_wait();
-        pin32(u);
-        pin32(u + 32);
-        maximum(u);
-        maximum(u + 32);
-        tld32(tS + 64, u);
-        tld32(tS + 96, u + 32);
-        ld_wait();
-        pin32(u);
-        pin32(u + 32);
-        maximum(u);
-        maximum(u + 32);
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
-        float alpha = 1.f;
-        if (mx > m + 8.f) {
-          alpha = m == -INFINITY ? 1.f : ex2(m - mx);
-          m = mx;
-        }
-        const float base = m == -INFINITY ? 0.f : m;
-        if (li > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {   // (S of this tile came after the last P V)
-          uint32_t w[32];
+      // scores are read 32 at a time, once for the maximum and once for the weights, which take over the
+      // columns of scores already used (16 for 32)
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-          for (int c = 0; c < HD; c += 32) {
-            tld32(tO + c, w);
-            ld_wait();
-            pin32(w);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
-            tst32(tO + c, w);
-          }
-          l2 = pack2(lo2(l2) * alpha, hi2(l2) * alpha);
-        }
-        const uint64_t nb = pack2(-base, -base);
-        auto weights = [&](const uint32_t* w, uint32_t* pk) {    // 32 scores -> 16 f16 pairs
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const uint64_t z = fma2((uint64_t)w[c + 1] << 32 | w[c], sl2_2, nb);
-            const float p0 = ex2(lo2(z)), p1 = ex2(hi2(z));
-            l2 = add2(l2, pack2(p0, p1));
-            pk[c / 2] = h2u(p0, p1);
-          }
-        };
-        // (chunk k's weights take columns 64 + 16 k: over scores already in registers)
-        uint32_t pk[16];
-        weights(u, pk);
-        tst16(tS + 96, pk);
-        tld32(tS, u);
-        weights(u + 32, pk);
-        tst16(tS + 112, pk);
+      for (int c = 0; c < BKV; c += 64) {
+        uint32_t u[64];
+        tld32(tS + c, u);
+        tld32(tS + c + 32, u + 32);
         ld_wait();
         pin32(u);
-        tld32(tS + 32, u + 32);
-        weights(u, pk);
-        tst16(tS + 64, pk);
-        ld_wait();
         pin32(u + 32);
-        weights(u + 32, pk);
-        tst16(tS + 80, pk);
+#pragma unroll
+        for (int k = 0; k < 64; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx4[e] = fmaxf(mx4[e], fmaxf(__uint_as_float(u[k + e]), __uint_as_float(u[k + 4 + e])));
+      }
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
+      float alpha = 1.f;
+      if (mx > m + 8.f) {
+        alpha = m == -INFINITY ? 1.f : ex2(m - mx);
+        m = mx;
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+      if (li > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {   // (S of this tile came after the last P V)
+        uint32_t w[32];
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+          tld32(tO + c, w);
+          ld_wait();
+          pin32(w);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
+          tst32(tO + c, w);
+        }
+        l2 = mul2(l2, pack2(alpha, alpha));
+      }
+      const uint64_t nb = pack2(-base, -base);
+      uint32_t u[32];
+      tld32(tS, u);
+#pragma unroll 1
+      for (int c = 0; c < BKV; c += 32) {
+        uint32_t pk[16];
+        ld_wait();
+        pin32(u);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const uint64_t z = fma2(pack2u(u[e], u[e + 1]), sl2_2, nb);
+          const float p0 = ex2(lo2(z)), p1 = ex2(hi2(z));
+          l2 = add2(l2, pack2(p0, p1));
+          pk[e / 2] = h2u(p0, p1);
+        }
+        if (c + 32 < BKV) tld32(tS + c + 32, u);
+        tst16(tS + c / 2, pk);
       }
       st_wait();
       fence_before();
@@ -807,7 +813,7 @@ cudaError_t launch_group(const SharedAttnArgs& a, const SeqTab<N>& tab, const Pl
                          cudaStream_t st) {
   using L = Lay<HD, E4M3>;
   CK_RET(cudaFuncSetAttribute(shared_kernel<HD, E4M3, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES));
-  CK_RET(launch_pdl(shared_kernel<HD, E4M3, N>, dim3((unsigned)((int64_t)pl.MP * a.Hkv * pl.ns)), dim3(NTHREADS),
+  CK_RET(launch_pdl(shared_kernel<HD, E4M3, N>, dim3((unsigned)((int64_t)pl.MP * a.Hkv * pl.ns)), dim3(threads_of(E4M3)),
                     L::BYTES, st, tab, map, a, pl));
   if (pl.ns > 1) {
     CK_RET(launch_pdl(combine_kernel<HD, N>, dim3((unsigned)((int64_t)pl.MT * a.Hkv * (HD / 4))), dim3(CTHREADS), 0, st,
