@@ -60,37 +60,33 @@ __device__ int g_err;                        // bounded waits record here (one w
 struct Plan {
   int V;          // packed query rows
   int G, RT, MT;  // q heads per kv head, query rows per tile, tiles
-  int MP;         // pairs of tiles: work items per kv head
-  int nt;         // tiles per item (1 or 2)
+  int MP;         // work items per kv head: tiles or pairs of tiles
+  int nt;         // tiles per item (1 or 2; the last item of an odd count has one)
   int ns;         // key parts per item
   int ncache;     // prefix tiles
 };
 
-// Shared memory: Q tiles, stages of f16 K or V tiles, raw e4m3 stages. Two query tiles: F stages that
-// both streams read; one query tile: its Q and a ring of FR stages for each stream (227 KB at hd 128:
-// 2 x 32 + 5 x 32, or 1 x 32 + 6 x 32; with raw stages 64 + 3 x 32 + 64, or 32 + 4 x 32 + 64).
-template <int HD, bool E4M3>
+// Shared memory: Q tiles, then stages of f16 K or V tiles. Two query tiles: F stages that both streams
+// read; one query tile: its Q and a ring of FR stages for each stream (227 KB at hd 128: 2 x 32 + 5 x 32,
+// or 1 x 32 + 6 x 32).
+template <int HD>
 struct Lay {
   static constexpr int TILE = BKV * HD * 2;
-  static constexpr int RAW = BKV * HD;
-  static constexpr int F = HD == 128 ? (E4M3 ? 3 : 5) : (E4M3 ? 5 : 7);
+  static constexpr int F = HD == 128 ? 5 : 7;
   static constexpr int FR = (F + 1) / 2;
-  static constexpr int RS = E4M3 ? (HD == 128 ? 4 : 6) : 1;
   static constexpr int Q = 0;                             // per tile HD/64 boxes of [128 rows][128 B]
   static constexpr int KV2 = Q + 2 * BQ * HD * 2;         // stages with two query tiles
   static constexpr int KV1 = Q + BQ * HD * 2;             // with one
-  static constexpr int R = KV2 + F * TILE;
-  static constexpr int SC = R + (E4M3 ? RS * RAW : 0);    // raw tiles' scales [RS][BKV]
-  static constexpr int TAB = SC + (E4M3 ? RS * BKV * 4 : 0);       // a copy of a small sequence table
+  static constexpr int TAB = KV2 + F * TILE;              // a copy of a small sequence table
   static constexpr int BAR = TAB + (2 * SEQ_TAB_SMALL + 2) * 4;
   static constexpr int NS = 2 * FR > F ? 2 * FR : F;
-  static constexpr int NBAR = 1 + 2 * NS + 6 + 2 + 2 + 4 + (E4M3 ? 2 * RS : 0);
+  static constexpr int NBAR = 1 + 2 * NS + 12 + 2 + 2 + 4;
   static constexpr int USED = BAR + NBAR * 8 + 16;
   static_assert(USED <= 227 * 1024, "shared memory of one CTA");
   // above half an SM: each CTA allocates all of TMEM, so two never share one
   static constexpr int BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
   static constexpr int OSTR = HD + 4;                     // floats per row of a stream's published sums
-  static_assert(KV1 + 2 * FR * TILE <= R, "both rings fit");
+  static_assert(KV1 + 2 * FR * TILE <= TAB, "both rings fit");
   static_assert(BQ * OSTR * 4 <= 2 * FR * TILE, "published sums fit the K/V stages");
 };
 
@@ -172,21 +168,19 @@ template <int HD, bool E4M3, int N>
 __global__ void __launch_bounds__(threads_of(E4M3), 1)
     shared_kernel(const __grid_constant__ SeqTab<N> table, const __grid_constant__ CUtensorMap mapKV,
                   const __grid_constant__ SharedAttnArgs a, const Plan pl) {
-  using L = Lay<HD, E4M3>;
-  constexpr int NB = HD / 64, F = L::F, FR = L::FR, NS = L::NS, RS = L::RS;
+  using L = Lay<HD>;
+  constexpr int NB = HD / 64, F = L::F, FR = L::FR, NS = L::NS;
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* bars = (uint64_t*)(sm + L::BAR);
   uint64_t* q_full = bars;
   uint64_t* full = bars + 1;                   // [NS]
   uint64_t* empty = full + NS;                 // [NS]
-  uint64_t* s_full = empty + NS;               // [2] by stream
-  uint64_t* p_full = s_full + 2;               // [2]
-  uint64_t* o_done = p_full + 2;               // [2] the stream's last product has completed
+  uint64_t* s_full = empty + NS;               // [2 streams][2 halves of the key tile]
+  uint64_t* p_full = s_full + 4;               // [2][2]
+  uint64_t* o_step = p_full + 4;               // [2][2] the half's P V has completed
+  uint64_t* o_done = o_step + 4;               // [2] the stream's last product has completed
   uint64_t* mma_idle = o_done + 2;             // [2]
-  uint64_t* turn = mma_idle + 2;               // [2] the stream may issue its products (two query tiles)
-  uint64_t* joined = turn + 2;                 // [4 quadrants] stream 1's sums are published
-  uint64_t* raw_full = joined + 4;             // [RS] (e4m3)
-  uint64_t* raw_empty = raw_full + RS;         // [RS]
+  uint64_t* joined = mma_idle + 2;                 // [4 quadrants] stream 1's sums are published
   uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // some own V element of this CTA is not finite
@@ -194,10 +188,12 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const int part = (int)(blockIdx.x % pl.ns), item = (int)(blockIdx.x / pl.ns);
   const int mp = item % pl.MP, g = item / pl.MP;
-  const bool two = 2 * mp + 1 < pl.MT;         // two query tiles; else one over alternate key tiles
-  const int v0 = 2 * mp * pl.RT;               // first packed row of the item, and one past its last
+  const bool two = pl.nt == 2 && 2 * mp + 1 < pl.MT;         // two query tiles; else one over alternate key tiles
+  const int v0 = pl.nt * mp * pl.RT;               // first packed row of the item, and one past its last
   const int v1 = min(pl.V, v0 + (two ? 2 : 1) * pl.RT);
 
+  // quadrants of 32 matrix rows that stream x's query tile fills (a single tile: both streams')
+  auto quads = [&](int x) { return (min(pl.RT, pl.V - (v0 + (two && x ? pl.RT : 0))) * pl.G + 31) / 32; };
   if (threadIdx.x == 0) {
     mbar_init(q_full, 8);
     for (int s = 0; s < NS; ++s) {
@@ -206,17 +202,14 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&mma_idle[x], 1);
-      mbar_init(&turn[x], 1);
-      mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&s_full[2 * x + h], 1);
+        mbar_init(&p_full[2 * x + h], quads(x));
+        mbar_init(&o_step[2 * x + h], 1);
+      }
       mbar_init(&o_done[x], 1);
     }
     for (int x = 0; x < 4; ++x) mbar_init(&joined[x], 1);
-    if constexpr (E4M3)
-      for (int r = 0; r < RS; ++r) {
-        mbar_init(&raw_full[r], 1 + 32);       // the tile's copy, and each producer lane's scales
-        mbar_init(&raw_empty[r], 8);           // every loader warp has seen it, and its own have taken it
-      }
     *abort_flag = 0;
     *v_flag = 0;
     mbar_init_fence();
@@ -249,36 +242,10 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
   uint8_t* kvst = sm + (two ? L::KV2 : L::KV1);
 
   if (warp == 0) {
-    // ---- TMA producer (e4m3: lane 0 the tiles, every lane four of a tile's scales)
+    // ---- TMA producer: prefix tiles of an f16 snapshot
     wait_prerequisites();
-    if (E4M3 || lane == 0) {
-      if constexpr (E4M3) {                    // raw items: the ring's prefix tiles in its order
-        int issued = 0;
-        for_ring<F, FR>(n, two, [&](int, int, bool is_v, int t) {
-          if (jb + t >= pl.ncache) return true;
-          const int r = issued % RS;
-          if (!__all_sync(0xffffffffu, mbar_wait(&raw_empty[r], ((issued / RS) & 1) ^ 1, abort_flag, &g_err,
-                                                 ERR_TIMEOUT) ? 1 : 0))
-            return false;
-          const int key0 = (jb + t) * BKV;
-          if (lane == 0) {
-            mbar_expect_tx(&raw_full[r], L::RAW);
-            tma4(sm + L::R + r * L::RAW, &mapKV, &raw_full[r], 0, g, key0, is_v ? 1 : 0);
-          }
-          float* sc = reinterpret_cast<float*>(sm + L::SC) + r * BKV;
-          const float* src = a.scales + ((int64_t)(is_v ? a.Hkv : 0) + g) * a.cap;
-#pragma unroll
-          for (int k = lane; k < BKV; k += 32) {
-            const bool in = key0 + k < a.P;    // (rows past the prefix: codes and scales are zeros)
-            cp_async4(sc + k, src + (in ? key0 + k : 0), in);
-          }
-          cp_async_arrive(&raw_full[r]);
-          ++issued;
-          return true;
-        });
-        if (*abort_flag)                       // copies in flight land before the CTA leaves
-          for (int x = issued > RS ? issued - RS : 0; x < issued; ++x) mbar_drain(&raw_full[x % RS], (x / RS) & 1);
-      } else {
+    if constexpr (!E4M3) {
+      if (lane == 0) {
         uint32_t fills = 0;                    // per slot: begun (bit s), parity of the last fill (bit 16 + s)
         for_ring<F, FR>(n, two, [&](int s, int ph, bool is_v, int t) {
           const int j = jb + t;
@@ -303,51 +270,68 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
     // the order they are issued, so S of its next tile may take the columns that P V reads before it
     const int x = warp == 1 ? 0 : 1;
     const bool leader = elect_one();
-    constexpr uint32_t ID_S = idesc_f16(BKV, 0, 0, 0), ID_O = idesc_f16(HD, 0, 0, 1);
+    constexpr uint32_t ID_S = idesc_f16(BKV / 2, 0, 0, 0), ID_O = idesc_f16(HD, 0, 0, 1);
     const uint32_t tS = tmem + x * 128, tO = tmem + T_O + x * 128;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_err, ERR_TIMEOUT) ? 1 : 0) != 0;
     };
     const uint64_t qd = desc_sw128(smem_u32(sm + L::Q) + (two && x ? BQ * HD * 2 : 0), 16);
-    int done = 0;                              // products P V issued
-    int group = 0;                             // turns taken
-    auto take_turn = [&]() { return !two || wait(&turn[x], (x ? group : group - 1) & 1); };
-    auto pass_turn = [&]() {
-      if (two && leader) mbar_arrive(&turn[x ^ 1]);
-      ++group;
+    const int step = two ? 1 : 2;
+    int vslot = 0;
+    auto scores = [&](int h, int s) {          // S = Q K^T over half h of the tile in slot s
+      const uint64_t kd = desc_sw128(smem_u32(kvst + s * L::TILE) + h * (BKV / 2 * 128), 16);
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; ++kk) {
+        const uint64_t off = (uint64_t)(((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4);
+        mma_ss(tS + h * (BKV / 2), qd + (uint64_t)(((kk >> 2) * (BQ * 128) + (kk & 3) * 32) >> 4), kd + off, ID_S,
+               kk > 0 ? 1u : 0u);
+      }
+      commit(&s_full[2 * x + h]);
+    };
+    auto values = [&](int h, int s, bool acc) {   // O += P V over half h
+      const uint64_t vd = desc_sw128(smem_u32(kvst + s * L::TILE) + h * (BKV / 2 * 128), BKV * 128);
+#pragma unroll
+      for (int kk = 0; kk < BKV / 32; ++kk)
+        mma_ts(tO, tS + h * (BKV / 2) + kk * 8, vd + (uint64_t)(kk * 16 * 128 >> 4), ID_O, (acc || kk > 0) ? 1u : 0u);
+      commit(&o_step[2 * x + h]);
     };
     if (n > 0 && wait(q_full, 0))
       for_ring<F, FR>(n, two, [&](int s, int ph, bool is_v, int t) {
         if (!two && (t & 1) != x) return true;           // the other stream's tile
+        const int i = two ? t : t >> 1;                  // the stream's tile
         if (!wait(&full[s], ph)) return false;
-        const uint32_t addr = smem_u32(kvst + s * L::TILE);
         if (is_v) {
-          if (!wait(&p_full[x], done & 1) || !take_turn()) return false;
+          const bool last = t + step >= n;
+          if (!wait(&p_full[2 * x], i & 1)) return false;
           fence_after();
-          if (leader) {                        // O += P V
-            const uint64_t vd = desc_sw128(addr, BKV * 128);
-#pragma unroll
-            for (int kk = 0; kk < BKV / 16; ++kk)
-              mma_ts(tO, tS + kk * 8, vd + (uint64_t)(kk * 16 * 128 >> 4), ID_O, (done > 0 || kk > 0) ? 1u : 0u);
-            if (t + (two ? 1 : 2) >= n) commit(&o_done[x]);
-            commit(&empty[s]);
-          }
-          ++done;
-          if (two && t + 1 >= n) pass_turn();
-        } else {
-          if (t == 0 && !take_turn()) return false;
-          fence_after();
-          if (leader) {                        // S = Q K^T
-            const uint64_t kd = desc_sw128(addr, 16);
-#pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk) {
-              const uint64_t off = (uint64_t)(((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4);
-              mma_ss(tS, qd + off, kd + off, ID_S, kk > 0 ? 1u : 0u);
+          if (leader) values(0, s, i > 0);
+          __syncwarp();
+          vslot = s;
+          if (last) {
+            if (!wait(&p_full[2 * x + 1], i & 1)) return false;
+            fence_after();
+            if (leader) {
+              values(1, s, true);
+              commit(&o_done[x]);
+              commit(&empty[s]);
             }
-            commit(&s_full[x]);
+          }
+        } else {
+          fence_after();
+          if (leader) scores(0, s);
+          __syncwarp();
+          if (t >= step) {
+            if (!wait(&p_full[2 * x + 1], (i - 1) & 1)) return false;
+            fence_after();
+            if (leader) {
+              values(1, vslot, true);
+              commit(&empty[vslot]);
+            }
+          }
+          if (leader) {
+            scores(1, s);
             commit(&empty[s]);
           }
-          if (two) pass_turn();
         }
         __syncwarp();
         return true;
@@ -373,80 +357,108 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
       }
       const int c = lane % CH;
       bool bad = false;
-      uint4 x[PASSES];
+      constexpr int BATCH = E4M3 ? PASSES / 2 : PASSES;       // reads issued together (registers)
+#pragma unroll 1
+      for (int p0 = 0; p0 < PASSES; p0 += BATCH) {
+        uint4 x[BATCH];
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        const int64_t o = __shfl_sync(0xffffffffu, off, p * RPI + lane / CH);
-        x[p] = o >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + o) + c) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        if (is_v && (nonfinite2(x[p].x) || nonfinite2(x[p].y) || nonfinite2(x[p].z) || nonfinite2(x[p].w))) {
-          bad = true;
-          x[p] = make_uint4(drop_nonfinite2(x[p].x), drop_nonfinite2(x[p].y), drop_nonfinite2(x[p].z),
-                            drop_nonfinite2(x[p].w));
+        for (int p = 0; p < BATCH; ++p) {
+          const int64_t o = __shfl_sync(0xffffffffu, off, (p0 + p) * RPI + lane / CH);
+          x[p] = o >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + o) + c) : make_uint4(0, 0, 0, 0);
         }
-        const int r = lw * 32 + p * RPI + lane / CH;
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * (BKV * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x[p];
+#pragma unroll
+        for (int p = 0; p < BATCH; ++p) {
+          if (is_v && (nonfinite2(x[p].x) || nonfinite2(x[p].y) || nonfinite2(x[p].z) || nonfinite2(x[p].w))) {
+            bad = true;
+            x[p] = make_uint4(drop_nonfinite2(x[p].x), drop_nonfinite2(x[p].y), drop_nonfinite2(x[p].z),
+                              drop_nonfinite2(x[p].w));
+          }
+          const int r = lw * 32 + (p0 + p) * RPI + lane / CH;
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * (BKV * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x[p];
+        }
       }
       if (bad) *v_flag = 1;
     };
-    int raw = 0;                               // raw items taken
+    // e4m3 prefix: LPR lanes of 16 codes per row, RP rows a pass, PN passes; the lanes of a row's second 64
+    // columns take their two 8-code halves in the other order, so that no store conflicts
+    constexpr int LPR = HD / 16, RP = 32 / LPR, PN = 32 / RP;
+    const int ci = lane % LPR, sw = HD == 128 && ci >= 4 ? 1 : 0;
+    const int c0 = ((2 * ci) & 7) + sw, c1 = ((2 * ci) & 7) + 1 - sw;
+    const int64_t krow = (int64_t)a.Hkv * HD;              // bytes from key to key
+    const uint8_t* codes = (const uint8_t*)a.kv + (int64_t)plane * a.cap * krow + (int64_t)g * HD;
+    const float* scales = a.scales + ((int64_t)plane * a.Hkv + g) * a.cap;
+    uint4 code[PN];                                        // of this warp's rows of its plane's next tile
+    float sc = 0.f;                                        // and the scale of its row `lane`
+    auto read = [&](int j, int p) {                        // (rows past the prefix: codes and scales are zeros)
+      const int key = j * BKV + lw * 32 + p * RP + lane / LPR;
+      return key < a.P ? __ldg(reinterpret_cast<const uint4*>(codes + key * krow) + ci) : make_uint4(0, 0, 0, 0);
+    };
+    auto fetch_scale = [&](int j) {
+      const int key = j * BKV + lw * 32 + lane;
+      sc = key < a.P ? __ldg(scales + key) : 0.f;
+    };
+    auto prefetch = [&](int j) {
+      const int key = j * BKV + lw * 32 + lane;
+      if (j < min(pl.ncache, je) && key < a.P) l2_prefetch(codes + key * krow);
+      if (lane == 0 && j < min(pl.ncache, je)) l2_prefetch(scales + j * BKV + lw * 32);
+    };
     wait_prerequisites();
-    for_ring<F, FR>(n, two, [&](int s, int fill_ph, bool is_v, int t) {
-      const int j = jb + t;
-      const uint32_t ph = fill_ph ^ 1;
+    if constexpr (E4M3)
+      if (jb < min(pl.ncache, je)) {
+        fetch_scale(jb);
+#pragma unroll
+        for (int p = 0; p < PN; ++p) code[p] = read(jb, p);
+        prefetch(jb + 1);
+        prefetch(jb + 2);
+      }
+    // One loop (a stream's ring takes K_0, V_0, K_1, ...): inlined at for_ring's calls, it moves the codes in
+    // flight from copy to copy, and waits for them there (1300 cycles a tile). A plane's warps see every
+    // second fill of a slot only; a parity wait needs all fills but the last to be over, and they are: their
+    // own last tile came after the consumption of an item behind those.
+    for (int it = 0; it < (E4M3 ? n : 2 * n); ++it) {
+      const int t = E4M3 ? it : it >> 1;
+      const bool is_v = E4M3 ? plane == 1 : it & 1;
+      const int i = 2 * (two ? t : t >> 1) + (is_v ? 1 : 0), ring = two ? F : FR;
+      const int s = (two || !(t & 1) ? 0 : FR) + i % ring, j = jb + t;
+      if (!wwait(&empty[s], ((i / ring) & 1) ^ 1)) break;
       uint8_t* dst = kvst + s * L::TILE;
       if (j >= pl.ncache) {
-        if (E4M3 && is_v != (plane == 1)) return true;
-        if (!wwait(&empty[s], ph)) return false;
         load_own(j - pl.ncache, is_v ? a.vn : a.kn, dst, is_v);
       } else if constexpr (E4M3) {
-        // every loader warp looks at every raw tile (a parity wait must see each phase), its plane's
-        // warps convert it
-        const int r = raw % RS;
-        if (!wwait(&raw_full[r], (raw / RS) & 1)) return false;
-        ++raw;
-        if (is_v != (plane == 1)) {
-          if (lane == 0) mbar_arrive(&raw_empty[r]);
-          return true;
-        }
-        if (!wwait(&empty[s], ph)) return false;
-        const float sc = reinterpret_cast<const float*>(sm + L::SC)[r * BKV + lw * 32 + lane];   // this lane's row
         const bool fast = __all_sync(0xffffffffu, sc <= 128.f && __half2float(__float2half_rn(sc)) == sc);
-        // LPR lanes of 16 codes per row, RP rows a pass; the lanes of a row's second 64 columns take
-        // their two 8-code halves in the other order, so that no store conflicts
-        constexpr int LPR = HD / 16, RP = 32 / LPR;
-        const int ci = lane % LPR, sw = HD == 128 && ci >= 4 ? 1 : 0;
-        const uint8_t* src = sm + L::R + r * L::RAW + (lw * 32) * HD + lane * 16;
         uint8_t* d = dst + (ci >> 2) * (BKV * 128) + (lw * 32 + lane / LPR) * 128;
-        const int c0 = ((2 * ci) & 7) + sw, c1 = ((2 * ci) & 7) + 1 - sw;
-        auto convert = [&](auto is_fast, int p) {
+        const bool more = j + 1 < min(pl.ncache, je);
+        const float rsc = sc;
+        auto convert = [&](auto is_fast, const uint4 cc, int p) {
           constexpr bool FAST = decltype(is_fast)::value;
-          const float rs = __shfl_sync(0xffffffffu, sc, p * RP + lane / LPR);
+          const float rs = __shfl_sync(0xffffffffu, rsc, p * RP + lane / LPR);
           const int x = (p * RP + lane / LPR) & 7;
-          const uint2 a0 = *reinterpret_cast<const uint2*>(src + p * RP * HD + sw * 8);
-          const uint2 a1 = *reinterpret_cast<const uint2*>(src + p * RP * HD + 8 - sw * 8);
-          *reinterpret_cast<uint4*>(d + p * RP * 128 + ((c0 ^ x) << 4)) = codes_to_half<FAST>(a0, rs);
-          *reinterpret_cast<uint4*>(d + p * RP * 128 + ((c1 ^ x) << 4)) = codes_to_half<FAST>(a1, rs);
+          const uint2 lo = make_uint2(cc.x, cc.y), hi = make_uint2(cc.z, cc.w);
+          *reinterpret_cast<uint4*>(d + p * RP * 128 + ((c0 ^ x) << 4)) = codes_to_half<FAST>(sw ? hi : lo, rs);
+          *reinterpret_cast<uint4*>(d + p * RP * 128 + ((c1 ^ x) << 4)) = codes_to_half<FAST>(sw ? lo : hi, rs);
         };
         if (fast) {
 #pragma unroll
-          for (int p = 0; p < 32 / RP; ++p) convert(std::true_type{}, p);
-        } else {
+          for (int p = 0; p < PN; ++p) convert(std::true_type{}, code[p], p);
+        } else {                               // (rare: reads the codes again, one pass at a time)
 #pragma unroll 1
-          for (int p = 0; p < 32 / RP; ++p) convert(std::false_type{}, p);
+          for (int p = 0; p < PN; ++p) convert(std::false_type{}, read(j, p), p);
         }
+        fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&raw_empty[r]);
-      } else {
-        if (!wwait(&empty[s], ph)) return false;   // the producer's tile: only the arrival
+        if (lane == 0) mbar_arrive(&full[s]);
+        prefetch(j + 3);
+        if (more) {                            // (behind the fence, which waits for reads in flight too)
+          fetch_scale(j + 1);
+#pragma unroll
+          for (int p = 0; p < PN; ++p) code[p] = read(j + 1, p);
+        }
+        continue;
       }
-      fence_async_smem();                          // this warp's writes are the MMA's to read
-      __syncwarp();
+      fence_async_smem();                          // this warp's writes are the MMA's to read (the producer's
+      __syncwarp();                                // tiles: only the arrival)
       if (lane == 0) mbar_arrive(&full[s]);
-      return true;
-    });
+    }
   } else {
     // ---- softmax of stream x: row r = TMEM lane r
     auto wwait = [&](uint64_t* bar, uint32_t parity) {
@@ -465,7 +477,7 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
       vs = tab.cum[s];
       row = (int64_t)tab.row0[s] + (vq - vs);
     }
-    const bool idle = !__any_sync(0xffffffffu, live);
+    const bool idle = quad >= quads(x);                  // no live row: nothing to do past Q's zeros
     wait_prerequisites();
     {   // Q rows of the quadrant; absent rows are zeros. One tile: each stream loads half of the chunks
       constexpr int CH = HD / 8;
@@ -499,58 +511,41 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
     float m = -INFINITY;                       // running maximum (log2 domain)
     uint64_t l2 = 0;                           // the row's sum, two partial sums
     bool ok = true;
-    int li = 0;                                // tiles this stream has taken
-    for (int t = two ? 0 : x; t < n && ok; t += two ? 1 : 2, ++li) {
-      if (!wwait(&s_full[x], li & 1)) { ok = false; break; }
-      if (idle) {
-        if (lane == 0) mbar_arrive(&p_full[x]);
-        continue;
-      }
+    int li = 0;                                // half tiles this stream has taken
+    for (int t = two ? 0 : x; t < n && ok && !idle; t += (li & 1) ? 0 : two ? 1 : 2) {
+      const int hh = li & 1, ph = (li >> 1) & 1;
+      if (!wwait(&s_full[2 * x + hh], ph)) { ok = false; break; }
+      ++li;
       fence_after();
-      // visible keys of this tile: columns lo .. hi
+      uint32_t u[64];
+      tld32(tS + hh * 64, u);
+      tld32(tS + hh * 64 + 32, u + 32);
+      // visible keys of this half: columns lo .. hi
       const int j = jb + t;
       int lo = 0, hi;
       if (j < pl.ncache) {
-        hi = a.P - 1 - j * BKV;
+        hi = a.P - 1 - j * BKV - hh * 64;
       } else {
-        const int base = kb + (j - pl.ncache) * BKV;
+        const int base = kb + (j - pl.ncache) * BKV + hh * 64;
         lo = vs - base;
         hi = live ? vq - base : -1;
       }
-      if (!__all_sync(0xffffffffu, lo <= 0 && hi >= BKV - 1)) {
-        // some row does not see all keys: -inf into its hidden scores, in place
-#pragma unroll 1
-        for (int c = 0; c < BKV; c += 32) {
-          const int a0 = min(max(lo - c, 0), 32), a1 = min(max(hi - c + 1, 0), 32);   // columns a0 .. a1-1
-          const uint32_t seen = a1 > a0 ? (0xffffffffu >> (32 - (a1 - a0))) << a0 : 0u;
-          uint32_t w[32];
-          tld32(tS + c, w);
-          ld_wait();
-          pin32(w);
+      ld_wait();
+      pin32(u);
+      pin32(u + 32);
+      if (!__all_sync(0xffffffffu, lo <= 0 && hi >= 63)) {   // some row does not see all keys: -inf for the hidden
+        const int a0 = min(max(lo, 0), 64), a1 = min(max(hi + 1, 0), 64);   // columns a0 .. a1-1
+        const uint64_t seen = a1 > a0 ? (~0ull >> (64 - (a1 - a0))) << a0 : 0ull;
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!(seen & (1u << e))) w[e] = 0xff800000u;
-          tst32(tS + c, w);
-        }
-        st_wait();
+        for (int e = 0; e < 64; ++e)
+          if (!((e < 32 ? (uint32_t)seen : (uint32_t)(seen >> 32)) & (1u << (e & 31)))) u[e] = 0xff800000u;
       }
-      // scores are read 32 at a time, once for the maximum and once for the weights, which take over the
-      // columns of scores already used (16 for 32)
       float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-      for (int c = 0; c < BKV; c += 64) {
-        uint32_t u[64];
-        tld32(tS + c, u);
-        tld32(tS + c + 32, u + 32);
-        ld_wait();
-        pin32(u);
-        pin32(u + 32);
 #pragma unroll
-        for (int k = 0; k < 64; k += 8)
+      for (int k = 0; k < 64; k += 8)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx4[e] = fmaxf(mx4[e], fmaxf(__uint_as_float(u[k + e]), __uint_as_float(u[k + 4 + e])));
-      }
+        for (int e = 0; e < 4; ++e)
+          mx4[e] = fmaxf(mx4[e], fmaxf(__uint_as_float(u[k + e]), __uint_as_float(u[k + 4 + e])));
       const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
       float alpha = 1.f;
       if (mx > m + 8.f) {
@@ -558,41 +553,38 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
         m = mx;
       }
       const float base = m == -INFINITY ? 0.f : m;
-      if (li > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {   // (S of this tile came after the last P V)
-        uint32_t w[32];
+      if (li > 1 && __any_sync(0xffffffffu, alpha != 1.f)) {   // once the last P V has completed
+        if (!wwait(&o_step[2 * x + (hh ^ 1)], ((li - 2) >> 1) & 1)) { ok = false; break; }
+        fence_after();
+        uint32_t w[16];
 #pragma unroll 1
-        for (int c = 0; c < HD; c += 32) {
-          tld32(tO + c, w);
+        for (int c = 0; c < HD; c += 16) {
+          tld16(tO + c, w);
           ld_wait();
-          pin32(w);
+          pin<16>(w);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
-          tst32(tO + c, w);
+          for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
+          tst16(tO + c, w);
         }
         l2 = mul2(l2, pack2(alpha, alpha));
       }
       const uint64_t nb = pack2(-base, -base);
-      uint32_t u[32];
-      tld32(tS, u);
-#pragma unroll 1
-      for (int c = 0; c < BKV; c += 32) {
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
         uint32_t pk[16];
-        ld_wait();
-        pin32(u);
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const uint64_t z = fma2(pack2u(u[e], u[e + 1]), sl2_2, nb);
+          const uint64_t z = fma2(pack2u(u[c + e], u[c + e + 1]), sl2_2, nb);
           const float p0 = ex2(lo2(z)), p1 = ex2(hi2(z));
           l2 = add2(l2, pack2(p0, p1));
           pk[e / 2] = h2u(p0, p1);
         }
-        if (c + 32 < BKV) tld32(tS + c + 32, u);
-        tst16(tS + c / 2, pk);
+        tst16(tS + hh * 64 + c / 2, pk);
       }
       st_wait();
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[x]);
+      if (lane == 0) mbar_arrive(&p_full[2 * x + hh]);
     }
     // ---- epilogue
     float l = lo2(l2) + hi2(l2);
@@ -616,7 +608,7 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
       if (ok && n > 0) ok = wwait(&o_done[0], 0);
       if (ok) {
         float o[32];
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < HD; c += 32) {
           sums(c, o);
 #pragma unroll
@@ -648,11 +640,10 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
         const int k1 = min(vq, kb + (je - pl.ncache) * BKV - 1);
         const int64_t pi = (int64_t)blockIdx.x * pl.nt + (two ? x : 0);
         uint8_t* ostage = sm + L::Q + (two && x ? BQ * HD * 2 : 0);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < HD; c += 32) {
           float o[32];
           sums(c, o);
-          if (!live) continue;                 // (sums is warp-collective, what follows is not)
           if (!two) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
@@ -663,7 +654,7 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
               o[e + 3] = (w0 != 0.f ? w0 * o[e + 3] : 0.f) + (w1 != 0.f ? w1 * y.w : 0.f);
             }
           }
-          if (fix)
+          if (fix)                             // (a row that is not live has no own rows)
             for (int kv = k0; kv <= k1; ++kv) {
               const f16* vp = a.vn + (row - (vq - kv)) * a.kv_stride + (int64_t)g * HD + c;
 #pragma unroll
@@ -679,10 +670,24 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
               *reinterpret_cast<uint4*>(dst + ((((c + e) / 8) ^ (r & 7)) << 4)) =
                   make_uint4(h2u(o[e] * inv, o[e + 1] * inv), h2u(o[e + 2] * inv, o[e + 3] * inv),
                              h2u(o[e + 4] * inv, o[e + 5] * inv), h2u(o[e + 6] * inv, o[e + 7] * inv));
-          } else {                             // [parts][HD / 4][BQ] groups of 4 sums: coalesced over the rows
-            float4* wo = reinterpret_cast<float4*>(a.ws) + (pi * (HD / 4) + c / 4) * BQ + r;
+          } else {                             // the warp's [HD / 8][32] groups of 4 sums, half of the columns at a time
+            float4* stage = reinterpret_cast<float4*>(ostage + quad * (HD * 64));
+            const int half = HD / 2, cc = c % half;
+            if (c == half) {                   // the first half is out of the stage
+              if (lane == 0) tma_store_read_wait();
+              __syncwarp();
+            }
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) wo[e / 4 * BQ] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 32; e += 4)
+              stage[(cc + e) / 4 * 32 + lane] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            if (cc + 32 == half) {
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                bulk_store((float*)a.ws + ((pi * 4 + quad) * HD + c + 32 - half) * 32, stage, HD * 64);
+                tma_store_commit();
+              }
+            }
           }
         }
         if (pl.ns == 1) {                      // whole rows out of the warp's stage
@@ -698,6 +703,7 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
                   *reinterpret_cast<const uint4*>(ostage + rr * (HD * 2) + ((c ^ (rr & 7)) << 4));
           }
         }
+        if (pl.ns > 1 && lane == 0) tma_store_wait();
         if (live && pl.ns > 1)
           reinterpret_cast<float2*>((float*)a.ws + (int64_t)gridDim.x * pl.nt * BQ * HD)[pi * BQ + r] = make_float2(m, l);
       }
@@ -710,81 +716,121 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
   }
 }
 
-// Joins the parts of a row in part order: M = max m, o = sum 2^(m - M) o / sum 2^(m - M) l. One
-// thread per (row of a query tile, 4 columns), consecutive threads on consecutive rows: the parts
-// are read in whole lines. A part without a visible key (m = -inf, l = 0) holds no sums.
-constexpr int CTHREADS = 128;
+// Joins the parts of a row: M = max m, o = sum 2^(m - M) o / sum 2^(m - M) l. A part without a visible key
+// (m = -inf, l = 0) holds no sums. A block joins 32 rows x 8 columns; warp w takes the parts w, w + W, ...,
+// and the W sums are joined through shared memory: every order is fixed by the sizes. All of a warp's reads
+// are issued together (reading m before o, part after part, cost 5.6 us for 9 parts and 9 us for 19, mostly
+// round trips to L2).
+constexpr int CWARPS = 8, CCOLS = 8;
+__device__ __forceinline__ float part_weight(float m, float M) { return m == M ? 1.f : t5::ex2(m - M); }
 template <int HD, int N>
-__global__ void __launch_bounds__(CTHREADS)
+__global__ void __launch_bounds__(CWARPS * 32, 4)
     combine_kernel(const __grid_constant__ SeqTab<N> table, const __grid_constant__ SharedAttnArgs a, const Plan pl) {
+  __shared__ float4 po[CWARPS][CCOLS / 4][36];
+  __shared__ float2 pml[CWARPS][32];
   allow_dependents();
-  const int r = threadIdx.x, c4 = blockIdx.x % (HD / 4), tile = blockIdx.x / (HD / 4);
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, W = blockDim.x >> 5;
+  const int cb = blockIdx.x % (HD / CCOLS), quad = blockIdx.x / (HD / CCOLS) % 4, tile = blockIdx.x / (HD / CCOLS * 4);
   const int mt = tile % pl.MT, g = tile / pl.MT;
-  const int vr = mt * pl.RT + r / pl.G;
-  const bool live = r < pl.RT * pl.G && vr < pl.V;
-  int64_t row = 0;
-  if (live) {
-    const TabView tab{table.n, table.cum, table.row0};
-    const int s = seq_of(tab, vr);
-    row = (int64_t)tab.row0[s] + vr - tab.cum[s];
-  }
+  const int rows = min(pl.RT, pl.V - mt * pl.RT) * pl.G;       // of this query tile
+  if (quad * 32 >= rows) return;
+  const TabView tab{table.n, table.cum, table.row0};
+  auto out_at = [&](int r) {                                   // where matrix row r of the tile goes
+    const int vr = mt * pl.RT + r / pl.G, s = seq_of(tab, vr);
+    return (((int64_t)tab.row0[s] + vr - tab.cum[s]) * a.Hq + g * pl.G + r % pl.G) * HD + cb * CCOLS;
+  };
+  constexpr int CP = CCOLS / 2;
+  int r = quad * 32 + threadIdx.x / CP;                        // the first row that this thread writes
+  int64_t at = threadIdx.x < 32 * CP && r < rows ? out_at(r) : 0;
   wait_prerequisites();
-  if (!live) return;
   // this tile's parts lie nt apart, from p0 on
-  const int64_t p0 = ((int64_t)g * pl.MP + mt / 2) * pl.ns * pl.nt + mt % 2;
+  const int64_t p0 = ((int64_t)g * pl.MP + mt / pl.nt) * pl.ns * pl.nt + mt % pl.nt;
   const float2* ml =
       reinterpret_cast<const float2*>((const float*)a.ws + (int64_t)pl.MP * a.Hkv * pl.ns * pl.nt * BQ * HD) +
-      p0 * BQ + r;
-  const float4* po = reinterpret_cast<const float4*>(a.ws) + (p0 * (HD / 4) + c4) * BQ + r;
-  float M = -INFINITY;
-#pragma unroll 8
-  for (int p = 0; p < pl.ns; ++p) M = fmaxf(M, ml[(int64_t)p * pl.nt * BQ].x);
-  float sum = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int p = 0; p < pl.ns; ++p) {
-    const float2 x = ml[(int64_t)p * pl.nt * BQ];
-    const float4 v = po[(int64_t)p * pl.nt * (HD / 4) * BQ];
-    const bool none = x.x == -INFINITY && x.y == 0.f;
-    const float w = x.x == M ? 1.f : t5::ex2(x.x - M);         // (M infinite: the parts that reach it)
-    if (!none) {
-      sum += w * x.y;
-      o.x += w * v.x;
-      o.y += w * v.y;
-      o.z += w * v.z;
-      o.w += w * v.w;
+      p0 * BQ + quad * 32 + lane;
+  const float4* ps = reinterpret_cast<const float4*>(a.ws) + ((p0 * 4 + quad) * (HD / 4) + cb * (CCOLS / 4)) * 32 + lane;
+  float m = -INFINITY, l = 0.f;
+  float4 o[CCOLS / 4] = {};
+  constexpr int U = 4;                                         // parts read together
+  for (int p = w; p < pl.ns; p += U * W) {
+    float2 x[U];
+    float4 v[U][CCOLS / 4];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      x[k] = make_float2(-INFINITY, 0.f);
+      if (p + k * W < pl.ns) {
+        x[k] = __ldcg(ml + (int64_t)(p + k * W) * pl.nt * BQ);
+#pragma unroll
+        for (int c = 0; c < CCOLS / 4; ++c) v[k][c] = __ldcg(ps + ((int64_t)(p + k * W) * pl.nt * HD + c) * 32);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (x[k].x == -INFINITY && x[k].y == 0.f) continue;
+      const float M = fmaxf(m, x[k].x), wo = part_weight(m, M), wp = part_weight(x[k].x, M);
+      m = M;
+      l = wo * l + wp * x[k].y;
+#pragma unroll
+      for (int c = 0; c < CCOLS / 4; ++c) {
+        o[c].x = wo * o[c].x + wp * v[k][c].x;
+        o[c].y = wo * o[c].y + wp * v[k][c].y;
+        o[c].z = wo * o[c].z + wp * v[k][c].z;
+        o[c].w = wo * o[c].w + wp * v[k][c].w;
+      }
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  *reinterpret_cast<uint2*>(a.out + (row * a.Hq + g * pl.G + r % pl.G) * HD + c4 * 4) =
-      make_uint2(t5::h2u(o.x * inv, o.y * inv), t5::h2u(o.z * inv, o.w * inv));
+  pml[w][lane] = make_float2(m, l);
+#pragma unroll
+  for (int c = 0; c < CCOLS / 4; ++c) po[w][c][lane] = o[c];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * CP; i += blockDim.x) {    // (row, 2 columns)
+    const int lr = i / CP, cp = i % CP;
+    if (i != threadIdx.x) {
+      r = quad * 32 + lr;
+      at = r < rows ? out_at(r) : 0;
+    }
+    if (r >= rows) continue;
+    float M = -INFINITY, sum = 0.f, y0 = 0.f, y1 = 0.f;
+    for (int k = 0; k < W; ++k) M = fmaxf(M, pml[k][lr].x);
+    for (int k = 0; k < W; ++k) {
+      const float2 x = pml[k][lr];
+      if (x.x == -INFINITY && x.y == 0.f) continue;
+      const float wp = part_weight(x.x, M);
+      const float2 v = reinterpret_cast<const float2*>(&po[k][cp >> 1][lr])[cp & 1];
+      sum += wp * x.y;
+      y0 += wp * v.x;
+      y1 += wp * v.y;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint32_t*>(a.out + at + cp * 2) = t5::h2u(y0 * inv, y1 * inv);
+  }
 }
 
 // How many parts an item's key tiles are split into: the count with the least estimated time, waves
 // of CTAs x (key tiles per part + a CTA's fixed cost), plus, when split, the join's launch and its
 // reads of the parts. Units: a key tile of two query tiles; one query tile alone takes about 0.55
 // of it. At most 64 parts, at most 8 CTAs an SM.
-Plan make_plan(int V, int max_len, int P, int Hq, int Hkv, int num_sms) {
+Plan make_plan(int V, int max_len, int P, int Hq, int Hkv, int hd, int num_sms) {
   Plan p;
   p.V = V;
   p.G = Hq / Hkv;
   p.RT = BQ / p.G;
   p.MT = (V + p.RT - 1) / p.RT;
-  p.MP = (p.MT + 1) / 2;
-  p.nt = p.MT > 1 ? 2 : 1;
   p.ncache = (int)(((int64_t)P + BKV - 1) / BKV);
-  const int64_t items = (int64_t)p.MP * Hkv;
-  const int64_t total = p.ncache + (std::min<int64_t>(V, (int64_t)max_len - 1 + p.nt * p.RT) + BKV - 1) / BKV;
-  const double unit = p.nt == 2 ? 1.0 : 0.55;
-  p.ns = 1;
-  double best = 0;
-  for (int ns = 1; ns <= 64 && ns <= total && (ns == 1 || items * ns <= 8ll * num_sms); ++ns) {
-    const double waves = (double)((items * ns + num_sms - 1) / num_sms);
-    double t = waves * (unit * (double)((total + ns - 1) / ns) + 2.5);
-    if (ns > 1) t += 2.5 + 0.01 * (double)(items * ns * p.nt);
-    if (ns == 1 || t < best) {
-      best = t;
-      p.ns = ns;
+  double best = -1;
+  for (int nt = 1; nt <= 2 && nt <= p.MT; ++nt) {
+    const int64_t MP = (p.MT + nt - 1) / nt, items = MP * Hkv;
+    const int64_t total = p.ncache + (std::min<int64_t>(V, (int64_t)max_len - 1 + nt * p.RT) + BKV - 1) / BKV;
+    for (int ns = 1; ns <= 64 && ns <= total && (ns == 1 || items * ns <= 8ll * num_sms); ++ns) {
+      const double waves = (double)((items * ns + num_sms - 1) / num_sms);
+      double t = waves * ((nt == 2 ? 1.3 : 0.75) * (double)((total + ns - 1) / ns) + 4.5);
+      if (ns > 1) t += 3.0 + 0.0002 * (double)(items * ns * nt * hd);
+      if (best < 0 || t < best) {
+        best = t;
+        p.nt = nt;
+        p.MP = (int)MP;
+        p.ns = ns;
+      }
     }
   }
   return p;
@@ -811,12 +857,14 @@ int pack_group(SeqTab<SEQ_TAB_LARGE>& t, int s, int n_seq, const int* row0, cons
 template <int HD, bool E4M3, int N>
 cudaError_t launch_group(const SharedAttnArgs& a, const SeqTab<N>& tab, const Plan& pl, const CUtensorMap& map,
                          cudaStream_t st) {
-  using L = Lay<HD, E4M3>;
+  using L = Lay<HD>;
   CK_RET(cudaFuncSetAttribute(shared_kernel<HD, E4M3, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES));
   CK_RET(launch_pdl(shared_kernel<HD, E4M3, N>, dim3((unsigned)((int64_t)pl.MP * a.Hkv * pl.ns)), dim3(threads_of(E4M3)),
                     L::BYTES, st, tab, map, a, pl));
   if (pl.ns > 1) {
-    CK_RET(launch_pdl(combine_kernel<HD, N>, dim3((unsigned)((int64_t)pl.MT * a.Hkv * (HD / 4))), dim3(CTHREADS), 0, st,
+    const int warps = std::min(CWARPS, (pl.ns + 1) / 2);
+    CK_RET(launch_pdl(combine_kernel<HD, N>, dim3((unsigned)((int64_t)pl.MT * a.Hkv * (HD / CCOLS * 4))),
+                      dim3((unsigned)(32 * warps)), 0, st,
                       tab, a, pl));
   }
   return cudaSuccess;
@@ -841,7 +889,7 @@ int64_t attention_shared_ws_bytes(int n_seq, const int* len, int P, int Hq, int 
     int max_len;
     s = sha::pack_group(t, s, n_seq, nullptr, len, &max_len);
     if (t.n == 0) continue;
-    const sha::Plan p = sha::make_plan(t.cum[t.n], max_len, P, Hq, Hkv, num_sms);
+    const sha::Plan p = sha::make_plan(t.cum[t.n], max_len, P, Hq, Hkv, hd, num_sms);
     if (p.ns > 1) need = std::max<int64_t>(need, (int64_t)p.MP * Hkv * p.ns * p.nt * sha::BQ * (hd + 2) * 4);
   }
   return need;
@@ -850,14 +898,12 @@ int64_t attention_shared_ws_bytes(int n_seq, const int* len, int P, int Hq, int 
 cudaError_t launch_attention_shared(const SharedAttnArgs& a, int n_seq, const int* row0, const int* len, int num_sms,
                                     cudaStream_t st) {
   CUtensorMap map = {};
-  if (a.P > 0) {
+  if (a.P > 0 && !a.e4m3) {
     // the P rows of each plane (rows past P read as zeros, never as what the capacity holds)
-    const uint64_t es = a.e4m3 ? 1 : 2;
     const uint64_t dims[4] = {(uint64_t)a.hd, (uint64_t)a.Hkv, (uint64_t)a.P, 2};
-    const uint64_t str[3] = {a.hd * es, (uint64_t)a.Hkv * a.hd * es, (uint64_t)a.cap * a.Hkv * a.hd * es};
-    const uint32_t box[4] = {a.e4m3 ? (uint32_t)a.hd : 64u, 1, sha::BKV, 1};
-    if (!encode_tensor_map(&map, a.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, a.kv,
-                           dims, str, box, a.e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B))
+    const uint64_t str[3] = {a.hd * 2ull, a.Hkv * a.hd * 2ull, (uint64_t)a.cap * a.Hkv * a.hd * 2};
+    const uint32_t box[4] = {64, 1, sha::BKV, 1};
+    if (!encode_tensor_map(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, a.kv, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
   SeqTab<SEQ_TAB_LARGE> t;
@@ -865,7 +911,7 @@ cudaError_t launch_attention_shared(const SharedAttnArgs& a, int n_seq, const in
     int max_len;
     s = sha::pack_group(t, s, n_seq, row0, len, &max_len);
     if (t.n == 0) continue;
-    const sha::Plan pl = sha::make_plan(t.cum[t.n], max_len, a.P, a.Hq, a.Hkv, num_sms);
+    const sha::Plan pl = sha::make_plan(t.cum[t.n], max_len, a.P, a.Hq, a.Hkv, a.hd, num_sms);
     if ((int64_t)pl.MP * a.Hkv * std::max(pl.ns, pl.nt * a.hd / 4) > INT_MAX) return cudaErrorInvalidValue;
     if (t.n <= SEQ_TAB_SMALL) {
       SeqTab<SEQ_TAB_SMALL> u;
