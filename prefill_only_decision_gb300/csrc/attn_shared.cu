@@ -90,29 +90,18 @@ struct Lay {
   static_assert(BQ * OSTR * 4 <= 2 * FR * TILE, "published sums fit the K/V stages");
 };
 
-// The tiles of K and V in the order the products take them: K_0 .. K_{lead-1}, then V_t, K_{t+lead}
-// for t = 0, 1, ... (lead = 1 when both streams take the same key tiles, 2 when they take turns).
-// f(slot, phase, is_v, tile) returns false to stop. With one query tile a stream only ever waits for
-// its own slots: a parity wait must never run more than one phase ahead of a slot, which waiting
-// past the other stream's fills (they complete in any order) could.
-template <int F, int FR, typename Fn>
-__device__ __forceinline__ void for_ring(int n, bool two, Fn f) {
-  int c[2] = {0, 0};
-  auto step = [&](bool is_v, int t) {
-    if (two) {
-      const int i = c[0]++;
-      return f(i % F, (i / F) & 1, is_v, t);
-    }
-    const int i = (t & 1) ? c[1]++ : c[0]++;
-    return f(((t & 1) ? FR : 0) + i % FR, (i / FR) & 1, is_v, t);
-  };
-  const int lead = two ? 1 : 2;
-  for (int t = 0; t < lead && t < n; ++t)
-    if (!step(false, t)) return;
-  for (int t = 0; t < n; ++t) {
-    if (!step(true, t)) return;
-    if (t + lead < n && !step(false, t + lead)) return;
-  }
+// A stage of the ring of K and V tiles. With two query tiles both streams read one ring K_0, V_0, K_1, ...;
+// with one, each stream has its own, of its tiles: a parity wait must never run more than one phase ahead
+// of a slot, which waiting past the other stream's fills (they complete in any order) could.
+struct Slot {
+  int s;
+  uint32_t ph;
+};
+template <int F, int FR>
+__device__ __forceinline__ Slot slot_of(bool two, int t, bool is_v) {
+  const uint32_t i = 2 * (two ? t : t >> 1) + (is_v ? 1 : 0);
+  if (two) return {(int)(i % F), i / F & 1};
+  return {(t & 1 ? FR : 0) + (int)(i % FR), i / FR & 1};
 }
 
 // Sequence tables as a kernel searches them: a small one from its copy in shared memory, a large
@@ -247,9 +236,15 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
     if constexpr (!E4M3) {
       if (lane == 0) {
         uint32_t fills = 0;                    // per slot: begun (bit s), parity of the last fill (bit 16 + s)
-        for_ring<F, FR>(n, two, [&](int s, int ph, bool is_v, int t) {
-          const int j = jb + t;
-          if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, &g_err, ERR_TIMEOUT)) return false;
+        const int lead = two ? 1 : 2;          // K_0 .. K_{lead-1}, then V_t, K_{t+lead}
+        for (int q = 0; q < 2 * n + lead - 1; ++q) {
+          const int e = q - lead;
+          const bool is_v = e >= 0 && !(e & 1);
+          const int t = e < 0 ? q : is_v ? e >> 1 : lead + (e >> 1), j = jb + t;
+          if (t >= n) continue;
+          const Slot k = slot_of<F, FR>(two, t, is_v);
+          const int s = k.s;
+          if (!mbar_wait(&empty[s], k.ph ^ 1, abort_flag, &g_err, ERR_TIMEOUT)) break;
           if (j < pl.ncache) {
             mbar_expect_tx(&full[s], L::TILE);
             for (int b = 0; b < NB; ++b)
@@ -257,9 +252,8 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
           } else {
             mbar_arrive(&full[s]);
           }
-          fills = (fills & ~(1u << (16 + s))) | 1u << s | (uint32_t)ph << (16 + s);
-          return true;
-        });
+          fills = (fills & ~(1u << (16 + s))) | 1u << s | k.ph << (16 + s);
+        }
         if (*abort_flag)
           for (int s = 0; s < NS; ++s)
             if ((fills >> s) & 1) mbar_drain(&full[s], (fills >> (16 + s)) & 1);
@@ -276,8 +270,6 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_err, ERR_TIMEOUT) ? 1 : 0) != 0;
     };
     const uint64_t qd = desc_sw128(smem_u32(sm + L::Q) + (two && x ? BQ * HD * 2 : 0), 16);
-    const int step = two ? 1 : 2;
-    int vslot = 0;
     auto scores = [&](int h, int s) {          // S = Q K^T over half h of the tile in slot s
       const uint64_t kd = desc_sw128(smem_u32(kvst + s * L::TILE) + h * (BKV / 2 * 128), 16);
 #pragma unroll
@@ -295,47 +287,40 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
         mma_ts(tO, tS + h * (BKV / 2) + kk * 8, vd + (uint64_t)(kk * 16 * 128 >> 4), ID_O, (acc || kk > 0) ? 1u : 0u);
       commit(&o_step[2 * x + h]);
     };
-    if (n > 0 && wait(q_full, 0))
-      for_ring<F, FR>(n, two, [&](int s, int ph, bool is_v, int t) {
-        if (!two && (t & 1) != x) return true;           // the other stream's tile
-        const int i = two ? t : t >> 1;                  // the stream's tile
-        if (!wait(&full[s], ph)) return false;
-        if (is_v) {
-          const bool last = t + step >= n;
-          if (!wait(&p_full[2 * x], i & 1)) return false;
-          fence_after();
-          if (leader) values(0, s, i > 0);
-          __syncwarp();
-          vslot = s;
-          if (last) {
-            if (!wait(&p_full[2 * x + 1], i & 1)) return false;
+    // of each half h: P V of tile i - 1, then S of tile i into the same columns
+    const int cnt = two ? n : (n + 1 - x) >> 1;
+    if (cnt > 0 && wait(q_full, 0))
+      for (int i = 0; i <= cnt; ++i) {
+        const int t = two ? i : 2 * i + x;
+        const Slot k = slot_of<F, FR>(two, t, false), v = slot_of<F, FR>(two, t - (two ? 1 : 2), true);   // (unused: v at i = 0, k at cnt)
+        auto half = [&](auto hc) {
+          constexpr int h = decltype(hc)::value;
+          if (i > 0) {
+            if (h == 0 && !wait(&full[v.s], v.ph)) return false;
+            if (!wait(&p_full[2 * x + h], (i - 1) & 1)) return false;
             fence_after();
             if (leader) {
-              values(1, s, true);
-              commit(&o_done[x]);
-              commit(&empty[s]);
+              values(h, v.s, h > 0 || i > 1);
+              if (h) commit(&empty[v.s]);
+              if (h && i == cnt) commit(&o_done[x]);
             }
+            __syncwarp();
           }
-        } else {
-          fence_after();
-          if (leader) scores(0, s);
-          __syncwarp();
-          if (t >= step) {
-            if (!wait(&p_full[2 * x + 1], (i - 1) & 1)) return false;
-            fence_after();
+          if (i < cnt) {
+            if (h == 0) {
+              if (!wait(&full[k.s], k.ph)) return false;
+              fence_after();
+            }
             if (leader) {
-              values(1, vslot, true);
-              commit(&empty[vslot]);
+              scores(h, k.s);
+              if (h) commit(&empty[k.s]);
             }
+            __syncwarp();
           }
-          if (leader) {
-            scores(1, s);
-            commit(&empty[s]);
-          }
-        }
-        __syncwarp();
-        return true;
-      });
+          return true;
+        };
+        if (!half(std::integral_constant<int, 0>{}) || !half(std::integral_constant<int, 1>{})) break;
+      }
     if (leader) {
       commit(&mma_idle[x]);
       mbar_drain(&mma_idle[x], 0);             // every MMA issued above has completed
@@ -411,16 +396,14 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
         prefetch(jb + 1);
         prefetch(jb + 2);
       }
-    // One loop (a stream's ring takes K_0, V_0, K_1, ...): inlined at for_ring's calls, it moves the codes in
-    // flight from copy to copy, and waits for them there (1300 cycles a tile). A plane's warps see every
-    // second fill of a slot only; a parity wait needs all fills but the last to be over, and they are: their
-    // own last tile came after the consumption of an item behind those.
+    // A plane's warps see every second fill of a slot only; a parity wait needs all fills but the last to be
+    // over, and they are: the warps' own last tile came after the consumption of an item behind those.
     for (int it = 0; it < (E4M3 ? n : 2 * n); ++it) {
       const int t = E4M3 ? it : it >> 1;
       const bool is_v = E4M3 ? plane == 1 : it & 1;
-      const int i = 2 * (two ? t : t >> 1) + (is_v ? 1 : 0), ring = two ? F : FR;
-      const int s = (two || !(t & 1) ? 0 : FR) + i % ring, j = jb + t;
-      if (!wwait(&empty[s], ((i / ring) & 1) ^ 1)) break;
+      const Slot k = slot_of<F, FR>(two, t, is_v);
+      const int s = k.s, j = jb + t;
+      if (!wwait(&empty[s], k.ph ^ 1)) break;
       uint8_t* dst = kvst + s * L::TILE;
       if (j >= pl.ncache) {
         load_own(j - pl.ncache, is_v ? a.vn : a.kn, dst, is_v);
