@@ -8,27 +8,31 @@
 // (sequence, q head), reads it once per sequence and head.
 //
 // One pass over the keys with a running maximum and sum in fp32, in two streams of S = Q K^T,
-// softmax, O += P V that take turns on the tensor cores, so that one stream's softmax runs under
-// the other's products. The streams are two query tiles over the same key tiles or, for the last
-// query tile of an odd count, one query tile over the even and the odd key tiles (joined at the
-// end). Work items are (kv head, pair of query tiles); an item's key tiles are split over `ns`
-// CTAs when that shortens the call, and combine_kernel joins their (o, m, l) in part order (no
-// atomics: the same bits every time). One CTA per SM, 15 warps (19 with an e4m3 prefix):
-//   warp 0      TMA producer: prefix tiles (f16 tiles, or e4m3 tiles into a ring of raw stages)
-//   warps 1, 14 MMA issue of stream 0 and 1. With two query tiles they take turns, a stream's P V and
-//               next S = Q K^T at a time: issued side by side the products share the tensor cores, both
-//               streams get them late, and their softmaxes then run at the same time with the tensor
-//               cores idle (16 q heads, 1340 rows over 65536: 606 us, by turns 575 us)
-//   warps 2-5, 6-9  softmax of stream 0, 1: one thread per row (TMEM lane). Running max with a lazy
-//               rescale (O and l move only when the row's maximum grows by more than 2^8). P (f16)
-//               goes back into the TMEM columns of S and is the A operand of
-//               O += P V from there: no shared-memory round trip. Warps whose 32 rows are all past
-//               the tile's last row only keep the barriers going.
+// softmax, O += P V that share the tensor cores. The streams are two query tiles over the same key
+// tiles or, with one query tile an item (small calls, and the last of an odd count), that tile over
+// the even and the odd key tiles, joined at the end. A stream takes a key tile in two halves of 64
+// keys with S in TMEM columns of their own: while the softmax works on one half, the products P V of
+// the half before and S of the half behind it run. (One S of 128 columns: softmax and products of a
+// stream take turns, and both streams' products collide; 65536 rows, 1340 packed rows x 16 heads: 574
+// us, in halves 470. The halves' S reads Q twice, 1.5 x the shared-memory time of S.)
+// Work items are (kv head, query tile or pair of tiles); an item's key tiles are split over `ns` CTAs
+// when that shortens the call, and combine_kernel joins their (o, m, l) in an order that the sizes fix
+// (no atomics: the same bits every time). One CTA per SM, 15 warps (19 with an e4m3 prefix):
+//   warp 0      TMA producer: f16 prefix tiles
+//   warps 1, 14 MMA issue of stream 0 and 1
+//   warps 2-5, 6-9  softmax of stream 0, 1: one thread per row (TMEM lane), 64 scores in registers.
+//               Running max with a lazy rescale (O and l move only when the row's maximum grows by more
+//               than 2^8, once the last P V has completed). P (f16) goes back into the TMEM columns of
+//               S and is the A operand of O += P V from there: no shared-memory round trip. Warps whose
+//               32 rows are all past the tile's last row leave at once: their polling slowed the others.
 //   warps 10-13 loaders: the batch's own keys (gathered row by row through the sequence table), and
-//               e4m3 prefix tiles: codes from the raw stage to f16 in the MMA's swizzled layout. With
-//               an e4m3 prefix they take the K tiles and warps 15-18 the V tiles: four warps alone
-//               (2050 cycles a tile) held a CTA to 15 GB/s of codes, half its share of the HBM rate
-// K and V tiles share one ring of stages in the order the products take them.
+//               e4m3 prefix tiles: codes from memory through registers (read one tile ahead, asked for in
+//               L2 three ahead) to f16 in the MMA's swizzled layout. With an e4m3 prefix they take the K
+//               tiles and warps 15-18 the V tiles. (Codes through a shared-memory ring cost a third of
+//               its bandwidth, the bound of this kernel: 65536 rows 645 us, straight from memory 544.)
+// K and V tiles share one ring of stages in the order the products take them. Each role is one short
+// loop with one copy of its body: the roles together overflow the instruction cache when they are
+// inlined several times (four copies: f16 491 us instead of 470, e4m3 571 instead of 544).
 // Own keys are packed the same way as queries: row r's visible own keys are the packed rows
 // start(r) .. r, so one masked tile serves many short sequences. A masked weight is an exact zero,
 // but 0 x NaN is not: the loaders replace non-finite own V elements by 0 and flag the CTA, and
@@ -789,10 +793,13 @@ __global__ void __launch_bounds__(CWARPS * 32, 4)
   }
 }
 
-// How many parts an item's key tiles are split into: the count with the least estimated time, waves
-// of CTAs x (key tiles per part + a CTA's fixed cost), plus, when split, the join's launch and its
-// reads of the parts. Units: a key tile of two query tiles; one query tile alone takes about 0.55
-// of it. At most 64 parts, at most 8 CTAs an SM.
+// One or two query tiles an item, and how many parts an item's key tiles are split into: the choice with
+// the least estimated time (us, all constants measured): waves of CTAs x (key tiles per part + a CTA's fixed
+// cost) and, when split, the join's launch and the sums that are written and read. A key tile takes 1.13 us
+// with two query tiles and 0.66 with one, or as long as all CTAs' tiles need at 14 TB/s. Against the
+// best of 80 forced choices, over 10 calls from 64 rows x 1024 to 1470 x 20000: within 8 %, mostly 3 %.
+// (16 q heads, 128 rows over 2048: one part 19.2 us, seven 12.9; two tiles an item 28.1 and 14.1.) At most
+// 64 parts, at most 8 CTAs an SM.
 Plan make_plan(int V, int max_len, int P, int Hq, int Hkv, int hd, int num_sms) {
   Plan p;
   p.V = V;
@@ -805,9 +812,11 @@ Plan make_plan(int V, int max_len, int P, int Hq, int Hkv, int hd, int num_sms) 
     const int64_t MP = (p.MT + nt - 1) / nt, items = MP * Hkv;
     const int64_t total = p.ncache + (std::min<int64_t>(V, (int64_t)max_len - 1 + nt * p.RT) + BKV - 1) / BKV;
     for (int ns = 1; ns <= 64 && ns <= total && (ns == 1 || items * ns <= 8ll * num_sms); ++ns) {
-      const double waves = (double)((items * ns + num_sms - 1) / num_sms);
-      double t = waves * ((nt == 2 ? 1.3 : 0.75) * (double)((total + ns - 1) / ns) + 4.5);
-      if (ns > 1) t += 3.0 + 0.0002 * (double)(items * ns * nt * hd);
+      const int64_t ctas = items * ns;
+      const double waves = (double)((ctas + num_sms - 1) / num_sms);
+      const double l2 = (double)std::min<int64_t>(ctas, num_sms) * (4 * BKV) * hd / 14e6;
+      double t = waves * (std::max(nt == 2 ? 1.13 : 0.66, l2) * (double)((total + ns - 1) / ns) + 4.5);
+      if (ns > 1) t += 2.8 + 0.00006 * (double)(ctas * nt * hd);
       if (best < 0 || t < best) {
         best = t;
         p.nt = nt;
