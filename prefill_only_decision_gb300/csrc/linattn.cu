@@ -12,20 +12,25 @@
 // pass over the chunks. What bounds it: q, k, v read and o written once, 4 x 32 KB per chunk and
 // head at 128 x 128, about 2.9 us of an SM's share of the HBM rate; the products of a chunk take
 // about 1.3 us of tensor time.
-// Operand precision: products take 16-bit operands and sum in fp32. Q, K and V enter as given. The
-// weights of V in a chunk, the decayed Q rows and the state's operand copy are rounded once to the
-// rows' type (the state itself never is). The decayed values v_j lam^(n-1-j) of the state update are
-// split into two such numbers (hi + lo), because the state is kept and returned in fp32: one
-// rounding of 2^-9 (bf16) would show in it. f16 rows: weights, decayed Q and the state's copy are
-// scaled by powers of two so that they use f16's range whatever the magnitudes: the state's copy by
-// 2^a (from a running bound lam^n bound + n max|v| max|k| on the state), the weights by 2^c (from
-// dk max|q| max|k|, c for each 32 rows), the decayed Q by 2^(c - a), the outputs by 2^-c; f16's 30
-// binades leave room for how far above the values such bounds lie. The decayed values, with the
-// state they are added to, are scaled by 2^b (b per chunk), so that the low parts stay above f16's
+// Operand precision: products take 16-bit operands and sum in fp32. Q, K and V enter as given: of a row's
+// decay lam^(i+1) = 2^e r, Q takes 2^e (exact), the outputs r in fp32, the weights 1 / r with their own
+// decay (a rounded decayed Q put the outputs' error at 1.57 x one rounding to the rows' type, instead of
+// 1.41). The weights of V in a chunk and the state's operand copy are rounded once to the rows' type (the
+// state itself never is). The decayed values v_j lam^(n-1-j) of the state update are split into such
+// numbers, because the state is kept and returned in fp32: two for f16 (they leave 5e-8), three for bf16
+// (two leave 2.5e-6, three put the state's error at 3e-7, most of it fp32's, and cost 202 us instead of
+// 182 on 16476 rows x 32 heads). Their products run small parts first: the sums lose less. f16 rows:
+// weights, scaled Q and the state's copy are scaled by powers of two so that they use f16's range whatever
+// the magnitudes: the state's copy by 2^a (from a running bound lam^n bound + n max|v| max|k| on the
+// state), the weights by 2^c (from dk max|q| max|k|, c for each 32 rows), Q by 2^(c - a), the outputs by
+// 2^-c; f16's 30 binades leave room for how far above the values such bounds lie. The decayed values, with
+// the state they are added to, are scaled by 2^b (b per chunk), so that the low parts stay above f16's
 // smallest number.
+// Where: f16's scaled Q is in TMEM beside the weights; bf16's is in its shared-memory tile, and the third
+// parts take its TMEM columns (so they wait for the weights, and the next Q K^T waits for them).
 // One CTA per SM, 23 warps: 0 TMA producer (two stages of Q, K, V); 1 and 18 MMA issue (1: Q K^T and
 // the outputs, 18: the state); 2-9 rows of the chunk (TMEM lane = row, two threads a row: weights,
-// decayed Q); 10-17 value rows (TMEM lane = value row, two threads a row: the split decayed values,
+// scaled Q); 10-17 value rows (TMEM lane = value row, two threads a row: the split decayed values,
 // the state's copy and decay); 19-22 outputs (a thread a row). Their passes are loops over 32
 // columns, not unrolled code: a chunk's worth of straight-line code per role does not stay in the
 // instruction cache, and took longer.
@@ -97,7 +102,7 @@ __device__ __forceinline__ int find(const int* cum, int n, int i) {
 }
 
 // TMEM columns: weights of V, per half of 64 columns: fp32, then 16-bit in its first 32 columns and
-// the half's decayed Q in its last 32 | outputs | state | low and high parts of the decayed values
+// the half's scaled Q (f16) or third parts of the decayed values (bf16) in its last 32 | outputs | state | low and high parts of the decayed values
 constexpr int TMEM_COLS = 512;
 constexpr int T_P = 0, T_O = 128, T_S = 256, T_VL = 384, T_VH = 448;
 
@@ -119,6 +124,12 @@ struct Lay {
 // Smallest e with |x| < 2^e (finite x != 0).
 __device__ __forceinline__ int exp_above(float x) { return (int)((__float_as_uint(x) >> 23) & 255) - 126; }
 __device__ __forceinline__ float h_bits(uint32_t u) { return __half2float(__ushort_as_half((unsigned short)u)); }
+// A normal x > 0 as 2^e r with r in [1, 2): p2 = 2^e, returns r (else p2 = x, r = 1).
+__device__ __forceinline__ float split_pow2(float x, float& p2) {
+  const uint32_t b = __float_as_uint(x);
+  p2 = b >> 23 ? __uint_as_float(b & 0x7f800000u) : x;
+  return b >> 23 ? __uint_as_float((b & 0x7fffffu) | 0x3f800000u) : 1.f;
+}
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 .. 127
 
 // Terms of non-finite V elements, which the products leave out (out of line: hardly ever taken).
@@ -188,7 +199,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* empty = bars + 6;                  // [3][2] its slot may be filled again
   uint64_t* clean = bars + 12;                 // [2] K and V: rows past the end and non-finite V are zeros
   uint64_t* p_full = bars + 14;                // Q K^T is in TMEM
-  uint64_t* p_ready = bars + 15;               // weights and decayed Q are in TMEM
+  uint64_t* p_ready = bars + 15;               // weights and scaled Q are in TMEM
   uint64_t* s_ready = bars + 16;               // the state's copy is in shared memory, its decay applied
   uint64_t* v_ready = bars + 23;               // [2] the decayed values are in TMEM, V has been read for them
                                                // (two: the row warps may see one a chunk late)
@@ -234,7 +245,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 6; ++i) mbar_init(&full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&empty[i], 8);                 // Q: the row warps have read it (behind its products)
+      mbar_init(&empty[i], F16 ? 8 : 1);       // Q: the row warps have read it (behind its products; bf16: the outputs' products have)
       mbar_init(&empty[2 + i], OUT ? 2 : 1);   // K: the products of the weights, and of the state
       mbar_init(&empty[4 + i], OUT ? 4 : 1);   // V: the outputs, staged there (!OUT: the state's products)
       mbar_init(&clean[i], 8);
@@ -350,6 +361,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const uint32_t ph = c & 1, sph = (c >> 1) & 1;
         const uint32_t base = smem_u32(sm + st * L::STAGE);
         if (!wwait(&full[st], sph) || !wwait(&full[2 + st], sph)) break;
+        if (!F16 && c > 0 && !wwait(ds_done, (c - 1) & 1)) break;   // (the third parts in these columns have been read)
         fence_after();
         if (leader) {                          // Q K^T (in order behind the products that read these columns)
           const uint64_t qd = desc_sw128(base, 16), kd = desc_sw128(base + L::QB, 16);
@@ -365,14 +377,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (!wwait(&clean[st], sph) || !wwait(s_ready, ph) || !wwait(p_ready, ph)) break;
         if (c > 0 && !wwait(o_free, (c - 1) & 1)) break;
         fence_after();
-        if (leader) {                          // O = (decayed Q) S^T + weights V
+        if (leader) {                          // O = (scaled Q) S^T + weights V
           const uint64_t sd = desc_sw128(smem_u32(sm + L::S16), 16), vd = desc_sw128(base + 2 * L::QB, C * 128);
 #pragma unroll
           for (int kk = 0; kk < DK / 16; ++kk) {
-            const int q = kk < DK / 32 ? 32 + kk * 8 : 96 + (kk - DK / 32) * 8;
-            mma_ts(tmem + T_O, tmem + T_P + q, sd + (uint64_t)(((kk >> 2) * (DV * 128) + (kk & 3) * 32) >> 4), ID_QS,
-                   kk > 0 ? 1u : 0u);
+            const uint64_t so = sd + (uint64_t)(((kk >> 2) * (DV * 128) + (kk & 3) * 32) >> 4);
+            if constexpr (F16) {
+              const int q = kk < DK / 32 ? 32 + kk * 8 : 96 + (kk - DK / 32) * 8;
+              mma_ts(tmem + T_O, tmem + T_P + q, so, ID_QS, kk > 0 ? 1u : 0u);
+            } else {
+              const uint64_t qo = desc_sw128(base, 16) + (uint64_t)(((kk >> 2) * (C * 128) + (kk & 3) * 32) >> 4);
+              mma_ss(tmem + T_O, qo, so, ID_QS, kk > 0 ? 1u : 0u);
+            }
           }
+          if (!F16) commit(&empty[st]);
 #pragma unroll
           for (int kk = 0; kk < C / 16; ++kk)
             mma_ts(tmem + T_O, tmem + T_P + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8),
@@ -396,13 +414,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       fence_after();
       if (leader) {
         const uint64_t kd = desc_sw128(smem_u32(sm + st * L::STAGE + L::QB), C * 128);
+        // (small parts first: the tensor cores' sums lose less)
+        if constexpr (!F16) {
+#pragma unroll
+          for (int kk = 0; kk < C / 16; ++kk)
+            mma_ts(tmem + T_S, tmem + T_P + (kk < 4 ? 32 + kk * 8 : 96 + (kk - 4) * 8),
+                   kd + (uint64_t)(kk * 16 * 128 >> 4), ID_S, OUT || c > 0 || kk > 0 ? 1u : 0u);
+        }
 #pragma unroll
         for (int kk = 0; kk < C / 16; ++kk)
-          mma_ts(tmem + T_S, tmem + T_VH + kk * 8, kd + (uint64_t)(kk * 16 * 128 >> 4), ID_S,
-                 OUT || c > 0 || kk > 0 ? 1u : 0u);
+          mma_ts(tmem + T_S, tmem + T_VL + kk * 8, kd + (uint64_t)(kk * 16 * 128 >> 4), ID_S,
+                 !F16 || OUT || c > 0 || kk > 0 ? 1u : 0u);
 #pragma unroll
         for (int kk = 0; kk < C / 16; ++kk)
-          mma_ts(tmem + T_S, tmem + T_VL + kk * 8, kd + (uint64_t)(kk * 16 * 128 >> 4), ID_S, 1u);
+          mma_ts(tmem + T_S, tmem + T_VH + kk * 8, kd + (uint64_t)(kk * 16 * 128 >> 4), ID_S, 1u);
         commit(ds_done);
         commit(&empty[2 + st]);
         if (!OUT) commit(&empty[4 + st]);
@@ -415,13 +440,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
   } else if (warp < 10) {
     // ---- rows of the chunk: two threads per row i, each half of its weights (columns 64 half ..), of
-    // its decayed Q. `scale` enters with the outputs
+    // its scaled Q. `scale` enters with the outputs
     if constexpr (OUT) {
       const int quad = warp & 3, half = (warp - 2) >> 2, i = quad * 32 + lane;
       const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
       constexpr int HQ = DK / 2;               // this half's Q elements
       const uint32_t tP = tmem + lane_off + T_P + half * 64;
-      const float qs = pw(i + 1);
+      float qs;                                // lam^(i+1) = qs r: Q takes the power of two, the outputs r
+      const float rinv = 1.f / split_pow2(pw(i + 1), qs);
       float bound = 0.f;                       // at least every finite |state element| (f16)
       if (F16 && nch > 0 && wwait(smax, 0)) bound = start_bound();
       for (int c = 0; c < nch; ++c) {
@@ -432,7 +458,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           return *reinterpret_cast<const uint4*>(qrow + (q >> 3) * (C * 128) + (((q & 7) ^ (i & 7)) << 4));
         };
         if (!wwait(&full[st], sph)) break;
-        float fp = 1.f, fq = qs;
+        float fp = rinv, fq = qs;
         if constexpr (F16) {                   // c of these 32 rows
           uint32_t m = 0, mk = 0;
 #pragma unroll 4
@@ -476,7 +502,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (qm > 0 && km > 0) cexp = min(cexp, 14 - (eq + ek + (DK == 128 ? 7 : 6)));
           if (qm > 0 && sa < 100) cexp = min(cexp, sa + 14 - eq);
           cexp = max(cexp, -100);
-          fp = pow2f(cexp);
+          fp = pow2f(cexp) * rinv;
           const int qe = cexp - sa;            // (at most 14 - eq, or the state is zero)
           fq = qe < -126 ? 0.f : qs * pow2f(min(qe, 126));
           if (half == 0 && lane == 0) c_exp[ph * 4 + quad] = cexp;
@@ -499,8 +525,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const float* w = wv + C - 1 - i + b;   // lam^(i-b-e) at w[e] (past the diagonal: not used)
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float x0 = __uint_as_float(u[e]) * (F16 ? w[e] * fp : w[e]);
-              const float x1 = __uint_as_float(u[e + 1]) * (F16 ? w[e + 1] * fp : w[e + 1]);
+              const float x0 = __uint_as_float(u[e]) * (w[e] * fp);
+              const float x1 = __uint_as_float(u[e + 1]) * (w[e + 1] * fp);
               p[e / 2] = pack(T(), b + e <= i ? x0 : 0.f, b + e + 1 <= i ? x1 : 0.f);
             }
           }
@@ -508,7 +534,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           tst16(tP + 16 * k, p);
         }
 #pragma unroll 1
-        for (int k = 0; k < HQ / 32; ++k) {    // decayed Q
+        for (int k = 0; k < HQ / 32; ++k) {    // scaled Q
           uint32_t u[16];
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4) {
@@ -520,16 +546,26 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               u[4 * k4 + e] = pack(T(), f.x * fq, f.y * fq);
             }
           }
-          tst16(tP + 32 + 16 * k, u);
+          if constexpr (F16) {
+            tst16(tP + 32 + 16 * k, u);
+          } else {                             // in place
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4) {
+              const int q = half * (HQ / 8) + 4 * k + k4;
+              *reinterpret_cast<uint4*>(const_cast<uint8_t*>(qrow) + (q >> 3) * (C * 128) + (((q & 7) ^ (i & 7)) << 4)) =
+                  make_uint4(u[4 * k4], u[4 * k4 + 1], u[4 * k4 + 2], u[4 * k4 + 3]);
+            }
+          }
         }
         st_wait();
+        if (!F16) fence_async_smem();
         fence_before();
         if constexpr (F16) {                   // (before p_ready: V's maximum is there until then)
           if (!wwait(&clean[st], sph)) break;
           bound = grown(bound, min(C, end - beg - c * C), max8(vmax + st * 8), max8(kmax + ph * 8));
         }
         arrive(p_ready);
-        if (lane == 0) mbar_arrive(&empty[st]);
+        if (F16 && lane == 0) mbar_arrive(&empty[st]);
       }
     }
   } else if (warp >= 19) {
@@ -538,11 +574,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if constexpr (OUT) {
       const int quad = warp & 3, i = quad * 32 + lane;
       const uint32_t tO = tmem + ((uint32_t)(quad * 32) << 16) + T_O;
+      float p2;
+      const float fr = a.scale * split_pow2(pw(i + 1), p2);
       for (int c = 0; c < nch; ++c) {
         const int st = c & 1, n = min(C, end - beg - c * C);
         if (!wwait(o_full, c & 1) || !wwait(&v_ready[st], (c >> 1) & 1)) break;
         fence_after();
-        const float f = F16 ? a.scale * pow2f(-c_exp[(c & 1) * 4 + quad]) : a.scale;
+        const float f = F16 ? fr * pow2f(-c_exp[(c & 1) * 4 + quad]) : fr;
         const uint64_t f2 = pack2(f, f);
         const bool fix = *v_flag;
         uint8_t* stage = sm + st * L::STAGE + 2 * L::QB;
@@ -780,9 +818,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const uint8_t* col = vt + (dv >> 6) * (C * 128) + (dv & 7) * 2 + half * (64 * 128);
         const int ch = (dv & 63) >> 3;
         const float* w = wv + (n == C ? 0 : C) + half * 64;
+        if (!F16 && OUT) {                     // (the weights' columns that the third parts take)
+          if (!wwait(p_ready, c & 1)) { ok = false; break; }
+          fence_after();
+        }
 #pragma unroll 1
         for (int t0 = 0; t0 < 64; t0 += 32) {
-          uint32_t hi[16], lo[16];
+          uint32_t hi[16], lo[16], third[16];
 #pragma unroll
           for (int t = 0; t < 32; t += 4) {
             const float4 w4 = *reinterpret_cast<const float4*>(w + t0 + t);
@@ -799,10 +841,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               const float2 f = unpack(T(), hp);
               hi[(t + e) / 2] = hp;
               lo[(t + e) / 2] = pack(T(), y[e] - f.x, y[e + 1] - f.y);
+              if constexpr (!F16) {
+                const float2 g = unpack(T(), lo[(t + e) / 2]);
+                third[(t + e) / 2] = pack(T(), y[e] - f.x - g.x, y[e + 1] - f.y - g.y);
+              }
             }
           }
           tst16(tVH + t0 / 2, hi);
           tst16(tVL + t0 / 2, lo);
+          if constexpr (!F16) tst16(tmem + lane_off + T_P + half * 64 + 32 + t0 / 2, third);
         }
       }
       st_wait();
