@@ -138,8 +138,8 @@ int s1_op_kv_dequant_async(const void* codes, const float* scales, int32_t cap, 
 
 /* Attention of a batch over one shared prefix: sequence s covers rows row0[s] .. +len[s]-1
  * (host arrays; len >= 0, sequences in ascending order without overlap, unused rows between
- * them allowed: they are neither read nor written). Each of its queries attends to the P rows
- * of the snapshot and causally to its own sequence's rows:
+ * them allowed: what they hold does not matter, and they are not written). Each of its queries
+ * attends to the P rows of the snapshot and causally to its own sequence's rows:
  *   out = softmax(sm_scale q.k) v, q head h reading kv head floor(h * Hkv / Hq).
  * The prefix is read once for up to floor(128 / (Hq / Hkv)) query rows, whichever sequences
  * they belong to (s1_op_attention reads it once per sequence and q head); single tokens

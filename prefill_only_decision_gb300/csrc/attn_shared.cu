@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
         mma_ts(tO, tS + h * (BKV / 2) + kk * 8, vd + (uint64_t)(kk * 16 * 128 >> 4), ID_O, (acc || kk > 0) ? 1u : 0u);
       commit(&o_step[2 * x + h]);
     };
+    wait_prerequisites();                      // (a bounded wait must not begin while the calls before still run)
     // of each half h: P V of tile i - 1, then S of tile i into the same columns
     const int cnt = two ? n : (n + 1 - x) >> 1;
     if (cnt > 0 && wait(q_full, 0))
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
       if (j >= pl.ncache) {
         load_own(j - pl.ncache, is_v ? a.vn : a.kn, dst, is_v);
       } else if constexpr (E4M3) {
-        const bool fast = __all_sync(0xffffffffu, sc <= 128.f && __half2float(__float2half_rn(sc)) == sc);
+        const bool fast = __all_sync(0xffffffffu, fabsf(sc) <= 128.f && __half2float(__float2half_rn(sc)) == sc);
         uint8_t* d = dst + (ci >> 2) * (BKV * 128) + (lw * 32 + lane / LPR) * 128;
         const bool more = j + 1 < min(pl.ncache, je);
         const float rsc = sc;

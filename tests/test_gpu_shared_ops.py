@@ -686,3 +686,131 @@ def test_prefix_snapshot_and_questions(B):
     rows.compare()
     qs.compare()
     tok.compare()
+
+
+# ---- what a caller may do besides ------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", ["f16", "e4m3"])
+def test_snapshot_offsets_past_32_bits(B, fmt):
+    """Rows whose byte offset in a plane lies past 2^32: written and read back (e4m3), and attended to.
+    The other 2^26 (2^25) rows are zeros: five keys score 64 above them, so those weigh e^-64 each
+    (2^26 of them less than 2^-60), and the five equally: the result is the mean of five values,
+    after the weights (exactly 1) rounded once to f16, with fp32 sums: 2^-11 of the largest value."""
+    hd, n = 64, 5
+    cap = (1 << 26 if fmt == "e4m3" else 1 << 25) + 1000
+    g = np.random.default_rng(5)
+    k = torch.full((n, hd), 2.0, dtype=torch.float16, device="cuda")
+    v = torch.from_numpy(g.standard_normal((n, hd))).half().cuda()
+    if fmt == "e4m3":
+        kv = torch.zeros(2, cap, 1, hd, dtype=torch.uint8, device="cuda")
+        scales = torch.ones(2, 1, cap, device="cuda")
+        B.op_kv_quant_async(k.data_ptr(), v.data_ptr(), B.S1_F16, hd, hd, n, 1, hd, kv.data_ptr(), scales.data_ptr(),
+                            cap, cap - n, stream())
+        c, sc = quant_ref(v.double().cpu().numpy())
+        used = E4M3[c] * sc[:, None]
+        assert np.array_equal(kv[1, cap - n:, 0].cpu().numpy(), c)
+        assert not kv[:, :cap - n].any()
+        back = torch.full((2, n, hd), 7.0, dtype=torch.float16, device="cuda")
+        B.op_kv_dequant_async(kv.data_ptr(), scales.data_ptr(), cap, cap - n, n, 1, hd, back[0].data_ptr(),
+                              back[1].data_ptr(), B.S1_F16, hd, hd, stream())
+        assert np.array_equal(back[1].double().cpu().numpy(), used) and (back[0] == 2).all()
+    else:
+        kv = torch.zeros(2, cap, 1, hd, dtype=torch.float16, device="cuda")
+        kv[0, cap - n:, 0], kv[1, cap - n:, 0] = k, v
+        scales, used = None, v.double().cpu().numpy()
+    q = torch.ones(1, 1, hd, dtype=torch.float16, device="cuda")
+    out = torch.full((1, 1, hd), 55.0, dtype=torch.float16, device="cuda")
+    nb = B.op_attention_shared_workspace([1], cap, 1, 1, hd)
+    ws = torch.empty(max(nb, 16), dtype=torch.uint8, device="cuda")
+    B.op_attention_shared_async(q.data_ptr(), hd, 0, 0, 0, [0], [1], kv.data_ptr(),
+                                0 if scales is None else scales.data_ptr(),
+                                B.S1_KV_F16 if fmt == "f16" else B.S1_KV_E4M3, cap, cap, 1, 1, hd, 0.5, out.data_ptr(),
+                                ws.data_ptr(), ws.numel(), stream())
+    B.op_sync(stream())
+    err = np.abs(out[0, 0].double().cpu().numpy() - used.mean(0)).max()
+    assert err <= 2.0 ** -11 * np.abs(used).max() + 1e-7, err
+
+
+@pytest.mark.parametrize("graphs", [False, True])
+def test_calls_at_once(B, graphs):
+    """Calls on two streams, eager or replayed, each with buffers and a workspace of its own: the bits
+    of the calls made alone."""
+    ops = [Attn(B, 16, 4, 128, 5000, [3, 1], "e4m3"), Attn(B, 16, 4, 128, 5000, [40, 1, 200], "f16"),
+           Lin(B, 4, 128, 128, [900, 20], "bf16", "own"), Lin(B, 4, 128, 128, [300] * 3, "f16", "shared")]
+    alone = []
+    for a in ops:
+        a.call()
+        B.op_sync(stream())
+        alone.append((a.out.clone(), a.S_out.clone() if isinstance(a, Lin) else None))
+        a.out.fill_(55)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    pairs = [(ops[i], streams[i % 2]) for i in range(4)]
+    held = {}
+    if graphs:
+        for i, (a, st) in enumerate(pairs):
+            with torch.cuda.stream(st):
+                held[i] = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(held[i], stream=st):
+                    a.call(a.ws)
+        torch.cuda.synchronize()
+    for _ in range(8):
+        for i, (a, st) in enumerate(pairs):
+            with torch.cuda.stream(st):
+                held[i].replay() if graphs else a.call(a.ws, st.cuda_stream)
+    for st in streams:
+        B.op_sync(st.cuda_stream)
+    for a, (out, S) in zip(ops, alone):
+        assert torch.equal(a.out, out)
+        assert S is None or torch.equal(a.S_out, S)
+
+
+def test_short_calls_behind_a_long_one(B):
+    """Calls are launched while the one before still runs; none starts before its end or gives up on it."""
+    long = Attn(B, 16, 4, 128, 3000, [700] * 6, "f16")
+    short = Attn(B, 16, 4, 128, 257, [2, 1], "e4m3")
+    for a in (long, short):
+        a.call()
+    torch.cuda.synchronize()
+    one, two = long.out.clone(), short.out.clone()
+    for _ in range(5):
+        long.out.fill_(55)
+        short.out.fill_(55)
+        for a in (long, short, long, short, short):
+            a.call(a.ws)
+    B.op_sync(stream())
+    assert torch.equal(one, long.out) and torch.equal(two, short.out)
+    assert np.abs(two.double().cpu().numpy() - short.ref()).max() <= short.tol()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens", [[2, 3], [130, 128], [300]])
+def test_linattn_states_keep_fp32(B, dtype, lens):
+    """Rounded factors would show in the returned states: two bf16 parts of a decayed value leave up to
+    2^-18 of it. Parts leave at most 2^-24; fp32 decays of up to 300 rows (the log and its exponential
+    2^-23 each, once a row in the reference's terms and once a chunk here) and sums of 2^-24 a step stay
+    below 2^-20."""
+    a = Lin(B, 3, 128, 64, lens, dtype, "own", log_decay=[-0.01, -0.3, -0.0005])
+    a.call()
+    B.op_sync(stream())
+    _, _, S, A = a.ref()
+    es = np.abs(a.S_out.double().cpu().numpy() - S)
+    assert (es <= 2.0 ** -20 * A).all(), (es / (A + 1e-30)).max()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_linattn_outputs_of_a_long_memory(B, dtype):
+    """Outputs that come from the state alone (zero keys after it): Q and its decay take no rounding of
+    their own, so the error is the state's copy and the result, half a step each, and fp32's."""
+    a = Lin(B, 2, 128, 128, [100], dtype, "own", log_decay=[-0.004, -0.05])
+    q, k, v = a.parts()
+    k.zero_()
+    a.call()
+    B.op_sync(stream())
+    out, _, _, _ = a.ref()
+    qd = np.abs(q.double().cpu().numpy().reshape(100, 2, 128))
+    S0 = np.abs(a.S_in.double().cpu().numpy()[0])
+    lam = np.exp(a.ld.double().cpu().numpy())
+    mag = a.scale * np.einsum("hij,thj->thi", S0, qd) * lam[None, :, None] ** np.arange(1, 101)[:, None, None]
+    u = U[dtype]
+    err = np.abs(a.out.double().cpu().numpy() - out)
+    assert (err <= u * mag + u * np.abs(out) + 2.0 ** -18 * mag).all(), (err / (mag + 1e-30)).max() / u
