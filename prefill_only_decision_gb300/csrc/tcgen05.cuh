@@ -116,14 +116,6 @@ __device__ __forceinline__ void tma4(void* dst, const CUtensorMap* map, uint64_t
       : "memory");
 }
 
-// One 4-byte asynchronous copy into shared memory (zeros if !take), and this thread's arrival on
-// `bar` once all its copies have landed (counted in the barrier's arrivals).
-__device__ __forceinline__ void cp_async4(void* dst, const void* src, bool take) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(take ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 
 // Shared-memory matrix descriptor, 128-byte swizzle. K-major operands (rows of 64 16-bit elements,
 // 8-row groups 1024 B apart): lbo unused. MN-major operands (64-element blocks along M or N, rows
