@@ -808,6 +808,8 @@ Plan make_plan(int V, int max_len, int P, int Hq, int Hkv, int hd, int num_sms) 
   p.RT = BQ / p.G;
   p.MT = (V + p.RT - 1) / p.RT;
   p.ncache = (int)(((int64_t)P + BKV - 1) / BKV);
+  p.nt = p.ns = 1;
+  p.MP = p.MT;
   double best = -1;
   for (int nt = 1; nt <= 2 && nt <= p.MT; ++nt) {
     const int64_t MP = (p.MT + nt - 1) / nt, items = MP * Hkv;
