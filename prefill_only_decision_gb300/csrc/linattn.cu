@@ -14,7 +14,7 @@
 // about 1.3 us of tensor time. Measured: 4.0 us a chunk with all SMs busy (the chain of the state from
 // chunk to chunk through two products and two passes of the value-row warps) and 6 us before the first
 // and behind the last; 1024 rows x 16 heads f16 21.8 us, 16476 x 32 bf16
-// 202 us (its reads and writes alone: 81).
+// 194 us (its reads and writes alone: 81).
 // Operand precision: products take 16-bit operands and sum in fp32. Q, K and V enter as given: of a row's
 // decay lam^(i+1) = 2^e r, Q takes 2^e (exact), the outputs r in fp32, the weights 1 / r with their own
 // decay (a rounded decayed Q put the outputs' error at 1.57 x one rounding to the rows' type, instead of
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tma4(sm + L::STAGE + b * (DV * 128) + y * 128, from_ws ? &mapWs : &mapIn, in_full, 32 * b, y, h,
                  from_ws ? ws_slot : (a.s_in_stride ? tab.seq0 + s : 0));
       };
-      if (nch == 0 || !late) start();
+      if (nch == 0) start();
       for (int c = 0; c < nch && ok; ++c) {
         if (c == 1 && has_start) ok = mbar_wait(in_free, 0, abort_flag, &g_err, ERR_TIMEOUT);
         if (!ok) break;
@@ -347,20 +347,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           for (int b = 0; b < boxes; ++b) tma3(dst + b * C * 128, map, &full[slot], 64 * b, h, r);
           fills = (fills & ~(1u << (8 + slot))) | 1u << slot | (uint32_t)((c >> 1) & 1) << (8 + slot);
         };
-        // the chunk after the next into L2: its loads wait for slots, and then find it there
-        const int cp = c == 0 ? 1 : c + 2;
-        for (int d = cp; d <= c + 2 && d < nch; ++d) {
-          const int rp = (int)(row0 + d * C);
-          for (int b = 0; b < DK / 64; ++b) {
-            if (OUT) tma3_prefetch(&mapQ, 64 * b, h, rp);
-            tma3_prefetch(&mapK, 64 * b, h, rp);
-          }
-          for (int b = 0; b < DV / 64; ++b) tma3_prefetch(&mapV, 64 * b, h, rp);
-        }
         if (OUT) load(0, &mapQ, base, DK / 64, L::QB);
         load(1, &mapK, base + L::QB, DK / 64, L::QB);
         load(2, &mapV, base + 2 * L::QB, DV / 64, L::VB);
-        if (c == 0 && late) start();
+        if (c == 0) start();
       }
       if (*abort_flag && started) mbar_drain(in_full, 0);
       if (*abort_flag)                         // copies in flight land before the CTA leaves
