@@ -118,7 +118,7 @@ struct Lay {
   static constexpr int WV = S16 + DV * DK * 2 + 16;        // lam^(127-t), t = -1 .. 127; the same for the last
                                                            // chunk's length, t = 0 .. 127
   static constexpr int BAR = WV + 2 * C * 4;
-  static constexpr int NBAR = 28;
+  static constexpr int NBAR = 29;
   static constexpr int USED = BAR + NBAR * 8 + 52 * 4;
   static_assert(USED <= 227 * 1024, "shared memory of one CTA");
   // above half an SM: each CTA allocates all of TMEM, so two never share one
@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* in_full = bars + 26;               // the start state is in shared memory
   uint64_t* in_free = bars + 27;               // it has been taken from there
   uint64_t* k_known = bars + 25;               // max |K| of the chunk is known (f16)
+  uint64_t* p_read = bars + 28;                // Q K^T has left TMEM (bf16)
   uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // V has held a non-finite element
@@ -266,6 +267,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(k_known, 8);
     mbar_init(in_full, 1);
     mbar_init(in_free, 8);
+    mbar_init(p_read, 8);
     *abort_flag = 0;
     *v_flag = 0;
     mbar_init_fence();
@@ -542,6 +544,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           __syncwarp();
           tst16(tP + 16 * k, p);
+        }
+        if constexpr (!F16) {
+          fence_before();
+          arrive(p_read);
         }
 #pragma unroll 1
         for (int k = 0; k < HQ / 32; ++k) {    // scaled Q
@@ -832,7 +838,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int ch = (dv & 63) >> 3;
         const float* w = wv + (n == C ? 0 : C) + half * 64;
         if (!F16 && OUT) {                     // (the weights' columns that the third parts take)
-          if (!wwait(p_ready, c & 1)) { ok = false; break; }
+          if (!wwait(p_read, c & 1)) { ok = false; break; }
           fence_after();
         }
 #pragma unroll 1
