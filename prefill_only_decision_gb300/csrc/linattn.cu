@@ -13,16 +13,16 @@
 // head at 128 x 128, about 2.9 us of an SM's share of the HBM rate; the products of a chunk take
 // about 1.3 us of tensor time. Measured: 4.0 us a chunk with all SMs busy (the chain of the state from
 // chunk to chunk through two products and two passes of the value-row warps) and 6 us before the first
-// and behind the last; 1024 rows x 16 heads f16 21.8 us, 16476 x 32 bf16
-// 194 us (its reads and writes alone: 81).
+// and behind the last; 1024 rows x 16 heads f16 21.6 us, 16476 x 32 bf16 188 us
+// (its reads and writes alone: 81).
 // Operand precision: products take 16-bit operands and sum in fp32. Q, K and V enter as given: of a row's
 // decay lam^(i+1) = 2^e r, Q takes 2^e (exact), the outputs r in fp32, the weights 1 / r with their own
 // decay (a rounded decayed Q put the outputs' error at 1.57 x one rounding to the rows' type, instead of
 // 1.41). The weights of V in a chunk and the state's operand copy are rounded once to the rows' type (the
 // state itself never is). The decayed values v_j lam^(n-1-j) of the state update are split into such
 // numbers, because the state is kept and returned in fp32: two for f16 (they leave 5e-8), three for bf16
-// (two leave 2.5e-6, three put the state's error at 3e-7, most of it fp32's, and cost 202 us instead of
-// 182 on 16476 rows x 32 heads). Their products run small parts first: the sums lose less. f16 rows:
+// (two leave 2.5e-6, three put the state's error at 3e-7, most of it fp32's, and took 16476 rows x 32
+// heads from 182 to 202 us, 188 since they wait for no more than they must). Their products run small parts first: the sums lose less. f16 rows:
 // weights, scaled Q and the state's copy are scaled by powers of two so that they use f16's range whatever
 // the magnitudes: the state's copy by 2^a (from a running bound lam^n bound + n max|v| max|k| on the
 // state), the weights by 2^c (from dk max|q| max|k|, c for each 32 rows), Q by 2^(c - a), the outputs by
