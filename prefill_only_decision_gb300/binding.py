@@ -133,6 +133,14 @@ def _i32(a) -> np.ndarray:
     return np.ascontiguousarray(a, dtype=np.int32)
 
 
+def _addr(a: np.ndarray) -> int:
+    """Address of a contiguous array (`a.ctypes.data`, which takes three times as long)."""
+    try:
+        return C.addressof(C.c_char.from_buffer(a))
+    except (TypeError, ValueError):          # read-only, empty
+        return a.ctypes.data
+
+
 def _iptr(a: np.ndarray):
     return a.ctypes.data_as(C.POINTER(C.c_int32))
 
@@ -504,15 +512,15 @@ def op_attention_shared_async(q: int, q_stride: int, k_new: int, v_new: int, kv_
                               sm_scale: float, out: int, workspace: int, workspace_bytes: int, stream: int = 0):
     """Attention of a batch over one shared prefix (s1_op_attention_shared_async)."""
     r0, ln = _seq_arrays(row0, lens)
-    check(lib().s1_op_attention_shared_async(q, q_stride, k_new, v_new, kv_stride, len(r0), r0.ctypes.data,
-                                             ln.ctypes.data, kv, scales, kv_format, P, cap, Hq, Hkv, hd, sm_scale,
+    check(lib().s1_op_attention_shared_async(q, q_stride, k_new, v_new, kv_stride, len(r0), _addr(r0),
+                                             _addr(ln), kv, scales, kv_format, P, cap, Hq, Hkv, hd, sm_scale,
                                              out, workspace, workspace_bytes, stream))
 
 
 def op_attention_shared_workspace(lens, P: int, Hq: int, Hkv: int, hd: int) -> int:
     """Workspace bytes of op_attention_shared_async for these sizes on the current device."""
     ln, out = _i32(lens), C.c_int64()
-    check(lib().s1_op_attention_shared_workspace(len(ln), ln.ctypes.data, P, Hq, Hkv, hd, C.byref(out)))
+    check(lib().s1_op_attention_shared_workspace(len(ln), _addr(ln), P, Hq, Hkv, hd, C.byref(out)))
     return out.value
 
 
@@ -521,15 +529,15 @@ def op_linattn_async(q: int, k: int, v: int, dtype: int, q_stride: int, k_stride
                      out: int, workspace: int, workspace_bytes: int, stream: int = 0):
     """Linear attention with a decay per head over packed sequences (s1_op_linattn_async)."""
     r0, ln = _seq_arrays(row0, lens)
-    check(lib().s1_op_linattn_async(q, k, v, dtype, q_stride, k_stride, v_stride, log_decay, len(r0), r0.ctypes.data,
-                                    ln.ctypes.data, H, dk, dv, scale, S_in, s_in_stride, S_out, out, workspace,
+    check(lib().s1_op_linattn_async(q, k, v, dtype, q_stride, k_stride, v_stride, log_decay, len(r0), _addr(r0),
+                                    _addr(ln), H, dk, dv, scale, S_in, s_in_stride, S_out, out, workspace,
                                     workspace_bytes, stream))
 
 
 def op_linattn_workspace(lens, H: int, dk: int, dv: int) -> int:
     """Workspace bytes of op_linattn_async for these sizes on the current device."""
     ln, out = _i32(lens), C.c_int64()
-    check(lib().s1_op_linattn_workspace(len(ln), ln.ctypes.data, H, dk, dv, C.byref(out)))
+    check(lib().s1_op_linattn_workspace(len(ln), _addr(ln), H, dk, dv, C.byref(out)))
     return out.value
 
 
