@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
   uint64_t* o_step = p_full + 4;               // [2][2] the half's P V has completed
   uint64_t* o_done = o_step + 4;               // [2] the stream's last product has completed
   uint64_t* mma_idle = o_done + 2;             // [2]
-  uint64_t* joined = mma_idle + 2;                 // [4 quadrants] stream 1's sums are published
+  uint64_t* joined = mma_idle + 2;             // [4 quadrants] stream 1's sums are published
   uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // some own V element of this CTA is not finite
@@ -297,7 +297,8 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
     if (cnt > 0 && wait(q_full, 0))
       for (int i = 0; i <= cnt; ++i) {
         const int t = two ? i : 2 * i + x;
-        const Slot k = slot_of<F, FR>(two, t, false), v = slot_of<F, FR>(two, t - (two ? 1 : 2), true);   // (unused: v at i = 0, k at cnt)
+        const Slot k = slot_of<F, FR>(two, t, false);                    // (unused at i = cnt)
+        const Slot v = slot_of<F, FR>(two, t - (two ? 1 : 2), true);     // (unused at i = 0)
         auto half = [&](auto hc) {
           constexpr int h = decltype(hc)::value;
           if (i > 0) {
@@ -859,8 +860,7 @@ cudaError_t launch_group(const SharedAttnArgs& a, const SeqTab<N>& tab, const Pl
   if (pl.ns > 1) {
     const int warps = std::min(CWARPS, (pl.ns + 1) / 2);
     CK_RET(launch_pdl(combine_kernel<HD, N>, dim3((unsigned)((int64_t)pl.MT * a.Hkv * (HD / CCOLS * 4))),
-                      dim3((unsigned)(32 * warps)), 0, st,
-                      tab, a, pl));
+                      dim3((unsigned)(32 * warps)), 0, st, tab, a, pl));
   }
   return cudaSuccess;
 }
@@ -875,7 +875,9 @@ cudaError_t launch_tab(const SharedAttnArgs& a, const SeqTab<N>& tab, const Plan
 
 }  // namespace sha
 
-cudaError_t attention_shared_error_word(int** out) { return cudaGetSymbolAddress(reinterpret_cast<void**>(out), sha::g_err); }
+cudaError_t attention_shared_error_word(int** out) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(out), sha::g_err);
+}
 
 int64_t attention_shared_ws_bytes(int n_seq, const int* len, int P, int Hq, int Hkv, int hd, int num_sms) {
   int64_t need = 0;

@@ -273,7 +273,8 @@ static cudaError_t quant_t(const T* k, const T* v, int64_t ks, int64_t vs, int r
     const bool large = 2ll * n_vec * (HD / 8) >= kvc::LARGE;
     const uint32_t bl = large ? 4 * per : per;
     CK_RET(launch_pdl(large ? kvc::quant_kernel<T, HD, VEC, 4> : kvc::quant_kernel<T, HD, VEC, 1>,
-                      dim3((n_vec + bl - 1) / bl, 2), dim3(kvc::THREADS), 0, st, k + (int64_t)r * ks, v + (int64_t)r * vs, ks, vs, n_vec, Hkv, codes, scales, cap, pos0 + r));
+                      dim3((n_vec + bl - 1) / bl, 2), dim3(kvc::THREADS), 0, st, k + (int64_t)r * ks,
+                      v + (int64_t)r * vs, ks, vs, n_vec, Hkv, codes, scales, cap, pos0 + r));
   }
   return cudaSuccess;
 }
@@ -287,7 +288,8 @@ static cudaError_t dequant_t(const uint8_t* codes, const float* scales, int cap,
     const bool large = 2ll * n_vec * (HD / 8) >= kvc::LARGE;
     const uint32_t bl = large ? 4 * per : per;
     CK_RET(launch_pdl(large ? kvc::dequant_kernel<T, HD, VEC, 4> : kvc::dequant_kernel<T, HD, VEC, 1>,
-                      dim3((n_vec + bl - 1) / bl, 2), dim3(kvc::THREADS), 0, st, codes, scales, cap, pos0 + r, n_vec, Hkv, k + (int64_t)r * ks, v + (int64_t)r * vs, ks, vs));
+                      dim3((n_vec + bl - 1) / bl, 2), dim3(kvc::THREADS), 0, st, codes, scales, cap, pos0 + r, n_vec,
+                      Hkv, k + (int64_t)r * ks, v + (int64_t)r * vs, ks, vs));
   }
   return cudaSuccess;
 }

@@ -22,8 +22,9 @@
 // state itself never is). The decayed values v_j lam^(n-1-j) of the state update are split into such
 // numbers, because the state is kept and returned in fp32: two for f16 (they leave 5e-8), three for bf16
 // (two leave 2.5e-6, three put the state's error at 3e-7, most of it fp32's, and took 16476 rows x 32
-// heads from 182 to 202 us, 188 since they wait for no more than they must). Their products run small parts first: the sums lose less. f16 rows:
-// weights, scaled Q and the state's copy are scaled by powers of two so that they use f16's range whatever
+// heads from 182 to 202 us, 188 since they wait for no more than they must). Their products run small
+// parts first: the sums lose less.
+// f16 rows: weights, scaled Q and the state's copy are scaled by powers of two so that they use f16's range whatever
 // the magnitudes: the state's copy by 2^a (from a running bound lam^n bound + n max|v| max|k| on the
 // state), the weights by 2^c (from dk max|q| max|k|, c for each 32 rows), Q by 2^(c - a), the outputs by
 // 2^-c; f16's 30 binades leave room for how far above the values such bounds lie. The decayed values, with
@@ -106,7 +107,8 @@ __device__ __forceinline__ int find(const int* cum, int n, int i) {
 }
 
 // TMEM columns: weights of V, per half of 64 columns: fp32, then 16-bit in its first 32 columns and
-// the half's scaled Q (f16) or third parts of the decayed values (bf16) in its last 32 | outputs | state | low and high parts of the decayed values
+// the half's scaled Q (f16) or third parts of the decayed values (bf16) in its last 32 | outputs | state |
+// low and high parts of the decayed values
 constexpr int TMEM_COLS = 512;
 constexpr int T_P = 0, T_O = 128, T_S = 256, T_VL = 384, T_VH = 448;
 
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 6; ++i) mbar_init(&full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&empty[i], F16 ? 8 : 1);       // Q: the row warps have read it (behind its products; bf16: the outputs' products have)
+      mbar_init(&empty[i], F16 ? 8 : 1);       // Q: the row warps have read it (bf16: the outputs' products)
       mbar_init(&empty[2 + i], OUT ? 2 : 1);   // K: the products of the weights, and of the state
       mbar_init(&empty[4 + i], OUT ? 4 : 1);   // V: the outputs, staged there (!OUT: the state's products)
       mbar_init(&clean[i], 8);
@@ -274,7 +276,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
   if (warp == 1) tmem_alloc<TMEM_COLS>(tmem_slot);
   // The contributions' launch lets the next ones begin when the call's inputs are there. So the pass over
-  // the chunks behind it (split) waits for its start state only, and loads its first chunk meanwhile (1024 x 16 heads: 23.6 us without, 21.8 with).
+  // the chunks behind it (split) waits for its start state only, and loads its first chunk meanwhile (1024 x
+  // 16 heads: 23.6 us without, 21.8 with).
   const bool late = OUT && tab.split;
   if (OUT) allow_dependents();
   if (!late) wait_prerequisites();
@@ -1090,12 +1093,14 @@ static cudaError_t lin_launch(const LinAttnArgs& a, const lin::Tab& t, int64_t s
   if (slots > 0) {
     CK_RET(cudaFuncSetAttribute(lin::chunk_kernel<T, DK, DV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 L::BYTES));
-    CK_RET(launch_pdl(lin::chunk_kernel<T, DK, DV, false>, grid, block, L::BYTES, st, t, m[0], m[1], m[2], m[3], m[4], m[5], m[6], a));
+    CK_RET(launch_pdl(lin::chunk_kernel<T, DK, DV, false>, grid, block, L::BYTES, st, t, m[0], m[1], m[2], m[3],
+                      m[4], m[5], m[6], a));
     const int64_t per4 = (int64_t)a.H * DK * DV / 4;
     CK_RET(launch_pdl(lin::scan_kernel, dim3((unsigned)((per4 + 255) / 256), t.n), dim3(256), 0, st, t, a));
   }
   CK_RET(cudaFuncSetAttribute(lin::chunk_kernel<T, DK, DV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES));
-  return launch_pdl(lin::chunk_kernel<T, DK, DV, true>, grid, block, L::BYTES, st, t, m[0], m[1], m[2], m[3], m[4], m[5], m[6], a);
+  return launch_pdl(lin::chunk_kernel<T, DK, DV, true>, grid, block, L::BYTES, st, t, m[0], m[1], m[2], m[3], m[4],
+                    m[5], m[6], a);
 }
 
 cudaError_t launch_linattn(const LinAttnArgs& a, int n_seq, const int* row0, const int* len, int num_sms,
