@@ -121,7 +121,7 @@ struct Lay {
                                                            // chunk's length, t = 0 .. 127
   static constexpr int BAR = WV + 2 * C * 4;
   static constexpr int NBAR = 29;
-  static constexpr int USED = BAR + NBAR * 8 + 52 * 4;
+  static constexpr int USED = BAR + NBAR * 8 + 64 * 4;
   static_assert(USED <= 227 * 1024, "shared memory of one CTA");
   // above half an SM: each CTA allocates all of TMEM, so two never share one
   static constexpr int BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
@@ -221,10 +221,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // V has held a non-finite element
+  // What orders a slot's next write behind its last read:
+  // vmax: written for chunk c + 2 behind o_full(c), so behind p_ready(c), which the row warps arrive at after
+  //   their read of chunk c's, and behind ds_done(c), so behind the value rows' own reads up to v_ready(c).
+  // kmax: the value rows read chunk c - 1's in their iteration c, up to s_ready(c). The row warps meet that only
+  //   at p_full(c + 1) (Q K^T of c + 1 is issued behind the outputs of c), so two slots are too few: three, and
+  //   the write for chunk c + 2 comes behind p_full(c + 1).
+  // c_exp: the output warps read chunk c's up to o_free(c), which the outputs of c + 1 wait for, and Q K^T of
+  //   c + 2 is behind those: three slots, and the write for chunk c + 3 comes behind p_full(c + 2).
+  // wmax: written once. v_flag: only ever set.
   volatile int* vmax = (volatile int*)(tmem_slot + 3);     // [2 stages][8 warps] max |V| as f16 bits
-  volatile int* kmax = (volatile int*)(tmem_slot + 19);    // [2][8] max |K|, by chunk parity
-  volatile float* wmax = (volatile float*)(tmem_slot + 35);  // [8] max |start state| per warp
-  volatile int* c_exp = (volatile int*)(tmem_slot + 43);   // [2][4] c of 32 rows, by chunk parity (f16)
+  volatile int* kmax = (volatile int*)(tmem_slot + 19);    // [3][8] max |K|, by chunk mod 3
+  volatile float* wmax = (volatile float*)(tmem_slot + 43);  // [8] max |start state| per warp
+  volatile int* c_exp = (volatile int*)(tmem_slot + 51);   // [3][4] c of 32 rows, by chunk mod 3 (f16)
   float* wv = reinterpret_cast<float*>(sm + L::WV);
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -507,10 +516,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
           }
           mk = __reduce_max_sync(0xffffffffu, max(mk & 0xffffu, mk >> 16));
-          if (lane == 0) kmax[ph * 8 + warp - 2] = (int)mk;
+          if (lane == 0) kmax[c % 3 * 8 + warp - 2] = (int)mk;
           arrive(k_known);
           if (!wwait(k_known, ph)) break;
-          const uint32_t km = max8(kmax + ph * 8);
+          const uint32_t km = max8(kmax + c % 3 * 8);
           const int sa = scale_exp(bound);
           const int eq = exp_above(h_bits(qm)), ek = exp_above(h_bits(km));
           int cexp = 100;
@@ -520,7 +529,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           fp = pow2f(cexp) * rinv;
           const int qe = cexp - sa;            // (at most 14 - eq, or the state is zero)
           fq = qe < -126 ? 0.f : qs * pow2f(min(qe, 126));
-          if (half == 0 && lane == 0) c_exp[ph * 4 + quad] = cexp;
+          if (half == 0 && lane == 0) c_exp[c % 3 * 4 + quad] = cexp;
         }
         if (!wwait(p_full, ph)) break;
         fence_after();
@@ -581,7 +590,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         fence_before();
         if constexpr (F16) {                   // (before p_ready: V's maximum is there until then)
           if (!wwait(&clean[st], sph)) break;
-          bound = grown(bound, min(C, end - beg - c * C), max8(vmax + st * 8), max8(kmax + ph * 8));
+          bound = grown(bound, min(C, end - beg - c * C), max8(vmax + st * 8), max8(kmax + c % 3 * 8));
         }
         arrive(p_ready);
         if (F16 && lane == 0) mbar_arrive(&empty[st]);
@@ -601,7 +610,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int st = c & 1, n = min(C, end - beg - c * C);
         if (!wwait(o_full, c & 1) || !wwait(&v_ready[st], (c >> 1) & 1)) break;
         fence_after();
-        const float f = F16 ? fr * pow2f(-c_exp[(c & 1) * 4 + quad]) : fr;
+        const float f = F16 ? fr * pow2f(-c_exp[c % 3 * 4 + quad]) : fr;
         const uint64_t f2 = pack2(f, f);
         const bool fix = *v_flag;
         uint8_t* stage = sm + st * L::STAGE + 2 * L::QB;
@@ -794,7 +803,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (OUT && c > 0 && !wwait(o_full, (c - 1) & 1)) { ok = false; break; }   // (its state copy has been read)
       int bnew = 0, sa = 0;
       if constexpr (F16) {                     // decayed values below 2^14, and the scaled state finite
-        if (OUT && c > 0) bound = grown(bound, C, vm, max8(kmax + (st ^ 1) * 8));
+        if (OUT && c > 0) bound = grown(bound, C, vm, max8(kmax + (c - 1) % 3 * 8));
         vm = max8(vmax + st * 8);
         if (vm > 0) bnew = 14 - exp_above(h_bits(vm));
         if (bound > 0.f) bnew = min(bnew, 120 - exp_above(bound));

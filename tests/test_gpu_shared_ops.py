@@ -814,3 +814,60 @@ def test_linattn_outputs_of_a_long_memory(B, dtype):
     u = U[dtype]
     err = np.abs(a.out.double().cpu().numpy() - out)
     assert (err <= u * mag + u * np.abs(out) + 2.0 ** -18 * mag).all(), (err / (mag + 1e-30)).max() / u
+
+
+class LongLin(Lin):
+    """As Lin, with the recurrence in 64 bits on the GPU (all heads of a row at once), for thousands of rows."""
+
+    def ref(self):
+        q, k, v = (t.double().reshape(self.R, self.H, -1) for t in self.parts())
+        lam = torch.exp(self.ld.double().clamp(max=0))[:, None, None]
+        out = torch.full((self.R, self.H, self.dv), 55.0, dtype=torch.float64, device="cuda")
+        mag = torch.zeros_like(out)
+        Ss, As = [], []
+        for s, (r0, n) in enumerate(zip(self.row0, self.lens)):
+            S = torch.zeros(self.H, self.dv, self.dk, dtype=torch.float64, device="cuda")
+            if self.S_in is not None:
+                S = self.S_in[s if self.state == "own" else 0].double()
+            A = S.abs()
+            for t in range(r0, r0 + n):
+                x = v[t][:, :, None] * k[t][:, None, :]
+                S, A = lam * S + x, lam * A + x.abs()
+                out[t] = self.scale * (S @ q[t][:, :, None])[..., 0]
+                mag[t] = self.scale * (A @ q[t].abs()[:, :, None])[..., 0]
+            Ss.append(S)
+            As.append(A)
+        return tuple(x.cpu().numpy() for x in (out, mag, torch.stack(Ss), torch.stack(As)))
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 128)])
+def test_linattn_f16_many_chunks_at_full_load(B, dk, dv):
+    """Every SM works through many f16 chunks whose magnitudes differ by 2^12 (keys and values by 2^6 each
+    from one chunk to the next, queries with a period of three): each chunk's scales are its own. Against the
+    recurrence (compare()'s tolerance), and the same bits 50 times, alone and beside a call on another stream."""
+    lens = [2900, 2817, 3000, 2560, 2700]
+    a = LongLin(B, 32, dk, dv, lens, "f16", "own")
+    q, k, v = a.parts()
+    for r0, n in zip(a.row0, a.lens):
+        c = torch.arange(n, device="cuda") // 128
+        loud = torch.where(c % 2 == 0, 8.0, 0.125).half()[:, None]
+        k[r0:r0 + n] *= loud
+        v[r0:r0 + n] *= loud
+        q[r0:r0 + n] *= (2.0 ** (-2.0 * (c % 3))).half()[:, None]
+    a.check()
+    one, S = a.out.clone(), a.S_out.clone()
+    b = Lin(B, 32, dk, dv, [1500, 1400, 1300], "f16", "shared", seed=2)
+    b.call()
+    torch.cuda.synchronize()
+    b_one = b.out.clone()
+    other = torch.cuda.Stream()
+    for i in range(50):
+        a.out.fill_(55)
+        a.S_out.fill_(9)
+        if i >= 25:
+            b.call(b.ws, other.cuda_stream)
+        a.call(a.ws)
+        assert torch.equal(a.out, one) and torch.equal(a.S_out, S), i
+    B.op_sync(other.cuda_stream)
+    B.op_sync(stream())
+    assert torch.equal(b.out, b_one)
