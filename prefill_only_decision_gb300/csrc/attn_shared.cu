@@ -390,8 +390,9 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
     };
     auto prefetch = [&](int j) {
       const int key = j * BKV + lw * 32 + lane;
-      if (j < min(pl.ncache, je) && key < a.P) l2_prefetch(codes + key * krow);
-      if (lane == 0 && j < min(pl.ncache, je)) l2_prefetch(scales + j * BKV + lw * 32);
+      if (j >= min(pl.ncache, je) || key >= a.P) return;   // (nothing behind the prefix: it may end the allocation)
+      l2_prefetch(codes + key * krow);
+      if (lane == 0) l2_prefetch(scales + key);
     };
     wait_prerequisites();
     if constexpr (E4M3)

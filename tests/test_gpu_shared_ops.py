@@ -871,3 +871,13 @@ def test_linattn_f16_many_chunks_at_full_load(B, dk, dv):
     B.op_sync(other.cuda_stream)
     B.op_sync(stream())
     assert torch.equal(b.out, b_one)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("P", [1, 33, 100, 129, 1000])
+def test_attention_snapshot_without_spare_rows(B, P, hd):
+    """An 8-bit snapshot of exactly P rows, codes and scales each the whole of their allocation, whose
+    last key tile is not full."""
+    a = Attn(B, 4, 2, hd, P, [3, 1], "e4m3")
+    a.kv, a.scales, a.cap = a.kv[:, :P].contiguous(), a.scales[:, :, :P].contiguous(), P
+    a.check()
