@@ -26,10 +26,14 @@
 // parts first: the sums lose less.
 // f16 rows: weights, scaled Q and the state's copy are scaled by powers of two so that they use f16's range whatever
 // the magnitudes: the state's copy by 2^a (from a running bound lam^n bound + n max|v| max|k| on the
-// state), the weights by 2^c (from dk max|q| max|k|, c for each 32 rows), Q by 2^(c - a), the outputs by
-// 2^-c; f16's 30 binades leave room for how far above the values such bounds lie. The decayed values, with
-// the state they are added to, are scaled by 2^b (b per chunk), so that the low parts stay above f16's
-// smallest number.
+// state before the chunk), a row's weights by 2^c, its Q by 2^(c - a) and its outputs by 2^-c, with c from the
+// row's own largest weight and largest |q|: a row's scales depend on nothing that it does not see, and a large
+// element costs only rows that have it in their sums anyway. (c for 32 rows at once from dk max|q| max|k| of the
+// whole chunk needed one pass over the weights less, 16384 rows x 32 heads 212 us instead of 217, 8000 x 16 of 64
+// 52 instead of 56, but a key of 4000 in a later row cost ordinary rows before it percents.) What lies 2^28 below such a maximum loses bits; bounds lie far less above the values. The decayed
+// values, with the state they are added to, are scaled by 2^b (b per chunk), so that the low parts stay above f16's
+// smallest number: a value keeps fp32's accuracy down to 2^-15 of the chunk's largest, below that it is off by at
+// most 2^-38 of that.
 // Where: f16's scaled Q is in TMEM beside the weights; bf16's is in its shared-memory tile, and the third
 // parts take its TMEM columns (so they wait for the weights, and the next Q K^T waits for them).
 // One CTA per SM, 23 warps: 0 TMA producer (two stages of Q, K, V); 1 and 18 MMA issue (1: Q K^T and
@@ -120,8 +124,8 @@ struct Lay {
   static constexpr int WV = S16 + DV * DK * 2 + 16;        // lam^(127-t), t = -1 .. 127; the same for the last
                                                            // chunk's length, t = 0 .. 127
   static constexpr int BAR = WV + 2 * C * 4;
-  static constexpr int NBAR = 29;
-  static constexpr int USED = BAR + NBAR * 8 + 64 * 4;
+  static constexpr int NBAR = 33;
+  static constexpr int USED = BAR + NBAR * 8 + (51 + 64 + 64) * 4;
   static_assert(USED <= 227 * 1024, "shared memory of one CTA");
   // above half an SM: each CTA allocates all of TMEM, so two never share one
   static constexpr int BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
@@ -218,6 +222,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* in_free = bars + 27;               // it has been taken from there
   uint64_t* k_known = bars + 25;               // max |K| of the chunk is known (f16)
   uint64_t* p_read = bars + 28;                // Q K^T has left TMEM (bf16)
+  uint64_t* r_known = bars + 29;               // [4 quadrants] both halves of its rows' largest weights are known (f16)
   uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // V has held a non-finite element
@@ -227,13 +232,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   // kmax: the value rows read chunk c - 1's in their iteration c, up to s_ready(c). The row warps meet that only
   //   at p_full(c + 1) (Q K^T of c + 1 is issued behind the outputs of c), so two slots are too few: three, and
   //   the write for chunk c + 2 comes behind p_full(c + 1).
-  // c_exp: the output warps read chunk c's up to o_free(c), which the outputs of c + 1 wait for, and Q K^T of
-  //   c + 2 is behind those: three slots, and the write for chunk c + 3 comes behind p_full(c + 2).
+  // w_exp: read up to p_ready(c), written for chunk c + 1 behind p_full(c + 1), so behind the outputs of c.
+  // c_exp: the output warps read chunk c's up to o_free(c), which the outputs of c + 1 wait for; written for
+  //   chunk c + 2 behind p_full(c + 2), so behind those.
   // wmax: written once. v_flag: only ever set.
   volatile int* vmax = (volatile int*)(tmem_slot + 3);     // [2 stages][8 warps] max |V| as f16 bits
   volatile int* kmax = (volatile int*)(tmem_slot + 19);    // [3][8] max |K|, by chunk mod 3
   volatile float* wmax = (volatile float*)(tmem_slot + 43);  // [8] max |start state| per warp
-  volatile int* c_exp = (volatile int*)(tmem_slot + 51);   // [3][4] c of 32 rows, by chunk mod 3 (f16)
+  volatile signed char* c_exp = (volatile signed char*)(tmem_slot + 51);    // [2][128] c of the rows, by chunk parity (f16)
+  volatile signed char* w_exp = (volatile signed char*)(tmem_slot + 115);   // [2 halves][128] the rows' weights are below
+                                                                            // 2^(w_exp + 2); -128: zeros (f16)
   float* wv = reinterpret_cast<float*>(sm + L::WV);
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -279,6 +287,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(in_full, 1);
     mbar_init(in_free, 8);
     mbar_init(p_read, 8);
+    for (int i = 0; i < 4; ++i) mbar_init(&r_known[i], 2);
     *abort_flag = 0;
     *v_flag = 0;
     mbar_init_fence();
@@ -319,7 +328,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int k = 0; k < 8; ++k) x = fmaxf(x, wmax[k]);
     return x;
   };
-  auto scale_exp = [](float bound) { return bound > 0.f ? max(-100, min(100, 14 - exp_above(bound))) : 100; };
+  auto scale_exp = [](float bound) { return bound > 0.f ? max(-114, min(100, 14 - exp_above(bound))) : 100; };
   auto grown = [&](float bound, int n, uint32_t vm, uint32_t km) {
     // (each product rounded by itself: two roles form the same number)
     const float add = __fmul_rn(__fmul_rn(1.00001f * (float)n, h_bits(vm)), h_bits(km));
@@ -483,17 +492,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         };
         if (!wwait(&full[st], sph)) break;
         float fp = rinv, fq = qs;
-        if constexpr (F16) {                   // c of these 32 rows
+        uint32_t qm = 0;                       // max |Q| of the row (f16)
+        if constexpr (F16) {
           uint32_t m = 0, mk = 0;
 #pragma unroll 4
           for (int q = 0; q < DK / 8; ++q) {
             const uint4 v = q16(q);
             m = absmax2(T(), m, absmax2(T(), absmax2(T(), v.x, v.y), absmax2(T(), v.z, v.w)));
           }
-          // (rows with a non-finite element, and rows of another sequence, take no part)
-          uint32_t qm = max(m & 0xffffu, m >> 16);
-          if (qm >= 0x7c00u || i >= end - beg - c * C) qm = 0;
-          qm = __reduce_max_sync(0xffffffffu, qm);
+          qm = max(m & 0xffffu, m >> 16);
+          if (qm >= 0x7c00u) qm = 0;           // (a row with a non-finite element: no scale makes its outputs finite)
           // this warp's share of K; rows past the end and non-finite elements aside
           const int n = min(C, end - beg - c * C), k0 = (warp - 2) * (L::QB / 8) + lane * 16;
           if (!wwait(&full[2 + st], sph)) break;
@@ -518,21 +526,45 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           mk = __reduce_max_sync(0xffffffffu, max(mk & 0xffffu, mk >> 16));
           if (lane == 0) kmax[c % 3 * 8 + warp - 2] = (int)mk;
           arrive(k_known);
-          if (!wwait(k_known, ph)) break;
-          const uint32_t km = max8(kmax + c % 3 * 8);
-          const int sa = scale_exp(bound);
-          const int eq = exp_above(h_bits(qm)), ek = exp_above(h_bits(km));
-          int cexp = 100;
-          if (qm > 0 && km > 0) cexp = min(cexp, 14 - (eq + ek + (DK == 128 ? 7 : 6)));
-          if (qm > 0 && sa < 100) cexp = min(cexp, sa + 14 - eq);
-          cexp = max(cexp, -100);
-          fp = pow2f(cexp) * rinv;
-          const int qe = cexp - sa;            // (at most 14 - eq, or the state is zero)
-          fq = qe < -126 ? 0.f : qs * pow2f(min(qe, 126));
-          if (half == 0 && lane == 0) c_exp[c % 3 * 4 + quad] = cexp;
         }
         if (!wwait(p_full, ph)) break;
         fence_after();
+        if constexpr (F16) {                   // c of the row, from its own weights: fp32, decayed, in place
+          float mx = 0.f;
+#pragma unroll 1
+          for (int k = 0; k < 2; ++k) {
+            const int b = 64 * half + 32 * k;
+            if (b > quad * 32) break;
+            uint32_t u[32];
+            __syncwarp();
+            tld32(tP + 32 * k, u);
+            ld_wait();
+            pin32(u);
+            const float* w = wv + C - 1 - i + b;   // lam^(i-b-e) at w[e] (past the diagonal: not used)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float x = b + e <= i ? __uint_as_float(u[e]) * w[e] : 0.f;
+              mx = fmaxf(mx, fabsf(x));
+              u[e] = __float_as_uint(x);
+            }
+            tst32(tP + 32 * k, u);
+          }
+          st_wait();
+          w_exp[half * C + i] = (signed char)(mx > 0.f ? exp_above(mx) - 2 : -128);   // (-125 .. 129, - 2)
+          arrive(&r_known[quad]);
+          if (!wwait(&r_known[quad], ph)) break;
+          const int we = max(w_exp[i], w_exp[C + i]), sa = scale_exp(bound);
+          int cexp = 100;
+          if (we > -128) cexp = min(cexp, 12 - we);
+          // (q 2^e, where qs = 2^e or, below the normal numbers, less than 2^-126)
+          const int eq = exp_above(h_bits(qm)) + max((int)(__float_as_uint(qs) >> 23), 1) - 127;
+          if (qm > 0 && qs > 0.f && sa < 100) cexp = min(cexp, sa + 14 - eq);
+          cexp = max(cexp, -120);
+          fp = pow2f(cexp) * rinv;
+          const int qe = cexp - sa;            // |q| qs 2^qe < 2^14, or the state is zero
+          fq = qe < -126 ? 0.f : qe > 126 ? qs * pow2f(126) * pow2f(qe - 126) : qs * pow2f(qe);
+          if (half == 0) c_exp[ph * C + i] = (signed char)cexp;
+        }
 #pragma unroll 1
         for (int k = 0; k < 2; ++k) {
           // 32 weights of V: lam^(i-j) q_i.k_j, 0 for j > i; 16-bit in place, behind what is still to be read
@@ -543,15 +575,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int e = 0; e < 16; ++e) p[e] = 0;
           } else {
             uint32_t u[32];
+            __syncwarp();
             tld32(tP + 32 * k, u);
             ld_wait();
             pin32(u);
-            const float* w = wv + C - 1 - i + b;   // lam^(i-b-e) at w[e] (past the diagonal: not used)
+            if constexpr (F16) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float x0 = __uint_as_float(u[e]) * (w[e] * fp);
-              const float x1 = __uint_as_float(u[e + 1]) * (w[e + 1] * fp);
-              p[e / 2] = pack(T(), b + e <= i ? x0 : 0.f, b + e + 1 <= i ? x1 : 0.f);
+              for (int e = 0; e < 32; e += 2)
+                p[e / 2] = pack(T(), __uint_as_float(u[e]) * fp, __uint_as_float(u[e + 1]) * fp);
+            } else {
+              const float* w = wv + C - 1 - i + b;   // lam^(i-b-e) at w[e] (past the diagonal: not used)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float x0 = __uint_as_float(u[e]) * (w[e] * fp);
+                const float x1 = __uint_as_float(u[e + 1]) * (w[e + 1] * fp);
+                p[e / 2] = pack(T(), b + e <= i ? x0 : 0.f, b + e + 1 <= i ? x1 : 0.f);
+              }
             }
           }
           __syncwarp();
@@ -589,7 +628,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (!F16) fence_async_smem();
         fence_before();
         if constexpr (F16) {                   // (before p_ready: V's maximum is there until then)
-          if (!wwait(&clean[st], sph)) break;
+          if (!wwait(&clean[st], sph) || !wwait(k_known, ph)) break;
           bound = grown(bound, min(C, end - beg - c * C), max8(vmax + st * 8), max8(kmax + c % 3 * 8));
         }
         arrive(p_ready);
@@ -610,7 +649,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int st = c & 1, n = min(C, end - beg - c * C);
         if (!wwait(o_full, c & 1) || !wwait(&v_ready[st], (c >> 1) & 1)) break;
         fence_after();
-        const float f = F16 ? fr * pow2f(-c_exp[c % 3 * 4 + quad]) : fr;
+        const float f = F16 ? fr * pow2f(-c_exp[(c & 1) * C + i]) : fr;
         const uint64_t f2 = pack2(f, f);
         const bool fix = *v_flag;
         uint8_t* stage = sm + st * L::STAGE + 2 * L::QB;

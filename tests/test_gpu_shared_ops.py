@@ -881,3 +881,41 @@ def test_attention_snapshot_without_spare_rows(B, P, hd):
     a = Attn(B, 4, 2, hd, P, [3, 1], "e4m3")
     a.kv, a.scales, a.cap = a.kv[:, :P].contiguous(), a.scales[:, :, :P].contiguous(), P
     a.check()
+
+
+def _outlier_call(B, which, value, lens, state, dtype, log_decay):
+    a = Lin(B, 2, 128, 128, lens, dtype, state, log_decay=log_decay, seed=11)
+    a.scale = 2.0 ** -10                 # (outputs of the outlier's own rows within f16)
+    if value is not None:
+        if which == "S":
+            a.S_in[-1, 0, 7, 9] = value
+        else:
+            a.parts()["qkv".index(which)][a.row0[1] + which_row(which), 5] = value
+    return a
+
+
+def which_row(which):
+    return 31 if which in "qv" else 127
+
+
+@pytest.mark.parametrize("log_decay", [[-0.01, -0.01], [-1.5, -0.01], [-0.0005, -0.3]])
+@pytest.mark.parametrize("state", ["none", "own"])
+@pytest.mark.parametrize("value", [256.0, 4000.0, 60000.0])
+@pytest.mark.parametrize("which", ["q", "k", "v", "S"])
+def test_linattn_f16_outliers(B, which, value, state, log_decay):
+    """One large finite element (row 31 or 127 of the second sequence, or of its initial state): the rows
+    that do not see it keep their bits, those that do keep compare()'s tolerance (their sums of magnitudes
+    hold the large terms only where the formula has them)."""
+    if which == "S" and state == "none":
+        pytest.skip("no initial state")
+    lens = [40, 300]
+    a = _outlier_call(B, which, value, lens, state, "f16", log_decay)
+    b = _outlier_call(B, which, None, lens, state, "f16", log_decay)
+    a.check()
+    b.check()
+    first = 0 if which == "S" else a.row0[1] + which_row(which)
+    assert torch.equal(a.out[:40], b.out[:40]) and torch.equal(a.out[:, 1], b.out[:, 1])
+    assert torch.equal(a.out[:max(first, 40)], b.out[:max(first, 40)])
+    assert torch.equal(a.S_out[0], b.S_out[0])
+    if which == "q":
+        assert torch.equal(a.out[first + 1:], b.out[first + 1:]) and torch.equal(a.S_out, b.S_out)
