@@ -22,7 +22,7 @@
 //   warps 1, 14 MMA issue of stream 0 and 1
 //   warps 2-5, 6-9  softmax of stream 0, 1: one thread per row (TMEM lane), 64 scores in registers.
 //               Running max with a lazy rescale (O and l move only when the row's maximum grows by more
-//               than 2^8, once the last P V has completed). P (f16) goes back into the TMEM columns of
+//               than 2^GROW, once the last P V has completed). P (f16) goes back into the TMEM columns of
 //               S and is the A operand of O += P V from there: no shared-memory round trip. Warps whose
 //               32 rows are all past the tile's last row leave at once: their polling slowed the others.
 //   warps 10-13 loaders: the batch's own keys (gathered row by row through the sequence table), and
@@ -58,6 +58,12 @@ constexpr int threads_of(bool e4m3) { return (e4m3 ? 19 : 15) * 32; }
 constexpr int TMEM_COLS = 512;               // S of stream x at 128 x, O at 256 + 128 x
 constexpr int T_O = 256;
 constexpr int ERR_TIMEOUT = 0x401;
+// Weights are 2^(z - m + HEAD), z the score and m the running maximum (log2 domain), which a row's maximum may
+// pass by GROW before it moves: at most 2^15, within f16. So a weight keeps f16's precision down to 2^-24 of
+// the largest, and one that is lost is below 2^-35 of it: 65536 of those are 2^-19 of the result. (HEAD = 0 and
+// GROW = 8 lost what lies below 2^-25: behind a sink, all of the result. GROW of 8, 6, 5, 4, 3 with HEAD = 15 -
+// GROW: 1340 rows over 65536 keys 472, 471, 473, 478, 484 us.)
+constexpr float GROW = 5.f, HEAD = 15.f - GROW;
 
 __device__ int g_err;                        // bounded waits record here (one word per device)
 
@@ -538,11 +544,11 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
           mx4[e] = fmaxf(mx4[e], fmaxf(__uint_as_float(u[k + e]), __uint_as_float(u[k + 4 + e])));
       const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
       float alpha = 1.f;
-      if (mx > m + 8.f) {
+      if (mx > m + GROW) {
         alpha = m == -INFINITY ? 1.f : ex2(m - mx);
         m = mx;
       }
-      const float base = m == -INFINITY ? 0.f : m;
+      const float base = m == -INFINITY ? 0.f : m - HEAD;
       if (li > 1 && __any_sync(0xffffffffu, alpha != 1.f)) {   // once the last P V has completed
         if (!wwait(&o_step[2 * x + (hh ^ 1)], ((li - 2) >> 1) & 1)) { ok = false; break; }
         fence_after();

@@ -919,3 +919,35 @@ def test_linattn_f16_outliers(B, which, value, state, log_decay):
     assert torch.equal(a.S_out[0], b.S_out[0])
     if which == "q":
         assert torch.equal(a.out[first + 1:], b.out[first + 1:]) and torch.equal(a.S_out, b.S_out)
+
+
+@pytest.mark.parametrize("fmt", ["f16", "e4m3"])
+@pytest.mark.parametrize("gap", [12.0, 16.0, 17.0, 18.0])
+@pytest.mark.parametrize("where", [0, 65535, 30001])
+def test_attention_sink(B, fmt, gap, where):
+    """One key scores `gap` above 65535 equal others and has the value zero (an attention sink): the result is
+    the others' mean value times their share of the weights. Their weights are equal, so each is rounded to f16
+    alike: by half a step, 2^-11, where e^-gap >= 2^-24, else by 2^-35 of the sink's weight; the result's own
+    rounding is 2^-11 of it. fp32 scores and exponentials are off by less than 2^-18, and the tensor cores' sums of
+    at most 4096 steps, each dropping less than 2^-23 of the sum so far, by less than 2^-12."""
+    hd, P = 64, 65536
+    g = np.random.default_rng(4)
+    v = torch.from_numpy(1 + 0.25 * g.random((P, hd))).half()
+    v[where] = 0
+    k = torch.zeros(P, hd).half()
+    k[where] = 2                             # scale 1 / 8, q = gap / 16: score 64 * 2 * gap / 128
+    a = Attn(B, 1, 1, hd, P, [1], fmt, own=False)
+    a.x[:] = gap / 16
+    src = torch.stack([k, v]).cuda().contiguous()
+    if fmt == "f16":
+        a.kv[:, :P, 0] = src
+        used = v.double().numpy()
+    else:
+        B.op_kv_quant_async(src[0].data_ptr(), src[1].data_ptr(), B.S1_F16, hd, hd, P, 1, hd, a.kv.data_ptr(),
+                            a.scales.data_ptr(), a.cap, 0, stream())
+        used = E4M3[a.kv[1, :P, 0].cpu().numpy()] * a.scales[1, 0, :P].double().cpu().numpy()[:, None]
+    ref = used.sum(0) / (P - 1 + math.exp(gap))
+    a.call()
+    B.op_sync(stream())
+    err = np.abs(a.out[0, 0].double().cpu().numpy() - ref) / ref
+    assert err.max() <= max(2.0 ** -11, 2.0 ** -35 * math.exp(gap)) + 2.0 ** -11 + 2.0 ** -12 + 2.0 ** -18, err.max()
