@@ -565,6 +565,7 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
         l2 = mul2(l2, pack2(alpha, alpha));
       }
       const uint64_t nb = pack2(-base, -base);
+      uint64_t sum2 = 0;                       // (of this half: one by one, small weights would not reach a large sum)
 #pragma unroll
       for (int c = 0; c < 64; c += 32) {
         uint32_t pk[16];
@@ -572,11 +573,12 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
         for (int e = 0; e < 32; e += 2) {
           const uint64_t z = fma2(pack2u(u[c + e], u[c + e + 1]), sl2_2, nb);
           const float p0 = ex2(lo2(z)), p1 = ex2(hi2(z));
-          l2 = add2(l2, pack2(p0, p1));
+          sum2 = add2(sum2, pack2(p0, p1));
           pk[e / 2] = h2u(p0, p1);
         }
         tst16(tS + hh * 64 + c / 2, pk);
       }
+      l2 = add2(l2, sum2);
       st_wait();
       fence_before();
       __syncwarp();
@@ -808,7 +810,10 @@ __global__ void __launch_bounds__(CWARPS * 32, 4)
 // with two query tiles and 0.66 with one, or as long as all CTAs' tiles need at 14 TB/s. Against the
 // best of 80 forced choices, over 10 calls from 64 rows x 1024 to 1470 x 20000: within 8 %, mostly 3 %.
 // (16 q heads, 128 rows over 2048: one part 19.2 us, seven 12.9; two tiles an item 28.1 and 14.1.) At most
-// 64 parts, at most 8 CTAs an SM.
+// 64 parts, at most 8 CTAs an SM; and at least as many parts as keep each to LONGEST key tiles, whatever the
+// estimate: the tensor cores add to one sum per output and drop what lies below its last bits (2^18, 2^20 keys of
+// equal weight in one part: results 0.11, 0.61 percent low; in parts of at most LONGEST tiles 0.003 at both).
+constexpr int LONGEST = 1024;
 Plan make_plan(int V, int max_len, int P, int Hq, int Hkv, int hd, int num_sms) {
   Plan p;
   p.V = V;
@@ -822,7 +827,8 @@ Plan make_plan(int V, int max_len, int P, int Hq, int Hkv, int hd, int num_sms) 
   for (int nt = 1; nt <= 2 && nt <= p.MT; ++nt) {
     const int64_t MP = (p.MT + nt - 1) / nt, items = MP * Hkv;
     const int64_t total = p.ncache + (std::min<int64_t>(V, (int64_t)max_len - 1 + nt * p.RT) + BKV - 1) / BKV;
-    for (int ns = 1; ns <= 64 && ns <= total && (ns == 1 || items * ns <= 8ll * num_sms); ++ns) {
+    const int least = (int)std::min<int64_t>(64, (total + LONGEST - 1) / LONGEST);
+    for (int ns = least; ns <= 64 && ns <= total && (ns == least || items * ns <= 8ll * num_sms); ++ns) {
       const int64_t ctas = items * ns;
       const double waves = (double)((ctas + num_sms - 1) / num_sms);
       const double l2 = (double)std::min<int64_t>(ctas, num_sms) * (4 * BKV) * hd / 14e6;

@@ -951,3 +951,25 @@ def test_attention_sink(B, fmt, gap, where):
     B.op_sync(stream())
     err = np.abs(a.out[0, 0].double().cpu().numpy() - ref) / ref
     assert err.max() <= max(2.0 ** -11, 2.0 ** -35 * math.exp(gap)) + 2.0 ** -11 + 2.0 ** -12 + 2.0 ** -18, err.max()
+
+
+def test_attention_sink_first_of_a_million(B):
+    """A sink 17 above the 2^20 - 1 keys behind it, for so many rows that their sums need no split over CTAs: the
+    small weights (2^-24.5 of the sink's) together weigh 4 percent, and reach the sum although each alone is below
+    half of its last bit. A half tile's 32 terms a lane are exact to 2^-19 and together 11.07 steps (2^-13) of a
+    sum of 2^10, so at least 11 are added: 0.7 percent of those 4, 2^-11 of the sum. Else as in
+    test_attention_sink, with 2^-8 for the products' sums."""
+    hd, P, Hq, rows, gap = 64, 1 << 20, 4, 9728, 17.0
+    g = np.random.default_rng(4)
+    v = torch.from_numpy(1 + 0.25 * g.random((P, hd))).half().cuda()
+    v[0] = 0
+    a = Attn(B, Hq, 1, hd, P, [rows], "f16", own=False)
+    a.x[:] = gap / 16
+    a.kv[0, :P] = 0
+    a.kv[0, 0] = 2
+    a.kv[1, :P, 0] = v
+    ref = v.double().sum(0).cpu().numpy() / (P - 1 + math.exp(gap))
+    a.call()
+    B.op_sync(stream())
+    err = np.abs(a.out.double().cpu().numpy() - ref) / ref
+    assert err.max() <= 2.0 ** -35 * math.exp(gap) + 2 * 2.0 ** -11 + 2.0 ** -8 + 2.0 ** -18, err.max()
