@@ -166,7 +166,8 @@ int s1_op_attention_shared_workspace(int32_t n_seq, const int32_t* len, int32_t 
  *   S_t = exp(log_decay[h]) S_{t-1} + v_t k_t^T,   o_t = scale * S_t q_t.
  * q, k [., H, dk], v [., H, dv] of dtype S1_F16 or S1_BF16, row strides in elements (multiples
  * of 8, 16-byte aligned pointers); dk, dv 64 or 128. log_decay: fp32 [H], <= 0 (-inf: no
- * memory); larger values count as 0. row0, len: as in s1_op_attention_shared_async.
+ * memory); larger values count as 0, NaN makes the head's outputs and states NaN. row0, len: as
+ * in s1_op_attention_shared_async.
  * S_in: fp32 [n_seq, H, dv, dk] initial states, sequence s reading S_in + s * s_in_stride:
  * s_in_stride = H * dv * dk for a state of its own, 0 for one state that all sequences
  * continue; NULL: zero. S_out: fp32 [n_seq, H, dv, dk] final states, or NULL; S_out == S_in is

@@ -73,12 +73,15 @@ __device__ __forceinline__ float2 unpack(bf16, uint32_t u) {
 __device__ __forceinline__ bool nonfinite(f16, uint32_t u16) { return (u16 & 0x7c00u) == 0x7c00u; }
 __device__ __forceinline__ bool nonfinite(bf16, uint32_t u16) { return (u16 & 0x7f80u) == 0x7f80u; }
 
+// A head's log decay, at most 0; NaN stays NaN (fminf would make it no decay).
+__device__ __forceinline__ float capped(float log_decay) { return log_decay > 0.f ? 0.f : log_decay; }
 // log2 of a head's decay: at most 0, and never -inf (2^-1e4 is 0 as well, and 0 * -1e4 is 0)
 __device__ __forceinline__ float log2_decay(float log_decay) {
-  return fmaxf(fminf(log_decay, 0.f) * 1.4426950408889634f, -1e4f);
+  const float l2 = capped(log_decay) * 1.4426950408889634f;
+  return l2 < -1e4f ? -1e4f : l2;
 }
 // exp of a head's log decay: at most 1, exactly 0 for -inf
-__device__ __forceinline__ float decay(float log_decay) { return expf(fminf(log_decay, 0.f)); }
+__device__ __forceinline__ float decay(float log_decay) { return expf(capped(log_decay)); }
 
 constexpr int C = 128;                       // rows of a chunk
 constexpr int NTHREADS = 23 * 32;

@@ -973,3 +973,23 @@ def test_attention_sink_first_of_a_million(B):
     B.op_sync(stream())
     err = np.abs(a.out.double().cpu().numpy() - ref) / ref
     assert err.max() <= 2.0 ** -35 * math.exp(gap) + 2 * 2.0 ** -11 + 2.0 ** -8 + 2.0 ** -18, err.max()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("state", ["none", "own"])
+def test_linattn_nan_decay(B, state, dtype):
+    """A NaN decay is not taken for none: its head's outputs and states are NaN, the other heads' keep their bits."""
+    lens = [1, 300, 0, 129]
+    for step in (False, True):
+        a, b = (Lin(B, 3, 64, 128, [1] * 4 if step else lens, dtype, state, log_decay=[-0.1, x, -0.2])
+                for x in (float("nan"), -0.3))
+        for x in (a, b):
+            x.step() if step else x.call()
+        B.op_sync(stream())
+        assert torch.isnan(a.out[:, 1]).all()
+        full = [i for i, n in enumerate(a.lens) if n]
+        assert torch.isnan(a.S_out[full, 1]).all()
+        assert torch.equal(a.out[:, ::2], b.out[:, ::2]) and torch.equal(a.S_out[:, ::2], b.S_out[:, ::2])
+        for i, n in enumerate(a.lens):       # (an empty sequence's state is its initial one)
+            if n == 0:
+                assert torch.equal(a.S_out[i], a.S_in[i] if a.S_in is not None else torch.zeros_like(a.S_out[i]))
