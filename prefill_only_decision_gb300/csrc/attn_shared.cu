@@ -731,7 +731,10 @@ __global__ void __launch_bounds__(CWARPS * 32, 4)
   const int cb = blockIdx.x % (HD / CCOLS), quad = blockIdx.x / (HD / CCOLS) % 4, tile = blockIdx.x / (HD / CCOLS * 4);
   const int mt = tile % pl.MT, g = tile / pl.MT;
   const int rows = min(pl.RT, pl.V - mt * pl.RT) * pl.G;       // of this query tile
-  if (quad * 32 >= rows) return;
+  if (quad * 32 >= rows) {
+    wait_prerequisites();                                      // (every CTA: this grid's end is then the one before's, too)
+    return;
+  }
   const TabView tab{table.n, table.cum, table.row0};
   auto out_at = [&](int r) {                                   // where matrix row r of the tile goes
     const int vr = mt * pl.RT + r / pl.G, s = seq_of(tab, vr);
