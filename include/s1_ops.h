@@ -112,8 +112,10 @@ int s1_op_rmsnorm(const float* x, const float* w, int32_t R, int32_t d, float ep
 enum { S1_KV_F16 = 0, S1_KV_E4M3 = 1 };   /* formats of a K/V snapshot */
 
 /* Waits for `stream` and reports a bounded device wait that gave up in any of the operators
- * below on the current device since the last report (S1_ERR_DEVICE_TIMEOUT; the outputs of the
- * calls in question are then unspecified). */
+ * below on the current device, whichever stream it ran on, and that no earlier call has reported
+ * (S1_ERR_DEVICE_TIMEOUT; the outputs of the calls in question are then unspecified). Each give-up
+ * is reported once, to the first caller that comes after it: a program that uses several
+ * streams takes a report as all of theirs. */
 int s1_op_sync(void* stream);
 
 /* Writes n_rows rows of keys and values into an 8-bit snapshot, quantising them on the way.

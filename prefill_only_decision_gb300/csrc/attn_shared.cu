@@ -57,7 +57,6 @@ constexpr int BQ = 128, BKV = 128;
 constexpr int threads_of(bool e4m3) { return (e4m3 ? 19 : 15) * 32; }
 constexpr int TMEM_COLS = 512;               // S of stream x at 128 x, O at 256 + 128 x
 constexpr int T_O = 256;
-constexpr int ERR_TIMEOUT = 0x401;
 // Weights are 2^(z - m + HEAD), z the score and m the running maximum (log2 domain), which a row's maximum may
 // pass by GROW before it moves: at most 2^15, within f16. So a weight keeps f16's precision down to 2^-24 of
 // the largest, and one that is lost is below 2^-35 of it: 65536 of those are 2^-19 of the result. (HEAD = 0 and
@@ -65,7 +64,7 @@ constexpr int ERR_TIMEOUT = 0x401;
 // GROW: 1340 rows over 65536 keys 472, 471, 473, 478, 484 us.)
 constexpr float GROW = 5.f, HEAD = 15.f - GROW;
 
-__device__ int g_err;                        // bounded waits record here (one word per device)
+__device__ uint64_t g_given_up;              // when a bounded wait last gave up, per device; never cleared
 
 struct Plan {
   int V;          // packed query rows
@@ -254,7 +253,7 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
           if (t >= n) continue;
           const Slot k = slot_of<F, FR>(two, t, is_v);
           const int s = k.s;
-          if (!mbar_wait(&empty[s], k.ph ^ 1, abort_flag, &g_err, ERR_TIMEOUT)) break;
+          if (!mbar_wait(&empty[s], k.ph ^ 1, abort_flag, &g_given_up)) break;
           if (j < pl.ncache) {
             mbar_expect_tx(&full[s], L::TILE);
             for (int b = 0; b < NB; ++b)
@@ -277,7 +276,7 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
     constexpr uint32_t ID_S = idesc_f16(BKV / 2, 0, 0, 0), ID_O = idesc_f16(HD, 0, 0, 1);
     const uint32_t tS = tmem + x * 128, tO = tmem + T_O + x * 128;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_err, ERR_TIMEOUT) ? 1 : 0) != 0;
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_given_up) ? 1 : 0) != 0;
     };
     const uint64_t qd = desc_sw128(smem_u32(sm + L::Q) + (two && x ? BQ * HD * 2 : 0), 16);
     auto scores = [&](int h, int s) {          // S = Q K^T over half h of the tile in slot s
@@ -341,7 +340,7 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
     // ---- loaders: rows 32 lw .. +31 of every tile
     const int lw = warp < 14 ? warp - 10 : warp - 15, plane = warp < 14 ? 0 : 1;   // (f16 prefix: both planes)
     auto wwait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_err, ERR_TIMEOUT) ? 1 : 0) != 0;
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_given_up) ? 1 : 0) != 0;
     };
     // own rows of tile jo: CH chunks of 16 bytes per row, RPI rows per pass of the warp
     constexpr int CH = HD / 8, RPI = 32 / CH, PASSES = 32 / RPI;
@@ -458,7 +457,7 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
   } else {
     // ---- softmax of stream x: row r = TMEM lane r
     auto wwait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_err, ERR_TIMEOUT) ? 1 : 0) != 0;
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_given_up) ? 1 : 0) != 0;
     };
     const int x = (warp - 2) >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;
@@ -891,8 +890,8 @@ cudaError_t launch_tab(const SharedAttnArgs& a, const SeqTab<N>& tab, const Plan
 
 }  // namespace sha
 
-cudaError_t attention_shared_error_word(int** out) {
-  return cudaGetSymbolAddress(reinterpret_cast<void**>(out), sha::g_err);
+cudaError_t attention_shared_gave_up_word(uint64_t** out) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(out), sha::g_given_up);
 }
 
 int64_t attention_shared_ws_bytes(int n_seq, const int* len, int P, int Hq, int Hkv, int hd, int num_sms) {

@@ -194,9 +194,9 @@ struct SeqTab {
 };
 constexpr int SEQ_TAB_SMALL = 64, SEQ_TAB_LARGE = 2048;   // sequences per launch (0.5 KB, 16 KB)
 
-// Words of the current device in which the operators' bounded waits record that they gave up.
-cudaError_t attention_shared_error_word(int** out);
-cudaError_t linattn_error_word(int** out);
+// Words of the current device in which the operators' bounded waits note that they gave up.
+cudaError_t attention_shared_gave_up_word(uint64_t** out);
+cudaError_t linattn_gave_up_word(uint64_t** out);
 // A tensor map encoded afresh (arguments as tensor_map's).
 bool encode_tensor_map(CUtensorMap* out, CUtensorMapDataType dtype, int rank, const void* ptr, const uint64_t* dims,
                        const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);

@@ -85,9 +85,8 @@ __device__ __forceinline__ float decay(float log_decay) { return expf(capped(log
 
 constexpr int C = 128;                       // rows of a chunk
 constexpr int NTHREADS = 23 * 32;
-constexpr int ERR_TIMEOUT = 0x501;
 
-__device__ int g_err;                        // bounded waits record here (one word per device)
+__device__ uint64_t g_given_up;              // when a bounded wait last gave up, per device; never cleared
 
 constexpr int MAX_SEQ = 256;                 // sequences per launch
 
@@ -316,7 +315,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   fence_after();
   const uint32_t tmem = *tmem_slot;
   auto wwait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_err, ERR_TIMEOUT) ? 1 : 0) != 0;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_given_up) ? 1 : 0) != 0;
   };
   // f16: the state's scale exponent a, and the bound on the state after a chunk of n rows
   auto max8 = [](volatile int* m) {
@@ -361,13 +360,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       };
       if (nch == 0) start();
       for (int c = 0; c < nch && ok; ++c) {
-        if (c == 1 && has_start) ok = mbar_wait(in_free, 0, abort_flag, &g_err, ERR_TIMEOUT);
+        if (c == 1 && has_start) ok = mbar_wait(in_free, 0, abort_flag, &g_given_up);
         if (!ok) break;
         const int st = c & 1, r = (int)(row0 + c * C);
         uint8_t* base = sm + st * L::STAGE;
         auto load = [&](int which, const CUtensorMap* map, uint8_t* dst, int boxes, int bytes) {
           const int slot = 2 * which + st;
-          ok = ok && mbar_wait(&empty[slot], ((c >> 1) & 1) ^ 1, abort_flag, &g_err, ERR_TIMEOUT);
+          ok = ok && mbar_wait(&empty[slot], ((c >> 1) & 1) ^ 1, abort_flag, &g_given_up);
           if (!ok) return;
           mbar_expect_tx(&full[slot], bytes);
           for (int b = 0; b < boxes; ++b) tma3(dst + b * C * 128, map, &full[slot], 64 * b, h, r);
@@ -1054,7 +1053,7 @@ __global__ void __launch_bounds__(128)
 
 }  // namespace lin
 
-cudaError_t linattn_error_word(int** out) { return cudaGetSymbolAddress(reinterpret_cast<void**>(out), lin::g_err); }
+cudaError_t linattn_gave_up_word(uint64_t** out) { return cudaGetSymbolAddress(reinterpret_cast<void**>(out), lin::g_given_up); }
 
 // Rows per segment (a multiple of the chunk) for a group of sequences: the count with the least
 // estimated time in us. A CTA's cost is a fixed part and a part per chunk, as measured at 128 x 128 (3.1

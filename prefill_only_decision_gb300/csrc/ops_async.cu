@@ -3,6 +3,7 @@
 #include <new>
 
 #include "common.cuh"
+#include "giveups.h"
 #include "../../include/s1.h"
 #include "../../include/s1_ops.h"
 
@@ -100,22 +101,25 @@ int check_lin(const void* q, const void* k, const void* v, int32_t dtype, int64_
 extern "C" {
 
 int s1_op_sync(void* stream) {
+  static GiveUps<2> told;
   cudaStream_t st = (cudaStream_t)stream;
-  int* word[2] = {nullptr, nullptr};
-  int h[2] = {0, 0};
-  const int zero = 0;
-  cudaError_t e = attention_shared_error_word(&word[0]);
-  if (e == cudaSuccess) e = linattn_error_word(&word[1]);
-  for (int i = 0; i < 2 && e == cudaSuccess; ++i)
-    e = cudaMemcpyAsync(&h[i], word[i], sizeof(int), cudaMemcpyDeviceToHost, st);
+  uint64_t* word[2] = {nullptr, nullptr};
+  int dev = 0;
+  bool any = false;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = attention_shared_gave_up_word(&word[0]);
+  if (e == cudaSuccess) e = linattn_gave_up_word(&word[1]);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  for (int i = 0; i < 2 && e == cudaSuccess; ++i)
-    if (h[i]) {
-      e = cudaMemcpyAsync(word[i], &zero, sizeof(int), cudaMemcpyHostToDevice, st);
-      if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    }
+  if (e == cudaSuccess)
+    e = (cudaError_t)told.news(dev, [&](uint64_t* now) {
+      cudaError_t r = cudaSuccess;
+      for (int i = 0; i < 2 && r == cudaSuccess; ++i)
+        r = cudaMemcpyAsync(&now[i], word[i], sizeof(now[i]), cudaMemcpyDeviceToHost, st);
+      if (r == cudaSuccess) r = cudaStreamSynchronize(st);
+      return (int)r;
+    }, &any);
   if (e != cudaSuccess) return cuda_rc(e, "op_sync");
-  if (h[0] || h[1]) return s1::set_error(S1_ERR_DEVICE_TIMEOUT, "op_sync: a bounded device wait gave up");
+  if (any) return s1::set_error(S1_ERR_DEVICE_TIMEOUT, "op_sync: a bounded device wait gave up");
   return S1_OK;
 }
 

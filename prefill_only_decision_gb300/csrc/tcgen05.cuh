@@ -48,11 +48,11 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Bounded wait; false (with `code` recorded in *d_err) on expiry, or when another role gave up. The
+// Bounded wait; false (the time in *given_up) on expiry, or when another role gave up. The
 // timer and the flag are looked at once in 64 polls: a wait on the critical path that read them first
 // would cost more than what it waits for (a flag read in every poll: 2 to 4 % of these kernels' time).
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* d_err,
-                                          int code) {
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          uint64_t* given_up) {
   uint64_t t0 = 0;
   for (uint32_t it = 1; !mbar_try(bar, parity); ++it)
     if ((it & 63) == 0) {
@@ -60,7 +60,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
       if (t0 == 0) t0 = t;
       if (*abort_flag || t - t0 > WAIT_NS) {
         *abort_flag = 1;
-        if (t - t0 > WAIT_NS) *reinterpret_cast<volatile int*>(d_err) = code;
+        if (t - t0 > WAIT_NS) *reinterpret_cast<volatile uint64_t*>(given_up) = t;
         return false;
       }
     }
