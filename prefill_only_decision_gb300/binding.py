@@ -486,9 +486,16 @@ def op_sync(stream: int = 0):
     check(lib().s1_op_sync(stream))
 
 
+def _fits(bits: int):
+    """Refuses sizes beyond 32 bits (given ORed together), which ctypes would cut to other sizes."""
+    if bits >> 31 not in (0, -1):
+        raise ValueError("a size does not fit 32 bits")
+
+
 def op_kv_quant_async(k: int, v: int, dtype: int, k_stride: int, v_stride: int, n_rows: int, Hkv: int, hd: int,
                       codes: int, scales: int, cap: int, pos0: int, stream: int = 0):
     """Write K/V rows into an 8-bit snapshot (s1_op_kv_quant_async)."""
+    _fits(n_rows | Hkv | hd | cap | pos0)
     check(lib().s1_op_kv_quant_async(k, v, dtype, k_stride, v_stride, n_rows, Hkv, hd, codes, scales, cap, pos0,
                                      stream))
 
@@ -496,13 +503,26 @@ def op_kv_quant_async(k: int, v: int, dtype: int, k_stride: int, v_stride: int, 
 def op_kv_dequant_async(codes: int, scales: int, cap: int, pos0: int, n_rows: int, Hkv: int, hd: int, k: int, v: int,
                         dtype: int, k_stride: int, v_stride: int, stream: int = 0):
     """Read rows of an 8-bit snapshot back (s1_op_kv_dequant_async)."""
+    _fits(n_rows | Hkv | hd | cap | pos0)
     check(lib().s1_op_kv_dequant_async(codes, scales, cap, pos0, n_rows, Hkv, hd, k, v, dtype, k_stride, v_stride,
                                        stream))
 
 
+def _seq_i32(a) -> np.ndarray:
+    """Row numbers or lengths as int32; what that cannot hold is refused, not wrapped or cut."""
+    a = np.asarray(a)
+    if a.ndim != 1:
+        raise ValueError("row0 and lens must be 1-D and of the same length")
+    if a.dtype != np.int32:
+        if a.size and (a.dtype.kind not in "iu" or a.min() < -2 ** 31 or a.max() >= 2 ** 31):
+            raise ValueError("row0 and lens must be integers of 32 bits")
+        a = a.astype(np.int32)
+    return np.ascontiguousarray(a)
+
+
 def _seq_arrays(row0, lens):
-    r0, ln = _i32(row0), _i32(lens)
-    if r0.shape != ln.shape or r0.ndim != 1:
+    r0, ln = _seq_i32(row0), _seq_i32(lens)
+    if r0.shape != ln.shape:
         raise ValueError("row0 and lens must be 1-D and of the same length")
     return r0, ln
 
@@ -511,6 +531,7 @@ def op_attention_shared_async(q: int, q_stride: int, k_new: int, v_new: int, kv_
                               scales: int, kv_format: int, P: int, cap: int, Hq: int, Hkv: int, hd: int,
                               sm_scale: float, out: int, workspace: int, workspace_bytes: int, stream: int = 0):
     """Attention of a batch over one shared prefix (s1_op_attention_shared_async)."""
+    _fits(P | cap | Hq | Hkv | hd)
     r0, ln = _seq_arrays(row0, lens)
     check(lib().s1_op_attention_shared_async(q, q_stride, k_new, v_new, kv_stride, len(r0), _addr(r0),
                                              _addr(ln), kv, scales, kv_format, P, cap, Hq, Hkv, hd, sm_scale,
@@ -519,7 +540,8 @@ def op_attention_shared_async(q: int, q_stride: int, k_new: int, v_new: int, kv_
 
 def op_attention_shared_workspace(lens, P: int, Hq: int, Hkv: int, hd: int) -> int:
     """Workspace bytes of op_attention_shared_async for these sizes on the current device."""
-    ln, out = _i32(lens), C.c_int64()
+    _fits(P | Hq | Hkv | hd)
+    ln, out = _seq_i32(lens), C.c_int64()
     check(lib().s1_op_attention_shared_workspace(len(ln), _addr(ln), P, Hq, Hkv, hd, C.byref(out)))
     return out.value
 
@@ -528,6 +550,7 @@ def op_linattn_async(q: int, k: int, v: int, dtype: int, q_stride: int, k_stride
                      row0, lens, H: int, dk: int, dv: int, scale: float, S_in: int, s_in_stride: int, S_out: int,
                      out: int, workspace: int, workspace_bytes: int, stream: int = 0):
     """Linear attention with a decay per head over packed sequences (s1_op_linattn_async)."""
+    _fits(H | dk | dv)
     r0, ln = _seq_arrays(row0, lens)
     check(lib().s1_op_linattn_async(q, k, v, dtype, q_stride, k_stride, v_stride, log_decay, len(r0), _addr(r0),
                                     _addr(ln), H, dk, dv, scale, S_in, s_in_stride, S_out, out, workspace,
@@ -536,7 +559,8 @@ def op_linattn_async(q: int, k: int, v: int, dtype: int, q_stride: int, k_stride
 
 def op_linattn_workspace(lens, H: int, dk: int, dv: int) -> int:
     """Workspace bytes of op_linattn_async for these sizes on the current device."""
-    ln, out = _i32(lens), C.c_int64()
+    _fits(H | dk | dv)
+    ln, out = _seq_i32(lens), C.c_int64()
     check(lib().s1_op_linattn_workspace(len(ln), _addr(ln), H, dk, dv, C.byref(out)))
     return out.value
 
@@ -545,5 +569,6 @@ def op_linattn_step_async(q: int, k: int, v: int, dtype: int, q_stride: int, k_s
                           log_decay: int, n: int, H: int, dk: int, dv: int, scale: float, S_in: int, s_in_stride: int,
                           S_out: int, out: int, stream: int = 0):
     """One token of the recurrence for each of n sequences (s1_op_linattn_step_async)."""
+    _fits(n | H | dk | dv)
     check(lib().s1_op_linattn_step_async(q, k, v, dtype, q_stride, k_stride, v_stride, log_decay, n, H, dk, dv, scale,
                                          S_in, s_in_stride, S_out, out, stream))

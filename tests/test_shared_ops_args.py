@@ -138,3 +138,53 @@ def test_null_outputs_of_the_sizing_calls(B):
     assert B.lib().s1_op_attention_shared_workspace(1, ln.ctypes.data, 4, 8, 2, 128, None) == ARG
     out = C.c_int64()
     assert B.lib().s1_op_attention_shared_workspace(1, None, 4, 8, 2, 128, C.byref(out)) == ARG
+
+
+@pytest.mark.parametrize("bad", [np.array([2 ** 32, 2 ** 32 + 8]), np.array([0, 2 ** 31]), [0, 2 ** 40], [0.0, 8.5],
+                                 np.array([0, -2 ** 31 - 1]), [[0, 8]], np.array([0, 2 ** 63], np.uint64)])
+def test_sequence_arrays_are_not_wrapped(B, bad):
+    """Rows and lengths that 32 bits cannot hold, fractions and tables are refused; they would become other rows."""
+    with pytest.raises(ValueError):
+        B.op_attention_shared_async(**{**AT, "row0": bad})
+    kw = dict(workspace=P, workspace_bytes=1 << 40, **LA)
+    with pytest.raises(ValueError):
+        B.op_linattn_async(row0=bad, lens=[8, 3], **kw)
+    with pytest.raises(ValueError):
+        B.op_linattn_async(row0=[0, 8], lens=bad, **kw)
+    with pytest.raises(ValueError):
+        B.op_linattn_workspace(bad, 8, 128, 128)
+    with pytest.raises(ValueError):
+        B.op_attention_shared_workspace(bad, 100, 16, 4, 128)
+
+
+@pytest.mark.parametrize("lens", [[5, 0, 7], np.array([5, 0, 7]), np.array([5, 9, 0, 9, 7])[::2], (5, 0, 7),
+                                  np.array([5, 0, 7], np.uint8)])
+def test_sequence_arrays_of_other_types(B, lens):
+    want = B.op_linattn_workspace(np.array([5, 0, 7], np.int32), 8, 128, 128)
+    assert B.op_linattn_workspace(lens, 8, 128, 128) == want
+    assert B.op_linattn_workspace([], 8, 128, 128) == 0
+
+
+BIG = 2 ** 32
+
+
+def test_sizes_are_not_cut(B):
+    """A size beyond 32 bits is refused; cut to its low half it would be another one."""
+    for name in ("n_rows", "cap", "pos0", "Hkv", "hd"):
+        for f in (B.op_kv_quant_async, B.op_kv_dequant_async):
+            with pytest.raises(ValueError):
+                f(**{**KV, name: KV[name] + BIG})
+    for name in ("P", "cap", "Hq", "Hkv", "hd"):
+        with pytest.raises(ValueError):
+            B.op_attention_shared_async(**{**AT, name: AT[name] + BIG})
+    for name in ("H", "dk", "dv"):
+        with pytest.raises(ValueError):
+            B.op_linattn_async(row0=[0], lens=[5], workspace=P, workspace_bytes=1 << 40, **{**LA, name: LA[name] + BIG})
+        with pytest.raises(ValueError):
+            B.op_linattn_step_async(n=3, **{**LA, name: LA[name] - 2 * BIG})
+    with pytest.raises(ValueError):
+        B.op_linattn_step_async(n=3 + BIG, **LA)
+    with pytest.raises(ValueError):
+        B.op_attention_shared_workspace([4], P=100 + BIG, Hq=16, Hkv=4, hd=128)
+    with pytest.raises(ValueError):
+        B.op_linattn_workspace([4], 8 + BIG, 128, 128)
