@@ -25,15 +25,16 @@
 // heads from 182 to 202 us, 188 since they wait for no more than they must). Their products run small
 // parts first: the sums lose less.
 // f16 rows: weights, scaled Q and the state's copy are scaled by powers of two so that they use f16's range whatever
-// the magnitudes: the state's copy by 2^a (from a running bound lam^n bound + n max|v| max|k| on the
-// state before the chunk), a row's weights by 2^c, its Q by 2^(c - a) and its outputs by 2^-c, with c from the
+// the magnitudes: the state's copy by 2^a (from a running bound on the state before the chunk, to which each row adds
+// lam^(n-1-j) max|v_j| max|k_j|), a row's weights by 2^c, its Q by 2^(c - a) and its outputs by 2^-c, with c from the
 // row's own largest weight and largest |q|: a row's scales depend on nothing that it does not see, and a large
 // element costs only rows that have it in their sums anyway. (c for 32 rows at once from dk max|q| max|k| of the
-// whole chunk needed one pass over the weights less, 16384 rows x 32 heads 212 us instead of 217, 8000 x 16 of 64
-// 52 instead of 56, but a key of 4000 in a later row cost ordinary rows before it percents.) What lies 2^28 below such a maximum loses bits; bounds lie far less above the values. The decayed
-// values, with the state they are added to, are scaled by 2^b (b per chunk), so that the low parts stay above f16's
-// smallest number: a value keeps fp32's accuracy down to 2^-15 of the chunk's largest, below that it is off by at
-// most 2^-38 of that.
+// whole chunk, and a bound that grew by n max|v| max|k| a chunk, needed a pass over the weights less, 16384 rows x 32
+// heads 212 us instead of 218, 8000 x 16 of 64 52 instead of 58; but a key of 4000 in a later row cost ordinary
+// rows before it percents, and so did elements of 9000 rows after them where the decay had long forgotten them.)
+// The decayed values, with the state they are added to, are scaled by 2^b (b per chunk, from its largest decayed
+// value), so that the low parts stay above f16's smallest number: a decayed value keeps 2^-24 of itself down to 2^-13
+// of the chunk's largest, and is off by at most 2^-37 of that below.
 // Where: f16's scaled Q is in TMEM beside the weights; bf16's is in its shared-memory tile, and the third
 // parts take its TMEM columns (so they wait for the weights, and the next Q K^T waits for them).
 // One CTA per SM, 23 warps: 0 TMA producer (two stages of Q, K, V); 1 and 18 MMA issue (1: Q K^T and
@@ -127,7 +128,7 @@ struct Lay {
                                                            // chunk's length, t = 0 .. 127
   static constexpr int BAR = WV + 2 * C * 4;
   static constexpr int NBAR = 33;
-  static constexpr int USED = BAR + NBAR * 8 + (51 + 64 + 64) * 4;
+  static constexpr int USED = BAR + NBAR * 8 + 13 * 4 + 12 * C;
   static_assert(USED <= 227 * 1024, "shared memory of one CTA");
   // above half an SM: each CTA allocates all of TMEM, so two never share one
   static constexpr int BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
@@ -228,22 +229,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // V has held a non-finite element
+  // f16: powers of two from the magnitudes. Rows' bytes are exponents e, magnitudes below 2^e (-128: zeros).
   // What orders a slot's next write behind its last read:
-  // vmax: written for chunk c + 2 behind o_full(c), so behind p_ready(c), which the row warps arrive at after
+  // v_exp: written for chunk c + 2 behind o_full(c), so behind p_ready(c), which the row warps arrive at after
   //   their read of chunk c's, and behind ds_done(c), so behind the value rows' own reads up to v_ready(c).
-  // kmax: the value rows read chunk c - 1's in their iteration c, up to s_ready(c). The row warps meet that only
-  //   at p_full(c + 1) (Q K^T of c + 1 is issued behind the outputs of c), so two slots are too few: three, and
-  //   the write for chunk c + 2 comes behind p_full(c + 1).
+  // k_exp: written for chunk c + 2 behind p_full(c + 1), so behind the outputs of c and the row warps' p_ready(c).
   // w_exp: read up to p_ready(c), written for chunk c + 1 behind p_full(c + 1), so behind the outputs of c.
   // c_exp: the output warps read chunk c's up to o_free(c), which the outputs of c + 1 wait for; written for
   //   chunk c + 2 behind p_full(c + 2), so behind those.
+  // bnd: chunk c's is read by the value rows up to s_ready(c); written for chunk c + 2 behind p_full(c + 1), so
+  //   behind the outputs of c, which wait for s_ready(c).
   // wmax: written once. v_flag: only ever set.
-  volatile int* vmax = (volatile int*)(tmem_slot + 3);     // [2 stages][8 warps] max |V| as f16 bits
-  volatile int* kmax = (volatile int*)(tmem_slot + 19);    // [3][8] max |K|, by chunk mod 3
-  volatile float* wmax = (volatile float*)(tmem_slot + 43);  // [8] max |start state| per warp
-  volatile signed char* c_exp = (volatile signed char*)(tmem_slot + 51);    // [2][128] c of the rows, by chunk parity (f16)
-  volatile signed char* w_exp = (volatile signed char*)(tmem_slot + 115);   // [2 halves][128] the rows' weights are below
-                                                                            // 2^(w_exp + 2); -128: zeros (f16)
+  volatile float* wmax = (volatile float*)(tmem_slot + 3);   // [8] max |start state| per warp
+  volatile float* bnd = (volatile float*)(tmem_slot + 11);   // [2] bound on the state before a chunk, by chunk parity
+  volatile signed char* c_exp = (volatile signed char*)(tmem_slot + 13);   // [2][128] c of the rows, by chunk parity
+  volatile signed char* w_exp = c_exp + 2 * C;             // [2 halves][128] the rows' weights, less 2
+  volatile signed char* k_exp = w_exp + 2 * C;             // [2 parities][2 halves][128] the rows of K
+  volatile signed char* v_exp = k_exp + 4 * C;             // [2][2][128] the rows of V
   float* wv = reinterpret_cast<float*>(sm + L::WV);
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -317,12 +319,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   auto wwait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_given_up) ? 1 : 0) != 0;
   };
-  // f16: the state's scale exponent a, and the bound on the state after a chunk of n rows
-  auto max8 = [](volatile int* m) {
-    int x = 0;
+  // f16: the larger exponent of both halves, rows 4 lane .. + 3; those rows' weights lam^(n-1-t)
+  auto exps4 = [&](volatile signed char* e, int* x) {
+    const int a = *reinterpret_cast<volatile int*>(e + 4 * lane), b = *reinterpret_cast<volatile int*>(e + C + 4 * lane);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x = max(x, m[k]);
-    return (uint32_t)x;
+    for (int k = 0; k < 4; ++k) x[k] = max((int)(signed char)(a >> 8 * k), (int)(signed char)(b >> 8 * k));
+  };
+  auto weights4 = [&](int n, float* w) {
+    const float4 v = *reinterpret_cast<const float4*>(wv + (n == C ? 0 : C) + 4 * lane);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
   };
   auto start_bound = [&]() {
     float x = 0.f;
@@ -330,12 +335,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int k = 0; k < 8; ++k) x = fmaxf(x, wmax[k]);
     return x;
   };
+  // the state's scale exponent a
   auto scale_exp = [](float bound) { return bound > 0.f ? max(-114, min(100, 14 - exp_above(bound))) : 100; };
-  auto grown = [&](float bound, int n, uint32_t vm, uint32_t km) {
-    // (each product rounded by itself: two roles form the same number)
-    const float add = __fmul_rn(__fmul_rn(1.00001f * (float)n, h_bits(vm)), h_bits(km));
-    return __fadd_rn(__fmul_rn(__fmul_rn(bound, wv[C - 1 - n]), 1.00001f), add);
-  };
   auto pw = [&](int d) { return wv[C - 1 - d]; };   // lam^d, d = 0 .. 128
   auto arrive = [&](uint64_t* bar) {           // once per warp, after what it wrote
     __syncwarp();
@@ -495,6 +496,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (!wwait(&full[st], sph)) break;
         float fp = rinv, fq = qs;
         uint32_t qm = 0;                       // max |Q| of the row (f16)
+        float next = 0.f;                      // the bound after this chunk
         if constexpr (F16) {
           uint32_t m = 0, mk = 0;
 #pragma unroll 4
@@ -504,30 +506,47 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           qm = max(m & 0xffffu, m >> 16);
           if (qm >= 0x7c00u) qm = 0;           // (a row with a non-finite element: no scale makes its outputs finite)
-          // this warp's share of K; rows past the end and non-finite elements aside
-          const int n = min(C, end - beg - c * C), k0 = (warp - 2) * (L::QB / 8) + lane * 16;
           if (!wwait(&full[2 + st], sph)) break;
-          const uint8_t* kt = sm + st * L::STAGE + L::QB + k0;
-#pragma unroll
-          for (int k = 0; k < L::QB / 8 / 512; ++k) {
-            const uint4 v = *reinterpret_cast<const uint4*>(kt + k * 512);
-            const uint32_t x = absmax2(T(), absmax2(T(), v.x, v.y), absmax2(T(), v.z, v.w));
-            if ((k0 + k * 512 >> 7) % C < n) mk = absmax2(T(), mk, x);
-          }
-          if (max(mk & 0xffffu, mk >> 16) >= 0x7c00u) {
-            mk = 0;
-#pragma unroll 1
-            for (int k = 0; k < L::QB / 8 / 512 * 4; ++k) {
-              const bool in = (k0 + (k >> 2) * 512 >> 7) % C < n;
-              const uint32_t w = in ? *reinterpret_cast<const uint32_t*>(kt + (k >> 2) * 512 + (k & 3) * 4) : 0u;
-              const uint32_t lo = nonfinite(T(), w & 0xffffu) ? 0u : w & 0x7fffu;
-              const uint32_t hi = nonfinite(T(), w >> 16) ? 0u : w >> 16 & 0x7fffu;
-              mk = absmax2(T(), mk, lo | hi << 16);
+          if (c + 1 < nch) {                   // (the last chunk: nothing follows)
+            // this half of row i of K; non-finite elements aside
+            const uint8_t* krow = sm + st * L::STAGE + L::QB + i * 128;
+            auto k16 = [&](int q) {
+              q += half * (DK / 16);
+              return *reinterpret_cast<const uint4*>(krow + (q >> 3) * (C * 128) + (((q & 7) ^ (i & 7)) << 4));
+            };
+#pragma unroll 4
+            for (int q = 0; q < DK / 16; ++q) {
+              const uint4 v = k16(q);
+              mk = absmax2(T(), mk, absmax2(T(), absmax2(T(), v.x, v.y), absmax2(T(), v.z, v.w)));
             }
+            if (max(mk & 0xffffu, mk >> 16) >= 0x7c00u) {
+              mk = 0;
+#pragma unroll 1
+              for (int q = 0; q < DK / 16; ++q) {
+                const uint4 v = k16(q);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  mk = absmax2(T(), mk, (nonfinite(T(), w[e] & 0xffffu) ? 0u : w[e] & 0x7fffu) |
+                                            (nonfinite(T(), w[e] >> 16) ? 0u : w[e] & 0x7fff0000u));
+              }
+            }
+            mk = max(mk & 0xffffu, mk >> 16);
+            k_exp[(ph * 2 + half) * C + i] = (signed char)(mk > 0 && i < end - beg - c * C ? exp_above(h_bits(mk)) : -128);
+            arrive(k_known);
+            // the state after this chunk: lam^n S and the terms, row by row
+            if (!wwait(&clean[st], sph) || !wwait(k_known, ph)) break;
+            const int n = min(C, end - beg - c * C);
+            int ke[4], ve[4];
+            float w[4], add = 0.f;
+            exps4(k_exp + ph * 2 * C, ke);
+            exps4(v_exp + ph * 2 * C, ve);
+            weights4(n, w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (ke[k] + ve[k] > -100) add += w[k] * pow2f(ke[k] + ve[k]);
+            next = 1.00001f * (bound * pw(n)) + 1.0001f * warp_sum(add);
           }
-          mk = __reduce_max_sync(0xffffffffu, max(mk & 0xffffu, mk >> 16));
-          if (lane == 0) kmax[c % 3 * 8 + warp - 2] = (int)mk;
-          arrive(k_known);
         }
         if (!wwait(p_full, ph)) break;
         fence_after();
@@ -566,6 +585,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           const int qe = cexp - sa;            // |q| qs 2^qe < 2^14, or the state is zero
           fq = qe < -126 ? 0.f : qe > 126 ? qs * pow2f(126) * pow2f(qe - 126) : qs * pow2f(qe);
           if (half == 0) c_exp[ph * C + i] = (signed char)cexp;
+          bound = next;
+          if (warp == 2 && lane == 0) bnd[ph ^ 1] = next;
         }
 #pragma unroll 1
         for (int k = 0; k < 2; ++k) {
@@ -629,10 +650,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         st_wait();
         if (!F16) fence_async_smem();
         fence_before();
-        if constexpr (F16) {                   // (before p_ready: V's maximum is there until then)
-          if (!wwait(&clean[st], sph) || !wwait(k_known, ph)) break;
-          bound = grown(bound, min(C, end - beg - c * C), max8(vmax + st * 8), max8(kmax + c % 3 * 8));
-        }
         arrive(p_ready);
         if (F16 && lane == 0) mbar_arrive(&empty[st]);
         if (!F16 && c == 0) settle();
@@ -733,44 +750,49 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int e = 0; e < 32; ++e) x[e] = F16 ? __uint_as_float(u[e]) * f : __uint_as_float(u[e]);
     };
     float bound = 0.f;                         // at least every finite |state element| (f16)
-    // rows past the end to zeros (K and V), non-finite V elements to zero; f16: max |V|
+    // rows past the end to zeros (K and V), non-finite V elements to zero; f16: the exponents of V's rows. A
+    // thread takes DV / 16 chunks of 16 bytes of V: half of row r (bf16: in memory order)
     auto cleaning = [&](int c) {
       const int st = c & 1, n = min(C, end - beg - c * C);
       const uint32_t sph = (c >> 1) & 1;
       uint8_t* kt = sm + st * L::STAGE + L::QB;
       uint8_t* vt = kt + L::QB;
-      constexpr int KC = DK / 8, PER = C * DV / 8 / 256;
+      constexpr int KC = DK / 8, VQ = DV / 16;
       const int tid = wi * 32 + lane;
+      auto v16 = [&](int q) {
+        const int x = half * VQ + q;
+        return reinterpret_cast<uint4*>(F16 ? vt + (x >> 3) * (C * 128) + r * 128 + (((x & 7) ^ (r & 7)) << 4)
+                                            : vt + (q * 256 + tid) * 16);
+      };
+      auto past = [&](int q) { return (F16 ? r : ((q * 256 + tid) >> 3) % C) >= n; };
       if (!wwait(&full[2 + st], sph) || !wwait(&full[4 + st], sph)) return false;
-      bool bad = false, wrote = false;
+      bool bad = false, wrote = n < C;
       uint32_t vm = 0;
       {
-        uint4 v[PER];                          // 16-byte chunks in memory order: box, row, chunk
+        uint4 v[VQ];
 #pragma unroll
-        for (int k = 0; k < PER; ++k) v[k] = *reinterpret_cast<const uint4*>(vt + (k * 256 + tid) * 16);
+        for (int q = 0; q < VQ; ++q) v[q] = *v16(q);
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
-          const uint32_t x = absmax2(T(), absmax2(T(), v[k].x, v[k].y), absmax2(T(), v[k].z, v[k].w));
-          if ((((k * 256 + tid) >> 3) % C) < n) vm = absmax2(T(), vm, x);
-          else *reinterpret_cast<uint4*>(vt + (k * 256 + tid) * 16) = make_uint4(0, 0, 0, 0);
+        for (int q = 0; q < VQ; ++q) {
+          const uint32_t x = absmax2(T(), absmax2(T(), v[q].x, v[q].y), absmax2(T(), v[q].z, v[q].w));
+          if (!past(q)) vm = absmax2(T(), vm, x);
+          else *v16(q) = make_uint4(0, 0, 0, 0);
         }
       }
-      wrote = n < C;
       if (max(vm & 0xffffu, vm >> 16) >= (F16 ? 0x7c00u : 0x7f80u)) {   // some element is to be replaced
         vm = 0;
 #pragma unroll 1
-        for (int k = 0; k < PER; ++k) {
-          uint32_t* at = reinterpret_cast<uint32_t*>(vt + (k * 256 + tid) * 16);
-          const bool past = (((k * 256 + tid) >> 3) % C) >= n;
+        for (int q = 0; q < VQ; ++q) {
+          uint32_t* at = reinterpret_cast<uint32_t*>(v16(q));
+          if (past(q)) continue;
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t w = at[q];
-            if (past) continue;
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w = at[e];
             const bool lo = nonfinite(T(), w & 0xffffu), hi = nonfinite(T(), w >> 16);
             bad |= lo || hi;
             if (lo) w &= 0xffff0000u;
             if (hi) w &= 0xffffu;
-            at[q] = w;
+            at[e] = w;
             vm = absmax2(T(), vm, w);
           }
         }
@@ -783,8 +805,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       if (bad) *v_flag = 1;
       if constexpr (F16) {
-        vm = __reduce_max_sync(0xffffffffu, max(vm & 0xffffu, vm >> 16));
-        if (lane == 0) vmax[st * 8 + wi] = (int)vm;
+        vm = max(vm & 0xffffu, vm >> 16);
+        v_exp[(st * 2 + half) * C + r] = (signed char)(vm > 0 ? exp_above(h_bits(vm)) : -128);
       }
       if (wrote) fence_async_smem();
       arrive(&clean[st]);
@@ -834,7 +856,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         bound = start_bound();
       }
     }
-    uint32_t vm = 0;                           // max |V| of the last chunk begun (f16)
     for (int c = 0; c < nch && ok; ++c) {
       const int st = c & 1, n = min(C, end - beg - c * C);
       const uint32_t sph = (c >> 1) & 1;
@@ -844,9 +865,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (OUT && c > 0 && !wwait(o_full, (c - 1) & 1)) { ok = false; break; }   // (its state copy has been read)
       int bnew = 0, sa = 0;
       if constexpr (F16) {                     // decayed values below 2^14, and the scaled state finite
-        if (OUT && c > 0) bound = grown(bound, C, vm, max8(kmax + (c - 1) % 3 * 8));
-        vm = max8(vmax + st * 8);
-        if (vm > 0) bnew = 14 - exp_above(h_bits(vm));
+        if (OUT && c > 0) bound = bnd[st];
+        int ve[4];
+        float w[4], x = 0.f;
+        exps4(v_exp + st * 2 * C, ve);
+        weights4(n, w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (ve[k] > -128) x = fmaxf(x, w[k] * pow2f(ve[k]));
+        x = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+        if (x > 0.f) bnew = min(60, 14 - exp_above(x));
         if (bound > 0.f) bnew = min(bnew, 120 - exp_above(bound));
         sa = scale_exp(bound);
       }

@@ -993,3 +993,37 @@ def test_linattn_nan_decay(B, state, dtype):
         for i, n in enumerate(a.lens):       # (an empty sequence's state is its initial one)
             if n == 0:
                 assert torch.equal(a.S_out[i], a.S_in[i] if a.S_in is not None else torch.zeros_like(a.S_out[i]))
+
+
+@pytest.mark.parametrize("log_decay", [[-0.7, -0.005], [-3.0, -0.1], [0.0, -0.0004]])
+@pytest.mark.parametrize("state", ["none", "own"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_linattn_f16_sparse_large_elements(B, D, state, log_decay):
+    """Two elements in a thousand of q, k and v are 3000 times the others. Outputs keep compare()'s tolerance,
+    elements that hold none of the large ones, or whose decay has forgotten them, too. States: a decayed value
+    is off by at most 2^-37 of its chunk's largest besides (below |v|'s largest), so the state by that times the
+    sum of |k|, decayed from the chunk's end on."""
+    a = Lin(B, 2, D, D, [300, 141], "f16", state, log_decay=log_decay, seed=21)
+    g = np.random.default_rng(8)
+    large = torch.from_numpy(g.random(tuple(a.x.shape)) < 0.002).cuda()
+    a.x.copy_(torch.where(large, a.x * 3000, a.x).clamp(-60000, 60000))
+    a.scale = 2.0 ** -13
+    a.call()
+    B.op_sync(stream())
+    out, mag, S, A = a.ref()
+    got = a.out.double().cpu().numpy()
+    tol = 3 * U["f16"] * mag + 1e-6 * mag + 1e-7
+    over = np.abs(out) - tol > 65520         # (past f16's largest number)
+    assert (got[over] == np.copysign(np.inf, out[over])).all()
+    fits = np.abs(out) + tol < 65520
+    err = np.abs(got[fits] - out[fits])
+    assert fits.mean() > 0.9 and (err <= tol[fits]).all(), (err / (mag[fits] + 1e-30)).max() / U["f16"]
+    k, v = (np.abs(t.double().cpu().numpy().reshape(a.R, 2, D)) for t in a.parts()[1:])
+    lam = np.exp(a.ld.double().cpu().numpy())
+    for s, (r0, n) in enumerate(zip(a.row0, a.lens)):
+        floor = np.zeros((2, D))
+        for c in range(0, n, 128):
+            rows = slice(r0 + c, r0 + min(n, c + 128))
+            floor += v[rows].max() * k[rows].sum(0) * (lam ** (n - min(n, c + 128)))[:, None]
+        es = np.abs(a.S_out[s].double().cpu().numpy() - S[s])
+        assert (es <= (2.0 ** -16 + 2.0 ** -18) * A[s] + 2.0 ** -37 * floor[:, None, :] + 1e-9).all()
