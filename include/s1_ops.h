@@ -152,11 +152,11 @@ int s1_op_kv_dequant_async(const void* codes, const float* scales, int32_t cap, 
  * (S1_KV_E4M3; used as the f16 values s1_op_kv_dequant_async gives); rows P .. cap-1 are not
  * read; may be NULL when P == 0. hd 64 or 128, Hq % Hkv == 0, Hq / Hkv <= 128. Softmax
  * statistics and sums are fp32; the weights are rounded to f16 for the products, with f16's
- * precision down to 2^-24 of a row's largest. A query that
- * sees nothing, or whose scores are all -inf, gives zeros. Values that a query does not see
- * never reach it, whatever they hold (NaN and infinities included). out f16 [., Hq, hd],
- * contiguous rows, 16-byte aligned. workspace: 16-byte aligned, at least the bytes that
- * s1_op_attention_shared_workspace gives for these sizes on this device. */
+ * precision down to 2^-24 of a row's largest. A query that sees nothing, or whose scores are all
+ * -inf, gives zeros. Values that a query does not see never reach it, whatever they hold (NaN and
+ * infinities included). out f16 [., Hq, hd], contiguous rows, 16-byte aligned. workspace: 16-byte
+ * aligned, at least the bytes that s1_op_attention_shared_workspace gives for these sizes on this
+ * device. */
 int s1_op_attention_shared_async(const void* q, int64_t q_stride, const void* k_new, const void* v_new,
                                  int64_t kv_stride, int32_t n_seq, const int32_t* row0, const int32_t* len,
                                  const void* kv, const float* scales, int32_t kv_format, int32_t P, int32_t cap,
@@ -178,9 +178,9 @@ int s1_op_attention_shared_workspace(int32_t n_seq, const int32_t* len, int32_t 
  * sequence's final state is its initial one. out: dtype [., H, dv], contiguous rows, 16-byte
  * aligned. States, and sums over rows, are fp32; for the products the weights within 128 rows and
  * a copy of the state are each rounded once to dtype (a copy only: the state itself keeps its
- * bits), and a chunk's decayed values are split into parts that keep 2^-24 of each (f16: at least
- * 2^-37 of the chunk's largest). workspace: as above, s1_op_linattn_workspace. A row never reaches
- * an earlier row or another sequence, whatever it holds. */
+ * bits), and decayed values are split into parts that leave 2^-24 of each, or f16 2^-37 of the
+ * largest within 128 rows where that is more. workspace: as above, s1_op_linattn_workspace. A row
+ * never reaches an earlier row or another sequence, whatever it holds. */
 int s1_op_linattn_async(const void* q, const void* k, const void* v, int32_t dtype, int64_t q_stride,
                         int64_t k_stride, int64_t v_stride, const float* log_decay, int32_t n_seq,
                         const int32_t* row0, const int32_t* len, int32_t H, int32_t dk, int32_t dv, float scale,

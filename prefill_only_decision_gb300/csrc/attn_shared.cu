@@ -14,7 +14,8 @@
 // keys with S in TMEM columns of their own: while the softmax works on one half, the products P V of
 // the half before and S of the half behind it run. (One S of 128 columns: softmax and products of a
 // stream take turns, and both streams' products collide; 65536 rows, 1340 packed rows x 16 heads: 574
-// us, in halves 470. The halves' S reads Q twice, 1.5 x the shared-memory time of S.)
+// us, in halves 471, or 525 after a second of load, when the clock has come down. The halves' S reads Q
+// twice, 1.5 x the shared-memory time of S.)
 // Work items are (kv head, query tile or pair of tiles); an item's key tiles are split over `ns` CTAs
 // when that shortens the call, and combine_kernel joins their (o, m, l) in an order that the sizes fix
 // (no atomics: the same bits every time). One CTA per SM, 15 warps (19 with an e4m3 prefix):

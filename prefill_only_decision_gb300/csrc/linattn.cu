@@ -13,8 +13,8 @@
 // head at 128 x 128, about 2.9 us of an SM's share of the HBM rate; the products of a chunk take
 // about 1.3 us of tensor time. Measured: 4.0 us a chunk with all SMs busy (the chain of the state from
 // chunk to chunk through two products and two passes of the value-row warps) and 6 us before the first
-// and behind the last; 1024 rows x 16 heads f16 21.6 us, 16476 x 32 bf16 188 us
-// (its reads and writes alone: 81).
+// and behind the last; 1024 rows x 16 heads f16 21.7 us, 16476 x 32 bf16 189 us, f16
+// 217 (its reads and writes alone: 81); 64 x 64, 16476 x 32 bf16 151, f16 180 (40).
 // Operand precision: products take 16-bit operands and sum in fp32. Q, K and V enter as given: of a row's
 // decay lam^(i+1) = 2^e r, Q takes 2^e (exact), the outputs r in fp32, the weights 1 / r with their own
 // decay (a rounded decayed Q put the outputs' error at 1.57 x one rounding to the rows' type, instead of
