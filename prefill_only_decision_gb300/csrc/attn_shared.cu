@@ -7,7 +7,7 @@
 // tile reads each 128-key tile of the prefix once; s1_op_attention's kernel, one tile per
 // (sequence, q head), reads it once per sequence and head.
 //
-// One pass over the keys with a running maximum and sum in fp32, in two streams of S = Q K^T,
+// One pass over the keys with a running base (near the maximum) and sum in fp32, in two streams of S = Q K^T,
 // softmax, O += P V that share the tensor cores. The streams are two query tiles over the same key
 // tiles or, with one query tile an item (small calls, and the last of an odd count), that tile over
 // the even and the odd key tiles, joined at the end. A stream takes a key tile in two halves of 64
@@ -22,8 +22,8 @@
 //   warp 0      TMA producer: f16 prefix tiles
 //   warps 1, 14 MMA issue of stream 0 and 1
 //   warps 2-5, 6-9  softmax of stream 0, 1: one thread per row (TMEM lane), 64 scores in registers.
-//               Running max with a lazy rescale (O and l move only when the row's maximum grows by more
-//               than 2^GROW, once the last P V has completed). P (f16) goes back into the TMEM columns of
+//               Running base with a lazy rescale (O and l move only when the row's weights would pass
+//               2^TOP, once the last P V has completed). P (f16) goes back into the TMEM columns of
 //               S and is the A operand of O += P V from there: no shared-memory round trip. Warps whose
 //               32 rows are all past the tile's last row leave at once: their polling slowed the others.
 //   warps 10-13 loaders: the batch's own keys (gathered row by row through the sequence table), and
@@ -58,12 +58,12 @@ constexpr int BQ = 128, BKV = 128;
 constexpr int threads_of(bool e4m3) { return (e4m3 ? 19 : 15) * 32; }
 constexpr int TMEM_COLS = 512;               // S of stream x at 128 x, O at 256 + 128 x
 constexpr int T_O = 256;
-// Weights are 2^(z - m + HEAD), z the score and m the running maximum (log2 domain), which a row's maximum may
-// pass by GROW before it moves: at most 2^15, within f16. So a weight keeps f16's precision down to 2^-24 of
-// the largest, and one that is lost is below 2^-35 of it: 65536 of those are 2^-19 of the result. (HEAD = 0 and
-// GROW = 8 lost what lies below 2^-25: behind a sink, all of the result. GROW of 8, 6, 5, 4, 3 with HEAD = 15 -
-// GROW: 1340 rows over 65536 keys 472, 471, 473, 478, 484 us.)
-constexpr float GROW = 5.f, HEAD = 15.f - GROW;
+// Weights are 2^(z - m), z the score (log2 domain) and m a base that a row moves to HEAD below its maximum when they
+// would pass 2^TOP, within f16. So a weight keeps f16's precision down to 2^-24 of the largest, and one that is
+// lost is below 2^-35 of it: 65536 of those are 2^-19 of the result. (A base at the maximum, moved when that grew by
+// 2^8, lost what lies below 2^-25: behind a sink, all of the result. HEAD of 7, 9, 10, 11, 12: 1340 rows over 65536
+// keys 472, 471, 473, 478, 484 us.) Maxima past FAR are their own base: fp32 does not hold HEAD beside them.
+constexpr float HEAD = 10.f, TOP = 15.f, FAR = 4194304.f;
 
 __device__ uint64_t g_given_up;              // when a bounded wait last gave up, per device; never cleared
 
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
     const uint32_t tS = tmem + lane_off + x * 128, tO = tmem + lane_off + T_O + x * 128;
     const float sl2 = a.scale * 1.4426950408889634f;
     const uint64_t sl2_2 = pack2(sl2, sl2);
-    float m = -INFINITY;                       // running maximum (log2 domain)
+    float m = -INFINITY;                       // the row's base
     uint64_t l2 = 0;                           // the row's sum, two partial sums
     bool ok = true;
     int li = 0;                                // half tiles this stream has taken
@@ -544,11 +544,12 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
           mx4[e] = fmaxf(mx4[e], fmaxf(__uint_as_float(u[k + e]), __uint_as_float(u[k + 4 + e])));
       const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
       float alpha = 1.f;
-      if (mx > m + GROW) {
-        alpha = m == -INFINITY ? 1.f : ex2(m - mx);
-        m = mx;
+      if (mx - m > TOP) {
+        const float to = fabsf(mx) < FAR ? mx - HEAD : mx;
+        alpha = m == -INFINITY ? 1.f : ex2(m - to);
+        m = to;
       }
-      const float base = m == -INFINITY ? 0.f : m - HEAD;
+      const float base = m == -INFINITY ? 0.f : m;
       if (li > 1 && __any_sync(0xffffffffu, alpha != 1.f)) {   // once the last P V has completed
         if (!wwait(&o_step[2 * x + (hh ^ 1)], ((li - 2) >> 1) & 1)) { ok = false; break; }
         fence_after();
@@ -714,8 +715,8 @@ __global__ void __launch_bounds__(threads_of(E4M3), 1)
   }
 }
 
-// Joins the parts of a row: M = max m, o = sum 2^(m - M) o / sum 2^(m - M) l. A part without a visible key
-// (m = -inf, l = 0) holds no sums. A block joins 32 rows x 8 columns; warp w takes the parts w, w + W, ...,
+// Joins the parts of a row, m their bases: M = max m, o = sum 2^(m - M) o / sum 2^(m - M) l. A part without a
+// visible key (m = -inf, l = 0) holds no sums. A block joins 32 rows x 8 columns; warp w takes the parts w, w + W, ...,
 // and the W sums are joined through shared memory: every order is fixed by the sizes. All of a warp's reads
 // are issued together (reading m before o, part after part, cost 5.6 us for 9 parts and 9 us for 19, mostly
 // round trips to L2).
@@ -732,7 +733,7 @@ __global__ void __launch_bounds__(CWARPS * 32, 4)
   const int mt = tile % pl.MT, g = tile / pl.MT;
   const int rows = min(pl.RT, pl.V - mt * pl.RT) * pl.G;       // of this query tile
   if (quad * 32 >= rows) {
-    wait_prerequisites();                                      // (every CTA: this grid's end is then the one before's, too)
+    wait_prerequisites();                                      // (every CTA: a grid's end is then the one before's, too)
     return;
   }
   const TabView tab{table.n, table.cum, table.row0};

@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* mma_idle = bars + 21;              // [2]
   uint64_t* in_full = bars + 26;               // the start state is in shared memory
   uint64_t* in_free = bars + 27;               // it has been taken from there
-  uint64_t* k_known = bars + 25;               // max |K| of the chunk is known (f16)
+  uint64_t* k_known = bars + 25;               // the exponents of K's rows are known (f16)
   uint64_t* p_read = bars + 28;                // Q K^T has left TMEM (bf16)
   uint64_t* r_known = bars + 29;               // [4 quadrants] both halves of its rows' largest weights are known (f16)
   uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   };
   // f16: the larger exponent of both halves, rows 4 lane .. + 3; those rows' weights lam^(n-1-t)
   auto exps4 = [&](volatile signed char* e, int* x) {
-    const int a = *reinterpret_cast<volatile int*>(e + 4 * lane), b = *reinterpret_cast<volatile int*>(e + C + 4 * lane);
+    const int a = *reinterpret_cast<volatile int*>(e + 4 * lane);
+    const int b = *reinterpret_cast<volatile int*>(e + C + 4 * lane);
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[k] = max((int)(signed char)(a >> 8 * k), (int)(signed char)(b >> 8 * k));
   };
@@ -532,7 +533,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               }
             }
             mk = max(mk & 0xffffu, mk >> 16);
-            k_exp[(ph * 2 + half) * C + i] = (signed char)(mk > 0 && i < end - beg - c * C ? exp_above(h_bits(mk)) : -128);
+            const bool in = i < end - beg - c * C;
+            k_exp[(ph * 2 + half) * C + i] = (signed char)(mk > 0 && in ? exp_above(h_bits(mk)) : -128);
             arrive(k_known);
             // the state after this chunk: lam^n S and the terms, row by row
             if (!wwait(&clean[st], sph) || !wwait(k_known, ph)) break;
@@ -1081,7 +1083,9 @@ __global__ void __launch_bounds__(128)
 
 }  // namespace lin
 
-cudaError_t linattn_gave_up_word(uint64_t** out) { return cudaGetSymbolAddress(reinterpret_cast<void**>(out), lin::g_given_up); }
+cudaError_t linattn_gave_up_word(uint64_t** out) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(out), lin::g_given_up);
+}
 
 // Rows per segment (a multiple of the chunk) for a group of sequences: the count with the least
 // estimated time in us. A CTA's cost is a fixed part and a part per chunk, as measured at 128 x 128 (3.1

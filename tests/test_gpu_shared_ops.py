@@ -1027,3 +1027,34 @@ def test_linattn_f16_sparse_large_elements(B, D, state, log_decay):
             floor += v[rows].max() * k[rows].sum(0) * (lam ** (n - min(n, c + 128)))[:, None]
         es = np.abs(a.S_out[s].double().cpu().numpy() - S[s])
         assert (es <= (2.0 ** -16 + 2.0 ** -18) * A[s] + 2.0 ** -37 * floor[:, None, :] + 1e-9).all()
+
+
+@pytest.mark.parametrize("fmt", ["f16", "e4m3"])
+@pytest.mark.parametrize("e", [-24, -6, -2, -1, 0, 1, 3, 5])
+def test_attention_scores_far_from_zero(B, fmt, e):
+    """Equal scores of 2^22 2^e (up to 2^27, where fp32's steps are 8 and more): every weight is the same, whatever
+    its rounding, so the result is the values' mean (tol()); and one key behind them that scores a step of its
+    type higher (2^12 2^e and more, so it takes all the weight) gives its value, rounded."""
+    hd, P = 64, 700
+    for one in (False, True):
+        if one and e < -2:
+            continue
+        a = Attn(B, 4, 1, hd, P, [3], fmt, own=False)
+        k = torch.full((P, hd), 256.0, dtype=torch.float16)
+        if one:
+            k[555] += 0.25 if fmt == "f16" else 32
+        if fmt == "f16":
+            a.kv[0, :P, 0] = k.cuda()
+        else:
+            k, v = k.cuda(), torch.from_numpy(np.random.default_rng(6).standard_normal((P, hd))).half().cuda()
+            B.op_kv_quant_async(k.data_ptr(), v.data_ptr(), B.S1_F16, hd, hd, P, 1, hd, a.kv.data_ptr(),
+                                a.scales.data_ptr(), a.cap, 0, stream())
+            a.used = (E4M3[a.kv[:, :P].cpu().numpy()] *
+                      a.scales[:, :, :P].double().cpu().numpy().transpose(0, 2, 1)[..., None])
+        a.x[:] = 256
+        a.scale = 2.0 ** e
+        a.call()
+        B.op_sync(stream())
+        got = a.out.double().cpu().numpy()
+        ref = a.used[1][555, 0] if one else a.used[1][:, 0].mean(0)
+        assert np.abs(got - ref).max() <= a.tol(), (one, np.abs(got - ref).max())
