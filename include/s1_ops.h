@@ -179,8 +179,9 @@ int s1_op_attention_shared_workspace(int32_t n_seq, const int32_t* len, int32_t 
  * aligned. States, and sums over rows, are fp32; for the products the weights within 128 rows and
  * a copy of the state are each rounded once to dtype (a copy only: the state itself keeps its
  * bits), and decayed values are split into parts that leave 2^-24 of each, or f16 2^-37 of the
- * largest within 128 rows where that is more. workspace: as above, s1_op_linattn_workspace. A row
- * never reaches an earlier row or another sequence, whatever it holds. */
+ * largest within 128 rows where that is more (f16 terms 2^-28 below a row's largest weight lose
+ * bits, too). workspace: as above, s1_op_linattn_workspace. A row never reaches an earlier row or
+ * another sequence, whatever it holds. */
 int s1_op_linattn_async(const void* q, const void* k, const void* v, int32_t dtype, int64_t q_stride,
                         int64_t k_stride, int64_t v_stride, const float* log_decay, int32_t n_seq,
                         const int32_t* row0, const int32_t* len, int32_t H, int32_t dk, int32_t dv, float scale,

@@ -32,6 +32,8 @@
 // whole chunk, and a bound that grew by n max|v| max|k| a chunk, needed a pass over the weights less, 16384 rows x 32
 // heads 212 us instead of 218, 8000 x 16 of 64 52 instead of 58; but a key of 4000 in a later row cost ordinary
 // rows before it percents, and so did elements of 9000 rows after them where the decay had long forgotten them.)
+// What lies 2^28 below a row's largest weight, or below the bound, loses bits: an output whose values are all zeros
+// next to such a weight keeps less of what the state gives it (bf16 has no such limit).
 // The decayed values, with the state they are added to, are scaled by 2^b (b per chunk, from its largest decayed
 // value), so that the low parts stay above f16's smallest number: a decayed value keeps 2^-24 of itself down to 2^-13
 // of the chunk's largest, and is off by at most 2^-37 of that below.
