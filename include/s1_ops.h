@@ -109,7 +109,8 @@ int s1_op_rmsnorm(const float* x, const float* w, int32_t R, int32_t d, float ep
  * S1_ERR_UNSUPPORTED for a shape the kernels do not take. Outputs must not overlap inputs
  * except where stated. A workspace holds nothing between calls: calls ordered on one stream may
  * share one, calls (or graph replays) that can overlap need one each. */
-enum { S1_KV_F16 = 0, S1_KV_E4M3 = 1 };   /* formats of a K/V snapshot */
+enum { S1_KV_F16 = 0, S1_KV_E4M3 = 1,     /* formats of a K/V snapshot */
+       S1_KV_BF16 = 2 };                  /* (of a paged cache only) */
 
 /* Waits for `stream` and reports a bounded device wait that gave up in any of the operators
  * below on the current device, whichever stream it ran on, and that no earlier call has reported
@@ -195,6 +196,87 @@ int s1_op_linattn_step_async(const void* q, const void* k, const void* v, int32_
                              int64_t k_stride, int64_t v_stride, const float* log_decay, int32_t n, int32_t H,
                              int32_t dk, int32_t dv, float scale, const float* S_in, int64_t s_in_stride,
                              float* S_out, void* out, void* stream);
+
+/* ---- stream-ordered operators around a paged K/V cache -------------------------------------
+ * For sequences with caches of their own that grow row by row: rotary positions, rows appended to
+ * pages, attention of prompts and of single tokens over the pages. Calls, streams, workspaces, errors
+ * and s1_op_sync as for the operators above. */
+
+/* Rotary positions: of each head's first 2 * n_pairs elements, pair (i, i + n_pairs) is turned by the
+ * angle pos[axis[i]] * inv_freq[i] (rotate-half; the rest of the head stays as it is):
+ *   y_i = x_i cos - x_{i+n_pairs} sin,   y_{i+n_pairs} = x_{i+n_pairs} cos + x_i sin.
+ * Text has one axis; pictures and video have one for each of time, height and width, in runs of
+ * pairs or taking turns, as axis says. Angles are exact to 2^-64 turns times the position, whatever the
+ * position; sine, cosine and products are fp32. Negated frequencies undo a rotation (and give its gradient). */
+typedef struct s1_rope_spec {
+  const double* inv_freq;      /* host [n_pairs], radians per position, finite                    */
+  const uint8_t* axis;         /* host [n_pairs], each below n_axes; NULL: axis 0                 */
+  int32_t n_pairs;             /* a multiple of 8, at most hd / 2                                 */
+  int32_t n_axes;              /* 1 .. 4                                                          */
+} s1_rope_spec;
+
+/* A paged cache. data: [2, n_pages, Hkv, page_rows, hd] (K plane, V plane), f16, bf16, or e4m3 codes with
+ * scales fp32 [2, n_pages, Hkv, page_rows] (positive; appended rows follow s1_op_kv_quant_async's rule, so
+ * theirs are powers of two), 16-byte aligned (scales 4). page_rows 16, 32, 64 or 128; hd 64 or 128.
+ * table: DEVICE int32 [n_seq, table_stride], the first cols of a row in use: row j of sequence s is row
+ * j % page_rows of page table[s][j / page_rows]. Entries past a sequence's rows are not read. A page id
+ * outside 0 .. n_pages - 1 is never followed: its rows read as zeros, and rows appended to it are dropped. */
+typedef struct s1_kv_pages {
+  void* data;
+  float* scales;               /* NULL unless S1_KV_E4M3 */
+  int32_t format;              /* S1_KV_F16, S1_KV_BF16 or S1_KV_E4M3 */
+  int32_t n_pages, page_rows, Hkv, hd;
+  const int32_t* table;
+  int32_t n_seq, cols;
+  int64_t table_stride;
+} s1_kv_pages;
+
+/* Rotates rows: x of dtype (S1_F16, S1_BF16, S1_F32), row i at x + i * x_stride (elements), [H][hd] within a
+ * row (q and k slices of a projection that lie side by side are one call); hd 64 or 128. pos: DEVICE
+ * int32, axis a of row i at pos[a * pos_stride + i], any value. out: out_dtype (dtype, or for fp32 rows any of the three),
+ * row stride out_stride; out == x with the same type and stride rotates in place, no other overlap.
+ * 16-byte aligned rows take wide accesses, others element accesses. */
+int s1_op_rope_async(const void* x, int32_t dtype, int64_t x_stride, int32_t n_rows, int32_t H, int32_t hd,
+                     const s1_rope_spec* rope, const int32_t* pos, int64_t pos_stride, void* out, int32_t out_dtype,
+                     int64_t out_stride, void* stream);
+
+/* Appends rows to a paged cache, rotated on the way: row i (q [Hq][hd], k and v [Hkv][hd] of dtype, strides in
+ * elements) becomes row at[i] of sequence seq[i]; its k and q are rotated at pos (as in s1_op_rope_async;
+ * NULL: at[i] on every axis; rope NULL: no rotation), k and v are rounded to the cache's format (to nearest; e4m3: the
+ * fp32 values quantised by s1_op_kv_quant_async's rule), q to q_dtype in q_out [n_rows, Hq, hd] (S1_F16 or S1_BF16; q and
+ * q_out both NULL, then Hq 0: no queries). seq, at: DEVICE int32; seq NULL: row i belongs to sequence i (n_rows <= n_seq).
+ * at[i] < 0: the row is padding, nothing of it is written. A place that does not exist (a sequence or row outside the table,
+ * a bad page id) drops k and v. Two rows of one call must not name one place. Other rows of the
+ * pages are not touched. */
+int s1_op_kv_append_async(const void* q, const void* k, const void* v, int32_t dtype, int64_t q_stride, int64_t k_stride,
+                          int64_t v_stride, int32_t n_rows, int32_t Hq, const s1_rope_spec* rope, const int32_t* pos,
+                          int64_t pos_stride, const int32_t* seq, const int32_t* at, const s1_kv_pages* pages, void* q_out,
+                          int32_t q_dtype, void* stream);
+
+/* Attention of one new token of each of n sequences over its pages (n <= n_seq): token s at position
+ * p = pos[s] (DEVICE int32) of table row s sees the cached rows j <= p with p - j < window or j < sinks (window 0: all
+ * of them; its own row, too, so append it first):  out = softmax(sm_scale q.k) v, q head h reading kv head
+ * floor(h * Hkv / Hq). q, out: q_dtype, which is the pages' type (S1_F16 or S1_BF16 with e4m3
+ * pages), q row stride q_stride (a multiple of 8 elements), out [n, Hq, hd]; q, out 16-byte aligned.
+ * Rows past the table's cols * page_rows do not exist. A token that sees nothing (pos < 0) gives zeros. Each visible
+ * row is read once for up to 16 q heads of its kv head, long and short sequences' rows split evenly over the SMs and
+ * joined in a fixed order; the split follows pos on the device, so a captured call stays balanced as positions grow.
+ * Softmax statistics and sums are fp32, the weights are rounded once to the product's 16-bit type (f16 for e4m3 codes),
+ * f16 with its precision down to 2^-28 of the largest. What hidden rows hold does not matter. */
+int s1_op_attention_paged_step_async(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n, int32_t Hq,
+                                     const s1_kv_pages* pages, const int32_t* pos, int32_t window, int32_t sinks,
+                                     float sm_scale, void* out, void* workspace, int64_t workspace_bytes, void* stream);
+int s1_op_attention_paged_step_workspace(int32_t n, int32_t Hq, int32_t Hkv, int32_t hd, int64_t* bytes);
+
+/* The same for prompts: sequence s has query rows row0[s] .. +len[s]-1 (host arrays, as in
+ * s1_op_attention_shared_async) at positions pos0[s] .. (host; pos0 + len <= cols * page_rows) of table row s, and each
+ * sees the rows that a token at its position sees. Rows of no sequence are not written. */
+int s1_op_attention_paged_async(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n_seq, const int32_t* row0,
+                                const int32_t* len, const int32_t* pos0, int32_t Hq, const s1_kv_pages* pages,
+                                int32_t window, int32_t sinks, float sm_scale, void* out, void* workspace,
+                                int64_t workspace_bytes, void* stream);
+int s1_op_attention_paged_workspace(int32_t n_seq, const int32_t* len, const int32_t* pos0, int32_t Hq, int32_t Hkv,
+                                    int32_t hd, int32_t window, int32_t sinks, int64_t* bytes);
 
 /* ---- instrumentation of a model (handles from s1.h) -------------------------------------
  * s1_profile(m, 1) starts recording CUDA events around every launch of the model on its

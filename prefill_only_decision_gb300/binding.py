@@ -18,6 +18,7 @@ S1_OK, S1_ERR_INVALID_ARG, S1_ERR_INVALID_HANDLE, S1_ERR_OOM, S1_ERR_BUDGET, S1_
     S1_ERR_DEVICE_TIMEOUT, S1_ERR_UNSUPPORTED = range(8)
 S1_F32, S1_BF16, S1_F16 = 0, 1, 2
 S1_KV_F16, S1_KV_E4M3 = 0, 1             # K/V snapshot formats of op_attention_shared_async
+S1_KV_BF16 = 2                           # (of a paged cache only)
 S1_NOALLOC_WS_FLOATS = 4 * 1024 * 1024   # fixed split-K scratch of s1_op_gemm_noalloc (include/s1_ops.h)
 S1_STAT_COUNT = 8
 PROF_NCLASS = 8
@@ -114,6 +115,14 @@ def lib():
         "s1_op_linattn_workspace": (C.c_int, [i32, vp, i32, i32, i32, P(i64)]),
         "s1_op_linattn_step_async": (C.c_int, [vp, vp, vp, i32, i64, i64, i64, vp, i32, i32, i32, i32, f32, vp, i64,
                                                vp, vp, vp]),
+        "s1_op_rope_async": (C.c_int, [vp, i32, i64, i32, i32, i32, vp, vp, i64, vp, i32, i64, vp]),
+        "s1_op_kv_append_async": (C.c_int, [vp, vp, vp, i32, i64, i64, i64, i32, i32, vp, vp, i64, vp, vp, vp, vp, i32,
+                                            vp]),
+        "s1_op_attention_paged_step_async": (C.c_int, [vp, i32, i64, i32, i32, vp, vp, i32, i32, f32, vp, vp, i64, vp]),
+        "s1_op_attention_paged_step_workspace": (C.c_int, [i32, i32, i32, i32, P(i64)]),
+        "s1_op_attention_paged_async": (C.c_int, [vp, i32, i64, i32, vp, vp, vp, i32, vp, i32, i32, f32, vp, vp, i64,
+                                                  vp]),
+        "s1_op_attention_paged_workspace": (C.c_int, [i32, vp, vp, i32, i32, i32, i32, i32, P(i64)]),
         "s1_gemm_plan": (C.c_int, [i32, i32, i32, i32, i32, i32, P(i32)]),
     }
     for name, (res, args) in sig.items():
@@ -572,3 +581,97 @@ def op_linattn_step_async(q: int, k: int, v: int, dtype: int, q_stride: int, k_s
     _fits(n | H | dk | dv)
     check(lib().s1_op_linattn_step_async(q, k, v, dtype, q_stride, k_stride, v_stride, log_decay, n, H, dk, dv, scale,
                                          S_in, s_in_stride, S_out, out, stream))
+
+
+# -- stream-ordered operators around a paged K/V cache -------------------------------------------
+class Rope(C.Structure):
+    """A rotation (s1_rope_spec): radians per position of each pair, and the pairs' position axes
+    (None: one axis). Keeps its own copies."""
+    _fields_ = [("inv_freq", C.c_void_p), ("axis", C.c_void_p), ("n_pairs", C.c_int32), ("n_axes", C.c_int32)]
+
+    def __init__(self, inv_freq, axis=None, n_axes: Optional[int] = None):
+        self._w = np.ascontiguousarray(inv_freq, dtype=np.float64)
+        a = np.zeros(self._w.shape, np.int64) if axis is None else np.asarray(axis)
+        if self._w.ndim != 1 or a.shape != self._w.shape:
+            raise ValueError("inv_freq and axis must be 1-D and of the same length")
+        if a.size and (a.dtype.kind not in "iu" or a.min() < 0 or a.max() > 255):
+            raise ValueError("an axis is out of range")
+        self._a = np.ascontiguousarray(a, dtype=np.uint8)
+        if n_axes is None:
+            n_axes = int(a.max()) + 1 if a.size else 1
+        _fits(n_axes)
+        super().__init__(_addr(self._w), _addr(self._a), len(self._w), n_axes)
+
+
+class KvPages(C.Structure):
+    """A paged cache (s1_kv_pages); pointers are device addresses, the caller keeps their memory."""
+    _fields_ = [("data", C.c_void_p), ("scales", C.c_void_p), ("format", C.c_int32), ("n_pages", C.c_int32),
+                ("page_rows", C.c_int32), ("Hkv", C.c_int32), ("hd", C.c_int32), ("table", C.c_void_p),
+                ("n_seq", C.c_int32), ("cols", C.c_int32), ("table_stride", C.c_int64)]
+
+    def __init__(self, data: int, scales: int, format: int, n_pages: int, page_rows: int, Hkv: int, hd: int, table: int,
+                 n_seq: int, cols: int, table_stride: Optional[int] = None):
+        _fits(format | n_pages | page_rows | Hkv | hd | n_seq | cols)
+        super().__init__(data, scales, format, n_pages, page_rows, Hkv, hd, table, n_seq, cols,
+                         cols if table_stride is None else table_stride)
+
+
+def _ref(spec):
+    """Address of a spec (NULL for None)."""
+    return None if spec is None else C.addressof(spec)
+
+
+def op_rope_async(x: int, dtype: int, x_stride: int, n_rows: int, H: int, hd: int, rope: Rope, pos: int, pos_stride: int,
+                  out: int, out_dtype: int, out_stride: int, stream: int = 0):
+    """Rotary positions with one or several axes (s1_op_rope_async)."""
+    _fits(n_rows | H | hd)
+    check(lib().s1_op_rope_async(x, dtype, x_stride, n_rows, H, hd, _ref(rope), pos, pos_stride, out, out_dtype,
+                                 out_stride, stream))
+
+
+def op_kv_append_async(q: int, k: int, v: int, dtype: int, q_stride: int, k_stride: int, v_stride: int, n_rows: int,
+                       Hq: int, rope: Optional[Rope], pos: int, pos_stride: int, seq: int, at: int, pages: KvPages,
+                       q_out: int, q_dtype: int, stream: int = 0):
+    """Append rotated keys, and values, to a paged cache (s1_op_kv_append_async)."""
+    _fits(n_rows | Hq)
+    check(lib().s1_op_kv_append_async(q, k, v, dtype, q_stride, k_stride, v_stride, n_rows, Hq, _ref(rope), pos,
+                                      pos_stride, seq, at, _ref(pages), q_out, q_dtype, stream))
+
+
+def op_attention_paged_step_async(q: int, q_dtype: int, q_stride: int, n: int, Hq: int, pages: KvPages, pos: int,
+                                  window: int, sinks: int, sm_scale: float, out: int, workspace: int,
+                                  workspace_bytes: int, stream: int = 0):
+    """Attention of one new token of each sequence over its pages (s1_op_attention_paged_step_async)."""
+    _fits(n | Hq | window | sinks)
+    check(lib().s1_op_attention_paged_step_async(q, q_dtype, q_stride, n, Hq, _ref(pages), pos, window, sinks, sm_scale,
+                                                 out, workspace, workspace_bytes, stream))
+
+
+def op_attention_paged_step_workspace(n: int, Hq: int, Hkv: int, hd: int) -> int:
+    """Workspace bytes of op_attention_paged_step_async for these sizes on the current device."""
+    _fits(n | Hq | Hkv | hd)
+    out = C.c_int64()
+    check(lib().s1_op_attention_paged_step_workspace(n, Hq, Hkv, hd, C.byref(out)))
+    return out.value
+
+
+def op_attention_paged_async(q: int, q_dtype: int, q_stride: int, row0, lens, pos0, Hq: int, pages: KvPages, window: int,
+                             sinks: int, sm_scale: float, out: int, workspace: int, workspace_bytes: int,
+                             stream: int = 0):
+    """Attention of prompt rows over their pages (s1_op_attention_paged_async)."""
+    _fits(Hq | window | sinks)
+    r0, ln = _seq_arrays(row0, lens)
+    p0, _ = _seq_arrays(pos0, lens)
+    check(lib().s1_op_attention_paged_async(q, q_dtype, q_stride, len(r0), _addr(r0), _addr(ln), _addr(p0), Hq,
+                                            _ref(pages), window, sinks, sm_scale, out, workspace, workspace_bytes,
+                                            stream))
+
+
+def op_attention_paged_workspace(lens, pos0, Hq: int, Hkv: int, hd: int, window: int, sinks: int) -> int:
+    """Workspace bytes of op_attention_paged_async for these sizes on the current device."""
+    _fits(Hq | Hkv | hd | window | sinks)
+    ln, p0 = _seq_arrays(lens, pos0)
+    out = C.c_int64()
+    check(lib().s1_op_attention_paged_workspace(len(ln), _addr(ln), _addr(p0), Hq, Hkv, hd, window, sinks,
+                                                C.byref(out)))
+    return out.value

@@ -239,4 +239,56 @@ cudaError_t launch_linattn(const LinAttnArgs& a, int n_seq, const int* row0, con
 int64_t linattn_ws_bytes(int n_seq, const int* len, int H, int dk, int dv, int num_sms);
 cudaError_t launch_linattn_step(const LinAttnArgs& a, int n, cudaStream_t st);
 
+
+// ---- operators around a paged K/V cache (stream-ordered; s1_ops.h) ----
+enum KvFormat { KVF_F16 = 0, KVF_E4M3 = 1, KVF_BF16 = 2 };   // the values of S1_KV_*
+struct PagesArgs {
+  void* data;                  // [2, n_pages, Hkv, page_rows, hd]
+  float* scales;               // [2, n_pages, Hkv, page_rows] (e4m3)
+  int format, n_pages, shift;  // page_rows = 1 << shift
+  int Hkv, hd;
+  const int* table;            // [n_seq, table_stride]
+  int n_seq, cols;
+  int64_t table_stride;
+};
+constexpr int MAX_PAIRS = 64;  // hd / 2
+struct RopeArgs {
+  uint64_t turn[MAX_PAIRS];    // turns per position, the fraction in units of 2^-64
+  uint8_t axis[MAX_PAIRS];
+  int n_pairs;                 // 0: no rotation
+};
+struct RowsArgs {
+  const void *q, *k, *v;       // rows to rotate (k, v NULL: rotation alone)
+  int64_t q_stride, k_stride, v_stride;
+  int n_rows, Hq, hd;
+  const int* pos;              // [n_axes, pos_stride]; NULL: at on every axis
+  int64_t pos_stride;
+  const int *seq, *at;
+  PagesArgs pages;
+  void* q_out;
+  int q_out_type;              // ElemType
+  int64_t q_out_stride;
+  RopeArgs rope;
+};
+cudaError_t launch_rope_rows(const RowsArgs& a, int dtype, cudaStream_t st);
+
+struct PagedAttnArgs {
+  const void* q;
+  int bf16;                    // q and out: bf16, else f16
+  int64_t q_stride;
+  int Hq;
+  PagesArgs pages;
+  int window, sinks;
+  float scale;
+  void *out, *ws;
+};
+// Single tokens: pos on the device.
+cudaError_t launch_attention_paged_step(const PagedAttnArgs& a, int n, const int* pos, int num_sms, cudaStream_t st);
+int64_t attention_paged_step_ws_bytes(int n, int Hq, int Hkv, int hd, int num_sms);
+// Prompts: sequences as host arrays (empty ones allowed).
+cudaError_t launch_attention_paged(const PagedAttnArgs& a, int n_seq, const int* row0, const int* len, const int* pos0,
+                                   int num_sms, cudaStream_t st);
+int64_t attention_paged_ws_bytes(int n_seq, const int* len, const int* pos0, int Hq, int Hkv, int hd, int window, int sinks,
+                                 int num_sms);
+
 }  // namespace s1
