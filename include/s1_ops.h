@@ -217,7 +217,7 @@ typedef struct s1_rope_spec {
 
 /* A paged cache. data: [2, n_pages, Hkv, page_rows, hd] (K plane, V plane), f16, bf16, or e4m3 codes with
  * scales fp32 [2, n_pages, Hkv, page_rows] (positive; appended rows follow s1_op_kv_quant_async's rule, so
- * theirs are powers of two), 16-byte aligned (scales 4). page_rows 16, 32, 64 or 128; hd 64 or 128.
+ * theirs are powers of two), both 16-byte aligned. page_rows 16, 32, 64 or 128; hd 64 or 128.
  * table: DEVICE int32 [n_seq, table_stride], the first cols of a row in use: row j of sequence s is row
  * j % page_rows of page table[s][j / page_rows]. Entries past a sequence's rows are not read. A page id
  * outside 0 .. n_pages - 1 is never followed: its rows read as zeros, and rows appended to it are dropped. */
@@ -262,7 +262,7 @@ int s1_op_kv_append_async(const void* q, const void* k, const void* v, int32_t d
  * row is read once for up to 16 q heads of its kv head, long and short sequences' rows split evenly over the SMs and
  * joined in a fixed order; the split follows pos on the device, so a captured call stays balanced as positions grow.
  * Softmax statistics and sums are fp32, the weights are rounded once to the product's 16-bit type (f16 for e4m3 codes),
- * f16 with its precision down to 2^-28 of the largest. What hidden rows hold does not matter. */
+ * f16 with its precision down to 2^-24 of the largest. What hidden rows hold does not matter. */
 int s1_op_attention_paged_step_async(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n, int32_t Hq,
                                      const s1_kv_pages* pages, const int32_t* pos, int32_t window, int32_t sinks,
                                      float sm_scale, void* out, void* workspace, int64_t workspace_bytes, void* stream);

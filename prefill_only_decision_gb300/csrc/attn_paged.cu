@@ -100,13 +100,6 @@ cudaError_t launch_simple(const PromptTab& t, const PagedAttnArgs& a, const int*
 }
 }  // namespace pga
 
-cudaError_t launch_attention_paged_step(const PagedAttnArgs& a, int n, const int* pos, int, cudaStream_t st) {
-  pga::PromptTab t;
-  t.n = 0;
-  return pga::launch_simple(t, a, pos, n, st);
-}
-int64_t attention_paged_step_ws_bytes(int, int, int, int, int) { return 0; }
-
 cudaError_t launch_attention_paged(const PagedAttnArgs& a, int n_seq, const int* row0, const int* len, const int* pos0,
                                    int, cudaStream_t st) {
   pga::PromptTab t;

@@ -197,6 +197,7 @@ constexpr int SEQ_TAB_SMALL = 64, SEQ_TAB_LARGE = 2048;   // sequences per launc
 // Words of the current device in which the operators' bounded waits note that they gave up.
 cudaError_t attention_shared_gave_up_word(uint64_t** out);
 cudaError_t linattn_gave_up_word(uint64_t** out);
+cudaError_t attention_step_gave_up_word(uint64_t** out);
 // A tensor map encoded afresh (arguments as tensor_map's).
 bool encode_tensor_map(CUtensorMap* out, CUtensorMapDataType dtype, int rank, const void* ptr, const uint64_t* dims,
                        const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);

@@ -46,8 +46,8 @@ int check_pages(const s1_kv_pages* p, PagesArgs* out) {
   if ((int64_t)p->cols * p->page_rows > INT32_MAX) return unsupported("pages: a sequence of more than 2^31 - 1 rows");
   if (!p->data || (!p->table && p->n_seq > 0 && p->cols > 0)) return bad("pages: a NULL pointer");
   if ((p->format == S1_KV_E4M3) != (p->scales != nullptr)) return bad("pages: scales go with S1_KV_E4M3, and only with it");
-  if (!aligned(p->data, 16) || !aligned(p->scales, 4) || !aligned(p->table, 4))
-    return bad("pages: misaligned pointer (data 16 bytes, scales and table 4)");
+  if (!aligned(p->data, 16) || !aligned(p->scales, 16) || !aligned(p->table, 4))
+    return bad("pages: misaligned pointer (data and scales 16 bytes, table 4)");
   int shift = 4;
   while ((1 << shift) < p->page_rows) ++shift;
   *out = PagesArgs{p->data, p->scales, p->format, p->n_pages, shift, p->Hkv, p->hd, p->table, p->n_seq, p->cols,
