@@ -1,123 +1,1031 @@
-// Attention over a paged K/V cache: prompts and single tokens, with a sliding window and sinks.
+// Attention of prompts over a paged K/V cache, with a sliding window and sinks, on the 5th-generation tensor cores.
 //
-// The simplest right form: a warp per (query row, q head) takes the visible rows one by one with a running maximum and sum.
+// Query row i of sequence s, at position p, sees the cached rows j <= p with p - j < window or j < sinks:
+// o = softmax(scale q.k) v. The rows of a sequence and the G = Hq / Hkv q heads that share a kv head are packed into tiles of
+// 128 matrix rows, RT = floor(128 / G) query rows x G heads. An item is (sequence, tile or two neighbouring tiles, kv head) with
+// the 128-key tiles that its rows see: the sinks' and the window's. Its key tiles are split over `ns` CTAs, one choice per
+// sequence, when that shortens the call, and combine_kernel joins their (o, m, l) in an order that the sizes fix.
+//
+// One pass over the keys with a running base (near the maximum) and sum in fp32, in two streams of S = Q K^T, softmax,
+// O += P V that share the tensor cores: two query tiles over the same key tiles, or one query tile over the even and the odd
+// key tiles, joined at the end. A stream takes a key tile in two halves of 64 keys with S in TMEM columns of their own, so that
+// products run while the softmax works on the other half. One CTA per SM, 15 warps (19 with e4m3 pages):
+//   warp 0      TMA producer: a page box (page x 64 elements) per lane, page ids asked for a tile ahead
+//   warps 1, 14 MMA issue of stream 0 and 1
+//   warps 2-5, 6-9  softmax of stream 0, 1: one thread per row (TMEM lane), 64 scores in registers, a lazy rescale of O; P
+//               goes back into the TMEM columns of S and is the A operand of O += P V from there
+//   warps 10-13 scan the value tiles that hold rows which some query does not see: a hidden row's weight is an exact zero, but
+//               0 x NaN is not, so non-finite elements there become 0 and the epilogue adds them to the rows that do see
+//               them. (Rows behind a sequence's end and pages that are not loaded are such rows.) With e4m3 pages they widen
+//               the K tiles instead and warps 15-18 the V tiles, codes from memory through registers.
+// e4m3 pages: the operands are f16, code x scale x 2^(7 - E), E a bound of the scales' exponents (K: of the tile; V: running,
+// so that O keeps one unit, rescaled when the bound grows): scales of any size fit f16, and a row 2^-27 below the largest keeps
+// its code's bits. bf16 queries over them become f16 by a power of two per row.
+// Every mbarrier wait is bounded; on expiry an error word is set and every role leaves.
 #include <algorithm>
 #include <climits>
+#include <type_traits>
+#include <vector>
 
 #include <cuda_fp8.h>
 
-#include "common.cuh"
-#include "kvrows.cuh"
+#include "paged.cuh"
 
 namespace s1 {
-namespace pga {
+namespace pgp {
+using namespace t5;
+using namespace pga;
 
-constexpr int TAB = 1024;
-// Packed sequences of one launch by value: rows of sequence seq[i] are row0[i] .. row0[i] + cum[i + 1] - cum[i] - 1.
-struct PromptTab {
-  int n;
-  int cum[TAB + 1];
-  int row0[TAB], pos0[TAB], seq[TAB];
+constexpr int BQ = 128, BKV = 128, TAB_SMALL = 64, TAB_LARGE = 1024;
+enum Kind { F16 = 0, BF16 = 1, E4M3 = 2, E4M3_QBF = 3 };
+constexpr bool is_e4m3(int kind) { return kind >= E4M3; }
+constexpr bool out_bf16(int kind) { return kind == BF16 || kind == E4M3_QBF; }
+constexpr int threads_of(int kind) { return (is_e4m3(kind) ? 19 : 15) * 32; }
+constexpr int TMEM_COLS = 512;               // S of stream x at 128 x, O at 256 + 128 x
+constexpr int T_O = 256;
+constexpr int BASES = 16;                    // tiles whose exponent bounds are kept (more than are ever in flight)
+
+__device__ uint64_t g_given_up;              // when a bounded wait last gave up, per device; never cleared
+
+// Sequences of one launch, by value (a captured graph keeps its own copy), those with split items first.
+template <int N>
+struct Tab {
+  int n, split;                // sequences; CTAs of the split ones
+  int start[N + 1];            // first CTA of a sequence
+  int tiles[N + 1];            // query tiles x kv heads of the split sequences before it
+  int row0[N], pos0[N], len[N], seq[N], ns[N];
+};
+struct Plan {
+  int G, RT, nt;               // q heads per kv head, query rows per tile, tiles per item
 };
 
-template <typename T>
-__global__ void __launch_bounds__(256)
-    simple_kernel(const __grid_constant__ PromptTab tab, const __grid_constant__ PagedAttnArgs a, const int* pos, int n) {
-  allow_dependents();
-  wait_prerequisites();
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int64_t rows = pos ? n : tab.cum[tab.n];
-  if (item >= rows * a.Hq) return;
-  const int v = (int)(item / a.Hq), h = (int)(item % a.Hq);
-  int s = v, p, row = v;
-  if (pos) {
-    p = pos[v];
+template <int HD>
+struct Lay {
+  static constexpr int TILE = BKV * HD * 2;
+  static constexpr int F = HD == 128 ? 5 : 7, FR = 3;     // stages of both streams' ring, or of each stream's own; odd
+  static constexpr int Q = 0;                             // per tile HD/64 boxes of [128 rows][128 B]
+  static constexpr int KV2 = Q + 2 * BQ * HD * 2;         // stages with two query tiles
+  static constexpr int KV1 = Q + BQ * HD * 2;             // with one
+  static constexpr int QSC = KV2 + F * TILE;              // [2][128] floats: what a row's q was divided by
+  static constexpr int BASE = QSC + 2 * BQ * 4;           // [2][BASES] exponent bounds
+  static constexpr int BAR = BASE + 2 * BASES * 4;
+  static constexpr int NS = 2 * FR > F ? 2 * FR : F;
+  static constexpr int NBAR = 1 + 4 * NS + 12 + 2 + 2 + 4;
+  static constexpr int USED = BAR + NBAR * 8 + 16;
+  static_assert(USED <= 227 * 1024, "shared memory of one CTA");
+  // above half an SM: each CTA allocates all of TMEM, so two never share one
+  static constexpr int BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
+  static constexpr int OSTR = HD + 4;                     // floats per row of a stream's published sums
+  static_assert(KV1 + 2 * FR * TILE <= QSC, "both rings fit");
+  static_assert(BQ * OSTR * 4 <= 2 * FR * TILE, "published sums fit the K/V stages");
+  static_assert(F % 2 == 1 && FR % 2 == 1, "a slot holds K and V tiles in turn");
+};
+
+// A stage of the ring of K and V tiles K_0, V_0, K_1, ... With two query tiles both streams read one ring; with one, each
+// stream has its own, of its tiles: a parity wait must never run more than one phase ahead of a slot, nor behind it. For that
+// K and V fills have barriers of their own, too: who waits for one kind does not see the other's phases.
+struct Slot {
+  int s;
+  uint32_t ph, kind_ph;        // parity of this fill, and of it among the slot's fills of its kind (they take turns)
+};
+template <int F, int FR>
+__device__ __forceinline__ Slot slot_of(bool two, int t, bool is_v) {
+  const uint32_t i = 2 * (two ? t : t >> 1) + (is_v ? 1 : 0);
+  if (two) return {(int)(i % F), i / F & 1, i / F >> 1 & 1};
+  return {(t & 1 ? FR : 0) + (int)(i % FR), i / FR & 1, i / FR >> 1 & 1};
+}
+
+template <bool BF>
+__device__ __forceinline__ bool nonfinite2(uint32_t x) {   // either element of the pair
+  constexpr uint32_t E = BF ? 0x7f80u : 0x7c00u;
+  return (x & E) == E || (x >> 16 & E) == E;
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t drop_nonfinite2(uint32_t x) {
+  constexpr uint32_t E = BF ? 0x7f80u : 0x7c00u;
+  if ((x & E) == E) x &= 0xffff0000u;
+  if ((x >> 16 & E) == E) x &= 0xffffu;
+  return x;
+}
+template <bool BF>
+__device__ __forceinline__ bool drop_nonfinite(uint4& x) {   // true: there was one
+  if (!(nonfinite2<BF>(x.x) || nonfinite2<BF>(x.y) || nonfinite2<BF>(x.z) || nonfinite2<BF>(x.w))) return false;
+  x = make_uint4(drop_nonfinite2<BF>(x.x), drop_nonfinite2<BF>(x.y), drop_nonfinite2<BF>(x.z), drop_nonfinite2<BF>(x.w));
+  return true;
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack_w(float a, float b) {
+  if constexpr (BF) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
   } else {
-    int i = 0;
-    while (tab.cum[i + 1] <= v) ++i;
-    row = tab.row0[i] + v - tab.cum[i];
-    p = tab.pos0[i] + v - tab.cum[i];
-    s = tab.seq[i];
+    return h2u(a, b);
   }
-  const PagesArgs& pg = a.pages;
-  const int kvh = h / (a.Hq / pg.Hkv), E = pg.hd / 32;
-  float q[4], o[4] = {};
-  for (int e = 0; e < E; ++e)
-    q[e] = kvc::to_f(((const T*)a.q)[row * a.q_stride + (int64_t)h * pg.hd + e * 32 + lane]);
-  float m = -INFINITY, l = 0.f;
-  const int64_t end = min((int64_t)p + 1, (int64_t)pg.cols << pg.shift);
-  for (int64_t j = 0; j < end; ++j) {
-    if (a.window && p - j >= a.window && j >= a.sinks) {
-      j = p - a.window;                      // (the next is the window's first)
-      continue;
+}
+__device__ __forceinline__ float pow2f(int e) { return ldexpf(1.f, e); }   // (rare: any e)
+
+// Eight e4m3 codes times f to f16. FAST: f is an f16 value.
+template <bool FAST>
+__device__ __forceinline__ uint4 codes_to_half(const uint2 c, float f) {
+  const uint32_t w[2] = {c.x, c.y};
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 x = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3));
+    if constexpr (FAST) {
+      const __half2 y = __hmul2(x, __float2half2_rn(f));
+      h[i] = *reinterpret_cast<const uint32_t*>(&y);
+    } else {
+      const float2 z = __half22float2(x);
+      h[i] = h2u(z.x * f, z.y * f);
     }
-    const int id = pg.table[s * pg.table_stride + (j >> pg.shift)];
-    const bool ok = id >= 0 && id < pg.n_pages;
-    const int64_t vec = (((int64_t)id * pg.Hkv + kvh) << pg.shift) + (j & ((1 << pg.shift) - 1));
-    const int64_t plane = ((int64_t)pg.n_pages * pg.Hkv) << pg.shift;
-    float k[4], vv[4], dot = 0.f;
-    for (int e = 0; e < E; ++e) {
-      const int64_t i0 = vec * pg.hd + e * 32 + lane, i1 = i0 + plane * pg.hd;
-      k[e] = vv[e] = 0.f;
-      if (!ok) continue;
-      if (pg.format == KVF_E4M3) {
-        const auto dec = [&](int64_t i) {
-          return __half2float(__half(__nv_cvt_fp8_to_halfraw(((const __nv_fp8_storage_t*)pg.data)[i], __NV_E4M3)));
+  }
+  return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+// The exponent bound of a scale: scale < 2^E. Scales that are not finite or not there have none.
+constexpr int NO_BOUND = -1000;
+__device__ __forceinline__ int bound_of(float scale) {
+  const uint32_t u = __float_as_uint(scale);
+  return (u >> 23) == 0 || (u >> 23) >= 255 ? NO_BOUND : (int)(u >> 23) - 126;
+}
+
+template <int HD, int KIND, int N>
+__global__ void __launch_bounds__(threads_of(KIND), 1)
+    paged_kernel(const __grid_constant__ Tab<N> tab, const __grid_constant__ CUtensorMap mapKV,
+                 const __grid_constant__ PagedAttnArgs a, const Plan pl) {
+  using L = Lay<HD>;
+  constexpr bool E4 = is_e4m3(KIND), PBF = KIND == BF16, OBF = out_bf16(KIND);
+  constexpr int NB = HD / 64, F = L::F, FR = L::FR, NS = L::NS;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  uint64_t* bars = (uint64_t*)(sm + L::BAR);
+  uint64_t* q_full = bars;
+  uint64_t* full = bars + 1;                   // [NS] a K tile is there
+  uint64_t* vfull = full + NS;                 // [NS] a V tile is there
+  uint64_t* empty = vfull + NS;                // [NS]
+  uint64_t* ready = empty + NS;                // [NS] the V tile holds no non-finite element of a hidden row (not with e4m3)
+  uint64_t* s_full = ready + NS;               // [2 streams][2 halves of the key tile]
+  uint64_t* p_full = s_full + 4;               // [2][2]
+  uint64_t* o_step = p_full + 4;               // [2][2] the half's P V has completed
+  uint64_t* o_done = o_step + 4;               // [2] the stream's last product has completed
+  uint64_t* mma_idle = o_done + 2;             // [2]
+  uint64_t* joined = mma_idle + 2;             // [4 quadrants] stream 1's sums are published
+  uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // a value of a partly hidden tile is not finite
+  volatile int* base_k = (volatile int*)(sm + L::BASE);    // [BASES] by tile
+  volatile int* base_v = base_k + BASES;
+
+  const PagesArgs& pg = a.pages;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  // this CTA's sequence, item and part
+  int si = 0;
+  for (int hi = tab.n - 1; si < hi;) {
+    const int mid = (si + hi + 1) >> 1;
+    if (tab.start[mid] <= (int)blockIdx.x) si = mid;
+    else hi = mid - 1;
+  }
+  const int len = tab.len[si], ns = tab.ns[si], MT = (len + pl.RT - 1) / pl.RT, MP = (MT + pl.nt - 1) / pl.nt;
+  const int local = (int)blockIdx.x - tab.start[si], part = local % ns, item = local / ns;
+  const int g = item % pg.Hkv, mp = MP - 1 - item / pg.Hkv;   // (the last rows see most: first)
+  const bool two = pl.nt == 2 && 2 * mp + 1 < MT;  // two query tiles; else one over alternate key tiles
+  const int v0 = pl.nt * mp * pl.RT;               // first row of the item, and one past its last
+  const int v1 = min(len, v0 + (two ? 2 : 1) * pl.RT);
+  const int p_first = tab.pos0[si] + v0, p_last = tab.pos0[si] + v1 - 1;
+  Seen all;                                        // what some row of the item sees
+  all.end = p_last + 1;
+  all.lo = a.window && p_first - (a.window - 1) > 0 ? p_first - (a.window - 1) : 0;
+  all.sk = min(a.sinks, all.lo);
+  const Tiles tl = tiles_of<BKV>(all);
+  const int total = tl.count(), per = (total + ns - 1) / ns;
+  const int jb = min(total, part * per), n = min(total, jb + per) - jb;
+  uint8_t* kvst = sm + (two ? L::KV2 : L::KV1);
+  // a key tile that some row does not see in full
+  auto partly = [&](int j0) {
+    return j0 + BKV - 1 > p_first || (a.window && p_last - j0 >= a.window && j0 + BKV > a.sinks);
+  };
+
+  // quadrants of 32 matrix rows that stream x's query tile fills (a single tile: both streams')
+  auto quads = [&](int x) { return (min(pl.RT, v1 - (v0 + (two && x ? pl.RT : 0))) * pl.G + 31) / 32; };
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 8);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], E4 ? 4 : 1);
+      mbar_init(&vfull[s], E4 ? 4 : 1);
+      mbar_init(&empty[s], two ? 2 : 1);       // the streams that read the slot
+      mbar_init(&ready[s], 4);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&mma_idle[x], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&s_full[2 * x + h], 1);
+        mbar_init(&p_full[2 * x + h], quads(x));
+        mbar_init(&o_step[2 * x + h], 1);
+      }
+      mbar_init(&o_done[x], 1);
+    }
+    for (int x = 0; x < 4; ++x) mbar_init(&joined[x], 1);
+    *abort_flag = 0;
+    *v_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc<TMEM_COLS>(tmem_slot);
+  allow_dependents();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto wwait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_given_up) ? 1 : 0) != 0;
+  };
+  // the fills in the order in which they are made: K_0 .. K_{lead-1}, then V_t, K_{t+lead}; fn(t, is V) for those that there are
+  const int lead = two ? 1 : 2;
+  auto fills = [&](auto&& fn) {
+    for (int q = 0; q < 2 * n + lead - 1; ++q) {
+      const int e = q - lead;
+      const bool is_v = e >= 0 && !(e & 1);
+      const int t = e < 0 ? q : is_v ? e >> 1 : lead + (e >> 1);
+      if (!fn(t, is_v)) break;
+    }
+  };
+
+  uint32_t done = 0;           // (producer) per slot and kind: begun (bit d), parity of the last fill (bit 16 + d)
+  if (warp == 0) {
+    // ---- TMA producer
+    wait_prerequisites();
+    if constexpr (!E4) {
+      const int npg = BKV >> pg.shift, box = lane % NB, pp = lane / NB, last = (all.end - 1) >> pg.shift;
+      const int64_t trow = (int64_t)tab.seq[si] * pg.table_stride;
+      auto page_id = [&](int t) {              // of this lane's part of tile t
+        if (t >= n || pp >= npg) return -1;
+        const int col = (tl.at(jb + t) * BKV >> pg.shift) + pp;
+        return col <= last ? pg.table[trow + col] : -1;
+      };
+      int id_next = page_id(0), id = -1, id_before = -1;      // of the K tile to come, of the latest and of the one before it
+      fills([&](int t, bool is_v) {
+        if (!is_v) {
+          id_before = id;
+          id = id_next;
+        }
+        if (t >= n) return true;
+        const Slot k = slot_of<F, FR>(two, t, is_v);
+        const int s = k.s, j0 = tl.at(jb + t) * BKV, pid = is_v && lead == 2 ? id_before : id;
+        if (!wwait(&empty[s], k.ph ^ 1)) return false;
+        const int there = min(npg, last - (j0 >> pg.shift) + 1);   // pages that the sequence has
+        uint64_t* bar = is_v ? &vfull[s] : &full[s];
+        if (lane == 0) mbar_expect_tx(bar, (uint32_t)(there << pg.shift) * (HD * 2));
+        __syncwarp();
+        if (pp < there)
+          tma5(kvst + s * L::TILE + box * (BKV * 128) + (pp << pg.shift) * 128, &mapKV, bar, 64 * box, 0, g, pid, is_v ? 1 : 0);
+        const int d = 2 * s + (is_v ? 1 : 0);
+        done = (done & ~(1u << (16 + d))) | 1u << d | k.kind_ph << (16 + d);
+        if (!is_v) id_next = page_id(t + 1);
+        return true;
+      });
+    }
+  } else if (warp == 1 || warp == 14) {
+    // ---- MMA issue of stream x: the whole warp waits, one lane issues. A stream's products run in
+    // the order they are issued, so S of its next tile may take the columns that P V reads before it
+    const int x = warp == 1 ? 0 : 1;
+    const bool leader = elect_one();
+    constexpr uint32_t ID_S = idesc_f16(BKV / 2, PBF, 0, 0), ID_O = idesc_f16(HD, PBF, 0, 1);
+    const uint32_t tS = tmem + x * 128, tO = tmem + T_O + x * 128;
+    const uint64_t qd = desc_sw128(smem_u32(sm + L::Q) + (two && x ? BQ * HD * 2 : 0), 16);
+    auto scores = [&](int h, int s) {          // S = Q K^T over half h of the tile in slot s
+      const uint64_t kd = desc_sw128(smem_u32(kvst + s * L::TILE) + h * (BKV / 2 * 128), 16);
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; ++kk) {
+        const uint64_t off = (uint64_t)(((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4);
+        mma_ss(tS + h * (BKV / 2), qd + (uint64_t)(((kk >> 2) * (BQ * 128) + (kk & 3) * 32) >> 4), kd + off, ID_S,
+               kk > 0 ? 1u : 0u);
+      }
+      commit(&s_full[2 * x + h]);
+    };
+    auto values = [&](int h, int s, bool acc) {   // O += P V over half h
+      const uint64_t vd = desc_sw128(smem_u32(kvst + s * L::TILE) + h * (BKV / 2 * 128), BKV * 128);
+#pragma unroll
+      for (int kk = 0; kk < BKV / 32; ++kk)
+        mma_ts(tO, tS + h * (BKV / 2) + kk * 8, vd + (uint64_t)(kk * 16 * 128 >> 4), ID_O, (acc || kk > 0) ? 1u : 0u);
+      commit(&o_step[2 * x + h]);
+    };
+    wait_prerequisites();                      // (a bounded wait must not begin while the calls before still run)
+    // of each half h: P V of tile i - 1, then S of tile i into the same columns
+    const int cnt = two ? n : (n + 1 - x) >> 1;
+    if (cnt > 0 && wwait(q_full, 0))
+      for (int i = 0; i <= cnt; ++i) {
+        const int t = two ? i : 2 * i + x;
+        const Slot k = slot_of<F, FR>(two, t, false);                    // (unused at i = cnt)
+        const Slot v = slot_of<F, FR>(two, t - (two ? 1 : 2), true);     // (unused at i = 0)
+        auto half = [&](auto hc) {
+          constexpr int h = decltype(hc)::value;
+          if (i > 0) {
+            if (h == 0 && (!wwait(&vfull[v.s], v.kind_ph) || (!E4 && !wwait(&ready[v.s], v.kind_ph)))) return false;
+            if (!wwait(&p_full[2 * x + h], (i - 1) & 1)) return false;
+            fence_after();
+            if (leader) {
+              values(h, v.s, h > 0 || i > 1);
+              if (h) commit(&empty[v.s]);
+              if (h && i == cnt) commit(&o_done[x]);
+            }
+            __syncwarp();
+          }
+          if (i < cnt) {
+            if (h == 0) {
+              if (!wwait(&full[k.s], k.kind_ph)) return false;
+              fence_after();
+            }
+            if (leader) {
+              scores(h, k.s);
+              if (h) commit(&empty[k.s]);
+            }
+            __syncwarp();
+          }
+          return true;
         };
-        k[e] = dec(i0) * pg.scales[vec];
-        vv[e] = dec(i1) * pg.scales[vec + plane];
-      } else if (pg.format == KVF_BF16) {
-        k[e] = bf2f(((const bf16*)pg.data)[i0]);
-        vv[e] = bf2f(((const bf16*)pg.data)[i1]);
-      } else {
-        k[e] = h2f(((const f16*)pg.data)[i0]);
-        vv[e] = h2f(((const f16*)pg.data)[i1]);
+        if (!half(std::integral_constant<int, 0>{}) || !half(std::integral_constant<int, 1>{})) break;
+      }
+    if (leader) {
+      commit(&mma_idle[x]);
+      mbar_drain(&mma_idle[x], 0);             // every MMA issued above has completed
+    }
+  } else if (warp >= 10 && warp != 14) {
+    const int lw = warp < 14 ? warp - 10 : warp - 15;
+    wait_prerequisites();
+    if constexpr (!E4) {
+      // ---- scan of the partly hidden V tiles: rows 32 lw .. +31
+      constexpr int CH = HD / 8, RPI = 32 / CH;
+      for (int t = 0; t < n; ++t) {
+        const Slot k = slot_of<F, FR>(two, t, true);
+        if (!wwait(&vfull[k.s], k.kind_ph)) break;
+        if (partly(tl.at(jb + t) * BKV)) {
+          uint8_t* tile = kvst + k.s * L::TILE;
+          const int c = lane % CH;
+          bool bad = false;
+#pragma unroll 4
+          for (int p = 0; p < 32 / RPI; ++p) {
+            const int r = lw * 32 + p * RPI + lane / CH;
+            uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * (BKV * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            uint4 x = *at;
+            if (drop_nonfinite<PBF>(x)) {
+              *at = x;
+              bad = true;
+            }
+          }
+          if (bad) *v_flag = 1;
+          fence_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ready[k.s]);
+      }
+    } else {
+      // ---- e4m3 pages: this warp's 32 rows of every tile of its plane. LPR lanes of 16 codes per row, RP rows a pass, PN
+      // passes; the lanes of a row's second 64 columns take their two 8-code halves in the other order, so that no store
+      // conflicts. Rows that no query sees are zeros.
+      const int plane = warp < 14 ? 0 : 1;
+      constexpr int LPR = HD / 16, RP = 32 / LPR, PN = 32 / RP;
+      const int ci = lane % LPR, sw = HD == 128 && ci >= 4 ? 1 : 0;
+      const int c0 = ((2 * ci) & 7) + sw, c1 = ((2 * ci) & 7) + 1 - sw;
+      const int64_t trow = (int64_t)tab.seq[si] * pg.table_stride;
+      const int mask = (1 << pg.shift) - 1;
+      auto vector_of = [&](int key) -> int64_t {               // of a cached row's K, -1: none that a query sees
+        if (key >= all.end || (key < all.lo && key >= all.sk)) return -1;
+        const int id = pg.table[trow + (key >> pg.shift)];
+        if (id < 0 || id >= pg.n_pages) return -1;
+        return (((int64_t)id * pg.Hkv + g) << pg.shift) + (key & mask);
+      };
+      const int64_t to_v = ((int64_t)pg.n_pages * pg.Hkv) << pg.shift;   // from a K vector to its V vector
+      uint4 code[PN];                                          // of this warp's rows of its plane's next tile
+      int64_t vec = -1, vec_next = -1;                         // vector of row `lane` in tile t + 1, and in the one behind it
+      int64_t q4[4], q4_next[4];                               // the K vectors of rows lane, lane + 32, .. of those tiles
+      float sk4[4], sv4[4];                                    // their scales, of tile t + 1
+      int run_v = NO_BOUND;
+      auto lookup = [&](int t) {
+        const int j0 = t < n ? tl.at(jb + t) * BKV : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q4_next[i] = t < n ? vector_of(j0 + 32 * i + lane) : -1;
+        vec_next = lw == 0 ? q4_next[0] : lw == 1 ? q4_next[1] : lw == 2 ? q4_next[2] : q4_next[3];
+        if (plane && vec_next >= 0) vec_next += to_v;
+      };
+      auto read = [&](int64_t v, int p) {
+        const int64_t w = __shfl_sync(0xffffffffu, v, p * RP + lane / LPR);
+        return w >= 0 ? __ldg(reinterpret_cast<const uint4*>((const uint8_t*)pg.data + w * HD) + ci) : make_uint4(0, 0, 0, 0);
+      };
+      auto fetch = [&]() {                                     // scales and codes of the tile that lookup found
+        vec = vec_next;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          q4[i] = q4_next[i];
+          sk4[i] = plane == 0 && q4[i] >= 0 ? __ldg(pg.scales + q4[i]) : 0.f;
+          sv4[i] = q4[i] >= 0 ? __ldg(pg.scales + q4[i] + to_v) : 0.f;
+        }
+#pragma unroll
+        for (int p = 0; p < PN; ++p) code[p] = read(vec, p);
+      };
+      lookup(0);
+      if (n > 0) fetch();
+      lookup(1);
+      for (int t = 0; t < n; ++t) {
+        const Slot k = slot_of<F, FR>(two, t, plane == 1);
+        // exponent bounds: of the tile's K scales, and the running one of V's (both planes' warps follow it)
+        int bk = NO_BOUND, bv = NO_BOUND;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          bk = max(bk, bound_of(sk4[i]));
+          bv = max(bv, bound_of(sv4[i]));
+        }
+        bk = __reduce_max_sync(0xffffffffu, bk);
+        run_v = max(run_v, __reduce_max_sync(0xffffffffu, bv));
+        if (bk == NO_BOUND) bk = 0;
+        const int E = plane ? (run_v == NO_BOUND ? 0 : run_v) : bk;
+        const float mine = plane ? (lw == 0 ? sv4[0] : lw == 1 ? sv4[1] : lw == 2 ? sv4[2] : sv4[3])
+                                 : (lw == 0 ? sk4[0] : lw == 1 ? sk4[1] : lw == 2 ? sk4[2] : sk4[3]);
+        const float fac = ldexpf(mine, 7 - E);                 // below 2^7
+        if (!wwait(&empty[k.s], k.ph ^ 1)) break;
+        uint8_t* dst = kvst + k.s * L::TILE;
+        const bool fast = __all_sync(0xffffffffu, __half2float(__float2half_rn(fac)) == fac);
+        const bool check = plane && partly(tl.at(jb + t) * BKV);
+        uint8_t* d = dst + (ci >> 2) * (BKV * 128) + (lw * 32 + lane / LPR) * 128;
+        bool bad = false;
+        auto convert = [&](auto is_fast, const uint4 cc, int p) {
+          constexpr bool FAST = decltype(is_fast)::value;
+          const float f = __shfl_sync(0xffffffffu, fac, p * RP + lane / LPR);
+          const int x = (p * RP + lane / LPR) & 7;
+          const uint2 lo = make_uint2(cc.x, cc.y), hi = make_uint2(cc.z, cc.w);
+          uint4 h0 = codes_to_half<FAST>(sw ? hi : lo, f), h1 = codes_to_half<FAST>(sw ? lo : hi, f);
+          if (check) bad |= drop_nonfinite<false>(h0) | drop_nonfinite<false>(h1);
+          *reinterpret_cast<uint4*>(d + p * RP * 128 + ((c0 ^ x) << 4)) = h0;
+          *reinterpret_cast<uint4*>(d + p * RP * 128 + ((c1 ^ x) << 4)) = h1;
+        };
+        if (fast) {
+#pragma unroll
+          for (int p = 0; p < PN; ++p) convert(std::true_type{}, code[p], p);
+        } else {                               // (rare: reads the codes again, one pass at a time)
+#pragma unroll 1
+          for (int p = 0; p < PN; ++p) convert(std::false_type{}, read(vec, p), p);
+        }
+        if (bad) *v_flag = 1;
+        if (plane == 0 && lw == 0 && lane == 0) {
+          base_k[t % BASES] = bk;
+          base_v[t % BASES] = run_v == NO_BOUND ? 0 : run_v;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(plane ? &vfull[k.s] : &full[k.s]);
+        if (t + 1 < n) {
+          fetch();
+          lookup(t + 2);
+        }
       }
     }
-    for (int e = 0; e < E; ++e) dot += q[e] * k[e];
-    const float z = warp_sum(dot) * a.scale;
-    const float M = fmaxf(m, z);
-    if (M == -INFINITY) continue;
-    const float alpha = m == M ? 1.f : expf(m - M), w = z == M ? 1.f : expf(z - M);
-    l = l * alpha + w;
-    for (int e = 0; e < E; ++e) o[e] = o[e] * alpha + w * vv[e];
-    m = M;
+  } else {
+    // ---- softmax of stream x: row r = TMEM lane r
+    const int x = (warp - 2) >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const int q0 = v0 + (two && x ? pl.RT : 0);          // the tile's first row of the sequence
+    const int vq = q0 + r / pl.G;                        // this row's
+    const bool live = r < pl.RT * pl.G && vq < v1 && vq < q0 + pl.RT;
+    const int h = g * pl.G + r % pl.G;
+    const int64_t row = live ? (int64_t)tab.row0[si] + vq : -1;        // row of q and out
+    const int pos = live ? tab.pos0[si] + vq : p_last;   // (rows that are not there: any, nothing reads them)
+    const int row_lo = a.window && pos - (a.window - 1) > 0 ? pos - (a.window - 1) : 0;
+    const bool idle = quad >= quads(x);                  // no live row: nothing to do past Q's zeros
+    float* qsc = (float*)(sm + L::QSC) + (two && x ? BQ : 0);
+    wait_prerequisites();
+    {   // Q rows of the quadrant; absent rows are zeros. One tile: each stream loads half of the rows
+      constexpr int CH = HD / 8;
+      const int64_t off = live ? row * a.q_stride + (int64_t)h * HD : -1;
+      uint8_t* dst = sm + L::Q + (two && x ? BQ * HD * 2 : 0);
+      auto load = [&](auto count, int first) {           // `count` of the CH passes over 32 rows x CH chunks
+        constexpr int PN = decltype(count)::value;
+        uint4 v[PN];
+#pragma unroll
+        for (int p = 0; p < PN; ++p) {
+          const int e = (first + p) * 32 + lane;
+          const int64_t o = __shfl_sync(0xffffffffu, off, e / CH);
+          v[p] = o >= 0 ? __ldg(reinterpret_cast<const uint4*>((const uint16_t*)a.q + o) + e % CH) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int p = 0; p < PN; ++p) {
+          const int e = (first + p) * 32 + lane, rr = quad * 32 + e / CH, c = e % CH;
+          if constexpr (KIND == E4M3_QBF) {              // to f16, the row's largest element near 2^14
+            uint32_t top = 0;
+            uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
+#pragma unroll
+            for (int o = CH / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int E = min(max((int)(top >> 7) - 127, -100), 127);
+            const float up = __uint_as_float((uint32_t)(14 - E + 127) << 23);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = h2u(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
+            v[p] = make_uint4(w[0], w[1], w[2], w[3]);
+            if (c == 0) qsc[rr] = __uint_as_float((uint32_t)(E - 14 + 127) << 23);
+          }
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * (BQ * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v[p];
+        }
+      };
+      if (two) load(std::integral_constant<int, CH>{}, 0);
+      else load(std::integral_constant<int, CH / 2>{}, x * (CH / 2));
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t tS = tmem + lane_off + x * 128, tO = tmem + lane_off + T_O + x * 128;
+    float sl2 = a.scale * 1.4426950408889634f;
+    float m = -INFINITY;                       // the row's base
+    uint64_t l2 = 0;                           // the row's sum, two partial sums
+    bool ok = true;
+    int li = 0;                                // half tiles this stream has taken
+    int unit = 0;                              // e4m3: O counts 2^(unit - 7)
+    if constexpr (KIND == E4M3_QBF) {          // (all rows' factors: the two streams may have loaded half each)
+      if (n > 0) ok = wwait(q_full, 0);
+      sl2 *= qsc[r];
+    }
+    for (int t = two ? 0 : x; t < n && ok && !idle; t += (li & 1) ? 0 : two ? 1 : 2) {
+      const int hh = li & 1, ph = (li >> 1) & 1;
+      if (!wwait(&s_full[2 * x + hh], ph)) { ok = false; break; }
+      ++li;
+      fence_after();
+      uint32_t u[64];
+      tld32(tS + hh * 64, u);
+      tld32(tS + hh * 64 + 32, u + 32);
+      // visible keys of this half: columns lo .. hi, and those below sk
+      const int base_j = tl.at(jb + t) * BKV + hh * 64;
+      const int lo = row_lo - base_j, hi = pos - base_j, sk = a.sinks - base_j;
+      float zs = sl2;
+      int unit_now = unit;
+      if constexpr (E4) {
+        zs *= pow2f(base_k[t % BASES] - 7);
+        unit_now = base_v[t % BASES];
+      }
+      ld_wait();
+      pin32(u);
+      pin32(u + 32);
+      if (!__all_sync(0xffffffffu, (lo <= 0 || sk >= 64) && hi >= 63)) {   // some row does not see all keys: -inf for the hidden
+        auto upto = [](int c) { return c <= 0 ? 0ull : c >= 64 ? ~0ull : ~0ull >> (64 - c); };   // columns below c
+        const uint64_t seen = upto(hi + 1) & (~upto(lo) | upto(sk));
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (!((e < 32 ? (uint32_t)seen : (uint32_t)(seen >> 32)) & (1u << (e & 31)))) u[e] = 0xff800000u;
+      }
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < 64; k += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          mx4[e] = fmaxf(mx4[e], fmaxf(__uint_as_float(u[k + e]), __uint_as_float(u[k + 4 + e])));
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * zs;
+      float alpha = 1.f;
+      if (mx - m > TOP) {
+        const float to = fabsf(mx) < FAR ? mx - HEAD : mx;
+        alpha = m == -INFINITY ? 1.f : ex2(m - to);
+        m = to;
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+      const bool moved = E4 && unit_now != unit;
+      if (li > 1 && (moved || __any_sync(0xffffffffu, alpha != 1.f))) {   // once the last P V has completed
+        if (!wwait(&o_step[2 * x + (hh ^ 1)], ((li - 2) >> 1) & 1)) { ok = false; break; }
+        fence_after();
+        const float beta = moved ? alpha * pow2f(unit - unit_now) : alpha;
+        uint32_t w[16];
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 16) {
+          tld16(tO + c, w);
+          ld_wait();
+          pin<16>(w);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * beta);
+          tst16(tO + c, w);
+        }
+        l2 = mul2(l2, pack2(alpha, alpha));
+      }
+      unit = unit_now;
+      const uint64_t nb = pack2(-base, -base), zs2 = pack2(zs, zs);
+      uint64_t sum2 = 0;                       // (of this half: one by one, small weights would not reach a large sum)
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const uint64_t z = fma2(pack2u(u[c + e], u[c + e + 1]), zs2, nb);
+          const float p0 = ex2(lo2(z)), p1 = ex2(hi2(z));
+          sum2 = add2(sum2, pack2(p0, p1));
+          pk[e / 2] = pack_w<PBF>(p0, p1);
+        }
+        tst16(tS + hh * 64 + c / 2, pk);
+      }
+      l2 = add2(l2, sum2);
+      st_wait();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[2 * x + hh]);
+    }
+    // ---- epilogue
+    float l = lo2(l2) + hi2(l2);
+    if (ok && li > 0) ok = wwait(&o_done[x], 0);
+    fence_after();
+    const float scale_o = E4 ? pow2f(unit - 7) : 1.f;
+    auto sums = [&](int c, float* o) {         // 32 columns of this row's sums (zeros without a tile)
+      uint32_t w[32];
+      __syncwarp();
+      if (li > 0) {
+        tld32(tO + c, w);
+        ld_wait();
+        pin32(w);
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = li > 0 ? __uint_as_float(w[e]) * scale_o : 0.f;
+    };
+    float* pub = reinterpret_cast<float*>(kvst) + r * L::OSTR;
+    float w0 = 1.f, w1 = 0.f;                  // weights of the two streams' sums
+    if (!two && x == 1 && !idle) {
+      // publish (o, m, l) in the K/V stages once stream 0 has read its last tile from them
+      if (ok && n > 0) ok = wwait(&o_done[0], 0);
+      if (ok) {
+        float o[32];
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+          sums(c, o);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(pub + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+        *reinterpret_cast<float2*>(pub + HD) = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&joined[quad]);
+      }
+    } else if (!idle) {
+      if (!two && ok) {
+        ok = wwait(&joined[quad], 0);
+        if (ok) {
+          const float2 ml = *reinterpret_cast<const float2*>(pub + HD);
+          const bool has0 = !(m == -INFINITY && l == 0.f), has1 = !(ml.x == -INFINITY && ml.y == 0.f);
+          const float M = fmaxf(m, ml.x);
+          w0 = has0 ? ex2(m - M) : 0.f;
+          w1 = has1 ? ex2(ml.x - M) : 0.f;
+          if (m == ml.x) w0 = has0 ? 1.f : 0.f, w1 = has1 ? 1.f : 0.f;   // (also both infinite)
+          l = (has0 ? w0 * l : 0.f) + (has1 ? w1 * ml.y : 0.f);
+          m = M;
+        }
+      }
+      if (ok) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const bool fix = live && *v_flag;      // non-finite values of partly hidden tiles: into the rows that see them
+        const int64_t pi = (int64_t)blockIdx.x * 2 + (two ? x : 0);
+        uint8_t* ostage = sm + L::Q + (two && x ? BQ * HD * 2 : 0);
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          sums(c, o);
+          if (!two) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(pub + c + e);
+              o[e] = (w0 != 0.f ? w0 * o[e] : 0.f) + (w1 != 0.f ? w1 * y.x : 0.f);
+              o[e + 1] = (w0 != 0.f ? w0 * o[e + 1] : 0.f) + (w1 != 0.f ? w1 * y.y : 0.f);
+              o[e + 2] = (w0 != 0.f ? w0 * o[e + 2] : 0.f) + (w1 != 0.f ? w1 * y.z : 0.f);
+              o[e + 3] = (w0 != 0.f ? w0 * o[e + 3] : 0.f) + (w1 != 0.f ? w1 * y.w : 0.f);
+            }
+          }
+          if (fix)
+            for (int t = 0; t < n; ++t) {
+              const int j0 = tl.at(jb + t) * BKV;
+              if (!partly(j0)) continue;
+              for (int j = j0; j < j0 + BKV && j <= pos; ++j) {
+                if (j < row_lo && j >= a.sinks) continue;
+                const int id = pg.table[(int64_t)tab.seq[si] * pg.table_stride + (j >> pg.shift)];
+                if (id < 0 || id >= pg.n_pages) continue;
+                const int64_t vec = (((pg.n_pages + (int64_t)id) * pg.Hkv + g) << pg.shift) + (j & ((1 << pg.shift) - 1));
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const int64_t at = vec * HD + c + e;
+                  float y;
+                  if constexpr (E4) {
+                    y = __half2float(__half(__nv_cvt_fp8_to_halfraw(((const __nv_fp8_storage_t*)pg.data)[at], __NV_E4M3))) *
+                        pg.scales[vec];
+                  } else if constexpr (PBF) {
+                    y = bf2f(((const bf16*)pg.data)[at]);
+                  } else {
+                    y = h2f(((const f16*)pg.data)[at]);
+                  }
+                  if (!isfinite(y)) o[e] += y;
+                }
+              }
+            }
+          if (ns == 1) {                       // 16-bit row into the (consumed) Q tile, chunks swizzled
+            uint8_t* dst = ostage + r * (HD * 2);
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(dst + ((((c + e) / 8) ^ (r & 7)) << 4)) = make_uint4(
+                  pack_w<OBF>(o[e] * inv, o[e + 1] * inv), pack_w<OBF>(o[e + 2] * inv, o[e + 3] * inv),
+                  pack_w<OBF>(o[e + 4] * inv, o[e + 5] * inv), pack_w<OBF>(o[e + 6] * inv, o[e + 7] * inv));
+          } else {                             // the warp's [HD / 8][32] groups of 4 sums, half of the columns at a time
+            float4* stage = reinterpret_cast<float4*>(ostage + quad * (HD * 64));
+            const int half = HD / 2, cc = c % half;
+            if (c == half) {                   // the first half is out of the stage
+              if (lane == 0) tma_store_read_wait();
+              __syncwarp();
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              stage[(cc + e) / 4 * 32 + lane] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            if (cc + 32 == half) {
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                bulk_store((float*)a.ws + ((pi * 4 + quad) * HD + c + 32 - half) * 32, stage, HD * 64);
+                tma_store_commit();
+              }
+            }
+          }
+        }
+        if (ns == 1) {                         // whole rows out of the warp's stage
+          __syncwarp();
+          constexpr int CH = HD / 8;
+          const int64_t off = live ? (row * a.Hq + h) * HD : -1;
+#pragma unroll
+          for (int p = 0; p < CH; ++p) {
+            const int e = p * 32 + lane, rr = quad * 32 + e / CH, c = e % CH;
+            const int64_t o = __shfl_sync(0xffffffffu, off, e / CH);
+            if (o >= 0)
+              *reinterpret_cast<uint4*>((uint16_t*)a.out + o + c * 8) =
+                  *reinterpret_cast<const uint4*>(ostage + rr * (HD * 2) + ((c ^ (rr & 7)) << 4));
+          }
+        }
+        if (ns > 1 && lane == 0) tma_store_wait();
+        if (live && ns > 1)
+          reinterpret_cast<float2*>((float*)a.ws + (int64_t)tab.split * 2 * BQ * HD)[pi * BQ + r] = make_float2(m, l);
+      }
+    }
   }
-  for (int e = 0; e < E; ++e) {
-    const float y = l == 0.f ? 0.f : o[e] / l;
-    T* dst = (T*)a.out + ((int64_t)row * a.Hq + h) * pg.hd + e * 32 + lane;
-    if constexpr (std::is_same<T, f16>::value) *dst = f2h(y);
-    else *dst = f2bf(y);
+  __syncthreads();
+  if (warp == 0 && *abort_flag)                // nothing in flight when the CTA leaves
+    for (int d = 0; d < 2 * NS; ++d)
+      if ((done >> d) & 1) mbar_drain(d & 1 ? &vfull[d >> 1] : &full[d >> 1], (done >> (16 + d)) & 1);
+  if (warp == 1) {
+    fence_after();
+    tmem_free<TMEM_COLS>(tmem);
   }
 }
 
-cudaError_t launch_simple(const PromptTab& t, const PagedAttnArgs& a, const int* pos, int n, cudaStream_t st) {
-  const int64_t warps = (int64_t)(pos ? n : t.cum[t.n]) * a.Hq;
-  if ((warps + 7) / 8 > INT_MAX) return cudaErrorInvalidValue;
-  return launch_pdl(a.bf16 ? simple_kernel<bf16> : simple_kernel<f16>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st,
-                    t, a, pos, n);
+// Joins the parts of a row, m their bases: M = max m, o = sum 2^(m - M) o / sum 2^(m - M) l. A part without a
+// visible key (m = -inf, l = 0) holds no sums. A block joins 32 rows x 8 columns; warp w takes the parts w, w + W, ...,
+// and the W sums are joined through shared memory: every order is fixed by the sizes. A warp's reads are issued together.
+constexpr int CWARPS = 8, CCOLS = 8;
+__device__ __forceinline__ float part_weight(float m, float M) { return m == M ? 1.f : t5::ex2(m - M); }
+template <int HD, bool OBF, int N>
+__global__ void __launch_bounds__(CWARPS * 32, 4)
+    combine_kernel(const __grid_constant__ Tab<N> tab, const __grid_constant__ PagedAttnArgs a, const Plan pl) {
+  __shared__ float4 po[CWARPS][CCOLS / 4][36];
+  __shared__ float2 pml[CWARPS][32];
+  allow_dependents();
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, W = blockDim.x >> 5, Hkv = a.pages.Hkv;
+  const int cb = blockIdx.x % (HD / CCOLS), quad = blockIdx.x / (HD / CCOLS) % 4, tile = blockIdx.x / (HD / CCOLS * 4);
+  int si = 0;
+  while (tab.tiles[si + 1] <= tile) ++si;
+  const int len = tab.len[si], ns = tab.ns[si], MT = (len + pl.RT - 1) / pl.RT, MP = (MT + pl.nt - 1) / pl.nt;
+  const int lt = tile - tab.tiles[si], mt = lt % MT, g = lt / MT;
+  const int rows = min(pl.RT, len - mt * pl.RT) * pl.G;        // of this query tile
+  wait_prerequisites();                                        // (every CTA: a grid's end is then the one before's, too)
+  if (quad * 32 >= rows) return;
+  auto out_at = [&](int r) {                                   // where matrix row r of the tile goes
+    return (((int64_t)tab.row0[si] + mt * pl.RT + r / pl.G) * a.Hq + g * pl.G + r % pl.G) * HD + cb * CCOLS;
+  };
+  // this tile's parts: CTAs side by side, two tile slots each
+  const int mp = mt / pl.nt, item = (MP - 1 - mp) * Hkv + g;
+  const int64_t p0 = ((int64_t)tab.start[si] + (int64_t)item * ns) * 2 + mt % pl.nt;
+  const float2* ml = reinterpret_cast<const float2*>((const float*)a.ws + (int64_t)tab.split * 2 * BQ * HD) + p0 * BQ +
+                     quad * 32 + lane;
+  const float4* ps = reinterpret_cast<const float4*>(a.ws) + ((p0 * 4 + quad) * (HD / 4) + cb * (CCOLS / 4)) * 32 + lane;
+  float m = -INFINITY, l = 0.f;
+  float4 o[CCOLS / 4] = {};
+  constexpr int U = 4;                                         // parts read together
+  for (int p = w; p < ns; p += U * W) {
+    float2 x[U];
+    float4 v[U][CCOLS / 4];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      x[k] = make_float2(-INFINITY, 0.f);
+      if (p + k * W < ns) {
+        x[k] = __ldcg(ml + (int64_t)(p + k * W) * 2 * BQ);
+#pragma unroll
+        for (int c = 0; c < CCOLS / 4; ++c) v[k][c] = __ldcg(ps + ((int64_t)(p + k * W) * 2 * HD + c) * 32);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (x[k].x == -INFINITY && x[k].y == 0.f) continue;
+      const float M = fmaxf(m, x[k].x), wo = part_weight(m, M), wp = part_weight(x[k].x, M);
+      m = M;
+      l = wo * l + wp * x[k].y;
+#pragma unroll
+      for (int c = 0; c < CCOLS / 4; ++c) {
+        o[c].x = wo * o[c].x + wp * v[k][c].x;
+        o[c].y = wo * o[c].y + wp * v[k][c].y;
+        o[c].z = wo * o[c].z + wp * v[k][c].z;
+        o[c].w = wo * o[c].w + wp * v[k][c].w;
+      }
+    }
+  }
+  pml[w][lane] = make_float2(m, l);
+#pragma unroll
+  for (int c = 0; c < CCOLS / 4; ++c) po[w][c][lane] = o[c];
+  __syncthreads();
+  constexpr int CP = CCOLS / 2;
+  for (int i = threadIdx.x; i < 32 * CP; i += blockDim.x) {    // (row, 2 columns)
+    const int lr = i / CP, cp = i % CP, r = quad * 32 + lr;
+    if (r >= rows) continue;
+    float M = -INFINITY, sum = 0.f, y0 = 0.f, y1 = 0.f;
+    for (int k = 0; k < W; ++k) M = fmaxf(M, pml[k][lr].x);
+    for (int k = 0; k < W; ++k) {
+      const float2 x = pml[k][lr];
+      if (x.x == -INFINITY && x.y == 0.f) continue;
+      const float wp = part_weight(x.x, M);
+      const float2 v = reinterpret_cast<const float2*>(&po[k][cp >> 1][lr])[cp & 1];
+      sum += wp * x.y;
+      y0 += wp * v.x;
+      y1 += wp * v.y;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint32_t*>((uint16_t*)a.out + out_at(r) + cp * 2) = pack_w<OBF>(y0 * inv, y1 * inv);
+  }
 }
-}  // namespace pga
+
+// Key tiles of the item whose rows start at v0 of a sequence at pos0.
+int item_tiles(int pos0, int v0, int v1, int window, int sinks) {
+  const int p_first = pos0 + v0;
+  Seen s;
+  s.end = pos0 + v1;
+  s.lo = window && p_first - (window - 1) > 0 ? p_first - (window - 1) : 0;
+  s.sk = std::min(sinks, s.lo);
+  return tiles_of<BKV>(s).count();
+}
+
+// One launch: sequences s0 .. (empty ones left out) with one or two query tiles an item and, per sequence, the parts that an
+// item's key tiles are split into: the choice with the least estimated time (us, the constants measured for the kernels
+// that share this structure): a key tile takes 1.13 us with two query tiles and 0.66 with one, a CTA 4.5 besides, the join
+// 2.8 and its sums; CTAs fill the SMs as they come, the longest first. An item is split into parts of `per` key
+// tiles; at most 64 parts, and parts of at most LONGEST tiles (the tensor cores add to one sum per output and drop what lies
+// below its last bits).
+constexpr int LONGEST = 1024;
+struct Group {
+  Plan pl;
+  Tab<TAB_LARGE> tab;
+  int next;                    // the first sequence not taken
+  int max_ns;
+};
+void plan_group(Group& gr, int s0, int n_seq, const int* row0, const int* len, const int* pos0, int Hq, int Hkv, int hd,
+                int window, int sinks, int num_sms) {
+  Plan& pl = gr.pl;
+  Tab<TAB_LARGE>& t = gr.tab;
+  pl.G = Hq / Hkv;
+  pl.RT = BQ / pl.G;
+  struct Seq {
+    int s, ns;
+    int64_t items[2], sum[2];    // by tiles per item
+    int top[2];
+  };
+  static thread_local std::vector<Seq> seqs;
+  seqs.clear();
+  int s = s0;
+  int64_t all_tiles = 0;
+  for (; s < n_seq && (int)seqs.size() < TAB_LARGE; ++s) {
+    if (len[s] == 0) continue;
+    const int64_t MT = ((int64_t)len[s] + pl.RT - 1) / pl.RT;
+    if (!seqs.empty() && (all_tiles + MT) * Hkv * std::max(64, hd / 2) > INT_MAX) break;   // (CTA numbers stay within 31 bits)
+    all_tiles += MT;
+    Seq q{s, 1, {}, {}, {}};
+    for (int k = 0; k < 2; ++k) {
+      const int rows = (k + 1) * pl.RT;
+      q.items[k] = ((int64_t)len[s] + rows - 1) / rows;
+      for (int64_t v0 = 0; v0 < len[s]; v0 += rows) {
+        const int c = item_tiles(pos0[s], (int)v0, (int)std::min<int64_t>(len[s], v0 + rows), window, sinks);
+        q.sum[k] += c;
+        q.top[k] = std::max(q.top[k], c);
+      }
+    }
+    seqs.push_back(q);
+  }
+  gr.next = s;
+  double best = -1;
+  int best_per = 1;
+  pl.nt = 1;
+  for (int k = 0; k < 2; ++k) {
+    int longest = 0;
+    for (const Seq& q : seqs) longest = std::max(longest, q.top[k]);
+    const double c = k ? 1.13 : 0.66;
+    int last = 0;
+    for (int parts = (longest + LONGEST - 1) / LONGEST; parts <= 64 && parts <= longest; ++parts) {
+      const int per = (longest + parts - 1) / parts;
+      if (per == last) continue;
+      last = per;
+      double cost = 0, top = 0;
+      int64_t ctas = 0, joined = 0;
+      for (const Seq& q : seqs) {
+        const int ns = (q.top[k] + per - 1) / per;
+        const int64_t n = q.items[k] * Hkv * ns;
+        ctas += n;
+        if (ns > 1) joined += n;
+        cost += c * (double)(q.sum[k] * Hkv) + 4.5 * (double)n;
+        top = std::max(top, c * ((q.top[k] + ns - 1) / ns) + 4.5);
+      }
+      double time = ctas <= num_sms ? top : std::max(top, cost / num_sms + 0.5 * top);
+      if (joined) time += 2.8 + 0.00006 * (double)(joined * (k + 1) * hd);
+      if (best < 0 || time < best) {
+        best = time;
+        best_per = per;
+        pl.nt = k + 1;
+      }
+      if (ctas > 8ll * num_sms) break;
+    }
+  }
+  const int k = pl.nt - 1;
+  for (Seq& q : seqs) q.ns = (q.top[k] + best_per - 1) / best_per;
+  std::sort(seqs.begin(), seqs.end(), [&](const Seq& x, const Seq& y) {
+    if ((x.ns > 1) != (y.ns > 1)) return x.ns > 1;
+    if (x.ns == 1 && x.top[k] != y.top[k]) return x.top[k] > y.top[k];
+    return x.s < y.s;
+  });
+  t.n = (int)seqs.size();
+  t.start[0] = t.tiles[0] = t.split = 0;
+  gr.max_ns = 1;
+  for (int i = 0; i < t.n; ++i) {
+    const Seq& q = seqs[i];
+    t.row0[i] = row0 ? row0[q.s] : 0;
+    t.pos0[i] = pos0[q.s];
+    t.len[i] = len[q.s];
+    t.seq[i] = q.s;
+    t.ns[i] = q.ns;
+    t.start[i + 1] = t.start[i] + (int)(q.items[k] * Hkv * q.ns);
+    t.tiles[i + 1] = t.tiles[i] + (q.ns > 1 ? (int)(q.items[0] * Hkv) : 0);
+    if (q.ns > 1) t.split = t.start[i + 1];
+    gr.max_ns = std::max(gr.max_ns, q.ns);
+  }
+}
+
+template <int HD, int KIND, int N>
+cudaError_t launch_tab(const PagedAttnArgs& a, const Tab<N>& tab, const Plan& pl, int max_ns, const CUtensorMap& map,
+                       cudaStream_t st) {
+  using L = Lay<HD>;
+  CK_RET(cudaFuncSetAttribute(paged_kernel<HD, KIND, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES));
+  CK_RET(launch_pdl(paged_kernel<HD, KIND, N>, dim3((unsigned)tab.start[tab.n]), dim3(threads_of(KIND)), L::BYTES, st, tab,
+                    map, a, pl));
+  if (max_ns > 1)
+    CK_RET(launch_pdl(combine_kernel<HD, out_bf16(KIND), N>, dim3((unsigned)(tab.tiles[tab.n] * (HD / CCOLS * 4))),
+                      dim3((unsigned)(32 * std::min(CWARPS, (max_ns + 1) / 2))), 0, st, tab, a, pl));
+  return cudaSuccess;
+}
+template <int HD, int KIND>
+cudaError_t launch_group(const PagedAttnArgs& a, const Group& gr, cudaStream_t st) {
+  CUtensorMap map = {};
+  if (!is_e4m3(KIND) && !pages_map(&map, a.pages, 1 << a.pages.shift)) return cudaErrorInvalidValue;
+  const Tab<TAB_LARGE>& t = gr.tab;
+  if (t.n > TAB_SMALL) return launch_tab<HD, KIND, TAB_LARGE>(a, t, gr.pl, gr.max_ns, map, st);
+  Tab<TAB_SMALL> u;
+  u.n = t.n;
+  u.split = t.split;
+  std::copy(t.start, t.start + t.n + 1, u.start);
+  std::copy(t.tiles, t.tiles + t.n + 1, u.tiles);
+  std::copy(t.row0, t.row0 + t.n, u.row0);
+  std::copy(t.pos0, t.pos0 + t.n, u.pos0);
+  std::copy(t.len, t.len + t.n, u.len);
+  std::copy(t.seq, t.seq + t.n, u.seq);
+  std::copy(t.ns, t.ns + t.n, u.ns);
+  return launch_tab<HD, KIND, TAB_SMALL>(a, u, gr.pl, gr.max_ns, map, st);
+}
+template <int HD>
+cudaError_t launch_kind(const PagedAttnArgs& a, const Group& gr, cudaStream_t st) {
+  if (a.pages.format == KVF_F16) return launch_group<HD, F16>(a, gr, st);
+  if (a.pages.format == KVF_BF16) return launch_group<HD, BF16>(a, gr, st);
+  return a.bf16 ? launch_group<HD, E4M3_QBF>(a, gr, st) : launch_group<HD, E4M3>(a, gr, st);
+}
+}  // namespace pgp
+
+cudaError_t attention_paged_gave_up_word(uint64_t** out) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(out), pgp::g_given_up);
+}
+
+int64_t attention_paged_ws_bytes(int n_seq, const int* len, const int* pos0, int Hq, int Hkv, int hd, int window, int sinks,
+                                 int num_sms) {
+  int64_t need = 0;
+  pgp::Group gr;
+  for (int s = 0; s < n_seq; s = gr.next) {
+    pgp::plan_group(gr, s, n_seq, nullptr, len, pos0, Hq, Hkv, hd, window, sinks, num_sms);
+    need = std::max<int64_t>(need, (int64_t)gr.tab.split * 2 * pgp::BQ * (hd + 2) * 4);
+  }
+  return need;
+}
 
 cudaError_t launch_attention_paged(const PagedAttnArgs& a, int n_seq, const int* row0, const int* len, const int* pos0,
-                                   int, cudaStream_t st) {
-  pga::PromptTab t;
-  for (int s = 0; s < n_seq;) {
-    t.n = 0;
-    t.cum[0] = 0;
-    for (; s < n_seq && t.n < pga::TAB; ++s) {
-      if (len[s] == 0) continue;
-      t.row0[t.n] = row0[s];
-      t.pos0[t.n] = pos0[s];
-      t.seq[t.n] = s;
-      t.cum[t.n + 1] = t.cum[t.n] + len[s];
-      ++t.n;
-    }
-    if (t.n) CK_RET(pga::launch_simple(t, a, nullptr, 0, st));
+                                   int num_sms, cudaStream_t st) {
+  pgp::Group gr;
+  for (int s = 0; s < n_seq; s = gr.next) {
+    pgp::plan_group(gr, s, n_seq, row0, len, pos0, a.Hq, a.pages.Hkv, a.pages.hd, a.window, a.sinks, num_sms);
+    if (gr.tab.n == 0) continue;
+    CK_RET(a.pages.hd == 128 ? pgp::launch_kind<128>(a, gr, st) : pgp::launch_kind<64>(a, gr, st));
   }
   return cudaSuccess;
 }
-int64_t attention_paged_ws_bytes(int, const int*, const int*, int, int, int, int, int, int) { return 0; }
 
 }  // namespace s1

@@ -198,6 +198,7 @@ constexpr int SEQ_TAB_SMALL = 64, SEQ_TAB_LARGE = 2048;   // sequences per launc
 cudaError_t attention_shared_gave_up_word(uint64_t** out);
 cudaError_t linattn_gave_up_word(uint64_t** out);
 cudaError_t attention_step_gave_up_word(uint64_t** out);
+cudaError_t attention_paged_gave_up_word(uint64_t** out);
 // A tensor map encoded afresh (arguments as tensor_map's).
 bool encode_tensor_map(CUtensorMap* out, CUtensorMapDataType dtype, int rank, const void* ptr, const uint64_t* dims,
                        const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);

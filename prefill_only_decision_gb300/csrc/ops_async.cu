@@ -56,20 +56,21 @@ int check_lin(const void* q, const void* k, const void* v, int32_t dtype, int64_
 extern "C" {
 
 int s1_op_sync(void* stream) {
-  static GiveUps<3> told;
+  static GiveUps<4> told;
   cudaStream_t st = (cudaStream_t)stream;
-  uint64_t* word[3] = {};
+  uint64_t* word[4] = {};
   int dev = 0;
   bool any = false;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = attention_shared_gave_up_word(&word[0]);
   if (e == cudaSuccess) e = linattn_gave_up_word(&word[1]);
   if (e == cudaSuccess) e = attention_step_gave_up_word(&word[2]);
+  if (e == cudaSuccess) e = attention_paged_gave_up_word(&word[3]);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e == cudaSuccess)
     e = (cudaError_t)told.news(dev, [&](uint64_t* now) {
       cudaError_t r = cudaSuccess;
-      for (int i = 0; i < 3 && r == cudaSuccess; ++i)
+      for (int i = 0; i < 4 && r == cudaSuccess; ++i)
         r = cudaMemcpyAsync(&now[i], word[i], sizeof(now[i]), cudaMemcpyDeviceToHost, st);
       if (r == cudaSuccess) r = cudaStreamSynchronize(st);
       return (int)r;

@@ -43,7 +43,7 @@ int check_pages(const s1_kv_pages* p, PagesArgs* out) {
   if (p->Hkv < 1 || p->n_pages < 1 || p->n_seq < 0 || p->cols < 0) return bad("pages: a count is out of range");
   if (p->Hkv > 4096) return unsupported("pages: more than 4096 kv heads");
   if (p->table_stride < p->cols) return bad("pages: table_stride is below cols");
-  if ((int64_t)p->cols * p->page_rows > INT32_MAX) return unsupported("pages: a sequence of more than 2^31 - 1 rows");
+  if ((int64_t)p->cols * p->page_rows > (1 << 30)) return unsupported("pages: a table row of more than 2^30 cached rows");
   if (!p->data || (!p->table && p->n_seq > 0 && p->cols > 0)) return bad("pages: a NULL pointer");
   if ((p->format == S1_KV_E4M3) != (p->scales != nullptr)) return bad("pages: scales go with S1_KV_E4M3, and only with it");
   if (!aligned(p->data, 16) || !aligned(p->scales, 16) || !aligned(p->table, 4))
@@ -225,6 +225,9 @@ int s1_op_attention_paged_async(const void* q, int32_t q_dtype, int64_t q_stride
     if (pos0[s] < 0 || (int64_t)pos0[s] + len[s] > ((int64_t)pages->cols << a.pages.shift))
       return bad("attention_paged: a sequence ends past its table row, or starts below position 0");
   }
+  for (int s = 0; s < n_seq; ++s)
+    if (((int64_t)len[s] / (128 / (Hq / pages->Hkv)) + 1) * pages->Hkv * 64 > INT32_MAX)
+      return unsupported("attention_paged: a sequence of too many rows x heads for one call");
   if (rows == 0) return S1_OK;
   if (!q || !out) return bad("attention_paged: a NULL pointer");
   a.q = q;
