@@ -356,7 +356,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       for (int t = 0; t < n; ++t) {
         const Slot k = slot_of<F, FR>(two, t, true);
         if (!wwait(&vfull[k.s], k.kind_ph)) break;
-        if (partly(tl.at(jb + t) * BKV)) {
+        const int j0 = tl.at(jb + t) * BKV;
+        if (partly(j0)) {
           uint8_t* tile = kvst + k.s * L::TILE;
           const int c = lane % CH;
           bool bad = false;
@@ -367,7 +368,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
             uint4 x = *at;
             if (drop_nonfinite<PBF>(x)) {
               *at = x;
-              bad = true;
+              const int j = j0 + r;            // (rows that no query sees hold anything: nobody asks for their values)
+              bad |= j < all.end && (j >= all.lo || j < all.sk);
             }
           }
           if (bad) *v_flag = 1;
@@ -697,19 +699,32 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
                 const int id = pg.table[(int64_t)tab.seq[si] * pg.table_stride + (j >> pg.shift)];
                 if (id < 0 || id >= pg.n_pages) continue;
                 const int64_t vec = (((pg.n_pages + (int64_t)id) * pg.Hkv + g) << pg.shift) + (j & ((1 << pg.shift) - 1));
+                if constexpr (E4) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const int64_t at = vec * HD + c + e;
-                  float y;
-                  if constexpr (E4) {
-                    y = __half2float(__half(__nv_cvt_fp8_to_halfraw(((const __nv_fp8_storage_t*)pg.data)[at], __NV_E4M3))) *
-                        pg.scales[vec];
-                  } else if constexpr (PBF) {
-                    y = bf2f(((const bf16*)pg.data)[at]);
-                  } else {
-                    y = h2f(((const f16*)pg.data)[at]);
+                  for (int e = 0; e < 32; ++e) {
+                    const float y = __half2float(__half(__nv_cvt_fp8_to_halfraw(
+                                        ((const __nv_fp8_storage_t*)pg.data)[vec * HD + c + e], __NV_E4M3))) *
+                                    pg.scales[vec];
+                    if (!isfinite(y)) o[e] += y;
                   }
-                  if (!isfinite(y)) o[e] += y;
+                } else {
+                  const uint4* at = reinterpret_cast<const uint4*>((const uint16_t*)pg.data + vec * HD + c);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const uint4 y = at[e];
+                    const uint32_t y4[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                      if (nonfinite2<PBF>(y4[i])) {
+                        float f[2];
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                          const uint16_t raw = (uint16_t)(y4[i] >> (16 * z));
+                          f[z] = PBF ? __uint_as_float((uint32_t)raw << 16) : __half2float(__ushort_as_half(raw));
+                          if (!isfinite(f[z])) o[8 * e + 2 * i + z] += f[z];
+                        }
+                      }
+                  }
                 }
               }
             }

@@ -22,16 +22,18 @@ using kvc::Raw;
 
 constexpr int THREADS = 256, RB_MAX = 4;
 
-// cos and sin of pos * turn (2^-64 turns).
+// cos and sin of pos * turn (2^-64 turns): quadrant and rest, the rest's Taylor series (|y| <= pi / 4: the terms left out are
+// below 2^-29 of the sine and 2^-32 of the cosine).
 __device__ __forceinline__ float2 cos_sin(int pos, uint64_t turn) {
   const uint64_t ph = (uint64_t)(int64_t)pos * turn;
   const uint32_t p = (uint32_t)((ph + 0x80000000ull) >> 32);
   const uint32_t quad = (p + 0x20000000u) >> 30;
-  const int r = (int)(p - (quad << 30));                     // -2^29 .. 2^29 - 1
-  float s, c;
-  sincospif((float)r * 4.656612873077392578125e-10f, &s, &c);   // 2^-31
-  const float x = quad & 1 ? s : c, y = quad & 1 ? c : s;
-  return make_float2(quad == 1 || quad == 2 ? -x : x, quad >= 2 ? -y : y);
+  const float y = (float)(int)(p - (quad << 30)) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+  const float z = y * y;
+  const float s = fmaf(y * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), y);
+  const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
+  const float u = quad & 1 ? s : c, v = quad & 1 ? c : s;
+  return make_float2(quad == 1 || quad == 2 ? -u : u, quad >= 2 ? -v : v);
 }
 
 __device__ __forceinline__ uint32_t pack16(f16, float a, float b) {
@@ -86,8 +88,8 @@ __device__ __forceinline__ float finite_abs(float x) {
 
 // grid (row blocks of rb rows, head blocks of hb heads): heads 0 .. Hq-1 are q's, then k's, then v's.
 template <typename T, int HD, bool VEC, bool APPEND>
-__global__ void __launch_bounds__(THREADS) rows_kernel(const __grid_constant__ RowsArgs a, int rb, int hb, bool out_vec) {
-  constexpr int NU = HD / 16, U = sizeof(T) == 4 ? 2 : 4;
+__global__ void __launch_bounds__(THREADS, 4) rows_kernel(const __grid_constant__ RowsArgs a, int rb, int hb, bool out_vec) {
+  constexpr int NU = HD / 16, U = 2;
   __shared__ float4 cs[RB_MAX * MAX_PAIRS / 2];              // (cos, sin) pairs
   __shared__ int64_t place[RB_MAX];                          // of a row in a plane of pages: vector (head 0); -1: none
   __shared__ int live[RB_MAX];
@@ -96,72 +98,68 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const __grid_constant__ R
   const int np = a.rope.n_pairs, np8 = np / 8;
   const int r0 = blockIdx.x * rb, rows = min(rb, a.n_rows - r0);
   const int H = a.Hq + (APPEND ? 2 * a.pages.Hkv : 0);
-  const int h0 = blockIdx.y * hb, heads = min(hb, H - h0);
-  for (int i = threadIdx.x; i < rows * np; i += THREADS) {
-    const int row = i / np, pair = i - row * np;
-    const int p = !APPEND || a.pos ? a.pos[a.rope.axis[pair] * a.pos_stride + r0 + row] : a.at[r0 + row];
-    reinterpret_cast<float2*>(cs)[row * MAX_PAIRS + pair] = cos_sin(p, a.rope.turn[pair]);
-  }
-  if (threadIdx.x < rows) {
-    const int row = r0 + threadIdx.x;
-    int64_t at = -1;
-    int on = 1;
-    if constexpr (APPEND) {
-      const int j = a.at[row], s = a.seq ? a.seq[row] : row;
-      on = j >= 0;
-      const int col = j >> a.pages.shift;
-      if (on && s >= 0 && s < a.pages.n_seq && col < a.pages.cols) {
-        const int id = a.pages.table[s * a.pages.table_stride + col];
-        if (id >= 0 && id < a.pages.n_pages)
-          at = (((int64_t)id * a.pages.Hkv) << a.pages.shift) + (j & ((1 << a.pages.shift) - 1));
-      }
-    }
-    place[threadIdx.x] = at;
-    live[threadIdx.x] = on;
-  }
-  __syncthreads();
-  const int total = rows * heads * NU;
-  for (int b = 0; b < total; b += THREADS * U) {             // (the whole block: lanes past the end take part in shuffles)
-    Raw<T> x[U][2];
-    int row[U], h[U], c0[U], c1[U];
-    bool turn[U], in[U];
+  const int h0 = blockIdx.y * hb, heads = min(hb, H - h0), total = rows * heads * NU;
+  Raw<T> x[U][2];
+  int row[U], h[U];
+  // unit i: rows' heads in turn, hd / 16 units a head; two chunks c0 and c1 of 8 elements: a pair's two sides, or past the
+  // pairs two that stay
+  auto chunk0 = [&](int unit, int n8) { return unit < n8 ? unit : unit + n8; };
+  auto chunk1 = [&](int unit, int n8) { return unit < n8 ? unit + n8 : unit + NU; };
+  const int unit = threadIdx.x % NU;                         // (THREADS is a multiple of NU)
+  auto pairs8 = [&](int head) { return !APPEND || head < a.Hq + a.pages.Hkv ? np8 : 0; };
+  auto load = [&](int b) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t i = b + u * THREADS + threadIdx.x;
-      in[u] = i < (uint32_t)total;
-      const int unit = i % NU;
-      const uint32_t hr = in[u] ? i / NU : 0;
-      row[u] = hr / (uint32_t)heads;
-      h[u] = h0 + hr - row[u] * heads;
-      in[u] = in[u] && live[row[u]];
-      const T* src = (const T*)a.q + (r0 + row[u]) * a.q_stride + (int64_t)h[u] * HD;
-      bool rotated = true;
-      if constexpr (APPEND) {
+      const int i = b + u * THREADS + (int)threadIdx.x;
+      const int hr = i / NU;
+      int r = 0;
+#pragma unroll
+      for (int k = 1; k < RB_MAX; ++k) r += hr >= k * heads;
+      row[u] = i < total ? r : -1;
+      h[u] = h0 + hr - r * heads;
+      x[u][0] = x[u][1] = Raw<T>{};
+      if (row[u] < 0) continue;
+      const T* src = (const T*)a.q + (r0 + r) * a.q_stride + (int64_t)h[u] * HD;
+      if constexpr (APPEND)
         if (h[u] >= a.Hq) {
           const int hk = h[u] - a.Hq;
-          rotated = hk < a.pages.Hkv;
-          in[u] = in[u] && place[row[u]] >= 0;
-          src = rotated ? (const T*)a.k + (r0 + row[u]) * a.k_stride + (int64_t)hk * HD
-                        : (const T*)a.v + (r0 + row[u]) * a.v_stride + (int64_t)(hk - a.pages.Hkv) * HD;
+          src = hk < a.pages.Hkv ? (const T*)a.k + (r0 + r) * a.k_stride + (int64_t)hk * HD
+                                 : (const T*)a.v + (r0 + r) * a.v_stride + (int64_t)(hk - a.pages.Hkv) * HD;
         }
-      }
-      const int n8 = rotated ? np8 : 0;
-      turn[u] = unit < n8;                                   // chunks c and c + n8; past the pairs, side by side halves
-      c0[u] = turn[u] ? unit : unit + n8;
-      c1[u] = turn[u] ? unit + n8 : unit + NU;
-      x[u][0] = x[u][1] = Raw<T>{};
-      if (in[u]) {
-        x[u][0] = kvc::load8<T, VEC>(src + c0[u] * 8);
-        x[u][1] = kvc::load8<T, VEC>(src + c1[u] * 8);
-      }
+      const int n8 = pairs8(h[u]);
+      x[u][0] = kvc::load8<T, VEC>(src + chunk0(unit, n8) * 8);
+      x[u][1] = kvc::load8<T, VEC>(src + chunk1(unit, n8) * 8);
     }
+  };
+  load(0);                                                   // (in flight while the angles are made)
+  for (int i = threadIdx.x; i < rows * np; i += THREADS) {
+    const int rr = i / np, pair = i - rr * np;
+    const int p = !APPEND || a.pos ? a.pos[a.rope.axis[pair] * a.pos_stride + r0 + rr] : a.at[r0 + rr];
+    reinterpret_cast<float2*>(cs)[rr * MAX_PAIRS + pair] = cos_sin(p, a.rope.turn[pair]);
+  }
+  if (APPEND && threadIdx.x < rows) {
+    const int rr = r0 + threadIdx.x;
+    int64_t at = -1;
+    const int j = a.at[rr], s = a.seq ? a.seq[rr] : rr, col = j >> a.pages.shift;
+    if (j >= 0 && s >= 0 && s < a.pages.n_seq && col < a.pages.cols) {
+      const int id = a.pages.table[s * a.pages.table_stride + col];
+      if (id >= 0 && id < a.pages.n_pages)
+        at = (((int64_t)id * a.pages.Hkv) << a.pages.shift) + (j & ((1 << a.pages.shift) - 1));
+    }
+    place[threadIdx.x] = at;
+    live[threadIdx.x] = j >= 0;
+  }
+  __syncthreads();
+  for (int b = 0; b < total; b += THREADS * U) {             // (the whole block: lanes past the end take part in shuffles)
+    if (b) load(b);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float lo[8], hi[8];
       widen(x[u][0], lo);
       widen(x[u][1], hi);
-      if (turn[u]) {
-        const float4* t = cs + (row[u] * MAX_PAIRS + c0[u] * 8) / 2;
+      const int n8 = pairs8(h[u]), c0 = chunk0(unit, n8), c1 = chunk1(unit, n8), r = max(row[u], 0);
+      if (unit < n8) {
+        const float4* t = cs + (r * MAX_PAIRS + c0 * 8) / 2;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float4 w = t[e];
@@ -172,18 +170,25 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const __grid_constant__ R
           hi[2 * e + 1] = b1 * w.z + a1 * w.w;
         }
       }
+      bool in = row[u] >= 0;
       if constexpr (APPEND) {
         float m = 0.f;
-        if (a.pages.format == KVF_E4M3) {                    // the head's largest finite magnitude
+        if (a.pages.format == KVF_E4M3 && __any_sync(0xffffffffu, in && h[u] >= a.Hq)) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(finite_abs(lo[e]), finite_abs(hi[e])));
+          for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(lo[e]), fabsf(hi[e])));   // (NaN: left out)
+          if (isinf(m)) {                                    // the head's largest finite magnitude
+            m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(finite_abs(lo[e]), finite_abs(hi[e])));
+          }
 #pragma unroll
           for (int o = NU / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         }
-        if (!in[u]) continue;
-        if (h[u] >= a.Hq) {
+        in = in && live[r];
+        if (in && h[u] >= a.Hq) {
+          if (place[r] < 0) continue;
           const int hk = h[u] - a.Hq, plane = hk >= a.pages.Hkv, kvh = hk - plane * a.pages.Hkv;
-          const int64_t vec = (((int64_t)plane * a.pages.n_pages * a.pages.Hkv + kvh) << a.pages.shift) + place[row[u]];
+          const int64_t vec = (((int64_t)plane * a.pages.n_pages * a.pages.Hkv + kvh) << a.pages.shift) + place[r];
           if (a.pages.format == KVF_E4M3) {
             const int E = kvc::scale_exp(m);
             const float inv = kvc::pow2(-E);
@@ -195,21 +200,21 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const __grid_constant__ R
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 c[e] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * e] * inv, y[2 * e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-              *reinterpret_cast<uint2*>(codes + (half ? c1[u] : c0[u]) * 8) = kvc::pack_codes(c);
+              *reinterpret_cast<uint2*>(codes + (half ? c1 : c0) * 8) = kvc::pack_codes(c);
             }
-            if (threadIdx.x % NU == 0) a.pages.scales[vec] = kvc::pow2(E);
+            if (unit == 0) a.pages.scales[vec] = kvc::pow2(E);
           } else {
             const int type = a.pages.format == KVF_F16 ? ELEM_F16 : ELEM_BF16;
-            store8(a.pages.data, vec * HD + c0[u] * 8, type, lo, true);
-            store8(a.pages.data, vec * HD + c1[u] * 8, type, hi, true);
+            store8(a.pages.data, vec * HD + c0 * 8, type, lo, true);
+            store8(a.pages.data, vec * HD + c1 * 8, type, hi, true);
           }
           continue;
         }
       }
-      if (!in[u]) continue;
-      const int64_t o = (r0 + row[u]) * a.q_out_stride + (int64_t)h[u] * HD;
-      store8(a.q_out, o + c0[u] * 8, a.q_out_type, lo, out_vec);
-      store8(a.q_out, o + c1[u] * 8, a.q_out_type, hi, out_vec);
+      if (!in) continue;
+      const int64_t o = (r0 + r) * a.q_out_stride + (int64_t)h[u] * HD;
+      store8(a.q_out, o + c0 * 8, a.q_out_type, lo, out_vec);
+      store8(a.q_out, o + c1 * 8, a.q_out_type, hi, out_vec);
     }
   }
 }
@@ -218,9 +223,9 @@ template <typename T, int HD, bool VEC, bool APPEND>
 cudaError_t launch_t(const RowsArgs& a, bool out_vec, cudaStream_t st) {
   const int H = a.Hq + (APPEND ? 2 * a.pages.Hkv : 0);
   constexpr int NU = HD / 16;
-  // few rows: one row and 256 threads' worth of heads a block, so that they spread over the SMs
-  const bool small = (int64_t)a.n_rows * H * NU < 2ll * 152 * 2048;
-  const int rb = small ? 1 : RB_MAX, hb = small ? std::min(H, THREADS / NU) : H;
+  // few rows: fewer of them a block, and a block's heads those of one batch of loads, so that they spread over the SMs
+  const int rb = a.n_rows >= 152 * RB_MAX ? RB_MAX : a.n_rows >= 152 * 2 ? 2 : 1;
+  const int hb = rb == RB_MAX ? H : std::min(H, THREADS / NU);
   const dim3 grid((a.n_rows + rb - 1) / rb, (H + hb - 1) / hb);
   return launch_pdl(rows_kernel<T, HD, VEC, APPEND>, grid, dim3(THREADS), 0, st, a, rb, hb, out_vec);
 }
