@@ -8,18 +8,20 @@
 // which are written at once, and at most two in part, whose (o, m, l) join_kernel joins in the order of the CTAs: the
 // sizes and positions fix every order of summation.
 //
-// A CTA: warp 8 asks for the tiles by TMA (a lane per page box; page ids read 32 columns ahead) into a ring that holds
-// some 190 KB; 8 warps compute, four on the even and four on the odd tiles, 16 rows each, without any exchange until the pair
-// ends. With at most 16 query rows tcgen05's 128-row tiles would stand nearly empty and pass S and P through TMEM between
-// warps, so the products are mma.sync's m16n8k16, whose operands and results stay in one warp's registers: Q as the A operand, scores
-// in the layout in which P is the next A operand. Each warp keeps a running base and sum of its own rows.
+// A CTA: four warps ask for the tiles by TMA (a lane per page box; page ids read 32 columns ahead) into a ring of 130 to 190 KB;
+// the others compute, four a tile, 16 rows each, without any exchange until the pair ends. With at most 16 query rows
+// tcgen05's 128-row tiles would stand nearly empty and pass S and P through TMEM between warps, so the products are mma.sync's
+// m16n8k16, whose operands and results stay in one warp's registers, transposed: S^T = K Q^T and O^T = V^T P^T, cached rows
+// and value columns on the 16 side and 8 q heads on the 8 side (NH = 1, or 2 for more than 8 heads: twice the products on
+// the same K and V operands). One movmatrix turns 8 x 8 weights of S^T's layout into P^T's. Each warp keeps a running base
+// and sum of its own rows.
 //
 // e4m3 pages: the codes travel and are widened to f16 in registers. The sums over d and over rows do not care for
-// their order, so both products take the codes in the order in which wide shared-memory reads find them: key column
-// n of a product stands for row key8(n), and thread (g, t) holds chunk t of a K row (16 d's as four k-steps) and chunk g
-// of V rows (16 columns of the product's tiles). K scales multiply the scores. V scales go into the weights as exponents: the
+// their order, so both products take the codes in the order in which wide shared-memory reads find them: row
+// n of an 8-row block of S^T stands for cached row key8(n), and thread (g, t) holds chunk t of a K row (16 d's as four
+// k-steps) and chunk g of V rows (16 columns). K scales multiply the scores. V scales go into the weights as exponents: the
 // base is a running bound of z + e (V's scale 2^e f, f in [1/2, 1)), so neither f16 nor the sums see the scales' range.
-// bf16 queries over e4m3 pages become f16 by a power of two per row.
+// bf16 queries over e4m3 pages become f16 by a power of two per q head.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -33,22 +35,27 @@ namespace pgs {
 using namespace t5;
 using namespace pga;
 
-constexpr int KT = 64, WARPS = 8, THREADS = (WARPS + 1) * 32;
+constexpr int KT = 64, PRODUCERS = 4;
 enum Kind { F16 = 0, BF16 = 1, E4M3 = 2 };
 
 __device__ uint64_t g_given_up;              // when a bounded wait last gave up, per device; never cleared
 
-template <int HD, int KIND>
+// Computing warps: 8, or 12 with e4m3 pages of up to 8 q heads, where widening the codes takes most of the time (16 would leave
+// 96 registers a thread, too few).
+template <int HD, int KIND, int NH>
 struct Lay {
+  static constexpr int WARPS = KIND == E4M3 && NH == 1 ? 12 : 8, GROUPS = WARPS / 4;
+  static constexpr int THREADS = (WARPS + PRODUCERS) * 32;
   static constexpr int PLANE = KT * HD * (KIND == E4M3 ? 1 : 2), TILE = 2 * PLANE;
-  static constexpr int NST = KIND == E4M3 ? (HD == 128 ? 10 : 16) : (HD == 128 ? 6 : 12);   // even
+  static constexpr int NST = KIND == E4M3 ? (NH == 1 ? (HD == 128 ? 9 : 15) : (HD == 128 ? 8 : 16)) : (HD == 128 ? 6 : 12);
   static constexpr int SC = NST * TILE;                       // scales of a stage: [2][KT] floats (e4m3)
-  static constexpr int OSTR = HD + 4;                         // floats of a row in a warp's published sums
+  static constexpr int OSTR = HD + 4;                         // floats of a q head in a warp's published sums
   static constexpr int OUT = SC + (KIND == E4M3 ? NST * 2 * KT * 4 : 0);
   static constexpr int ML = OUT + WARPS * 8 * OSTR * 4;       // [WARPS][8] (m, l)
   static constexpr int BAR = ML + WARPS * 8 * 8;
   static constexpr int BYTES = BAR + 2 * NST * 8 + 64;
-  static_assert(BYTES + 1024 <= 227 * 1024 && NST % 2 == 0, "shared memory of one CTA");
+  static_assert(BYTES + 1024 <= 227 * 1024, "shared memory of one CTA");
+  static_assert(NST % GROUPS == 0, "a stage is always the same warps' to read");
 };
 
 struct StepArgs {
@@ -64,15 +71,21 @@ struct Record {
 };
 __host__ __device__ constexpr int64_t slot_floats(int hd) { return 16 * (hd + 2); }
 
-// Where score column n (0 .. 7) of a product's key tile lies among its 8 rows.
+// Where row n (0 .. 7) of an 8-row block of S^T lies among its cached rows.
 template <int KIND>
 __device__ __forceinline__ int key8(int n) {
   return KIND == E4M3 ? (n & 1 ? (n ^ 4) : n) : n;
 }
-// The column of O that element e (0, 1) of thread t's accumulator of tile b stands for.
+// The value column that row g (half 0) or g + 8 (half 1) of block b of O^T stands for.
 template <int HD, int KIND>
-__device__ __forceinline__ int out_col(int b, int t, int e) {
-  return KIND == E4M3 ? (HD / 8) * (2 * t + e) + b : 8 * b + 2 * t + e;
+__device__ __forceinline__ int out_col(int b, int g, int half) {
+  return KIND == E4M3 ? (HD / 8) * g + 2 * b + half : 16 * b + g + 8 * half;
+}
+// An 8 x 8 matrix of 16-bit elements, transposed over the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 template <bool BF>
@@ -97,9 +110,11 @@ __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
 }
-__device__ __forceinline__ uint32_t widen2(uint32_t codes) {   // two e4m3 codes (low 16 bits) to an f16 pair
-  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
-  return (uint32_t)r.y << 16 | r.x;
+// Four e4m3 codes to two f16 pairs.
+__device__ __forceinline__ void widen4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
 template <bool BF>
 __device__ __forceinline__ uint32_t pack_w(float a, float b) {
@@ -110,7 +125,8 @@ __device__ __forceinline__ uint32_t pack_w(float a, float b) {
     return h2u(a, b);
   }
 }
-__device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }   // the 8 computing warps
+template <int N>
+__device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }   // the computing warps
 
 // A run's position in the list of tiles.
 struct Cursor {
@@ -119,18 +135,18 @@ struct Cursor {
   Tiles tl;
 };
 
-template <int HD, int KIND, bool QBF>
-__global__ void __launch_bounds__(THREADS, 1)
+template <int HD, int KIND, bool QBF, int NH>
+__global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
     step_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ StepArgs sa) {
-  using L = Lay<HD, KIND>;
-  constexpr int NST = L::NST;
+  using L = Lay<HD, KIND, NH>;
+  constexpr int NST = L::NST, WARPS = L::WARPS, THREADS = L::THREADS, GROUPS = L::GROUPS;
   constexpr bool PBF = KIND == BF16;           // the products' type
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* full = (uint64_t*)(sm + L::BAR);   // [NST]
   uint64_t* empty = full + NST;                // [NST]
   volatile int* abort_flag = (volatile int*)(empty + NST);
   int* found = (int*)(empty + NST) + 1;        // the run's first sequence
-  __shared__ int64_t red[WARPS + 1];
+  __shared__ int64_t red[WARPS + PRODUCERS];
   __shared__ int64_t found_before;             // tiles (per pair) of the sequences before it
   const PagedAttnArgs& a = sa.a;
   const PagesArgs& pg = a.pages;
@@ -138,7 +154,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], PRODUCERS + (KIND == E4M3 ? 32 : 0));
       mbar_init(&empty[i], 4);
     }
     *abort_flag = 0;
@@ -167,7 +183,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     int64_t before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w <= WARPS; ++w) {
+    for (int w = 0; w < WARPS + PRODUCERS; ++w) {
       if (w < warp) before += red[w];
       all += red[w];
     }
@@ -215,73 +231,90 @@ __global__ void __launch_bounds__(THREADS, 1)
     c0.hg = (int)(r / c0.T);
     c0.t = (int)(r % c0.T);
   }
-  // runs fn(cursor, tiles of the pair in this run) over the pairs of the run
+  // runs fn(cursor, tiles of the pair in this run, the next pair's cursor, whether there is one) over the pairs of the run;
+  // positions are read a sequence ahead
   auto each_pair = [&](auto&& fn) {
+    auto pos_of = [&](int s) { return s < sa.n ? sa.pos[s] : -1; };
+    auto look_at = [&](Cursor& c, int s, int p) {
+      c.s = s;
+      c.v = seen_rows(p, rows, a.window, a.sinks);
+      c.tl = tiles_of<KT>(c.v);
+      c.T = c.tl.count();
+    };
+    if (u0 >= u1) return;
     Cursor c = c0;
-    for (int64_t u = u0; u < u1;) {
+    int ahead = pos_of(c.s + 1);
+    for (int64_t u = u0;;) {
       const int m = (int)min((int64_t)(c.T - c.t), u1 - u);
-      if (!fn(c, m)) return;
       u += m;
-      c.t = 0;
-      if (u < u1 && ++c.hg == sa.HG) {
-        c.hg = 0;
-        do look(c, c.s + 1);
-        while (c.T == 0);
+      Cursor nx = c;
+      nx.t = 0;
+      if (u < u1 && ++nx.hg == sa.HG) {
+        nx.hg = 0;
+        look_at(nx, c.s + 1, ahead);
+        while (nx.T == 0) look_at(nx, nx.s + 1, pos_of(nx.s + 1));
+        ahead = pos_of(nx.s + 1);
       }
+      if (!fn(c, m, nx, u < u1) || u >= u1) return;
+      c = nx;
     }
   };
 
-  int asked = 0;                               // tiles asked for (producer)
-  if (warp == WARPS) {
-    // ---- TMA producer
-    constexpr int NB = KIND == E4M3 ? 1 : HD / 64;
+  int asked = 0;                               // tiles asked for (producers)
+  if (warp >= WARPS) {
+    // ---- TMA producers: plane pw % 2, every second page box (a box is a loop's pass over its uniform operands, so one
+    // warp's boxes of 16-row pages take longer than their bytes: 200001 e4m3 rows in pages of 16, 128 with one warp 62, 45 us)
+    constexpr int NB = KIND == E4M3 ? 1 : HD / 64, ROW = KIND == E4M3 ? HD : 128;   // boxes of a page, bytes of a box row
+    const int pw = warp - WARPS, plane = pw & 1, half = pw >> 1;
     const int npg = pg.shift < 6 ? KT >> pg.shift : 1, br = KT / npg;     // pages of a tile, rows of a box
-    const int plane = lane & 1, box = (lane >> 1) % NB, part = (lane >> 1) / NB;
+    const int bi = 2 * lane + half, box = bi % NB, part = bi / NB;        // this lane's box
     int& i = asked;
-    each_pair([&](const Cursor& c, int m) {
-      const int64_t trow = (int64_t)c.s * pg.table_stride;
+    int cs = -1, blk = -1, cur = 0, ns_ = -1, nblk = -1, next = 0;        // page ids of 32 columns: of a block, and of the next
+    each_pair([&](const Cursor& c, int m, const Cursor& nx, bool more) {
       const int head = c.hg / sa.groups, last = (c.v.end - 1) >> pg.shift;
-      int blk = -1, cur = 0, next = 0;         // page ids of columns 32 blk .. +31, and of the block behind them
-      auto ids = [&](int b) {
+      auto ids = [&](const Cursor& w, int b) {
         const int col = b * 32 + lane;
-        return col <= last ? pg.table[trow + col] : -1;
+        return col <= (w.v.end - 1) >> pg.shift ? pg.table[(int64_t)w.s * pg.table_stride + col] : -1;
       };
+      auto block_of = [&](const Cursor& w, int t) { return (w.tl.at(t) * KT >> pg.shift) >> 5; };
       for (int t = c.t; t < c.t + m; ++t, ++i) {
         const int j0 = c.tl.at(t) * KT, col = j0 >> pg.shift;
-        if (col >> 5 != blk) {
-          cur = blk >= 0 && col >> 5 == blk + 1 ? next : ids(col >> 5);
+        if (col >> 5 != blk || c.s != cs) {
+          cur = ns_ == c.s && nblk == col >> 5 ? next : ids(c, col >> 5);
+          cs = c.s;
           blk = col >> 5;
-          next = ids(blk + 1);
+          // the block that comes behind it: of this pair, or the next pair's first
+          if (block_of(c, c.t + m - 1) != blk) {
+            ns_ = c.s;
+            nblk = t < c.tl.head && block_of(c, c.tl.head - 1) == blk ? block_of(c, c.tl.head) : blk + 1;
+            next = ids(c, nblk);
+          } else if (more) {
+            ns_ = nx.s;
+            nblk = block_of(nx, 0);
+            next = ids(nx, nblk);
+          }
         }
         const int id = __shfl_sync(0xffffffffu, cur, (col + part) & 31);
         const int st = i % NST;
         if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], (i / NST & 1) ^ 1, abort_flag, &g_given_up) ? 1 : 0)) return false;
-        uint8_t* dst = sm + st * L::TILE;
         const int there = min(npg, last - col + 1);            // pages that the sequence has
-        const bool valid = id >= 0 && id < pg.n_pages;
-        uint32_t bytes = (uint32_t)(there * br) * (HD * (KIND == E4M3 ? 1 : 2) * 2);
+        if (lane == 0) mbar_expect_tx(&full[st], (uint32_t)((there * NB - half + 1) / 2 * br * ROW));
+        __syncwarp();
         if constexpr (KIND == E4M3) {
-          // scales: 64 to 256 contiguous bytes of a page; of a page that does not exist, ones
-          float* sc = (float*)(sm + L::SC) + st * 2 * KT + plane * KT + part * br;
-          const bool mine = lane < npg * 2 && part < there;
-          const uint32_t n_valid = __popc(__ballot_sync(0xffffffffu, mine && valid));
-          bytes += n_valid * (uint32_t)br * 4;
-          if (mine && !valid) {
-            for (int r = 0; r < br; ++r) sc[r] = 1.f;
-            fence_async_smem();
+          // the plane's scales, 4 rows a lane (rows without a page: zeros)
+          const int sr = 4 * lane, spart = sr / br;
+          const int sid = __shfl_sync(0xffffffffu, cur, (col + spart) & 31);
+          if (half == 0 && lane < KT / 4) {
+            const bool on = spart < there && sid >= 0 && sid < pg.n_pages;
+            copy16_async(sm + L::SC + (st * 2 * KT + plane * KT + sr) * 4,
+                         pg.scales + ((((int64_t)plane * pg.n_pages + (on ? sid : 0)) * pg.Hkv + head) << pg.shift) +
+                             ((j0 + sr) & ((1 << pg.shift) - 1)),
+                         on);
+            arrive_after_copies(&full[st]);
           }
-          __syncwarp();
-          if (lane == 0) mbar_expect_tx(&full[st], bytes);
-          __syncwarp();
-          if (mine && valid)
-            bulk_load(sc, pg.scales + ((((int64_t)plane * pg.n_pages + id) * pg.Hkv + head) << pg.shift) +
-                              (j0 & ((1 << pg.shift) - 1)), br * 4, &full[st]);
-        } else {
-          if (lane == 0) mbar_expect_tx(&full[st], bytes);
-          __syncwarp();
         }
-        if (lane < npg * NB * 2 && part < there)
-          tma5(dst + plane * L::PLANE + box * (KT * 128) + part * br * (KIND == E4M3 ? HD : 128), &map, &full[st], box * 64,
+        if (part < there)
+          tma5(sm + st * L::TILE + plane * L::PLANE + box * (KT * 128) + part * br * ROW, &map, &full[st], box * 64,
                j0 & ((1 << pg.shift) - 1), head, id, plane);
       }
       return true;
@@ -304,49 +337,63 @@ __global__ void __launch_bounds__(THREADS, 1)
       Record* rec = reinterpret_cast<Record*>((float*)a.ws + 2 * (int64_t)gridDim.x * slot_floats(HD)) + blockIdx.x;
       rec->valid = 0;
     }
-    each_pair([&](const Cursor& c, int m) {
-      const int kvh = c.hg / sa.groups, h0 = kvh * sa.G + (c.hg % sa.groups) * 16;
-      const int nq = min(16, (kvh + 1) * sa.G - h0);           // q heads of the pair
-      // Q as A fragments: rows g and g + 8; d of k-step ks as the K operand has it
-      uint32_t q[HD / 16][4];
-      float qs0 = sl2, qs1 = sl2;                              // what a score of row g, g + 8 is multiplied by
-      {
-        const uint16_t* qp = (const uint16_t*)a.q + (int64_t)c.s * a.q_stride + (int64_t)h0 * HD;
-        auto row = [&](int r, int ks, int half) -> uint32_t {
-          const int d = KIND == E4M3 ? 64 * (ks >> 2) + 16 * t4 + 4 * (ks & 3) + 2 * half : 16 * ks + 2 * t4 + 8 * half;
-          return r < nq ? __ldg(reinterpret_cast<const uint32_t*>(qp + r * HD + d)) : 0u;
-        };
+    uint32_t qn[NH][HD / 16][2];               // the next pair's q
+    auto load_q = [&](const Cursor& c) {
+      const int kvh = c.hg / sa.groups, h0 = kvh * sa.G + (c.hg % sa.groups) * 8 * NH;
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh) {
+        const int r = 8 * nh + g;
+        const uint16_t* qp = (const uint16_t*)a.q + (int64_t)c.s * a.q_stride + (int64_t)(h0 + r) * HD;
+        const bool there = r < min(8 * NH, (kvh + 1) * sa.G - h0);
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) q[ks][e] = row(g + 8 * (e & 1), ks, e >> 1);
-        if constexpr (KIND == E4M3 && QBF) {                   // to f16, the row's largest element near 2^14
-          uint32_t top[2] = {0, 0};
-#pragma unroll
-          for (int ks = 0; ks < HD / 16; ++ks)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              top[e & 1] = max(top[e & 1], max(q[ks][e] & 0x7fffu, q[ks][e] >> 16 & 0x7fffu));
-          float up[2];
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            top[r] = max(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-            top[r] = max(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-            const int E = min(max((int)(top[r] >> 7) - 127, -100), 127);
-            up[r] = __uint_as_float((uint32_t)(14 - E + 127) << 23);
-            (r ? qs1 : qs0) *= __uint_as_float((uint32_t)(E - 14 + 127) << 23);
+          for (int e = 0; e < 2; ++e) {
+            const int d = KIND == E4M3 ? 64 * (ks >> 2) + 16 * t4 + 4 * (ks & 3) + 2 * e : 16 * ks + 2 * t4 + 8 * e;
+            qn[nh][ks][e] = there ? __ldg(reinterpret_cast<const uint32_t*>(qp + d)) : 0u;
           }
+      }
+    };
+    constexpr bool AHEAD = NH == 1 || HD == 64;   // (the registers of 16 q heads of 128 leave no room)
+    if (AHEAD && u0 < u1) load_q(c0);
+    each_pair([&](const Cursor& c, int m, const Cursor& nx, bool more) {
+      const int kvh = c.hg / sa.groups, h0 = kvh * sa.G + (c.hg % sa.groups) * 8 * NH;
+      const int nq = min(8 * NH, (kvh + 1) * sa.G - h0);       // q heads of the pair
+      // Q^T as B fragments: q head 8 nh + g; d of k-step ks as the K operand has it
+      uint32_t q[NH][HD / 16][2];
+      float qs[NH][2];                                         // what a score of q head 8 nh + 2 t + e is multiplied by
+      if constexpr (!AHEAD) load_q(c);
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh) {
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks) q[nh][ks][0] = qn[nh][ks][0], q[nh][ks][1] = qn[nh][ks][1];
+        qs[nh][0] = qs[nh][1] = sl2;
+        if constexpr (KIND == E4M3 && QBF) {                   // to f16, the head's largest element near 2^14
+          uint32_t top = 0;
 #pragma unroll
           for (int ks = 0; ks < HD / 16; ++ks)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              q[ks][e] = h2u(__uint_as_float(q[ks][e] << 16) * up[e & 1],
-                             __uint_as_float(q[ks][e] & 0xffff0000u) * up[e & 1]);
+            for (int e = 0; e < 2; ++e) top = max(top, max(q[nh][ks][e] & 0x7fffu, q[nh][ks][e] >> 16 & 0x7fffu));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int E = min(max((int)(top >> 7) - 127, -100), 127);
+          const float up = __uint_as_float((uint32_t)(14 - E + 127) << 23);
+          const float down = sl2 * __uint_as_float((uint32_t)(E - 14 + 127) << 23);
+          qs[nh][0] = __shfl_sync(0xffffffffu, down, 8 * t4);  // (of heads 2 t and 2 t + 1)
+          qs[nh][1] = __shfl_sync(0xffffffffu, down, 8 * t4 + 4);
+#pragma unroll
+          for (int ks = 0; ks < HD / 16; ++ks)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              q[nh][ks][e] = h2u(__uint_as_float(q[nh][ks][e] << 16) * up, __uint_as_float(q[nh][ks][e] & 0xffff0000u) * up);
         }
       }
-      float o[HD / 8][4] = {};
-      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-      for (int x = (i + grp) & 1; x < m && ok; x += 2) {
+      if (AHEAD && more) load_q(nx);                           // (used when this pair has ended)
+      float o[NH][HD / 16][4] = {};
+      float mx[NH][2], sum[NH][2] = {};                        // base and sum of q heads 8 nh + 2 t + e
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh) mx[nh][0] = mx[nh][1] = -INFINITY;
+      for (int x = (grp - i % GROUPS + GROUPS) % GROUPS; x < m && ok; x += GROUPS) {
         const int tile = i + x, st = tile % NST;
         const int j0 = c.tl.at(c.t + x) * KT + sub * 16;       // this warp's first row
         if (!__all_sync(0xffffffffu, mbar_wait(&full[st], tile / NST & 1, abort_flag, &g_given_up) ? 1 : 0)) {
@@ -357,125 +404,126 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool none = j0 >= c.v.end || (j0 + 15 < c.v.lo && j0 >= c.v.sk);
         if (!none) {
           const uint32_t kb = base_k + st * L::TILE, vb = kb + L::PLANE;
-          float s[2][4] = {};
-          // ---- S = Q K^T
-          if constexpr (KIND != E4M3) {
-            const int r = sub * 16 + (lane & 7) + (lane & 16 ? 8 : 0), ch = lane >> 3 & 1;
-#pragma unroll
-            for (int ks = 0; ks < HD / 16; ++ks) {
-              uint32_t b[4];
-              ldsm4<false>(b, kb + (ks >> 2) * (KT * 128) + r * 128 + ((((ks & 3) * 2 + ch) ^ (r & 7)) << 4));
-              mma16816<PBF>(s[0], q[ks], b[0], b[1]);
-              mma16816<PBF>(s[1], q[ks], b[2], b[3]);
-            }
-          } else {
-#pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
-              const int r = sub * 16 + nb * 8 + key8<KIND>(g);
-#pragma unroll
-              for (int j = 0; j < HD / 64; ++j) {
-                const int ch = HD == 128 ? (4 * j + t4) ^ (r & 7) : t4 ^ (r >> 1 & 3);
-                uint32_t w[4];
-                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                             : "r"(kb + r * HD + (ch << 4)));
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mma16816<false>(s[nb], q[4 * j + k], widen2(w[k]), widen2(w[k] >> 16));
-              }
-            }
-          }
-          // ---- scores in the log2 domain, hidden rows -inf; t: what the base is taken from
-          float f[2][2];                                       // e4m3: V scales' fractions by (nb, e)
-          float ex[2][2];                                      // and exponents
-          uint32_t hid = 0;                                    // bit 2 nb + e: the row is hidden
-          if (!whole) {
-#pragma unroll
-            for (int x4 = 0; x4 < 4; ++x4) {
-              const int j = j0 + (x4 >> 1) * 8 + key8<KIND>(2 * t4 + (x4 & 1));
-              if (j >= c.v.end || (j < c.v.lo && j >= c.v.sk)) hid |= 1u << x4;
-            }
-          }
-#pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float f0 = qs0, f1 = qs1;
-              const bool h = hid >> (2 * nb + e) & 1;
-              if constexpr (KIND == E4M3) {
-                const float* sc = (const float*)(sm + L::SC) + st * 2 * KT + sub * 16 + nb * 8 + key8<KIND>(2 * t4 + e);
-                f0 *= sc[0];
-                f1 *= sc[0];
-                const uint32_t u = __float_as_uint(sc[KT]);
-                const int E = (int)(u >> 23) - 126;             // (scales below 2^-81: the rest stays in f)
-                ex[nb][e] = (float)max(E, -80);
-                f[nb][e] = E >= -80 ? __uint_as_float((u & 0x7fffffu) | 126u << 23) : sc[KT] * 1.208925819614629e24f;
-              }
-              s[nb][e] = h ? -INFINITY : s[nb][e] * f0;
-              s[nb][2 + e] = h ? -INFINITY : s[nb][2 + e] * f1;
-            }
-          auto key = [&](int nb, int e) {                      // score, or score and exponent
-            if constexpr (KIND == E4M3) return s[nb][e] + ex[nb][e & 1];
-            else return s[nb][e];
-          };
-          float x0 = fmaxf(fmaxf(key(0, 0), key(0, 1)), fmaxf(key(1, 0), key(1, 1)));
-          float x1 = fmaxf(fmaxf(key(0, 2), key(0, 3)), fmaxf(key(1, 2), key(1, 3)));
-          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-          const bool up0 = x0 - m0 > TOP, up1 = x1 - m1 > TOP;
-          if (__any_sync(0xffffffffu, up0 || up1)) {
-            const float n0 = up0 ? (fabsf(x0) < FAR ? x0 - HEAD : x0) : m0, n1 = up1 ? (fabsf(x1) < FAR ? x1 - HEAD : x1) : m1;
-            const float a0 = m0 == n0 || m0 == -INFINITY ? 1.f : ex2(m0 - n0);
-            const float a1 = m1 == n1 || m1 == -INFINITY ? 1.f : ex2(m1 - n1);
-            m0 = n0;
-            m1 = n1;
-            l0 *= a0;
-            l1 *= a1;
-#pragma unroll
-            for (int b = 0; b < HD / 8; ++b) {
-              o[b][0] *= a0;
-              o[b][1] *= a0;
-              o[b][2] *= a1;
-              o[b][3] *= a1;
-            }
-          }
-          const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
-          uint32_t p[4];
-#pragma unroll
-          for (int nb = 0; nb < 2; ++nb) {
-            float w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float b = e < 2 ? b0 : b1;
-              const float d = ex2(s[nb][e] - b);               // (e4m3: the sum's weight)
-              w[e] = d;
-              if constexpr (KIND == E4M3) w[e] = hid >> (2 * nb + (e & 1)) & 1 ? 0.f : ex2(s[nb][e] + ex[nb][e & 1] - b) * f[nb][e & 1];
-              (e < 2 ? l0 : l1) += d;
-            }
-            p[2 * nb] = pack_w<PBF>(w[0], w[1]);
-            p[2 * nb + 1] = pack_w<PBF>(w[2], w[3]);
-          }
-          // ---- O += P V; the V rows of hidden keys are zeros (0 x NaN is not)
-          uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;   // of the pairs (2t, 2t + 1), (2t + 8, 2t + 9)
-          if (!whole) {
-            keep0 = (hid & 1 ? 0u : 0xffffu) | (hid & 2 ? 0u : 0xffff0000u);
-            keep1 = (hid & 4 ? 0u : 0xffffu) | (hid & 8 ? 0u : 0xffff0000u);
-          }
+          float s[NH][4] = {};                                 // rows key8(g) (0, 1) and 8 + key8(g) (2, 3), heads 2 t + e
+          // ---- S^T = K Q^T
           if constexpr (KIND != E4M3) {
             const int r = sub * 16 + (lane & 15), ch = lane >> 4;
 #pragma unroll
-            for (int b = 0; b < HD / 8; b += 2) {
-              uint32_t v[4];
-              ldsm4<true>(v, vb + (b >> 3) * (KT * 128) + r * 128 + ((((b & 7) + ch) ^ (r & 7)) << 4));
-              if (!whole) {
-                v[0] &= keep0;
-                v[1] &= keep1;
-                v[2] &= keep0;
-                v[3] &= keep1;
+            for (int ks = 0; ks < HD / 16; ++ks) {
+              uint32_t k[4];
+              ldsm4<false>(k, kb + (ks >> 2) * (KT * 128) + r * 128 + ((((ks & 3) * 2 + ch) ^ (r & 7)) << 4));
+#pragma unroll
+              for (int nh = 0; nh < NH; ++nh) mma16816<PBF>(s[nh], k, q[nh][ks][0], q[nh][ks][1]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < HD / 64; ++j) {
+              uint32_t w[2][4];
+#pragma unroll
+              for (int nb = 0; nb < 2; ++nb) {
+                const int r = sub * 16 + nb * 8 + key8<KIND>(g);
+                const int ch = HD == 128 ? (4 * j + t4) ^ (r & 7) : t4 ^ (r >> 1 & 3);
+                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(w[nb][0]), "=r"(w[nb][1]), "=r"(w[nb][2]), "=r"(w[nb][3])
+                             : "r"(kb + r * HD + (ch << 4)));
               }
-              mma16816<PBF>(o[b], p, v[0], v[1]);
-              mma16816<PBF>(o[b + 1], p, v[2], v[3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t ka[4];
+                widen4(w[0][k], ka[0], ka[2]);
+                widen4(w[1][k], ka[1], ka[3]);
+#pragma unroll
+                for (int nh = 0; nh < NH; ++nh) mma16816<false>(s[nh], ka, q[nh][4 * j + k][0], q[nh][4 * j + k][1]);
+              }
+            }
+          }
+          // ---- scores in the log2 domain, hidden rows -inf
+          bool hid[2] = {false, false};                        // rows key8(g), 8 + key8(g)
+          float ks[2] = {1.f, 1.f}, f[2], ex[2];               // e4m3: K's scale, V's fraction and exponent
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int r = b * 8 + key8<KIND>(g), j = j0 + r;
+            if (!whole) hid[b] = j >= c.v.end || (j < c.v.lo && j >= c.v.sk);
+            if constexpr (KIND == E4M3) {
+              const float* sc = (const float*)(sm + L::SC) + st * 2 * KT + sub * 16 + r;
+              ks[b] = sc[0];
+              const uint32_t u = __float_as_uint(sc[KT]);
+              const int E = (int)(u >> 23) - 126;              // (scales below 2^-81: the rest stays in f)
+              ex[b] = (float)max(E, -80);
+              f[b] = E >= -80 ? __uint_as_float((u & 0x7fffffu) | 126u << 23) : sc[KT] * 1.208925819614629e24f;
+            }
+          }
+          uint32_t p[NH][2];                                   // P^T: rows 2 t, 2 t + 1 of each block, q head g
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh) {
+            float up[2];                                       // what the bases are taken from: score, or score and exponent
+            bool move[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+              for (int b = 0; b < 2; ++b) s[nh][2 * b + e] = hid[b] ? -INFINITY : s[nh][2 * b + e] * (qs[nh][e] * ks[b]);
+              if constexpr (KIND == E4M3) up[e] = fmaxf(s[nh][e] + ex[0], s[nh][2 + e] + ex[1]);
+              else up[e] = fmaxf(s[nh][e], s[nh][2 + e]);
+            }
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) {
+              up[0] = fmaxf(up[0], __shfl_xor_sync(0xffffffffu, up[0], k));
+              up[1] = fmaxf(up[1], __shfl_xor_sync(0xffffffffu, up[1], k));
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) move[e] = up[e] - mx[nh][e] > TOP;
+            if (__any_sync(0xffffffffu, move[0] || move[1])) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float to = move[e] ? (fabsf(up[e]) < FAR ? up[e] - HEAD : up[e]) : mx[nh][e];
+                const float al = mx[nh][e] == to || mx[nh][e] == -INFINITY ? 1.f : ex2(mx[nh][e] - to);
+                mx[nh][e] = to;
+                sum[nh][e] *= al;
+#pragma unroll
+                for (int b = 0; b < HD / 16; ++b) {
+                  o[nh][b][e] *= al;
+                  o[nh][b][2 + e] *= al;
+                }
+              }
+            }
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float base = mx[nh][e] == -INFINITY ? 0.f : mx[nh][e];
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const float z = s[nh][2 * b + e], d = ex2(z - base);   // (e4m3: the sum's weight)
+                sum[nh][e] += d;
+                if constexpr (KIND == E4M3) w[2 * b + e] = hid[b] ? 0.f : ex2(z + ex[b] - base) * f[b];
+                else w[2 * b + e] = d;
+              }
+            }
+            p[nh][0] = transpose8(pack_w<PBF>(w[0], w[1]));
+            p[nh][1] = transpose8(pack_w<PBF>(w[2], w[3]));
+          }
+          // ---- O^T += V^T P^T; the values of hidden rows are zeros (0 x NaN is not)
+          uint32_t keep[2] = {0xffffffffu, 0xffffffffu};       // of the rows' pairs key8(2 t), key8(2 t + 1) of each block
+          if (!whole) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const uint32_t bits = __ballot_sync(0xffffffffu, hid[b]);   // (lane 4 n: row n)
+              keep[b] = (bits >> (8 * t4) & 1 ? 0u : 0xffffu) | (bits >> (8 * t4 + 4) & 1 ? 0u : 0xffff0000u);
+            }
+          }
+          if constexpr (KIND != E4M3) {
+            const int r = sub * 16 + (lane & 7) + (lane & 16 ? 8 : 0), ch = lane >> 3 & 1;
+#pragma unroll
+            for (int b = 0; b < HD / 16; ++b) {
+              uint32_t v[4];
+              ldsm4<true>(v, vb + (b >> 2) * (KT * 128) + r * 128 + ((((b & 3) * 2 + ch) ^ (r & 7)) << 4));
+              if (!whole) {
+                v[0] &= keep[0];
+                v[1] &= keep[0];
+                v[2] &= keep[1];
+                v[3] &= keep[1];
+              }
+#pragma unroll
+              for (int nh = 0; nh < NH; ++nh) mma16816<PBF>(o[nh][b], v, p[nh][0], p[nh][1]);
             }
           } else {
             constexpr int NW = HD / 32;                        // 32-bit words of a thread's V chunk
@@ -492,17 +540,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                              : "=r"(w[k][0]), "=r"(w[k][1])
                              : "r"(vb + r * HD + (((g >> 1) ^ (r >> 1 & 3)) << 4) + (g & 1) * 8));
             }
+            if (!whole) {                                      // (a NaN code of a hidden row: bytes of zero)
 #pragma unroll
-            for (int x4 = 0; x4 < NW; ++x4)
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int y = 0; y < NW; ++y) w[k][y] &= keep[k >> 1] >> (16 * (k & 1)) & 1 ? 0xffffffffu : 0u;
+            }
+#pragma unroll
+            for (int y = 0; y < NW; ++y)
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
-                const uint32_t y0 = __byte_perm(w[0][x4], w[1][x4], half ? 0x7362 : 0x5140);
-                const uint32_t y1 = __byte_perm(w[2][x4], w[3][x4], half ? 0x7362 : 0x5140);
+                const uint32_t y0 = __byte_perm(w[0][y], w[1][y], half ? 0x7362 : 0x5140);
+                const uint32_t y1 = __byte_perm(w[2][y], w[3][y], half ? 0x7362 : 0x5140);
+                uint32_t v[4];
+                widen4(y0, v[0], v[1]);
+                widen4(y1, v[2], v[3]);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const uint32_t v0 = widen2(y0 >> (16 * e)) & keep0, v1 = widen2(y1 >> (16 * e)) & keep1;
-                  mma16816<false>(o[4 * x4 + 2 * half + e], p, v0, v1);
-                }
+                for (int nh = 0; nh < NH; ++nh) mma16816<false>(o[nh][2 * y + half], v, p[nh][0], p[nh][1]);
               }
           }
         }
@@ -510,24 +564,26 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(&empty[st]);
       }
       i += m;
-      // ---- the pair ends here: the warps' sums through shared memory, 8 rows at a time
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+      // ---- the pair ends here: the warps' sums through shared memory, 8 q heads at a time
       const bool starts = c.t == 0, ends = c.t + m == c.T;
       float* slot = (float*)a.ws + (2 * (int64_t)blockIdx.x + (starts ? 1 : 0)) * slot_floats(HD);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int half = 0; half < NH; ++half) {
         if (8 * half >= nq) break;
-        if (t4 == 0) ml[warp * 8 + g] = half ? make_float2(m1, l1) : make_float2(m0, l0);
 #pragma unroll
-        for (int b = 0; b < HD / 8; ++b) {
-          float* at = pub + (warp * 8 + g) * L::OSTR;
-          at[out_col<HD, KIND>(b, t4, 0)] = o[b][2 * half];
-          at[out_col<HD, KIND>(b, t4, 1)] = o[b][2 * half + 1];
+        for (int e = 0; e < 2; ++e) {
+          float l = sum[half][e];
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+          if (g == 0) ml[warp * 8 + 2 * t4 + e] = make_float2(mx[half][e], l);
+          float* at = pub + (warp * 8 + 2 * t4 + e) * L::OSTR;
+#pragma unroll
+          for (int b = 0; b < HD / 16; ++b) {
+            at[out_col<HD, KIND>(b, g, 0)] = o[half][b][e];
+            at[out_col<HD, KIND>(b, g, 1)] = o[half][b][2 + e];
+          }
         }
-        group_sync();
+        group_sync<WARPS * 32>();
         constexpr int CV = HD / 4;                             // float4 columns
         for (int e = threadIdx.x; e < 8 * CV; e += WARPS * 32) {
           const int r = e / CV, cv = e % CV;
@@ -557,7 +613,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (cv == 0) reinterpret_cast<float2*>(slot + 16 * HD)[8 * half + r] = make_float2(M, lsum);
           }
         }
-        group_sync();
+        group_sync<WARPS * 32>();
       }
       if (ends && !starts && threadIdx.x == 0) {
         // the pair's first tile: list position u0 - c.t when this is the run's first pair (the only one it does not start)
@@ -572,14 +628,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     });
   }
   __syncthreads();
-  if (warp == WARPS && *abort_flag)            // nothing in flight when the CTA leaves
+  if (warp >= WARPS && *abort_flag)            // nothing in flight when the CTA leaves
     for (int st = 0; st < NST && st < asked; ++st) mbar_drain(&full[st], (asked - 1 - st) / NST & 1);
 }
 
 // Joins the parts of the pair that CTA blockIdx.x of the step ended: slot 2 first + 1, then slots 2 c of the CTAs behind it.
 // Block y takes rows y, y + gridDim.y, ...; its warps take the parts in turn, and their sums are joined in order.
 constexpr int JWARPS = 8;
-template <int HD, bool QBF>
+template <int HD, bool QBF, int NH>
 __global__ void __launch_bounds__(JWARPS * 32) join_kernel(const __grid_constant__ StepArgs sa, int C) {
   __shared__ float4 py[JWARPS][32];
   __shared__ float2 pml[JWARPS];
@@ -588,7 +644,7 @@ __global__ void __launch_bounds__(JWARPS * 32) join_kernel(const __grid_constant
   const float* ws = (const float*)sa.a.ws;
   const Record rec = reinterpret_cast<const Record*>(ws + 2 * (int64_t)C * slot_floats(HD))[blockIdx.x];
   if (!rec.valid) return;
-  const int kvh = rec.hg / sa.groups, h0 = kvh * sa.G + (rec.hg % sa.groups) * 16, nq = min(16, (kvh + 1) * sa.G - h0);
+  const int kvh = rec.hg / sa.groups, h0 = kvh * sa.G + (rec.hg % sa.groups) * 8 * NH, nq = min(8 * NH, (kvh + 1) * sa.G - h0);
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, parts = (int)blockIdx.x - rec.first + 1;
   for (int r = blockIdx.y; r < nq; r += gridDim.y) {
     float M = -INFINITY, l = 0.f;
@@ -627,20 +683,24 @@ __global__ void __launch_bounds__(JWARPS * 32) join_kernel(const __grid_constant
   }
 }
 
-template <int HD, int KIND, bool QBF>
+template <int HD, int KIND, bool QBF, int NH>
 cudaError_t launch(const StepArgs& sa, int num_sms, cudaStream_t st) {
-  using L = Lay<HD, KIND>;
+  using L = Lay<HD, KIND, NH>;
   CUtensorMap map;
   if (!pages_map(&map, sa.a.pages, std::min(KT, 1 << sa.a.pages.shift))) return cudaErrorInvalidValue;
-  CK_RET(cudaFuncSetAttribute(step_kernel<HD, KIND, QBF>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES));
-  CK_RET(launch_pdl(step_kernel<HD, KIND, QBF>, dim3((unsigned)num_sms), dim3(THREADS), L::BYTES, st, map, sa));
-  return launch_pdl(join_kernel<HD, QBF>, dim3((unsigned)num_sms, 4), dim3(JWARPS * 32), 0, st, sa, num_sms);
+  CK_RET(cudaFuncSetAttribute(step_kernel<HD, KIND, QBF, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES));
+  CK_RET(launch_pdl(step_kernel<HD, KIND, QBF, NH>, dim3((unsigned)num_sms), dim3(L::THREADS), L::BYTES, st, map, sa));
+  return launch_pdl(join_kernel<HD, QBF, NH>, dim3((unsigned)num_sms, 4), dim3(JWARPS * 32), 0, st, sa, num_sms);
+}
+template <int HD, int KIND, bool QBF>
+cudaError_t launch_nh(const StepArgs& sa, int num_sms, cudaStream_t st) {
+  return sa.G <= 8 ? launch<HD, KIND, QBF, 1>(sa, num_sms, st) : launch<HD, KIND, QBF, 2>(sa, num_sms, st);
 }
 template <int HD>
 cudaError_t launch_kind(const StepArgs& sa, int num_sms, cudaStream_t st) {
-  if (sa.a.pages.format == KVF_F16) return launch<HD, F16, false>(sa, num_sms, st);
-  if (sa.a.pages.format == KVF_BF16) return launch<HD, BF16, true>(sa, num_sms, st);
-  return sa.a.bf16 ? launch<HD, E4M3, true>(sa, num_sms, st) : launch<HD, E4M3, false>(sa, num_sms, st);
+  if (sa.a.pages.format == KVF_F16) return launch_nh<HD, F16, false>(sa, num_sms, st);
+  if (sa.a.pages.format == KVF_BF16) return launch_nh<HD, BF16, true>(sa, num_sms, st);
+  return sa.a.bf16 ? launch_nh<HD, E4M3, true>(sa, num_sms, st) : launch_nh<HD, E4M3, false>(sa, num_sms, st);
 }
 }  // namespace pgs
 
@@ -654,7 +714,7 @@ int64_t attention_paged_step_ws_bytes(int, int, int, int hd, int num_sms) {
 
 cudaError_t launch_attention_paged_step(const PagedAttnArgs& a, int n, const int* pos, int num_sms, cudaStream_t st) {
   pgs::StepArgs sa{a, pos, n, a.Hq / a.pages.Hkv, 0, 0};
-  sa.groups = (sa.G + 15) / 16;
+  sa.groups = sa.G <= 8 ? 1 : (sa.G + 15) / 16;
   sa.HG = sa.groups * a.pages.Hkv;
   return a.pages.hd == 128 ? pgs::launch_kind<128>(sa, num_sms, st) : pgs::launch_kind<64>(sa, num_sms, st);
 }

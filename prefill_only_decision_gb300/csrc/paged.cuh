@@ -49,12 +49,13 @@ __device__ __forceinline__ void tma5(void* dst, const CUtensorMap* map, uint64_t
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(t5::smem_u32(bar))
       : "memory");
 }
-// Contiguous bytes (16-byte aligned, a multiple of 16) into shared memory.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   t5::smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(t5::smem_u32(bar))
-               : "memory");
+// 16 bytes into shared memory, zeros where !on; and an arrival (counted in the barrier's number) once this thread's copies are
+// there.
+__device__ __forceinline__ void copy16_async(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(t5::smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(t5::smem_u32(bar)) : "memory");
 }
 
 // The pages as a tensor (hd, page rows, heads, pages, planes) in boxes of `rows` rows of up to 128 bytes. A page id outside
