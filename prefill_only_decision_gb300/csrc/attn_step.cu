@@ -8,7 +8,7 @@
 // which are written at once, and at most two in part, whose (o, m, l) join_kernel joins in the order of the CTAs: the
 // sizes and positions fix every order of summation.
 //
-// A CTA: four warps ask for the tiles by TMA (a lane per page box; page ids read 32 columns ahead) into a ring of 130 to 190 KB;
+// A CTA: three warps ask for the tiles by TMA (a lane per page box; page ids read 32 columns ahead) into a ring of 130 to 190 KB;
 // the others compute, four a tile, 16 rows each, without any exchange until the pair ends. With at most 16 query rows
 // tcgen05's 128-row tiles would stand nearly empty and pass S and P through TMEM between warps, so the products are mma.sync's
 // m16n8k16, whose operands and results stay in one warp's registers, transposed: S^T = K Q^T and O^T = V^T P^T, cached rows
@@ -35,7 +35,7 @@ namespace pgs {
 using namespace t5;
 using namespace pga;
 
-constexpr int KT = 64, PRODUCERS = 4;
+constexpr int KT = 64, PRODUCERS = 3;
 enum Kind { F16 = 0, BF16 = 1, E4M3 = 2 };
 
 __device__ uint64_t g_given_up;              // when a bounded wait last gave up, per device; never cleared
@@ -47,7 +47,7 @@ struct Lay {
   static constexpr int WARPS = KIND == E4M3 && NH == 1 ? 12 : 8, GROUPS = WARPS / 4;
   static constexpr int THREADS = (WARPS + PRODUCERS) * 32;
   static constexpr int PLANE = KT * HD * (KIND == E4M3 ? 1 : 2), TILE = 2 * PLANE;
-  static constexpr int NST = KIND == E4M3 ? (NH == 1 ? (HD == 128 ? 9 : 15) : (HD == 128 ? 8 : 16)) : (HD == 128 ? 6 : 12);
+  static constexpr int NST = KIND == E4M3 && NH == 1 ? (HD == 128 ? 9 : 15) : HD == 128 ? 6 : 12;
   static constexpr int SC = NST * TILE;                       // scales of a stage: [2][KT] floats (e4m3)
   static constexpr int OSTR = HD + 4;                         // floats of a q head in a warp's published sums
   static constexpr int OUT = SC + (KIND == E4M3 ? NST * 2 * KT * 4 : 0);
@@ -55,7 +55,7 @@ struct Lay {
   static constexpr int BAR = ML + WARPS * 8 * 8;
   static constexpr int BYTES = BAR + 2 * NST * 8 + 64;
   static_assert(BYTES + 1024 <= 227 * 1024, "shared memory of one CTA");
-  static_assert(NST % GROUPS == 0, "a stage is always the same warps' to read");
+  static_assert(NST % GROUPS == 0 && NST % PRODUCERS == 0, "a stage is always the same warps' to fill and to read");
 };
 
 struct StepArgs {
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
-      mbar_init(&full[i], PRODUCERS + (KIND == E4M3 ? 32 : 0));
+      mbar_init(&full[i], KIND == E4M3 ? 33 : 1);
       mbar_init(&empty[i], 4);
     }
     *abort_flag = 0;
@@ -260,15 +260,14 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
     }
   };
 
-  int asked = 0;                               // tiles asked for (producers)
+  uint32_t filled = 0;                         // (producers) per stage: filled (bit st), parity of the last fill (bit 16 + st)
   if (warp >= WARPS) {
-    // ---- TMA producers: plane pw % 2, every second page box (a box is a loop's pass over its uniform operands, so one
-    // warp's boxes of 16-row pages take longer than their bytes: 200001 e4m3 rows in pages of 16, 128 with one warp 62, 45 us)
+    // ---- TMA producers: every third tile each (a warp passes once over its loop for each box, whose operands are uniform: with
+    // one warp, or four for a quarter of each tile, the tiles of 16-row pages or 64-byte rows take longer than their bytes)
     constexpr int NB = KIND == E4M3 ? 1 : HD / 64, ROW = KIND == E4M3 ? HD : 128;   // boxes of a page, bytes of a box row
-    const int pw = warp - WARPS, plane = pw & 1, half = pw >> 1;
+    const int pw = warp - WARPS, plane = lane & 1, box = (lane >> 1) % NB, part = (lane >> 1) / NB;   // this lane's box
     const int npg = pg.shift < 6 ? KT >> pg.shift : 1, br = KT / npg;     // pages of a tile, rows of a box
-    const int bi = 2 * lane + half, box = bi % NB, part = bi / NB;        // this lane's box
-    int& i = asked;
+    int i = 0;
     int cs = -1, blk = -1, cur = 0, ns_ = -1, nblk = -1, next = 0;        // page ids of 32 columns: of a block, and of the next
     each_pair([&](const Cursor& c, int m, const Cursor& nx, bool more) {
       const int head = c.hg / sa.groups, last = (c.v.end - 1) >> pg.shift;
@@ -277,8 +276,10 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
         return col <= (w.v.end - 1) >> pg.shift ? pg.table[(int64_t)w.s * pg.table_stride + col] : -1;
       };
       auto block_of = [&](const Cursor& w, int t) { return (w.tl.at(t) * KT >> pg.shift) >> 5; };
-      for (int t = c.t; t < c.t + m; ++t, ++i) {
-        const int j0 = c.tl.at(t) * KT, col = j0 >> pg.shift;
+      const int i0 = i;
+      i += m;
+      for (int x = (pw - i0 % PRODUCERS + PRODUCERS) % PRODUCERS; x < m; x += PRODUCERS) {
+        const int t = c.t + x, j0 = c.tl.at(t) * KT, col = j0 >> pg.shift;
         if (col >> 5 != blk || c.s != cs) {
           cur = ns_ == c.s && nblk == col >> 5 ? next : ids(c, col >> 5);
           cs = c.s;
@@ -295,24 +296,23 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
           }
         }
         const int id = __shfl_sync(0xffffffffu, cur, (col + part) & 31);
-        const int st = i % NST;
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], (i / NST & 1) ^ 1, abort_flag, &g_given_up) ? 1 : 0)) return false;
+        const int tile = i0 + x, st = tile % NST;
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], (tile / NST & 1) ^ 1, abort_flag, &g_given_up) ? 1 : 0)) return false;
         const int there = min(npg, last - col + 1);            // pages that the sequence has
-        if (lane == 0) mbar_expect_tx(&full[st], (uint32_t)((there * NB - half + 1) / 2 * br * ROW));
+        if (lane == 0) mbar_expect_tx(&full[st], (uint32_t)(there * NB * 2 * br * ROW));
         __syncwarp();
         if constexpr (KIND == E4M3) {
-          // the plane's scales, 4 rows a lane (rows without a page: zeros)
-          const int sr = 4 * lane, spart = sr / br;
+          // the tile's scales, 4 rows of a plane a lane (rows without a page: zeros)
+          const int sr = 4 * (lane & 15), sp = lane >> 4, spart = sr / br;
           const int sid = __shfl_sync(0xffffffffu, cur, (col + spart) & 31);
-          if (half == 0 && lane < KT / 4) {
-            const bool on = spart < there && sid >= 0 && sid < pg.n_pages;
-            copy16_async(sm + L::SC + (st * 2 * KT + plane * KT + sr) * 4,
-                         pg.scales + ((((int64_t)plane * pg.n_pages + (on ? sid : 0)) * pg.Hkv + head) << pg.shift) +
-                             ((j0 + sr) & ((1 << pg.shift) - 1)),
-                         on);
-            arrive_after_copies(&full[st]);
-          }
+          const bool on = spart < there && sid >= 0 && sid < pg.n_pages;
+          copy16_async(sm + L::SC + (st * 2 * KT + sp * KT + sr) * 4,
+                       pg.scales + ((((int64_t)sp * pg.n_pages + (on ? sid : 0)) * pg.Hkv + head) << pg.shift) +
+                           ((j0 + sr) & ((1 << pg.shift) - 1)),
+                       on);
+          arrive_after_copies(&full[st]);
         }
+        filled = (filled & ~(1u << (16 + st))) | 1u << st | (uint32_t)(tile / NST & 1) << (16 + st);
         if (part < there)
           tma5(sm + st * L::TILE + plane * L::PLANE + box * (KT * 128) + part * br * ROW, &map, &full[st], box * 64,
                j0 & ((1 << pg.shift) - 1), head, id, plane);
@@ -629,7 +629,8 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
   }
   __syncthreads();
   if (warp >= WARPS && *abort_flag)            // nothing in flight when the CTA leaves
-    for (int st = 0; st < NST && st < asked; ++st) mbar_drain(&full[st], (asked - 1 - st) / NST & 1);
+    for (int st = warp - WARPS; st < NST; st += PRODUCERS)
+      if (filled >> st & 1) mbar_drain(&full[st], filled >> (16 + st) & 1);
 }
 
 // Joins the parts of the pair that CTA blockIdx.x of the step ended: slot 2 first + 1, then slots 2 c of the CTAs behind it.
