@@ -70,7 +70,7 @@ struct Lay {
   static constexpr int BASE = QSC + 2 * BQ * 4;           // [2][BASES] exponent bounds
   static constexpr int BAR = BASE + 2 * BASES * 4;
   static constexpr int NS = 2 * FR > F ? 2 * FR : F;
-  static constexpr int NBAR = 1 + 4 * NS + 12 + 2 + 2 + 4;
+  static constexpr int NBAR = 3 + 4 * NS + 12 + 2 + 2 + 4;
   static constexpr int USED = BAR + NBAR * 8 + 16;
   static_assert(USED <= 227 * 1024, "shared memory of one CTA");
   // above half an SM: each CTA allocates all of TMEM, so two never share one
@@ -88,11 +88,12 @@ struct Slot {
   int s;
   uint32_t ph, kind_ph;        // parity of this fill, and of it among the slot's fills of its kind (they take turns)
 };
+// (both: the ring of both streams; else stream x's; k: the tile's number in the ring)
 template <int F, int FR>
-__device__ __forceinline__ Slot slot_of(bool two, int t, bool is_v) {
-  const uint32_t i = 2 * (two ? t : t >> 1) + (is_v ? 1 : 0);
-  if (two) return {(int)(i % F), i / F & 1, i / F >> 1 & 1};
-  return {(t & 1 ? FR : 0) + (int)(i % FR), i / FR & 1, i / FR >> 1 & 1};
+__device__ __forceinline__ Slot slot_of(bool both, int x, int k, bool is_v) {
+  const uint32_t i = 2 * (uint32_t)k + (is_v ? 1 : 0);
+  if (both) return {(int)(i % F), i / F & 1, i / F >> 1 & 1};
+  return {(x ? FR : 0) + (int)(i % FR), i / FR & 1, i / FR >> 1 & 1};
 }
 
 template <bool BF>
@@ -150,24 +151,118 @@ __device__ __forceinline__ int bound_of(float scale) {
   return (u >> 23) == 0 || (u >> 23) >= 255 ? NO_BOUND : (int)(u >> 23) - 126;
 }
 
+// One of a CTA's items: (sequence, one or two query tiles, kv head) and a part of its key tiles.
+struct Item {
+  int w, si, g, ns, len;       // number in the list, sequence (of the table), kv head, the sequence's parts per item and rows
+  int v0, v1;                  // first row of the sequence, and one past its last
+  int p_first, p_last;         // positions of the first and the last row
+  bool two;                    // a second query tile
+  Seen all;                    // what some row sees
+  int n, head, sink0, tail0;   // the part's key tiles: t < head: sink0 + t, else tail0 + t
+  // a key tile, or row, that some query row does not see
+  __device__ bool partly(int j0, int window, int sinks) const {
+    return j0 + BKV - 1 > p_first || (window && p_last - j0 >= window && j0 + BKV > sinks);
+  }
+  __device__ int tile(int t) const { return (t + (t < head ? sink0 : tail0)) * BKV; }
+};
+template <int N>
+__device__ __forceinline__ Item item_of(const Tab<N>& tab, const PagedAttnArgs& a, const Plan& pl, int w) {
+  Item it;
+  int si = 0;
+  for (int hi = tab.n - 1; si < hi;) {
+    const int mid = (si + hi + 1) >> 1;
+    if (tab.start[mid] <= w) si = mid;
+    else hi = mid - 1;
+  }
+  it.w = w;
+  it.si = si;
+  it.len = tab.len[si];
+  it.ns = tab.ns[si];
+  const int MT = (it.len + pl.RT - 1) / pl.RT, MP = (MT + pl.nt - 1) / pl.nt;
+  const int local = w - tab.start[si], part = local % it.ns, item = local / it.ns;
+  it.g = item % a.pages.Hkv;
+  const int mp = MP - 1 - item / a.pages.Hkv;      // (the last rows see most: first)
+  it.two = pl.nt == 2 && 2 * mp + 1 < MT;
+  it.v0 = pl.nt * mp * pl.RT;
+  it.v1 = min(it.len, it.v0 + (it.two ? 2 : 1) * pl.RT);
+  it.p_first = tab.pos0[si] + it.v0;
+  it.p_last = tab.pos0[si] + it.v1 - 1;
+  it.all.end = it.p_last + 1;
+  it.all.lo = a.window && it.p_first - (a.window - 1) > 0 ? it.p_first - (a.window - 1) : 0;
+  it.all.sk = min(a.sinks, it.all.lo);
+  const Tiles tl = tiles_of<BKV>(it.all);
+  const int total = tl.count(), per = (total + it.ns - 1) / it.ns, jb = min(total, part * per);
+  it.n = min(total, jb + per) - jb;
+  it.head = tl.head - jb;
+  it.sink0 = jb;
+  it.tail0 = tl.first - tl.head + jb;
+  return it;
+}
+
+// Adds the non-finite elements of columns c .. c + 31 of the partly hidden value rows that a query sees.
+template <bool E4, bool PBF>
+__device__ __forceinline__ void add_nonfinite(const Item& it, const PagedAttnArgs& a, int seq, int pos, int row_lo, int c,
+                                              uint32_t* o) {
+  const PagesArgs& pg = a.pages;
+  auto add = [](uint32_t& x, float y) { x = __float_as_uint(__uint_as_float(x) + y); };
+  for (int t = 0; t < it.n; ++t) {
+    const int j0 = it.tile(t);
+    if (!it.partly(j0, a.window, a.sinks)) continue;
+    for (int j = j0; j < j0 + BKV && j <= pos; ++j) {
+      if (j < row_lo && j >= a.sinks) continue;
+      const int id = pg.table[(int64_t)seq * pg.table_stride + (j >> pg.shift)];
+      if (id < 0 || id >= pg.n_pages) continue;
+      const int64_t vec = (((pg.n_pages + (int64_t)id) * pg.Hkv + it.g) << pg.shift) + (j & ((1 << pg.shift) - 1));
+      if constexpr (E4) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float y =
+              __half2float(__half(__nv_cvt_fp8_to_halfraw(((const __nv_fp8_storage_t*)pg.data)[vec * pg.hd + c + e], __NV_E4M3))) *
+              pg.scales[vec];
+          if (!isfinite(y)) add(o[e], y);
+        }
+      } else {
+        const uint4* at = reinterpret_cast<const uint4*>((const uint16_t*)pg.data + vec * pg.hd + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint4 y = at[e];
+          const uint32_t y4[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (nonfinite2<PBF>(y4[i])) {
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const uint16_t raw = (uint16_t)(y4[i] >> (16 * z));
+                const float f = PBF ? __uint_as_float((uint32_t)raw << 16) : __half2float(__ushort_as_half(raw));
+                if (!isfinite(f)) add(o[8 * e + 2 * i + z], f);
+              }
+            }
+        }
+      }
+    }
+  }
+}
+
 template <int HD, int KIND, int N>
 __global__ void __launch_bounds__(threads_of(KIND), 1)
     paged_kernel(const __grid_constant__ Tab<N> tab, const __grid_constant__ CUtensorMap mapKV,
-                 const __grid_constant__ PagedAttnArgs a, const Plan pl) {
+                 const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ PagedAttnArgs a, const Plan pl) {
   using L = Lay<HD>;
-  constexpr bool E4 = is_e4m3(KIND), PBF = KIND == BF16, OBF = out_bf16(KIND);
+  constexpr bool E4 = is_e4m3(KIND), PBF = KIND == BF16, OBF = out_bf16(KIND), QTMA = KIND != E4M3_QBF;
   constexpr int NB = HD / 64, F = L::F, FR = L::FR, NS = L::NS;
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* bars = (uint64_t*)(sm + L::BAR);
-  uint64_t* q_full = bars;
-  uint64_t* full = bars + 1;                   // [NS] a K tile is there
+  uint64_t* q_full = bars;                     // an item's Q is there
+  uint64_t* q_empty = bars + 1;                // its products have read it
+  uint64_t* kv_free = bars + 2;                // (one query tile) the published sums in the K/V stages are read
+  uint64_t* full = bars + 3;                   // [NS] a K tile is there
   uint64_t* vfull = full + NS;                 // [NS] a V tile is there
   uint64_t* empty = vfull + NS;                // [NS]
   uint64_t* ready = empty + NS;                // [NS] the V tile holds no non-finite element of a hidden row (not with e4m3)
   uint64_t* s_full = ready + NS;               // [2 streams][2 halves of the key tile]
   uint64_t* p_full = s_full + 4;               // [2][2]
   uint64_t* o_step = p_full + 4;               // [2][2] the half's P V has completed
-  uint64_t* o_done = o_step + 4;               // [2] the stream's last product has completed
+  uint64_t* o_done = o_step + 4;               // [2] the stream's last product of an item has completed
   uint64_t* mma_idle = o_done + 2;             // [2]
   uint64_t* joined = mma_idle + 2;             // [4 quadrants] stream 1's sums are published
   uint32_t* tmem_slot = (uint32_t*)(bars + L::NBAR);
@@ -178,48 +273,22 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
 
   const PagesArgs& pg = a.pages;
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  // this CTA's sequence, item and part
-  int si = 0;
-  for (int hi = tab.n - 1; si < hi;) {
-    const int mid = (si + hi + 1) >> 1;
-    if (tab.start[mid] <= (int)blockIdx.x) si = mid;
-    else hi = mid - 1;
-  }
-  const int len = tab.len[si], ns = tab.ns[si], MT = (len + pl.RT - 1) / pl.RT, MP = (MT + pl.nt - 1) / pl.nt;
-  const int local = (int)blockIdx.x - tab.start[si], part = local % ns, item = local / ns;
-  const int g = item % pg.Hkv, mp = MP - 1 - item / pg.Hkv;   // (the last rows see most: first)
-  const bool two = pl.nt == 2 && 2 * mp + 1 < MT;  // two query tiles; else one over alternate key tiles
-  const int v0 = pl.nt * mp * pl.RT;               // first row of the item, and one past its last
-  const int v1 = min(len, v0 + (two ? 2 : 1) * pl.RT);
-  const int p_first = tab.pos0[si] + v0, p_last = tab.pos0[si] + v1 - 1;
-  Seen all;                                        // what some row of the item sees
-  all.end = p_last + 1;
-  all.lo = a.window && p_first - (a.window - 1) > 0 ? p_first - (a.window - 1) : 0;
-  all.sk = min(a.sinks, all.lo);
-  const Tiles tl = tiles_of<BKV>(all);
-  const int total = tl.count(), per = (total + ns - 1) / ns;
-  const int jb = min(total, part * per), n = min(total, jb + per) - jb;
-  uint8_t* kvst = sm + (two ? L::KV2 : L::KV1);
-  // a key tile that some row does not see in full
-  auto partly = [&](int j0) {
-    return j0 + BKV - 1 > p_first || (a.window && p_last - j0 >= a.window && j0 + BKV > a.sinks);
-  };
-
-  // quadrants of 32 matrix rows that stream x's query tile fills (a single tile: both streams')
-  auto quads = [&](int x) { return (min(pl.RT, v1 - (v0 + (two && x ? pl.RT : 0))) * pl.G + 31) / 32; };
+  const bool pair = pl.nt == 2;                // two query tiles share the ring; else one's key tiles alternate
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 8);
+    mbar_init(q_full, QTMA ? 1 : 8);
+    mbar_init(q_empty, 2);
+    mbar_init(kv_free, 4);
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], E4 ? 4 : 1);
       mbar_init(&vfull[s], E4 ? 4 : 1);
-      mbar_init(&empty[s], two ? 2 : 1);       // the streams that read the slot
+      mbar_init(&empty[s], pair ? 2 : 1);      // the streams that read the slot
       mbar_init(&ready[s], 4);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&mma_idle[x], 1);
       for (int h = 0; h < 2; ++h) {
         mbar_init(&s_full[2 * x + h], 1);
-        mbar_init(&p_full[2 * x + h], quads(x));
+        mbar_init(&p_full[2 * x + h], 4);
         mbar_init(&o_step[2 * x + h], 1);
       }
       mbar_init(&o_done[x], 1);
@@ -234,54 +303,91 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
+  uint8_t* kvst = sm + (pair ? L::KV2 : L::KV1);
   auto wwait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_given_up) ? 1 : 0) != 0;
   };
-  // the fills in the order in which they are made: K_0 .. K_{lead-1}, then V_t, K_{t+lead}; fn(t, is V) for those that there are
-  const int lead = two ? 1 : 2;
-  auto fills = [&](auto&& fn) {
+  // This CTA's items: every gridDim-th of the list, there and back again, so that a list that grows cheaper stays even.
+  // fn(item, its number, tiles before it of stream 0 and of stream 1) until it returns false.
+  auto each_item = [&](auto&& fn) {
+    int t0 = 0, t1 = 0, k = 0;
+    for (int round = 0;; ++round) {
+      const int64_t w0 = (int64_t)round * gridDim.x;
+      if (w0 >= tab.start[tab.n]) break;
+      const int64_t w = w0 + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      if (w >= tab.start[tab.n]) continue;
+      const Item it = item_of(tab, a, pl, (int)w);
+      if (!fn(it, k, t0, t1)) break;
+      t0 += pair ? it.n : (it.n + 1) >> 1;
+      t1 += pair ? (it.two ? it.n : 0) : it.n >> 1;
+      ++k;
+    }
+  };
+  // an item's tile t in the ring: the stream whose ring it is (pair: 0), and its number there
+  auto slot = [&](int t, bool is_v, int t0, int t1) {
+    return pair ? slot_of<F, FR>(true, 0, t0 + t, is_v) : slot_of<F, FR>(false, t & 1, (t & 1 ? t1 : t0) + (t >> 1), is_v);
+  };
+  // an item's fills in the order in which they are made: K_0 .. K_{lead-1}, then V_t, K_{t+lead}
+  const int lead = pair ? 1 : 2;
+  auto fills = [&](int n, auto&& fn) {
     for (int q = 0; q < 2 * n + lead - 1; ++q) {
       const int e = q - lead;
       const bool is_v = e >= 0 && !(e & 1);
       const int t = e < 0 ? q : is_v ? e >> 1 : lead + (e >> 1);
-      if (!fn(t, is_v)) break;
+      if (!fn(t, is_v)) return false;
     }
+    return true;
   };
 
   uint32_t done = 0;           // (producer) per slot and kind: begun (bit d), parity of the last fill (bit 16 + d)
+  int q_done = 0;              // (producer) Q fills
   if (warp == 0) {
-    // ---- TMA producer
+    // ---- TMA producer: Q, and with 16-bit pages the K and V tiles
     wait_prerequisites();
-    if constexpr (!E4) {
-      const int npg = BKV >> pg.shift, box = lane % NB, pp = lane / NB, last = (all.end - 1) >> pg.shift;
-      const int64_t trow = (int64_t)tab.seq[si] * pg.table_stride;
+    const int npg = BKV >> pg.shift, box = lane % NB, pp = lane / NB;
+    each_item([&](const Item& it, int k, int t0, int t1) {
+      if constexpr (QTMA) {
+        if (!wwait(q_empty, (k & 1) ^ 1)) return false;
+        const int tiles = it.two ? 2 : 1;
+        if (lane == 0) mbar_expect_tx(q_full, (uint32_t)(tiles * NB * pl.G * pl.RT * 128));
+        __syncwarp();
+        if (lane < tiles * NB)
+          tma3(sm + L::Q + (lane / NB) * (BQ * HD * 2) + (lane % NB) * (BQ * 128), &mapQ, q_full, 64 * (lane % NB), it.g * pl.G,
+               tab.row0[it.si] + it.v0 + (lane / NB) * pl.RT);
+        q_done = k + 1;
+      }
+      if constexpr (E4) return true;
+      if (!pair && k > 0 && !wwait(kv_free, (k - 1) & 1)) return false;
+      const int last = (it.all.end - 1) >> pg.shift;
+      const int64_t trow = (int64_t)tab.seq[it.si] * pg.table_stride;
       auto page_id = [&](int t) {              // of this lane's part of tile t
-        if (t >= n || pp >= npg) return -1;
-        const int col = (tl.at(jb + t) * BKV >> pg.shift) + pp;
+        if (t >= it.n || pp >= npg) return -1;
+        const int col = (it.tile(t) >> pg.shift) + pp;
         return col <= last ? pg.table[trow + col] : -1;
       };
       int id_next = page_id(0), id = -1, id_before = -1;      // of the K tile to come, of the latest and of the one before it
-      fills([&](int t, bool is_v) {
+      return fills(it.n, [&](int t, bool is_v) {
         if (!is_v) {
           id_before = id;
           id = id_next;
         }
-        if (t >= n) return true;
-        const Slot k = slot_of<F, FR>(two, t, is_v);
-        const int s = k.s, j0 = tl.at(jb + t) * BKV, pid = is_v && lead == 2 ? id_before : id;
-        if (!wwait(&empty[s], k.ph ^ 1)) return false;
+        if (t >= it.n) return true;
+        const Slot sl = slot(t, is_v, t0, t1);
+        const int s = sl.s, j0 = it.tile(t), pid = is_v && lead == 2 ? id_before : id;
+        if (!wwait(&empty[s], sl.ph ^ 1)) return false;
         const int there = min(npg, last - (j0 >> pg.shift) + 1);   // pages that the sequence has
         uint64_t* bar = is_v ? &vfull[s] : &full[s];
         if (lane == 0) mbar_expect_tx(bar, (uint32_t)(there << pg.shift) * (HD * 2));
         __syncwarp();
         if (pp < there)
-          tma5(kvst + s * L::TILE + box * (BKV * 128) + (pp << pg.shift) * 128, &mapKV, bar, 64 * box, 0, g, pid, is_v ? 1 : 0);
+          tma5(kvst + s * L::TILE + box * (BKV * 128) + (pp << pg.shift) * 128, &mapKV, bar, 64 * box, 0, it.g, pid,
+               is_v ? 1 : 0);
         const int d = 2 * s + (is_v ? 1 : 0);
-        done = (done & ~(1u << (16 + d))) | 1u << d | k.kind_ph << (16 + d);
+        done = (done & ~(1u << (16 + d))) | 1u << d | sl.kind_ph << (16 + d);
         if (!is_v) id_next = page_id(t + 1);
         return true;
       });
-    }
+    });
   } else if (warp == 1 || warp == 14) {
     // ---- MMA issue of stream x: the whole warp waits, one lane issues. A stream's products run in
     // the order they are issued, so S of its next tile may take the columns that P V reads before it
@@ -289,7 +395,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
     const bool leader = elect_one();
     constexpr uint32_t ID_S = idesc_f16(BKV / 2, PBF, 0, 0), ID_O = idesc_f16(HD, PBF, 0, 1);
     const uint32_t tS = tmem + x * 128, tO = tmem + T_O + x * 128;
-    const uint64_t qd = desc_sw128(smem_u32(sm + L::Q) + (two && x ? BQ * HD * 2 : 0), 16);
+    const uint64_t qd = desc_sw128(smem_u32(sm + L::Q) + (pair && x ? BQ * HD * 2 : 0), 16);
     auto scores = [&](int h, int s) {          // S = Q K^T over half h of the tile in slot s
       const uint64_t kd = desc_sw128(smem_u32(kvst + s * L::TILE) + h * (BKV / 2 * 128), 16);
 #pragma unroll
@@ -308,41 +414,58 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       commit(&o_step[2 * x + h]);
     };
     wait_prerequisites();                      // (a bounded wait must not begin while the calls before still run)
-    // of each half h: P V of tile i - 1, then S of tile i into the same columns
-    const int cnt = two ? n : (n + 1 - x) >> 1;
-    if (cnt > 0 && wwait(q_full, 0))
-      for (int i = 0; i <= cnt; ++i) {
-        const int t = two ? i : 2 * i + x;
-        const Slot k = slot_of<F, FR>(two, t, false);                    // (unused at i = cnt)
-        const Slot v = slot_of<F, FR>(two, t - (two ? 1 : 2), true);     // (unused at i = 0)
+    each_item([&](const Item& it, int k, int t0, int t1) {
+      if (pair && x && !it.two) {              // no second tile: its share of the stages' release
+        if (!wwait(q_full, k & 1)) return false;   // (an arrival must not count for the item before)
+        if (lane == 0) mbar_arrive(q_empty);
+        return fills(it.n, [&](int t, bool is_v) {
+          if (t >= it.n) return true;
+          const Slot sl = slot(t, is_v, t0, t1);
+          if (!wwait(is_v ? &vfull[sl.s] : &full[sl.s], sl.kind_ph)) return false;
+          if (lane == 0) mbar_arrive(&empty[sl.s]);
+          return true;
+        });
+      }
+      // of each half h: P V of tile i - 1, then S of tile i into the same columns
+      const int cnt = pair ? it.n : (it.n + 1 - x) >> 1, before = x ? t1 : t0;
+      if (!wwait(q_full, k & 1)) return false;
+      if (cnt == 0 && lane == 0) mbar_arrive(q_empty);
+      fence_after();
+      for (int i = 0; cnt > 0 && i <= cnt; ++i) {
+        const int t = pair ? i : 2 * i + x;
+        const Slot ks = slot(t, false, t0, t1);                          // (unused at i = cnt)
+        const Slot vs = slot(t - (pair ? 1 : 2), true, t0, t1);          // (unused at i = 0)
         auto half = [&](auto hc) {
           constexpr int h = decltype(hc)::value;
           if (i > 0) {
-            if (h == 0 && (!wwait(&vfull[v.s], v.kind_ph) || (!E4 && !wwait(&ready[v.s], v.kind_ph)))) return false;
-            if (!wwait(&p_full[2 * x + h], (i - 1) & 1)) return false;
+            if (h == 0 && (!wwait(&vfull[vs.s], vs.kind_ph) || (!E4 && !wwait(&ready[vs.s], vs.kind_ph)))) return false;
+            if (!wwait(&p_full[2 * x + h], (before + i - 1) & 1)) return false;
             fence_after();
             if (leader) {
-              values(h, v.s, h > 0 || i > 1);
-              if (h) commit(&empty[v.s]);
+              values(h, vs.s, h > 0 || i > 1);
+              if (h) commit(&empty[vs.s]);
               if (h && i == cnt) commit(&o_done[x]);
             }
             __syncwarp();
           }
           if (i < cnt) {
             if (h == 0) {
-              if (!wwait(&full[k.s], k.kind_ph)) return false;
+              if (!wwait(&full[ks.s], ks.kind_ph)) return false;
               fence_after();
             }
             if (leader) {
-              scores(h, k.s);
-              if (h) commit(&empty[k.s]);
+              scores(h, ks.s);
+              if (h) commit(&empty[ks.s]);
+              if (h && i == cnt - 1) commit(q_empty);
             }
             __syncwarp();
           }
           return true;
         };
-        if (!half(std::integral_constant<int, 0>{}) || !half(std::integral_constant<int, 1>{})) break;
+        if (!half(std::integral_constant<int, 0>{}) || !half(std::integral_constant<int, 1>{})) return false;
       }
+      return true;
+    });
     if (leader) {
       commit(&mma_idle[x]);
       mbar_drain(&mma_idle[x], 0);             // every MMA issued above has completed
@@ -351,33 +474,54 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
     const int lw = warp < 14 ? warp - 10 : warp - 15;
     wait_prerequisites();
     if constexpr (!E4) {
-      // ---- scan of the partly hidden V tiles: rows 32 lw .. +31
-      constexpr int CH = HD / 8, RPI = 32 / CH;
-      for (int t = 0; t < n; ++t) {
-        const Slot k = slot_of<F, FR>(two, t, true);
-        if (!wwait(&vfull[k.s], k.kind_ph)) break;
-        const int j0 = tl.at(jb + t) * BKV;
-        if (partly(j0)) {
-          uint8_t* tile = kvst + k.s * L::TILE;
-          const int c = lane % CH;
-          bool bad = false;
-#pragma unroll 4
-          for (int p = 0; p < 32 / RPI; ++p) {
-            const int r = lw * 32 + p * RPI + lane / CH;
-            uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * (BKV * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-            uint4 x = *at;
-            if (drop_nonfinite<PBF>(x)) {
-              *at = x;
-              const int j = j0 + r;            // (rows that no query sees hold anything: nobody asks for their values)
-              bad |= j < all.end && (j >= all.lo || j < all.sk);
+      // ---- scan of the partly hidden V tiles: rows 32 lw .. +31. Magnitudes' maximum first; a tile with something that is
+      // not finite (rare) once more, to take it out
+      constexpr int CH = HD / 8, RPI = 32 / CH, PASSES = 32 / RPI;
+      const int c = lane % CH;
+      each_item([&](const Item& it, int, int t0, int t1) {
+        for (int t = 0; t < it.n; ++t) {
+          const Slot k = slot(t, true, t0, t1);
+          if (!wwait(&vfull[k.s], k.kind_ph)) return false;
+          const int j0 = it.tile(t);
+          if (it.partly(j0, a.window, a.sinks)) {
+            uint8_t* tile = kvst + k.s * L::TILE;
+            auto at = [&](int p) {
+              const int r = lw * 32 + p * RPI + lane / CH;
+              return reinterpret_cast<uint4*>(tile + (c >> 3) * (BKV * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            };
+            using T = std::conditional_t<PBF, bf16, f16>;
+            uint32_t top = 0;
+#pragma unroll
+            for (int p = 0; p < PASSES; p += 8) {
+              uint4 y[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (p + i < PASSES) y[i] = *at(p + i);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (p + i < PASSES)
+                  top = absmax2(T(), top, absmax2(T(), absmax2(T(), y[i].x, y[i].y), absmax2(T(), y[i].z, y[i].w)));
+            }
+            if (__any_sync(0xffffffffu, nonfinite2<PBF>(top))) {
+              bool bad = false;
+#pragma unroll 1
+              for (int p = 0; p < PASSES; ++p) {
+                uint4 x = *at(p);
+                if (drop_nonfinite<PBF>(x)) {
+                  *at(p) = x;
+                  const int j = j0 + lw * 32 + p * RPI + lane / CH;   // (of rows that no query sees nobody asks for the values)
+                  bad |= j < it.all.end && (j >= it.all.lo || j < it.all.sk);
+                }
+              }
+              if (bad) *v_flag = 1;
+              fence_async_smem();
             }
           }
-          if (bad) *v_flag = 1;
-          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ready[k.s]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ready[k.s]);
-      }
+        return true;
+      });
     } else {
       // ---- e4m3 pages: this warp's 32 rows of every tile of its plane. LPR lanes of 16 codes per row, RP rows a pass, PN
       // passes; the lanes of a row's second 64 columns take their two 8-code halves in the other order, so that no store
@@ -386,281 +530,275 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       constexpr int LPR = HD / 16, RP = 32 / LPR, PN = 32 / RP;
       const int ci = lane % LPR, sw = HD == 128 && ci >= 4 ? 1 : 0;
       const int c0 = ((2 * ci) & 7) + sw, c1 = ((2 * ci) & 7) + 1 - sw;
-      const int64_t trow = (int64_t)tab.seq[si] * pg.table_stride;
       const int mask = (1 << pg.shift) - 1;
-      auto vector_of = [&](int key) -> int64_t {               // of a cached row's K, -1: none that a query sees
-        if (key >= all.end || (key < all.lo && key >= all.sk)) return -1;
-        const int id = pg.table[trow + (key >> pg.shift)];
-        if (id < 0 || id >= pg.n_pages) return -1;
-        return (((int64_t)id * pg.Hkv + g) << pg.shift) + (key & mask);
-      };
       const int64_t to_v = ((int64_t)pg.n_pages * pg.Hkv) << pg.shift;   // from a K vector to its V vector
-      uint4 code[PN];                                          // of this warp's rows of its plane's next tile
-      int64_t vec = -1, vec_next = -1;                         // vector of row `lane` in tile t + 1, and in the one behind it
-      int64_t q4[4], q4_next[4];                               // the K vectors of rows lane, lane + 32, .. of those tiles
-      float sk4[4], sv4[4];                                    // their scales, of tile t + 1
-      int run_v = NO_BOUND;
-      auto lookup = [&](int t) {
-        const int j0 = t < n ? tl.at(jb + t) * BKV : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q4_next[i] = t < n ? vector_of(j0 + 32 * i + lane) : -1;
-        vec_next = lw == 0 ? q4_next[0] : lw == 1 ? q4_next[1] : lw == 2 ? q4_next[2] : q4_next[3];
-        if (plane && vec_next >= 0) vec_next += to_v;
-      };
-      auto read = [&](int64_t v, int p) {
-        const int64_t w = __shfl_sync(0xffffffffu, v, p * RP + lane / LPR);
-        return w >= 0 ? __ldg(reinterpret_cast<const uint4*>((const uint8_t*)pg.data + w * HD) + ci) : make_uint4(0, 0, 0, 0);
-      };
-      auto fetch = [&]() {                                     // scales and codes of the tile that lookup found
-        vec = vec_next;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          q4[i] = q4_next[i];
-          sk4[i] = plane == 0 && q4[i] >= 0 ? __ldg(pg.scales + q4[i]) : 0.f;
-          sv4[i] = q4[i] >= 0 ? __ldg(pg.scales + q4[i] + to_v) : 0.f;
-        }
-#pragma unroll
-        for (int p = 0; p < PN; ++p) code[p] = read(vec, p);
-      };
-      lookup(0);
-      if (n > 0) fetch();
-      lookup(1);
-      for (int t = 0; t < n; ++t) {
-        const Slot k = slot_of<F, FR>(two, t, plane == 1);
-        // exponent bounds: of the tile's K scales, and the running one of V's (both planes' warps follow it)
-        int bk = NO_BOUND, bv = NO_BOUND;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          bk = max(bk, bound_of(sk4[i]));
-          bv = max(bv, bound_of(sv4[i]));
-        }
-        bk = __reduce_max_sync(0xffffffffu, bk);
-        run_v = max(run_v, __reduce_max_sync(0xffffffffu, bv));
-        if (bk == NO_BOUND) bk = 0;
-        const int E = plane ? (run_v == NO_BOUND ? 0 : run_v) : bk;
-        const float mine = plane ? (lw == 0 ? sv4[0] : lw == 1 ? sv4[1] : lw == 2 ? sv4[2] : sv4[3])
-                                 : (lw == 0 ? sk4[0] : lw == 1 ? sk4[1] : lw == 2 ? sk4[2] : sk4[3]);
-        const float fac = ldexpf(mine, 7 - E);                 // below 2^7
-        if (!wwait(&empty[k.s], k.ph ^ 1)) break;
-        uint8_t* dst = kvst + k.s * L::TILE;
-        const bool fast = __all_sync(0xffffffffu, __half2float(__float2half_rn(fac)) == fac);
-        const bool check = plane && partly(tl.at(jb + t) * BKV);
-        uint8_t* d = dst + (ci >> 2) * (BKV * 128) + (lw * 32 + lane / LPR) * 128;
-        bool bad = false;
-        auto convert = [&](auto is_fast, const uint4 cc, int p) {
-          constexpr bool FAST = decltype(is_fast)::value;
-          const float f = __shfl_sync(0xffffffffu, fac, p * RP + lane / LPR);
-          const int x = (p * RP + lane / LPR) & 7;
-          const uint2 lo = make_uint2(cc.x, cc.y), hi = make_uint2(cc.z, cc.w);
-          uint4 h0 = codes_to_half<FAST>(sw ? hi : lo, f), h1 = codes_to_half<FAST>(sw ? lo : hi, f);
-          if (check) bad |= drop_nonfinite<false>(h0) | drop_nonfinite<false>(h1);
-          *reinterpret_cast<uint4*>(d + p * RP * 128 + ((c0 ^ x) << 4)) = h0;
-          *reinterpret_cast<uint4*>(d + p * RP * 128 + ((c1 ^ x) << 4)) = h1;
+      int tiles = 0;                                             // before the item
+      each_item([&](const Item& it, int k, int t0, int t1) {
+        if (!pair && k > 0 && !wwait(kv_free, (k - 1) & 1)) return false;
+        const int n = it.n;
+        const int64_t trow = (int64_t)tab.seq[it.si] * pg.table_stride;
+        auto vector_of = [&](int key) -> int64_t {               // of a cached row's K, -1: none that a query sees
+          if (key >= it.all.end || (key < it.all.lo && key >= it.all.sk)) return -1;
+          const int id = pg.table[trow + (key >> pg.shift)];
+          if (id < 0 || id >= pg.n_pages) return -1;
+          return (((int64_t)id * pg.Hkv + it.g) << pg.shift) + (key & mask);
         };
-        if (fast) {
+        uint4 code[PN];                                          // of this warp's rows of its plane's next tile
+        int64_t vec = -1, vec_next = -1;                         // vector of row `lane` in tile t + 1, and in the one behind it
+        int64_t q4[4], q4_next[4];                               // the K vectors of rows lane, lane + 32, .. of those tiles
+        float sk4[4], sv4[4];                                    // their scales, of tile t + 1
+        int run_v = NO_BOUND;
+        auto lookup = [&](int t) {
+          const int j0 = t < n ? it.tile(t) : 0;
 #pragma unroll
-          for (int p = 0; p < PN; ++p) convert(std::true_type{}, code[p], p);
-        } else {                               // (rare: reads the codes again, one pass at a time)
+          for (int i = 0; i < 4; ++i) q4_next[i] = t < n ? vector_of(j0 + 32 * i + lane) : -1;
+          vec_next = lw == 0 ? q4_next[0] : lw == 1 ? q4_next[1] : lw == 2 ? q4_next[2] : q4_next[3];
+          if (plane && vec_next >= 0) vec_next += to_v;
+        };
+        auto read = [&](int64_t v, int p) {
+          const int64_t w = __shfl_sync(0xffffffffu, v, p * RP + lane / LPR);
+          return w >= 0 ? __ldg(reinterpret_cast<const uint4*>((const uint8_t*)pg.data + w * HD) + ci) : make_uint4(0, 0, 0, 0);
+        };
+        auto fetch = [&]() {                                     // scales and codes of the tile that lookup found
+          vec = vec_next;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            q4[i] = q4_next[i];
+            sk4[i] = plane == 0 && q4[i] >= 0 ? __ldg(pg.scales + q4[i]) : 0.f;
+            sv4[i] = q4[i] >= 0 ? __ldg(pg.scales + q4[i] + to_v) : 0.f;
+          }
+#pragma unroll
+          for (int p = 0; p < PN; ++p) code[p] = read(vec, p);
+        };
+        lookup(0);
+        if (n > 0) fetch();
+        lookup(1);
+        for (int t = 0; t < n; ++t) {
+          const Slot ks = slot(t, plane == 1, t0, t1);
+          // exponent bounds: of the tile's K scales, and the running one of V's (both planes' warps follow it)
+          int bk = NO_BOUND, bv = NO_BOUND;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            bk = max(bk, bound_of(sk4[i]));
+            bv = max(bv, bound_of(sv4[i]));
+          }
+          bk = __reduce_max_sync(0xffffffffu, bk);
+          run_v = max(run_v, __reduce_max_sync(0xffffffffu, bv));
+          if (bk == NO_BOUND) bk = 0;
+          const int E = plane ? (run_v == NO_BOUND ? 0 : run_v) : bk;
+          const float mine = plane ? (lw == 0 ? sv4[0] : lw == 1 ? sv4[1] : lw == 2 ? sv4[2] : sv4[3])
+                                   : (lw == 0 ? sk4[0] : lw == 1 ? sk4[1] : lw == 2 ? sk4[2] : sk4[3]);
+          const float fac = ldexpf(mine, 7 - E);                 // below 2^7
+          if (!wwait(&empty[ks.s], ks.ph ^ 1)) return false;
+          uint8_t* dst = kvst + ks.s * L::TILE;
+          const bool fast = __all_sync(0xffffffffu, __half2float(__float2half_rn(fac)) == fac);
+          const bool check = plane && it.partly(it.tile(t), a.window, a.sinks);
+          uint8_t* d = dst + (ci >> 2) * (BKV * 128) + (lw * 32 + lane / LPR) * 128;
+          bool bad = false;
+          auto convert = [&](auto is_fast, const uint4 cc, int p) {
+            constexpr bool FAST = decltype(is_fast)::value;
+            const float f = __shfl_sync(0xffffffffu, fac, p * RP + lane / LPR);
+            const int x = (p * RP + lane / LPR) & 7;
+            const uint2 lo = make_uint2(cc.x, cc.y), hi = make_uint2(cc.z, cc.w);
+            uint4 h0 = codes_to_half<FAST>(sw ? hi : lo, f), h1 = codes_to_half<FAST>(sw ? lo : hi, f);
+            if (check) bad |= drop_nonfinite<false>(h0) | drop_nonfinite<false>(h1);
+            *reinterpret_cast<uint4*>(d + p * RP * 128 + ((c0 ^ x) << 4)) = h0;
+            *reinterpret_cast<uint4*>(d + p * RP * 128 + ((c1 ^ x) << 4)) = h1;
+          };
+          if (fast) {
+#pragma unroll
+            for (int p = 0; p < PN; ++p) convert(std::true_type{}, code[p], p);
+          } else {                               // (rare: reads the codes again, one pass at a time)
 #pragma unroll 1
-          for (int p = 0; p < PN; ++p) convert(std::false_type{}, read(vec, p), p);
+            for (int p = 0; p < PN; ++p) convert(std::false_type{}, read(vec, p), p);
+          }
+          if (bad) *v_flag = 1;
+          if (plane == 0 && lw == 0 && lane == 0) {
+            base_k[(tiles + t) % BASES] = bk;
+            base_v[(tiles + t) % BASES] = run_v == NO_BOUND ? 0 : run_v;
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(plane ? &vfull[ks.s] : &full[ks.s]);
+          if (t + 1 < n) {
+            fetch();
+            lookup(t + 2);
+          }
         }
-        if (bad) *v_flag = 1;
-        if (plane == 0 && lw == 0 && lane == 0) {
-          base_k[t % BASES] = bk;
-          base_v[t % BASES] = run_v == NO_BOUND ? 0 : run_v;
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(plane ? &vfull[k.s] : &full[k.s]);
-        if (t + 1 < n) {
-          fetch();
-          lookup(t + 2);
-        }
-      }
+        tiles += n;
+        return true;
+      });
     }
   } else {
     // ---- softmax of stream x: row r = TMEM lane r
     const int x = (warp - 2) >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;
-    const int q0 = v0 + (two && x ? pl.RT : 0);          // the tile's first row of the sequence
-    const int vq = q0 + r / pl.G;                        // this row's
-    const bool live = r < pl.RT * pl.G && vq < v1 && vq < q0 + pl.RT;
-    const int h = g * pl.G + r % pl.G;
-    const int64_t row = live ? (int64_t)tab.row0[si] + vq : -1;        // row of q and out
-    const int pos = live ? tab.pos0[si] + vq : p_last;   // (rows that are not there: any, nothing reads them)
-    const int row_lo = a.window && pos - (a.window - 1) > 0 ? pos - (a.window - 1) : 0;
-    const bool idle = quad >= quads(x);                  // no live row: nothing to do past Q's zeros
-    float* qsc = (float*)(sm + L::QSC) + (two && x ? BQ : 0);
-    wait_prerequisites();
-    {   // Q rows of the quadrant; absent rows are zeros. One tile: each stream loads half of the rows
-      constexpr int CH = HD / 8;
-      const int64_t off = live ? row * a.q_stride + (int64_t)h * HD : -1;
-      uint8_t* dst = sm + L::Q + (two && x ? BQ * HD * 2 : 0);
-      auto load = [&](auto count, int first) {           // `count` of the CH passes over 32 rows x CH chunks
-        constexpr int PN = decltype(count)::value;
-        uint4 v[PN];
-#pragma unroll
-        for (int p = 0; p < PN; ++p) {
-          const int e = (first + p) * 32 + lane;
-          const int64_t o = __shfl_sync(0xffffffffu, off, e / CH);
-          v[p] = o >= 0 ? __ldg(reinterpret_cast<const uint4*>((const uint16_t*)a.q + o) + e % CH) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int p = 0; p < PN; ++p) {
-          const int e = (first + p) * 32 + lane, rr = quad * 32 + e / CH, c = e % CH;
-          if constexpr (KIND == E4M3_QBF) {              // to f16, the row's largest element near 2^14
-            uint32_t top = 0;
-            uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
-#pragma unroll
-            for (int o = CH / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int E = min(max((int)(top >> 7) - 127, -100), 127);
-            const float up = __uint_as_float((uint32_t)(14 - E + 127) << 23);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = h2u(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
-            v[p] = make_uint4(w[0], w[1], w[2], w[3]);
-            if (c == 0) qsc[rr] = __uint_as_float((uint32_t)(E - 14 + 127) << 23);
-          }
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * (BQ * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v[p];
-        }
-      };
-      if (two) load(std::integral_constant<int, CH>{}, 0);
-      else load(std::integral_constant<int, CH / 2>{}, x * (CH / 2));
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-    }
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t tS = tmem + lane_off + x * 128, tO = tmem + lane_off + T_O + x * 128;
-    float sl2 = a.scale * 1.4426950408889634f;
-    float m = -INFINITY;                       // the row's base
-    uint64_t l2 = 0;                           // the row's sum, two partial sums
-    bool ok = true;
-    int li = 0;                                // half tiles this stream has taken
-    int unit = 0;                              // e4m3: O counts 2^(unit - 7)
-    if constexpr (KIND == E4M3_QBF) {          // (all rows' factors: the two streams may have loaded half each)
-      if (n > 0) ok = wwait(q_full, 0);
-      sl2 *= qsc[r];
-    }
-    for (int t = two ? 0 : x; t < n && ok && !idle; t += (li & 1) ? 0 : two ? 1 : 2) {
-      const int hh = li & 1, ph = (li >> 1) & 1;
-      if (!wwait(&s_full[2 * x + hh], ph)) { ok = false; break; }
-      ++li;
-      fence_after();
-      uint32_t u[64];
-      tld32(tS + hh * 64, u);
-      tld32(tS + hh * 64 + 32, u + 32);
-      // visible keys of this half: columns lo .. hi, and those below sk
-      const int base_j = tl.at(jb + t) * BKV + hh * 64;
-      const int lo = row_lo - base_j, hi = pos - base_j, sk = a.sinks - base_j;
-      float zs = sl2;
-      int unit_now = unit;
-      if constexpr (E4) {
-        zs *= pow2f(base_k[t % BASES] - 7);
-        unit_now = base_v[t % BASES];
-      }
-      ld_wait();
-      pin32(u);
-      pin32(u + 32);
-      if (!__all_sync(0xffffffffu, (lo <= 0 || sk >= 64) && hi >= 63)) {   // some row does not see all keys: -inf for the hidden
-        auto upto = [](int c) { return c <= 0 ? 0ull : c >= 64 ? ~0ull : ~0ull >> (64 - c); };   // columns below c
-        const uint64_t seen = upto(hi + 1) & (~upto(lo) | upto(sk));
-#pragma unroll
-        for (int e = 0; e < 64; ++e)
-          if (!((e < 32 ? (uint32_t)seen : (uint32_t)(seen >> 32)) & (1u << (e & 31)))) u[e] = 0xff800000u;
-      }
-      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int k = 0; k < 64; k += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mx4[e] = fmaxf(mx4[e], fmaxf(__uint_as_float(u[k + e]), __uint_as_float(u[k + 4 + e])));
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * zs;
-      float alpha = 1.f;
-      if (mx - m > TOP) {
-        const float to = fabsf(mx) < FAR ? mx - HEAD : mx;
-        alpha = m == -INFINITY ? 1.f : ex2(m - to);
-        m = to;
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-      const bool moved = E4 && unit_now != unit;
-      if (li > 1 && (moved || __any_sync(0xffffffffu, alpha != 1.f))) {   // once the last P V has completed
-        if (!wwait(&o_step[2 * x + (hh ^ 1)], ((li - 2) >> 1) & 1)) { ok = false; break; }
-        fence_after();
-        const float beta = moved ? alpha * pow2f(unit - unit_now) : alpha;
-        uint32_t w[16];
-#pragma unroll 1
-        for (int c = 0; c < HD; c += 16) {
-          tld16(tO + c, w);
-          ld_wait();
-          pin<16>(w);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * beta);
-          tst16(tO + c, w);
-        }
-        l2 = mul2(l2, pack2(alpha, alpha));
-      }
-      unit = unit_now;
-      const uint64_t nb = pack2(-base, -base), zs2 = pack2(zs, zs);
-      uint64_t sum2 = 0;                       // (of this half: one by one, small weights would not reach a large sum)
-#pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const uint64_t z = fma2(pack2u(u[c + e], u[c + e + 1]), zs2, nb);
-          const float p0 = ex2(lo2(z)), p1 = ex2(hi2(z));
-          sum2 = add2(sum2, pack2(p0, p1));
-          pk[e / 2] = pack_w<PBF>(p0, p1);
-        }
-        tst16(tS + hh * 64 + c / 2, pk);
-      }
-      l2 = add2(l2, sum2);
-      st_wait();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[2 * x + hh]);
-    }
-    // ---- epilogue
-    float l = lo2(l2) + hi2(l2);
-    if (ok && li > 0) ok = wwait(&o_done[x], 0);
-    fence_after();
-    const float scale_o = E4 ? pow2f(unit - 7) : 1.f;
-    auto sums = [&](int c, float* o) {         // 32 columns of this row's sums (zeros without a tile)
-      uint32_t w[32];
-      __syncwarp();
-      if (li > 0) {
-        tld32(tO + c, w);
-        ld_wait();
-        pin32(w);
-      }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = li > 0 ? __uint_as_float(w[e]) * scale_o : 0.f;
-    };
+    float* qsc = (float*)(sm + L::QSC) + (pair && x ? BQ : 0);
     float* pub = reinterpret_cast<float*>(kvst) + r * L::OSTR;
-    float w0 = 1.f, w1 = 0.f;                  // weights of the two streams' sums
-    if (!two && x == 1 && !idle) {
-      // publish (o, m, l) in the K/V stages once stream 0 has read its last tile from them
-      if (ok && n > 0) ok = wwait(&o_done[0], 0);
-      if (ok) {
-        float o[32];
-#pragma unroll 1
-        for (int c = 0; c < HD; c += 32) {
-          sums(c, o);
+    int tiles = 0, dn0 = 0, dn1 = 0;           // before the item: key tiles, and o_done phases of the two streams
+    wait_prerequisites();
+    each_item([&](const Item& first_look, int k, int t0, int t1) {
+      Item it = first_look;
+      const int n = it.n, before = x ? t1 : t0;
+      struct Row {
+        bool live, idle;       // idle: the warp's quadrant of 32 matrix rows is past the tile's last; it only keeps the barriers going
+        int h, pos, lo;        // q head, position and the window's first key
+        int64_t at;            // row of q and out
+      };
+      auto row_of = [&](const Item& i) {
+        Row w;
+        const int q0 = i.v0 + (pair && x ? pl.RT : 0);     // the tile's first row of the sequence
+        const int vq = q0 + r / pl.G;                      // this row's
+        w.live = r < pl.RT * pl.G && vq < i.v1 && vq < q0 + pl.RT;
+        w.idle = quad * 32 >= (min(i.v1, q0 + pl.RT) - q0) * pl.G;
+        w.h = i.g * pl.G + r % pl.G;
+        w.at = (int64_t)tab.row0[i.si] + vq;
+        w.pos = w.live ? tab.pos0[i.si] + vq : i.p_last;   // (rows that are not there: any, nothing reads them)
+        w.lo = a.window && w.pos - (a.window - 1) > 0 ? w.pos - (a.window - 1) : 0;
+        return w;
+      };
+      Row rw = row_of(it);
+      const bool idle = rw.idle, none = pair && x && !it.two;   // none: no second tile at all
+      const int pos = rw.pos, row_lo = rw.lo;
+      float sl2 = a.scale * 1.4426950408889634f;
+      if constexpr (!QTMA) {   // bf16 Q rows of the quadrant to f16; absent rows are zeros. One tile: each stream half of the rows
+        constexpr int CH = HD / 8;
+        if (!wwait(q_empty, (k & 1) ^ 1)) return false;
+        const int64_t off = rw.live ? rw.at * a.q_stride + (int64_t)rw.h * HD : -1;
+        uint8_t* dst = sm + L::Q + (pair && x ? BQ * HD * 2 : 0);
+        const int first = pair ? 0 : x * (CH / 2), count = pair ? CH : CH / 2;
+#pragma unroll 2
+        for (int p = first; p < first + count; ++p) {      // 32 rows x CH chunks
+          const int e = p * 32 + lane, rr = quad * 32 + e / CH, c = e % CH;
+          const int64_t o = __shfl_sync(0xffffffffu, off, e / CH);
+          const uint4 v = o >= 0 ? __ldg(reinterpret_cast<const uint4*>((const uint16_t*)a.q + o) + c) : make_uint4(0, 0, 0, 0);
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t top = 0;                                // the row's largest element near 2^14
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(pub + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
+#pragma unroll
+          for (int s = CH / 2; s > 0; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
+          const int E = min(max((int)(top >> 7) - 127, -100), 127);
+          const float up = __uint_as_float((uint32_t)(14 - E + 127) << 23);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = h2u(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
+          if (c == 0) qsc[rr] = __uint_as_float((uint32_t)(E - 14 + 127) << 23);
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * (BQ * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
         }
-        *reinterpret_cast<float2*>(pub + HD) = make_float2(m, l);
+        fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&joined[quad]);
+        if (lane == 0) mbar_arrive(q_full);
+        if (!wwait(q_full, k & 1)) return false;           // (the two streams may have loaded half of the rows each)
+        sl2 *= qsc[r];
       }
-    } else if (!idle) {
-      if (!two && ok) {
-        ok = wwait(&joined[quad], 0);
-        if (ok) {
+      float m = -INFINITY;                       // the row's base
+      uint64_t l2 = 0;                           // the row's sum, two partial sums
+      int li = 0;                                // half tiles this stream has taken
+      int unit = 0;                              // e4m3: O counts 2^(unit - 7)
+      for (int t = pair ? 0 : x; t < n && !none; t += (li & 1) ? 0 : pair ? 1 : 2) {
+        const int hh = li & 1, ph = (before + (li >> 1)) & 1;
+        if (!wwait(&s_full[2 * x + hh], ph)) return false;
+        ++li;
+        if (idle) {
+          if (lane == 0) mbar_arrive(&p_full[2 * x + hh]);
+          continue;
+        }
+        fence_after();
+        uint32_t u[64];
+        tld32(tS + hh * 64, u);
+        tld32(tS + hh * 64 + 32, u + 32);
+        // visible keys of this half: columns lo .. hi, and those below sk
+        const int base_j = it.tile(t) + hh * 64;
+        const int lo = row_lo - base_j, hi = pos - base_j, sk = a.sinks - base_j;
+        float zs = sl2;
+        int unit_now = unit;
+        if constexpr (E4) {
+          zs *= pow2f(base_k[(tiles + t) % BASES] - 7);
+          unit_now = base_v[(tiles + t) % BASES];
+        }
+        ld_wait();
+        pin32(u);
+        pin32(u + 32);
+        if (!__all_sync(0xffffffffu, (lo <= 0 || sk >= 64) && hi >= 63)) {   // some row does not see all keys: -inf for the hidden
+          auto upto = [](int c) { return c <= 0 ? 0ull : c >= 64 ? ~0ull : ~0ull >> (64 - c); };   // columns below c
+          const uint64_t seen = upto(hi + 1) & (~upto(lo) | upto(sk));
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (!((e < 32 ? (uint32_t)seen : (uint32_t)(seen >> 32)) & (1u << (e & 31)))) u[e] = 0xff800000u;
+        }
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k8 = 0; k8 < 64; k8 += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx4[e] = fmaxf(mx4[e], fmaxf(__uint_as_float(u[k8 + e]), __uint_as_float(u[k8 + 4 + e])));
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * zs;
+        float alpha = 1.f;
+        if (mx - m > TOP) {
+          const float to = fabsf(mx) < FAR ? mx - HEAD : mx;
+          alpha = m == -INFINITY ? 1.f : ex2(m - to);
+          m = to;
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        const bool moved = E4 && unit_now != unit;
+        if (li > 1 && (moved || __any_sync(0xffffffffu, alpha != 1.f))) {   // once the last P V has completed
+          if (!wwait(&o_step[2 * x + (hh ^ 1)], (before + ((li - 2) >> 1)) & 1)) return false;
+          fence_after();
+          const float beta = moved ? alpha * pow2f(unit - unit_now) : alpha;
+          uint32_t w[16];
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 16) {
+            tld16(tO + c, w);
+            ld_wait();
+            pin<16>(w);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * beta);
+            tst16(tO + c, w);
+          }
+          l2 = mul2(l2, pack2(alpha, alpha));
+        }
+        unit = unit_now;
+        const uint64_t nb = pack2(-base, -base), zs2 = pack2(zs, zs);
+        uint64_t sum2 = 0;                       // (of this half: one by one, small weights would not reach a large sum)
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const uint64_t z = fma2(pack2u(u[c + e], u[c + e + 1]), zs2, nb);
+            const float p0 = ex2(lo2(z)), p1 = ex2(hi2(z));
+            sum2 = add2(sum2, pack2(p0, p1));
+            pk[e / 2] = pack_w<PBF>(p0, p1);
+          }
+          tst16(tS + hh * 64 + c / 2, pk);
+        }
+        l2 = add2(l2, sum2);
+        st_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * x + hh]);
+      }
+      // ---- the item's end (what the loop did not need is made again: registers). Its sums stay in TMEM until the next item's first weights are announced
+      int w_again = it.w;
+      asm volatile("" : "+r"(w_again));
+      it = item_of(tab, a, pl, w_again);
+      rw = row_of(it);
+      float l = lo2(l2) + hi2(l2);
+      if (li > 0 && !wwait(&o_done[x], (x ? dn1 : dn0) & 1)) return false;
+      fence_after();
+      const float scale_o = E4 ? pow2f(unit - 7) : 1.f;
+      float w0 = 1.f, w1 = 0.f;                  // weights of the two streams' sums
+      const bool publish = !pair && x == 1;      // (o, m, l) into the K/V stages, for stream 0
+      if (publish) {                             // once stream 0 has read its last tile from them, and the sums of the item before
+        if (n > 0 && !wwait(&o_done[0], dn0 & 1)) return false;
+        if (k > 0 && !wwait(kv_free, (k - 1) & 1)) return false;
+      } else if (!pair) {
+        if (!wwait(&joined[quad], k & 1)) return false;
+        if (!idle) {
           const float2 ml = *reinterpret_cast<const float2*>(pub + HD);
           const bool has0 = !(m == -INFINITY && l == 0.f), has1 = !(ml.x == -INFINITY && ml.y == 0.f);
           const float M = fmaxf(m, ml.x);
@@ -671,113 +809,79 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
           m = M;
         }
       }
-      if (ok) {
+      if (!idle && !none) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const bool fix = live && *v_flag;      // non-finite values of partly hidden tiles: into the rows that see them
-        const int64_t pi = (int64_t)blockIdx.x * 2 + (two ? x : 0);
-        uint8_t* ostage = sm + L::Q + (two && x ? BQ * HD * 2 : 0);
+        const bool fix = rw.live && !publish && *v_flag;   // non-finite values of partly hidden tiles: into the rows that see them
+        const int64_t pi = (int64_t)it.w * 2 + (pair ? x : 0);
 #pragma unroll 1
-        for (int c = 0; c < HD; c += 32) {
-          float o[32];
-          sums(c, o);
-          if (!two) {
+        for (int c = 0; c < HD; c += 32) {       // (zeros without a tile)
+          uint32_t u[32];
+          if (li > 0) {
+            tld32(tO + c, u);
+            ld_wait();
+            pin32(u);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) u[e] = li > 0 ? __float_as_uint(__uint_as_float(u[e]) * scale_o) : 0u;
+          float4* at = reinterpret_cast<float4*>(pub + c);
+          if (publish) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) at[e / 4] = make_float4(__uint_as_float(u[e]), __uint_as_float(u[e + 1]), __uint_as_float(u[e + 2]), __uint_as_float(u[e + 3]));
+            continue;
+          }
+          if (!pair) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float4 y = *reinterpret_cast<const float4*>(pub + c + e);
-              o[e] = (w0 != 0.f ? w0 * o[e] : 0.f) + (w1 != 0.f ? w1 * y.x : 0.f);
-              o[e + 1] = (w0 != 0.f ? w0 * o[e + 1] : 0.f) + (w1 != 0.f ? w1 * y.y : 0.f);
-              o[e + 2] = (w0 != 0.f ? w0 * o[e + 2] : 0.f) + (w1 != 0.f ? w1 * y.z : 0.f);
-              o[e + 3] = (w0 != 0.f ? w0 * o[e + 3] : 0.f) + (w1 != 0.f ? w1 * y.w : 0.f);
+              const float4 y = at[e / 4];
+              u[e] = __float_as_uint((w0 != 0.f ? w0 * __uint_as_float(u[e]) : 0.f) + (w1 != 0.f ? w1 * y.x : 0.f));
+              u[e + 1] = __float_as_uint((w0 != 0.f ? w0 * __uint_as_float(u[e + 1]) : 0.f) + (w1 != 0.f ? w1 * y.y : 0.f));
+              u[e + 2] = __float_as_uint((w0 != 0.f ? w0 * __uint_as_float(u[e + 2]) : 0.f) + (w1 != 0.f ? w1 * y.z : 0.f));
+              u[e + 3] = __float_as_uint((w0 != 0.f ? w0 * __uint_as_float(u[e + 3]) : 0.f) + (w1 != 0.f ? w1 * y.w : 0.f));
             }
           }
-          if (fix)
-            for (int t = 0; t < n; ++t) {
-              const int j0 = tl.at(jb + t) * BKV;
-              if (!partly(j0)) continue;
-              for (int j = j0; j < j0 + BKV && j <= pos; ++j) {
-                if (j < row_lo && j >= a.sinks) continue;
-                const int id = pg.table[(int64_t)tab.seq[si] * pg.table_stride + (j >> pg.shift)];
-                if (id < 0 || id >= pg.n_pages) continue;
-                const int64_t vec = (((pg.n_pages + (int64_t)id) * pg.Hkv + g) << pg.shift) + (j & ((1 << pg.shift) - 1));
-                if constexpr (E4) {
+          if (fix) add_nonfinite<E4, PBF>(it, a, tab.seq[it.si], rw.pos, rw.lo, c, u);
+          if (it.ns == 1) {
+            if (rw.live) {
+              uint4* dst = reinterpret_cast<uint4*>((uint16_t*)a.out + (rw.at * a.Hq + rw.h) * HD + c);
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) {
-                    const float y = __half2float(__half(__nv_cvt_fp8_to_halfraw(
-                                        ((const __nv_fp8_storage_t*)pg.data)[vec * HD + c + e], __NV_E4M3))) *
-                                    pg.scales[vec];
-                    if (!isfinite(y)) o[e] += y;
-                  }
-                } else {
-                  const uint4* at = reinterpret_cast<const uint4*>((const uint16_t*)pg.data + vec * HD + c);
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const uint4 y = at[e];
-                    const uint32_t y4[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                      if (nonfinite2<PBF>(y4[i])) {
-                        float f[2];
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                          const uint16_t raw = (uint16_t)(y4[i] >> (16 * z));
-                          f[z] = PBF ? __uint_as_float((uint32_t)raw << 16) : __half2float(__ushort_as_half(raw));
-                          if (!isfinite(f[z])) o[8 * e + 2 * i + z] += f[z];
-                        }
-                      }
-                  }
-                }
-              }
+              for (int e = 0; e < 32; e += 8)
+                dst[e / 8] = make_uint4(pack_w<OBF>(__uint_as_float(u[e]) * inv, __uint_as_float(u[e + 1]) * inv), pack_w<OBF>(__uint_as_float(u[e + 2]) * inv, __uint_as_float(u[e + 3]) * inv),
+                                        pack_w<OBF>(__uint_as_float(u[e + 4]) * inv, __uint_as_float(u[e + 5]) * inv),
+                                        pack_w<OBF>(__uint_as_float(u[e + 6]) * inv, __uint_as_float(u[e + 7]) * inv));
             }
-          if (ns == 1) {                       // 16-bit row into the (consumed) Q tile, chunks swizzled
-            uint8_t* dst = ostage + r * (HD * 2);
+          } else {                               // [HD / 4][32 rows] groups of 4 sums
+            float4* dst = reinterpret_cast<float4*>(a.ws) + ((pi * 4 + quad) * (HD / 4) + c / 4) * 32 + lane;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(dst + ((((c + e) / 8) ^ (r & 7)) << 4)) = make_uint4(
-                  pack_w<OBF>(o[e] * inv, o[e + 1] * inv), pack_w<OBF>(o[e + 2] * inv, o[e + 3] * inv),
-                  pack_w<OBF>(o[e + 4] * inv, o[e + 5] * inv), pack_w<OBF>(o[e + 6] * inv, o[e + 7] * inv));
-          } else {                             // the warp's [HD / 8][32] groups of 4 sums, half of the columns at a time
-            float4* stage = reinterpret_cast<float4*>(ostage + quad * (HD * 64));
-            const int half = HD / 2, cc = c % half;
-            if (c == half) {                   // the first half is out of the stage
-              if (lane == 0) tma_store_read_wait();
-              __syncwarp();
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              stage[(cc + e) / 4 * 32 + lane] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            if (cc + 32 == half) {
-              fence_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                bulk_store((float*)a.ws + ((pi * 4 + quad) * HD + c + 32 - half) * 32, stage, HD * 64);
-                tma_store_commit();
-              }
-            }
+            for (int e = 0; e < 32; e += 4) dst[e / 4 * 32] = make_float4(__uint_as_float(u[e]), __uint_as_float(u[e + 1]), __uint_as_float(u[e + 2]), __uint_as_float(u[e + 3]));
           }
         }
-        if (ns == 1) {                         // whole rows out of the warp's stage
-          __syncwarp();
-          constexpr int CH = HD / 8;
-          const int64_t off = live ? (row * a.Hq + h) * HD : -1;
-#pragma unroll
-          for (int p = 0; p < CH; ++p) {
-            const int e = p * 32 + lane, rr = quad * 32 + e / CH, c = e % CH;
-            const int64_t o = __shfl_sync(0xffffffffu, off, e / CH);
-            if (o >= 0)
-              *reinterpret_cast<uint4*>((uint16_t*)a.out + o + c * 8) =
-                  *reinterpret_cast<const uint4*>(ostage + rr * (HD * 2) + ((c ^ (rr & 7)) << 4));
-          }
-        }
-        if (ns > 1 && lane == 0) tma_store_wait();
-        if (live && ns > 1)
+        if (publish) *reinterpret_cast<float2*>(pub + HD) = make_float2(m, l);
+        else if (rw.live && it.ns > 1)
           reinterpret_cast<float2*>((float*)a.ws + (int64_t)tab.split * 2 * BQ * HD)[pi * BQ + r] = make_float2(m, l);
       }
-    }
+      if (publish) {
+        fence_async_smem();                      // (TMA tiles follow these writes)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&joined[quad]);
+      }
+      if (!pair && x == 0) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kv_free);
+      }
+      fence_before();                            // (the reads of O come before the next item's products)
+      tiles += n;
+      dn0 += pair ? n > 0 : n > 0;
+      dn1 += pair ? n > 0 && it.two : n > 1;
+      return true;
+    });
   }
   __syncthreads();
-  if (warp == 0 && *abort_flag)                // nothing in flight when the CTA leaves
+  if (warp == 0 && *abort_flag) {              // nothing in flight when the CTA leaves
+    if (q_done) mbar_drain(q_full, (q_done - 1) & 1);
     for (int d = 0; d < 2 * NS; ++d)
       if ((done >> d) & 1) mbar_drain(d & 1 ? &vfull[d >> 1] : &full[d >> 1], (done >> (16 + d)) & 1);
+  }
   if (warp == 1) {
     fence_after();
     tmem_free<TMEM_COLS>(tmem);
@@ -878,11 +982,12 @@ int item_tiles(int pos0, int v0, int v1, int window, int sinks) {
 }
 
 // One launch: sequences s0 .. (empty ones left out) with one or two query tiles an item and, per sequence, the parts that an
-// item's key tiles are split into: the choice with the least estimated time (us, the constants measured for the kernels
-// that share this structure): a key tile takes 1.13 us with two query tiles and 0.66 with one, a CTA 4.5 besides, the join
-// 2.8 and its sums; CTAs fill the SMs as they come, the longest first. An item is split into parts of `per` key
-// tiles; at most 64 parts, and parts of at most LONGEST tiles (the tensor cores add to one sum per output and drop what lies
-// below its last bits).
+// item's key tiles are split into: the choice with the least estimated time (us, measured): a key tile takes 1.13 us with two
+// query tiles and 0.66 with one, an item ITEM besides and a CTA's start and end 6, the join 2.8 and its sums. CTAs take the
+// items in rounds: as many as there are rounds of average ones, or an even share and a third of the longest where lengths
+// differ. An item is split into parts of `per` key tiles; at most 64 parts, and parts of at most LONGEST tiles (the
+// tensor cores add to one sum per output and drop what lies below its last bits).
+constexpr double ITEM = 3.0;
 constexpr int LONGEST = 1024;
 struct Group {
   Plan pl;
@@ -942,10 +1047,11 @@ void plan_group(Group& gr, int s0, int n_seq, const int* row0, const int* len, c
         const int64_t n = q.items[k] * Hkv * ns;
         ctas += n;
         if (ns > 1) joined += n;
-        cost += c * (double)(q.sum[k] * Hkv) + 4.5 * (double)n;
-        top = std::max(top, c * ((q.top[k] + ns - 1) / ns) + 4.5);
+        cost += c * (double)(q.sum[k] * Hkv) + ITEM * (double)n;
+        top = std::max(top, c * ((q.top[k] + ns - 1) / ns) + ITEM);
       }
-      double time = ctas <= num_sms ? top : std::max(top, cost / num_sms + 0.5 * top);
+      const double rounds = (double)((ctas + num_sms - 1) / num_sms), mean = cost / (double)ctas;
+      double time = 6 + (ctas <= num_sms ? top : std::max(rounds * mean, cost / num_sms + 0.33 * (top - mean)));
       if (joined) time += 2.8 + 0.00006 * (double)(joined * (k + 1) * hd);
       if (best < 0 || time < best) {
         best = time;
@@ -981,22 +1087,33 @@ void plan_group(Group& gr, int s0, int n_seq, const int* row0, const int* len, c
 
 template <int HD, int KIND, int N>
 cudaError_t launch_tab(const PagedAttnArgs& a, const Tab<N>& tab, const Plan& pl, int max_ns, const CUtensorMap& map,
-                       cudaStream_t st) {
+                       int num_sms, cudaStream_t st) {
   using L = Lay<HD>;
+  CUtensorMap map_q = {};
+  if (KIND != E4M3_QBF) {      // (hd, q heads, rows): a tile's rows x heads are one box
+    int rows = 0;
+    for (int i = 0; i < tab.n; ++i) rows = std::max(rows, tab.row0[i] + tab.len[i]);
+    const uint64_t dims[3] = {(uint64_t)HD, (uint64_t)a.Hq, (uint64_t)rows};
+    const uint64_t str[2] = {HD * 2, (uint64_t)a.q_stride * 2};
+    const uint32_t box[3] = {64, (uint32_t)pl.G, (uint32_t)pl.RT};
+    if (!encode_tensor_map(&map_q, KIND == BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, a.q,
+                           dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
   CK_RET(cudaFuncSetAttribute(paged_kernel<HD, KIND, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES));
-  CK_RET(launch_pdl(paged_kernel<HD, KIND, N>, dim3((unsigned)tab.start[tab.n]), dim3(threads_of(KIND)), L::BYTES, st, tab,
-                    map, a, pl));
+  CK_RET(launch_pdl(paged_kernel<HD, KIND, N>, dim3((unsigned)std::min(tab.start[tab.n], num_sms)), dim3(threads_of(KIND)),
+                    L::BYTES, st, tab, map, map_q, a, pl));
   if (max_ns > 1)
     CK_RET(launch_pdl(combine_kernel<HD, out_bf16(KIND), N>, dim3((unsigned)(tab.tiles[tab.n] * (HD / CCOLS * 4))),
                       dim3((unsigned)(32 * std::min(CWARPS, (max_ns + 1) / 2))), 0, st, tab, a, pl));
   return cudaSuccess;
 }
 template <int HD, int KIND>
-cudaError_t launch_group(const PagedAttnArgs& a, const Group& gr, cudaStream_t st) {
+cudaError_t launch_group(const PagedAttnArgs& a, const Group& gr, int num_sms, cudaStream_t st) {
   CUtensorMap map = {};
   if (!is_e4m3(KIND) && !pages_map(&map, a.pages, 1 << a.pages.shift)) return cudaErrorInvalidValue;
   const Tab<TAB_LARGE>& t = gr.tab;
-  if (t.n > TAB_SMALL) return launch_tab<HD, KIND, TAB_LARGE>(a, t, gr.pl, gr.max_ns, map, st);
+  if (t.n > TAB_SMALL) return launch_tab<HD, KIND, TAB_LARGE>(a, t, gr.pl, gr.max_ns, map, num_sms, st);
   Tab<TAB_SMALL> u;
   u.n = t.n;
   u.split = t.split;
@@ -1007,13 +1124,13 @@ cudaError_t launch_group(const PagedAttnArgs& a, const Group& gr, cudaStream_t s
   std::copy(t.len, t.len + t.n, u.len);
   std::copy(t.seq, t.seq + t.n, u.seq);
   std::copy(t.ns, t.ns + t.n, u.ns);
-  return launch_tab<HD, KIND, TAB_SMALL>(a, u, gr.pl, gr.max_ns, map, st);
+  return launch_tab<HD, KIND, TAB_SMALL>(a, u, gr.pl, gr.max_ns, map, num_sms, st);
 }
 template <int HD>
-cudaError_t launch_kind(const PagedAttnArgs& a, const Group& gr, cudaStream_t st) {
-  if (a.pages.format == KVF_F16) return launch_group<HD, F16>(a, gr, st);
-  if (a.pages.format == KVF_BF16) return launch_group<HD, BF16>(a, gr, st);
-  return a.bf16 ? launch_group<HD, E4M3_QBF>(a, gr, st) : launch_group<HD, E4M3>(a, gr, st);
+cudaError_t launch_kind(const PagedAttnArgs& a, const Group& gr, int num_sms, cudaStream_t st) {
+  if (a.pages.format == KVF_F16) return launch_group<HD, F16>(a, gr, num_sms, st);
+  if (a.pages.format == KVF_BF16) return launch_group<HD, BF16>(a, gr, num_sms, st);
+  return a.bf16 ? launch_group<HD, E4M3_QBF>(a, gr, num_sms, st) : launch_group<HD, E4M3>(a, gr, num_sms, st);
 }
 }  // namespace pgp
 
@@ -1038,7 +1155,7 @@ cudaError_t launch_attention_paged(const PagedAttnArgs& a, int n_seq, const int*
   for (int s = 0; s < n_seq; s = gr.next) {
     pgp::plan_group(gr, s, n_seq, row0, len, pos0, a.Hq, a.pages.Hkv, a.pages.hd, a.window, a.sinks, num_sms);
     if (gr.tab.n == 0) continue;
-    CK_RET(a.pages.hd == 128 ? pgp::launch_kind<128>(a, gr, st) : pgp::launch_kind<64>(a, gr, st));
+    CK_RET(a.pages.hd == 128 ? pgp::launch_kind<128>(a, gr, num_sms, st) : pgp::launch_kind<64>(a, gr, num_sms, st));
   }
   return cudaSuccess;
 }
