@@ -43,6 +43,7 @@ constexpr bool out_bf16(int kind) { return kind == BF16 || kind == E4M3_QBF; }
 constexpr int threads_of(int kind) { return (is_e4m3(kind) ? 19 : 15) * 32; }
 constexpr int TMEM_COLS = 512;               // S of stream x at 128 x, O at 256 + 128 x
 constexpr int T_O = 256;
+constexpr int ITEMS = 18;                    // of a CTA's items, kept in shared memory (later ones are made when their turn comes)
 constexpr int BASES = 16;                    // tiles whose exponent bounds are kept (more than are ever in flight)
 
 __device__ uint64_t g_given_up;              // when a bounded wait last gave up, per device; never cleared
@@ -68,7 +69,8 @@ struct Lay {
   static constexpr int KV1 = Q + BQ * HD * 2;             // with one
   static constexpr int QSC = KV2 + F * TILE;              // [2][128] floats: what a row's q was divided by
   static constexpr int BASE = QSC + 2 * BQ * 4;           // [2][BASES] exponent bounds
-  static constexpr int BAR = BASE + 2 * BASES * 4;
+  static constexpr int TABLE = BASE + 2 * BASES * 4;       // the CTA's first ITEMS items
+  static constexpr int BAR = TABLE + ITEMS * 64;
   static constexpr int NS = 2 * FR > F ? 2 * FR : F;
   static constexpr int NBAR = 3 + 4 * NS + 12 + 2 + 2 + 4;
   static constexpr int USED = BAR + NBAR * 8 + 16;
@@ -152,18 +154,18 @@ __device__ __forceinline__ int bound_of(float scale) {
 }
 
 // One of a CTA's items: (sequence, one or two query tiles, kv head) and a part of its key tiles.
-struct Item {
-  int w, si, g, ns, len;       // number in the list, sequence (of the table), kv head, the sequence's parts per item and rows
-  int v0, v1;                  // first row of the sequence, and one past its last
-  int p_first, p_last;         // positions of the first and the last row
-  bool two;                    // a second query tile
-  Seen all;                    // what some row sees
-  int n, head, sink0, tail0;   // the part's key tiles: t < head: sink0 + t, else tail0 + t
-  // a key tile, or row, that some query row does not see
-  __device__ bool partly(int j0, int window, int sinks) const {
-    return j0 + BKV - 1 > p_first || (window && p_last - j0 >= window && j0 + BKV > sinks);
-  }
+struct alignas(16) Item {
+  int w, ns, g, two;           // number in the list, parts of the sequence's items, kv head, whether there is a second query tile
+  int row0, seq, v0, v1;       // the sequence's first row of q, its row of the table; the item's first row and one past its last
+  int pos0, lo, sk, n;         // position of the sequence's first row; what some row sees: [0, sk) and [lo, end()); key tiles
+  int head, sink0, tail0, pad;   // tile t: t < head: sink0 + t, else tail0 + t
+  __device__ int p_first() const { return pos0 + v0; }
+  __device__ int end() const { return pos0 + v1; }
   __device__ int tile(int t) const { return (t + (t < head ? sink0 : tail0)) * BKV; }
+  // a key tile that some query row does not see in full
+  __device__ bool partly(int j0, int window, int sinks) const {
+    return j0 + BKV - 1 > p_first() || (window && end() - 1 - j0 >= window && j0 + BKV > sinks);
+  }
 };
 template <int N>
 __device__ __forceinline__ Item item_of(const Tab<N>& tab, const PagedAttnArgs& a, const Plan& pl, int w) {
@@ -174,34 +176,37 @@ __device__ __forceinline__ Item item_of(const Tab<N>& tab, const PagedAttnArgs& 
     if (tab.start[mid] <= w) si = mid;
     else hi = mid - 1;
   }
+  const int len = tab.len[si], MT = (len + pl.RT - 1) / pl.RT, MP = (MT + pl.nt - 1) / pl.nt;
   it.w = w;
-  it.si = si;
-  it.len = tab.len[si];
   it.ns = tab.ns[si];
-  const int MT = (it.len + pl.RT - 1) / pl.RT, MP = (MT + pl.nt - 1) / pl.nt;
+  it.row0 = tab.row0[si];
+  it.seq = tab.seq[si];
+  it.pos0 = tab.pos0[si];
   const int local = w - tab.start[si], part = local % it.ns, item = local / it.ns;
   it.g = item % a.pages.Hkv;
   const int mp = MP - 1 - item / a.pages.Hkv;      // (the last rows see most: first)
   it.two = pl.nt == 2 && 2 * mp + 1 < MT;
   it.v0 = pl.nt * mp * pl.RT;
-  it.v1 = min(it.len, it.v0 + (it.two ? 2 : 1) * pl.RT);
-  it.p_first = tab.pos0[si] + it.v0;
-  it.p_last = tab.pos0[si] + it.v1 - 1;
-  it.all.end = it.p_last + 1;
-  it.all.lo = a.window && it.p_first - (a.window - 1) > 0 ? it.p_first - (a.window - 1) : 0;
-  it.all.sk = min(a.sinks, it.all.lo);
-  const Tiles tl = tiles_of<BKV>(it.all);
+  it.v1 = min(len, it.v0 + (it.two ? 2 : 1) * pl.RT);
+  Seen all;
+  all.end = it.end();
+  all.lo = a.window && it.p_first() - (a.window - 1) > 0 ? it.p_first() - (a.window - 1) : 0;
+  all.sk = min(a.sinks, all.lo);
+  it.lo = all.lo;
+  it.sk = all.sk;
+  const Tiles tl = tiles_of<BKV>(all);
   const int total = tl.count(), per = (total + it.ns - 1) / it.ns, jb = min(total, part * per);
   it.n = min(total, jb + per) - jb;
   it.head = tl.head - jb;
   it.sink0 = jb;
   it.tail0 = tl.first - tl.head + jb;
+  it.pad = 0;
   return it;
 }
 
 // Adds the non-finite elements of columns c .. c + 31 of the partly hidden value rows that a query sees.
 template <bool E4, bool PBF>
-__device__ __forceinline__ void add_nonfinite(const Item& it, const PagedAttnArgs& a, int seq, int pos, int row_lo, int c,
+__device__ __forceinline__ void add_nonfinite(const Item& it, const PagedAttnArgs& a, int pos, int row_lo, int c,
                                               uint32_t* o) {
   const PagesArgs& pg = a.pages;
   auto add = [](uint32_t& x, float y) { x = __float_as_uint(__uint_as_float(x) + y); };
@@ -210,7 +215,7 @@ __device__ __forceinline__ void add_nonfinite(const Item& it, const PagedAttnArg
     if (!it.partly(j0, a.window, a.sinks)) continue;
     for (int j = j0; j < j0 + BKV && j <= pos; ++j) {
       if (j < row_lo && j >= a.sinks) continue;
-      const int id = pg.table[(int64_t)seq * pg.table_stride + (j >> pg.shift)];
+      const int id = pg.table[(int64_t)it.seq * pg.table_stride + (j >> pg.shift)];
       if (id < 0 || id >= pg.n_pages) continue;
       const int64_t vec = (((pg.n_pages + (int64_t)id) * pg.Hkv + it.g) << pg.shift) + (j & ((1 << pg.shift) - 1));
       if constexpr (E4) {
@@ -299,6 +304,13 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc<TMEM_COLS>(tmem_slot);
+  // every gridDim-th item of the list, there and back again, so that a list that grows cheaper stays even
+  const int listed = tab.start[tab.n];
+  auto number_of = [&](int k) { return k * (int)gridDim.x + (int)(k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x); };
+  const int rounds = (listed + (int)gridDim.x - 1) / (int)gridDim.x, items = rounds - (number_of(rounds - 1) >= listed ? 1 : 0);
+  Item* table = reinterpret_cast<Item*>(sm + L::TABLE);
+  if (threadIdx.x >= 64 && (int)threadIdx.x - 64 < min(items, ITEMS))
+    table[threadIdx.x - 64] = item_of(tab, a, pl, number_of((int)threadIdx.x - 64));
   allow_dependents();
   __syncthreads();
   fence_after();
@@ -307,20 +319,15 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
   auto wwait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_given_up) ? 1 : 0) != 0;
   };
-  // This CTA's items: every gridDim-th of the list, there and back again, so that a list that grows cheaper stays even.
-  // fn(item, its number, tiles before it of stream 0 and of stream 1) until it returns false.
+  // This CTA's items: fn(item, its number, tiles before it of stream 0 and of stream 1) until it returns false.
+  auto item_at = [&](int k) { return k < ITEMS ? table[k] : item_of(tab, a, pl, number_of(k)); };
   auto each_item = [&](auto&& fn) {
-    int t0 = 0, t1 = 0, k = 0;
-    for (int round = 0;; ++round) {
-      const int64_t w0 = (int64_t)round * gridDim.x;
-      if (w0 >= tab.start[tab.n]) break;
-      const int64_t w = w0 + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      if (w >= tab.start[tab.n]) continue;
-      const Item it = item_of(tab, a, pl, (int)w);
+    int t0 = 0, t1 = 0;
+    for (int k = 0; k < items; ++k) {
+      const Item it = item_at(k);
       if (!fn(it, k, t0, t1)) break;
       t0 += pair ? it.n : (it.n + 1) >> 1;
       t1 += pair ? (it.two ? it.n : 0) : it.n >> 1;
-      ++k;
     }
   };
   // an item's tile t in the ring: the stream whose ring it is (pair: 0), and its number there
@@ -353,13 +360,13 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         __syncwarp();
         if (lane < tiles * NB)
           tma3(sm + L::Q + (lane / NB) * (BQ * HD * 2) + (lane % NB) * (BQ * 128), &mapQ, q_full, 64 * (lane % NB), it.g * pl.G,
-               tab.row0[it.si] + it.v0 + (lane / NB) * pl.RT);
+               it.row0 + it.v0 + (lane / NB) * pl.RT);
         q_done = k + 1;
       }
       if constexpr (E4) return true;
       if (!pair && k > 0 && !wwait(kv_free, (k - 1) & 1)) return false;
-      const int last = (it.all.end - 1) >> pg.shift;
-      const int64_t trow = (int64_t)tab.seq[it.si] * pg.table_stride;
+      const int last = (it.end() - 1) >> pg.shift;
+      const int64_t trow = (int64_t)it.seq * pg.table_stride;
       auto page_id = [&](int t) {              // of this lane's part of tile t
         if (t >= it.n || pp >= npg) return -1;
         const int col = (it.tile(t) >> pg.shift) + pp;
@@ -510,7 +517,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
                 if (drop_nonfinite<PBF>(x)) {
                   *at(p) = x;
                   const int j = j0 + lw * 32 + p * RPI + lane / CH;   // (of rows that no query sees nobody asks for the values)
-                  bad |= j < it.all.end && (j >= it.all.lo || j < it.all.sk);
+                  bad |= j < it.end() && (j >= it.lo || j < it.sk);
                 }
               }
               if (bad) *v_flag = 1;
@@ -536,9 +543,9 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       each_item([&](const Item& it, int k, int t0, int t1) {
         if (!pair && k > 0 && !wwait(kv_free, (k - 1) & 1)) return false;
         const int n = it.n;
-        const int64_t trow = (int64_t)tab.seq[it.si] * pg.table_stride;
+        const int64_t trow = (int64_t)it.seq * pg.table_stride;
         auto vector_of = [&](int key) -> int64_t {               // of a cached row's K, -1: none that a query sees
-          if (key >= it.all.end || (key < it.all.lo && key >= it.all.sk)) return -1;
+          if (key >= it.end() || (key < it.lo && key >= it.sk)) return -1;
           const int id = pg.table[trow + (key >> pg.shift)];
           if (id < 0 || id >= pg.n_pages) return -1;
           return (((int64_t)id * pg.Hkv + it.g) << pg.shift) + (key & mask);
@@ -632,30 +639,28 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
   } else {
     // ---- softmax of stream x: row r = TMEM lane r
     const int x = (warp - 2) >> 2, quad = warp & 3;
-    const int r = quad * 32 + lane;
+    const int r = quad * 32 + lane, r_row = r / pl.G, r_head = r % pl.G;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t tS = tmem + lane_off + x * 128, tO = tmem + lane_off + T_O + x * 128;
     float* qsc = (float*)(sm + L::QSC) + (pair && x ? BQ : 0);
     float* pub = reinterpret_cast<float*>(kvst) + r * L::OSTR;
     int tiles = 0, dn0 = 0, dn1 = 0;           // before the item: key tiles, and o_done phases of the two streams
     wait_prerequisites();
-    each_item([&](const Item& first_look, int k, int t0, int t1) {
-      Item it = first_look;
+    each_item([&](const Item& it, int k, int t0, int t1) {
       const int n = it.n, before = x ? t1 : t0;
       struct Row {
         bool live, idle;       // idle: the warp's quadrant of 32 matrix rows is past the tile's last; it only keeps the barriers going
-        int h, pos, lo;        // q head, position and the window's first key
-        int64_t at;            // row of q and out
+        int pos, lo;           // position and the window's first key
+        int64_t at;            // (row of q and out) * Hq + q head
       };
       auto row_of = [&](const Item& i) {
         Row w;
         const int q0 = i.v0 + (pair && x ? pl.RT : 0);     // the tile's first row of the sequence
-        const int vq = q0 + r / pl.G;                      // this row's
+        const int vq = q0 + r_row;                         // this row's
         w.live = r < pl.RT * pl.G && vq < i.v1 && vq < q0 + pl.RT;
         w.idle = quad * 32 >= (min(i.v1, q0 + pl.RT) - q0) * pl.G;
-        w.h = i.g * pl.G + r % pl.G;
-        w.at = (int64_t)tab.row0[i.si] + vq;
-        w.pos = w.live ? tab.pos0[i.si] + vq : i.p_last;   // (rows that are not there: any, nothing reads them)
+        w.at = ((int64_t)i.row0 + vq) * a.Hq + i.g * pl.G + r_head;
+        w.pos = w.live ? i.pos0 + vq : i.end() - 1;        // (rows that are not there: any, nothing reads them)
         w.lo = a.window && w.pos - (a.window - 1) > 0 ? w.pos - (a.window - 1) : 0;
         return w;
       };
@@ -666,7 +671,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       if constexpr (!QTMA) {   // bf16 Q rows of the quadrant to f16; absent rows are zeros. One tile: each stream half of the rows
         constexpr int CH = HD / 8;
         if (!wwait(q_empty, (k & 1) ^ 1)) return false;
-        const int64_t off = rw.live ? rw.at * a.q_stride + (int64_t)rw.h * HD : -1;
+        const int64_t off = rw.live ? ((int64_t)it.row0 + it.v0 + (pair && x ? pl.RT : 0) + r_row) * a.q_stride +
+                                          (int64_t)(it.g * pl.G + r_head) * HD : -1;
         uint8_t* dst = sm + L::Q + (pair && x ? BQ * HD * 2 : 0);
         const int first = pair ? 0 : x * (CH / 2), count = pair ? CH : CH / 2;
 #pragma unroll 2
@@ -783,10 +789,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         if (lane == 0) mbar_arrive(&p_full[2 * x + hh]);
       }
       // ---- the item's end (what the loop did not need is made again: registers). Its sums stay in TMEM until the next item's first weights are announced
-      int w_again = it.w;
-      asm volatile("" : "+r"(w_again));
-      it = item_of(tab, a, pl, w_again);
-      rw = row_of(it);
+      const Item ie = item_at(k);
+      rw = row_of(ie);
       float l = lo2(l2) + hi2(l2);
       if (li > 0 && !wwait(&o_done[x], (x ? dn1 : dn0) & 1)) return false;
       fence_after();
@@ -812,7 +816,10 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       if (!idle && !none) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const bool fix = rw.live && !publish && *v_flag;   // non-finite values of partly hidden tiles: into the rows that see them
-        const int64_t pi = (int64_t)it.w * 2 + (pair ? x : 0);
+        const int64_t pi = (int64_t)ie.w * 2 + (pair ? x : 0);
+        int64_t to[4];                           // where the rows of this lane's group of four go
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to[e] = __shfl_sync(0xffffffffu, rw.live ? rw.at : -1, (lane & ~3) + e);
 #pragma unroll 1
         for (int c = 0; c < HD; c += 32) {       // (zeros without a tile)
           uint32_t u[32];
@@ -839,16 +846,34 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
               u[e + 3] = __float_as_uint((w0 != 0.f ? w0 * __uint_as_float(u[e + 3]) : 0.f) + (w1 != 0.f ? w1 * y.w : 0.f));
             }
           }
-          if (fix) add_nonfinite<E4, PBF>(it, a, tab.seq[it.si], rw.pos, rw.lo, c, u);
-          if (it.ns == 1) {
-            if (rw.live) {
-              uint4* dst = reinterpret_cast<uint4*>((uint16_t*)a.out + (rw.at * a.Hq + rw.h) * HD + c);
+          if (fix) add_nonfinite<E4, PBF>(ie, a, rw.pos, rw.lo, c, u);
+          if (ie.ns == 1) {
+            // 16-byte pieces change places within four lanes, so that each store has 64 bytes of a row side by side (a row's
+            // own piece in every lane: 32 lines a store, the epilogue 3.3 us instead of 1)
+            uint32_t y[16];
 #pragma unroll
-              for (int e = 0; e < 32; e += 8)
-                dst[e / 8] = make_uint4(pack_w<OBF>(__uint_as_float(u[e]) * inv, __uint_as_float(u[e + 1]) * inv), pack_w<OBF>(__uint_as_float(u[e + 2]) * inv, __uint_as_float(u[e + 3]) * inv),
-                                        pack_w<OBF>(__uint_as_float(u[e + 4]) * inv, __uint_as_float(u[e + 5]) * inv),
-                                        pack_w<OBF>(__uint_as_float(u[e + 6]) * inv, __uint_as_float(u[e + 7]) * inv));
+            for (int e = 0; e < 16; ++e)
+              y[e] = pack_w<OBF>(__uint_as_float(u[2 * e]) * inv, __uint_as_float(u[2 * e + 1]) * inv);
+#pragma unroll
+            for (int step = 1; step <= 2; step <<= 1) {
+              const bool up = lane & step;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (!(e & step)) {
+#pragma unroll
+                  for (int z = 0; z < 4; ++z) {
+                    uint32_t &lo_ = y[4 * e + z], &hi_ = y[4 * (e + step) + z];
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo_ : hi_, step);
+                    if (up) lo_ = got;
+                    else hi_ = got;
+                  }
+                }
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (to[e] >= 0)
+                *reinterpret_cast<uint4*>((uint16_t*)a.out + to[e] * HD + c + (lane & 3) * 8) =
+                    make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
           } else {                               // [HD / 4][32 rows] groups of 4 sums
             float4* dst = reinterpret_cast<float4*>(a.ws) + ((pi * 4 + quad) * (HD / 4) + c / 4) * 32 + lane;
 #pragma unroll
@@ -856,7 +881,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
           }
         }
         if (publish) *reinterpret_cast<float2*>(pub + HD) = make_float2(m, l);
-        else if (rw.live && it.ns > 1)
+        else if (rw.live && ie.ns > 1)
           reinterpret_cast<float2*>((float*)a.ws + (int64_t)tab.split * 2 * BQ * HD)[pi * BQ + r] = make_float2(m, l);
       }
       if (publish) {
