@@ -182,9 +182,12 @@ __device__ __forceinline__ Item item_of(const Tab<N>& tab, const PagedAttnArgs& 
   it.row0 = tab.row0[si];
   it.seq = tab.seq[si];
   it.pos0 = tab.pos0[si];
-  const int local = w - tab.start[si], part = local % it.ns, item = local / it.ns;
-  it.g = item % a.pages.Hkv;
-  const int mp = MP - 1 - item / a.pages.Hkv;      // (the last rows see most: first)
+  // whole items: the last rows, which see most, first; parts: the items that read the same keys side by side
+  const int local = w - tab.start[si], part = it.ns > 1 ? local / (MP * a.pages.Hkv) : 0;
+  const int item = local - part * MP * a.pages.Hkv, a0 = it.ns > 1 ? MP : a.pages.Hkv;
+  const int q = item / a0, r = item - q * a0;
+  it.g = it.ns > 1 ? q : r;
+  const int mp = MP - 1 - (it.ns > 1 ? r : q);
   it.two = pl.nt == 2 && 2 * mp + 1 < MT;
   it.v0 = pl.nt * mp * pl.RT;
   it.v1 = min(len, it.v0 + (it.two ? 2 : 1) * pl.RT);
@@ -936,9 +939,9 @@ __global__ void __launch_bounds__(CWARPS * 32, 4)
   auto out_at = [&](int r) {                                   // where matrix row r of the tile goes
     return (((int64_t)tab.row0[si] + mt * pl.RT + r / pl.G) * a.Hq + g * pl.G + r % pl.G) * HD + cb * CCOLS;
   };
-  // this tile's parts: CTAs side by side, two tile slots each
-  const int mp = mt / pl.nt, item = (MP - 1 - mp) * Hkv + g;
-  const int64_t p0 = ((int64_t)tab.start[si] + (int64_t)item * ns) * 2 + mt % pl.nt;
+  // this tile's parts, two tile slots each, MP * Hkv items apart
+  const int mp = mt / pl.nt;
+  const int64_t p0 = ((int64_t)tab.start[si] + (int64_t)g * MP + MP - 1 - mp) * 2 + mt % pl.nt, apart = (int64_t)MP * Hkv * 2;
   const float2* ml = reinterpret_cast<const float2*>((const float*)a.ws + (int64_t)tab.split * 2 * BQ * HD) + p0 * BQ +
                      quad * 32 + lane;
   const float4* ps = reinterpret_cast<const float4*>(a.ws) + ((p0 * 4 + quad) * (HD / 4) + cb * (CCOLS / 4)) * 32 + lane;
@@ -952,9 +955,9 @@ __global__ void __launch_bounds__(CWARPS * 32, 4)
     for (int k = 0; k < U; ++k) {
       x[k] = make_float2(-INFINITY, 0.f);
       if (p + k * W < ns) {
-        x[k] = __ldcg(ml + (int64_t)(p + k * W) * 2 * BQ);
+        x[k] = __ldcg(ml + (p + k * W) * apart * BQ);
 #pragma unroll
-        for (int c = 0; c < CCOLS / 4; ++c) v[k][c] = __ldcg(ps + ((int64_t)(p + k * W) * 2 * HD + c) * 32);
+        for (int c = 0; c < CCOLS / 4; ++c) v[k][c] = __ldcg(ps + ((p + k * W) * apart * HD + c) * 32);
       }
     }
 #pragma unroll
