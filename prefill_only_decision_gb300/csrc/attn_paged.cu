@@ -69,7 +69,7 @@ struct Lay {
   static constexpr int KV1 = Q + BQ * HD * 2;             // with one
   static constexpr int QSC = KV2 + F * TILE;              // [2][128] floats: what a row's q was divided by
   static constexpr int BASE = QSC + 2 * BQ * 4;           // [2][BASES] exponent bounds
-  static constexpr int TABLE = BASE + 2 * BASES * 4;       // the CTA's first ITEMS items
+  static constexpr int TABLE = BASE + (2 * BASES + 16) * 4;       // the CTA's first ITEMS items
   static constexpr int BAR = TABLE + ITEMS * 64;
   static constexpr int NS = 2 * FR > F ? 2 * FR : F;
   static constexpr int NBAR = 3 + 4 * NS + 12 + 2 + 2 + 4;
@@ -146,6 +146,12 @@ __device__ __forceinline__ uint4 codes_to_half(const uint2 c, float f) {
   return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
+// The four warps of a plane's loaders.
+__device__ __forceinline__ void plane_sync(int plane) {
+  if (plane) asm volatile("bar.sync 2, 128;" ::: "memory");
+  else asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+
 // The exponent bound of a scale: scale < 2^E. Scales that are not finite or not there have none.
 constexpr int NO_BOUND = -1000;
 __device__ __forceinline__ int bound_of(float scale) {
@@ -207,8 +213,8 @@ __device__ __forceinline__ Item item_of(const Tab<N>& tab, const PagedAttnArgs& 
   return it;
 }
 
-// Adds the non-finite elements of columns c .. c + 31 of the partly hidden value rows that a query sees.
-template <bool E4, bool PBF>
+// Adds the non-finite elements of columns c .. c + CW - 1 of the partly hidden value rows that a query sees.
+template <bool E4, bool PBF, int CW>
 __device__ __forceinline__ void add_nonfinite(const Item& it, const PagedAttnArgs& a, int pos, int row_lo, int c,
                                               uint32_t* o) {
   const PagesArgs& pg = a.pages;
@@ -223,7 +229,7 @@ __device__ __forceinline__ void add_nonfinite(const Item& it, const PagedAttnArg
       const int64_t vec = (((pg.n_pages + (int64_t)id) * pg.Hkv + it.g) << pg.shift) + (j & ((1 << pg.shift) - 1));
       if constexpr (E4) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
+        for (int e = 0; e < CW; ++e) {
           const float y =
               __half2float(__half(__nv_cvt_fp8_to_halfraw(((const __nv_fp8_storage_t*)pg.data)[vec * pg.hd + c + e], __NV_E4M3))) *
               pg.scales[vec];
@@ -232,7 +238,7 @@ __device__ __forceinline__ void add_nonfinite(const Item& it, const PagedAttnArg
       } else {
         const uint4* at = reinterpret_cast<const uint4*>((const uint16_t*)pg.data + vec * pg.hd + c);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < CW / 8; ++e) {
           const uint4 y = at[e];
           const uint32_t y4[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* v_flag = (volatile int*)(tmem_slot + 2);   // a value of a partly hidden tile is not finite
   volatile int* base_k = (volatile int*)(sm + L::BASE);    // [BASES] by tile
-  volatile int* base_v = base_k + BASES;
+  volatile int* base_v = base_k + BASES + 16;              // (between them the loaders' bounds)
 
   const PagesArgs& pg = a.pages;
   const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -535,71 +541,53 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
     } else {
       // ---- e4m3 pages: this warp's 32 rows of every tile of its plane. LPR lanes of 16 codes per row, RP rows a pass, PN
       // passes; the lanes of a row's second 64 columns take their two 8-code halves in the other order, so that no store
-      // conflicts. Rows that no query sees are zeros.
+      // conflicts. Rows that no query sees are zeros. A plane's warps agree on the tile's exponent bound through shared memory.
       const int plane = warp < 14 ? 0 : 1;
       constexpr int LPR = HD / 16, RP = 32 / LPR, PN = 32 / RP;
       const int ci = lane % LPR, sw = HD == 128 && ci >= 4 ? 1 : 0;
       const int c0 = ((2 * ci) & 7) + sw, c1 = ((2 * ci) & 7) + 1 - sw;
       const int mask = (1 << pg.shift) - 1;
-      const int64_t to_v = ((int64_t)pg.n_pages * pg.Hkv) << pg.shift;   // from a K vector to its V vector
+      volatile int* bounds = (volatile int*)(sm + L::BASE) + BASES + 8 * plane;   // [2][4 warps] by tile parity
       int tiles = 0;                                             // before the item
+      bool ok = true;                                            // (a warp that gave up still meets the others of its plane)
       each_item([&](const Item& it, int k, int t0, int t1) {
-        if (!pair && k > 0 && !wwait(kv_free, (k - 1) & 1)) return false;
+        if (!pair && k > 0 && ok) ok = wwait(kv_free, (k - 1) & 1);
         const int n = it.n;
-        const int64_t trow = (int64_t)it.seq * pg.table_stride;
-        auto vector_of = [&](int key) -> int64_t {               // of a cached row's K, -1: none that a query sees
+        auto vector_of = [&](int t) -> int64_t {                 // of row `lane` of tile t; -1: none that a query sees
+          if (t >= n) return -1;
+          const int key = it.tile(t) + lw * 32 + lane;
           if (key >= it.end() || (key < it.lo && key >= it.sk)) return -1;
-          const int id = pg.table[trow + (key >> pg.shift)];
+          const int id = pg.table[(int64_t)it.seq * pg.table_stride + (key >> pg.shift)];
           if (id < 0 || id >= pg.n_pages) return -1;
-          return (((int64_t)id * pg.Hkv + it.g) << pg.shift) + (key & mask);
+          return ((((int64_t)plane * pg.n_pages + id) * pg.Hkv + it.g) << pg.shift) + (key & mask);
         };
-        uint4 code[PN];                                          // of this warp's rows of its plane's next tile
-        int64_t vec = -1, vec_next = -1;                         // vector of row `lane` in tile t + 1, and in the one behind it
-        int64_t q4[4], q4_next[4];                               // the K vectors of rows lane, lane + 32, .. of those tiles
-        float sk4[4], sv4[4];                                    // their scales, of tile t + 1
-        int run_v = NO_BOUND;
-        auto lookup = [&](int t) {
-          const int j0 = t < n ? it.tile(t) : 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) q4_next[i] = t < n ? vector_of(j0 + 32 * i + lane) : -1;
-          vec_next = lw == 0 ? q4_next[0] : lw == 1 ? q4_next[1] : lw == 2 ? q4_next[2] : q4_next[3];
-          if (plane && vec_next >= 0) vec_next += to_v;
-        };
+        uint4 code[PN];                                          // of this warp's rows of the next tile
+        float sc = 0.f;                                          // and the scale of its row `lane`
+        int run = NO_BOUND;
         auto read = [&](int64_t v, int p) {
           const int64_t w = __shfl_sync(0xffffffffu, v, p * RP + lane / LPR);
           return w >= 0 ? __ldg(reinterpret_cast<const uint4*>((const uint8_t*)pg.data + w * HD) + ci) : make_uint4(0, 0, 0, 0);
         };
-        auto fetch = [&]() {                                     // scales and codes of the tile that lookup found
-          vec = vec_next;
+        auto fetch = [&](int64_t v) {
+          sc = v >= 0 ? __ldg(pg.scales + v) : 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            q4[i] = q4_next[i];
-            sk4[i] = plane == 0 && q4[i] >= 0 ? __ldg(pg.scales + q4[i]) : 0.f;
-            sv4[i] = q4[i] >= 0 ? __ldg(pg.scales + q4[i] + to_v) : 0.f;
-          }
-#pragma unroll
-          for (int p = 0; p < PN; ++p) code[p] = read(vec, p);
+          for (int p = 0; p < PN; ++p) code[p] = read(v, p);
         };
-        lookup(0);
-        if (n > 0) fetch();
-        lookup(1);
+        int64_t vec = vector_of(0), next = vector_of(1);         // (page ids a tile ahead of the codes)
+        if (n > 0) fetch(vec);
         for (int t = 0; t < n; ++t) {
           const Slot ks = slot(t, plane == 1, t0, t1);
-          // exponent bounds: of the tile's K scales, and the running one of V's (both planes' warps follow it)
-          int bk = NO_BOUND, bv = NO_BOUND;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            bk = max(bk, bound_of(sk4[i]));
-            bv = max(bv, bound_of(sv4[i]));
-          }
-          bk = __reduce_max_sync(0xffffffffu, bk);
-          run_v = max(run_v, __reduce_max_sync(0xffffffffu, bv));
-          if (bk == NO_BOUND) bk = 0;
-          const int E = plane ? (run_v == NO_BOUND ? 0 : run_v) : bk;
-          const float mine = plane ? (lw == 0 ? sv4[0] : lw == 1 ? sv4[1] : lw == 2 ? sv4[2] : sv4[3])
-                                   : (lw == 0 ? sk4[0] : lw == 1 ? sk4[1] : lw == 2 ? sk4[2] : sk4[3]);
-          const float fac = ldexpf(mine, 7 - E);                 // below 2^7
-          if (!wwait(&empty[ks.s], ks.ph ^ 1)) return false;
+          // the exponent bound: K's of the tile, V's running
+          const int mine = __reduce_max_sync(0xffffffffu, bound_of(sc));
+          if (lane == 0) bounds[4 * ((tiles + t) & 1) + lw] = mine;
+          plane_sync(plane);
+          const volatile int* w4 = bounds + 4 * ((tiles + t) & 1);
+          const int top = max(max(w4[0], w4[1]), max(w4[2], w4[3]));
+          run = plane ? max(run, top) : top;
+          const int E = run == NO_BOUND ? 0 : run;
+          const float fac = ldexpf(sc, 7 - E);                   // below 2^7
+          if (ok) ok = wwait(&empty[ks.s], ks.ph ^ 1);
+          if (!ok) continue;
           uint8_t* dst = kvst + ks.s * L::TILE;
           const bool fast = __all_sync(0xffffffffu, __half2float(__float2half_rn(fac)) == fac);
           const bool check = plane && it.partly(it.tile(t), a.window, a.sinks);
@@ -623,17 +611,13 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
             for (int p = 0; p < PN; ++p) convert(std::false_type{}, read(vec, p), p);
           }
           if (bad) *v_flag = 1;
-          if (plane == 0 && lw == 0 && lane == 0) {
-            base_k[(tiles + t) % BASES] = bk;
-            base_v[(tiles + t) % BASES] = run_v == NO_BOUND ? 0 : run_v;
-          }
+          if (lw == 0 && lane == 0) (plane ? base_v : base_k)[(tiles + t) % BASES] = E;
           fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(plane ? &vfull[ks.s] : &full[ks.s]);
-          if (t + 1 < n) {
-            fetch();
-            lookup(t + 2);
-          }
+          vec = next;
+          next = vector_of(t + 2);
+          if (t + 1 < n) fetch(vec);
         }
         tiles += n;
         return true;
@@ -727,6 +711,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         int unit_now = unit;
         if constexpr (E4) {
           zs *= pow2f(base_k[(tiles + t) % BASES] - 7);
+          const Slot vs = slot(t, true, t0, t1);               // (V's bound comes with the V tile)
+          if (hh == 0 && !wwait(&vfull[vs.s], vs.kind_ph)) return false;
           unit_now = base_v[(tiles + t) % BASES];
         }
         ld_wait();
@@ -820,48 +806,52 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const bool fix = rw.live && !publish && *v_flag;   // non-finite values of partly hidden tiles: into the rows that see them
         const int64_t pi = (int64_t)ie.w * 2 + (pair ? x : 0);
-        int64_t to[4];                           // where the rows of this lane's group of four go
+        constexpr int CW = E4 ? 16 : 32, PIECES = CW / 8;   // columns at a time (e4m3: 96 registers a thread)
+        int64_t to[PIECES];                      // where the rows of this lane's group of PIECES go
 #pragma unroll
-        for (int e = 0; e < 4; ++e) to[e] = __shfl_sync(0xffffffffu, rw.live ? rw.at : -1, (lane & ~3) + e);
+        for (int e = 0; e < PIECES; ++e) to[e] = __shfl_sync(0xffffffffu, rw.live ? rw.at : -1, (lane & ~(PIECES - 1)) + e);
 #pragma unroll 1
-        for (int c = 0; c < HD; c += 32) {       // (zeros without a tile)
-          uint32_t u[32];
+        for (int c = 0; c < HD; c += CW) {       // (zeros without a tile)
+          uint32_t u[CW];
           if (li > 0) {
-            tld32(tO + c, u);
+            if constexpr (CW == 32) tld32(tO + c, u);
+            else tld16(tO + c, u);
             ld_wait();
-            pin32(u);
+            pin<CW>(u);
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) u[e] = li > 0 ? __float_as_uint(__uint_as_float(u[e]) * scale_o) : 0u;
+          for (int e = 0; e < CW; ++e) u[e] = li > 0 ? __float_as_uint(__uint_as_float(u[e]) * scale_o) : 0u;
           float4* at = reinterpret_cast<float4*>(pub + c);
           if (publish) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) at[e / 4] = make_float4(__uint_as_float(u[e]), __uint_as_float(u[e + 1]), __uint_as_float(u[e + 2]), __uint_as_float(u[e + 3]));
+            for (int e = 0; e < CW; e += 4)
+              at[e / 4] = make_float4(__uint_as_float(u[e]), __uint_as_float(u[e + 1]), __uint_as_float(u[e + 2]),
+                                      __uint_as_float(u[e + 3]));
             continue;
           }
           if (!pair) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
+            for (int e = 0; e < CW; e += 4) {
               const float4 y = at[e / 4];
-              u[e] = __float_as_uint((w0 != 0.f ? w0 * __uint_as_float(u[e]) : 0.f) + (w1 != 0.f ? w1 * y.x : 0.f));
-              u[e + 1] = __float_as_uint((w0 != 0.f ? w0 * __uint_as_float(u[e + 1]) : 0.f) + (w1 != 0.f ? w1 * y.y : 0.f));
-              u[e + 2] = __float_as_uint((w0 != 0.f ? w0 * __uint_as_float(u[e + 2]) : 0.f) + (w1 != 0.f ? w1 * y.z : 0.f));
-              u[e + 3] = __float_as_uint((w0 != 0.f ? w0 * __uint_as_float(u[e + 3]) : 0.f) + (w1 != 0.f ? w1 * y.w : 0.f));
+              const float y4[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                u[e + z] = __float_as_uint((w0 != 0.f ? w0 * __uint_as_float(u[e + z]) : 0.f) + (w1 != 0.f ? w1 * y4[z] : 0.f));
             }
           }
-          if (fix) add_nonfinite<E4, PBF>(ie, a, rw.pos, rw.lo, c, u);
+          if (fix) add_nonfinite<E4, PBF, CW>(ie, a, rw.pos, rw.lo, c, u);
           if (ie.ns == 1) {
-            // 16-byte pieces change places within four lanes, so that each store has 64 bytes of a row side by side (a row's
-            // own piece in every lane: 32 lines a store, the epilogue 3.3 us instead of 1)
-            uint32_t y[16];
+            // 16-byte pieces change places within PIECES lanes, so that each store has PIECES * 16 bytes of a row side by side
+            // (a row's own piece in every lane: 32 lines a store, the end of an item 3.3 us instead of 2)
+            uint32_t y[CW / 2];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < CW / 2; ++e)
               y[e] = pack_w<OBF>(__uint_as_float(u[2 * e]) * inv, __uint_as_float(u[2 * e + 1]) * inv);
 #pragma unroll
-            for (int step = 1; step <= 2; step <<= 1) {
+            for (int step = 1; step < PIECES; step <<= 1) {
               const bool up = lane & step;
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
+              for (int e = 0; e < PIECES; ++e)
                 if (!(e & step)) {
 #pragma unroll
                   for (int z = 0; z < 4; ++z) {
@@ -873,14 +863,16 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < PIECES; ++e)
               if (to[e] >= 0)
-                *reinterpret_cast<uint4*>((uint16_t*)a.out + to[e] * HD + c + (lane & 3) * 8) =
+                *reinterpret_cast<uint4*>((uint16_t*)a.out + to[e] * HD + c + (lane & (PIECES - 1)) * 8) =
                     make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
           } else {                               // [HD / 4][32 rows] groups of 4 sums
             float4* dst = reinterpret_cast<float4*>(a.ws) + ((pi * 4 + quad) * (HD / 4) + c / 4) * 32 + lane;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) dst[e / 4 * 32] = make_float4(__uint_as_float(u[e]), __uint_as_float(u[e + 1]), __uint_as_float(u[e + 2]), __uint_as_float(u[e + 3]));
+            for (int e = 0; e < CW; e += 4)
+              dst[e / 4 * 32] = make_float4(__uint_as_float(u[e]), __uint_as_float(u[e + 1]), __uint_as_float(u[e + 2]),
+                                            __uint_as_float(u[e + 3]));
           }
         }
         if (publish) *reinterpret_cast<float2*>(pub + HD) = make_float2(m, l);
