@@ -272,7 +272,7 @@ struct RowsArgs {
   int64_t q_out_stride;
   RopeArgs rope;
 };
-cudaError_t launch_rope_rows(const RowsArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_rope_rows(const RowsArgs& a, int dtype, int num_sms, cudaStream_t st);
 
 struct PagedAttnArgs {
   const void* q;

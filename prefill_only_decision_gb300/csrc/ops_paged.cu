@@ -111,7 +111,7 @@ int s1_op_rope_async(const void* x, int32_t dtype, int64_t x_stride, int32_t n_r
   a.q_out = out;
   a.q_out_type = out_dtype;
   a.q_out_stride = out_stride;
-  return cuda_rc(launch_rope_rows(a, dtype, (cudaStream_t)stream), "rope");
+  return cuda_rc(launch_rope_rows(a, dtype, sm_count(), (cudaStream_t)stream), "rope");
 }
 
 int s1_op_kv_append_async(const void* q, const void* k, const void* v, int32_t dtype, int64_t q_stride, int64_t k_stride,
@@ -154,7 +154,7 @@ int s1_op_kv_append_async(const void* q, const void* k, const void* v, int32_t d
   a.q_out = q_out;
   a.q_out_type = q_dtype;
   a.q_out_stride = Hq * hd;
-  return cuda_rc(launch_rope_rows(a, dtype, (cudaStream_t)stream), "kv_append");
+  return cuda_rc(launch_rope_rows(a, dtype, sm_count(), (cudaStream_t)stream), "kv_append");
 }
 
 int s1_op_attention_paged_step_workspace(int32_t n, int32_t Hq, int32_t Hkv, int32_t hd, int64_t* bytes) {

@@ -5,10 +5,12 @@
 // is one 64-bit product whose overflow is the whole turns. Its top 32 bits give the quadrant and an angle within an eighth
 // of a turn, whose sine and cosine fp32 holds to its last bit or two.
 //
-// Every element is read and written once: HBM bound. A block takes RB rows: it computes the rows' n_pairs sines and cosines
-// once into shared memory for all heads (a sine in every thread that uses one would cost five times the rotation
-// itself), then a thread turns 2 x 8 elements of a head at a time, chunk c and its partner chunk, hd / 16 threads a
-// head, U of them loaded before the first is used.
+// Every element is read and written once: HBM bound. A block takes tiles of RB rows in turn: for each it makes the rows' n_pairs
+// sines and cosines once into shared memory for all heads (a sine in every thread that uses one would cost five times the
+// rotation itself), then a thread turns 2 x 8 elements of a head at a time, chunk c and its partner chunk, hd / 16 threads a
+// head, U of them loaded before the first is used. Blocks stay because a thread then looks its pair's frequency up once (lanes
+// that index kernel parameters differently are served one by one: 70001 rows to e4m3 192 us with a block per tile), and so that
+// the next tile's positions and page ids are on their way under the present one.
 #include <algorithm>
 
 #include <cuda_fp8.h>
@@ -90,15 +92,49 @@ __device__ __forceinline__ float finite_abs(float x) {
 template <typename T, int HD, bool VEC, bool APPEND>
 __global__ void __launch_bounds__(THREADS, 4) rows_kernel(const __grid_constant__ RowsArgs a, int rb, int hb, bool out_vec) {
   constexpr int NU = HD / 16, U = 2;
-  __shared__ float4 cs[RB_MAX * MAX_PAIRS / 2];              // (cos, sin) pairs
-  __shared__ int64_t place[RB_MAX];                          // of a row in a plane of pages: vector (head 0); -1: none
-  __shared__ int live[RB_MAX];
+  __shared__ float4 cs[2][RB_MAX * MAX_PAIRS / 2];           // (cos, sin) pairs, by tile parity
+  __shared__ int64_t place[2][RB_MAX];                       // of a row in a plane of pages: vector (head 0); -1: none
+  __shared__ int live[2][RB_MAX];
   allow_dependents();
-  wait_prerequisites();
   const int np = a.rope.n_pairs, np8 = np / 8;
-  const int r0 = blockIdx.x * rb, rows = min(rb, a.n_rows - r0);
   const int H = a.Hq + (APPEND ? 2 * a.pages.Hkv : 0);
-  const int h0 = blockIdx.y * hb, heads = min(hb, H - h0), total = rows * heads * NU;
+  const int h0 = blockIdx.y * hb, heads = min(hb, H - h0);
+  // this thread's angle: row trow of each tile, pair tpair
+  const int trow = np ? (int)threadIdx.x / np : RB_MAX, tpair = np ? (int)threadIdx.x - trow * np : 0;
+  uint64_t turn = 0;
+  int64_t axis = 0;
+  if (trow < rb) {
+    const uint64_t* t = a.rope.turn;
+    const uint8_t* x = a.rope.axis;
+    asm volatile("" : "+l"(t), "+l"(x));                     // (loads, not indexed constants)
+    turn = t[tpair];
+    axis = x[tpair];
+  }
+  wait_prerequisites();
+  const int tiles = (a.n_rows + rb - 1) / rb;
+  auto angle_pos = [&](int tile) {
+    const int r = tile * rb + trow;
+    if (trow >= rb || tile >= tiles || r >= a.n_rows) return 0;
+    return !APPEND || a.pos ? a.pos[axis * a.pos_stride + r] : a.at[r];
+  };
+  // threads 0 .. rb - 1: where the tile's rows go
+  struct Where {
+    int j, s;
+  };
+  auto where = [&](int tile) {
+    Where w = {-1, 0};
+    const int r = tile * rb + (int)threadIdx.x;
+    if (!APPEND || threadIdx.x >= rb || tile >= tiles || r >= a.n_rows) return w;
+    w.j = a.at[r];
+    w.s = a.seq ? a.seq[r] : r;
+    return w;
+  };
+  auto page_of = [&](const Where& w) {                       // -1: none
+    if (!APPEND || w.j < 0 || w.s < 0 || w.s >= a.pages.n_seq || w.j >> a.pages.shift >= a.pages.cols) return -1;
+    const int id = a.pages.table[w.s * a.pages.table_stride + (w.j >> a.pages.shift)];
+    return id < a.pages.n_pages ? id : -1;
+  };
+  int r0, total;                                             // of the tile at hand: first row, units
   Raw<T> x[U][2];
   int row[U], h[U];
   // unit i: rows' heads in turn, hd / 16 units a head; two chunks c0 and c1 of 8 elements: a pair's two sides, or past the
@@ -131,25 +167,23 @@ __global__ void __launch_bounds__(THREADS, 4) rows_kernel(const __grid_constant_
       x[u][1] = kvc::load8<T, VEC>(src + chunk1(unit, n8) * 8);
     }
   };
+  int pos = angle_pos(blockIdx.x);                           // a tile ahead of its use
+  Where w = where(blockIdx.x), w_next = where(blockIdx.x + gridDim.x);
+  int id = page_of(w);
+  for (int tile = blockIdx.x, buf = 0; tile < tiles; tile += gridDim.x, buf ^= 1) {
+  r0 = tile * rb;
+  total = min(rb, a.n_rows - r0) * heads * NU;
   load(0);                                                   // (in flight while the angles are made)
-  for (int i = threadIdx.x; i < rows * np; i += THREADS) {
-    const int rr = i / np, pair = i - rr * np;
-    const int p = !APPEND || a.pos ? a.pos[a.rope.axis[pair] * a.pos_stride + r0 + rr] : a.at[r0 + rr];
-    reinterpret_cast<float2*>(cs)[rr * MAX_PAIRS + pair] = cos_sin(p, a.rope.turn[pair]);
+  if (trow < rb) reinterpret_cast<float2*>(cs[buf])[trow * MAX_PAIRS + tpair] = cos_sin(pos, turn);
+  if (APPEND && threadIdx.x < rb) {
+    place[buf][threadIdx.x] = id < 0 ? -1 : (((int64_t)id * a.pages.Hkv) << a.pages.shift) + (w.j & ((1 << a.pages.shift) - 1));
+    live[buf][threadIdx.x] = w.j >= 0;
   }
-  if (APPEND && threadIdx.x < rows) {
-    const int rr = r0 + threadIdx.x;
-    int64_t at = -1;
-    const int j = a.at[rr], s = a.seq ? a.seq[rr] : rr, col = j >> a.pages.shift;
-    if (j >= 0 && s >= 0 && s < a.pages.n_seq && col < a.pages.cols) {
-      const int id = a.pages.table[s * a.pages.table_stride + col];
-      if (id >= 0 && id < a.pages.n_pages)
-        at = (((int64_t)id * a.pages.Hkv) << a.pages.shift) + (j & ((1 << a.pages.shift) - 1));
-    }
-    place[threadIdx.x] = at;
-    live[threadIdx.x] = j >= 0;
-  }
-  __syncthreads();
+  __syncthreads();                                           // (one a tile: the other buffer's readers are past the sync before)
+  pos = angle_pos(tile + gridDim.x);
+  w = w_next;
+  id = page_of(w);
+  w_next = where(tile + 2 * gridDim.x);
   for (int b = 0; b < total; b += THREADS * U) {             // (the whole block: lanes past the end take part in shuffles)
     if (b) load(b);
 #pragma unroll
@@ -159,7 +193,7 @@ __global__ void __launch_bounds__(THREADS, 4) rows_kernel(const __grid_constant_
       widen(x[u][1], hi);
       const int n8 = pairs8(h[u]), c0 = chunk0(unit, n8), c1 = chunk1(unit, n8), r = max(row[u], 0);
       if (unit < n8) {
-        const float4* t = cs + (r * MAX_PAIRS + c0 * 8) / 2;
+        const float4* t = cs[buf] + (r * MAX_PAIRS + c0 * 8) / 2;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float4 w = t[e];
@@ -184,11 +218,11 @@ __global__ void __launch_bounds__(THREADS, 4) rows_kernel(const __grid_constant_
 #pragma unroll
           for (int o = NU / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         }
-        in = in && live[r];
+        in = in && live[buf][r];
         if (in && h[u] >= a.Hq) {
-          if (place[r] < 0) continue;
+          if (place[buf][r] < 0) continue;
           const int hk = h[u] - a.Hq, plane = hk >= a.pages.Hkv, kvh = hk - plane * a.pages.Hkv;
-          const int64_t vec = (((int64_t)plane * a.pages.n_pages * a.pages.Hkv + kvh) << a.pages.shift) + place[r];
+          const int64_t vec = (((int64_t)plane * a.pages.n_pages * a.pages.Hkv + kvh) << a.pages.shift) + place[buf][r];
           if (a.pages.format == KVF_E4M3) {
             const int E = kvc::scale_exp(m);
             const float inv = kvc::pow2(-E);
@@ -217,37 +251,38 @@ __global__ void __launch_bounds__(THREADS, 4) rows_kernel(const __grid_constant_
       store8(a.q_out, o + c1 * 8, a.q_out_type, hi, out_vec);
     }
   }
+  }
 }
 
 template <typename T, int HD, bool VEC, bool APPEND>
-cudaError_t launch_t(const RowsArgs& a, bool out_vec, cudaStream_t st) {
+cudaError_t launch_t(const RowsArgs& a, bool out_vec, int num_sms, cudaStream_t st) {
   const int H = a.Hq + (APPEND ? 2 * a.pages.Hkv : 0);
   constexpr int NU = HD / 16;
   // few rows: fewer of them a block, and a block's heads those of one batch of loads, so that they spread over the SMs
   const int rb = a.n_rows >= 152 * RB_MAX ? RB_MAX : a.n_rows >= 152 * 2 ? 2 : 1;
   const int hb = rb == RB_MAX ? H : std::min(H, THREADS / NU);
-  const dim3 grid((a.n_rows + rb - 1) / rb, (H + hb - 1) / hb);
+  const dim3 grid(std::min((a.n_rows + rb - 1) / rb, 4 * num_sms), (H + hb - 1) / hb);
   return launch_pdl(rows_kernel<T, HD, VEC, APPEND>, grid, dim3(THREADS), 0, st, a, rb, hb, out_vec);
 }
 template <typename T, int HD>
-cudaError_t launch_vec(const RowsArgs& a, cudaStream_t st) {
+cudaError_t launch_vec(const RowsArgs& a, int num_sms, cudaStream_t st) {
   auto ok = [](const void* p, int64_t stride, int es) { return (((uintptr_t)p | (uintptr_t)(stride * es)) & 15) == 0; };
   const bool append = a.k != nullptr;
   const int es = sizeof(T);
   const bool vec = ok(a.q, a.q_stride, es) && (!append || (ok(a.k, a.k_stride, es) && ok(a.v, a.v_stride, es)));
   const bool out_vec = ok(a.q_out, a.q_out_stride, a.q_out_type == ELEM_F32 ? 4 : 2);
-  if (append) return vec ? launch_t<T, HD, true, true>(a, out_vec, st) : launch_t<T, HD, false, true>(a, out_vec, st);
-  return vec ? launch_t<T, HD, true, false>(a, out_vec, st) : launch_t<T, HD, false, false>(a, out_vec, st);
+  if (append) return vec ? launch_t<T, HD, true, true>(a, out_vec, num_sms, st) : launch_t<T, HD, false, true>(a, out_vec, num_sms, st);
+  return vec ? launch_t<T, HD, true, false>(a, out_vec, num_sms, st) : launch_t<T, HD, false, false>(a, out_vec, num_sms, st);
 }
 template <typename T>
-cudaError_t launch_hd(const RowsArgs& a, cudaStream_t st) {
-  return a.hd == 128 ? launch_vec<T, 128>(a, st) : launch_vec<T, 64>(a, st);
+cudaError_t launch_hd(const RowsArgs& a, int num_sms, cudaStream_t st) {
+  return a.hd == 128 ? launch_vec<T, 128>(a, num_sms, st) : launch_vec<T, 64>(a, num_sms, st);
 }
 }  // namespace rap
 
-cudaError_t launch_rope_rows(const RowsArgs& a, int dtype, cudaStream_t st) {
-  if (dtype == ELEM_F32) return rap::launch_hd<float>(a, st);
-  return dtype == ELEM_F16 ? rap::launch_hd<f16>(a, st) : rap::launch_hd<bf16>(a, st);
+cudaError_t launch_rope_rows(const RowsArgs& a, int dtype, int num_sms, cudaStream_t st) {
+  if (dtype == ELEM_F32) return rap::launch_hd<float>(a, num_sms, st);
+  return dtype == ELEM_F16 ? rap::launch_hd<f16>(a, num_sms, st) : rap::launch_hd<bf16>(a, num_sms, st);
 }
 
 }  // namespace s1
