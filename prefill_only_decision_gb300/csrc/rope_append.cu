@@ -22,7 +22,7 @@ namespace s1 {
 namespace rap {
 using kvc::Raw;
 
-constexpr int THREADS = 256, RB_MAX = 4;
+constexpr int THREADS = 256, RB_MAX = 16, PASSES = 4;         // rows of a tile; angles of a tile that a thread makes
 
 // cos and sin of pos * turn (2^-64 turns): quadrant and rest, the rest's Taylor series (|y| <= pi / 4: the terms left out are
 // below 2^-29 of the sine and 2^-32 of the cosine).
@@ -89,9 +89,13 @@ __device__ __forceinline__ float finite_abs(float x) {
 }
 
 // grid (row blocks of rb rows, head blocks of hb heads): heads 0 .. Hq-1 are q's, then k's, then v's.
-template <typename T, int HD, bool VEC, bool APPEND>
-__global__ void __launch_bounds__(THREADS, 4) rows_kernel(const __grid_constant__ RowsArgs a, int rb, int hb, bool out_vec) {
-  constexpr int NU = HD / 16, U = 2;
+// U, the units a thread loads at once: 2, and 1 where a call is small. Blocks of an SM: 4 with 16-bit rows, 3 with fp32 ones, whose
+// loads take twice the registers (70001 rows f16 to e4m3 with 3, 4, 5 blocks: 157, 147, 163 us; 12345 rows f32 to bf16 40.6,
+// 46, 61 us; U of 1, 3, 4 f16: 165, 152, 162 us; 37 tokens with U of 1 and 2: 2.9, 3.4 us).
+constexpr int blocks_of(size_t es) { return es == 4 ? 3 : 4; }
+template <typename T, int HD, bool VEC, bool APPEND, int U>
+__global__ void __launch_bounds__(THREADS, blocks_of(sizeof(T))) rows_kernel(const __grid_constant__ RowsArgs a, int rb, int hb, bool out_vec) {
+  constexpr int NU = HD / 16;
   __shared__ float4 cs[2][RB_MAX * MAX_PAIRS / 2];           // (cos, sin) pairs, by tile parity
   __shared__ int64_t place[2][RB_MAX];                       // of a row in a plane of pages: vector (head 0); -1: none
   __shared__ int live[2][RB_MAX];
@@ -99,11 +103,13 @@ __global__ void __launch_bounds__(THREADS, 4) rows_kernel(const __grid_constant_
   const int np = a.rope.n_pairs, np8 = np / 8;
   const int H = a.Hq + (APPEND ? 2 * a.pages.Hkv : 0);
   const int h0 = blockIdx.y * hb, heads = min(hb, H - h0);
-  // this thread's angle: row trow of each tile, pair tpair
-  const int trow = np ? (int)threadIdx.x / np : RB_MAX, tpair = np ? (int)threadIdx.x - trow * np : 0;
+  const uint32_t magic = 0xffffffffu / (uint32_t)heads + 1;
+  // this thread's angles: pair tpair of rows trow, trow + rstep, .. of each tile
+  const int trow = np ? (int)threadIdx.x / np : RB_MAX, tpair = np ? (int)threadIdx.x - trow * np : 0, rstep = np ? THREADS / np : 1;
+  const bool angles = np && trow < min(rb, rstep);
   uint64_t turn = 0;
   int64_t axis = 0;
-  if (trow < rb) {
+  if (angles) {
     const uint64_t* t = a.rope.turn;
     const uint8_t* x = a.rope.axis;
     asm volatile("" : "+l"(t), "+l"(x));                     // (loads, not indexed constants)
@@ -112,10 +118,15 @@ __global__ void __launch_bounds__(THREADS, 4) rows_kernel(const __grid_constant_
   }
   wait_prerequisites();
   const int tiles = (a.n_rows + rb - 1) / rb;
-  auto angle_pos = [&](int tile) {
-    const int r = tile * rb + trow;
-    if (trow >= rb || tile >= tiles || r >= a.n_rows) return 0;
-    return !APPEND || a.pos ? a.pos[axis * a.pos_stride + r] : a.at[r];
+  int pos[PASSES];                                           // a tile ahead of their use
+  auto positions = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const int rr = trow + i * rstep;
+      pos[i] = 0;
+      if (!angles || tile >= tiles || rr >= rb || tile * rb + rr >= a.n_rows) continue;
+      pos[i] = !APPEND || a.pos ? a.pos[axis * a.pos_stride + tile * rb + rr] : a.at[tile * rb + rr];
+    }
   };
   // threads 0 .. rb - 1: where the tile's rows go
   struct Where {
@@ -148,9 +159,7 @@ __global__ void __launch_bounds__(THREADS, 4) rows_kernel(const __grid_constant_
     for (int u = 0; u < U; ++u) {
       const int i = b + u * THREADS + (int)threadIdx.x;
       const int hr = i / NU;
-      int r = 0;
-#pragma unroll
-      for (int k = 1; k < RB_MAX; ++k) r += hr >= k * heads;
+      const int r = heads == 1 ? hr : (int)__umulhi((uint32_t)hr, magic);   // hr / heads (hr < 16 heads, heads < 2^14)
       row[u] = i < total ? r : -1;
       h[u] = h0 + hr - r * heads;
       x[u][0] = x[u][1] = Raw<T>{};
@@ -167,90 +176,94 @@ __global__ void __launch_bounds__(THREADS, 4) rows_kernel(const __grid_constant_
       x[u][1] = kvc::load8<T, VEC>(src + chunk1(unit, n8) * 8);
     }
   };
-  int pos = angle_pos(blockIdx.x);                           // a tile ahead of its use
+  positions(blockIdx.x);
   Where w = where(blockIdx.x), w_next = where(blockIdx.x + gridDim.x);
   int id = page_of(w);
   for (int tile = blockIdx.x, buf = 0; tile < tiles; tile += gridDim.x, buf ^= 1) {
-  r0 = tile * rb;
-  total = min(rb, a.n_rows - r0) * heads * NU;
-  load(0);                                                   // (in flight while the angles are made)
-  if (trow < rb) reinterpret_cast<float2*>(cs[buf])[trow * MAX_PAIRS + tpair] = cos_sin(pos, turn);
-  if (APPEND && threadIdx.x < rb) {
-    place[buf][threadIdx.x] = id < 0 ? -1 : (((int64_t)id * a.pages.Hkv) << a.pages.shift) + (w.j & ((1 << a.pages.shift) - 1));
-    live[buf][threadIdx.x] = w.j >= 0;
-  }
-  __syncthreads();                                           // (one a tile: the other buffer's readers are past the sync before)
-  pos = angle_pos(tile + gridDim.x);
-  w = w_next;
-  id = page_of(w);
-  w_next = where(tile + 2 * gridDim.x);
-  for (int b = 0; b < total; b += THREADS * U) {             // (the whole block: lanes past the end take part in shuffles)
-    if (b) load(b);
+    r0 = tile * rb;
+    total = min(rb, a.n_rows - r0) * heads * NU;
+    load(0);                                                   // (in flight while the angles are made)
+    if (angles)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float lo[8], hi[8];
-      widen(x[u][0], lo);
-      widen(x[u][1], hi);
-      const int n8 = pairs8(h[u]), c0 = chunk0(unit, n8), c1 = chunk1(unit, n8), r = max(row[u], 0);
-      if (unit < n8) {
-        const float4* t = cs[buf] + (r * MAX_PAIRS + c0 * 8) / 2;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 w = t[e];
-          const float a0 = lo[2 * e], b0 = hi[2 * e], a1 = lo[2 * e + 1], b1 = hi[2 * e + 1];
-          lo[2 * e] = a0 * w.x - b0 * w.y;
-          hi[2 * e] = b0 * w.x + a0 * w.y;
-          lo[2 * e + 1] = a1 * w.z - b1 * w.w;
-          hi[2 * e + 1] = b1 * w.z + a1 * w.w;
-        }
-      }
-      bool in = row[u] >= 0;
-      if constexpr (APPEND) {
-        float m = 0.f;
-        if (a.pages.format == KVF_E4M3 && __any_sync(0xffffffffu, in && h[u] >= a.Hq)) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(lo[e]), fabsf(hi[e])));   // (NaN: left out)
-          if (isinf(m)) {                                    // the head's largest finite magnitude
-            m = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(finite_abs(lo[e]), finite_abs(hi[e])));
-          }
-#pragma unroll
-          for (int o = NU / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        }
-        in = in && live[buf][r];
-        if (in && h[u] >= a.Hq) {
-          if (place[buf][r] < 0) continue;
-          const int hk = h[u] - a.Hq, plane = hk >= a.pages.Hkv, kvh = hk - plane * a.pages.Hkv;
-          const int64_t vec = (((int64_t)plane * a.pages.n_pages * a.pages.Hkv + kvh) << a.pages.shift) + place[buf][r];
-          if (a.pages.format == KVF_E4M3) {
-            const int E = kvc::scale_exp(m);
-            const float inv = kvc::pow2(-E);
-            uint8_t* codes = (uint8_t*)a.pages.data + vec * HD;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const float* y = half ? hi : lo;
-              uint16_t c[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                c[e] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * e] * inv, y[2 * e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-              *reinterpret_cast<uint2*>(codes + (half ? c1 : c0) * 8) = kvc::pack_codes(c);
-            }
-            if (unit == 0) a.pages.scales[vec] = kvc::pow2(E);
-          } else {
-            const int type = a.pages.format == KVF_F16 ? ELEM_F16 : ELEM_BF16;
-            store8(a.pages.data, vec * HD + c0 * 8, type, lo, true);
-            store8(a.pages.data, vec * HD + c1 * 8, type, hi, true);
-          }
-          continue;
-        }
-      }
-      if (!in) continue;
-      const int64_t o = (r0 + r) * a.q_out_stride + (int64_t)h[u] * HD;
-      store8(a.q_out, o + c0 * 8, a.q_out_type, lo, out_vec);
-      store8(a.q_out, o + c1 * 8, a.q_out_type, hi, out_vec);
+      for (int i = 0; i < PASSES; ++i)
+        if (trow + i * rstep < rb)
+          reinterpret_cast<float2*>(cs[buf])[(trow + i * rstep) * MAX_PAIRS + tpair] = cos_sin(pos[i], turn);
+    if (APPEND && threadIdx.x < rb) {
+      place[buf][threadIdx.x] = id < 0 ? -1 : (((int64_t)id * a.pages.Hkv) << a.pages.shift) + (w.j & ((1 << a.pages.shift) - 1));
+      live[buf][threadIdx.x] = w.j >= 0;
     }
-  }
+    __syncthreads();                                           // (one a tile: the other buffer's readers are past the sync before)
+    positions(tile + gridDim.x);
+    w = w_next;
+    id = page_of(w);
+    w_next = where(tile + 2 * gridDim.x);
+    for (int b = 0; b < total; b += THREADS * U) {             // (the whole block: lanes past the end take part in shuffles)
+      if (b) load(b);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float lo[8], hi[8];
+        widen(x[u][0], lo);
+        widen(x[u][1], hi);
+        const int n8 = pairs8(h[u]), c0 = chunk0(unit, n8), c1 = chunk1(unit, n8), r = max(row[u], 0);
+        if (unit < n8) {
+          const float4* t = cs[buf] + (r * MAX_PAIRS + c0 * 8) / 2;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 w = t[e];
+            const float a0 = lo[2 * e], b0 = hi[2 * e], a1 = lo[2 * e + 1], b1 = hi[2 * e + 1];
+            lo[2 * e] = a0 * w.x - b0 * w.y;
+            hi[2 * e] = b0 * w.x + a0 * w.y;
+            lo[2 * e + 1] = a1 * w.z - b1 * w.w;
+            hi[2 * e + 1] = b1 * w.z + a1 * w.w;
+          }
+        }
+        bool in = row[u] >= 0;
+        if constexpr (APPEND) {
+          float m = 0.f;
+          if (a.pages.format == KVF_E4M3 && __any_sync(0xffffffffu, in && h[u] >= a.Hq)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(lo[e]), fabsf(hi[e])));   // (NaN: left out)
+            if (isinf(m)) {                                    // the head's largest finite magnitude
+              m = 0.f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(finite_abs(lo[e]), finite_abs(hi[e])));
+            }
+#pragma unroll
+            for (int o = NU / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          }
+          in = in && live[buf][r];
+          if (in && h[u] >= a.Hq) {
+            if (place[buf][r] < 0) continue;
+            const int hk = h[u] - a.Hq, plane = hk >= a.pages.Hkv, kvh = hk - plane * a.pages.Hkv;
+            const int64_t vec = (((int64_t)plane * a.pages.n_pages * a.pages.Hkv + kvh) << a.pages.shift) + place[buf][r];
+            if (a.pages.format == KVF_E4M3) {
+              const int E = kvc::scale_exp(m);
+              const float inv = kvc::pow2(-E);
+              uint8_t* codes = (uint8_t*)a.pages.data + vec * HD;
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const float* y = half ? hi : lo;
+                uint16_t c[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  c[e] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * e] * inv, y[2 * e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+                *reinterpret_cast<uint2*>(codes + (half ? c1 : c0) * 8) = kvc::pack_codes(c);
+              }
+              if (unit == 0) a.pages.scales[vec] = kvc::pow2(E);
+            } else {
+              const int type = a.pages.format == KVF_F16 ? ELEM_F16 : ELEM_BF16;
+              store8(a.pages.data, vec * HD + c0 * 8, type, lo, true);
+              store8(a.pages.data, vec * HD + c1 * 8, type, hi, true);
+            }
+            continue;
+          }
+        }
+        if (!in) continue;
+        const int64_t o = (r0 + r) * a.q_out_stride + (int64_t)h[u] * HD;
+        store8(a.q_out, o + c0 * 8, a.q_out_type, lo, out_vec);
+        store8(a.q_out, o + c1 * 8, a.q_out_type, hi, out_vec);
+      }
+    }
   }
 }
 
@@ -258,11 +271,17 @@ template <typename T, int HD, bool VEC, bool APPEND>
 cudaError_t launch_t(const RowsArgs& a, bool out_vec, int num_sms, cudaStream_t st) {
   const int H = a.Hq + (APPEND ? 2 * a.pages.Hkv : 0);
   constexpr int NU = HD / 16;
-  // few rows: fewer of them a block, and a block's heads those of one batch of loads, so that they spread over the SMs
-  const int rb = a.n_rows >= 152 * RB_MAX ? RB_MAX : a.n_rows >= 152 * 2 ? 2 : 1;
-  const int hb = rb == RB_MAX ? H : std::min(H, THREADS / NU);
-  const dim3 grid(std::min((a.n_rows + rb - 1) / rb, 4 * num_sms), (H + hb - 1) / hb);
-  return launch_pdl(rows_kernel<T, HD, VEC, APPEND>, grid, dim3(THREADS), 0, st, a, rb, hb, out_vec);
+  // A tile holds enough rows for one or two of a thread's batches; fewer where the rows then would not reach all SMs, and of
+  // few rows a block takes the heads of one batch of loads. At most 8192 heads a block.
+  const int want = std::max(PASSES, (4 * THREADS + H * NU - 1) / (H * NU));
+  int rb = 1;
+  const int enough = (sizeof(T) == 4 ? 2 : 4) * num_sms;      // tiles (1280 rows f16 with one, two, four an SM: 7.4, 6.9, 6.1 us;
+  while (rb < RB_MAX && rb < want && a.n_rows >= 2 * rb * enough) rb *= 2;   // 1500 rows f32 9.6, 6.9, 7.8)
+  rb = std::min(rb, PASSES * (a.rope.n_pairs ? THREADS / a.rope.n_pairs : THREADS));
+  const int hb = rb >= 4 ? std::min(H, 8192) : std::min(H, THREADS / NU);
+  const dim3 grid(std::min((a.n_rows + rb - 1) / rb, blocks_of(sizeof(T)) * num_sms), (H + hb - 1) / hb);
+  return launch_pdl(rb >= 4 ? rows_kernel<T, HD, VEC, APPEND, 2> : rows_kernel<T, HD, VEC, APPEND, 1>, grid, dim3(THREADS), 0, st,
+                    a, rb, hb, out_vec);
 }
 template <typename T, int HD>
 cudaError_t launch_vec(const RowsArgs& a, int num_sms, cudaStream_t st) {
