@@ -36,6 +36,7 @@ using namespace t5;
 using namespace pga;
 
 constexpr int KT = 64, PRODUCERS = 3;
+constexpr int LANE_SEQS = 8;                 // up to 32 times as many sequences are counted by each warp alone
 enum Kind { F16 = 0, BF16 = 1, E4M3 = 2 };
 
 __device__ uint64_t g_given_up;              // when a bounded wait last gave up, per device; never cleared
@@ -145,9 +146,7 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
   uint64_t* full = (uint64_t*)(sm + L::BAR);   // [NST]
   uint64_t* empty = full + NST;                // [NST]
   volatile int* abort_flag = (volatile int*)(empty + NST);
-  int* found = (int*)(empty + NST) + 1;        // the run's first sequence
-  __shared__ int64_t red[WARPS + PRODUCERS];
-  __shared__ int64_t found_before;             // tiles (per pair) of the sequences before it
+  __shared__ int red[WARPS + PRODUCERS], found[2];
   const PagedAttnArgs& a = sa.a;
   const PagesArgs& pg = a.pages;
   const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -160,102 +159,133 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
     *abort_flag = 0;
     mbar_init_fence();
   }
+  __syncthreads();
   allow_dependents();
   wait_prerequisites();
 
   // ---- this CTA's run of the list of tiles
-  const int rows = (int)(((int64_t)pg.cols) << pg.shift);
-  auto look = [&](Cursor& c, int s) {
+  const int rows = (int)(((int64_t)pg.cols) << pg.shift), HG = sa.HG;
+  auto look_at = [&](Cursor& c, int s, int p) {
     c.s = s;
-    c.v = seen_rows(sa.pos[s], rows, a.window, a.sinks);
+    c.v = seen_rows(p, rows, a.window, a.sinks);
     c.tl = tiles_of<KT>(c.v);
     c.T = c.tl.count();
   };
-  auto tiles_at = [&](int s) { return s < sa.n ? tiles_of<KT>(seen_rows(sa.pos[s], rows, a.window, a.sinks)).count() : 0; };
-  auto block_scan = [&](int64_t x, int64_t* total) {          // inclusive, over the block's threads
+  auto pos_of = [&](int s) { return s < sa.n ? sa.pos[s] : -1; };
+  auto tiles_at = [&](int p) { return tiles_of<KT>(seen_rows(p, rows, a.window, a.sinks)).count(); };
+  auto warp_scan = [&](int x) {                // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    __syncthreads();
-    if (lane == 31) red[warp] = x;
-    __syncthreads();
-    int64_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS + PRODUCERS; ++w) {
-      if (w < warp) before += red[w];
-      all += red[w];
-    }
-    *total = all;
-    return x + before;
+    return x;
   };
-  int64_t per_head = 0, first_scan = 0;
-  for (int b = 0; b < sa.n; b += THREADS) {
-    int64_t t;
-    const int64_t x = block_scan(tiles_at(b + (int)threadIdx.x), &t);
-    if (b == 0) first_scan = x;
-    per_head += t;
-  }
-  const int64_t units = per_head * sa.HG;
-  const int64_t C = min(units, (int64_t)gridDim.x);          // CTAs with a run: none of them is empty
-  const int64_t u0 = blockIdx.x < C ? units * blockIdx.x / C : 0, u1 = blockIdx.x < C ? units * (blockIdx.x + 1) / C : 0;
-  if (u0 < u1) {                               // the first sequence whose tiles reach beyond u0
-    int64_t carry = 0;
-    bool there = false;
-    for (int b = 0; b < sa.n && !there; b += THREADS) {
-      int64_t t;
-      const int s = b + (int)threadIdx.x;
-      const int64_t mine = tiles_at(s), x = b == 0 ? first_scan : block_scan(mine, &t);
-      if (b == 0) t = INT64_MAX;
-      const int64_t end = carry + x;
-      if (end * sa.HG > u0 && (end - mine) * sa.HG <= u0) {
-        *found = s;
-        found_before = end - mine;
+  // the run, from the number of tiles per (kv head, group) of all sequences: the first units % C CTAs have one more
+  struct Run {
+    int u0, u1, C, q, rem;
+  };
+  auto run_of = [&](int per_head) {
+    Run r;
+    const int units = per_head * HG, b = (int)blockIdx.x;
+    r.C = max(1, min(units, (int)gridDim.x));  // CTAs with a run
+    r.q = (int)((uint32_t)units / (uint32_t)r.C);
+    r.rem = units - r.q * r.C;
+    r.u0 = b * r.q + min(b, r.rem);
+    r.u1 = b < r.C ? r.u0 + r.q + (b < r.rem ? 1 : 0) : r.u0;
+    return r;
+  };
+  Run run;
+  int s0 = 0, before = 0;                      // the run's first sequence, and the tiles (per pair) of those before it
+  if (sa.n <= 32 * LANE_SEQS) {                // every warp by itself
+    const int K = (sa.n + 31) / 32;
+    int t[LANE_SEQS], mine = 0;
+#pragma unroll
+    for (int i = 0; i < LANE_SEQS; ++i) t[i] = i < K ? pos_of(lane * K + i) : -1;
+#pragma unroll
+    for (int i = 0; i < LANE_SEQS; ++i) mine += t[i] = tiles_at(t[i]);
+    const int end = warp_scan(mine);
+    run = run_of(__shfl_sync(0xffffffffu, end, 31));
+    const uint32_t past = __ballot_sync(0xffffffffu, (int64_t)end * HG > run.u0);   // (the first of them holds it)
+    int at = end - mine, s = lane * K;
+#pragma unroll
+    for (int i = 0; i < LANE_SEQS; ++i)
+      if (i < K && (int64_t)(at + t[i]) * HG <= run.u0) {
+        at += t[i];
+        ++s;
+      } else {
+        break;
+      }
+    const int owner = past ? __ffs(past) - 1 : 0;
+    s0 = __shfl_sync(0xffffffffu, s, owner);
+    before = __shfl_sync(0xffffffffu, at, owner);
+  } else {                                     // the block, THREADS sequences at a time
+    auto block_scan = [&](int x, int* total) {
+      x = warp_scan(x);
+      __syncthreads();
+      if (lane == 31) red[warp] = x;
+      __syncthreads();
+      int head = 0, all = 0;
+      for (int w = 0; w < WARPS + PRODUCERS; ++w) {
+        if (w < warp) head += red[w];
+        all += red[w];
+      }
+      *total = all;
+      return x + head;
+    };
+    int per_head = 0;
+    for (int b = 0; b < sa.n; b += THREADS) {
+      int t;
+      block_scan(tiles_at(pos_of(b + (int)threadIdx.x)), &t);
+      per_head += t;
+    }
+    run = run_of(per_head);
+    if (run.u0 < run.u1) {
+      bool there = false;
+      for (int b = 0, carry = 0; !there; b += THREADS) {
+        int t;
+        const int mine = tiles_at(pos_of(b + (int)threadIdx.x)), end = carry + block_scan(mine, &t);
+        if ((int64_t)end * HG > run.u0 && (int64_t)(end - mine) * HG <= run.u0) {
+          found[0] = b + (int)threadIdx.x;
+          found[1] = end - mine;
+        }
+        carry += t;
+        there = (int64_t)carry * HG > run.u0;
       }
       __syncthreads();
-      if (b == 0) {                            // (the first block's total again: the last thread's)
-        if (threadIdx.x == THREADS - 1) red[0] = x;
-        __syncthreads();
-        t = red[0];
-      }
-      carry += t;
-      there = carry * sa.HG > u0;
+      s0 = found[0];
+      before = found[1];
     }
   }
-  __syncthreads();
   Cursor c0 = {};
-  if (u0 < u1) {
-    look(c0, *found);
-    const int64_t r = u0 - found_before * sa.HG;
-    c0.hg = (int)(r / c0.T);
-    c0.t = (int)(r % c0.T);
+  if (run.u0 < run.u1) {
+    look_at(c0, s0, pos_of(s0));
+    const int r = run.u0 - before * HG;
+    c0.hg = r / c0.T;
+    c0.t = r - c0.hg * c0.T;
   }
   // runs fn(cursor, tiles of the pair in this run, the next pair's cursor, whether there is one) over the pairs of the run;
-  // positions are read a sequence ahead
+  // positions are read 32 sequences at a time
   auto each_pair = [&](auto&& fn) {
-    auto pos_of = [&](int s) { return s < sa.n ? sa.pos[s] : -1; };
-    auto look_at = [&](Cursor& c, int s, int p) {
-      c.s = s;
-      c.v = seen_rows(p, rows, a.window, a.sinks);
-      c.tl = tiles_of<KT>(c.v);
-      c.T = c.tl.count();
-    };
-    if (u0 >= u1) return;
+    if (run.u0 >= run.u1) return;
     Cursor c = c0;
-    int ahead = pos_of(c.s + 1);
-    for (int64_t u = u0;;) {
-      const int m = (int)min((int64_t)(c.T - c.t), u1 - u);
+    int base = c.s + 1, ahead = pos_of(base + lane);
+    for (int u = run.u0;;) {
+      const int m = min(c.T - c.t, run.u1 - u);
       u += m;
       Cursor nx = c;
       nx.t = 0;
-      if (u < u1 && ++nx.hg == sa.HG) {
+      if (u < run.u1 && ++nx.hg == HG) {       // the next sequence that sees something
         nx.hg = 0;
-        look_at(nx, c.s + 1, ahead);
-        while (nx.T == 0) look_at(nx, nx.s + 1, pos_of(nx.s + 1));
-        ahead = pos_of(nx.s + 1);
+        uint32_t some;
+        while (!(some = __ballot_sync(0xffffffffu, base + lane > c.s && tiles_at(ahead) > 0)) && base < sa.n) {
+          base += 32;
+          ahead = pos_of(base + lane);
+        }
+        const int l = __ffs(some) - 1;
+        look_at(nx, base + l, __shfl_sync(0xffffffffu, ahead, l));
       }
-      if (!fn(c, m, nx, u < u1) || u >= u1) return;
+      if (!fn(c, m, nx, u < run.u1) || u >= run.u1) return;
       c = nx;
     }
   };
@@ -330,7 +360,7 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
     int i = 0;                                 // tiles of the run before the pair
     // tokens that see nothing: zeros
     for (int s = blockIdx.x; s < sa.n; s += gridDim.x)
-      if (sa.pos[s] < 0 || tiles_at(s) == 0)
+      if (tiles_at(sa.pos[s]) == 0)
         for (int e = threadIdx.x; e < a.Hq * HD / 8; e += WARPS * 32)
           reinterpret_cast<uint4*>((uint16_t*)a.out + (int64_t)s * a.Hq * HD)[e] = make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) {
@@ -355,7 +385,7 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
       }
     };
     constexpr bool AHEAD = NH == 1 || HD == 64;   // (the registers of 16 q heads of 128 leave no room)
-    if (AHEAD && u0 < u1) load_q(c0);
+    if (AHEAD && run.u0 < run.u1) load_q(c0);
     each_pair([&](const Cursor& c, int m, const Cursor& nx, bool more) {
       const int kvh = c.hg / sa.groups, h0 = kvh * sa.G + (c.hg % sa.groups) * 8 * NH;
       const int nq = min(8 * NH, (kvh + 1) * sa.G - h0);       // q heads of the pair
@@ -616,13 +646,12 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
         group_sync<WARPS * 32>();
       }
       if (ends && !starts && threadIdx.x == 0) {
-        // the pair's first tile: list position u0 - c.t when this is the run's first pair (the only one it does not start)
-        const int64_t at = u0 - c.t;
-        int64_t f = at * C / units;                            // the CTA whose run holds it
-        while (units * (f + 1) / C <= at) ++f;
-        while (units * f / C > at) --f;
+        // the pair's first tile: list position u0 - c.t (this is the run's first pair, the only one it does not start), and
+        // the CTA whose run holds it
+        const int at = run.u0 - c.t, more = run.rem * (run.q + 1);
+        const int f = at < more ? at / (run.q + 1) : run.rem + (at - more) / run.q;
         Record* rec = reinterpret_cast<Record*>((float*)a.ws + 2 * (int64_t)gridDim.x * slot_floats(HD)) + blockIdx.x;
-        *rec = Record{c.s, c.hg, (int)f, 1};
+        *rec = Record{c.s, c.hg, f, 1};
       }
       return true;
     });

@@ -173,6 +173,8 @@ int s1_op_attention_paged_step_async(const void* q, int32_t q_dtype, int64_t q_s
   const int rc = check_attn(q, q_dtype, q_stride, Hq, pages, window, sinks, sm_scale, out, workspace, &a.pages);
   if (rc != S1_OK) return rc;
   if (n < 0 || n > pages->n_seq) return bad("attention_paged_step: n must be 0 .. n_seq");
+  if ((int64_t)n * pages->Hkv * ((Hq / pages->Hkv + 15) / 16) * (((int64_t)pages->cols << a.pages.shift) / 64 + 2) > INT32_MAX)
+    return unsupported("attention_paged_step: n * kv heads * rows of the table is above 2^37");
   if (n == 0) return S1_OK;
   if (!q || !out || !pos) return bad("attention_paged_step: a NULL pointer");
   if (!aligned(pos, 4)) return bad("attention_paged_step: misaligned pos");
