@@ -661,7 +661,9 @@ def op_attention_paged_async(q: int, q_dtype: int, q_stride: int, row0, lens, po
     """Attention of prompt rows over their pages (s1_op_attention_paged_async)."""
     _fits(Hq | window | sinks)
     r0, ln = _seq_arrays(row0, lens)
-    p0, _ = _seq_arrays(pos0, lens)
+    p0 = _seq_i32(pos0)
+    if p0.shape != ln.shape:
+        raise ValueError("pos0 and lens must be of the same length")
     check(lib().s1_op_attention_paged_async(q, q_dtype, q_stride, len(r0), _addr(r0), _addr(ln), _addr(p0), Hq,
                                             _ref(pages), window, sinks, sm_scale, out, workspace, workspace_bytes,
                                             stream))

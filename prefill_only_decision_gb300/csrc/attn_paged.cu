@@ -1015,6 +1015,7 @@ struct Group {
   int next;                    // the first sequence not taken
   int max_ns;
 };
+int64_t most_parts(int pos0, int len) { return std::max<int64_t>(64, ((int64_t)pos0 + len) / BKV / LONGEST + 2); }
 void plan_group(Group& gr, int s0, int n_seq, const int* row0, const int* len, const int* pos0, int Hq, int Hkv, int hd,
                 int window, int sinks, int num_sms) {
   Plan& pl = gr.pl;
@@ -1029,12 +1030,13 @@ void plan_group(Group& gr, int s0, int n_seq, const int* row0, const int* len, c
   static thread_local std::vector<Seq> seqs;
   seqs.clear();
   int s = s0;
-  int64_t all_tiles = 0;
+  int64_t all_tiles = 0, most = 0;
   for (; s < n_seq && (int)seqs.size() < TAB_LARGE; ++s) {
     if (len[s] == 0) continue;
     const int64_t MT = ((int64_t)len[s] + pl.RT - 1) / pl.RT;
-    if (!seqs.empty() && (all_tiles + MT) * Hkv * std::max(64, hd / 2) > INT_MAX) break;   // (CTA numbers stay within 31 bits)
     all_tiles += MT;
+    most = std::max(most, most_parts(pos0[s], len[s]));
+    if (!seqs.empty() && all_tiles * Hkv * most > INT_MAX) break;   // (numbers of items and of the join's blocks stay within 31 bits)
     Seq q{s, 1, {}, {}, {}};
     for (int k = 0; k < 2; ++k) {
       const int rows = (k + 1) * pl.RT;
@@ -1056,7 +1058,8 @@ void plan_group(Group& gr, int s0, int n_seq, const int* row0, const int* len, c
     for (const Seq& q : seqs) longest = std::max(longest, q.top[k]);
     const double c = k ? 1.13 : 0.66;
     int last = 0;
-    for (int parts = (longest + LONGEST - 1) / LONGEST; parts <= 64 && parts <= longest; ++parts) {
+    const int least = (longest + LONGEST - 1) / LONGEST;
+    for (int parts = least; parts == least || (parts <= 64 && parts <= longest); ++parts) {
       const int per = (longest + parts - 1) / parts;
       if (per == last) continue;
       last = per;
@@ -1154,9 +1157,16 @@ cudaError_t launch_kind(const PagedAttnArgs& a, const Group& gr, int num_sms, cu
 }
 }  // namespace pgp
 
+bool attention_paged_fits(int len, int pos0, int Hq, int Hkv) {
+  const int RT = pgp::BQ / (Hq / Hkv);
+  return ((int64_t)len / RT + 1) * Hkv * pgp::most_parts(pos0, len) <= INT_MAX;
+}
+
 cudaError_t attention_paged_gave_up_word(uint64_t** out) {
   return cudaGetSymbolAddress(reinterpret_cast<void**>(out), pgp::g_given_up);
 }
+
+static int64_t group_ws_bytes(const pgp::Group& gr, int hd) { return (int64_t)gr.tab.split * 2 * pgp::BQ * (hd + 2) * 4; }
 
 int64_t attention_paged_ws_bytes(int n_seq, const int* len, const int* pos0, int Hq, int Hkv, int hd, int window, int sinks,
                                  int num_sms) {
@@ -1164,18 +1174,29 @@ int64_t attention_paged_ws_bytes(int n_seq, const int* len, const int* pos0, int
   pgp::Group gr;
   for (int s = 0; s < n_seq; s = gr.next) {
     pgp::plan_group(gr, s, n_seq, nullptr, len, pos0, Hq, Hkv, hd, window, sinks, num_sms);
-    need = std::max<int64_t>(need, (int64_t)gr.tab.split * 2 * pgp::BQ * (hd + 2) * 4);
+    need = std::max(need, group_ws_bytes(gr, hd));
   }
   return need;
 }
 
 cudaError_t launch_attention_paged(const PagedAttnArgs& a, int n_seq, const int* row0, const int* len, const int* pos0,
-                                   int num_sms, cudaStream_t st) {
+                                   int num_sms, int64_t ws_bytes, bool* too_small, cudaStream_t st) {
   pgp::Group gr;
+  const PagesArgs& pg = a.pages;
+  *too_small = false;
   for (int s = 0; s < n_seq; s = gr.next) {
-    pgp::plan_group(gr, s, n_seq, row0, len, pos0, a.Hq, a.pages.Hkv, a.pages.hd, a.window, a.sinks, num_sms);
+    pgp::plan_group(gr, s, n_seq, row0, len, pos0, a.Hq, pg.Hkv, pg.hd, a.window, a.sinks, num_sms);
+    if (s == 0) {              // before anything is launched: the workspace of all groups (one, mostly)
+      const int64_t need = gr.next == n_seq ? group_ws_bytes(gr, pg.hd)
+                                            : attention_paged_ws_bytes(n_seq, len, pos0, a.Hq, pg.Hkv, pg.hd, a.window,
+                                                                       a.sinks, num_sms);
+      if (need > 0 && (!a.ws || ws_bytes < need)) {
+        *too_small = true;
+        return cudaSuccess;
+      }
+    }
     if (gr.tab.n == 0) continue;
-    CK_RET(a.pages.hd == 128 ? pgp::launch_kind<128>(a, gr, num_sms, st) : pgp::launch_kind<64>(a, gr, num_sms, st));
+    CK_RET(pg.hd == 128 ? pgp::launch_kind<128>(a, gr, num_sms, st) : pgp::launch_kind<64>(a, gr, num_sms, st));
   }
   return cudaSuccess;
 }

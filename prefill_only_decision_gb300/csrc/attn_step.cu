@@ -607,6 +607,7 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
           for (int k = 4; k < 32; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
           if (g == 0) ml[warp * 8 + 2 * t4 + e] = make_float2(mx[half][e], l);
           float* at = pub + (warp * 8 + 2 * t4 + e) * L::OSTR;
+          if (8 * half + 2 * t4 + e >= nq) continue;           // (no such q head)
 #pragma unroll
           for (int b = 0; b < HD / 16; ++b) {
             at[out_col<HD, KIND>(b, g, 0)] = o[half][b][e];

@@ -203,6 +203,9 @@ int s1_op_attention_paged_workspace(int32_t n_seq, const int32_t* len, const int
   if (const char* m = check_seqs(n_seq, nullptr, len)) return bad(m);
   for (int s = 0; s < n_seq; ++s)
     if (pos0[s] < 0 || (int64_t)pos0[s] + len[s] > INT32_MAX) return bad("attention_paged: a position is out of range");
+  for (int s = 0; s < n_seq; ++s)
+    if (!attention_paged_fits(len[s], pos0[s], Hq, Hkv))
+      return unsupported("attention_paged: a sequence of too many rows x heads for one call");
   try {
     *bytes = attention_paged_ws_bytes(n_seq, len, pos0, Hq, Hkv, hd, window, sinks, sm_count());
   } catch (const std::bad_alloc&) {
@@ -228,7 +231,7 @@ int s1_op_attention_paged_async(const void* q, int32_t q_dtype, int64_t q_stride
       return bad("attention_paged: a sequence ends past its table row, or starts below position 0");
   }
   for (int s = 0; s < n_seq; ++s)
-    if (((int64_t)len[s] / (128 / (Hq / pages->Hkv)) + 1) * pages->Hkv * 64 > INT32_MAX)
+    if (!attention_paged_fits(len[s], pos0[s], Hq, pages->Hkv))
       return unsupported("attention_paged: a sequence of too many rows x heads for one call");
   if (rows == 0) return S1_OK;
   if (!q || !out) return bad("attention_paged: a NULL pointer");
@@ -243,9 +246,11 @@ int s1_op_attention_paged_async(const void* q, int32_t q_dtype, int64_t q_stride
   a.ws = workspace;
   const int sms = sm_count();
   try {
-    const int64_t need = attention_paged_ws_bytes(n_seq, len, pos0, Hq, pages->Hkv, pages->hd, window, sinks, sms);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return bad("attention_paged: the workspace is too small");
-    return cuda_rc(launch_attention_paged(a, n_seq, row0, len, pos0, sms, (cudaStream_t)stream), "attention_paged");
+    bool too_small;
+    const cudaError_t e =
+        launch_attention_paged(a, n_seq, row0, len, pos0, sms, workspace_bytes, &too_small, (cudaStream_t)stream);
+    if (too_small) return bad("attention_paged: the workspace is too small");
+    return cuda_rc(e, "attention_paged");
   } catch (const std::bad_alloc&) {
     return s1::set_error(S1_ERR_OOM, "attention_paged: host memory");
   }

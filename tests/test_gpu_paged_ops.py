@@ -128,6 +128,19 @@ def test_rope_far_positions(B):
 
 
 # ---- a paged cache on both sides -------------------------------------------------------------
+def quantise(x):
+    """quant_ref's codes and scales without its loop over vectors (finite values)."""
+    a = np.abs(x).max(-1)
+    m, e = np.frexp(a)                                     # a = m 2^e, 1/2 <= m < 1; 448 = 0.875 * 2^9
+    scale = np.where(a > 0, np.exp2(np.maximum(np.where(m <= 0.875, e - 9, e - 8), -126).astype(float)), 1.0)
+    y = x / scale[..., None]
+    grid = E4M3[:127]
+    mid = (grid[1:] + grid[:-1]) / 2
+    mag = np.minimum(np.abs(y), 448.0)
+    lo, hi = np.searchsorted(mid, mag, side="left"), np.searchsorted(mid, mag, side="right")
+    return np.where((lo != hi) & (lo % 2 == 1), hi, lo) + 128 * np.signbit(y), scale
+
+
 class Cache:
     """A pool of pages in random order. Rows that no sequence owns, the rest of each last page and spare
     pages hold NaN; table entries behind a sequence's pages hold a page id that is far out of range."""
@@ -171,7 +184,7 @@ class Cache:
         pid, off = (torch.from_numpy(t.astype(np.int64)).cuda() for t in self.places(i, n))
         for plane in range(2):
             if self.fmt == "e4m3":
-                c, s = quant_ref(x[plane])
+                c, s = quantise(x[plane])
                 self.data[plane][pid, :, off] = torch.from_numpy(c.astype(np.uint8)).cuda()
                 self.scales[plane][pid, :, off] = torch.from_numpy(s).float().cuda()
                 x[plane] = E4M3[c] * s[..., None]
@@ -589,6 +602,46 @@ def test_many_sequences(B, n):
     pos = [int(p) for p in g.integers(-3, 40, n)]
     Paged(B, 2, 1, 64, pos, None, "f16", page=16, window=9, sinks=1).check()
     Paged(B, 2, 1, 64, [max(0, p) for p in pos], [int(x) for x in g.integers(0, 4, n)], "f16", page=16).check()
+
+
+def test_step_with_few_active_sequences(B):
+    """Thousands of padding tokens between the ones that see something."""
+    for n, active in ((3000, [7, 8, 1200, 2999]), (200, [199]), (257, [0, 256]), (40, [])):
+        pos = [-1 - i % 3 for i in range(n)]
+        for k, i in enumerate(active):
+            pos[i] = 700 * k + 3
+        Paged(B, 6, 3, 64, pos, None, "f16", page=16).check()
+
+
+def sampled(a, rows):
+    """check() for some rows; all others of a sequence finite."""
+    a.call()
+    a.B.op_sync(stream())
+    got, ref = a.out.double().cpu().numpy(), a.ref(set(rows))
+    assert np.abs(got[rows] - ref[rows]).max() <= a.tol() and np.isfinite(got).all()
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16", "e4m3"])
+def test_prompt_of_many_items(B, fmt):
+    """More items than a few per SM, of two query tiles (one long sequence), of one (many short ones), and of both lengths
+    with the long ones' keys split."""
+    g = np.random.default_rng(4)
+    a = Paged(B, 64, 64, 64, [0], [12000], fmt, page=64, window=40, sinks=2)
+    sampled(a, [0, 39, 40, 41, 127, 128, 255, 256] + [int(r) for r in g.integers(0, 12000, 20)] + [11999])
+    lens = [int(x) for x in g.integers(1, 60, 150)]
+    a = Paged(B, 64, 64, 64, [int(x) for x in g.integers(0, 300, 150)], lens, fmt, page=16, gap=1)
+    rows = sorted(int(a.row0[s] + g.integers(0, lens[s])) for s in range(0, 150, 5))
+    sampled(a, rows)
+    Paged(B, 8, 2, 128, [20000, 0, 7, 15000], [5, 300, 2, 40], fmt, page=32, gap=2).check()
+
+
+@pytest.mark.parametrize("kind", ["step", "prompt"])
+def test_sequences_that_share_pages(B, kind):
+    """Two sequences whose tables name the same pages see the same rows."""
+    a = Paged(B, 8, 2, 64, [300, 300], None if kind == "step" else [40, 40], "f16", page=32)
+    a.c.d_table[1] = a.c.d_table[0]
+    a.c.rows[1] = a.c.rows[0]
+    a.check()
 
 
 @pytest.mark.parametrize("fmt", ["f16", "e4m3"])

@@ -159,6 +159,16 @@ def test_prompt_workspace_refusals(B, bad, code):
             **{**dict(lens=[4], pos0=[9], Hq=16, Hkv=4, hd=128, window=0, sinks=0), **bad})
 
 
+def test_calls_too_large(B):
+    """Sizes whose numbers of tiles or items leave 31 bits."""
+    big = pages(B, n_seq=4096, cols=2 ** 23, Hkv=64, page_rows=128)
+    refused(B, UNSUP, B.op_attention_paged_step_async, **step(B, pages=big, n=4096, Hq=64, q_stride=64 * 128))
+    refused(B, UNSUP, B.op_attention_paged_async,
+            **prompt(B, pages=big, row0=[0], lens=[2 ** 29], pos0=[0], Hq=64, q_stride=64 * 128))
+    refused(B, UNSUP, B.op_attention_paged_workspace, lens=[2 ** 30], pos0=[0], Hq=64, Hkv=64, hd=128, window=0, sinks=0)
+    assert B.op_attention_paged_workspace([4], [2 ** 30], 4, 4, 128, 0, 0) > 0      # more than 64 parts
+
+
 def test_null_outputs_of_the_sizing_calls(B):
     one = np.array([4], np.int32)
     out = C.c_int64()
