@@ -626,10 +626,10 @@ def test_prompt_of_many_items(B, fmt):
     """More items than a few per SM, of two query tiles (one long sequence), of one (many short ones), and of both lengths
     with the long ones' keys split."""
     g = np.random.default_rng(4)
-    a = Paged(B, 64, 64, 64, [0], [12000], fmt, page=64, window=40, sinks=2)
-    sampled(a, [0, 39, 40, 41, 127, 128, 255, 256] + [int(r) for r in g.integers(0, 12000, 20)] + [11999])
+    a = Paged(B, 128, 8, 64, [0], [6000], fmt, page=64, window=40, sinks=2)
+    sampled(a, [0, 7, 8, 15, 16, 39, 40, 41, 127, 128] + [int(r) for r in g.integers(0, 6000, 20)] + [5999])
     lens = [int(x) for x in g.integers(1, 60, 150)]
-    a = Paged(B, 64, 64, 64, [int(x) for x in g.integers(0, 300, 150)], lens, fmt, page=16, gap=1)
+    a = Paged(B, 32, 32, 64, [int(x) for x in g.integers(0, 300, 150)], lens, fmt, page=16, gap=1)
     rows = sorted(int(a.row0[s] + g.integers(0, lens[s])) for s in range(0, 150, 5))
     sampled(a, rows)
     Paged(B, 8, 2, 128, [20000, 0, 7, 15000], [5, 300, 2, 40], fmt, page=32, gap=2).check()
