@@ -125,18 +125,19 @@ __device__ __forceinline__ uint32_t pack_w(float a, float b) {
     return h2u(a, b);
   }
 }
-__device__ __forceinline__ float pow2f(int e) { return ldexpf(1.f, e); }   // (rare: any e)
 
 // Eight e4m3 codes times f to f16. FAST: f is an f16 value.
 template <bool FAST>
 __device__ __forceinline__ uint4 codes_to_half(const uint2 c, float f) {
-  const uint32_t w[2] = {c.x, c.y};
   uint32_t h[4];
+  widen4(c.x, h[0], h[1]);
+  widen4(c.y, h[2], h[3]);
+  const __half2 f2 = __float2half2_rn(f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2 x = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3));
+    const __half2 x = *reinterpret_cast<const __half2*>(&h[i]);
     if constexpr (FAST) {
-      const __half2 y = __hmul2(x, __float2half2_rn(f));
+      const __half2 y = __hmul2(x, f2);
       h[i] = *reinterpret_cast<const uint32_t*>(&y);
     } else {
       const float2 z = __half22float2(x);
@@ -585,7 +586,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
           const int top = max(max(w4[0], w4[1]), max(w4[2], w4[3]));
           run = plane ? max(run, top) : top;
           const int E = run == NO_BOUND ? 0 : run;
-          const float fac = ldexpf(sc, 7 - E);                   // below 2^7
+          const int up = (7 - E) >> 1;                           // (2^(7 - E) itself may pass fp32's range)
+          const float fac = sc * pow2f(up) * pow2f(7 - E - up);  // below 2^7
           if (ok) ok = wwait(&empty[ks.s], ks.ph ^ 1);
           if (!ok) continue;
           uint8_t* dst = kvst + ks.s * L::TILE;
@@ -783,7 +785,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       float l = lo2(l2) + hi2(l2);
       if (li > 0 && !wwait(&o_done[x], (x ? dn1 : dn0) & 1)) return false;
       fence_after();
-      const float scale_o = E4 ? pow2f(unit - 7) : 1.f;
+      const float scale_o = E4 ? pow2f(unit - 7) : 1.f, mean = E4 ? (l == 0.f ? 0.f : 1.f / l) : 1.f;   // (SHARE: e4m3)
       float w0 = 1.f, w1 = 0.f;                  // weights of the two streams' sums
       const bool publish = !pair && x == 1;      // (o, m, l) into the K/V stages, for stream 0
       if (publish) {                             // once stream 0 has read its last tile from them, and the sums of the item before
@@ -798,12 +800,18 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
           w0 = has0 ? ex2(m - M) : 0.f;
           w1 = has1 ? ex2(ml.x - M) : 0.f;
           if (m == ml.x) w0 = has0 ? 1.f : 0.f, w1 = has1 ? 1.f : 0.f;   // (also both infinite)
-          l = (has0 ? w0 * l : 0.f) + (has1 ? w1 * ml.y : 0.f);
+          const float l0 = has0 ? w0 * l : 0.f, l1 = has1 ? w1 * ml.y : 0.f;
+          l = l0 + l1;
           m = M;
+          if constexpr (E4) {                    // of the means
+            const float one = l == 0.f ? 0.f : 1.f / l;
+            w0 = l0 * one;
+            w1 = l1 * one;
+          }
         }
       }
       if (!idle && !none) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = E4 ? 1.f : l == 0.f ? 0.f : 1.f / l;
         const bool fix = rw.live && !publish && *v_flag;   // non-finite values of partly hidden tiles: into the rows that see them
         const int64_t pi = (int64_t)ie.w * 2 + (pair ? x : 0);
         constexpr int CW = E4 ? 16 : 32, PIECES = CW / 8;   // columns at a time (e4m3: 96 registers a thread)
@@ -820,7 +828,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
             pin<CW>(u);
           }
 #pragma unroll
-          for (int e = 0; e < CW; ++e) u[e] = li > 0 ? __float_as_uint(__uint_as_float(u[e]) * scale_o) : 0u;
+          for (int e = 0; e < CW; ++e) u[e] = li > 0 ? __float_as_uint(E4 ? __uint_as_float(u[e]) * mean * scale_o : __uint_as_float(u[e])) : 0u;
           float4* at = reinterpret_cast<float4*>(pub + c);
           if (publish) {
 #pragma unroll
@@ -909,11 +917,11 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
 }
 
 // Joins the parts of a row, m their bases: M = max m, o = sum 2^(m - M) o / sum 2^(m - M) l. A part without a
-// visible key (m = -inf, l = 0) holds no sums. A block joins 32 rows x 8 columns; warp w takes the parts w, w + W, ...,
+// visible key (m = -inf, l = 0) holds no sums. MEANS: o / l instead of o (SHARE). A block joins 32 rows x 8 columns; warp w takes the parts w, w + W, ...,
 // and the W sums are joined through shared memory: every order is fixed by the sizes. A warp's reads are issued together.
 constexpr int CWARPS = 8, CCOLS = 8;
 __device__ __forceinline__ float part_weight(float m, float M) { return m == M ? 1.f : t5::ex2(m - M); }
-template <int HD, bool OBF, int N>
+template <int HD, bool OBF, bool MEANS, int N>
 __global__ void __launch_bounds__(CWARPS * 32, 4)
     combine_kernel(const __grid_constant__ Tab<N> tab, const __grid_constant__ PagedAttnArgs a, const Plan pl) {
   __shared__ float4 po[CWARPS][CCOLS / 4][36];
@@ -958,12 +966,13 @@ __global__ void __launch_bounds__(CWARPS * 32, 4)
       const float M = fmaxf(m, x[k].x), wo = part_weight(m, M), wp = part_weight(x[k].x, M);
       m = M;
       l = wo * l + wp * x[k].y;
+      const float ws = MEANS ? wp * x[k].y * SHARE : wp;
 #pragma unroll
       for (int c = 0; c < CCOLS / 4; ++c) {
-        o[c].x = wo * o[c].x + wp * v[k][c].x;
-        o[c].y = wo * o[c].y + wp * v[k][c].y;
-        o[c].z = wo * o[c].z + wp * v[k][c].z;
-        o[c].w = wo * o[c].w + wp * v[k][c].w;
+        o[c].x = wo * o[c].x + ws * v[k][c].x;
+        o[c].y = wo * o[c].y + ws * v[k][c].y;
+        o[c].z = wo * o[c].z + ws * v[k][c].z;
+        o[c].w = wo * o[c].w + ws * v[k][c].w;
       }
     }
   }
@@ -986,7 +995,7 @@ __global__ void __launch_bounds__(CWARPS * 32, 4)
       y0 += wp * v.x;
       y1 += wp * v.y;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : (MEANS ? UNSHARE : 1.f) / sum;
     *reinterpret_cast<uint32_t*>((uint16_t*)a.out + out_at(r) + cp * 2) = pack_w<OBF>(y0 * inv, y1 * inv);
   }
 }
@@ -1127,7 +1136,7 @@ cudaError_t launch_tab(const PagedAttnArgs& a, const Tab<N>& tab, const Plan& pl
   CK_RET(launch_pdl(paged_kernel<HD, KIND, N>, dim3((unsigned)std::min(tab.start[tab.n], num_sms)), dim3(threads_of(KIND)),
                     L::BYTES, st, tab, map, map_q, a, pl));
   if (max_ns > 1)
-    CK_RET(launch_pdl(combine_kernel<HD, out_bf16(KIND), N>, dim3((unsigned)(tab.tiles[tab.n] * (HD / CCOLS * 4))),
+    CK_RET(launch_pdl(combine_kernel<HD, out_bf16(KIND), is_e4m3(KIND), N>, dim3((unsigned)(tab.tiles[tab.n] * (HD / CCOLS * 4))),
                       dim3((unsigned)(32 * std::min(CWARPS, (max_ns + 1) / 2))), 0, st, tab, a, pl));
   return cudaSuccess;
 }

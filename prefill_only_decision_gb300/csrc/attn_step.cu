@@ -20,7 +20,8 @@
 // their order, so both products take the codes in the order in which wide shared-memory reads find them: row
 // n of an 8-row block of S^T stands for cached row key8(n), and thread (g, t) holds chunk t of a K row (16 d's as four
 // k-steps) and chunk g of V rows (16 columns). K scales multiply the scores. V scales go into the weights as exponents: the
-// base is a running bound of z + e (V's scale 2^e f, f in [1/2, 1)), so neither f16 nor the sums see the scales' range.
+// base is a running bound of z + e (V's scale 2^(unit + e) f, f in [1/2, 1), unit a warp's first), so neither f16 nor the sums see
+// the scales' range.
 // bf16 queries over e4m3 pages become f16 by a power of two per q head.
 #include <algorithm>
 #include <climits>
@@ -36,6 +37,7 @@ using namespace t5;
 using namespace pga;
 
 constexpr int KT = 64, PRODUCERS = 3;
+constexpr int NO_UNIT = -10000;
 constexpr int LANE_SEQS = 8;                 // up to 32 times as many sequences are counted by each warp alone
 enum Kind { F16 = 0, BF16 = 1, E4M3 = 2 };
 
@@ -66,7 +68,7 @@ struct StepArgs {
 };
 
 // Part slots of the workspace: slot 2 c for the pair that CTA c's run continues, 2 c + 1 for the one that it starts and does not
-// end; 16 rows of hd sums, then 16 (m, l). Behind them a record for each CTA: the pair whose last tile its run holds.
+// end; 16 q heads of hd sums (means with e4m3 pages), then 16 (m, l). Behind them a record for each CTA: the pair whose last tile its run holds.
 struct Record {
   int seq, hg, first, valid;   // first: the CTA with the pair's first tile
 };
@@ -110,12 +112,6 @@ __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
-}
-// Four e4m3 codes to two f16 pairs.
-__device__ __forceinline__ void widen4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(codes));
 }
 template <bool BF>
 __device__ __forceinline__ uint32_t pack_w(float a, float b) {
@@ -421,6 +417,7 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
       if (AHEAD && more) load_q(nx);                           // (used when this pair has ended)
       float o[NH][HD / 16][4] = {};
       float mx[NH][2], sum[NH][2] = {};                        // base and sum of q heads 8 nh + 2 t + e
+      int unit = NO_UNIT;                                      // e4m3: O counts 2^unit, the bound of the first scales seen
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh) mx[nh][0] = mx[nh][1] = -INFINITY;
       for (int x = (grp - i % GROUPS + GROUPS) % GROUPS; x < m && ok; x += GROUPS) {
@@ -478,9 +475,11 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
               const float* sc = (const float*)(sm + L::SC) + st * 2 * KT + sub * 16 + r;
               ks[b] = sc[0];
               const uint32_t u = __float_as_uint(sc[KT]);
-              const int E = (int)(u >> 23) - 126;              // (scales below 2^-81: the rest stays in f)
-              ex[b] = (float)max(E, -80);
-              f[b] = E >= -80 ? __uint_as_float((u & 0x7fffffu) | 126u << 23) : sc[KT] * 1.208925819614629e24f;
+              const int E = (int)(u >> 23) - 126;
+              if (unit == NO_UNIT) unit = __reduce_max_sync(0xffffffffu, hid[b] ? NO_UNIT : E);
+              const int rel = E - unit, up = (80 - unit) >> 1;   // (2^-80 below the unit: the rest stays in f)
+              ex[b] = (float)max(rel, -80);
+              f[b] = rel >= -80 ? __uint_as_float((u & 0x7fffffu) | 126u << 23) : sc[KT] * pow2f(up) * pow2f(80 - unit - up);
             }
           }
           uint32_t p[NH][2];                                   // P^T: rows 2 t, 2 t + 1 of each block, q head g
@@ -608,6 +607,15 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
           if (g == 0) ml[warp * 8 + 2 * t4 + e] = make_float2(mx[half][e], l);
           float* at = pub + (warp * 8 + 2 * t4 + e) * L::OSTR;
           if (8 * half + 2 * t4 + e >= nq) continue;           // (no such q head)
+          if constexpr (KIND == E4M3) {
+            const float inv = l == 0.f || unit == NO_UNIT ? 0.f : 1.f / l, u0 = pow2f(max(unit, -200) >> 1),
+                        u1 = pow2f(max(unit, -200) - (max(unit, -200) >> 1));
+#pragma unroll
+            for (int b = 0; b < HD / 16; ++b) {
+              o[half][b][e] = o[half][b][e] * inv * u0 * u1;
+              o[half][b][2 + e] = o[half][b][2 + e] * inv * u0 * u1;
+            }
+          }
 #pragma unroll
           for (int b = 0; b < HD / 16; ++b) {
             at[out_col<HD, KIND>(b, g, 0)] = o[half][b][e];
@@ -630,13 +638,18 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
             const float wt = z.x == M ? 1.f : ex2(z.x - M);
             const float4 v = *reinterpret_cast<const float4*>(pub + (w * 8 + r) * L::OSTR + cv * 4);
             lsum += wt * z.y;
-            y.x += wt * v.x;
-            y.y += wt * v.y;
-            y.z += wt * v.z;
-            y.w += wt * v.w;
+            const float wo = KIND == E4M3 ? wt * z.y * SHARE : wt;
+            y.x += wo * v.x;
+            y.y += wo * v.y;
+            y.z += wo * v.z;
+            y.w += wo * v.w;
+          }
+          if constexpr (KIND == E4M3) {                        // a mean again
+            const float inv = lsum == 0.f ? 0.f : UNSHARE / lsum;
+            y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
           }
           if (starts && ends) {
-            const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+            const float inv = KIND == E4M3 ? 1.f : lsum == 0.f ? 0.f : 1.f / lsum;
             *reinterpret_cast<uint2*>((uint16_t*)a.out + ((int64_t)c.s * a.Hq + h0 + 8 * half + r) * HD + cv * 4) =
                 make_uint2(pack_w<QBF>(y.x * inv, y.y * inv), pack_w<QBF>(y.z * inv, y.w * inv));
           } else {
@@ -666,7 +679,7 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
 // Joins the parts of the pair that CTA blockIdx.x of the step ended: slot 2 first + 1, then slots 2 c of the CTAs behind it.
 // Block y takes rows y, y + gridDim.y, ...; its warps take the parts in turn, and their sums are joined in order.
 constexpr int JWARPS = 8;
-template <int HD, bool QBF, int NH>
+template <int HD, bool QBF, int NH, bool MEANS>
 __global__ void __launch_bounds__(JWARPS * 32) join_kernel(const __grid_constant__ StepArgs sa, int C) {
   __shared__ float4 py[JWARPS][32];
   __shared__ float2 pml[JWARPS];
@@ -689,7 +702,8 @@ __global__ void __launch_bounds__(JWARPS * 32) join_kernel(const __grid_constant
       const float N = fmaxf(M, z.x), a0 = M == N || l == 0.f ? 1.f : ex2(M - N), a1 = z.x == N ? 1.f : ex2(z.x - N);
       M = N;
       l = a0 * l + a1 * z.y;
-      y = make_float4(a0 * y.x + a1 * v.x, a0 * y.y + a1 * v.y, a0 * y.z + a1 * v.z, a0 * y.w + a1 * v.w);
+      const float wo = MEANS ? a1 * z.y * SHARE : a1;
+      y = make_float4(a0 * y.x + wo * v.x, a0 * y.y + wo * v.y, a0 * y.z + wo * v.z, a0 * y.w + wo * v.w);
     }
     py[w][lane] = y;
     if (lane == 0) pml[w] = make_float2(M, l);
@@ -706,7 +720,7 @@ __global__ void __launch_bounds__(JWARPS * 32) join_kernel(const __grid_constant
         s += wt * z.y;
         o = make_float4(o.x + wt * v.x, o.y + wt * v.y, o.z + wt * v.z, o.w + wt * v.w);
       }
-      const float inv = s == 0.f ? 0.f : 1.f / s;
+      const float inv = s == 0.f ? 0.f : (MEANS ? UNSHARE : 1.f) / s;
       *reinterpret_cast<uint2*>((uint16_t*)sa.a.out + ((int64_t)rec.seq * sa.a.Hq + h0 + r) * HD + lane * 4) =
           make_uint2(pack_w<QBF>(o.x * inv, o.y * inv), pack_w<QBF>(o.z * inv, o.w * inv));
     }
@@ -721,7 +735,7 @@ cudaError_t launch(const StepArgs& sa, int num_sms, cudaStream_t st) {
   if (!pages_map(&map, sa.a.pages, std::min(KT, 1 << sa.a.pages.shift))) return cudaErrorInvalidValue;
   CK_RET(cudaFuncSetAttribute(step_kernel<HD, KIND, QBF, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES));
   CK_RET(launch_pdl(step_kernel<HD, KIND, QBF, NH>, dim3((unsigned)num_sms), dim3(L::THREADS), L::BYTES, st, map, sa));
-  return launch_pdl(join_kernel<HD, QBF, NH>, dim3((unsigned)num_sms, 4), dim3(JWARPS * 32), 0, st, sa, num_sms);
+  return launch_pdl(join_kernel<HD, QBF, NH, KIND == E4M3>, dim3((unsigned)num_sms, 4), dim3(JWARPS * 32), 0, st, sa, num_sms);
 }
 template <int HD, int KIND, bool QBF>
 cudaError_t launch_nh(const StepArgs& sa, int num_sms, cudaStream_t st) {

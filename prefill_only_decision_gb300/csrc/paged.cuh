@@ -58,6 +58,21 @@ __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(t5::smem_u32(bar)) : "memory");
 }
 
+// Four e4m3 codes to two f16 pairs.
+__device__ __forceinline__ void widen4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+}
+// 2^e, e at most 127.
+__device__ __forceinline__ float pow2f(int e) {
+  return __uint_as_float(e >= -126 ? (uint32_t)(e + 127) << 23 : e >= -149 ? 1u << (e + 149) : 0u);
+}
+
+// Sums over e4m3 pages pass between warps, CTAs and kernels as means (o / l), since V's scales may leave fp32 no room beside the
+// weights; such a mean's share is its l times 2^-SHARE, which leaves room on both sides.
+constexpr float SHARE = 9.5367431640625e-7f, UNSHARE = 1048576.f;   // 2^-20, 2^20
+
 // The pages as a tensor (hd, page rows, heads, pages, planes) in boxes of `rows` rows of up to 128 bytes. A page id outside
 // 0 .. n_pages - 1 is outside the tensor, which TMA reads as zeros.
 inline bool pages_map(CUtensorMap* map, const PagesArgs& p, int rows) {

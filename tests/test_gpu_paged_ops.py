@@ -490,6 +490,19 @@ def test_8_bit_scales_out_of_the_ordinary(B, kind):
 
 
 @pytest.mark.parametrize("kind", ["step", "prompt"])
+def test_8_bit_scales_at_the_ends_of_their_range(B, kind):
+    """All K scales near fp32's smallest (the queries bring the scores back) and V scales near its smallest or largest, bf16."""
+    for ek, ev in ((-116, -110), (-100, 112), (90, 0)):
+        a = Paged(B, 4, 1, 64, [140], None if kind == "step" else [40], "e4m3", page=16, q_type="bf16")
+        pid, off = (torch.from_numpy(t.astype(np.int64)).cuda() for t in a.c.places(0, len(a.c.rows[0][0])))
+        for plane, e in ((0, ek), (1, ev)):
+            a.c.scales[plane][pid, :, off] *= 2.0 ** e
+            a.c.rows[0][plane] *= 2.0 ** e
+        a.q *= 2.0 ** -ek
+        a.check()
+
+
+@pytest.mark.parametrize("kind", ["step", "prompt"])
 @pytest.mark.parametrize("fmt", ["f16", "bf16", "e4m3"])
 def test_hidden_rows_do_not_matter(B, kind, fmt):
     """NaN in keys and values that a window hides, or that lie ahead, reaches only the rows that see them."""
