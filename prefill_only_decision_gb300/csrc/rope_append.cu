@@ -17,9 +17,11 @@
 
 #include "common.cuh"
 #include "kvrows.cuh"
+#include "tcgen05.cuh"
 
 namespace s1 {
 namespace rap {
+using namespace t5;
 using kvc::Raw;
 
 constexpr int THREADS = 256, RB_MAX = 16, PASSES = 4;         // rows of a tile; angles of a tile that a thread makes
@@ -76,6 +78,15 @@ __device__ __forceinline__ void store8(void* base, int64_t off, int type, const 
     }
   }
 }
+// Two pairs (lo[i], hi[i]) turned at once.
+__device__ __forceinline__ void turn2(float* lo, float* hi, uint64_t c, uint64_t s, uint64_t minus_s) {
+  const uint64_t a = pack2(lo[0], lo[1]), b = pack2(hi[0], hi[1]);
+  const uint64_t x = fma2(a, c, mul2(b, minus_s)), y = fma2(b, c, mul2(a, s));
+  lo[0] = lo2(x);
+  lo[1] = hi2(x);
+  hi[0] = lo2(y);
+  hi[1] = hi2(y);
+}
 template <typename T>
 __device__ __forceinline__ void widen(const Raw<T>& r, float* x) {
   T t[8];
@@ -96,7 +107,7 @@ constexpr int blocks_of(size_t es) { return es == 4 ? 3 : 4; }
 template <typename T, int HD, bool VEC, bool APPEND, int U>
 __global__ void __launch_bounds__(THREADS, blocks_of(sizeof(T))) rows_kernel(const __grid_constant__ RowsArgs a, int rb, int hb, bool out_vec) {
   constexpr int NU = HD / 16;
-  __shared__ float4 cs[2][RB_MAX * MAX_PAIRS / 2];           // (cos, sin) pairs, by tile parity
+  __shared__ float4 cs[2][RB_MAX][2][MAX_PAIRS / 4];         // cosines, then sines, by tile parity and row
   __shared__ int64_t place[2][RB_MAX];                       // of a row in a plane of pages: vector (head 0); -1: none
   __shared__ int live[2][RB_MAX];
   allow_dependents();
@@ -186,8 +197,12 @@ __global__ void __launch_bounds__(THREADS, blocks_of(sizeof(T))) rows_kernel(con
     if (angles)
 #pragma unroll
       for (int i = 0; i < PASSES; ++i)
-        if (trow + i * rstep < rb)
-          reinterpret_cast<float2*>(cs[buf])[(trow + i * rstep) * MAX_PAIRS + tpair] = cos_sin(pos[i], turn);
+        if (trow + i * rstep < rb) {
+          const float2 t = cos_sin(pos[i], turn);
+          float* at = reinterpret_cast<float*>(cs[buf][trow + i * rstep]) + tpair;
+          at[0] = t.x;
+          at[MAX_PAIRS] = t.y;
+        }
     if (APPEND && threadIdx.x < rb) {
       place[buf][threadIdx.x] = id < 0 ? -1 : (((int64_t)id * a.pages.Hkv) << a.pages.shift) + (w.j & ((1 << a.pages.shift) - 1));
       live[buf][threadIdx.x] = w.j >= 0;
@@ -206,15 +221,11 @@ __global__ void __launch_bounds__(THREADS, blocks_of(sizeof(T))) rows_kernel(con
         widen(x[u][1], hi);
         const int n8 = pairs8(h[u]), c0 = chunk0(unit, n8), c1 = chunk1(unit, n8), r = max(row[u], 0);
         if (unit < n8) {
-          const float4* t = cs[buf] + (r * MAX_PAIRS + c0 * 8) / 2;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 w = t[e];
-            const float a0 = lo[2 * e], b0 = hi[2 * e], a1 = lo[2 * e + 1], b1 = hi[2 * e + 1];
-            lo[2 * e] = a0 * w.x - b0 * w.y;
-            hi[2 * e] = b0 * w.x + a0 * w.y;
-            lo[2 * e + 1] = a1 * w.z - b1 * w.w;
-            hi[2 * e + 1] = b1 * w.z + a1 * w.w;
+          for (int e = 0; e < 2; ++e) {
+            const float4 c = cs[buf][r][0][c0 * 2 + e], s = cs[buf][r][1][c0 * 2 + e];
+            turn2(lo + 4 * e, hi + 4 * e, pack2(c.x, c.y), pack2(s.x, s.y), pack2(-s.x, -s.y));
+            turn2(lo + 4 * e + 2, hi + 4 * e + 2, pack2(c.z, c.w), pack2(s.z, s.w), pack2(-s.z, -s.w));
           }
         }
         bool in = row[u] >= 0;
