@@ -9,8 +9,9 @@
 // One pass over the keys with a running base (near the maximum) and sum in fp32, in two streams of S = Q K^T, softmax,
 // O += P V that share the tensor cores: two query tiles over the same key tiles, or one query tile over the even and the odd
 // key tiles, joined at the end. A stream takes a key tile in two halves of 64 keys with S in TMEM columns of their own, so that
-// products run while the softmax works on the other half. One CTA per SM, 15 warps (19 with e4m3 pages):
-//   warp 0      TMA producer: a page box (page x 64 elements) per lane, page ids asked for a tile ahead
+// products run while the softmax works on the other half. One CTA per SM, 16 warps (19 with e4m3 pages):
+//   warps 0, 15 TMA producers: Q and K, and V: a page box (page x 64 elements) per lane, page ids asked for a tile ahead (one warp
+//               for both: 16-row pages 450 us where 32-row ones took 376)
 //   warps 1, 14 MMA issue of stream 0 and 1
 //   warps 2-5, 6-9  softmax of stream 0, 1: one thread per row (TMEM lane), 64 scores in registers, a lazy rescale of O; P
 //               goes back into the TMEM columns of S and is the A operand of O += P V from there
@@ -40,7 +41,7 @@ constexpr int BQ = 128, BKV = 128, TAB_SMALL = 64, TAB_LARGE = 1024;
 enum Kind { F16 = 0, BF16 = 1, E4M3 = 2, E4M3_QBF = 3 };
 constexpr bool is_e4m3(int kind) { return kind >= E4M3; }
 constexpr bool out_bf16(int kind) { return kind == BF16 || kind == E4M3_QBF; }
-constexpr int threads_of(int kind) { return (is_e4m3(kind) ? 19 : 15) * 32; }
+constexpr int threads_of(int kind) { return (is_e4m3(kind) ? 19 : 16) * 32; }
 constexpr int TMEM_COLS = 512;               // S of stream x at 128 x, O at 256 + 128 x
 constexpr int T_O = 256;
 constexpr int ITEMS = 18;                    // of a CTA's items, kept in shared memory (later ones are made when their turn comes)
@@ -344,26 +345,18 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
   auto slot = [&](int t, bool is_v, int t0, int t1) {
     return pair ? slot_of<F, FR>(true, 0, t0 + t, is_v) : slot_of<F, FR>(false, t & 1, (t & 1 ? t1 : t0) + (t >> 1), is_v);
   };
-  // an item's fills in the order in which they are made: K_0 .. K_{lead-1}, then V_t, K_{t+lead}
-  const int lead = pair ? 1 : 2;
-  auto fills = [&](int n, auto&& fn) {
-    for (int q = 0; q < 2 * n + lead - 1; ++q) {
-      const int e = q - lead;
-      const bool is_v = e >= 0 && !(e & 1);
-      const int t = e < 0 ? q : is_v ? e >> 1 : lead + (e >> 1);
-      if (!fn(t, is_v)) return false;
-    }
-    return true;
-  };
-
-  uint32_t done = 0;           // (producer) per slot and kind: begun (bit d), parity of the last fill (bit 16 + d)
+  uint32_t done = 0;           // (producers) per slot: begun (bit s), parity of the last fill of their kind (bit 16 + s)
   int q_done = 0;              // (producer) Q fills
-  if (warp == 0) {
-    // ---- TMA producer: Q, and with 16-bit pages the K and V tiles
+  if (warp == 0 || (!E4 && warp == 15)) {
+    // ---- TMA producers: Q, and with 16-bit pages the K tiles and (warp 15) the V tiles. A producer sees every second fill of a
+    // slot only; a parity wait needs all fills but the last to be over, and they are: the producer's own last tile came
+    // after the consumption of an item behind those.
     wait_prerequisites();
+    const bool is_v = warp == 15;
+    uint64_t* bar = is_v ? vfull : full;
     const int npg = BKV >> pg.shift, box = lane % NB, pp = lane / NB;
     each_item([&](const Item& it, int k, int t0, int t1) {
-      if constexpr (QTMA) {
+      if (QTMA && !is_v) {
         if (!wwait(q_empty, (k & 1) ^ 1)) return false;
         const int tiles = it.two ? 2 : 1;
         if (lane == 0) mbar_expect_tx(q_full, (uint32_t)(tiles * NB * pl.G * pl.RT * 128));
@@ -382,28 +375,21 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         const int col = (it.tile(t) >> pg.shift) + pp;
         return col <= last ? pg.table[trow + col] : -1;
       };
-      int id_next = page_id(0), id = -1, id_before = -1;      // of the K tile to come, of the latest and of the one before it
-      return fills(it.n, [&](int t, bool is_v) {
-        if (!is_v) {
-          id_before = id;
-          id = id_next;
-        }
-        if (t >= it.n) return true;
+      int next = page_id(0);                   // asked for a tile ahead
+      for (int t = 0; t < it.n; ++t) {
         const Slot sl = slot(t, is_v, t0, t1);
-        const int s = sl.s, j0 = it.tile(t), pid = is_v && lead == 2 ? id_before : id;
+        const int s = sl.s, j0 = it.tile(t), id = next;
+        next = page_id(t + 1);
         if (!wwait(&empty[s], sl.ph ^ 1)) return false;
         const int there = min(npg, last - (j0 >> pg.shift) + 1);   // pages that the sequence has
-        uint64_t* bar = is_v ? &vfull[s] : &full[s];
-        if (lane == 0) mbar_expect_tx(bar, (uint32_t)(there << pg.shift) * (HD * 2));
+        if (lane == 0) mbar_expect_tx(&bar[s], (uint32_t)(there << pg.shift) * (HD * 2));
         __syncwarp();
         if (pp < there)
-          tma5(kvst + s * L::TILE + box * (BKV * 128) + (pp << pg.shift) * 128, &mapKV, bar, 64 * box, 0, it.g, pid,
+          tma5(kvst + s * L::TILE + box * (BKV * 128) + (pp << pg.shift) * 128, &mapKV, &bar[s], 64 * box, 0, it.g, id,
                is_v ? 1 : 0);
-        const int d = 2 * s + (is_v ? 1 : 0);
-        done = (done & ~(1u << (16 + d))) | 1u << d | sl.kind_ph << (16 + d);
-        if (!is_v) id_next = page_id(t + 1);
-        return true;
-      });
+        done = (done & ~(1u << (16 + s))) | 1u << s | sl.kind_ph << (16 + s);
+      }
+      return true;
     });
   } else if (warp == 1 || warp == 14) {
     // ---- MMA issue of stream x: the whole warp waits, one lane issues. A stream's products run in
@@ -435,13 +421,12 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       if (pair && x && !it.two) {              // no second tile: its share of the stages' release
         if (!wwait(q_full, k & 1)) return false;   // (an arrival must not count for the item before)
         if (lane == 0) mbar_arrive(q_empty);
-        return fills(it.n, [&](int t, bool is_v) {
-          if (t >= it.n) return true;
-          const Slot sl = slot(t, is_v, t0, t1);
-          if (!wwait(is_v ? &vfull[sl.s] : &full[sl.s], sl.kind_ph)) return false;
+        for (int t = 0; t < 2 * it.n; ++t) {
+          const Slot sl = slot(t >> 1, t & 1, t0, t1);
+          if (!wwait(t & 1 ? &vfull[sl.s] : &full[sl.s], sl.kind_ph)) return false;
           if (lane == 0) mbar_arrive(&empty[sl.s]);
-          return true;
-        });
+        }
+        return true;
       }
       // of each half h: P V of tile i - 1, then S of tile i into the same columns
       const int cnt = pair ? it.n : (it.n + 1 - x) >> 1, before = x ? t1 : t0;
@@ -487,7 +472,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       commit(&mma_idle[x]);
       mbar_drain(&mma_idle[x], 0);             // every MMA issued above has completed
     }
-  } else if (warp >= 10 && warp != 14) {
+  } else if (warp >= 10) {
     const int lw = warp < 14 ? warp - 10 : warp - 15;
     wait_prerequisites();
     if constexpr (!E4) {
@@ -905,10 +890,10 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
     });
   }
   __syncthreads();
-  if (warp == 0 && *abort_flag) {              // nothing in flight when the CTA leaves
+  if ((warp == 0 || warp == 15) && *abort_flag) {   // nothing in flight when the CTA leaves
     if (q_done) mbar_drain(q_full, (q_done - 1) & 1);
-    for (int d = 0; d < 2 * NS; ++d)
-      if ((done >> d) & 1) mbar_drain(d & 1 ? &vfull[d >> 1] : &full[d >> 1], (done >> (16 + d)) & 1);
+    for (int s = 0; s < NS; ++s)
+      if ((done >> s) & 1) mbar_drain(warp ? &vfull[s] : &full[s], (done >> (16 + s)) & 1);
   }
   if (warp == 1) {
     fence_after();
