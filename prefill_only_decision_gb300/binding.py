@@ -624,7 +624,7 @@ def _ref(spec):
 def op_rope_async(x: int, dtype: int, x_stride: int, n_rows: int, H: int, hd: int, rope: Rope, pos: int, pos_stride: int,
                   out: int, out_dtype: int, out_stride: int, stream: int = 0):
     """Rotary positions with one or several axes (s1_op_rope_async)."""
-    _fits(n_rows | H | hd)
+    _fits(n_rows | H | hd | dtype | out_dtype)
     check(lib().s1_op_rope_async(x, dtype, x_stride, n_rows, H, hd, _ref(rope), pos, pos_stride, out, out_dtype,
                                  out_stride, stream))
 
@@ -633,7 +633,7 @@ def op_kv_append_async(q: int, k: int, v: int, dtype: int, q_stride: int, k_stri
                        Hq: int, rope: Optional[Rope], pos: int, pos_stride: int, seq: int, at: int, pages: KvPages,
                        q_out: int, q_dtype: int, stream: int = 0):
     """Append rotated keys, and values, to a paged cache (s1_op_kv_append_async)."""
-    _fits(n_rows | Hq)
+    _fits(n_rows | Hq | dtype | q_dtype)
     check(lib().s1_op_kv_append_async(q, k, v, dtype, q_stride, k_stride, v_stride, n_rows, Hq, _ref(rope), pos,
                                       pos_stride, seq, at, _ref(pages), q_out, q_dtype, stream))
 
@@ -642,7 +642,7 @@ def op_attention_paged_step_async(q: int, q_dtype: int, q_stride: int, n: int, H
                                   window: int, sinks: int, sm_scale: float, out: int, workspace: int,
                                   workspace_bytes: int, stream: int = 0):
     """Attention of one new token of each sequence over its pages (s1_op_attention_paged_step_async)."""
-    _fits(n | Hq | window | sinks)
+    _fits(n | Hq | window | sinks | q_dtype)
     check(lib().s1_op_attention_paged_step_async(q, q_dtype, q_stride, n, Hq, _ref(pages), pos, window, sinks, sm_scale,
                                                  out, workspace, workspace_bytes, stream))
 
@@ -659,7 +659,7 @@ def op_attention_paged_async(q: int, q_dtype: int, q_stride: int, row0, lens, po
                              sinks: int, sm_scale: float, out: int, workspace: int, workspace_bytes: int,
                              stream: int = 0):
     """Attention of prompt rows over their pages (s1_op_attention_paged_async)."""
-    _fits(Hq | window | sinks)
+    _fits(Hq | window | sinks | q_dtype)
     r0, ln = _seq_arrays(row0, lens)
     p0 = _seq_i32(pos0)
     if p0.shape != ln.shape:

@@ -1,28 +1,33 @@
 // Attention of prompts over a paged K/V cache, with a sliding window and sinks, on the 5th-generation tensor cores.
 //
-// Query row i of sequence s, at position p, sees the cached rows j <= p with p - j < window or j < sinks:
-// o = softmax(scale q.k) v. The rows of a sequence and the G = Hq / Hkv q heads that share a kv head are packed into tiles of
-// 128 matrix rows, RT = floor(128 / G) query rows x G heads. An item is (sequence, tile or two neighbouring tiles, kv head) with
-// the 128-key tiles that its rows see: the sinks' and the window's. Its key tiles are split over `ns` CTAs, one choice per
-// sequence, when that shortens the call, and combine_kernel joins their (o, m, l) in an order that the sizes fix.
+// Query row i of sequence s, at position p, sees the cached rows j <= p with p - j < window or j < sinks: o =
+// softmax(scale q.k) v. The rows of a sequence and the G = Hq / Hkv q heads that share a kv head are packed into
+// tiles of 128 matrix rows, RT = floor(128 / G) query rows x G heads. An item is (sequence, tile or two neighbouring
+// tiles, kv head) with the 128-key tiles that its rows see: the sinks' and the window's. Its key tiles are split over
+// `ns` CTAs, one choice per sequence, when that shortens the call, and combine_kernel joins their (o, m, l) in an
+// order that the sizes fix.
 //
-// One pass over the keys with a running base (near the maximum) and sum in fp32, in two streams of S = Q K^T, softmax,
-// O += P V that share the tensor cores: two query tiles over the same key tiles, or one query tile over the even and the odd
-// key tiles, joined at the end. A stream takes a key tile in two halves of 64 keys with S in TMEM columns of their own, so that
-// products run while the softmax works on the other half. One CTA per SM, 16 warps (19 with e4m3 pages):
-//   warps 0, 15 TMA producers: Q and K, and V: a page box (page x 64 elements) per lane, page ids asked for a tile ahead (one warp
-//               for both: 16-row pages 450 us where 32-row ones took 376)
+// One pass over the keys with a running base (near the maximum) and sum in fp32, in two streams of S = Q K^T,
+// softmax, O += P V that share the tensor cores: two query tiles over the same key tiles, or one query tile over the
+// even and the odd key tiles, joined at the end. A stream takes a key tile in two halves of 64 keys with S in TMEM
+// columns of their own, so that products run while the softmax works on the other half. One CTA per SM, 16 warps (19
+// with e4m3 pages):
+//   warps 0, 15 TMA producers: Q and K, and V: a page box (page x 64 elements) per lane, page ids asked for a tile
+//               ahead (one warp for both: 16-row pages 450 us where 32-row ones took 376)
 //   warps 1, 14 MMA issue of stream 0 and 1
-//   warps 2-5, 6-9  softmax of stream 0, 1: one thread per row (TMEM lane), 64 scores in registers, a lazy rescale of O; P
-//               goes back into the TMEM columns of S and is the A operand of O += P V from there
-//   warps 10-13 scan the value tiles that hold rows which some query does not see: a hidden row's weight is an exact zero, but
-//               0 x NaN is not, so non-finite elements there become 0 and the epilogue adds them to the rows that do see
-//               them. (Rows behind a sequence's end and pages that are not loaded are such rows.) With e4m3 pages they widen
-//               the K tiles instead and warps 15-18 the V tiles, codes from memory through registers.
-// e4m3 pages: the operands are f16, code x scale x 2^(7 - E), E a bound of the scales' exponents (K: of the tile; V: running,
-// so that O keeps one unit, rescaled when the bound grows): scales of any size fit f16, and a row 2^-27 below the largest keeps
-// its code's bits. bf16 queries over them become f16 by a power of two per row.
-// Every mbarrier wait is bounded; on expiry an error word is set and every role leaves.
+//   warps 2-5, 6-9  softmax of stream 0, 1: one thread per row (TMEM lane), 64 scores in registers, a lazy rescale
+//               of O; P goes back into the TMEM columns of S and is the A operand of O += P V from there
+//   warps 10-13 scan the value tiles that hold rows which some query does not see: a hidden row's weight is an exact
+//               zero, but 0 x NaN is not, so non-finite elements there become 0 and an item's end adds them to the
+//               rows that do see them. (Rows behind a sequence's end and pages that are not loaded are such rows.)
+//               With e4m3 pages they widen the K tiles instead and warps 15-18 the V tiles, codes from memory through
+//               registers.
+// CTAs stay and take items in rounds, the longest first: the next item's Q, K and V are on their way while the last
+// one's sums leave (a CTA per item: 16476 rows, window 2048, 240 us; so 202).
+// e4m3 pages: the operands are f16, code x scale x 2^(7 - E), E a bound of the scales' exponents (K: of the tile; V:
+// running, so that O keeps one unit, rescaled when the bound grows): scales of any size fit f16, and a row 2^-27
+// below the largest keeps its code's bits. bf16 queries over them become f16 by a power of two per row. Every
+// mbarrier wait is bounded; on expiry an error word is set and every role leaves.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -44,7 +49,7 @@ constexpr bool out_bf16(int kind) { return kind == BF16 || kind == E4M3_QBF; }
 constexpr int threads_of(int kind) { return (is_e4m3(kind) ? 19 : 16) * 32; }
 constexpr int TMEM_COLS = 512;               // S of stream x at 128 x, O at 256 + 128 x
 constexpr int T_O = 256;
-constexpr int ITEMS = 18;                    // of a CTA's items, kept in shared memory (later ones are made when their turn comes)
+constexpr int ITEMS = 18;                    // of a CTA's items, kept in shared memory (later ones: made in their turn)
 constexpr int BASES = 16;                    // tiles whose exponent bounds are kept (more than are ever in flight)
 
 __device__ uint64_t g_given_up;              // when a bounded wait last gave up, per device; never cleared
@@ -84,9 +89,9 @@ struct Lay {
   static_assert(F % 2 == 1 && FR % 2 == 1, "a slot holds K and V tiles in turn");
 };
 
-// A stage of the ring of K and V tiles K_0, V_0, K_1, ... With two query tiles both streams read one ring; with one, each
-// stream has its own, of its tiles: a parity wait must never run more than one phase ahead of a slot, nor behind it. For that
-// K and V fills have barriers of their own, too: who waits for one kind does not see the other's phases.
+// A stage of the ring of K and V tiles K_0, V_0, K_1, ... With two query tiles both streams read one ring; with one,
+// each stream has its own, of its tiles: a parity wait must never run more than one phase ahead of a slot, nor behind
+// it. For that K and V fills have barriers of their own, too: who waits for one kind does not see the other's phases.
 struct Slot {
   int s;
   uint32_t ph, kind_ph;        // parity of this fill, and of it among the slot's fills of its kind (they take turns)
@@ -163,9 +168,9 @@ __device__ __forceinline__ int bound_of(float scale) {
 
 // One of a CTA's items: (sequence, one or two query tiles, kv head) and a part of its key tiles.
 struct alignas(16) Item {
-  int w, ns, g, two;           // number in the list, parts of the sequence's items, kv head, whether there is a second query tile
-  int row0, seq, v0, v1;       // the sequence's first row of q, its row of the table; the item's first row and one past its last
-  int pos0, lo, sk, n;         // position of the sequence's first row; what some row sees: [0, sk) and [lo, end()); key tiles
+  int w, ns, g, two;           // number in the list, parts of the sequence's items, kv head, is there a second query tile
+  int row0, seq, v0, v1;       // the sequence's first row of q, its row of the table; the item's first row, one past its last
+  int pos0, lo, sk, n;         // position of the sequence's first row; some row sees: [0, sk) and [lo, end()); key tiles
   int head, sink0, tail0, pad;   // tile t: t < head: sink0 + t, else tail0 + t
   __device__ int p_first() const { return pos0 + v0; }
   __device__ int end() const { return pos0 + v1; }
@@ -232,9 +237,8 @@ __device__ __forceinline__ void add_nonfinite(const Item& it, const PagedAttnArg
       if constexpr (E4) {
 #pragma unroll
         for (int e = 0; e < CW; ++e) {
-          const float y =
-              __half2float(__half(__nv_cvt_fp8_to_halfraw(((const __nv_fp8_storage_t*)pg.data)[vec * pg.hd + c + e], __NV_E4M3))) *
-              pg.scales[vec];
+          const __nv_fp8_storage_t code = ((const __nv_fp8_storage_t*)pg.data)[vec * pg.hd + c + e];
+          const float y = __half2float(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3))) * pg.scales[vec];
           if (!isfinite(y)) add(o[e], y);
         }
       } else {
@@ -274,7 +278,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
   uint64_t* full = bars + 3;                   // [NS] a K tile is there
   uint64_t* vfull = full + NS;                 // [NS] a V tile is there
   uint64_t* empty = vfull + NS;                // [NS]
-  uint64_t* ready = empty + NS;                // [NS] the V tile holds no non-finite element of a hidden row (not with e4m3)
+  uint64_t* ready = empty + NS;                // [NS] the V tile is scanned (not with e4m3)
   uint64_t* s_full = ready + NS;               // [2 streams][2 halves of the key tile]
   uint64_t* p_full = s_full + 4;               // [2][2]
   uint64_t* o_step = p_full + 4;               // [2][2] the half's P V has completed
@@ -318,7 +322,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
   // every gridDim-th item of the list, there and back again, so that a list that grows cheaper stays even
   const int listed = tab.start[tab.n];
   auto number_of = [&](int k) { return k * (int)gridDim.x + (int)(k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x); };
-  const int rounds = (listed + (int)gridDim.x - 1) / (int)gridDim.x, items = rounds - (number_of(rounds - 1) >= listed ? 1 : 0);
+  const int rounds = (listed + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int items = rounds - (number_of(rounds - 1) >= listed ? 1 : 0);
   Item* table = reinterpret_cast<Item*>(sm + L::TABLE);
   if (threadIdx.x >= 64 && (int)threadIdx.x - 64 < min(items, ITEMS))
     table[threadIdx.x - 64] = item_of(tab, a, pl, number_of((int)threadIdx.x - 64));
@@ -348,9 +353,9 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
   uint32_t done = 0;           // (producers) per slot: begun (bit s), parity of the last fill of their kind (bit 16 + s)
   int q_done = 0;              // (producer) Q fills
   if (warp == 0 || (!E4 && warp == 15)) {
-    // ---- TMA producers: Q, and with 16-bit pages the K tiles and (warp 15) the V tiles. A producer sees every second fill of a
-    // slot only; a parity wait needs all fills but the last to be over, and they are: the producer's own last tile came
-    // after the consumption of an item behind those.
+    // ---- TMA producers: Q, and with 16-bit pages the K tiles and (warp 15) the V tiles. A producer sees every
+    // second fill of a slot only; a parity wait needs all fills but the last to be over, and they are: the producer's
+    // own last tile came after the consumption of an item behind those.
     wait_prerequisites();
     const bool is_v = warp == 15;
     uint64_t* bar = is_v ? vfull : full;
@@ -362,8 +367,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         if (lane == 0) mbar_expect_tx(q_full, (uint32_t)(tiles * NB * pl.G * pl.RT * 128));
         __syncwarp();
         if (lane < tiles * NB)
-          tma3(sm + L::Q + (lane / NB) * (BQ * HD * 2) + (lane % NB) * (BQ * 128), &mapQ, q_full, 64 * (lane % NB), it.g * pl.G,
-               it.row0 + it.v0 + (lane / NB) * pl.RT);
+          tma3(sm + L::Q + (lane / NB) * (BQ * HD * 2) + (lane % NB) * (BQ * 128), &mapQ, q_full, 64 * (lane % NB),
+               it.g * pl.G, it.row0 + it.v0 + (lane / NB) * pl.RT);
         q_done = k + 1;
       }
       if constexpr (E4) return true;
@@ -476,8 +481,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
     const int lw = warp < 14 ? warp - 10 : warp - 15;
     wait_prerequisites();
     if constexpr (!E4) {
-      // ---- scan of the partly hidden V tiles: rows 32 lw .. +31. Magnitudes' maximum first; a tile with something that is
-      // not finite (rare) once more, to take it out
+      // ---- scan of the partly hidden V tiles: rows 32 lw .. +31. Magnitudes' maximum first; a tile with something
+      // that is not finite (rare) once more, to take it out
       constexpr int CH = HD / 8, RPI = 32 / CH, PASSES = 32 / RPI;
       const int c = lane % CH;
       each_item([&](const Item& it, int, int t0, int t1) {
@@ -511,7 +516,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
                 uint4 x = *at(p);
                 if (drop_nonfinite<PBF>(x)) {
                   *at(p) = x;
-                  const int j = j0 + lw * 32 + p * RPI + lane / CH;   // (of rows that no query sees nobody asks for the values)
+                  const int j = j0 + lw * 32 + p * RPI + lane / CH;   // (rows that no query sees: nobody asks)
                   bad |= j < it.end() && (j >= it.lo || j < it.sk);
                 }
               }
@@ -525,9 +530,10 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         return true;
       });
     } else {
-      // ---- e4m3 pages: this warp's 32 rows of every tile of its plane. LPR lanes of 16 codes per row, RP rows a pass, PN
-      // passes; the lanes of a row's second 64 columns take their two 8-code halves in the other order, so that no store
-      // conflicts. Rows that no query sees are zeros. A plane's warps agree on the tile's exponent bound through shared memory.
+      // ---- e4m3 pages: this warp's 32 rows of every tile of its plane. LPR lanes of 16 codes per row, RP rows a
+      // pass, PN passes; the lanes of a row's second 64 columns take their two 8-code halves in the other order, so
+      // that no store conflicts. Rows that no query sees are zeros. A plane's warps agree on the tile's exponent
+      // bound through shared memory.
       const int plane = warp < 14 ? 0 : 1;
       constexpr int LPR = HD / 16, RP = 32 / LPR, PN = 32 / RP;
       const int ci = lane % LPR, sw = HD == 128 && ci >= 4 ? 1 : 0;
@@ -552,7 +558,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         int run = NO_BOUND;
         auto read = [&](int64_t v, int p) {
           const int64_t w = __shfl_sync(0xffffffffu, v, p * RP + lane / LPR);
-          return w >= 0 ? __ldg(reinterpret_cast<const uint4*>((const uint8_t*)pg.data + w * HD) + ci) : make_uint4(0, 0, 0, 0);
+          return w >= 0 ? __ldg(reinterpret_cast<const uint4*>((const uint8_t*)pg.data + w * HD) + ci)
+                        : make_uint4(0, 0, 0, 0);
         };
         auto fetch = [&](int64_t v) {
           sc = v >= 0 ? __ldg(pg.scales + v) : 0.f;
@@ -623,7 +630,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
     each_item([&](const Item& it, int k, int t0, int t1) {
       const int n = it.n, before = x ? t1 : t0;
       struct Row {
-        bool live, idle;       // idle: the warp's quadrant of 32 matrix rows is past the tile's last; it only keeps the barriers going
+        bool live, idle;       // idle: the warp's 32 matrix rows are past the tile's last; it only keeps the barriers going
         int pos, lo;           // position and the window's first key
         int64_t at;            // (row of q and out) * Hq + q head
       };
@@ -642,7 +649,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       const bool idle = rw.idle, none = pair && x && !it.two;   // none: no second tile at all
       const int pos = rw.pos, row_lo = rw.lo;
       float sl2 = a.scale * 1.4426950408889634f;
-      if constexpr (!QTMA) {   // bf16 Q rows of the quadrant to f16; absent rows are zeros. One tile: each stream half of the rows
+      if constexpr (!QTMA) {   // bf16 Q rows of the quadrant to f16 (one tile: each stream half of them); absent rows are zeros
         constexpr int CH = HD / 8;
         if (!wwait(q_empty, (k & 1) ^ 1)) return false;
         const int64_t off = rw.live ? ((int64_t)it.row0 + it.v0 + (pair && x ? pl.RT : 0) + r_row) * a.q_stride +
@@ -653,7 +660,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         for (int p = first; p < first + count; ++p) {      // 32 rows x CH chunks
           const int e = p * 32 + lane, rr = quad * 32 + e / CH, c = e % CH;
           const int64_t o = __shfl_sync(0xffffffffu, off, e / CH);
-          const uint4 v = o >= 0 ? __ldg(reinterpret_cast<const uint4*>((const uint16_t*)a.q + o) + c) : make_uint4(0, 0, 0, 0);
+          const uint4 v = o >= 0 ? __ldg(reinterpret_cast<const uint4*>((const uint16_t*)a.q + o) + c)
+                                 : make_uint4(0, 0, 0, 0);
           uint32_t w[4] = {v.x, v.y, v.z, v.w};
           uint32_t top = 0;                                // the row's largest element near 2^14
 #pragma unroll
@@ -705,7 +713,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         ld_wait();
         pin32(u);
         pin32(u + 32);
-        if (!__all_sync(0xffffffffu, (lo <= 0 || sk >= 64) && hi >= 63)) {   // some row does not see all keys: -inf for the hidden
+        // some row does not see all keys: -inf for the hidden
+        if (!__all_sync(0xffffffffu, (lo <= 0 || sk >= 64) && hi >= 63)) {
           auto upto = [](int c) { return c <= 0 ? 0ull : c >= 64 ? ~0ull : ~0ull >> (64 - c); };   // columns below c
           const uint64_t seen = upto(hi + 1) & (~upto(lo) | upto(sk));
 #pragma unroll
@@ -764,7 +773,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[2 * x + hh]);
       }
-      // ---- the item's end (what the loop did not need is made again: registers). Its sums stay in TMEM until the next item's first weights are announced
+      // ---- the item's end (what the loop did not need is made again: registers). Its sums stay in TMEM until the
+      // next item's first weights are announced
       const Item ie = item_at(k);
       rw = row_of(ie);
       float l = lo2(l2) + hi2(l2);
@@ -773,7 +783,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       const float scale_o = E4 ? pow2f(unit - 7) : 1.f, mean = E4 ? (l == 0.f ? 0.f : 1.f / l) : 1.f;   // (SHARE: e4m3)
       float w0 = 1.f, w1 = 0.f;                  // weights of the two streams' sums
       const bool publish = !pair && x == 1;      // (o, m, l) into the K/V stages, for stream 0
-      if (publish) {                             // once stream 0 has read its last tile from them, and the sums of the item before
+      if (publish) {                             // once stream 0 has read its last tile, and the item before's sums, from them
         if (n > 0 && !wwait(&o_done[0], dn0 & 1)) return false;
         if (k > 0 && !wwait(kv_free, (k - 1) & 1)) return false;
       } else if (!pair) {
@@ -797,7 +807,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       }
       if (!idle && !none) {
         const float inv = E4 ? 1.f : l == 0.f ? 0.f : 1.f / l;
-        const bool fix = rw.live && !publish && *v_flag;   // non-finite values of partly hidden tiles: into the rows that see them
+        const bool fix = rw.live && !publish && *v_flag;   // non-finite values: into the rows that see them
         const int64_t pi = (int64_t)ie.w * 2 + (pair ? x : 0);
         constexpr int CW = E4 ? 16 : 32, PIECES = CW / 8;   // columns at a time (e4m3: 96 registers a thread)
         int64_t to[PIECES];                      // where the rows of this lane's group of PIECES go
@@ -813,7 +823,10 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
             pin<CW>(u);
           }
 #pragma unroll
-          for (int e = 0; e < CW; ++e) u[e] = li > 0 ? __float_as_uint(E4 ? __uint_as_float(u[e]) * mean * scale_o : __uint_as_float(u[e])) : 0u;
+          for (int e = 0; e < CW; ++e) {
+            if constexpr (E4) u[e] = __float_as_uint(__uint_as_float(u[e]) * mean * scale_o);
+            u[e] = li > 0 ? u[e] : 0u;
+          }
           float4* at = reinterpret_cast<float4*>(pub + c);
           if (publish) {
 #pragma unroll
@@ -829,13 +842,15 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
               const float y4[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
               for (int z = 0; z < 4; ++z)
-                u[e + z] = __float_as_uint((w0 != 0.f ? w0 * __uint_as_float(u[e + z]) : 0.f) + (w1 != 0.f ? w1 * y4[z] : 0.f));
+                u[e + z] = __float_as_uint((w0 != 0.f ? w0 * __uint_as_float(u[e + z]) : 0.f) +
+                                           (w1 != 0.f ? w1 * y4[z] : 0.f));
             }
           }
           if (fix) add_nonfinite<E4, PBF, CW>(ie, a, rw.pos, rw.lo, c, u);
           if (ie.ns == 1) {
-            // 16-byte pieces change places within PIECES lanes, so that each store has PIECES * 16 bytes of a row side by side
-            // (a row's own piece in every lane: 32 lines a store, the end of an item 3.3 us instead of 2)
+            // 16-byte pieces change places within PIECES lanes, so that each store has PIECES * 16 bytes of a row
+            // side by side (a row's own piece in every lane: 32 lines a store, the end of an item 3.3 us instead of
+            // 2)
             uint32_t y[CW / 2];
 #pragma unroll
             for (int e = 0; e < CW / 2; ++e)
@@ -901,9 +916,10 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
   }
 }
 
-// Joins the parts of a row, m their bases: M = max m, o = sum 2^(m - M) o / sum 2^(m - M) l. A part without a
-// visible key (m = -inf, l = 0) holds no sums. MEANS: o / l instead of o (SHARE). A block joins 32 rows x 8 columns; warp w takes the parts w, w + W, ...,
-// and the W sums are joined through shared memory: every order is fixed by the sizes. A warp's reads are issued together.
+// Joins the parts of a row, m their bases: M = max m, o = sum 2^(m - M) o / sum 2^(m - M) l. A part without a visible
+// key (m = -inf, l = 0) holds no sums. MEANS: o / l instead of o (SHARE). A block joins 32 rows x 8 columns; warp w
+// takes the parts w, w + W, ..., and the W sums are joined through shared memory: every order is fixed by the sizes.
+// A warp's reads are issued together.
 constexpr int CWARPS = 8, CCOLS = 8;
 __device__ __forceinline__ float part_weight(float m, float M) { return m == M ? 1.f : t5::ex2(m - M); }
 template <int HD, bool OBF, bool MEANS, int N>
@@ -926,7 +942,8 @@ __global__ void __launch_bounds__(CWARPS * 32, 4)
   };
   // this tile's parts, two tile slots each, MP * Hkv items apart
   const int mp = mt / pl.nt;
-  const int64_t p0 = ((int64_t)tab.start[si] + (int64_t)g * MP + MP - 1 - mp) * 2 + mt % pl.nt, apart = (int64_t)MP * Hkv * 2;
+  const int64_t p0 = ((int64_t)tab.start[si] + (int64_t)g * MP + MP - 1 - mp) * 2 + mt % pl.nt;
+  const int64_t apart = (int64_t)MP * Hkv * 2;
   const float2* ml = reinterpret_cast<const float2*>((const float*)a.ws + (int64_t)tab.split * 2 * BQ * HD) + p0 * BQ +
                      quad * 32 + lane;
   const float4* ps = reinterpret_cast<const float4*>(a.ws) + ((p0 * 4 + quad) * (HD / 4) + cb * (CCOLS / 4)) * 32 + lane;
@@ -995,12 +1012,12 @@ int item_tiles(int pos0, int v0, int v1, int window, int sinks) {
   return tiles_of<BKV>(s).count();
 }
 
-// One launch: sequences s0 .. (empty ones left out) with one or two query tiles an item and, per sequence, the parts that an
-// item's key tiles are split into: the choice with the least estimated time (us, measured): a key tile takes 1.13 us with two
-// query tiles and 0.66 with one, an item ITEM besides and a CTA's start and end 6, the join 2.8 and its sums. CTAs take the
-// items in rounds: as many as there are rounds of average ones, or an even share and a third of the longest where lengths
-// differ. An item is split into parts of `per` key tiles; at most 64 parts, and parts of at most LONGEST tiles (the
-// tensor cores add to one sum per output and drop what lies below its last bits).
+// One launch: sequences s0 .. (empty ones left out) with one or two query tiles an item and, per sequence, the parts
+// that an item's key tiles are split into: the choice with the least estimated time (us, measured): a key tile takes
+// 1.13 us with two query tiles and 0.66 with one, an item ITEM besides and a CTA's start and end 6, the join 2.8 and
+// its sums. CTAs take the items in rounds: as many as there are rounds of average ones, or an even share and a third
+// of the longest where lengths differ. An item is split into parts of `per` key tiles; at most 64 parts, and parts of
+// at most LONGEST tiles (the tensor cores add to one sum per output and drop what lies below its last bits).
 constexpr double ITEM = 3.0;
 constexpr int LONGEST = 1024;
 struct Group {
@@ -1030,7 +1047,7 @@ void plan_group(Group& gr, int s0, int n_seq, const int* row0, const int* len, c
     const int64_t MT = ((int64_t)len[s] + pl.RT - 1) / pl.RT;
     all_tiles += MT;
     most = std::max(most, most_parts(pos0[s], len[s]));
-    if (!seqs.empty() && all_tiles * Hkv * most > INT_MAX) break;   // (numbers of items and of the join's blocks stay within 31 bits)
+    if (!seqs.empty() && all_tiles * Hkv * most > INT_MAX) break;   // (numbers of items and join blocks stay in 31 bits)
     Seq q{s, 1, {}, {}, {}};
     for (int k = 0; k < 2; ++k) {
       const int rows = (k + 1) * pl.RT;
@@ -1121,7 +1138,8 @@ cudaError_t launch_tab(const PagedAttnArgs& a, const Tab<N>& tab, const Plan& pl
   CK_RET(launch_pdl(paged_kernel<HD, KIND, N>, dim3((unsigned)std::min(tab.start[tab.n], num_sms)), dim3(threads_of(KIND)),
                     L::BYTES, st, tab, map, map_q, a, pl));
   if (max_ns > 1)
-    CK_RET(launch_pdl(combine_kernel<HD, out_bf16(KIND), is_e4m3(KIND), N>, dim3((unsigned)(tab.tiles[tab.n] * (HD / CCOLS * 4))),
+    CK_RET(launch_pdl(combine_kernel<HD, out_bf16(KIND), is_e4m3(KIND), N>,
+                      dim3((unsigned)(tab.tiles[tab.n] * (HD / CCOLS * 4))),
                       dim3((unsigned)(32 * std::min(CWARPS, (max_ns + 1) / 2))), 0, st, tab, a, pl));
   return cudaSuccess;
 }

@@ -1,28 +1,28 @@
 // Attention of one new token of each sequence over a paged cache: o = softmax(scale q.K^T) V over the rows that the
 // token sees, every cached row read once for the (up to 16) q heads that share its kv head.
 //
-// Bound by HBM: 4 hd flops per q head for 4 hd bytes of an f16 row (K and V), 5 q heads: 5 flops a byte. So the split is
-// made for the memory system: the work of a call is the list of all 64-row tiles of all (sequence, kv head) pairs, and
-// CTA c of C (one per SM) takes the c-th of C equal runs of it, whatever the sequences' lengths. The runs follow from pos,
-// which every CTA reads on the device (a captured call stays balanced as positions grow). A run covers some pairs wholly,
-// which are written at once, and at most two in part, whose (o, m, l) join_kernel joins in the order of the CTAs: the
-// sizes and positions fix every order of summation.
+// Bound by HBM: 4 hd flops per q head for 4 hd bytes of an f16 row (K and V), 5 q heads: 5 flops a byte. So the split
+// is made for the memory system: the work of a call is the list of all 64-row tiles of all (sequence, kv head) pairs,
+// and CTA c of C (one per SM) takes the c-th of C equal runs of it, whatever the sequences' lengths. The runs follow
+// from pos, which every CTA reads on the device (a captured call stays balanced as positions grow). A run covers some
+// pairs wholly, which are written at once, and at most two in part, whose (o, m, l) join_kernel joins in the order of
+// the CTAs: the sizes and positions fix every order of summation.
 //
-// A CTA: three warps ask for the tiles by TMA (a lane per page box; page ids read 32 columns ahead) into a ring of 130 to 190 KB;
-// the others compute, four a tile, 16 rows each, without any exchange until the pair ends. With at most 16 query rows
-// tcgen05's 128-row tiles would stand nearly empty and pass S and P through TMEM between warps, so the products are mma.sync's
-// m16n8k16, whose operands and results stay in one warp's registers, transposed: S^T = K Q^T and O^T = V^T P^T, cached rows
-// and value columns on the 16 side and 8 q heads on the 8 side (NH = 1, or 2 for more than 8 heads: twice the products on
-// the same K and V operands). One movmatrix turns 8 x 8 weights of S^T's layout into P^T's. Each warp keeps a running base
-// and sum of its own rows.
+// A CTA: three warps ask for the tiles by TMA (a lane per page box; page ids read 32 columns ahead) into a ring of
+// 130 to 190 KB; the others compute, four a tile, 16 rows each, without any exchange until the pair ends. With at
+// most 16 query rows tcgen05's 128-row tiles would stand nearly empty and pass S and P through TMEM between warps, so
+// the products are mma.sync's m16n8k16, whose operands and results stay in one warp's registers, transposed: S^T = K
+// Q^T and O^T = V^T P^T, cached rows and value columns on the 16 side and 8 q heads on the 8 side (NH = 1, or 2 for
+// more than 8 heads: twice the products on the same K and V operands). One movmatrix turns 8 x 8 weights of S^T's
+// layout into P^T's. Each warp keeps a running base and sum of its own rows.
 //
 // e4m3 pages: the codes travel and are widened to f16 in registers. The sums over d and over rows do not care for
-// their order, so both products take the codes in the order in which wide shared-memory reads find them: row
-// n of an 8-row block of S^T stands for cached row key8(n), and thread (g, t) holds chunk t of a K row (16 d's as four
-// k-steps) and chunk g of V rows (16 columns). K scales multiply the scores. V scales go into the weights as exponents: the
-// base is a running bound of z + e (V's scale 2^(unit + e) f, f in [1/2, 1), unit a warp's first), so neither f16 nor the sums see
-// the scales' range.
-// bf16 queries over e4m3 pages become f16 by a power of two per q head.
+// their order, so both products take the codes in the order in which wide shared-memory reads find them: row n of an
+// 8-row block of S^T stands for cached row key8(n), and thread (g, t) holds chunk t of a K row (16 d's as four
+// k-steps) and chunk g of V rows (16 columns). K scales multiply the scores. V scales go into the weights as
+// exponents: the base is a running bound of z + e (V's scale 2^(unit + e) f, f in [1/2, 1), unit a warp's first), so
+// neither f16 nor the sums see the scales' range. bf16 queries over e4m3 pages become f16 by a power of two per q
+// head.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -43,8 +43,8 @@ enum Kind { F16 = 0, BF16 = 1, E4M3 = 2 };
 
 __device__ uint64_t g_given_up;              // when a bounded wait last gave up, per device; never cleared
 
-// Computing warps: 8, or 12 with e4m3 pages of up to 8 q heads, where widening the codes takes most of the time (16 would leave
-// 96 registers a thread, too few).
+// Computing warps: 8, or 12 with e4m3 pages of up to 8 q heads, where widening the codes takes most of the time (16
+// would leave 96 registers a thread, too few).
 template <int HD, int KIND, int NH>
 struct Lay {
   static constexpr int WARPS = KIND == E4M3 && NH == 1 ? 12 : 8, GROUPS = WARPS / 4;
@@ -67,8 +67,9 @@ struct StepArgs {
   int n, G, HG, groups;      // q heads per kv head; (kv head, group of 16 q heads) pairs of a sequence, groups per kv head
 };
 
-// Part slots of the workspace: slot 2 c for the pair that CTA c's run continues, 2 c + 1 for the one that it starts and does not
-// end; 16 q heads of hd sums (means with e4m3 pages), then 16 (m, l). Behind them a record for each CTA: the pair whose last tile its run holds.
+// Part slots of the workspace: slot 2 c for the pair that CTA c's run continues, 2 c + 1 for the one that it starts
+// and does not end; 16 q heads of hd sums (means with e4m3 pages), then 16 (m, l). Behind them a record for each CTA:
+// the pair whose last tile its run holds.
 struct Record {
   int seq, hg, first, valid;   // first: the CTA with the pair's first tile
 };
@@ -122,8 +123,9 @@ __device__ __forceinline__ uint32_t pack_w(float a, float b) {
     return h2u(a, b);
   }
 }
+// The computing warps.
 template <int N>
-__device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }   // the computing warps
+__device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
 
 // A run's position in the list of tiles.
 struct Cursor {
@@ -260,8 +262,8 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
     c0.hg = r / c0.T;
     c0.t = r - c0.hg * c0.T;
   }
-  // runs fn(cursor, tiles of the pair in this run, the next pair's cursor, whether there is one) over the pairs of the run;
-  // positions are read 32 sequences at a time
+  // runs fn(cursor, tiles of the pair in this run, the next pair's cursor, whether there is one) over the pairs of
+  // the run; positions are read 32 sequences at a time
   auto each_pair = [&](auto&& fn) {
     if (run.u0 >= run.u1) return;
     Cursor c = c0;
@@ -286,15 +288,16 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
     }
   };
 
-  uint32_t filled = 0;                         // (producers) per stage: filled (bit st), parity of the last fill (bit 16 + st)
+  uint32_t filled = 0;         // (producers) per stage: filled (bit st), parity of the last fill (bit 16 + st)
   if (warp >= WARPS) {
-    // ---- TMA producers: every third tile each (a warp passes once over its loop for each box, whose operands are uniform: with
-    // one warp, or four for a quarter of each tile, the tiles of 16-row pages or 64-byte rows take longer than their bytes)
+    // ---- TMA producers: every third tile each (a warp passes once over its loop for each box, whose operands are
+    // uniform: with one warp, or four for a quarter of each tile, the tiles of 16-row pages or 64-byte rows take
+    // longer than their bytes)
     constexpr int NB = KIND == E4M3 ? 1 : HD / 64, ROW = KIND == E4M3 ? HD : 128;   // boxes of a page, bytes of a box row
     const int pw = warp - WARPS, plane = lane & 1, box = (lane >> 1) % NB, part = (lane >> 1) / NB;   // this lane's box
     const int npg = pg.shift < 6 ? KT >> pg.shift : 1, br = KT / npg;     // pages of a tile, rows of a box
     int i = 0;
-    int cs = -1, blk = -1, cur = 0, ns_ = -1, nblk = -1, next = 0;        // page ids of 32 columns: of a block, and of the next
+    int cs = -1, blk = -1, cur = 0, ns_ = -1, nblk = -1, next = 0;   // page ids of 32 columns: of a block, and of the next
     each_pair([&](const Cursor& c, int m, const Cursor& nx, bool more) {
       const int head = c.hg / sa.groups, last = (c.v.end - 1) >> pg.shift;
       auto ids = [&](const Cursor& w, int b) {
@@ -323,7 +326,8 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
         }
         const int id = __shfl_sync(0xffffffffu, cur, (col + part) & 31);
         const int tile = i0 + x, st = tile % NST;
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], (tile / NST & 1) ^ 1, abort_flag, &g_given_up) ? 1 : 0)) return false;
+        const bool free = mbar_wait(&empty[st], (tile / NST & 1) ^ 1, abort_flag, &g_given_up);
+        if (!__all_sync(0xffffffffu, free ? 1 : 0)) return false;
         const int there = min(npg, last - col + 1);            // pages that the sequence has
         if (lane == 0) mbar_expect_tx(&full[st], (uint32_t)(there * NB * 2 * br * ROW));
         __syncwarp();
@@ -411,7 +415,8 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
           for (int ks = 0; ks < HD / 16; ++ks)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              q[nh][ks][e] = h2u(__uint_as_float(q[nh][ks][e] << 16) * up, __uint_as_float(q[nh][ks][e] & 0xffff0000u) * up);
+              q[nh][ks][e] = h2u(__uint_as_float(q[nh][ks][e] << 16) * up,
+                                 __uint_as_float(q[nh][ks][e] & 0xffff0000u) * up);
         }
       }
       if (AHEAD && more) load_q(nx);                           // (used when this pair has ended)
@@ -479,7 +484,8 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
               if (unit == NO_UNIT) unit = __reduce_max_sync(0xffffffffu, hid[b] ? NO_UNIT : E);
               const int rel = E - unit, up = (80 - unit) >> 1;   // (2^-80 below the unit: the rest stays in f)
               ex[b] = (float)max(rel, -80);
-              f[b] = rel >= -80 ? __uint_as_float((u & 0x7fffffu) | 126u << 23) : sc[KT] * pow2f(up) * pow2f(80 - unit - up);
+              f[b] = rel >= -80 ? __uint_as_float((u & 0x7fffffu) | 126u << 23)
+                                : sc[KT] * pow2f(up) * pow2f(80 - unit - up);
             }
           }
           uint32_t p[NH][2];                                   // P^T: rows 2 t, 2 t + 1 of each block, q head g
@@ -660,8 +666,8 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
         group_sync<WARPS * 32>();
       }
       if (ends && !starts && threadIdx.x == 0) {
-        // the pair's first tile: list position u0 - c.t (this is the run's first pair, the only one it does not start), and
-        // the CTA whose run holds it
+        // the pair's first tile: list position u0 - c.t (this is the run's first pair, the only one it does not
+        // start), and the CTA whose run holds it
         const int at = run.u0 - c.t, more = run.rem * (run.q + 1);
         const int f = at < more ? at / (run.q + 1) : run.rem + (at - more) / run.q;
         Record* rec = reinterpret_cast<Record*>((float*)a.ws + 2 * (int64_t)gridDim.x * slot_floats(HD)) + blockIdx.x;
@@ -676,8 +682,9 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
       if (filled >> st & 1) mbar_drain(&full[st], filled >> (16 + st) & 1);
 }
 
-// Joins the parts of the pair that CTA blockIdx.x of the step ended: slot 2 first + 1, then slots 2 c of the CTAs behind it.
-// Block y takes rows y, y + gridDim.y, ...; its warps take the parts in turn, and their sums are joined in order.
+// Joins the parts of the pair that CTA blockIdx.x of the step ended: slot 2 first + 1, then slots 2 c of the CTAs
+// behind it. Block y takes rows y, y + gridDim.y, ...; its warps take the parts in turn, and their sums are joined in
+// order.
 constexpr int JWARPS = 8;
 template <int HD, bool QBF, int NH, bool MEANS>
 __global__ void __launch_bounds__(JWARPS * 32) join_kernel(const __grid_constant__ StepArgs sa, int C) {
@@ -688,7 +695,8 @@ __global__ void __launch_bounds__(JWARPS * 32) join_kernel(const __grid_constant
   const float* ws = (const float*)sa.a.ws;
   const Record rec = reinterpret_cast<const Record*>(ws + 2 * (int64_t)C * slot_floats(HD))[blockIdx.x];
   if (!rec.valid) return;
-  const int kvh = rec.hg / sa.groups, h0 = kvh * sa.G + (rec.hg % sa.groups) * 8 * NH, nq = min(8 * NH, (kvh + 1) * sa.G - h0);
+  const int kvh = rec.hg / sa.groups, h0 = kvh * sa.G + (rec.hg % sa.groups) * 8 * NH;
+  const int nq = min(8 * NH, (kvh + 1) * sa.G - h0);
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, parts = (int)blockIdx.x - rec.first + 1;
   for (int r = blockIdx.y; r < nq; r += gridDim.y) {
     float M = -INFINITY, l = 0.f;
@@ -697,7 +705,8 @@ __global__ void __launch_bounds__(JWARPS * 32) join_kernel(const __grid_constant
     for (int p = w; p < parts; p += JWARPS) {
       const float* slot = ws + (p == 0 ? 2 * (int64_t)rec.first + 1 : 2 * (int64_t)(rec.first + p)) * slot_floats(HD);
       const float2 z = __ldcg(reinterpret_cast<const float2*>(slot + 16 * HD) + r);
-      const float4 v = lane < HD / 4 ? __ldcg(reinterpret_cast<const float4*>(slot + r * HD) + lane) : make_float4(0, 0, 0, 0);
+      const float4 v = lane < HD / 4 ? __ldcg(reinterpret_cast<const float4*>(slot + r * HD) + lane)
+                                     : make_float4(0, 0, 0, 0);
       if (z.x == -INFINITY && z.y == 0.f) continue;
       const float N = fmaxf(M, z.x), a0 = M == N || l == 0.f ? 1.f : ex2(M - N), a1 = z.x == N ? 1.f : ex2(z.x - N);
       M = N;
@@ -735,7 +744,8 @@ cudaError_t launch(const StepArgs& sa, int num_sms, cudaStream_t st) {
   if (!pages_map(&map, sa.a.pages, std::min(KT, 1 << sa.a.pages.shift))) return cudaErrorInvalidValue;
   CK_RET(cudaFuncSetAttribute(step_kernel<HD, KIND, QBF, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES));
   CK_RET(launch_pdl(step_kernel<HD, KIND, QBF, NH>, dim3((unsigned)num_sms), dim3(L::THREADS), L::BYTES, st, map, sa));
-  return launch_pdl(join_kernel<HD, QBF, NH, KIND == E4M3>, dim3((unsigned)num_sms, 4), dim3(JWARPS * 32), 0, st, sa, num_sms);
+  return launch_pdl(join_kernel<HD, QBF, NH, KIND == E4M3>, dim3((unsigned)num_sms, 4), dim3(JWARPS * 32), 0, st, sa,
+                    num_sms);
 }
 template <int HD, int KIND, bool QBF>
 cudaError_t launch_nh(const StepArgs& sa, int num_sms, cudaStream_t st) {

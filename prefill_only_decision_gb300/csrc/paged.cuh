@@ -6,9 +6,9 @@
 namespace s1 {
 namespace pga {
 
-// Weights are 2^(z - m), z the score (log2 domain) and m a base that a row moves to HEAD below its maximum when they would
-// pass 2^TOP, within f16: a weight keeps f16's precision down to 2^-24 of the largest (a base at the maximum would lose
-// what lies behind a sink). Maxima past FAR are their own base: fp32 does not hold HEAD beside them.
+// Weights are 2^(z - m), z the score (log2 domain) and m a base that a row moves to HEAD below its maximum when they
+// would pass 2^TOP, within f16: a weight keeps f16's precision down to 2^-24 of the largest (a base at the maximum
+// would lose what lies behind a sink). Maxima past FAR are their own base: fp32 does not hold HEAD beside them.
 constexpr float HEAD = 10.f, TOP = 15.f, FAR = 4194304.f;
 
 // The rows that a query at position p sees: [0, sk) and [lo, end).
@@ -42,17 +42,19 @@ __host__ __device__ __forceinline__ Tiles tiles_of(const Seen& s) {
   return t;
 }
 
-__device__ __forceinline__ void tma5(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w, int v) {
+__device__ __forceinline__ void tma5(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w,
+                                     int v) {
   asm volatile(
       "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
       "[%7];" ::"r"(t5::smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(t5::smem_u32(bar))
       : "memory");
 }
-// 16 bytes into shared memory, zeros where !on; and an arrival (counted in the barrier's number) once this thread's copies are
-// there.
+// 16 bytes into shared memory, zeros where !on; and an arrival (counted in the barrier's number) once this thread's
+// copies are there.
 __device__ __forceinline__ void copy16_async(void* dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(t5::smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(t5::smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
 }
 __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(t5::smem_u32(bar)) : "memory");
@@ -69,12 +71,12 @@ __device__ __forceinline__ float pow2f(int e) {
   return __uint_as_float(e >= -126 ? (uint32_t)(e + 127) << 23 : e >= -149 ? 1u << (e + 149) : 0u);
 }
 
-// Sums over e4m3 pages pass between warps, CTAs and kernels as means (o / l), since V's scales may leave fp32 no room beside the
-// weights; such a mean's share is its l times 2^-SHARE, which leaves room on both sides.
+// Sums over e4m3 pages pass between warps, CTAs and kernels as means (o / l), since V's scales may leave fp32 no room
+// beside the weights; such a mean's share is its l times 2^-SHARE, which leaves room on both sides.
 constexpr float SHARE = 9.5367431640625e-7f, UNSHARE = 1048576.f;   // 2^-20, 2^20
 
-// The pages as a tensor (hd, page rows, heads, pages, planes) in boxes of `rows` rows of up to 128 bytes. A page id outside
-// 0 .. n_pages - 1 is outside the tensor, which TMA reads as zeros.
+// The pages as a tensor (hd, page rows, heads, pages, planes) in boxes of `rows` rows of up to 128 bytes. A page id
+// outside 0 .. n_pages - 1 is outside the tensor, which TMA reads as zeros.
 inline bool pages_map(CUtensorMap* map, const PagesArgs& p, int rows) {
   const bool e4m3 = p.format == KVF_E4M3;
   const uint64_t es = e4m3 ? 1 : 2, row = p.hd * es, head = row << p.shift, page = head * p.Hkv;

@@ -1,16 +1,17 @@
 // Rotary positions of rows, and rows rotated on their way into a paged cache.
 //
-// Pair i of a head is turned by pos * w_i. In fp32 that angle is lost at far positions (2^20 radians: an error
-// of 0.06), and fp64 is slow here; turns as integers are neither: w_i / 2 pi modulo 1 in units of 2^-64 times the position
-// is one 64-bit product whose overflow is the whole turns. Its top 32 bits give the quadrant and an angle within an eighth
-// of a turn, whose sine and cosine fp32 holds to its last bit or two.
+// Pair i of a head is turned by pos * w_i. In fp32 that angle is lost at far positions (2^20 radians: an error of
+// 0.06), and fp64 is slow here; turns as integers are neither: w_i / 2 pi modulo 1 in units of 2^-64 times the
+// position is one 64-bit product whose overflow is the whole turns. Its top 32 bits give the quadrant and an angle
+// within an eighth of a turn, whose sine and cosine fp32 holds to its last bit or two.
 //
-// Every element is read and written once: HBM bound. A block takes tiles of RB rows in turn: for each it makes the rows' n_pairs
-// sines and cosines once into shared memory for all heads (a sine in every thread that uses one would cost five times the
-// rotation itself), then a thread turns 2 x 8 elements of a head at a time, chunk c and its partner chunk, hd / 16 threads a
-// head, U of them loaded before the first is used. Blocks stay because a thread then looks its pair's frequency up once (lanes
-// that index kernel parameters differently are served one by one: 70001 rows to e4m3 192 us with a block per tile), and so that
-// the next tile's positions and page ids are on their way under the present one.
+// Every element is read and written once: HBM bound. A block takes tiles of RB rows in turn: for each it makes the
+// rows' n_pairs sines and cosines once into shared memory for all heads (a sine in every thread that uses one would
+// cost five times the rotation itself), then a thread turns 2 x 8 elements of a head at a time, chunk c and its
+// partner chunk, hd / 16 threads a head, U of them loaded before the first is used. Blocks stay because a thread then
+// looks its pair's frequency up once (lanes that index kernel parameters differently are served one by one: 70001
+// rows to e4m3 192 us with a block per tile), and so that the next tile's positions and page ids are on their way
+// under the present one.
 #include <algorithm>
 
 #include <cuda_fp8.h>
@@ -26,8 +27,8 @@ using kvc::Raw;
 
 constexpr int THREADS = 256, RB_MAX = 16, PASSES = 4;         // rows of a tile; angles of a tile that a thread makes
 
-// cos and sin of pos * turn (2^-64 turns): quadrant and rest, the rest's Taylor series (|y| <= pi / 4: the terms left out are
-// below 2^-29 of the sine and 2^-32 of the cosine).
+// cos and sin of pos * turn (2^-64 turns): quadrant and rest, the rest's Taylor series (|y| <= pi / 4: the terms left
+// out are below 2^-29 of the sine and 2^-32 of the cosine).
 __device__ __forceinline__ float2 cos_sin(int pos, uint64_t turn) {
   const uint64_t ph = (uint64_t)(int64_t)pos * turn;
   const uint32_t p = (uint32_t)((ph + 0x80000000ull) >> 32);
@@ -99,13 +100,14 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a < __int_as_float(0x7f800000) ? a : 0.f;           // (NaN: 0)
 }
 
-// grid (row blocks of rb rows, head blocks of hb heads): heads 0 .. Hq-1 are q's, then k's, then v's.
-// U, the units a thread loads at once: 2, and 1 where a call is small. Blocks of an SM: 4 with 16-bit rows, 3 with fp32 ones, whose
-// loads take twice the registers (70001 rows f16 to e4m3 with 3, 4, 5 blocks: 157, 147, 163 us; 12345 rows f32 to bf16 40.6,
-// 46, 61 us; U of 1, 3, 4 f16: 165, 152, 162 us; 37 tokens with U of 1 and 2: 2.9, 3.4 us).
+// grid (row blocks of rb rows, head blocks of hb heads): heads 0 .. Hq-1 are q's, then k's, then v's. U, the units a
+// thread loads at once: 2, and 1 where a call is small. Blocks of an SM: 4 with 16-bit rows, 3 with fp32 ones, whose
+// loads take twice the registers (70001 rows f16 to e4m3 with 3, 4, 5 blocks: 157, 147, 163 us; 12345 rows f32 to
+// bf16 40.6, 46, 61 us; U of 1, 3, 4 f16: 165, 152, 162 us; 37 tokens with U of 1 and 2: 2.9, 3.4 us).
 constexpr int blocks_of(size_t es) { return es == 4 ? 3 : 4; }
 template <typename T, int HD, bool VEC, bool APPEND, int U>
-__global__ void __launch_bounds__(THREADS, blocks_of(sizeof(T))) rows_kernel(const __grid_constant__ RowsArgs a, int rb, int hb, bool out_vec) {
+__global__ void __launch_bounds__(THREADS, blocks_of(sizeof(T)))
+    rows_kernel(const __grid_constant__ RowsArgs a, int rb, int hb, bool out_vec) {
   constexpr int NU = HD / 16;
   __shared__ float4 cs[2][RB_MAX][2][MAX_PAIRS / 4];         // cosines, then sines, by tile parity and row
   __shared__ int64_t place[2][RB_MAX];                       // of a row in a plane of pages: vector (head 0); -1: none
@@ -116,7 +118,8 @@ __global__ void __launch_bounds__(THREADS, blocks_of(sizeof(T))) rows_kernel(con
   const int h0 = blockIdx.y * hb, heads = min(hb, H - h0);
   const uint32_t magic = 0xffffffffu / (uint32_t)heads + 1;
   // this thread's angles: pair tpair of rows trow, trow + rstep, .. of each tile
-  const int trow = np ? (int)threadIdx.x / np : RB_MAX, tpair = np ? (int)threadIdx.x - trow * np : 0, rstep = np ? THREADS / np : 1;
+  const int rstep = np ? THREADS / np : 1, trow = np ? (int)threadIdx.x / np : RB_MAX;
+  const int tpair = np ? (int)threadIdx.x - trow * np : 0;
   const bool angles = np && trow < min(rb, rstep);
   uint64_t turn = 0;
   int64_t axis = 0;
@@ -159,8 +162,8 @@ __global__ void __launch_bounds__(THREADS, blocks_of(sizeof(T))) rows_kernel(con
   int r0, total;                                             // of the tile at hand: first row, units
   Raw<T> x[U][2];
   int row[U], h[U];
-  // unit i: rows' heads in turn, hd / 16 units a head; two chunks c0 and c1 of 8 elements: a pair's two sides, or past the
-  // pairs two that stay
+  // unit i: rows' heads in turn, hd / 16 units a head; two chunks c0 and c1 of 8 elements: a pair's two sides, or
+  // past the pairs two that stay
   auto chunk0 = [&](int unit, int n8) { return unit < n8 ? unit : unit + n8; };
   auto chunk1 = [&](int unit, int n8) { return unit < n8 ? unit + n8 : unit + NU; };
   const int unit = threadIdx.x % NU;                         // (THREADS is a multiple of NU)
@@ -204,10 +207,11 @@ __global__ void __launch_bounds__(THREADS, blocks_of(sizeof(T))) rows_kernel(con
           at[MAX_PAIRS] = t.y;
         }
     if (APPEND && threadIdx.x < rb) {
-      place[buf][threadIdx.x] = id < 0 ? -1 : (((int64_t)id * a.pages.Hkv) << a.pages.shift) + (w.j & ((1 << a.pages.shift) - 1));
+      const int64_t first = ((int64_t)id * a.pages.Hkv) << a.pages.shift;
+      place[buf][threadIdx.x] = id < 0 ? -1 : first + (w.j & ((1 << a.pages.shift) - 1));
       live[buf][threadIdx.x] = w.j >= 0;
     }
-    __syncthreads();                                           // (one a tile: the other buffer's readers are past the sync before)
+    __syncthreads();                                         // (one a tile: the other buffer's readers passed the one before)
     positions(tile + gridDim.x);
     w = w_next;
     id = page_of(w);
@@ -282,17 +286,18 @@ template <typename T, int HD, bool VEC, bool APPEND>
 cudaError_t launch_t(const RowsArgs& a, bool out_vec, int num_sms, cudaStream_t st) {
   const int H = a.Hq + (APPEND ? 2 * a.pages.Hkv : 0);
   constexpr int NU = HD / 16;
-  // A tile holds enough rows for one or two of a thread's batches; fewer where the rows then would not reach all SMs, and of
-  // few rows a block takes the heads of one batch of loads. At most 8192 heads a block.
+  // A tile holds enough rows for one or two of a thread's batches; fewer where the rows then would not reach all SMs,
+  // and of few rows a block takes the heads of one batch of loads. At most 8192 heads a block.
   const int want = std::max(PASSES, (4 * THREADS + H * NU - 1) / (H * NU));
   int rb = 1;
-  const int enough = (sizeof(T) == 4 ? 2 : 4) * num_sms;      // tiles (1280 rows f16 with one, two, four an SM: 7.4, 6.9, 6.1 us;
-  while (rb < RB_MAX && rb < want && a.n_rows >= 2 * rb * enough) rb *= 2;   // 1500 rows f32 9.6, 6.9, 7.8)
+  // (1280 rows f16 with at least one, two, four tiles an SM: 7.4, 6.9, 6.1 us; 1500 rows f32 9.6, 6.9, 7.8)
+  const int enough = (sizeof(T) == 4 ? 2 : 4) * num_sms;
+  while (rb < RB_MAX && rb < want && a.n_rows >= 2 * rb * enough) rb *= 2;
   rb = std::min(rb, PASSES * (a.rope.n_pairs ? THREADS / a.rope.n_pairs : THREADS));
   const int hb = rb >= 4 ? std::min(H, 8192) : std::min(H, THREADS / NU);
   const dim3 grid(std::min((a.n_rows + rb - 1) / rb, blocks_of(sizeof(T)) * num_sms), (H + hb - 1) / hb);
-  return launch_pdl(rb >= 4 ? rows_kernel<T, HD, VEC, APPEND, 2> : rows_kernel<T, HD, VEC, APPEND, 1>, grid, dim3(THREADS), 0, st,
-                    a, rb, hb, out_vec);
+  return launch_pdl(rb >= 4 ? rows_kernel<T, HD, VEC, APPEND, 2> : rows_kernel<T, HD, VEC, APPEND, 1>, grid, dim3(THREADS),
+                    0, st, a, rb, hb, out_vec);
 }
 template <typename T, int HD>
 cudaError_t launch_vec(const RowsArgs& a, int num_sms, cudaStream_t st) {
@@ -301,7 +306,8 @@ cudaError_t launch_vec(const RowsArgs& a, int num_sms, cudaStream_t st) {
   const int es = sizeof(T);
   const bool vec = ok(a.q, a.q_stride, es) && (!append || (ok(a.k, a.k_stride, es) && ok(a.v, a.v_stride, es)));
   const bool out_vec = ok(a.q_out, a.q_out_stride, a.q_out_type == ELEM_F32 ? 4 : 2);
-  if (append) return vec ? launch_t<T, HD, true, true>(a, out_vec, num_sms, st) : launch_t<T, HD, false, true>(a, out_vec, num_sms, st);
+  if (append)
+    return vec ? launch_t<T, HD, true, true>(a, out_vec, num_sms, st) : launch_t<T, HD, false, true>(a, out_vec, num_sms, st);
   return vec ? launch_t<T, HD, true, false>(a, out_vec, num_sms, st) : launch_t<T, HD, false, false>(a, out_vec, num_sms, st);
 }
 template <typename T>
