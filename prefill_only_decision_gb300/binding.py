@@ -517,8 +517,13 @@ def op_kv_dequant_async(codes: int, scales: int, cap: int, pos0: int, n_rows: in
                                        stream))
 
 
+_I32 = np.dtype(np.int32)
+
+
 def _seq_i32(a) -> np.ndarray:
     """Row numbers or lengths as int32; what that cannot hold is refused, not wrapped or cut."""
+    if type(a) is np.ndarray and a.dtype is _I32 and a.ndim == 1 and a.flags.c_contiguous:
+        return a
     a = np.asarray(a)
     if a.ndim != 1:
         raise ValueError("row0 and lens must be 1-D and of the same length")

@@ -11,6 +11,8 @@ namespace {
 bool elem(int32_t t) { return t == S1_F16 || t == S1_BF16 || t == S1_F32; }
 size_t elem_bytes(int32_t t) { return t == S1_F32 ? 4 : 2; }
 
+constexpr double TWO_64 = 18446744073709551616.0;
+
 int check_rope(const s1_rope_spec* r, int32_t hd, RopeArgs* out) {
   out->n_pairs = 0;
   if (!r) return S1_OK;
@@ -25,9 +27,9 @@ int check_rope(const s1_rope_spec* r, int32_t hd, RopeArgs* out) {
     // w / 2 pi as hi + lo, so that its fraction is right to 2^-64 and not to a double's 2^-53
     const double w = std::fabs(r->inv_freq[i]), hi = w * 0.15915494309189535;
     const double lo = std::fma(w, 0.15915494309189535, -hi) + w * -9.839338337591243e-18;
-    const double frac = std::ldexp(hi - std::floor(hi), 64), rest = std::ldexp(lo, 64);   // 0 .. 2^64
-    const uint64_t turn = (frac >= 18446744073709551616.0 ? 0 : (uint64_t)frac) +
-                          (std::fabs(rest) < 9.2e18 ? (uint64_t)(int64_t)std::llround(rest) : 0);   // (past 2^52 turns: none)
+    const double frac = (hi - std::floor(hi)) * TWO_64, rest = lo * TWO_64;   // 0 .. 2^64
+    const uint64_t turn = (frac >= TWO_64 ? 0 : (uint64_t)frac) +
+                          (std::fabs(rest) < 9.2e18 ? (uint64_t)(int64_t)std::llround(rest) : 0);   // (past 2^52 turns: 0)
     out->turn[i] = r->inv_freq[i] < 0 ? 0 - turn : turn;
     out->axis[i] = r->axis ? r->axis[i] : 0;
   }
