@@ -258,11 +258,12 @@ int s1_op_kv_append_async(const void* q, const void* k, const void* v, int32_t d
  * of them; its own row, too, so append it first):  out = softmax(sm_scale q.k) v, q head h reading kv head
  * floor(h * Hkv / Hq). q, out: q_dtype, which is the pages' type (S1_F16 or S1_BF16 with e4m3
  * pages), q row stride q_stride (a multiple of 8 elements), out [n, Hq, hd]; q, out 16-byte aligned.
- * Rows past the table's cols * page_rows do not exist. A token that sees nothing (pos < 0) gives zeros. Each visible
- * row is read once for up to 16 q heads of its kv head, long and short sequences' rows split evenly over the SMs and
- * joined in a fixed order; the split follows pos on the device, so a captured call stays balanced as positions grow.
- * Softmax statistics and sums are fp32, the weights are rounded once to the product's 16-bit type (f16 for e4m3 codes),
- * f16 with its precision down to 2^-24 of the largest. What hidden rows hold does not matter. */
+ * Rows past the table's cols * page_rows do not exist. A token that sees nothing (pos < 0), or whose scores are all
+ * -inf, gives zeros. Each visible row is read once for up to 16 q heads of its kv head, long and short sequences' rows
+ * split evenly over the SMs and joined in a fixed order; the split follows pos on the device, so a captured call stays
+ * balanced as positions grow. Softmax statistics and sums are fp32, the weights are rounded once to the product's
+ * 16-bit type (f16 for e4m3 codes), f16 with its precision down to 2^-24 of the largest. What hidden rows hold does
+ * not matter. */
 int s1_op_attention_paged_step_async(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n, int32_t Hq,
                                      const s1_kv_pages* pages, const int32_t* pos, int32_t window, int32_t sinks,
                                      float sm_scale, void* out, void* workspace, int64_t workspace_bytes, void* stream);

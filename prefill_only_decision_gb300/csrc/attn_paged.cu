@@ -821,11 +821,12 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
             else tld16(tO + c, u);
             ld_wait();
             pin<CW>(u);
-          }
+            if constexpr (E4)
 #pragma unroll
-          for (int e = 0; e < CW; ++e) {
-            if constexpr (E4) u[e] = __float_as_uint(__uint_as_float(u[e]) * mean * scale_o);
-            u[e] = li > 0 ? u[e] : 0u;
+              for (int e = 0; e < CW; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * mean * scale_o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < CW; ++e) u[e] = 0u;
           }
           float4* at = reinterpret_cast<float4*>(pub + c);
           if (publish) {
