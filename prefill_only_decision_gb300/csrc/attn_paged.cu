@@ -1062,9 +1062,12 @@ void plan_group(Group& gr, int s0, int n_seq, const int* row0, const int* len, c
     seqs.push_back(q);
   }
   gr.next = s;
+  pl.nt = 1;
+  gr.max_ns = 1;
+  t.n = t.start[0] = t.tiles[0] = t.split = 0;
+  if (seqs.empty()) return;      // (nothing but empty sequences: no tiles to share out)
   double best = -1;
   int best_per = 1;
-  pl.nt = 1;
   for (int k = 0; k < 2; ++k) {
     int longest = 0;
     for (const Seq& q : seqs) longest = std::max(longest, q.top[k]);
@@ -1104,8 +1107,6 @@ void plan_group(Group& gr, int s0, int n_seq, const int* row0, const int* len, c
     return x.s < y.s;
   });
   t.n = (int)seqs.size();
-  t.start[0] = t.tiles[0] = t.split = 0;
-  gr.max_ns = 1;
   for (int i = 0; i < t.n; ++i) {
     const Seq& q = seqs[i];
     t.row0[i] = row0 ? row0[q.s] : 0;
