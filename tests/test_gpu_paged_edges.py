@@ -69,3 +69,40 @@ def close(a, got, ref=None):
     assert np.isfinite(got).all()
     err = np.abs(got - ref).max()
     assert err <= a.tol(), (err, a.tol())
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,hd", [(8, 64), (5, 128), (16, 64), (12, 128)])
+def test_step_of_many_tiles(B, Hq, hd, fmt):  # noqa: F811
+    """Scores that climb by 40 within each CTA's run and start again, that fall by as much, and that stay: the base of a warp's
+    rows moves from tile to tile, and the ring's stages are used again. The same bits every time."""
+    n = 200_001
+    a = long_step(B, Hq, hd, fmt, n)
+    base = a.c.rows[0].copy()
+    ramp = np.arange(n) % 1300 / 1300 * 40                # (a run: 3126 tiles / 152 = 20.6 of 64 rows)
+    for sign in (1, -1, 0):
+        x = base.copy()
+        x[0, :, 0, 0] = sign * (ramp + np.abs(x[0, :, 0, 1]))
+        a.q[:, ::hd] = float(hd ** 0.5)                   # (element 0 of each head: its key element is the score)
+        a.c.rows[0] = a.c._put(0, x)
+        got = call(a)
+        close(a, got)
+        first = a.out.clone()
+        for _ in range(3):
+            a.out.fill_(55.0)
+            a.call(a.ws)
+            assert torch.equal(a.out, first)
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16", "e4m3"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 70)])
+@pytest.mark.parametrize("Hq,Hkv,hd", [(8, 2, 64), (10, 2, 128), (12, 1, 128)])
+def test_step_of_many_pairs(B, Hq, Hkv, hd, window, sinks, fmt):  # noqa: F811
+    """Hundreds of sequences of about a thousand rows: pairs follow one another in a CTA, each of several tiles a warp, and
+    the stages go round many times."""
+    g = np.random.default_rng(hd + Hq)
+    pos = [int(p) for p in g.integers(600, 1500, 320)]
+    pos[3], pos[7], pos[100] = -1, 0, 5000
+    a = Paged(B, Hq, Hkv, hd, pos, None, fmt, page=16, window=window, sinks=sinks, spread=1.5)
+    positive_values(a)
+    close(a, call(a))
