@@ -20,9 +20,9 @@
 // their order, so both products take the codes in the order in which wide shared-memory reads find them: row n of an
 // 8-row block of S^T stands for cached row key8(n), and thread (g, t) holds chunk t of a K row (16 d's as four
 // k-steps) and chunk g of V rows (16 columns). K scales multiply the scores. V scales go into the weights as
-// exponents: the base is a running bound of z + e (V's scale 2^(unit + e) f, f in [1/2, 1), unit a warp's first), so
-// neither f16 nor the sums see the scales' range. bf16 queries over e4m3 pages become f16 by a power of two per q
-// head.
+// exponents (V's scale 2^(unit + e) f, f in [1/2, 1), unit a warp's first; rows of scale 0, of pages that are not
+// there, have no part in it): the products' base is a running bound of z + e, the sum's one of z alone, so neither f16
+// nor the sums see the scales' range. bf16 queries over e4m3 pages become f16 by a power of two per q head.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -37,7 +37,8 @@ using namespace t5;
 using namespace pga;
 
 constexpr int KT = 64, PRODUCERS = 3;
-constexpr int NO_UNIT = -10000;
+constexpr int NO_UNIT = 10000;               // (e4m3) no scale yet: far above all, so that rows without one weigh nothing
+constexpr float NO_BASE = -3.402823466e38f;  // below all scores; a first one always moves it (-inf - it: no weight)
 constexpr int LANE_SEQS = 8;                 // up to 32 times as many sequences are counted by each warp alone
 enum Kind { F16 = 0, BF16 = 1, E4M3 = 2 };
 
@@ -422,9 +423,10 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
       if (AHEAD && more) load_q(nx);                           // (used when this pair has ended)
       float o[NH][HD / 16][4] = {};
       float mx[NH][2], sum[NH][2] = {};                        // base and sum of q heads 8 nh + 2 t + e
+      float mz[NH][2];                                         // e4m3: the sum's base, and mx the products'
       int unit = NO_UNIT;                                      // e4m3: O counts 2^unit, the bound of the first scales seen
 #pragma unroll
-      for (int nh = 0; nh < NH; ++nh) mx[nh][0] = mx[nh][1] = -INFINITY;
+      for (int nh = 0; nh < NH; ++nh) mx[nh][0] = mx[nh][1] = mz[nh][0] = mz[nh][1] = NO_BASE;
       for (int x = (grp - i % GROUPS + GROUPS) % GROUPS; x < m && ok; x += GROUPS) {
         const int tile = i + x, st = tile % NST;
         const int j0 = c.tl.at(c.t + x) * KT + sub * 16;       // this warp's first row
@@ -479,26 +481,29 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
             if constexpr (KIND == E4M3) {
               const float* sc = (const float*)(sm + L::SC) + st * 2 * KT + sub * 16 + r;
               ks[b] = sc[0];
-              const uint32_t u = __float_as_uint(sc[KT]);
+              const float v = sc[KT];
+              const uint32_t u = __float_as_uint(v);
               const int E = (int)(u >> 23) - 126;
-              if (unit == NO_UNIT) unit = __reduce_max_sync(0xffffffffu, hid[b] ? NO_UNIT : E);
+              if (unit == NO_UNIT) {                           // (hidden rows and those of scale 0 have no say)
+                const int top = __reduce_max_sync(0xffffffffu, hid[b] || v == 0.f ? INT_MIN : E);
+                if (top != INT_MIN) unit = top;
+              }
               const int rel = E - unit, up = (80 - unit) >> 1;   // (2^-80 below the unit: the rest stays in f)
               ex[b] = (float)max(rel, -80);
-              f[b] = rel >= -80 ? __uint_as_float((u & 0x7fffffu) | 126u << 23)
-                                : sc[KT] * pow2f(up) * pow2f(80 - unit - up);
+              f[b] = rel >= -80 ? __uint_as_float((u & 0x7fffffu) | 126u << 23) : v * pow2f(up) * pow2f(80 - unit - up);
             }
           }
           uint32_t p[NH][2];                                   // P^T: rows 2 t, 2 t + 1 of each block, q head g
 #pragma unroll
           for (int nh = 0; nh < NH; ++nh) {
-            float up[2];                                       // what the bases are taken from: score, or score and exponent
+            float up[2], zt[2];                                // what the bases are taken from: score and exponent; score
             bool move[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
               for (int b = 0; b < 2; ++b) s[nh][2 * b + e] = hid[b] ? -INFINITY : s[nh][2 * b + e] * (qs[nh][e] * ks[b]);
-              if constexpr (KIND == E4M3) up[e] = fmaxf(s[nh][e] + ex[0], s[nh][2 + e] + ex[1]);
-              else up[e] = fmaxf(s[nh][e], s[nh][2 + e]);
+              zt[e] = fmaxf(s[nh][e], s[nh][2 + e]);
+              up[e] = KIND == E4M3 ? fmaxf(s[nh][e] + ex[0], s[nh][2 + e] + ex[1]) : zt[e];
             }
 #pragma unroll
             for (int k = 4; k < 32; k <<= 1) {
@@ -506,14 +511,25 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
               up[1] = fmaxf(up[1], __shfl_xor_sync(0xffffffffu, up[1], k));
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) move[e] = up[e] - mx[nh][e] > TOP;
+            for (int e = 0; e < 2; ++e)
+              move[e] = up[e] - mx[nh][e] > TOP || (KIND == E4M3 && zt[e] - mz[nh][e] > TOP);   // (zt: of a lane's rows)
             if (__any_sync(0xffffffffu, move[0] || move[1])) {
+              // where a base at b goes for a maximum x, and what is multiplied by al for it
+              auto moved = [](float b, float x) { return x - b > TOP ? (fabsf(x) < FAR ? x - HEAD : x) : b; };
+              auto shrink = [](float b, float to) { return b == to ? 1.f : ex2(b - to); };
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float to = move[e] ? (fabsf(up[e]) < FAR ? up[e] - HEAD : up[e]) : mx[nh][e];
-                const float al = mx[nh][e] == to || mx[nh][e] == -INFINITY ? 1.f : ex2(mx[nh][e] - to);
+                const float to = moved(mx[nh][e], up[e]), al = shrink(mx[nh][e], to);
                 mx[nh][e] = to;
-                sum[nh][e] *= al;
+                if constexpr (KIND == E4M3) {
+#pragma unroll
+                  for (int k = 4; k < 32; k <<= 1) zt[e] = fmaxf(zt[e], __shfl_xor_sync(0xffffffffu, zt[e], k));
+                  const float tz = moved(mz[nh][e], zt[e]);
+                  sum[nh][e] *= shrink(mz[nh][e], tz);
+                  mz[nh][e] = tz;
+                } else {
+                  sum[nh][e] *= al;
+                }
 #pragma unroll
                 for (int b = 0; b < HD / 16; ++b) {
                   o[nh][b][e] *= al;
@@ -524,10 +540,10 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
             float w[4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float base = mx[nh][e] == -INFINITY ? 0.f : mx[nh][e];
+              const float base = mx[nh][e], base_z = KIND == E4M3 ? mz[nh][e] : base;
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
-                const float z = s[nh][2 * b + e], d = ex2(z - base);   // (e4m3: the sum's weight)
+                const float z = s[nh][2 * b + e], d = ex2(z - base_z);   // (e4m3: the sum's weight)
                 sum[nh][e] += d;
                 if constexpr (KIND == E4M3) w[2 * b + e] = hid[b] ? 0.f : ex2(z + ex[b] - base) * f[b];
                 else w[2 * b + e] = d;
@@ -610,16 +626,18 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
           float l = sum[half][e];
 #pragma unroll
           for (int k = 4; k < 32; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-          if (g == 0) ml[warp * 8 + 2 * t4 + e] = make_float2(mx[half][e], l);
+          const float base = KIND == E4M3 ? mz[half][e] : mx[half][e];
+          if (g == 0) ml[warp * 8 + 2 * t4 + e] = make_float2(base == NO_BASE ? -INFINITY : base, l);
           float* at = pub + (warp * 8 + 2 * t4 + e) * L::OSTR;
           if (8 * half + 2 * t4 + e >= nq) continue;           // (no such q head)
           if constexpr (KIND == E4M3) {
-            const float inv = l == 0.f || unit == NO_UNIT ? 0.f : 1.f / l, u0 = pow2f(max(unit, -200) >> 1),
-                        u1 = pow2f(max(unit, -200) - (max(unit, -200) >> 1));
+            // O counts 2^(unit + mx - mz) beside the sum: half of it at a time, which fp32 holds
+            const bool some = l != 0.f && unit != NO_UNIT;
+            const float inv = some ? 1.f / l : 0.f, u = some ? ex2(0.5f * (mx[half][e] - mz[half][e] + (float)unit)) : 0.f;
 #pragma unroll
             for (int b = 0; b < HD / 16; ++b) {
-              o[half][b][e] = o[half][b][e] * inv * u0 * u1;
-              o[half][b][2 + e] = o[half][b][2 + e] * inv * u0 * u1;
+              o[half][b][e] = o[half][b][e] * inv * u * u;
+              o[half][b][2 + e] = o[half][b][2 + e] * inv * u * u;
             }
           }
 #pragma unroll

@@ -106,3 +106,48 @@ def test_step_of_many_pairs(B, Hq, Hkv, hd, window, sinks, fmt):  # noqa: F811
     a = Paged(B, Hq, Hkv, hd, pos, None, fmt, page=16, window=window, sinks=sinks, spread=1.5)
     positive_values(a)
     close(a, call(a))
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("Hq", [4, 12])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("up", [0, 6, 12, 100])
+def test_step_behind_absent_pages(B, Hq, hd, page, up):  # noqa: F811
+    """8-bit pages: whole tiles without a page between ordinary ones, first in the run of many a warp; values up to 2^up
+    times as large, scores wide enough that small weights make up part of the sum."""
+    a = long_step(B, Hq, hd, "e4m3", page=page, spread=1.4, q_type="bf16")
+    g = np.random.default_rng(up)
+    tiles = np.flatnonzero(g.random(LONG // 64) < 0.4)
+    tiles = np.union1d(tiles, [0, 1, 2, 3])
+    per = max(1, 64 // page)
+    drop_pages(a, 0, (tiles[:, None] * (64 // page) + np.arange(per)).ravel())
+    scale_rows(a, 0, 1, np.arange(LONG), 2.0 ** up)
+    close(a, call(a))
+    # one row takes nearly all of the weight
+    j = 64 * int(np.setdiff1d(np.arange(1000, 1100), tiles)[0]) + 5
+    q = a.q[0, :hd].double().cpu().numpy()
+    x = a.c.rows[0][:, j:j + 1].copy()
+    x[0, 0, 0] = 40 * q / (q @ q) * hd ** 0.5
+    a.q[:, :Hq * hd] = a.q[:, :hd].repeat(1, Hq)
+    rest = a.c.rows[0]
+    a.c.rows[0] = x
+    places = a.c.places
+    a.c.places = lambda i, n: (places(i, LONG)[0][j:j + 1], places(i, LONG)[1][j:j + 1])
+    rest[:, j:j + 1] = a.c._put(0, x)
+    a.c.places, a.c.rows[0] = places, rest
+    close(a, call(a))
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("Hq", [4, 12])
+@pytest.mark.parametrize("low,high", [(-117, 0), (-117, 110), (-60, 20), (-117, -60), (-20, 4)])
+def test_step_scales_that_grow(B, Hq, hd, low, high):  # noqa: F811
+    """8-bit pages: tiles whose V scales lie far below those of the tiles behind them, and far above."""
+    a = long_step(B, Hq, hd, "e4m3", spread=1.4, q_type="bf16")
+    g = np.random.default_rng(abs(high))
+    tile = np.arange(LONG) // 64
+    small = (g.random(tile[-1] + 1) < 0.5)[tile]
+    small[:64 * 12] = True
+    scale_rows(a, 0, 1, np.flatnonzero(small), 2.0 ** low)
+    scale_rows(a, 0, 1, np.flatnonzero(~small), 2.0 ** high)
+    close(a, call(a))
