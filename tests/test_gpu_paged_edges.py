@@ -151,3 +151,31 @@ def test_step_scales_that_grow(B, Hq, hd, low, high):  # noqa: F811
     scale_rows(a, 0, 1, np.flatnonzero(small), 2.0 ** low)
     scale_rows(a, 0, 1, np.flatnonzero(~small), 2.0 ** high)
     close(a, call(a))
+
+
+# ---- prompts and tokens over 8-bit pages: the ends of what fp32 holds --------------------------
+@pytest.mark.parametrize("up", [-100, 0, 100])
+def test_prompt_behind_absent_pages(B, up):  # noqa: F811
+    a = Paged(B, 4, 1, 64, [2500], [70], "e4m3", page=32, q_type="bf16", spread=1.4)
+    positive_values(a)
+    drop_pages(a, 0, list(range(12)) + [20, 21, 22, 23, 30, 50, 51, 52, 53])
+    scale_rows(a, 0, 1, np.arange(2570), 2.0 ** up)
+    close(a, call(a))
+
+
+@pytest.mark.parametrize("kind", ["step", "prompt"])
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("q_type", ["bf16", "f16"])
+def test_scores_that_vanish(B, kind, window, hd, q_type):  # noqa: F811
+    """Queries of zeros and small ones over tiny K scales: all scores are 0 to fp32, hidden rows stay hidden, and the result
+    is the mean of the visible values."""
+    for ek in (-20, -60, -116):
+        a = Paged(B, 4, 1, hd, [140, 300], None if kind == "step" else [40, 200], "e4m3", page=16, window=window,
+                  sinks=3 if window else 0, q_type=q_type)
+        positive_values(a)
+        for s in range(2):
+            scale_rows(a, s, 0, np.arange(a.c.rows[s].shape[1]), 2.0 ** ek)
+        a.q[::2] = 0
+        a.q[1::2] *= 2.0 ** (-90 if q_type == "bf16" else -6)
+        close(a, call(a))
