@@ -501,7 +501,11 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
-              for (int b = 0; b < 2; ++b) s[nh][2 * b + e] = hid[b] ? -INFINITY : s[nh][2 * b + e] * (qs[nh][e] * ks[b]);
+              for (int b = 0; b < 2; ++b) {
+                float zs = qs[nh][e] * ks[b];
+                if constexpr (KIND == E4M3) zs = fminf(zs, 3.402823466e38f);   // (0 x inf of a score of 0)
+                s[nh][2 * b + e] = hid[b] ? -INFINITY : s[nh][2 * b + e] * zs;
+              }
               zt[e] = fmaxf(s[nh][e], s[nh][2 + e]);
               up[e] = KIND == E4M3 ? fmaxf(s[nh][e] + ex[0], s[nh][2 + e] + ex[1]) : zt[e];
             }

@@ -1,4 +1,5 @@
 // Stream-ordered operators around a paged K/V cache (s1_ops.h): argument checks and dispatch.
+#include <algorithm>
 #include <cmath>
 #include <new>
 
@@ -12,6 +13,7 @@ bool elem(int32_t t) { return t == S1_F16 || t == S1_BF16 || t == S1_F32; }
 size_t elem_bytes(int32_t t) { return t == S1_F32 ? 4 : 2; }
 
 constexpr double TWO_64 = 18446744073709551616.0;
+constexpr float SCALE_MAX = 2.35e38f;   // times log2 e within fp32's range (scores of 0 would be NaN past it)
 
 int check_rope(const s1_rope_spec* r, int32_t hd, RopeArgs* out) {
   out->n_pairs = 0;
@@ -189,7 +191,7 @@ int s1_op_attention_paged_step_async(const void* q, int32_t q_dtype, int64_t q_s
   a.Hq = Hq;
   a.window = window;
   a.sinks = sinks;
-  a.scale = sm_scale;
+  a.scale = std::min(sm_scale, SCALE_MAX);
   a.out = out;
   a.ws = workspace;
   return cuda_rc(launch_attention_paged_step(a, n, pos, sms, (cudaStream_t)stream), "attention_paged_step");
@@ -243,7 +245,7 @@ int s1_op_attention_paged_async(const void* q, int32_t q_dtype, int64_t q_stride
   a.Hq = Hq;
   a.window = window;
   a.sinks = sinks;
-  a.scale = sm_scale;
+  a.scale = std::min(sm_scale, SCALE_MAX);
   a.out = out;
   a.ws = workspace;
   const int sms = sm_count();

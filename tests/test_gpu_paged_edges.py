@@ -179,3 +179,28 @@ def test_scores_that_vanish(B, kind, window, hd, q_type):  # noqa: F811
         a.q[::2] = 0
         a.q[1::2] *= 2.0 ** (-90 if q_type == "bf16" else -6)
         close(a, call(a))
+
+
+@pytest.mark.parametrize("kind", ["step", "prompt"])
+def test_scores_of_zero_times_what_fp32_does_not_hold(B, kind):  # noqa: F811
+    """A query and K scales whose product passes fp32's range, the keys' codes zeros where the query is not: scores of 0."""
+    a = Paged(B, 4, 1, 64, [140], None if kind == "step" else [40], "e4m3", page=16, q_type="bf16")
+    positive_values(a)
+    x = a.c.rows[0].copy()
+    x[0, :, 0, 0] = 0
+    a.c.rows[0] = a.c._put(0, x)
+    scale_rows(a, 0, 0, np.arange(x.shape[1]), 2.0 ** 60)
+    a.q[:] = 0
+    a.q[:, ::64] = 2.0 ** 125
+    close(a, call(a))
+
+
+@pytest.mark.parametrize("kind", ["step", "prompt"])
+@pytest.mark.parametrize("fmt", ["f16", "bf16", "e4m3"])
+def test_the_largest_sm_scale(B, kind, fmt):  # noqa: F811
+    """Scores of 0 at a scale that times log2 e passes fp32's range."""
+    a = Paged(B, 4, 1, 64, [140], None if kind == "step" else [40], fmt, page=16)
+    positive_values(a)
+    a.q[:] = 0
+    a.scale = 3.4e38
+    close(a, call(a))
