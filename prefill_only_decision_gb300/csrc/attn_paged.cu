@@ -159,11 +159,11 @@ __device__ __forceinline__ void plane_sync(int plane) {
   else asm volatile("bar.sync 1, 128;" ::: "memory");
 }
 
-// The exponent bound of a scale: scale < 2^E. Scales that are not finite or not there have none.
+// The exponent bound of a scale: scale < 2^E (subnormal ones: 2^-126). Scales that are not finite or not there have none.
 constexpr int NO_BOUND = -1000;
 __device__ __forceinline__ int bound_of(float scale) {
   const uint32_t u = __float_as_uint(scale);
-  return (u >> 23) == 0 || (u >> 23) >= 255 ? NO_BOUND : (int)(u >> 23) - 126;
+  return u == 0 || (u >> 23) >= 255 ? NO_BOUND : (int)(u >> 23) - 126;
 }
 
 // One of a CTA's items: (sequence, one or two query tiles, kv head) and a part of its key tiles.

@@ -38,6 +38,7 @@ using namespace pga;
 
 constexpr int KT = 64, PRODUCERS = 3;
 constexpr int NO_UNIT = 10000;               // (e4m3) no scale yet: far above all, so that rows without one weigh nothing
+constexpr int NEAR = 24;                     // (e4m3) exponents of V's scales this near the unit are ordinary
 constexpr float NO_BASE = -3.402823466e38f;  // below all scores; a first one always moves it (-inf - it: no weight)
 constexpr int LANE_SEQS = 8;                 // up to 32 times as many sequences are counted by each warp alone
 enum Kind { F16 = 0, BF16 = 1, E4M3 = 2 };
@@ -423,7 +424,11 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
       if (AHEAD && more) load_q(nx);                           // (used when this pair has ended)
       float o[NH][HD / 16][4] = {};
       float mx[NH][2], sum[NH][2] = {};                        // base and sum of q heads 8 nh + 2 t + e
-      float mz[NH][2];                                         // e4m3: the sum's base, and mx the products'
+      // e4m3: the sum's base (mx: the products'). It is looked at where mx moves; while exponents stay within NEAR that is
+      // enough: a move leaves mx - mz <= TOP - HEAD + NEAR, and a later z <= mx + TOP + NEAR is then below mz + 70. Once
+      // one did not (wide), it is looked at in every tile
+      float mz[NH][2];
+      bool wide = false;
       int unit = NO_UNIT;                                      // e4m3: O counts 2^unit, the bound of the first scales seen
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh) mx[nh][0] = mx[nh][1] = mz[nh][0] = mz[nh][1] = NO_BASE;
@@ -473,7 +478,7 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
           }
           // ---- scores in the log2 domain, hidden rows -inf
           bool hid[2] = {false, false};                        // rows key8(g), 8 + key8(g)
-          float ks[2] = {1.f, 1.f}, f[2], ex[2];               // e4m3: K's scale, V's fraction and exponent
+          float ks[2] = {1.f, 1.f}, v[2], f[2], ex[2];         // e4m3: K's scale, V's and its fraction and exponent
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             const int r = b * 8 + key8<KIND>(g), j = j0 + r;
@@ -481,22 +486,41 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
             if constexpr (KIND == E4M3) {
               const float* sc = (const float*)(sm + L::SC) + st * 2 * KT + sub * 16 + r;
               ks[b] = sc[0];
-              const float v = sc[KT];
-              const uint32_t u = __float_as_uint(v);
-              const int E = (int)(u >> 23) - 126;
-              if (unit == NO_UNIT) {                           // (hidden rows and those of scale 0 have no say)
-                const int top = __reduce_max_sync(0xffffffffu, hid[b] || v == 0.f ? INT_MIN : E);
-                if (top != INT_MIN) unit = top;
+              v[b] = sc[KT];
+            }
+          }
+          if constexpr (KIND == E4M3) {
+            int E[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const uint32_t u = __float_as_uint(v[b]);
+              E[b] = (int)(u >> 23) - 126;
+              ex[b] = (float)(E[b] - unit);
+              f[b] = __uint_as_float((u & 0x7fffffu) | 126u << 23);
+            }
+            // a first scale, one far from the unit, or one at or below fp32's smallest normal number
+            if (__any_sync(0xffffffffu, min(E[0], E[1]) < max(unit - NEAR, -125) || max(E[0], E[1]) > unit + NEAR)) {
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                if (unit == NO_UNIT) {                         // (hidden rows and those of scale 0 have no say)
+                  const int top = __reduce_max_sync(0xffffffffu, hid[b] || v[b] == 0.f ? INT_MIN : E[b]);
+                  if (top != INT_MIN) unit = top;
+                }
+              bool far = false;
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const int rel = max(E[b] - unit, -80), up = -(unit + rel);   // (2^-80 below the unit: the rest stays in f)
+                ex[b] = (float)rel;
+                f[b] = v[b] * pow2f(up >> 1) * pow2f(up - (up >> 1));
+                far |= !hid[b] && (rel < -NEAR || rel > NEAR);
               }
-              const int rel = E - unit, up = (80 - unit) >> 1;   // (2^-80 below the unit: the rest stays in f)
-              ex[b] = (float)max(rel, -80);
-              f[b] = rel >= -80 ? __uint_as_float((u & 0x7fffffu) | 126u << 23) : v * pow2f(up) * pow2f(80 - unit - up);
+              wide |= __any_sync(0xffffffffu, far) != 0;
             }
           }
           uint32_t p[NH][2];                                   // P^T: rows 2 t, 2 t + 1 of each block, q head g
 #pragma unroll
           for (int nh = 0; nh < NH; ++nh) {
-            float up[2], zt[2];                                // what the bases are taken from: score and exponent; score
+            float up[2];                                       // what the base is taken from: score, or score and exponent
             bool move[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -506,8 +530,8 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
                 if constexpr (KIND == E4M3) zs = fminf(zs, 3.402823466e38f);   // (0 x inf of a score of 0)
                 s[nh][2 * b + e] = hid[b] ? -INFINITY : s[nh][2 * b + e] * zs;
               }
-              zt[e] = fmaxf(s[nh][e], s[nh][2 + e]);
-              up[e] = KIND == E4M3 ? fmaxf(s[nh][e] + ex[0], s[nh][2 + e] + ex[1]) : zt[e];
+              if constexpr (KIND == E4M3) up[e] = fmaxf(s[nh][e] + ex[0], s[nh][2 + e] + ex[1]);
+              else up[e] = fmaxf(s[nh][e], s[nh][2 + e]);
             }
 #pragma unroll
             for (int k = 4; k < 32; k <<= 1) {
@@ -515,9 +539,8 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
               up[1] = fmaxf(up[1], __shfl_xor_sync(0xffffffffu, up[1], k));
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              move[e] = up[e] - mx[nh][e] > TOP || (KIND == E4M3 && zt[e] - mz[nh][e] > TOP);   // (zt: of a lane's rows)
-            if (__any_sync(0xffffffffu, move[0] || move[1])) {
+            for (int e = 0; e < 2; ++e) move[e] = up[e] - mx[nh][e] > TOP;
+            if (__any_sync(0xffffffffu, move[0] || move[1] || (KIND == E4M3 && wide))) {
               // where a base at b goes for a maximum x, and what is multiplied by al for it
               auto moved = [](float b, float x) { return x - b > TOP ? (fabsf(x) < FAR ? x - HEAD : x) : b; };
               auto shrink = [](float b, float to) { return b == to ? 1.f : ex2(b - to); };
@@ -526,9 +549,10 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
                 const float to = moved(mx[nh][e], up[e]), al = shrink(mx[nh][e], to);
                 mx[nh][e] = to;
                 if constexpr (KIND == E4M3) {
+                  float z = fmaxf(s[nh][e], s[nh][2 + e]);
 #pragma unroll
-                  for (int k = 4; k < 32; k <<= 1) zt[e] = fmaxf(zt[e], __shfl_xor_sync(0xffffffffu, zt[e], k));
-                  const float tz = moved(mz[nh][e], zt[e]);
+                  for (int k = 4; k < 32; k <<= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, k));
+                  const float tz = moved(mz[nh][e], z);
                   sum[nh][e] *= shrink(mz[nh][e], tz);
                   mz[nh][e] = tz;
                 } else {

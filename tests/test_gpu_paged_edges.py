@@ -108,10 +108,8 @@ def test_step_of_many_pairs(B, Hq, Hkv, hd, window, sinks, fmt):  # noqa: F811
     close(a, call(a))
 
 
-@pytest.mark.parametrize("hd", [64, 128])
-@pytest.mark.parametrize("Hq", [4, 12])
-@pytest.mark.parametrize("page", [16, 64])
-@pytest.mark.parametrize("up", [0, 6, 12, 100])
+@pytest.mark.parametrize("Hq,hd,page,up", [(4, 128, 64, 0), (12, 64, 16, 6), (4, 64, 16, 12), (12, 128, 64, 12),
+                                           (4, 128, 16, 100), (12, 64, 64, 100)])
 def test_step_behind_absent_pages(B, Hq, hd, page, up):  # noqa: F811
     """8-bit pages: whole tiles without a page between ordinary ones, first in the run of many a warp; values up to 2^up
     times as large, scores wide enough that small weights make up part of the sum."""
@@ -138,9 +136,8 @@ def test_step_behind_absent_pages(B, Hq, hd, page, up):  # noqa: F811
     close(a, call(a))
 
 
-@pytest.mark.parametrize("hd", [64, 128])
-@pytest.mark.parametrize("Hq", [4, 12])
-@pytest.mark.parametrize("low,high", [(-117, 0), (-117, 110), (-60, 20), (-117, -60), (-20, 4)])
+@pytest.mark.parametrize("Hq,hd,low,high", [(4, 128, -117, 0), (4, 64, -117, 110), (12, 128, -117, 110), (12, 64, -60, 20),
+                                            (4, 128, -117, -60), (12, 64, -20, 4)])
 def test_step_scales_that_grow(B, Hq, hd, low, high):  # noqa: F811
     """8-bit pages: tiles whose V scales lie far below those of the tiles behind them, and far above."""
     a = long_step(B, Hq, hd, "e4m3", spread=1.4, q_type="bf16")
@@ -204,3 +201,19 @@ def test_the_largest_sm_scale(B, kind, fmt):  # noqa: F811
     a.q[:] = 0
     a.scale = 3.4e38
     close(a, call(a))
+
+
+@pytest.mark.parametrize("kind", ["step", "prompt"])
+@pytest.mark.parametrize("exp", [-118, -124, -130])
+def test_subnormal_scales(B, kind, exp):  # noqa: F811
+    """V scales below fp32's smallest normal number (2^-126) count as what they are: ordinary ones (about 2^-7) times 2^exp,
+    of which fp32 keeps all bits."""
+    a = Paged(B, 4, 1, 64, [400], None if kind == "step" else [40], "e4m3", page=16, q_type="bf16")
+    positive_values(a)
+    n = a.c.rows[0].shape[1]
+    scale_rows(a, 0, 1, np.arange(n), 2.0 ** exp * np.where(np.arange(n) % 3 == 0, 1.375, 1.0))
+    got, ref = call(a), a.ref()
+    # besides: half a step of bf16's subnormals (2^-134); and the joins of at most 30 parts hold means times 2^-10 or more in
+    # fp32, each rounded by 2^-150, so 30 * 2^-140
+    assert (np.abs(got - ref) <= a.tol() + 2.0 ** -134 + 2.0 ** -135).all()
+    assert got.max() > 0
