@@ -782,7 +782,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       float l = lo2(l2) + hi2(l2);
       if (li > 0 && !wwait(&o_done[x], (x ? dn1 : dn0) & 1)) return false;
       fence_after();
-      const float scale_o = E4 ? pow2f(unit - 7) : 1.f, mean = E4 ? (l == 0.f ? 0.f : 1.f / l) : 1.f;   // (SHARE: e4m3)
+      const float scale_o = E4 ? pow2f(unit - 7) : 1.f, mean = E4 ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
       float w0 = 1.f, w1 = 0.f;                  // weights of the two streams' sums
       const bool publish = !pair && x == 1;      // (o, m, l) into the K/V stages, for stream 0
       if (publish) {                             // once stream 0 has read its last tile, and the item before's sums, from them
@@ -888,7 +888,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         }
         if (publish) *reinterpret_cast<float2*>(pub + HD) = make_float2(m, l);
         else if (rw.live && ie.ns > 1)
-          reinterpret_cast<float2*>((float*)a.ws + (int64_t)tab.split * 2 * BQ * HD)[pi * BQ + r] = make_float2(m, l);
+          reinterpret_cast<float2*>((float*)a.ws + (int64_t)tab.split * 2 * BQ * HD)[pi * BQ + r] =
+              E4 ? leveled(m, l) : make_float2(m, l);
       }
       if (publish) {
         fence_async_smem();                      // (TMA tiles follow these writes)

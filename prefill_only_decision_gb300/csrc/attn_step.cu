@@ -654,8 +654,8 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
           float l = sum[half][e];
 #pragma unroll
           for (int k = 4; k < 32; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-          const float base = KIND == E4M3 ? mz[half][e] : mx[half][e];
-          if (g == 0) ml[warp * 8 + 2 * t4 + e] = make_float2(base == NO_BASE ? -INFINITY : base, l);
+          const float m0 = KIND == E4M3 ? mz[half][e] : mx[half][e], m1 = m0 == NO_BASE ? -INFINITY : m0;
+          if (g == 0) ml[warp * 8 + 2 * t4 + e] = KIND == E4M3 ? leveled(m1, l) : make_float2(m1, l);
           float* at = pub + (warp * 8 + 2 * t4 + e) * L::OSTR;
           if (8 * half + 2 * t4 + e >= nq) continue;           // (no such q head)
           if constexpr (KIND == E4M3) {

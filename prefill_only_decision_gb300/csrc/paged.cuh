@@ -72,8 +72,14 @@ __device__ __forceinline__ float pow2f(int e) {
 }
 
 // Sums over e4m3 pages pass between warps, CTAs and kernels as means (o / l), since V's scales may leave fp32 no room
-// beside the weights; such a mean's share is its l times 2^-SHARE, which leaves room on both sides.
-constexpr float SHARE = 9.5367431640625e-7f, UNSHARE = 1048576.f;   // 2^-20, 2^20
+// beside the weights. Their l is brought to 1 .. 2 by its base (leveled), and a mean's share is l times SHARE: the
+// shares of 8192 parts together are at most 1, so that no sum passes the largest mean.
+constexpr float SHARE = 6.103515625e-5f, UNSHARE = 16384.f;   // 2^-14, 2^14
+__device__ __forceinline__ float2 leveled(float m, float l) {
+  const uint32_t u = __float_as_uint(l);
+  if (!(fabsf(m) < FAR) || u - 0x800000u >= 0x7f000000u) return make_float2(m, l);   // (bases that hold no more bits; 0, NaN)
+  return make_float2(m + (float)((int)(u >> 23) - 127), __uint_as_float((u & 0x7fffffu) | 127u << 23));
+}
 
 // The pages as a tensor (hd, page rows, heads, pages, planes) in boxes of `rows` rows of up to 128 bytes. A page id
 // outside 0 .. n_pages - 1 is outside the tensor, which TMA reads as zeros.

@@ -213,7 +213,20 @@ def test_subnormal_scales(B, kind, exp):  # noqa: F811
     n = a.c.rows[0].shape[1]
     scale_rows(a, 0, 1, np.arange(n), 2.0 ** exp * np.where(np.arange(n) % 3 == 0, 1.375, 1.0))
     got, ref = call(a), a.ref()
-    # besides: half a step of bf16's subnormals (2^-134); and the joins of at most 30 parts hold means times 2^-10 or more in
-    # fp32, each rounded by 2^-150, so 30 * 2^-140
+    # besides: half a step of bf16's subnormals (2^-134); and the two joins hold means times 2^-14 l in fp32 (l: 1 .. 2), each
+    # rounded by 2^-150, and divide by the sum of all these l: 2^-136 at most
     assert (np.abs(got - ref) <= a.tol() + 2.0 ** -134 + 2.0 ** -135).all()
     assert got.max() > 0
+
+
+@pytest.mark.parametrize("kind", ["step", "prompt"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_values_near_the_largest_number(B, kind, hd):  # noqa: F811
+    """V scales that bring the values to fp32's last binade: many rows of even weight, joined from many parts,
+    are a mean within their range."""
+    n = 60_000
+    a = Paged(B, 4, 1, hd, [n], None if kind == "step" else [9], "e4m3", page=64, q_type="bf16", spread=0.5)
+    positive_values(a)
+    scale_rows(a, 0, 1, np.arange(a.c.rows[0].shape[1]), 2.0 ** 126)
+    assert 2.0 ** 127 < a.c.rows[0][1].max() < 2.0 ** 128
+    close(a, call(a))
