@@ -209,7 +209,7 @@ int s1_op_linattn_step_async(const void* q, const void* k, const void* v, int32_
  * pairs or taking turns, as axis says. Angles are exact to 2^-64 turns times the position, whatever the
  * position; sine, cosine and products are fp32. Negated frequencies undo a rotation (and give its gradient). */
 typedef struct s1_rope_spec {
-  const double* inv_freq;      /* host [n_pairs], radians per position, finite                    */
+  const double* inv_freq;      /* host [n_pairs], radians per position, at most 2^40 either way   */
   const uint8_t* axis;         /* host [n_pairs], each below n_axes; NULL: axis 0                 */
   int32_t n_pairs;             /* a multiple of 8, at most hd / 2                                 */
   int32_t n_axes;              /* 1 .. 4                                                          */

@@ -12,7 +12,7 @@ namespace {
 bool elem(int32_t t) { return t == S1_F16 || t == S1_BF16 || t == S1_F32; }
 size_t elem_bytes(int32_t t) { return t == S1_F32 ? 4 : 2; }
 
-constexpr double TWO_64 = 18446744073709551616.0;
+constexpr double TWO_64 = 18446744073709551616.0, FREQ_MAX = 1099511627776.0;   // 2^64, 2^40
 constexpr float SCALE_MAX = 2.35e38f;   // times log2 e within fp32's range (scores of 0 would be NaN past it)
 
 int check_rope(const s1_rope_spec* r, int32_t hd, RopeArgs* out) {
@@ -25,13 +25,14 @@ int check_rope(const s1_rope_spec* r, int32_t hd, RopeArgs* out) {
   out->n_pairs = r->n_pairs;
   for (int i = 0; i < r->n_pairs; ++i) {
     if (!std::isfinite(r->inv_freq[i])) return bad("rope: a frequency is not finite");
+    if (std::fabs(r->inv_freq[i]) > FREQ_MAX) return unsupported("rope: a frequency above 2^40 radians per position");
     if (r->axis && r->axis[i] >= r->n_axes) return bad("rope: an axis is not below n_axes");
-    // w / 2 pi as hi + lo, so that its fraction is right to 2^-64 and not to a double's 2^-53
+    // w / 2 pi as hi + lo, so that its fraction is right to 2^-64 and not to a double's 2^-53 (up to FREQ_MAX: lo holds no
+    // more beside a larger hi)
     const double w = std::fabs(r->inv_freq[i]), hi = w * 0.15915494309189535;
     const double lo = std::fma(w, 0.15915494309189535, -hi) + w * -9.839338337591243e-18;
     const double frac = (hi - std::floor(hi)) * TWO_64, rest = lo * TWO_64;   // 0 .. 2^64
-    const uint64_t turn = (frac >= TWO_64 ? 0 : (uint64_t)frac) +
-                          (std::fabs(rest) < 9.2e18 ? (uint64_t)(int64_t)std::llround(rest) : 0);   // (past 2^52 turns: 0)
+    const uint64_t turn = (frac >= TWO_64 ? 0 : (uint64_t)frac) + (uint64_t)(int64_t)std::llround(rest);
     out->turn[i] = r->inv_freq[i] < 0 ? 0 - turn : turn;
     out->axis[i] = r->axis ? r->axis[i] : 0;
   }

@@ -3,7 +3,7 @@ are used again, pages that are not there, scales at the ends of their range. Aga
 import numpy as np
 import pytest
 
-from test_gpu_paged_ops import B, Paged, stream  # noqa: F401  (B: the fixture)
+from test_gpu_paged_ops import B, Paged, rotate_ref, rotation_tol, stream  # noqa: F401  (B: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -230,3 +230,21 @@ def test_values_near_the_largest_number(B, kind, hd):  # noqa: F811
     scale_rows(a, 0, 1, np.arange(a.c.rows[0].shape[1]), 2.0 ** 126)
     assert 2.0 ** 127 < a.c.rows[0][1].max() < 2.0 ** 128
     close(a, call(a))
+
+
+# ---- rotations --------------------------------------------------------------------------------
+def test_frequencies_of_any_size(B):  # noqa: F811
+    """From a turn in 2^60 positions to 2^40 radians a position, both ways, at positions out to both ends of 32 bits."""
+    g = np.random.default_rng(0)
+    w = np.concatenate([2.0 ** g.uniform(-60, 40, 30) * g.choice([-1.0, 1.0], 30), [2.0 ** 40, -2.0 ** 40]])
+    pos = np.array([[0, 1, -1, 2 ** 31 - 1, -2 ** 31, 77777, 2 ** 24 + 1]], np.int32)
+    rows, H, hd = pos.shape[1], 2, 64
+    x = torch.from_numpy(g.standard_normal((rows, H * hd))).float()
+    d, p = x.cuda(), torch.from_numpy(pos).cuda()
+    y = torch.empty_like(d)
+    B.op_rope_async(d.data_ptr(), B.S1_F32, H * hd, rows, H, hd, B.Rope(w), p.data_ptr(), rows, y.data_ptr(), B.S1_F32, H * hd,
+                    stream())
+    xd = x.double().numpy().reshape(rows, H, hd)
+    ref, got = rotate_ref(xd, pos, w, [0] * 32), y.double().cpu().numpy().reshape(rows, H, hd)
+    tol, u, tiny = rotation_tol(xd, 32, "f32")
+    assert (np.abs(got - ref) <= tol + u * np.abs(ref) + tiny).all(), np.abs(got - ref).max()
