@@ -206,8 +206,10 @@ int s1_op_linattn_step_async(const void* q, const void* k, const void* v, int32_
  * angle pos[axis[i]] * inv_freq[i] (rotate-half; the rest of the head stays as it is):
  *   y_i = x_i cos - x_{i+n_pairs} sin,   y_{i+n_pairs} = x_{i+n_pairs} cos + x_i sin.
  * Text has one axis; pictures and video have one for each of time, height and width, in runs of
- * pairs or taking turns, as axis says. Angles are exact to 2^-64 turns times the position, whatever the
- * position; sine, cosine and products are fp32. Negated frequencies undo a rotation (and give its gradient). */
+ * pairs or taking turns, as axis says. A frequency is held to 2^-64 turns, whole turns are left out exactly and the
+ * rest of an angle is rounded to 2^-32 turns: it is right to 2^-33 turns plus 2^-64 times the position, whatever the
+ * position. Sine and cosine, within 2^-23, and products are fp32. Negated frequencies undo a rotation (and give its
+ * gradient). */
 typedef struct s1_rope_spec {
   const double* inv_freq;      /* host [n_pairs], radians per position, at most 2^40 either way   */
   const uint8_t* axis;         /* host [n_pairs], each below n_axes; NULL: axis 0                 */

@@ -2,8 +2,8 @@
 //
 // Pair i of a head is turned by pos * w_i. In fp32 that angle is lost at far positions (2^20 radians: an error of
 // 0.06), and fp64 is slow here; turns as integers are neither: w_i / 2 pi modulo 1 in units of 2^-64 times the
-// position is one 64-bit product whose overflow is the whole turns. Its top 32 bits give the quadrant and an angle
-// within an eighth of a turn, whose sine and cosine fp32 holds to its last bit or two.
+// position is one 64-bit product whose overflow is the whole turns. Its top 32 bits (an angle is rounded to 2^-32 turns)
+// give the quadrant and an angle within an eighth of a turn, whose sine and cosine are within 2^-23.
 //
 // Every element is read and written once: HBM bound. A block takes tiles of RB rows in turn: for each it makes the
 // rows' n_pairs sines and cosines once into shared memory for all heads (a sine in every thread that uses one would
@@ -28,7 +28,7 @@ using kvc::Raw;
 constexpr int THREADS = 256, RB_MAX = 16, PASSES = 4;         // rows of a tile; angles of a tile that a thread makes
 
 // cos and sin of pos * turn (2^-64 turns): quadrant and rest, the rest's Taylor series (|y| <= pi / 4: the terms left
-// out are below 2^-29 of the sine and 2^-32 of the cosine).
+// out are below 2^-28 of the sine and 2^-32 of the cosine).
 __device__ __forceinline__ float2 cos_sin(int pos, uint64_t turn) {
   const uint64_t ph = (uint64_t)(int64_t)pos * turn;
   const uint32_t p = (uint32_t)((ph + 0x80000000ull) >> 32);
