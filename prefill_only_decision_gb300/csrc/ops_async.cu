@@ -8,6 +8,18 @@ using namespace s1::opc;
 using namespace s1;
 
 namespace {
+// The kernels' words side by side, for one copy to the host (a copy each: 36 us a call of s1_op_sync on an idle stream
+// with four of them, 19 with two).
+struct Words {
+  uint64_t* at[4];
+};
+__device__ uint64_t g_now[4];
+__global__ void gather_words(const Words w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (threadIdx.x == i) g_now[i] = *(volatile uint64_t*)w.at[i];
+}
+
 // Checks shared by both directions of the 8-bit snapshot. *skip: nothing to do.
 int check_kv(const void* k, const void* v, int32_t dtype, int64_t ks, int64_t vs, int32_t n_rows,
              int32_t Hkv, int32_t hd, const void* codes, const void* scales, int32_t cap, int32_t pos0, bool* skip) {
@@ -58,20 +70,22 @@ extern "C" {
 int s1_op_sync(void* stream) {
   static GiveUps<4> told;
   cudaStream_t st = (cudaStream_t)stream;
-  uint64_t* word[4] = {};
+  Words words = {};
+  void* now_at = nullptr;
   int dev = 0;
   bool any = false;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = attention_shared_gave_up_word(&word[0]);
-  if (e == cudaSuccess) e = linattn_gave_up_word(&word[1]);
-  if (e == cudaSuccess) e = attention_step_gave_up_word(&word[2]);
-  if (e == cudaSuccess) e = attention_paged_gave_up_word(&word[3]);
+  if (e == cudaSuccess) e = attention_shared_gave_up_word(&words.at[0]);
+  if (e == cudaSuccess) e = linattn_gave_up_word(&words.at[1]);
+  if (e == cudaSuccess) e = attention_step_gave_up_word(&words.at[2]);
+  if (e == cudaSuccess) e = attention_paged_gave_up_word(&words.at[3]);
+  if (e == cudaSuccess) e = cudaGetSymbolAddress(&now_at, g_now);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e == cudaSuccess)
-    e = (cudaError_t)told.news(dev, [&](uint64_t* now) {
-      cudaError_t r = cudaSuccess;
-      for (int i = 0; i < 4 && r == cudaSuccess; ++i)
-        r = cudaMemcpyAsync(&now[i], word[i], sizeof(now[i]), cudaMemcpyDeviceToHost, st);
+    e = (cudaError_t)told.news(dev, [&](uint64_t* now) {     // (one caller at a time: g_now is its own)
+      gather_words<<<1, 4, 0, st>>>(words);
+      cudaError_t r = cudaGetLastError();
+      if (r == cudaSuccess) r = cudaMemcpyAsync(now, now_at, sizeof(g_now), cudaMemcpyDeviceToHost, st);
       if (r == cudaSuccess) r = cudaStreamSynchronize(st);
       return (int)r;
     }, &any);
