@@ -122,15 +122,6 @@ __device__ __forceinline__ bool drop_nonfinite(uint4& x) {   // true: there was 
   x = make_uint4(drop_nonfinite2<BF>(x.x), drop_nonfinite2<BF>(x.y), drop_nonfinite2<BF>(x.z), drop_nonfinite2<BF>(x.w));
   return true;
 }
-template <bool BF>
-__device__ __forceinline__ uint32_t pack_w(float a, float b) {
-  if constexpr (BF) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    return h2u(a, b);
-  }
-}
 
 // Eight e4m3 codes times f to f16. FAST: f is an f16 value.
 template <bool FAST>
@@ -903,7 +894,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       }
       fence_before();                            // (the reads of O come before the next item's products)
       tiles += n;
-      dn0 += pair ? n > 0 : n > 0;
+      dn0 += n > 0;
       dn1 += pair ? n > 0 && it.two : n > 1;
       return true;
     });

@@ -116,15 +116,6 @@ __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
 }
-template <bool BF>
-__device__ __forceinline__ uint32_t pack_w(float a, float b) {
-  if constexpr (BF) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    return h2u(a, b);
-  }
-}
 // The computing warps.
 template <int N>
 __device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
@@ -352,7 +343,7 @@ __global__ void __launch_bounds__(Lay<HD, KIND, NH>::THREADS, 1)
       return true;
     });
   } else {
-    // ---- computing warps: rows 16 sub .. +15 of every second tile
+    // ---- computing warps: rows 16 sub .. +15 of every second tile, or third with 12 warps
     const int grp = warp >> 2, sub = warp & 3, g = lane >> 2, t4 = lane & 3;
     const float sl2 = a.scale * 1.4426950408889634f;
     float* pub = (float*)(sm + L::OUT);
@@ -809,7 +800,7 @@ cudaError_t attention_step_gave_up_word(uint64_t** out) {
   return cudaGetSymbolAddress(reinterpret_cast<void**>(out), pgs::g_given_up);
 }
 
-int64_t attention_paged_step_ws_bytes(int, int, int, int hd, int num_sms) {
+int64_t attention_paged_step_ws_bytes(int hd, int num_sms) {
   return (int64_t)num_sms * (2 * pgs::slot_floats(hd) * 4 + (int64_t)sizeof(pgs::Record));
 }
 

@@ -286,7 +286,7 @@ struct PagedAttnArgs {
 };
 // Single tokens: pos on the device.
 cudaError_t launch_attention_paged_step(const PagedAttnArgs& a, int n, const int* pos, int num_sms, cudaStream_t st);
-int64_t attention_paged_step_ws_bytes(int n, int Hq, int Hkv, int hd, int num_sms);
+int64_t attention_paged_step_ws_bytes(int hd, int num_sms);
 // Prompts: sequences as host arrays (empty ones allowed). *too_small: nothing was launched, the workspace is too small.
 cudaError_t launch_attention_paged(const PagedAttnArgs& a, int n_seq, const int* row0, const int* len, const int* pos0,
                                    int num_sms, int64_t ws_bytes, bool* too_small, cudaStream_t st);

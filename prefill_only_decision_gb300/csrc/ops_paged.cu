@@ -167,7 +167,7 @@ int s1_op_attention_paged_step_workspace(int32_t n, int32_t Hq, int32_t Hkv, int
   const int rc = check_heads(Hq, Hkv);
   if (rc != S1_OK) return rc;
   if (hd != 64 && hd != 128) return unsupported("attention_paged: head dim must be 64 or 128");
-  *bytes = attention_paged_step_ws_bytes(n, Hq, Hkv, hd, sm_count());
+  *bytes = attention_paged_step_ws_bytes(hd, sm_count());
   return S1_OK;
 }
 
@@ -184,7 +184,7 @@ int s1_op_attention_paged_step_async(const void* q, int32_t q_dtype, int64_t q_s
   if (!q || !out || !pos) return bad("attention_paged_step: a NULL pointer");
   if (!aligned(pos, 4)) return bad("attention_paged_step: misaligned pos");
   const int sms = sm_count();
-  const int64_t need = attention_paged_step_ws_bytes(n, Hq, pages->Hkv, pages->hd, sms);
+  const int64_t need = attention_paged_step_ws_bytes(pages->hd, sms);
   if (need > 0 && (!workspace || workspace_bytes < need)) return bad("attention_paged_step: the workspace is too small");
   a.q = q;
   a.bf16 = q_dtype == S1_BF16;

@@ -60,6 +60,16 @@ __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(t5::smem_u32(bar)) : "memory");
 }
 
+// Two fp32 values, rounded, as a pair of bf16 or f16.
+template <bool BF>
+__device__ __forceinline__ uint32_t pack_w(float a, float b) {
+  if constexpr (BF) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    return t5::h2u(a, b);
+  }
+}
 // Four e4m3 codes to two f16 pairs.
 __device__ __forceinline__ void widen4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
   asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
