@@ -101,7 +101,7 @@ def test_step_of_many_pairs(B, Hq, Hkv, hd, window, sinks, fmt):  # noqa: F811
     """Hundreds of sequences of about a thousand rows: pairs follow one another in a CTA, each of several tiles a warp, and
     the stages go round many times."""
     g = np.random.default_rng(hd + Hq)
-    pos = [int(p) for p in g.integers(600, 1500, 320)]
+    pos = [int(p) for p in g.integers(600, 1500, 160)]
     pos[3], pos[7], pos[100] = -1, 0, 5000
     a = Paged(B, Hq, Hkv, hd, pos, None, fmt, page=16, window=window, sinks=sinks, spread=1.5)
     positive_values(a)
