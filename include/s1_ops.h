@@ -200,7 +200,8 @@ int s1_op_linattn_step_async(const void* q, const void* k, const void* v, int32_
 /* ---- stream-ordered operators around a paged K/V cache -------------------------------------
  * For sequences with caches of their own that grow row by row: rotary positions, rows appended to
  * pages, attention of prompts and of single tokens over the pages. Calls, streams, workspaces, errors
- * and s1_op_sync as for the operators above. */
+ * and s1_op_sync as for the operators above. What the device arrays of numbers hold (positions, sequences, tables)
+ * is read more than once and must not change while a call runs. */
 
 /* Rotary positions: of each head's first 2 * n_pairs elements, pair (i, i + n_pairs) is turned by the
  * angle pos[axis[i]] * inv_freq[i] (rotate-half; the rest of the head stays as it is):
@@ -218,7 +219,7 @@ typedef struct s1_rope_spec {
 } s1_rope_spec;
 
 /* A paged cache. data: [2, n_pages, Hkv, page_rows, hd] (K plane, V plane), f16, bf16, or e4m3 codes with
- * scales fp32 [2, n_pages, Hkv, page_rows] (positive; appended rows follow s1_op_kv_quant_async's rule, so
+ * scales fp32 [2, n_pages, Hkv, page_rows] (positive and finite; appended rows follow s1_op_kv_quant_async's rule, so
  * theirs are powers of two), both 16-byte aligned. page_rows 16, 32, 64 or 128; hd 64 or 128.
  * table: DEVICE int32 [n_seq, table_stride], the first cols of a row in use: row j of sequence s is row
  * j % page_rows of page table[s][j / page_rows]. Entries past a sequence's rows are not read. A page id
@@ -264,8 +265,9 @@ int s1_op_kv_append_async(const void* q, const void* k, const void* v, int32_t d
  * -inf, gives zeros. Each visible row is read once for up to 16 q heads of its kv head, long and short sequences' rows
  * split evenly over the SMs and joined in a fixed order; the split follows pos on the device, so a captured call stays
  * balanced as positions grow. Softmax statistics and sums are fp32, the weights are rounded once to the product's
- * 16-bit type (f16 for e4m3 codes), f16 with its precision down to 2^-24 of the largest. What hidden rows hold does
- * not matter. */
+ * 16-bit type (f16 for e4m3 codes, V's scale then with the weight), f16 with its precision down to 2^-24 of the
+ * largest. bf16 queries over e4m3 pages become f16 by a power of two per head: elements below 2^-28 of the head's largest
+ * lose bits, below 2^-38 they count as 0. What hidden rows hold does not matter. */
 int s1_op_attention_paged_step_async(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n, int32_t Hq,
                                      const s1_kv_pages* pages, const int32_t* pos, int32_t window, int32_t sinks,
                                      float sm_scale, void* out, void* workspace, int64_t workspace_bytes, void* stream);
@@ -273,9 +275,9 @@ int s1_op_attention_paged_step_workspace(int32_t n, int32_t Hq, int32_t Hkv, int
 
 /* The same for prompts: sequence s has query rows row0[s] .. +len[s]-1 (host arrays, as in
  * s1_op_attention_shared_async) at positions pos0[s] .. (host; pos0 + len <= cols * page_rows) of table row s, and each
- * sees the rows that a token at its position sees. Rows of no sequence are not written. e4m3 pages: a row whose scale lies
- * more than 2^27 below the largest that its neighbours see loses bits. A sequence's query rows are read in whole tiles of
- * up to 128 / (Hq / Hkv) rows within the rows that row0 and len span. */
+ * sees the rows that a token at its position sees. Rows of no sequence are not written. e4m3 pages: a row whose scale
+ * lies more than 2^27 below the largest that its neighbours see loses bits (single tokens have no such limit). A
+ * sequence's query rows are read in whole tiles of up to 128 / (Hq / Hkv) rows within the rows that row0 and len span. */
 int s1_op_attention_paged_async(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n_seq, const int32_t* row0,
                                 const int32_t* len, const int32_t* pos0, int32_t Hq, const s1_kv_pages* pages,
                                 int32_t window, int32_t sinks, float sm_scale, void* out, void* workspace,
