@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         float zs = sl2;
         int unit_now = unit;
         if constexpr (E4) {
-          // a factor that vanishes would make -inf x 0 of the hidden keys (scores are below 2^36 of it, so 0 all the same), and
+          // a factor that vanishes would make -inf x 0 of the hidden keys (scores are below 2^39 of it, so 0 all the same), and
           // one past fp32's range 0 x inf of a score of 0
           zs = fminf(fmaxf(zs * pow2f(base_k[(tiles + t) % BASES] - 7), 1.17549435e-38f), 3.402823466e38f);
           const Slot vs = slot(t, true, t0, t1);               // (V's bound comes with the V tile)

@@ -85,7 +85,13 @@ int s1_op_sync(void* stream) {
     e = (cudaError_t)told.news(dev, [&](uint64_t* now) {     // (one caller at a time: g_now is its own)
       gather_words<<<1, 4, 0, st>>>(words);
       cudaError_t r = cudaGetLastError();
-      if (r == cudaSuccess) r = cudaMemcpyAsync(now, now_at, sizeof(g_now), cudaMemcpyDeviceToHost, st);
+      if (r == cudaSuccess) {
+        r = cudaMemcpyAsync(now, now_at, sizeof(g_now), cudaMemcpyDeviceToHost, st);
+      } else if (r == cudaErrorInvalidResourceHandle) {      // a stream of another device takes copies, but no kernel of this one
+        r = cudaSuccess;
+        for (int i = 0; i < 4 && r == cudaSuccess; ++i)
+          r = cudaMemcpyAsync(&now[i], words.at[i], sizeof(now[i]), cudaMemcpyDeviceToHost, st);
+      }
       if (r == cudaSuccess) r = cudaStreamSynchronize(st);
       return (int)r;
     }, &any);
