@@ -275,9 +275,10 @@ int s1_op_attention_paged_step_workspace(int32_t n, int32_t Hq, int32_t Hkv, int
 
 /* The same for prompts: sequence s has query rows row0[s] .. +len[s]-1 (host arrays, as in
  * s1_op_attention_shared_async) at positions pos0[s] .. (host; pos0 + len <= cols * page_rows) of table row s, and each
- * sees the rows that a token at its position sees. Rows of no sequence are not written. e4m3 pages: a row whose scale
- * lies more than 2^27 below the largest that its neighbours see loses bits (single tokens have no such limit). A
- * sequence's query rows are read in whole tiles of up to 128 / (Hq / Hkv) rows within the rows that row0 and len span. */
+ * sees the rows that a token at its position sees. Rows of no sequence are not written. e4m3 pages: code x scale is
+ * rounded to f16 (exact for powers of two, and for other scales of up to 7 bits), and a row whose scale lies more than
+ * 2^27 below the largest that its neighbours see loses bits (single tokens have no such limits). A sequence's query rows
+ * are read in whole tiles of up to 128 / (Hq / Hkv) rows within the rows that row0 and len span. */
 int s1_op_attention_paged_async(const void* q, int32_t q_dtype, int64_t q_stride, int32_t n_seq, const int32_t* row0,
                                 const int32_t* len, const int32_t* pos0, int32_t Hq, const s1_kv_pages* pages,
                                 int32_t window, int32_t sinks, float sm_scale, void* out, void* workspace,
